@@ -469,4 +469,8 @@ mok_status mok_selftest_bounded_count_wait(uint32_t limit_us, cudaStream_t strea
 #ifdef __cplusplus
 }
 #endif
+
+/* operators around the layer: the token sort, a linear layer, the optimizer step */
+#include "mok_ops.h"
+
 #endif /* MOK_H */

@@ -41,6 +41,10 @@ MOK_WS_BACKWARD_RECOMPUTE = 3
 MOK_WS_SHARED = 4
 MOK_WS_SHARED_BACKWARD = 5
 
+# mok_dtype
+MOK_DTYPE_BF16 = 0
+MOK_DTYPE_F32 = 1
+
 # mok_ws_item
 MOK_ITEM_X_RING = 0
 MOK_ITEM_X_RING_SCALE = 1
@@ -66,6 +70,8 @@ EXPORTED = [
     "mok_quantize_mxfp8_transposed", "mok_backward_mxfp8", "mok_shared_expert_backward",
     "mok_shared_expert_forward_mxfp8", "mok_shared_expert_backward_mxfp8",
     "mok_selftest_bounded_wait", "mok_selftest_bounded_count_wait", "mok_workspace_item",
+    "mok_check_rows_config", "mok_build_row_map", "mok_dispatch", "mok_dispatch_backward",
+    "mok_combine", "mok_combine_backward",
 ]
 
 # bytes of the fixed scratch array behind mok_build_schedule_noalloc
@@ -83,6 +89,14 @@ class MokSchedule(ctypes.Structure):
     _fields_ = [("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
                 ("perm", ctypes.c_void_p), ("inv", ctypes.c_void_p), ("segs", ctypes.c_void_p),
                 ("n_segs", ctypes.c_void_p)]
+
+
+class MokRowsConfig(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("T", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("capacity", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("n_rows", ctypes.c_int64), ("ld_tok", ctypes.c_int64),
+                ("ld_row", ctypes.c_int64)]
 
 
 class MokError(RuntimeError):
@@ -106,6 +120,7 @@ def lib():
         p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         cfgp = ctypes.POINTER(MokConfig)
         schp = ctypes.POINTER(MokSchedule)
+        rowsp = ctypes.POINTER(MokRowsConfig)
         sig = {
             "mok_abi_version": ([], ctypes.c_uint32),
             "mok_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -139,6 +154,12 @@ def lib():
             "mok_profile_read": ([i32, ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_char_p),
                                   ctypes.POINTER(i64), ctypes.POINTER(ctypes.c_double)],
                                  ctypes.c_int),
+            "mok_check_rows_config": ([rowsp], ctypes.c_int),
+            "mok_build_row_map": ([rowsp, p, schp, p, p, p, p], ctypes.c_int),
+            "mok_dispatch": ([rowsp, p, p, p, p, p, p], ctypes.c_int),
+            "mok_dispatch_backward": ([rowsp, p, p, p, p], ctypes.c_int),
+            "mok_combine": ([rowsp, p, p, p, p, p, p], ctypes.c_int),
+            "mok_combine_backward": ([rowsp, p, p, p, p, p, p, p, p, p], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -175,6 +196,15 @@ def make_config(T, H, I, E, K, minibatch=2368, ring_capacity=0, prec=MOK_BF16,
 def make_schedule(counts, offsets, perm, inv, segs, n_segs) -> MokSchedule:
     return MokSchedule(_ptr(counts), _ptr(offsets), _ptr(perm), _ptr(inv), _ptr(segs),
                        _ptr(n_segs))
+
+
+def make_rows(T, K, E, H, n_rows=None, dtype=MOK_DTYPE_BF16, ld_tok=None, ld_row=None,
+              capacity=0, abi_version=MOK_ABI_VERSION) -> MokRowsConfig:
+    """Configuration of the token sort; rows packed and enough of them unless given."""
+    if n_rows is None:
+        n_rows = T * K + 15 * min(E, T * K)
+    return MokRowsConfig(abi_version, T, K, E, H, dtype, capacity, 0, n_rows,
+                         H if ld_tok is None else ld_tok, H if ld_row is None else ld_row)
 
 
 def status_string(s) -> str:
@@ -327,3 +357,36 @@ def mok_profile_read(max_kinds=32):
     check(lib().mok_profile_read(max_kinds, ctypes.byref(n), names, launches, ms), "profile")
     return {names[i].decode(): (int(launches[i]), float(ms[i]))
             for i in range(min(n.value, max_kinds))}
+
+
+# ------------------------------------------------- operators around the layer (mok_ops.h)
+
+def mok_check_rows_config(cfg) -> int:
+    return lib().mok_check_rows_config(ctypes.byref(cfg))
+
+
+def mok_build_row_map(cfg, topk_idx, sched, row_map, starts, kept, stream=None) -> int:
+    return lib().mok_build_row_map(ctypes.byref(cfg), _ptr(topk_idx), ctypes.byref(sched),
+                                   _ptr(row_map), _ptr(starts), _ptr(kept), _stream(stream))
+
+
+def mok_dispatch(cfg, x, row_map, starts, kept, xs, stream=None) -> int:
+    return lib().mok_dispatch(ctypes.byref(cfg), _ptr(x), _ptr(row_map), _ptr(starts),
+                              _ptr(kept), _ptr(xs), _stream(stream))
+
+
+def mok_dispatch_backward(cfg, dxs, row_map, dx, stream=None) -> int:
+    return lib().mok_dispatch_backward(ctypes.byref(cfg), _ptr(dxs), _ptr(row_map), _ptr(dx),
+                                       _stream(stream))
+
+
+def mok_combine(cfg, rows, row_map, topk_w, residual, y, stream=None) -> int:
+    return lib().mok_combine(ctypes.byref(cfg), _ptr(rows), _ptr(row_map), _ptr(topk_w),
+                             _ptr(residual), _ptr(y), _stream(stream))
+
+
+def mok_combine_backward(cfg, dy, rows, row_map, starts, kept, topk_w, drows, d_topk_w,
+                         stream=None) -> int:
+    return lib().mok_combine_backward(ctypes.byref(cfg), _ptr(dy), _ptr(rows), _ptr(row_map),
+                                      _ptr(starts), _ptr(kept), _ptr(topk_w), _ptr(drows),
+                                      _ptr(d_topk_w), _stream(stream))

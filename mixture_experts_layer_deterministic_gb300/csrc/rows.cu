@@ -1,0 +1,589 @@
+// rows.cu -- the token sort as operators: row map, dispatch, combine and their gradients.
+//
+// With r(t,k) the row of routed id f = t*K + k (or none):
+//   dispatch           xs[r(t,k)] = x[t]
+//   combine            y[t] = res[t] + sum_k w[t,k] rows[r(t,k)]
+//   combine backward   drows[r(t,k)] = w[t,k] dy[t],  dw[t,k] = <rows[r(t,k)], dy[t]>
+//   dispatch backward  dx[t] = sum_k dxs[r(t,k)]       (combine with weights of one)
+// All of it is HBM traffic of R = T*K rows; every token row is touched once. Work is cut by
+// token and by column segment, so a row is read or written by whole warps, 16 bytes a lane.
+// Sums over k run in ascending k in fp32; dot products over H in a fixed tree: no atomics.
+#include "common.cuh"
+#include "mok_internal.h"
+
+namespace mok {
+namespace {
+
+constexpr int TPB = 256;
+constexpr int WARPS = TPB / 32;
+constexpr int MAX_E = 1024;
+
+inline unsigned grid_for(int64_t items, int per_block, int per_sm) {
+    const int64_t cap = (int64_t)device_sm_count() * per_sm;
+    int64_t b = (items + per_block - 1) / per_block;
+    if (b > cap) b = cap;
+    return (unsigned)(b < 1 ? 1 : b);
+}
+
+// ---------------------------------------------------------------- row map
+// Every block scans the experts' kept rows for itself (E <= 1024: ten steps in shared
+// memory), then maps its share of the ids: one launch, no order between blocks.
+__global__ void __launch_bounds__(MAX_E)
+    row_map_kernel(const int32_t *__restrict__ idx, const int32_t *__restrict__ counts,
+                   const int32_t *__restrict__ offsets, const int32_t *__restrict__ inv,
+                   int64_t R, int E, int capacity, int64_t n_rows, int32_t *__restrict__ map,
+                   int32_t *__restrict__ starts, int32_t *__restrict__ kept, int *status) {
+    __shared__ int64_t warp_sum[MAX_E / 32];
+    __shared__ int32_t s_start[MAX_E], s_kept[MAX_E], s_off[MAX_E];
+    const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+    int32_t n = 0;
+    if (e < E) {
+        n = counts[e];
+        if (n < 0 || n > R) {
+            raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+            n = 0;
+        }
+        if (capacity > 0 && n > capacity) n = capacity;
+    }
+    int64_t v = ((int64_t)n + 15) & ~(int64_t)15;
+    const int64_t own = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+    }
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    int64_t base = 0;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    const int64_t end = base + v, begin = end - own;
+    if (e < E) {
+        // past 31 bits nothing fits n_rows; the ids of such experts are dropped below
+        s_start[e] = begin < 0x7FFFFFFF ? (int32_t)begin : 0x7FFFFFFF;
+        s_kept[e] = n;
+        s_off[e] = offsets[e];
+        if (blockIdx.x == 0) {
+            starts[e] = s_start[e];
+            kept[e] = n;
+            if (e == E - 1) {
+                starts[E] = end < 0x7FFFFFFF ? (int32_t)end : 0x7FFFFFFF;
+                if (end > n_rows) raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+            }
+        }
+    }
+    __syncthreads();
+    const int64_t stride = (int64_t)gridDim.x * MAX_E;
+    for (int64_t f = (int64_t)blockIdx.x * MAX_E + threadIdx.x; f < R; f += stride) {
+        const int32_t x = idx[f];
+        int32_t row = -1;
+        if (x < 0 || x >= E) {
+            raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+        } else {
+            const int64_t rank = (int64_t)inv[f] - s_off[x];
+            if (rank < 0 || rank >= R) {
+                raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+            } else if (rank < s_kept[x] && (int64_t)s_start[x] + rank < n_rows) {
+                row = (int32_t)(s_start[x] + rank);
+            }
+        }
+        map[f] = row;
+    }
+}
+
+// ---------------------------------------------------------------- row access
+// Elements of a row handled per lane and step: one 16-byte vector, or one element where the
+// strides do not keep rows 16-byte aligned.
+template <bool F32>
+struct Elem {
+    static constexpr int BYTES = F32 ? 4 : 2;
+    static constexpr int PER = 16 / BYTES;  // elements of a 16-byte vector
+};
+
+// the routed row of id f: a valid row index, or -1 (an index at or past n_rows is reported)
+MOK_DEV int32_t row_of(const int32_t *__restrict__ map, int64_t f, int64_t n_rows, int *status) {
+    int32_t r = map[f];
+    if (r >= n_rows) {
+        raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+        r = -1;
+    }
+    return r;
+}
+
+template <bool F32>
+MOK_DEV float load_elem(const void *p, int64_t i) {
+    return F32 ? static_cast<const float *>(p)[i]
+               : bf16_to_f32(static_cast<const uint16_t *>(p)[i]);
+}
+template <bool F32>
+MOK_DEV void store_elem(void *p, int64_t i, float v) {
+    if (F32)
+        static_cast<float *>(p)[i] = v;
+    else
+        static_cast<uint16_t *>(p)[i] = f32_to_bf16(v);
+}
+template <bool F32>
+MOK_DEV void unpack(const uint4 &u, float (&v)[Elem<F32>::PER]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (F32) {
+            v[q] = __uint_as_float(w[q]);
+        } else {
+            v[2 * q] = bf16_lo(w[q]);
+            v[2 * q + 1] = bf16_hi(w[q]);
+        }
+    }
+}
+template <bool F32>
+MOK_DEV uint4 pack(const float (&v)[Elem<F32>::PER]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        w[q] = F32 ? __float_as_uint(v[q]) : pack_bf16x2(v[2 * q], v[2 * q + 1]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// zero rows of the sorted array after each expert's own: item (e, j), row kept[e] + j below
+// the next multiple of 16; one warp per item
+template <bool F32, bool VEC>
+MOK_DEV void zero_pad_row(int64_t item, const int32_t *__restrict__ starts,
+                          const int32_t *__restrict__ kept, int64_t n_rows, int H, int64_t ld,
+                          void *__restrict__ out, int lane) {
+    const int e = (int)(item >> 4), j = (int)(item & 15);
+    const int64_t n = kept[e];
+    if (n + j >= ((n + 15) & ~(int64_t)15)) return;
+    const int64_t row = starts[e] + n + j;
+    if (row < 0 || row >= n_rows) return;
+    uint8_t *p = static_cast<uint8_t *>(out) + row * ld * Elem<F32>::BYTES;
+    int c = 0;
+    if (VEC) {
+        c = H / Elem<F32>::PER * Elem<F32>::PER;
+        for (int v = lane; v < H / Elem<F32>::PER; v += 32)
+            reinterpret_cast<uint4 *>(p)[v] = make_uint4(0, 0, 0, 0);
+    }
+    for (c += lane; c < H; c += 32) store_elem<F32>(p, c, 0.f);
+}
+
+// ---------------------------------------------------------------- dispatch
+// Work item: (token, segment of 32*U vectors), one warp each; a token's row is read once and
+// written to the rows of its K copies. Items past the tokens' are the pad rows.
+template <bool F32, bool VEC, int U>
+__global__ void __launch_bounds__(TPB)
+    dispatch_kernel(const void *__restrict__ x, const int32_t *__restrict__ map,
+                    const int32_t *__restrict__ starts, const int32_t *__restrict__ kept,
+                    int64_t T, int K, int E, int H, int64_t ld_tok, int64_t ld_row,
+                    int64_t n_rows, void *__restrict__ xs, int *status) {
+    constexpr int B = Elem<F32>::BYTES, PER = VEC ? Elem<F32>::PER : 1;
+    const int lane = threadIdx.x & 31;
+    const int nv = H / PER;                          // whole vectors of a row
+    const int segs = (H + PER * 32 * U - 1) / (PER * 32 * U);
+    const int64_t tok_items = T * segs;
+    const int64_t items = tok_items + (starts != nullptr ? (int64_t)E * 16 : 0);
+    const int64_t nw = (int64_t)gridDim.x * WARPS;
+    for (int64_t it = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); it < items; it += nw) {
+        if (it >= tok_items) {
+            zero_pad_row<F32, VEC>(it - tok_items, starts, kept, n_rows, H, ld_row, xs, lane);
+            continue;
+        }
+        const int64_t t = it / segs;
+        const int v0 = (int)(it % segs) * 32 * U + lane;
+        const int32_t rk = lane < K ? row_of(map, t * K + lane, n_rows, status) : -1;
+        const uint8_t *src = static_cast<const uint8_t *>(x) + t * ld_tok * B;
+        if (VEC) {
+            uint4 b[U];
+            float tail = 0.f;  // the columns past the last whole vector, at most PER - 1
+            const int tc = nv * PER + lane;
+            const bool has_tail = v0 - lane + 32 * U > nv && tc < H;
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (v0 + 32 * j < nv) b[j] = ldg_nc_v4(src + (int64_t)(v0 + 32 * j) * 16);
+            if (has_tail) tail = load_elem<F32>(src, tc);
+            for (int k = 0; k < K; ++k) {
+                const int64_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
+                if (r < 0) continue;
+                uint8_t *dst = static_cast<uint8_t *>(xs) + r * ld_row * B;
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (v0 + 32 * j < nv) reinterpret_cast<uint4 *>(dst)[v0 + 32 * j] = b[j];
+                if (has_tail) store_elem<F32>(dst, tc, tail);
+            }
+        } else {
+            float b[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (v0 + 32 * j < nv) b[j] = load_elem<F32>(src, v0 + 32 * j);
+            for (int k = 0; k < K; ++k) {
+                const int64_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
+                if (r < 0) continue;
+                uint8_t *dst = static_cast<uint8_t *>(xs) + r * ld_row * B;
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (v0 + 32 * j < nv) store_elem<F32>(dst, v0 + 32 * j, b[j]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- combine
+// Work item: (token, segment of 32 vectors), one warp each. Lane k holds row and weight of
+// copy k; the K rows are read four at a time.
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(TPB)
+    combine_rows_kernel(const void *__restrict__ rows, const int32_t *__restrict__ map,
+                        const float *__restrict__ w, const void *res, int64_t T, int K, int H,
+                        int64_t ld_tok, int64_t ld_row, int64_t n_rows, void *y, int *status) {
+    constexpr int B = Elem<F32>::BYTES, PER = VEC ? Elem<F32>::PER : 1;
+    const int lane = threadIdx.x & 31;
+    const int segs = (H + PER * 32 - 1) / (PER * 32);
+    const int64_t items = T * segs;
+    const int64_t nw = (int64_t)gridDim.x * WARPS;
+    for (int64_t it = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); it < items; it += nw) {
+        const int64_t t = it / segs;
+        const int c = ((int)(it % segs) * 32 + lane) * PER;  // this lane's first column
+        const int32_t rk = lane < K ? row_of(map, t * K + lane, n_rows, status) : -1;
+        const float wk = lane < K ? (w != nullptr ? w[t * K + lane] : 1.0f) : 0.f;
+        const uint8_t *resp =
+            res != nullptr ? static_cast<const uint8_t *>(res) + t * ld_tok * B : nullptr;
+        uint8_t *yp = static_cast<uint8_t *>(y) + t * ld_tok * B;
+        const bool whole = VEC && c + PER <= H;
+        float acc[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) acc[q] = 0.f;
+        for (int k0 = 0; k0 < K; k0 += 4) {
+            uint4 b[4];
+            float e[4][VEC ? 1 : PER];
+            int32_t r[4];
+            float s[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = k0 + j;
+                r[j] = __shfl_sync(0xFFFFFFFFu, rk, k < K ? k : K - 1);
+                s[j] = __shfl_sync(0xFFFFFFFFu, wk, k < K ? k : K - 1);
+                if (k >= K) r[j] = -1;
+                if (r[j] < 0) continue;
+                const uint8_t *p = static_cast<const uint8_t *>(rows) + r[j] * ld_row * B;
+                if (VEC) {
+                    if (whole) b[j] = ldg_nc_v4(p + (int64_t)c * B);
+                } else if (c < H) {
+                    e[j][0] = load_elem<F32>(p, c);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (r[j] < 0) continue;
+                if constexpr (VEC) {
+                    float v[PER];
+                    if (whole) {
+                        unpack<F32>(b[j], v);
+                    } else {
+                        const uint8_t *p = static_cast<const uint8_t *>(rows) + r[j] * ld_row * B;
+#pragma unroll
+                        for (int q = 0; q < PER; ++q)
+                            v[q] = c + q < H ? load_elem<F32>(p, c + q) : 0.f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) acc[q] = fmaf(s[j], v[q], acc[q]);
+                } else if (c < H) {
+                    acc[0] = fmaf(s[j], e[j][0], acc[0]);
+                }
+            }
+        }
+        if constexpr (VEC) {
+            if (whole) {
+                if (resp != nullptr) {
+                    float v[PER];
+                    unpack<F32>(*reinterpret_cast<const uint4 *>(resp + (int64_t)c * B), v);
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) acc[q] += v[q];
+                }
+                *reinterpret_cast<uint4 *>(yp + (int64_t)c * B) = pack<F32>(acc);
+                continue;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (c + q < H)
+                store_elem<F32>(yp, c + q,
+                                acc[q] + (resp != nullptr ? load_elem<F32>(resp, c + q) : 0.f));
+    }
+}
+
+// ---------------------------------------------------------------- combine backward
+// One block per token; warp i takes the row's segments i, i + 8, ... of 32 vectors. Each warp
+// sums its part of the K dot products over its lanes by a butterfly, lane k keeping copy k's;
+// the warps' parts are added in warp order. Blocks past the tokens' zero the pad rows.
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(TPB)
+    combine_bwd_kernel(const void *__restrict__ dy, const void *__restrict__ rows,
+                       const int32_t *__restrict__ map, const int32_t *__restrict__ starts,
+                       const int32_t *__restrict__ kept, const float *__restrict__ w, int64_t T,
+                       int K, int E, int H, int64_t ld_tok, int64_t ld_row, int64_t n_rows,
+                       void *__restrict__ drows, float *__restrict__ dw, int *status) {
+    constexpr int B = Elem<F32>::BYTES, PER = VEC ? Elem<F32>::PER : 1;
+    __shared__ float part[WARPS][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool pads = starts != nullptr && drows != nullptr;
+    const int64_t items = T + (pads ? (int64_t)E * 16 / WARPS : 0);
+    for (int64_t t = blockIdx.x; t < items; t += gridDim.x) {
+        if (t >= T) {
+            zero_pad_row<F32, VEC>((t - T) * WARPS + warp, starts, kept, n_rows, H, ld_row, drows,
+                                   lane);
+            continue;
+        }
+        const int32_t rk = lane < K ? row_of(map, t * K + lane, n_rows, status) : -1;
+        const float wk = lane < K ? (w != nullptr ? w[t * K + lane] : 1.0f) : 0.f;
+        const uint8_t *dyp = static_cast<const uint8_t *>(dy) + t * ld_tok * B;
+        float dot = 0.f;  // lane k: this warp's part of <rows[r_k], dy>
+        for (int c0 = warp * 32 * PER; c0 < H; c0 += WARPS * 32 * PER) {
+            const int c = c0 + lane * PER;
+            const bool whole = c + PER <= H;
+            float g[PER];
+            if constexpr (VEC) {
+                if (whole) {
+                    unpack<F32>(ldg_nc_v4(dyp + (int64_t)c * B), g);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) g[q] = c + q < H ? load_elem<F32>(dyp, c + q) : 0.f;
+                }
+            } else {
+                g[0] = c < H ? load_elem<F32>(dyp, c) : 0.f;
+            }
+            for (int k = 0; k < K; ++k) {
+                const int64_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
+                if (r < 0) continue;
+                const float s = __shfl_sync(0xFFFFFFFFu, wk, k);
+                float v[PER], d[PER];
+#pragma unroll
+                for (int q = 0; q < PER; ++q) v[q] = 0.f;
+                if (dw != nullptr) {
+                    const uint8_t *p = static_cast<const uint8_t *>(rows) + r * ld_row * B;
+                    if constexpr (VEC) {
+                        if (whole) {
+                            unpack<F32>(ldg_nc_v4(p + (int64_t)c * B), v);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < PER; ++q)
+                                v[q] = c + q < H ? load_elem<F32>(p, c + q) : 0.f;
+                        }
+                    } else {
+                        v[0] = c < H ? load_elem<F32>(p, c) : 0.f;
+                    }
+                }
+                if (drows != nullptr) {
+                    uint8_t *o = static_cast<uint8_t *>(drows) + r * ld_row * B;
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) d[q] = s * g[q];
+                    bool done = false;
+                    if constexpr (VEC) {
+                        if (whole) {
+                            *reinterpret_cast<uint4 *>(o + (int64_t)c * B) = pack<F32>(d);
+                            done = true;
+                        }
+                    }
+                    if (!done) {
+#pragma unroll
+                        for (int q = 0; q < PER; ++q)
+                            if (c + q < H) store_elem<F32>(o, c + q, d[q]);
+                    }
+                }
+                if (dw != nullptr) {
+                    float a = 0.f;
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) a = fmaf(v[q], g[q], a);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                    if (lane == k) dot += a;
+                }
+            }
+        }
+        if (dw != nullptr) {
+            part[warp][lane] = dot;
+            __syncthreads();
+            if (warp == 0 && lane < K) {
+                float a = 0.f;
+#pragma unroll
+                for (int i = 0; i < WARPS; ++i) a += part[i][lane];
+                dw[t * K + lane] = a;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// rows start on 16-byte boundaries: both strides are multiples of 16 bytes
+bool vectors(const mok_rows_config &c) {
+    const int per = c.dtype == MOK_DTYPE_F32 ? 4 : 8;
+    return c.ld_tok % per == 0 && c.ld_row % per == 0;
+}
+
+}  // namespace
+
+// instantiate KERNEL<F32, VEC> for the configuration
+#define MOK_ROWS_CASES(c, CALL)                          \
+    do {                                                 \
+        const bool _v = vectors(c);                      \
+        if ((c).dtype == MOK_DTYPE_F32) {                \
+            if (_v) { CALL(true, true); }                \
+            else { CALL(true, false); }                  \
+        } else {                                         \
+            if (_v) { CALL(false, true); }               \
+            else { CALL(false, false); }                 \
+        }                                                \
+    } while (0)
+
+cudaError_t launch_build_row_map(const mok_rows_config &c, const int32_t *idx,
+                                 const mok_schedule &sch, int32_t *map, int32_t *starts,
+                                 int32_t *kept, int *status, cudaStream_t s) {
+    const int64_t R = (int64_t)c.T * c.K;
+    row_map_kernel<<<grid_for(R, MAX_E, 1), MAX_E, 0, s>>>(
+        idx, sch.counts, sch.offsets, sch.inv, R, c.E, c.capacity, c.n_rows, map, starts, kept,
+        status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_dispatch_rows(const mok_rows_config &c, const void *x, const int32_t *map,
+                                 const int32_t *starts, const int32_t *kept, void *xs,
+                                 int *status, cudaStream_t s) {
+    constexpr int U = 4;
+    const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
+    const int64_t segs = (c.H + per * 32 * U - 1) / (per * 32 * U);
+    const int64_t items = c.T * segs + (starts != nullptr ? (int64_t)c.E * 16 : 0);
+    if (items == 0) return cudaSuccess;
+#define CALL(F, V)                                                                        \
+    dispatch_kernel<F, V, U><<<grid_for(items, WARPS, 16), TPB, 0, s>>>(                  \
+        x, map, starts, kept, c.T, c.K, c.E, c.H, c.ld_tok, c.ld_row, c.n_rows, xs, status)
+    MOK_ROWS_CASES(c, CALL);
+#undef CALL
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, const int32_t *map,
+                                const float *w, const void *res, void *y, int *status,
+                                cudaStream_t s) {
+    if (c.T == 0) return cudaSuccess;
+    const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
+    const int64_t items = (int64_t)c.T * ((c.H + per * 32 - 1) / (per * 32));
+#define CALL(F, V)                                                                       \
+    combine_rows_kernel<F, V><<<grid_for(items, WARPS, 16), TPB, 0, s>>>(                \
+        rows, map, w, res, c.T, c.K, c.H, c.ld_tok, c.ld_row, c.n_rows, y, status)
+    MOK_ROWS_CASES(c, CALL);
+#undef CALL
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const void *rows,
+                               const int32_t *map, const int32_t *starts, const int32_t *kept,
+                               const float *w, void *drows, float *dw, int *status,
+                               cudaStream_t s) {
+    const int64_t items = c.T + (starts != nullptr && drows != nullptr ? (int64_t)c.E * 2 : 0);
+    if (items == 0) return cudaSuccess;
+#define CALL(F, V)                                                                         \
+    combine_bwd_kernel<F, V><<<grid_for(items, 1, 16), TPB, 0, s>>>(                       \
+        dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, c.ld_tok, c.ld_row, c.n_rows,  \
+        drows, dw, status)
+    MOK_ROWS_CASES(c, CALL);
+#undef CALL
+    return cudaGetLastError();
+}
+
+}  // namespace mok
+
+// ---------------------------------------------------------------- entry points
+using namespace mok;
+
+extern "C" {
+
+mok_status mok_check_rows_config(const mok_rows_config *c) {
+    if (c == nullptr) return MOK_ERR_INVALID_ARG;
+    if (c->abi_version != MOK_ABI_VERSION) return MOK_ERR_ABI;
+    if (c->T < 0 || c->K < 1 || c->K > 32 || c->E < 1 || c->E > MAX_E || c->H < 1)
+        return MOK_ERR_INVALID_ARG;
+    if (c->H > (1 << 24)) return MOK_ERR_INVALID_ARG;
+    if ((int64_t)c->T * c->K > 0x7FFFFFFF) return MOK_ERR_INVALID_ARG;
+    if (c->dtype != MOK_DTYPE_BF16 && c->dtype != MOK_DTYPE_F32) return MOK_ERR_INVALID_ARG;
+    if (c->capacity < 0 || c->reserved != 0) return MOK_ERR_INVALID_ARG;
+    if (c->n_rows < 0 || c->n_rows > 0x7FFFFFFF) return MOK_ERR_INVALID_ARG;
+    const int64_t most = (int64_t)1 << 30;
+    if (c->ld_tok < c->H || c->ld_row < c->H || c->ld_tok > most || c->ld_row > most)
+        return MOK_ERR_INVALID_ARG;
+    return MOK_OK;
+}
+
+mok_status mok_build_row_map(const mok_rows_config *c, const int32_t *topk_idx,
+                             const mok_schedule *sch, int32_t *row_map, int32_t *starts,
+                             int32_t *kept, cudaStream_t stream) {
+    mok_status st = mok_check_rows_config(c);
+    if (st != MOK_OK) return st;
+    int *status;
+    if ((st = current_device_status_word(&status)) != MOK_OK) return st;
+    if (!sch || !sch->counts || !sch->offsets || !starts || !kept) return MOK_ERR_INVALID_ARG;
+    if (c->T > 0 && (!topk_idx || !row_map || !sch->inv)) return MOK_ERR_INVALID_ARG;
+    const void *ps[] = {topk_idx, row_map, starts, kept, sch->counts, sch->offsets, sch->inv};
+    for (const void *p : ps)
+        if (p && !aligned16(p)) return MOK_ERR_INVALID_ARG;
+    MOK_LAUNCH(KK_ROW_MAP, 1,
+               launch_build_row_map(*c, topk_idx, *sch, row_map, starts, kept, status, stream));
+    return MOK_OK;
+}
+
+mok_status mok_dispatch(const mok_rows_config *c, const void *x, const int32_t *row_map,
+                        const int32_t *starts, const int32_t *kept, void *xs,
+                        cudaStream_t stream) {
+    mok_status st = mok_check_rows_config(c);
+    if (st != MOK_OK) return st;
+    int *status;
+    if ((st = current_device_status_word(&status)) != MOK_OK) return st;
+    if ((starts == nullptr) != (kept == nullptr)) return MOK_ERR_INVALID_ARG;
+    if (c->T > 0 && (!x || !row_map)) return MOK_ERR_INVALID_ARG;
+    if (!xs && c->n_rows > 0) return MOK_ERR_INVALID_ARG;
+    const void *ps[] = {x, row_map, starts, kept, xs};
+    for (const void *p : ps)
+        if (p && !aligned16(p)) return MOK_ERR_INVALID_ARG;
+    MOK_LAUNCH(KK_DISPATCH, 1,
+               launch_dispatch_rows(*c, x, row_map, starts, kept, xs, status, stream));
+    return MOK_OK;
+}
+
+mok_status mok_combine(const mok_rows_config *c, const void *rows, const int32_t *row_map,
+                       const float *topk_w, const void *residual, void *y,
+                       cudaStream_t stream) {
+    mok_status st = mok_check_rows_config(c);
+    if (st != MOK_OK) return st;
+    int *status;
+    if ((st = current_device_status_word(&status)) != MOK_OK) return st;
+    if (c->T > 0 && (!row_map || !y || (!rows && c->n_rows > 0))) return MOK_ERR_INVALID_ARG;
+    const void *ps[] = {rows, row_map, topk_w, residual, y};
+    for (const void *p : ps)
+        if (p && !aligned16(p)) return MOK_ERR_INVALID_ARG;
+    MOK_LAUNCH(KK_COMBINE_ROWS, 1,
+               launch_combine_rows(*c, rows, row_map, topk_w, residual, y, status, stream));
+    return MOK_OK;
+}
+
+mok_status mok_dispatch_backward(const mok_rows_config *c, const void *dxs,
+                                 const int32_t *row_map, void *dx, cudaStream_t stream) {
+    return mok_combine(c, dxs, row_map, nullptr, nullptr, dx, stream);
+}
+
+mok_status mok_combine_backward(const mok_rows_config *c, const void *dy, const void *rows,
+                                const int32_t *row_map, const int32_t *starts,
+                                const int32_t *kept, const float *topk_w, void *drows,
+                                float *d_topk_w, cudaStream_t stream) {
+    mok_status st = mok_check_rows_config(c);
+    if (st != MOK_OK) return st;
+    int *status;
+    if ((st = current_device_status_word(&status)) != MOK_OK) return st;
+    if (!drows && !d_topk_w) return MOK_ERR_INVALID_ARG;
+    if ((starts == nullptr) != (kept == nullptr)) return MOK_ERR_INVALID_ARG;
+    if (c->T > 0 && (!dy || !row_map)) return MOK_ERR_INVALID_ARG;
+    if (c->T > 0 && d_topk_w && !rows && c->n_rows > 0) return MOK_ERR_INVALID_ARG;
+    const void *ps[] = {dy, rows, row_map, starts, kept, topk_w, drows, d_topk_w};
+    for (const void *p : ps)
+        if (p && !aligned16(p)) return MOK_ERR_INVALID_ARG;
+    MOK_LAUNCH(KK_COMBINE_BWD, 1,
+               launch_combine_bwd(*c, dy, rows, row_map, starts, kept, topk_w, drows, d_topk_w,
+                                  status, stream));
+    return MOK_OK;
+}
+
+}  // extern "C"
