@@ -85,6 +85,64 @@ mok_status mok_combine_backward(const mok_rows_config *cfg, const void *dy, cons
                                 const int32_t *kept, const float *topk_w, void *drows,
                                 float *d_topk_w, cudaStream_t stream);
 
+/* ---- AdamW step over many tensors ---------------------------------------------------
+ *
+ * For every element, with g scaled by *grad_scale (NULL: one) and t = step:
+ *   m = beta1 m + (1 - beta1) g          v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32; p, m and v are then stored in their own types, the update itself using the
+ * unrounded m and v. `copy` (NULL, or bf16; only with fp32 parameters) receives p rounded to
+ * nearest even: the weights the layer's kernels read.
+ *
+ * MOK_STATE_F32: m and v are fp32 arrays.
+ * MOK_STATE_MXFP8: m and sqrt(v) are E4M3 codes with one E8M0 scale per 32 consecutive
+ *   elements (m_scale, v_scale: [ceil(n/32)] bytes), 33/32 bytes per element and state. The
+ *   scale is the least power of two (at least 2^-127) that brings the block's largest magnitude
+ *   to 448 or less, so nothing saturates; a sqrt(v) above zero is never stored as zero (the
+ *   least code instead), so m is never divided by eps alone. A block that holds an infinity
+ *   or a NaN gets scale byte 255 and reads back as NaN. All-zero bytes are the zero state.
+ *
+ * Rounding: to nearest even; with MOK_ADAMW_STOCHASTIC the 8-bit states and bf16 parameters are
+ * rounded up or down with probability proportional to the distance, so that changes smaller
+ * than a step (v moves by 1/1000 of itself at beta2 = 0.999, E4M3 steps are 1/16 or more) are
+ * kept on average. The random bits are a function of the seed and the element's number alone:
+ * with the tensors numbered one after another, each beginning at the next multiple of 32,
+ * element i gets h = mix(lo32(i) ^ mix(mix(hi32(i) ^ lo32(seed)) ^ hi32(seed))), mix being
+ * h ^= h>>16, h *= 0x85EBCA6B, h ^= h>>13, h *= 0xC2B2AE35, h ^= h>>16 (the MurmurHash3
+ * finaliser). m takes h's low 16 bits, sqrt(v) its high 16, a bf16 p the high 16 of
+ * mix(h + 0x9E3779B9). Give every step its own seed. */
+typedef enum mok_adamw_state { MOK_STATE_F32 = 0, MOK_STATE_MXFP8 = 1 } mok_adamw_state;
+#define MOK_ADAMW_STOCHASTIC 1u
+
+typedef struct mok_adamw_config {
+    uint32_t abi_version;     /* MOK_ABI_VERSION */
+    int32_t p_dtype, g_dtype; /* mok_dtype of parameters and gradients */
+    int32_t state;            /* mok_adamw_state */
+    uint32_t flags;           /* MOK_ADAMW_* */
+    int32_t step;             /* t >= 1 */
+    double lr, beta1, beta2, eps;
+    uint64_t seed;
+} mok_adamw_config;
+
+typedef struct mok_adamw_tensor {
+    void *p;       /* [n], in and out */
+    void *copy;    /* NULL or [n] bf16 out */
+    const void *g; /* [n] */
+    void *m, *v;   /* [n] fp32, or E4M3 codes of m and sqrt(v), in and out */
+    uint8_t *m_scale, *v_scale; /* [ceil(n/32)] E8M0, in and out (MXFP8 states; else NULL) */
+    int64_t n;     /* elements, >= 0 */
+    double weight_decay;
+} mok_adamw_tensor;
+
+/* lr, eps >= 0, 0 <= beta < 1, weight_decay finite. Host only. */
+mok_status mok_check_adamw_config(const mok_adamw_config *cfg);
+
+/* One step over `n_tensors` tensors (a host array, read before the call returns). The arrays
+ * of one call must not overlap. grad_scale: NULL or a device float (a clipping coefficient
+ * or an inverse loss scale, computed on the GPU without a host round trip). */
+mok_status mok_adamw_step(const mok_adamw_config *cfg, const mok_adamw_tensor *tensors,
+                          int32_t n_tensors, const float *grad_scale, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -45,6 +45,11 @@ MOK_WS_SHARED_BACKWARD = 5
 MOK_DTYPE_BF16 = 0
 MOK_DTYPE_F32 = 1
 
+# mok_adamw_state, mok_adamw_config.flags
+MOK_STATE_F32 = 0
+MOK_STATE_MXFP8 = 1
+MOK_ADAMW_STOCHASTIC = 1
+
 # mok_ws_item
 MOK_ITEM_X_RING = 0
 MOK_ITEM_X_RING_SCALE = 1
@@ -71,7 +76,7 @@ EXPORTED = [
     "mok_shared_expert_forward_mxfp8", "mok_shared_expert_backward_mxfp8",
     "mok_selftest_bounded_wait", "mok_selftest_bounded_count_wait", "mok_workspace_item",
     "mok_check_rows_config", "mok_build_row_map", "mok_dispatch", "mok_dispatch_backward",
-    "mok_combine", "mok_combine_backward",
+    "mok_combine", "mok_combine_backward", "mok_check_adamw_config", "mok_adamw_step",
 ]
 
 # bytes of the fixed scratch array behind mok_build_schedule_noalloc
@@ -99,6 +104,34 @@ class MokRowsConfig(ctypes.Structure):
                 ("ld_row", ctypes.c_int64)]
 
 
+class MokAdamwConfig(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("p_dtype", ctypes.c_int32),
+                ("g_dtype", ctypes.c_int32), ("state", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("step", ctypes.c_int32), ("lr", ctypes.c_double),
+                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("seed", ctypes.c_uint64)]
+
+
+class MokAdamwTensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_double)]
+
+
+class AdamwList:
+    """The tensors of an AdamW step as the host array mok_adamw_step takes."""
+
+    def __init__(self, entries):
+        names = ("p", "copy", "g", "m", "v", "m_scale", "v_scale")
+        self.tensors = [[e.get(k) for k in names] for e in entries]  # kept alive
+        self.n = len(entries)
+        self.array = (MokAdamwTensor * self.n)(*[
+            MokAdamwTensor(*[_ptr(t) for t in ts], int(e["n"]),
+                           float(e.get("weight_decay", 0.0)))
+            for ts, e in zip(self.tensors, entries)])
+
+
 class MokError(RuntimeError):
     def __init__(self, status, what=""):
         self.status = int(status)
@@ -121,6 +154,7 @@ def lib():
         cfgp = ctypes.POINTER(MokConfig)
         schp = ctypes.POINTER(MokSchedule)
         rowsp = ctypes.POINTER(MokRowsConfig)
+        adamp = ctypes.POINTER(MokAdamwConfig)
         sig = {
             "mok_abi_version": ([], ctypes.c_uint32),
             "mok_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -160,6 +194,9 @@ def lib():
             "mok_dispatch_backward": ([rowsp, p, p, p, p], ctypes.c_int),
             "mok_combine": ([rowsp, p, p, p, p, p, p], ctypes.c_int),
             "mok_combine_backward": ([rowsp, p, p, p, p, p, p, p, p, p], ctypes.c_int),
+            "mok_check_adamw_config": ([adamp], ctypes.c_int),
+            "mok_adamw_step": ([adamp, ctypes.POINTER(MokAdamwTensor), i32, p, p],
+                               ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -205,6 +242,19 @@ def make_rows(T, K, E, H, n_rows=None, dtype=MOK_DTYPE_BF16, ld_tok=None, ld_row
         n_rows = T * K + 15 * min(E, T * K)
     return MokRowsConfig(abi_version, T, K, E, H, dtype, capacity, 0, n_rows,
                          H if ld_tok is None else ld_tok, H if ld_row is None else ld_row)
+
+
+def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0, p_dtype=MOK_DTYPE_F32,
+               g_dtype=MOK_DTYPE_BF16, state=MOK_STATE_F32, flags=0,
+               abi_version=MOK_ABI_VERSION) -> MokAdamwConfig:
+    return MokAdamwConfig(abi_version, p_dtype, g_dtype, state, flags, step, lr, beta1, beta2,
+                          eps, seed)
+
+
+def make_adamw_list(entries) -> AdamwList:
+    """The tensors of a step, made once: dicts with p, g, m, v, n and, where they apply, copy,
+    m_scale, v_scale, weight_decay."""
+    return AdamwList(entries)
 
 
 def status_string(s) -> str:
@@ -390,3 +440,13 @@ def mok_combine_backward(cfg, dy, rows, row_map, starts, kept, topk_w, drows, d_
     return lib().mok_combine_backward(ctypes.byref(cfg), _ptr(dy), _ptr(rows), _ptr(row_map),
                                       _ptr(starts), _ptr(kept), _ptr(topk_w), _ptr(drows),
                                       _ptr(d_topk_w), _stream(stream))
+
+
+def mok_check_adamw_config(cfg) -> int:
+    return lib().mok_check_adamw_config(ctypes.byref(cfg))
+
+
+def mok_adamw_step(cfg, tensors, grad_scale=None, stream=None) -> int:
+    """One step over an AdamwList (make_adamw_list)."""
+    return lib().mok_adamw_step(ctypes.byref(cfg), tensors.array, tensors.n, _ptr(grad_scale),
+                                _stream(stream))

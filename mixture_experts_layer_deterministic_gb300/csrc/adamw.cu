@@ -1,0 +1,423 @@
+// adamw.cu -- an AdamW step over many tensors in one launch, states in fp32 or in MXFP8.
+//
+// Per element (fp32):  m = b1 m + (1-b1) g,  v = b2 v + (1-b2) g^2,
+//                      p = p (1 - lr wd) - lr/(1-b1^t) m / (sqrt(v)/sqrt(1-b2^t) + eps).
+// Every array is read once and written once, so HBM traffic is the floor: with fp32 master
+// parameters, a bf16 copy and bf16 gradients, 28 bytes per element with fp32 states and
+// 16.125 with MXFP8 states.
+//
+// The tensor list travels in the kernel's parameters (no device-side table to allocate, copy
+// or keep alive, and a captured graph holds its own). A block takes chunks of 2048 elements
+// of one tensor, found by a binary search over the tensors' first chunks; each thread owns
+// 8 consecutive elements, so four threads hold a 32-element MXFP8 block and its largest
+// magnitude takes two shuffles.
+#include <cmath>
+
+#include "common.cuh"
+#include "mok_internal.h"
+
+namespace mok {
+namespace {
+
+constexpr int TPB = 256;
+constexpr int PER = 8;             // elements per thread
+constexpr int CHUNK = TPB * PER;   // elements per block and step
+
+struct TensorDesc {
+    void *p, *copy;
+    const void *g;
+    void *m, *v;
+    uint8_t *ms, *vs;
+    int64_t n;
+    int64_t base;    // element number of the tensor's first element
+    uint32_t first;  // its first chunk
+    float decay;     // 1 - lr weight_decay
+};
+
+struct Scalars {
+    float b1, a1, b2, a2;  // beta and 1 - beta
+    float step;            // lr / (1 - beta1^t)
+    float inv_root;        // 1 / sqrt(1 - beta2^t)
+    float eps;
+    uint32_t seed_lo, seed_hi;
+    int n_tensors;
+    uint32_t n_chunks;
+    const float *gscale;
+};
+
+template <int NT>
+struct Params {
+    Scalars s;
+    TensorDesc t[NT];
+};
+constexpr int NT_SMALL = 16, NT_LARGE = 400;
+static_assert(sizeof(Params<NT_LARGE>) <= 32764, "kernel parameters");
+
+// the MurmurHash3 finaliser
+MOK_DEV uint32_t mix32(uint32_t h) {
+    h ^= h >> 16;
+    h *= 0x85EBCA6Bu;
+    h ^= h >> 13;
+    h *= 0xC2B2AE35u;
+    return h ^ (h >> 16);
+}
+
+template <bool F32>
+MOK_DEV void load8(const void *p, int64_t i, int64_t n, float (&v)[PER]) {
+    if (i + PER <= n) {
+        if (F32) {
+            const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+            const float4 b =
+                *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + 4);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a =
+                *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[2 * q] = bf16_lo(w[q]);
+                v[2 * q + 1] = bf16_hi(w[q]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const bool ok = i + q < n;
+            v[q] = !ok ? 0.f
+                   : F32 ? static_cast<const float *>(p)[i + q]
+                         : bf16_to_f32(static_cast<const uint16_t *>(p)[i + q]);
+        }
+    }
+}
+
+MOK_DEV void store8_f32(void *p, int64_t i, int64_t n, const float (&v)[PER]) {
+    float *o = static_cast<float *>(p) + i;
+    if (i + PER <= n) {
+        *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (i + q < n) o[q] = v[q];
+    }
+}
+
+MOK_DEV void store8_u16(void *p, int64_t i, int64_t n, const uint32_t (&w)[PER / 2]) {
+    uint16_t *o = static_cast<uint16_t *>(p) + i;
+    if (i + PER <= n) {
+        *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (i + q < n) o[q] = (uint16_t)(w[q / 2] >> (16 * (q & 1)));
+    }
+}
+
+// fp32 -> bf16, rounded up with probability r / 2^16 of what is cut off (r: 16 random bits);
+// infinities and NaN as they are
+MOK_DEV uint32_t bf16_stochastic(float f, uint32_t r) {
+    const uint32_t b = __float_as_uint(f);
+    if ((b & 0x7F800000u) == 0x7F800000u) return f32_to_bf16(f);
+    return (b + r) >> 16;
+}
+
+// 8 E4M3 codes to fp32 (before the scale)
+MOK_DEV void decode8(uint2 q, float scale, float (&v)[PER]) {
+    const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+    for (int j = 0; j < PER; j += 2) {
+        uint32_t h;
+        const uint16_t two = (uint16_t)(w[j / 4] >> (8 * (j & 3)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        float lo, hi;
+        asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.f32.f16 %0, a;\ncvt.f32.f16 %1, b;\n}\n"
+            : "=f"(lo), "=f"(hi)
+            : "r"(h));
+        v[j] = lo * scale;
+        v[j + 1] = hi * scale;
+    }
+}
+
+MOK_DEV uint2 load8_u8(const void *p, int64_t i, int64_t n) {
+    const uint8_t *s = static_cast<const uint8_t *>(p) + i;
+    if (i + PER <= n) return *reinterpret_cast<const uint2 *>(s);
+    uint2 q = make_uint2(0, 0);
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        if (i + j < n) (j < 4 ? q.x : q.y) |= (uint32_t)s[j] << (8 * (j & 3));
+    return q;
+}
+MOK_DEV void store8_u8(void *p, int64_t i, int64_t n, uint2 q) {
+    uint8_t *o = static_cast<uint8_t *>(p) + i;
+    if (i + PER <= n) {
+        *reinterpret_cast<uint2 *>(o) = q;
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (i + j < n) o[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+    }
+}
+
+// The MXFP8 encoder. A magnitude y = |x| / scale <= 448 keeps 4 significant bits (E4M3
+// normals, y >= 2^-6): adding 20 bits below the last kept one to its fp32 pattern and cutting
+// there rounds it, the carry moving into the exponent. Subnormals have the step 2^-9, which
+// is the step of the octave [2^-6, 2^-5): adding 2^-6 first moves them there.
+// The random bits are (r + 1/2) / 2^16 of a step.
+template <bool SR, bool POSITIVE>
+MOK_DEV uint32_t encode1(float x, float inv, uint32_t r16) {
+    const float y = fabsf(x) * inv;
+    const bool low = y < 0.015625f;
+    const uint32_t b = __float_as_uint(low ? y + 0.015625f : y);
+    const uint32_t rnd = SR ? (r16 << 4) + 8u : 0x7FFFFu + ((b >> 20) & 1u);
+    uint32_t code = ((b + rnd) >> 20) - (low ? 121u << 3 : 120u << 3);
+    if (POSITIVE) {
+        if (code == 0 && x > 0.f) code = 1;
+        return code;
+    }
+    return code | ((__float_as_uint(x) >> 24) & 0x80u);
+}
+
+// codes of this thread's 8 values; the 4 threads of a 32-element block share the scale, which
+// every one of them returns
+template <bool SR, bool POSITIVE>
+MOK_DEV uint2 encode8(const float (&x)[PER], const uint32_t (&r16)[PER], uint32_t *scale) {
+    uint32_t top = 0;  // as bit patterns: a NaN is the largest
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const uint32_t a = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+        top = a > top ? a : top;
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+        top = a > top ? a : top;
+    }
+    const int ef = (int)(top >> 23);
+    if (ef == 255) {
+        *scale = 255;
+        return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    }
+    int sb = ef - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    sb = sb < 0 ? 0 : sb;
+    *scale = (uint32_t)sb;
+    const float inv = mx_inv_scale((uint32_t)sb);
+    uint32_t q[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        q[j / 4] |= encode1<SR, POSITIVE>(x[j], inv, r16[j]) << (8 * (j & 3));
+    return make_uint2(q[0], q[1]);
+}
+
+template <int NT, bool PF32, bool GF32, bool S8, bool SR>
+__global__ void __launch_bounds__(TPB)
+    adamw_kernel(const __grid_constant__ Params<NT> P) {
+    const Scalars &S = P.s;
+    const float gs = S.gscale != nullptr ? *S.gscale : 1.0f;
+    for (uint32_t c = blockIdx.x; c < S.n_chunks; c += gridDim.x) {
+        int lo = 0, hi = S.n_tensors - 1;  // the last tensor whose first chunk is <= c
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (P.t[mid].first <= c) lo = mid; else hi = mid - 1;
+        }
+        const TensorDesc &t = P.t[lo];
+        const int64_t i = (int64_t)(c - t.first) * CHUNK + (int64_t)threadIdx.x * PER;
+        const int64_t n = t.n;
+        float p[PER], g[PER], m[PER], v[PER];
+        load8<PF32>(t.p, i, n, p);
+        load8<GF32>(t.g, i, n, g);
+        if (S8) {
+            const bool in = i < n;
+            const float sm = in ? mx_scale(t.ms[i >> 5]) : 0.f;
+            const float sv = in ? mx_scale(t.vs[i >> 5]) : 0.f;
+            decode8(load8_u8(t.m, i, n), sm, m);
+            decode8(load8_u8(t.v, i, n), sv, v);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) v[j] *= v[j];
+        } else {
+            load8<true>(t.m, i, n, m);
+            load8<true>(t.v, i, n, v);
+        }
+        uint32_t rp[PER], rm[PER], rv[PER];
+        if (SR) {
+            const int64_t e = t.base + i;  // 8 elements from a multiple of 8: one high word
+            const uint32_t key = mix32(mix32((uint32_t)((uint64_t)e >> 32) ^ S.seed_lo) ^ S.seed_hi);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const uint32_t h = mix32(((uint32_t)e + j) ^ key);
+                rm[j] = h & 0xFFFFu;
+                rv[j] = h >> 16;
+                rp[j] = PF32 ? 0u : mix32(h + 0x9E3779B9u) >> 16;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) rm[j] = rv[j] = rp[j] = 0;
+        }
+        float s[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const float gj = g[j] * gs;
+            m[j] = fmaf(S.a1, gj, S.b1 * m[j]);
+            v[j] = fmaf(S.a2, gj * gj, S.b2 * v[j]);
+            s[j] = sqrtf(v[j]);
+            p[j] = p[j] * t.decay - S.step * m[j] / fmaf(s[j], S.inv_root, S.eps);
+        }
+        if (PF32) {
+            store8_f32(t.p, i, n, p);
+            if (t.copy != nullptr) {
+                const uint32_t w[4] = {pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]),
+                                       pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7])};
+                store8_u16(t.copy, i, n, w);
+            }
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < PER; j += 2)
+                w[j / 2] = SR ? bf16_stochastic(p[j], rp[j]) |
+                                    (bf16_stochastic(p[j + 1], rp[j + 1]) << 16)
+                              : pack_bf16x2(p[j], p[j + 1]);
+            store8_u16(t.p, i, n, w);
+        }
+        if (S8) {
+            if (i + PER > n) {  // what lies past the tensor's end counts for nothing
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (i + j >= n) m[j] = s[j] = 0.f;
+            }
+            uint32_t sm, sv;
+            const uint2 qm = encode8<SR, false>(m, rm, &sm);
+            const uint2 qv = encode8<SR, true>(s, rv, &sv);
+            store8_u8(t.m, i, n, qm);
+            store8_u8(t.v, i, n, qv);
+            if ((threadIdx.x & 3) == 0 && i < n) {
+                t.ms[i >> 5] = (uint8_t)sm;
+                t.vs[i >> 5] = (uint8_t)sv;
+            }
+        } else {
+            store8_f32(t.m, i, n, m);
+            store8_f32(t.v, i, n, v);
+        }
+    }
+}
+
+template <int NT, bool PF32, bool GF32, bool S8, bool SR>
+cudaError_t launch(const Params<NT> &P, cudaStream_t s) {
+    const int64_t cap = (int64_t)device_sm_count() * 64;
+    const unsigned grid = (unsigned)(P.s.n_chunks < cap ? P.s.n_chunks : cap);
+    adamw_kernel<NT, PF32, GF32, S8, SR><<<grid, TPB, 0, s>>>(P);
+    return cudaGetLastError();
+}
+
+template <int NT>
+cudaError_t launch_group(const mok_adamw_config &c, Params<NT> &P, cudaStream_t s) {
+    const bool pf = c.p_dtype == MOK_DTYPE_F32, gf = c.g_dtype == MOK_DTYPE_F32;
+    const bool s8 = c.state == MOK_STATE_MXFP8;
+    const bool sr = (c.flags & MOK_ADAMW_STOCHASTIC) != 0 && (s8 || !pf);
+#define MOK_ADAMW_CASE(p_, g_, s_, r_) \
+    if (pf == p_ && gf == g_ && s8 == s_ && sr == r_) return launch<NT, p_, g_, s_, r_>(P, s)
+    MOK_ADAMW_CASE(true, true, false, false);
+    MOK_ADAMW_CASE(true, false, false, false);
+    MOK_ADAMW_CASE(true, true, true, false);
+    MOK_ADAMW_CASE(true, false, true, false);
+    MOK_ADAMW_CASE(true, true, true, true);
+    MOK_ADAMW_CASE(true, false, true, true);
+    MOK_ADAMW_CASE(false, true, false, false);
+    MOK_ADAMW_CASE(false, false, false, false);
+    MOK_ADAMW_CASE(false, true, false, true);
+    MOK_ADAMW_CASE(false, false, false, true);
+    MOK_ADAMW_CASE(false, true, true, false);
+    MOK_ADAMW_CASE(false, false, true, false);
+    MOK_ADAMW_CASE(false, true, true, true);
+    MOK_ADAMW_CASE(false, false, true, true);
+#undef MOK_ADAMW_CASE
+    return cudaErrorInvalidValue;
+}
+
+// tensors [t0, t1) as one launch; *base: element number of the first, advanced past the last
+template <int NT>
+cudaError_t step_group(const mok_adamw_config &c, const mok_adamw_tensor *ts, int t0, int t1,
+                       const float *gscale, int64_t *base, cudaStream_t s) {
+    Params<NT> P;
+    const double bc1 = 1.0 - pow(c.beta1, (double)c.step);
+    const double bc2 = 1.0 - pow(c.beta2, (double)c.step);
+    P.s.b1 = (float)c.beta1;
+    P.s.a1 = (float)(1.0 - c.beta1);
+    P.s.b2 = (float)c.beta2;
+    P.s.a2 = (float)(1.0 - c.beta2);
+    P.s.step = (float)(c.lr / bc1);
+    P.s.inv_root = (float)(1.0 / sqrt(bc2));
+    P.s.eps = (float)c.eps;
+    P.s.seed_lo = (uint32_t)c.seed;
+    P.s.seed_hi = (uint32_t)(c.seed >> 32);
+    P.s.gscale = gscale;
+    int n = 0;
+    int64_t chunks = 0;
+    for (int i = t0; i < t1; ++i) {
+        const mok_adamw_tensor &t = ts[i];
+        if (t.n == 0) continue;
+        P.t[n++] = TensorDesc{t.p, t.copy, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, *base,
+                              (uint32_t)chunks, (float)(1.0 - c.lr * t.weight_decay)};
+        chunks += (t.n + CHUNK - 1) / CHUNK;
+        *base += (t.n + 31) & ~(int64_t)31;
+    }
+    if (n == 0) return cudaSuccess;
+    if (chunks > 0xFFFFFFFFll) return cudaErrorInvalidValue;
+    P.s.n_tensors = n;
+    P.s.n_chunks = (uint32_t)chunks;
+    return launch_group<NT>(c, P, s);
+}
+
+}  // namespace
+}  // namespace mok
+
+using namespace mok;
+
+extern "C" {
+
+mok_status mok_check_adamw_config(const mok_adamw_config *c) {
+    if (c == nullptr) return MOK_ERR_INVALID_ARG;
+    if (c->abi_version != MOK_ABI_VERSION) return MOK_ERR_ABI;
+    const auto dtype_ok = [](int32_t d) { return d == MOK_DTYPE_BF16 || d == MOK_DTYPE_F32; };
+    if (!dtype_ok(c->p_dtype) || !dtype_ok(c->g_dtype)) return MOK_ERR_INVALID_ARG;
+    if (c->state != MOK_STATE_F32 && c->state != MOK_STATE_MXFP8) return MOK_ERR_INVALID_ARG;
+    if ((c->flags & ~MOK_ADAMW_STOCHASTIC) != 0 || c->step < 1) return MOK_ERR_INVALID_ARG;
+    if (!(c->lr >= 0) || !std::isfinite(c->lr)) return MOK_ERR_INVALID_ARG;
+    if (!(c->eps >= 0) || !std::isfinite(c->eps)) return MOK_ERR_INVALID_ARG;
+    if (!(c->beta1 >= 0 && c->beta1 < 1) || !(c->beta2 >= 0 && c->beta2 < 1))
+        return MOK_ERR_INVALID_ARG;
+    return MOK_OK;
+}
+
+mok_status mok_adamw_step(const mok_adamw_config *c, const mok_adamw_tensor *tensors,
+                          int32_t n_tensors, const float *grad_scale, cudaStream_t stream) {
+    mok_status st = mok_check_adamw_config(c);
+    if (st != MOK_OK) return st;
+    int *status;
+    if ((st = current_device_status_word(&status)) != MOK_OK) return st;
+    if (n_tensors < 0 || (n_tensors > 0 && tensors == nullptr)) return MOK_ERR_INVALID_ARG;
+    const bool s8 = c->state == MOK_STATE_MXFP8;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const mok_adamw_tensor &t = tensors[i];
+        if (t.n < 0 || t.n > ((int64_t)1 << 40) || !std::isfinite(t.weight_decay))
+            return MOK_ERR_INVALID_ARG;
+        if (t.copy != nullptr && c->p_dtype != MOK_DTYPE_F32) return MOK_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (!t.p || !t.g || !t.m || !t.v || (s8 && (!t.m_scale || !t.v_scale)))
+            return MOK_ERR_INVALID_ARG;
+        const void *ps[] = {t.p, t.copy, t.g, t.m, t.v};
+        for (const void *p : ps)
+            if (!aligned16(p)) return MOK_ERR_INVALID_ARG;
+    }
+    int64_t base = 0;
+    for (int t0 = 0; t0 < n_tensors; t0 += NT_LARGE) {
+        const int t1 = n_tensors - t0 < NT_LARGE ? n_tensors : t0 + NT_LARGE;
+        MOK_LAUNCH(KK_ADAMW, 1,
+                   t1 - t0 <= NT_SMALL
+                       ? step_group<NT_SMALL>(*c, tensors, t0, t1, grad_scale, &base, stream)
+                       : step_group<NT_LARGE>(*c, tensors, t0, t1, grad_scale, &base, stream));
+    }
+    return MOK_OK;
+}
+
+}  // extern "C"

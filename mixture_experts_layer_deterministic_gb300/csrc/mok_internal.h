@@ -14,7 +14,7 @@ enum KernelKind {
     KK_QUANTIZE, KK_PAD, KK_GATHER_BWD, KK_GEMM_G, KK_ROUTER_GRAD, KK_GEMM_DGRAD,
     KK_DX_REDUCE, KK_WGRAD13, KK_WGRAD2, KK_SCALE_ATOMS, KK_SHARED_UP, KK_SHARED_DOWN,
     KK_SHARED_BWD, KK_RING_FWD, KK_ROW_MAP, KK_DISPATCH, KK_COMBINE_ROWS, KK_COMBINE_BWD,
-    KK_COUNT
+    KK_ADAMW, KK_COUNT
 };
 // while profiling is on: brackets the launches between begin and end with events
 void prof_begin(int kind, cudaStream_t s);

@@ -12,7 +12,7 @@ const char *const kNames[KK_COUNT] = {
     "combine", "quantize_mxfp8", "pad_offsets", "gather_bwd", "gemm_g_swiglu_bwd",
     "router_grad", "gemm_dgrad_push", "dx_reduce", "wgrad_w13", "wgrad_w2", "scale_atoms",
     "shared_up_swiglu", "shared_down_add", "shared_backward", "ring_forward",
-    "row_map", "dispatch_rows", "combine_rows", "combine_rows_bwd"};
+    "row_map", "dispatch_rows", "combine_rows", "combine_rows_bwd", "adamw"};
 
 struct Rec {
     int kind;

@@ -25,3 +25,18 @@ def rows(**kw):
 ])
 def test_rows_config(kw, want):
     assert B.mok_check_rows_config(rows(**kw)) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(), OK), (dict(lr=0.0), OK), (dict(eps=0.0), OK), (dict(beta1=0.0, beta2=0.0), OK),
+    (dict(state=B.MOK_STATE_MXFP8, flags=B.MOK_ADAMW_STOCHASTIC), OK),
+    (dict(lr=-1.0), BAD), (dict(lr=float("nan")), BAD), (dict(lr=float("inf")), BAD),
+    (dict(beta1=1.0), BAD), (dict(beta2=-0.1), BAD), (dict(beta2=float("nan")), BAD),
+    (dict(eps=-1e-8), BAD), (dict(eps=float("inf")), BAD), (dict(step=0), BAD),
+    (dict(p_dtype=2), BAD), (dict(g_dtype=-1), BAD), (dict(state=2), BAD), (dict(flags=2), BAD),
+    (dict(abi_version=1), B.MOK_ERR_ABI),
+])
+def test_adamw_config(kw, want):
+    base = dict(lr=1e-3)
+    base.update(kw)
+    assert B.mok_check_adamw_config(B.make_adamw(**base)) == want
