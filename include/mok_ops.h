@@ -85,6 +85,77 @@ mok_status mok_combine_backward(const mok_rows_config *cfg, const void *dy, cons
                                 const int32_t *kept, const float *topk_w, void *drows,
                                 float *d_topk_w, cudaStream_t stream);
 
+/* ---- linear layer, for one matrix or one per group of rows ----------------------------
+ *
+ *   z = x W^T + b        y = act(z) + residual
+ *
+ * x [rows][in], W [groups][out][in], b [groups][out]; products in bf16 operands with fp32
+ * accumulation, everything after in fp32, rounded once. Two forms:
+ *  - dense: groups == 1, starts and counts NULL: every row takes W[0];
+ *  - grouped: group g owns rows [starts[g], starts[g] + counts[g]) (int32 device arrays; starts
+ *    [groups+1] are multiples of 16, as mok_build_row_map makes them, starts[g+1] at or past
+ *    starts[g] + counts[g], starts[groups] <= rows). The rows from there to the next multiple
+ *    of 16 are padding: written as zeros in y, z and dx, and read (as zeros) in x and, without
+ *    an activation, dy by the weight gradient, so they must hold zeros there, as mok_dispatch
+ *    and mok_combine_backward write them. Rows past that are neither read nor written. A group
+ *    that breaks these rules raises MOK_ERR_DEVICE_INVARIANT and counts as empty.
+ *
+ * Activations: none; relu; silu z sigma(z); gelu_tanh 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715
+ * z^3))); gelu 0.5 z (1 + erf(z / sqrt 2)).
+ *
+ * Limits: 1 <= groups <= 1024, 1 <= in_features, out_features <= 2^20 (any number, odd ones
+ * among them), 0 <= rows < 2^31 - 512; strides ld_in >= in, ld_w >= in, ld_out >= out are
+ * multiples of 8 elements. Columns past a matrix's width are neither read nor written. */
+typedef enum mok_activation {
+    MOK_ACT_NONE = 0,
+    MOK_ACT_RELU = 1,
+    MOK_ACT_SILU = 2,
+    MOK_ACT_GELU_TANH = 3,
+    MOK_ACT_GELU = 4
+} mok_activation;
+
+typedef struct mok_linear_config {
+    uint32_t abi_version; /* MOK_ABI_VERSION */
+    int32_t groups;
+    int32_t in_features, out_features;
+    int64_t rows;       /* rows of x, y, z, dy, dx */
+    int64_t ld_in;      /* row stride of x and dx */
+    int64_t ld_w;       /* row stride of W and dW (a group is out_features rows) */
+    int64_t ld_out;     /* row stride of y, z, residual and dy */
+    int32_t act;        /* mok_activation */
+    int32_t out_dtype;  /* mok_dtype of y and dy */
+    int32_t grad_dtype; /* mok_dtype of dx and dW */
+    int32_t reserved;   /* 0 */
+} mok_linear_config;
+
+typedef enum mok_linear_pass { MOK_LINEAR_FORWARD = 0, MOK_LINEAR_BACKWARD = 1 } mok_linear_pass;
+
+mok_status mok_check_linear_config(const mok_linear_config *cfg);
+
+/* Bytes of workspace of a pass (256-byte aligned, contents on entry do not matter); 0 for an
+ * invalid configuration. */
+size_t mok_linear_workspace_size(const mok_linear_config *cfg, int pass);
+
+/* Forward. x, w bf16; bias NULL or fp32; residual NULL or [rows][out] bf16 (may be y where y
+ * is bf16); y [rows][out]; z NULL or [rows][out] bf16 out: the value before the activation,
+ * which the backward needs where there is one. */
+mok_status mok_linear_forward(const mok_linear_config *cfg, const void *x, const void *w,
+                              const float *bias, const void *residual, const int32_t *starts,
+                              const int32_t *counts, void *y, void *z, void *ws,
+                              size_t ws_bytes, cudaStream_t stream);
+
+/* Backward, with dz = dy act'(z) (relu'(0) = 0):
+ *   dx = dz W        dW[g] = sum over the group's rows of dz^T x        db[g] = sum of dz
+ * dz is rounded to bf16 where it enters a product (exact where there is no activation and dy is
+ * bf16); db is the fp32 sum of the unrounded dz in a fixed order. The residual's gradient is dy.
+ *   z    [rows][out] bf16 from the forward, or NULL without an activation
+ *   dx   NULL or [rows][in] out; dw NULL or [groups][out][in] out (zero for an empty group);
+ *   db   NULL or [groups][out] fp32 out. At least one of the three. */
+mok_status mok_linear_backward(const mok_linear_config *cfg, const void *x, const void *w,
+                               const void *z, const void *dy, const int32_t *starts,
+                               const int32_t *counts, void *dx, void *dw, float *db, void *ws,
+                               size_t ws_bytes, cudaStream_t stream);
+
 /* ---- AdamW step over many tensors ---------------------------------------------------
  *
  * For every element, with g scaled by *grad_scale (NULL: one) and t = step:

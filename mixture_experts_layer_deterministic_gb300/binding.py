@@ -45,6 +45,17 @@ MOK_WS_SHARED_BACKWARD = 5
 MOK_DTYPE_BF16 = 0
 MOK_DTYPE_F32 = 1
 
+# mok_activation
+MOK_ACT_NONE = 0
+MOK_ACT_RELU = 1
+MOK_ACT_SILU = 2
+MOK_ACT_GELU_TANH = 3
+MOK_ACT_GELU = 4
+
+# mok_linear_pass
+MOK_LINEAR_FORWARD = 0
+MOK_LINEAR_BACKWARD = 1
+
 # mok_adamw_state, mok_adamw_config.flags
 MOK_STATE_F32 = 0
 MOK_STATE_MXFP8 = 1
@@ -77,6 +88,8 @@ EXPORTED = [
     "mok_selftest_bounded_wait", "mok_selftest_bounded_count_wait", "mok_workspace_item",
     "mok_check_rows_config", "mok_build_row_map", "mok_dispatch", "mok_dispatch_backward",
     "mok_combine", "mok_combine_backward", "mok_check_adamw_config", "mok_adamw_step",
+    "mok_check_linear_config", "mok_linear_workspace_size", "mok_linear_forward",
+    "mok_linear_backward",
 ]
 
 # bytes of the fixed scratch array behind mok_build_schedule_noalloc
@@ -102,6 +115,15 @@ class MokRowsConfig(ctypes.Structure):
                 ("capacity", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("n_rows", ctypes.c_int64), ("ld_tok", ctypes.c_int64),
                 ("ld_row", ctypes.c_int64)]
+
+
+class MokLinearConfig(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("groups", ctypes.c_int32),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("ld_in", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("act", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class MokAdamwConfig(ctypes.Structure):
@@ -154,6 +176,7 @@ def lib():
         cfgp = ctypes.POINTER(MokConfig)
         schp = ctypes.POINTER(MokSchedule)
         rowsp = ctypes.POINTER(MokRowsConfig)
+        linp = ctypes.POINTER(MokLinearConfig)
         adamp = ctypes.POINTER(MokAdamwConfig)
         sig = {
             "mok_abi_version": ([], ctypes.c_uint32),
@@ -194,6 +217,10 @@ def lib():
             "mok_dispatch_backward": ([rowsp, p, p, p, p], ctypes.c_int),
             "mok_combine": ([rowsp, p, p, p, p, p, p], ctypes.c_int),
             "mok_combine_backward": ([rowsp, p, p, p, p, p, p, p, p, p], ctypes.c_int),
+            "mok_check_linear_config": ([linp], ctypes.c_int),
+            "mok_linear_workspace_size": ([linp, ctypes.c_int], sz),
+            "mok_linear_forward": ([linp, p, p, p, p, p, p, p, p, p, sz, p], ctypes.c_int),
+            "mok_linear_backward": ([linp, p, p, p, p, p, p, p, p, p, p, sz, p], ctypes.c_int),
             "mok_check_adamw_config": ([adamp], ctypes.c_int),
             "mok_adamw_step": ([adamp, ctypes.POINTER(MokAdamwTensor), i32, p, p],
                                ctypes.c_int),
@@ -242,6 +269,18 @@ def make_rows(T, K, E, H, n_rows=None, dtype=MOK_DTYPE_BF16, ld_tok=None, ld_row
         n_rows = T * K + 15 * min(E, T * K)
     return MokRowsConfig(abi_version, T, K, E, H, dtype, capacity, 0, n_rows,
                          H if ld_tok is None else ld_tok, H if ld_row is None else ld_row)
+
+
+def make_linear(rows, in_features, out_features, groups=1, act=MOK_ACT_NONE,
+                out_dtype=MOK_DTYPE_BF16, grad_dtype=MOK_DTYPE_BF16, ld_in=None, ld_w=None,
+                ld_out=None, abi_version=MOK_ABI_VERSION) -> MokLinearConfig:
+    """Configuration of a linear layer; rows at the next multiple of 8 elements unless given."""
+    up8 = lambda n: (n + 7) // 8 * 8  # noqa: E731
+    return MokLinearConfig(abi_version, groups, in_features, out_features, rows,
+                           up8(in_features) if ld_in is None else ld_in,
+                           up8(in_features) if ld_w is None else ld_w,
+                           up8(out_features) if ld_out is None else ld_out, act, out_dtype,
+                           grad_dtype, 0)
 
 
 def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0, p_dtype=MOK_DTYPE_F32,
@@ -440,6 +479,28 @@ def mok_combine_backward(cfg, dy, rows, row_map, starts, kept, topk_w, drows, d_
     return lib().mok_combine_backward(ctypes.byref(cfg), _ptr(dy), _ptr(rows), _ptr(row_map),
                                       _ptr(starts), _ptr(kept), _ptr(topk_w), _ptr(drows),
                                       _ptr(d_topk_w), _stream(stream))
+
+
+def mok_check_linear_config(cfg) -> int:
+    return lib().mok_check_linear_config(ctypes.byref(cfg))
+
+
+def mok_linear_workspace_size(cfg, which) -> int:
+    return int(lib().mok_linear_workspace_size(ctypes.byref(cfg), int(which)))
+
+
+def mok_linear_forward(cfg, x, w, bias, residual, starts, counts, y, z, ws, ws_bytes,
+                       stream=None) -> int:
+    return lib().mok_linear_forward(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(bias),
+                                    _ptr(residual), _ptr(starts), _ptr(counts), _ptr(y),
+                                    _ptr(z), _ptr(ws), int(ws_bytes), _stream(stream))
+
+
+def mok_linear_backward(cfg, x, w, z, dy, starts, counts, dx, dw, db, ws, ws_bytes,
+                        stream=None) -> int:
+    return lib().mok_linear_backward(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(z), _ptr(dy),
+                                     _ptr(starts), _ptr(counts), _ptr(dx), _ptr(dw), _ptr(db),
+                                     _ptr(ws), int(ws_bytes), _stream(stream))
 
 
 def mok_check_adamw_config(cfg) -> int:

@@ -14,7 +14,7 @@
 #include <cmath>
 
 #include "common.cuh"
-#include "mok_internal.h"
+#include "ops_internal.h"
 
 namespace mok {
 namespace {
@@ -407,12 +407,12 @@ mok_status mok_adamw_step(const mok_adamw_config *c, const mok_adamw_tensor *ten
             return MOK_ERR_INVALID_ARG;
         const void *ps[] = {t.p, t.copy, t.g, t.m, t.v};
         for (const void *p : ps)
-            if (!aligned16(p)) return MOK_ERR_INVALID_ARG;
+            if (!op_aligned16(p)) return MOK_ERR_INVALID_ARG;
     }
     int64_t base = 0;
     for (int t0 = 0; t0 < n_tensors; t0 += NT_LARGE) {
         const int t1 = n_tensors - t0 < NT_LARGE ? n_tensors : t0 + NT_LARGE;
-        MOK_LAUNCH(KK_ADAMW, 1,
+        MOK_OP_LAUNCH(OP_ADAMW, 1,
                    t1 - t0 <= NT_SMALL
                        ? step_group<NT_SMALL>(*c, tensors, t0, t1, grad_scale, &base, stream)
                        : step_group<NT_LARGE>(*c, tensors, t0, t1, grad_scale, &base, stream));

@@ -38,6 +38,8 @@ mok_status check_device(int **status) {
     return MOK_OK;
 }
 
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
 // values that are only stored are fp32 under MOK_FLAG_FP32_STORAGE, else bf16
 bool f32_storage(const mok_config *c) { return (c->flags & MOK_FLAG_FP32_STORAGE) != 0; }
 size_t stored_bytes(const mok_config *c) { return f32_storage(c) ? 4 : 2; }
@@ -339,6 +341,15 @@ int device_sm_count() {
     return n;
 }
 }  // namespace mok
+
+// a launch of `nk` kernels of one kind, bracketed by events while profiling is on
+#define MOK_LAUNCH(kind, nk, expr)                         \
+    do {                                                   \
+        prof_begin(kind, stream);                          \
+        cudaError_t _e = (expr);                           \
+        prof_end(kind, stream, nk);                        \
+        if (_e != cudaSuccess) return MOK_ERR_CUDA;        \
+    } while (0)
 
 extern "C" {
 

@@ -1,0 +1,955 @@
+// linear.cu -- a linear layer for one matrix or one per group of rows: products with bias,
+// activation and residual in the epilogue, and their gradients.
+//
+//   forward   z = x W^T + b, y = act(z) + residual
+//   backward  dz = dy act'(z), dx = dz W, dW = dz^T x, db = sum of dz over the rows
+//
+// The three products run on pairs of SMs (tcgen05 cta_group::2, M = 256): the dimension that is
+// contiguous in the output (features of y, inputs of dx and dW) lies on M, so a warp's 32 TMEM
+// lanes store consecutive elements, and the rows of x (or the features of dW) lie on N, so a
+// ragged group costs at most 15 padding rows.
+//   Fwd  A = W    (K-major),  B = x   (K-major)   -> y (and z)   [features x rows]
+//   Dx   A = W    (MN-major), B = dz  (K-major)   -> dx          [inputs x rows]
+//   Dw   A = x    (MN-major), B = dz  (MN-major)  -> dW          [inputs x features]
+// W is a 3D tensor map (inputs, features, groups), so a tile past a matrix's edge reads zeros,
+// not the next group's matrix. Every output element is one fixed-order fp32 sum.
+//
+// Per CTA, 320 threads: warp 0 loads (TMA, both CTAs), warp 1 issues the MMAs (rank 0), warps
+// 2-9 drain accumulators, two sets of 256 TMEM columns alternating between units. Every wait is
+// bounded (2 s), after which MOK_ERR_TIMEOUT is recorded and the launch ends.
+#include "gemm_tc_core.cuh"
+#include "ops_internal.h"
+
+namespace mok {
+namespace {
+
+constexpr int BOX = 64 * 128;      // one 64 x 64 bf16 box (8 KB)
+constexpr int LSTAGES = 6;
+constexpr int LSTAGE_BYTES = 4 * BOX;
+constexpr uint32_t SET_COLS = 256; // TMEM columns of one accumulator set
+constexpr int LTILE = 256;         // most rows of a tile
+constexpr int SEG_K = 1024;        // fp32 outputs: K elements per accumulation segment
+constexpr int MAX_G = 1024;
+
+// ---------------------------------------------------------------- row tiles
+// A tile is up to `height` consecutive rows of one group. Dense: tile t covers rows
+// [t height, ..). Grouped: a list built on the device, int32 [cap][4] = (group, first row,
+// end row, 1 if the group's last), its count at list[-4].
+struct Tiles {
+    const int32_t *list;  // nullptr: dense
+    int64_t cap;
+    int64_t rows;
+    int height;
+    MOK_DEV int64_t count() const {
+        if (list == nullptr) return (rows + height - 1) / height;
+        return list[-4] < cap ? list[-4] : cap;
+    }
+    // pad: whether the tile's last rows are followed by padding up to a multiple of 16
+    MOK_DEV void get(int64_t t, int *g, int64_t *r0, int64_t *r1, bool *pad) const {
+        if (list == nullptr) {
+            *g = 0;
+            *r0 = t * height;
+            *r1 = *r0 + height < rows ? *r0 + height : rows;
+            *pad = false;
+        } else {
+            *g = list[4 * t];
+            *r0 = list[4 * t + 1];
+            *r1 = list[4 * t + 2];
+            *pad = list[4 * t + 3] != 0;
+        }
+    }
+};
+
+// Each group's rows in tiles of equal height (a multiple of 16, at most LTILE); valid[g] gets
+// the group's row count, 0 where its layout breaks the rules.
+__global__ void __launch_bounds__(MAX_G)
+    linear_tiles_kernel(const int32_t *__restrict__ starts, const int32_t *__restrict__ counts,
+                        int G, int64_t rows, int32_t *__restrict__ list, int64_t cap,
+                        int32_t *__restrict__ valid, int *status) {
+    __shared__ int32_t wsum[MAX_G / 32];
+    const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
+    int64_t b = 0, n = 0, h = LTILE;
+    int32_t nt = 0;
+    if (g < G) {
+        b = starts[g];
+        n = counts[g];
+        const int64_t e = starts[g + 1];
+        // the padding after the rows is written too, so it has to lie inside the group
+        if (n < 0 || b < 0 || (b & 15) != 0 || b + ((n + 15) & ~(int64_t)15) > e || e > rows) {
+            raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+            n = 0;
+        }
+        valid[g] = (int32_t)n;
+        if (n > 0) {
+            const int64_t n0 = (n + LTILE - 1) / LTILE;
+            h = ((n + n0 - 1) / n0 + 15) & ~(int64_t)15;
+            nt = (int32_t)((n + h - 1) / h);
+        }
+    }
+    int32_t v = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+    }
+    if (lane == 31) wsum[warp] = v;
+    __syncthreads();
+    int32_t at = v - nt;
+    for (int w = 0; w < warp; ++w) at += wsum[w];
+    if (g == MAX_G - 1) {
+        // overlapping groups can ask for more tiles than there are rows for
+        const int32_t total = at + nt;
+        list[-4] = (int32_t)(total < cap ? total : cap);
+        if (total > cap) raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+    }
+    for (int32_t i = 0; i < nt; ++i) {
+        const int64_t s = (int64_t)at + i;
+        if (s >= cap) break;
+        const int64_t r0 = b + i * h, r1 = r0 + h < b + n ? r0 + h : b + n;
+        reinterpret_cast<int4 *>(list)[s] =
+            make_int4(g, (int32_t)r0, (int32_t)r1, i == nt - 1 ? 1 : 0);
+    }
+}
+
+int64_t tiles_cap(int64_t rows, int G) { return G + rows / 16 / (LTILE / 16) + 1; }
+
+// ---------------------------------------------------------------- activations
+MOK_DEV float sigmoid_f(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+constexpr float GELU_C2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float GELU_A = 0.044715f;
+
+// 0.5 (1 + tanh u) = sigma(2u): gelu_tanh is z sigma(2 sqrt(2/pi) (z + a z^3))
+MOK_DEV float act_f(float z, int act) {
+    switch (act) {
+        case MOK_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
+        case MOK_ACT_SILU: return z * sigmoid_f(z);
+        case MOK_ACT_GELU_TANH: return z * sigmoid_f(GELU_C2 * fmaf(GELU_A * z * z, z, z));
+        case MOK_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    }
+    return z;
+}
+MOK_DEV float act_grad_f(float z, int act) {
+    switch (act) {
+        case MOK_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+        case MOK_ACT_SILU: {
+            const float s = sigmoid_f(z);
+            return s * fmaf(z, 1.0f - s, 1.0f);
+        }
+        case MOK_ACT_GELU_TANH: {
+            const float s = sigmoid_f(GELU_C2 * fmaf(GELU_A * z * z, z, z));
+            const float du = GELU_C2 * fmaf(3.0f * GELU_A * z, z, 1.0f);
+            return s * fmaf(z * (1.0f - s), du, 1.0f);
+        }
+        case MOK_ACT_GELU:
+            return fmaf(z, 0.3989422804014327f * expf(-0.5f * z * z),
+                        0.5f * erfcf(-0.70710678118654752f * z));
+    }
+    return 1.f;
+}
+
+// ---------------------------------------------------------------- the engine
+struct LinSmem {
+    uint64_t full[LSTAGES];   // rank 0: both CTAs' copies of the stage have landed
+    uint64_t empty[LSTAGES];  // each CTA: the MMAs that read the stage are done
+    uint64_t tmem_full[2];    // each CTA: accumulator set b holds a finished unit
+    uint64_t tmem_empty[2];   // rank 0: both CTAs' epilogues have drained set b
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr int LIN_SMEM = LSTAGES * LSTAGE_BYTES + 1024 + (int)sizeof(LinSmem);
+static_assert(LIN_SMEM <= 232448, "shared memory of a CTA");
+
+// one unit as one CTA of the pair loads and multiplies it
+struct LinGeom {
+    int32_t a0, a1, a2;  // A coordinates (per policy)
+    int32_t b0, b1;      // B coordinates
+    int nbox;            // MN-major B: 64-column boxes per CTA
+    int n_mma;           // N of each MMA
+    int k_steps;         // 16-element K steps
+};
+
+MOK_DEV void tma_load_3d_pair(void *smem_dst, const CUtensorMap *m, uint32_t bar_cluster,
+                              int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(tc::smem_u32(smem_dst)),
+        "l"((uint64_t)m), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+MOK_DEV void ld32(uint32_t c, float (&v)[32]) {
+    float a[16], b[16];
+    tc::tmem_ld16(c, a);
+    tc::tmem_ld16(c + 16, b);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        v[j] = a[j];
+        v[16 + j] = b[j];
+    }
+}
+
+struct Fwd {
+    static constexpr bool A_MN = false, B_MN = false;
+    Tiles tiles;
+    int n_mb;      // ceil(N / 256)
+    int segs;      // accumulation segments per unit (fp32 outputs), else 1
+    int Kin, N;
+    int64_t ld;    // row stride of y, z and residual
+    const float *bias;
+    const uint16_t *res;
+    void *y;
+    uint16_t *z;
+    int act;
+    bool y_f32;
+    int *status;
+
+    MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
+    MOK_DEV LinGeom geom(int64_t u, int seg, uint32_t rank) const {
+        int g;
+        int64_t r0, r1;
+        bool pad;
+        tiles.get(u / n_mb, &g, &r0, &r1, &pad);
+        LinGeom q;
+        q.n_mma = (int)((r1 - r0 + 15) & ~15);
+        q.a0 = seg * SEG_K;
+        q.a1 = (int)(u % n_mb) * 256 + (int)rank * 128;
+        q.a2 = g;
+        q.b0 = q.a0;
+        q.b1 = (int32_t)r0 + (int)rank * (q.n_mma / 2);
+        q.nbox = 1;
+        const int k = segs > 1 && Kin - q.a0 > SEG_K ? SEG_K : Kin - q.a0;
+        q.k_steps = (k + 15) / 16;
+        return q;
+    }
+    MOK_DEV uint32_t tx(const LinGeom &) const { return 4 * BOX; }
+    // A: 128 features x 64 inputs; B: 128 rows x 64 inputs, of which n_mma / 2 rows are used
+    MOK_DEV void load(uint8_t *st, uint32_t fb, const LinGeom &q, int k0, const CUtensorMap *tmA,
+                      const CUtensorMap *tmB) const {
+        tma_load_3d_pair(st, tmA, fb, q.a0 + k0, q.a1, q.a2);
+        tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, q.b0 + k0, q.b1);
+    }
+    MOK_DEV void epilogue(int64_t u, int seg, uint32_t rank, uint32_t c, int q, int hw,
+                          int lane) const {
+        int g;
+        int64_t r0, r1;
+        bool pad;
+        tiles.get(u / n_mb, &g, &r0, &r1, &pad);
+        const int nr = (int)(r1 - r0);
+        const int n_mma = (nr + 15) & ~15;
+        const int n_out = pad ? n_mma : nr;  // rows to write (the padding as zeros)
+        const int f = (int)(u % n_mb) * 256 + (int)rank * 128 + q * 32 + lane;
+        const bool ok = f < N;
+        const bool last = seg == segs - 1;
+        const float b = bias != nullptr && ok ? bias[(int64_t)g * N + f] : 0.f;
+        for (int n0 = 32 * hw; n0 < n_mma; n0 += 64) {
+            float v[32];
+            ld32(c + n0, v);
+            if (!ok) continue;
+            const int64_t o = (r0 + n0) * ld + f;
+            if (seg > 0) {  // the sum of the earlier segments, left in y by this thread
+                float a[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    a[j] = n0 + j < nr ? static_cast<const float *>(y)[o + (int64_t)j * ld] : 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += a[j];
+            }
+            if (!last) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (n0 + j < nr) static_cast<float *>(y)[o + (int64_t)j * ld] = v[j];
+                continue;
+            }
+            float rs[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                rs[j] = res != nullptr && n0 + j < nr ? bf16_to_f32(res[o + (int64_t)j * ld]) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                if (n0 + j >= n_out) continue;
+                const bool real = n0 + j < nr;
+                const float zv = real ? v[j] + b : 0.f;
+                if (z != nullptr) z[o + (int64_t)j * ld] = f32_to_bf16(zv);
+                st_val(y, o + (int64_t)j * ld, real ? act_f(zv, act) + rs[j] : 0.f, y_f32);
+            }
+        }
+    }
+};
+
+struct Dx {
+    static constexpr bool A_MN = true, B_MN = false;
+    Tiles tiles;
+    int n_mb;     // ceil(Kin / 256)
+    int segs;     // 1
+    int Kin, N;
+    int64_t ld;   // row stride of dx
+    void *dx;
+    bool f32;
+    int *status;
+
+    MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
+    MOK_DEV LinGeom geom(int64_t u, int, uint32_t rank) const {
+        int g;
+        int64_t r0, r1;
+        bool pad;
+        tiles.get(u / n_mb, &g, &r0, &r1, &pad);
+        LinGeom q;
+        q.n_mma = (int)((r1 - r0 + 15) & ~15);
+        q.a0 = (int)(u % n_mb) * 256 + (int)rank * 128;
+        q.a1 = 0;
+        q.a2 = g;
+        q.b0 = 0;
+        q.b1 = (int32_t)r0 + (int)rank * (q.n_mma / 2);
+        q.nbox = 1;
+        q.k_steps = (N + 15) / 16;
+        return q;
+    }
+    MOK_DEV uint32_t tx(const LinGeom &) const { return 4 * BOX; }
+    // A: two boxes of 64 inputs x 64 features; B: 128 rows x 64 features of dz
+    MOK_DEV void load(uint8_t *st, uint32_t fb, const LinGeom &q, int k0, const CUtensorMap *tmA,
+                      const CUtensorMap *tmB) const {
+        tma_load_3d_pair(st, tmA, fb, q.a0, k0, q.a2);
+        tma_load_3d_pair(st + BOX, tmA, fb, q.a0 + 64, k0, q.a2);
+        tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, k0, q.b1);
+    }
+    MOK_DEV void epilogue(int64_t u, int, uint32_t rank, uint32_t c, int q, int hw,
+                          int lane) const {
+        int g;
+        int64_t r0, r1;
+        bool pad;
+        tiles.get(u / n_mb, &g, &r0, &r1, &pad);
+        const int nr = (int)(r1 - r0);
+        const int n_mma = (nr + 15) & ~15;
+        const int n_out = pad ? n_mma : nr;
+        const int i = (int)(u % n_mb) * 256 + (int)rank * 128 + q * 32 + lane;
+        for (int n0 = 32 * hw; n0 < n_mma; n0 += 64) {
+            float v[32];
+            ld32(c + n0, v);
+            if (i >= Kin) continue;
+            const int64_t o = (r0 + n0) * ld + i;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (n0 + j < n_out) st_val(dx, o + (int64_t)j * ld, n0 + j < nr ? v[j] : 0.f, f32);
+        }
+    }
+};
+
+struct Dw {
+    static constexpr bool A_MN = true, B_MN = true;
+    const int32_t *starts, *valid;  // grouped: first row and row count of each group
+    int64_t rows;                   // dense
+    int G, n_mb, n_nb;              // ceil(Kin / 256), ceil(N / 256)
+    int segs;                       // 1
+    int Kin, N;
+    int64_t ld;                     // row stride of dW
+    void *dw;
+    bool f32;
+    int *status;
+
+    MOK_DEV int64_t n_units() const { return (int64_t)G * n_mb * n_nb; }
+    MOK_DEV void get(int64_t u, int *g, int *mb, int *nb) const {
+        *g = (int)(u / ((int64_t)n_mb * n_nb));
+        const int rest = (int)(u % ((int64_t)n_mb * n_nb));
+        *nb = rest / n_mb;
+        *mb = rest % n_mb;
+    }
+    MOK_DEV int64_t count(int g) const { return valid != nullptr ? valid[g] : rows; }
+    MOK_DEV LinGeom geom(int64_t u, int, uint32_t rank) const {
+        int g, mb, nb;
+        get(u, &g, &mb, &nb);
+        LinGeom q;
+        // MN-major B comes in boxes of 64 columns per CTA: N of the MMA is 128 or 256, columns
+        // past the matrix being zeros
+        q.n_mma = N - nb * 256 <= 128 ? 128 : 256;
+        q.nbox = q.n_mma / 128;
+        q.a0 = mb * 256 + (int)rank * 128;
+        q.a1 = starts != nullptr ? starts[g] : 0;
+        q.a2 = 0;
+        q.b0 = nb * 256 + (int)rank * (q.n_mma / 2);
+        q.b1 = q.a1;
+        q.k_steps = (int)((count(g) + 15) / 16);
+        return q;
+    }
+    MOK_DEV uint32_t tx(const LinGeom &q) const { return (2 + q.nbox) * BOX; }
+    MOK_DEV void load(uint8_t *st, uint32_t fb, const LinGeom &q, int k0, const CUtensorMap *tmA,
+                      const CUtensorMap *tmB) const {
+        tc::tma_load_2d_pair(st, tmA, fb, q.a0, q.a1 + k0);
+        tc::tma_load_2d_pair(st + BOX, tmA, fb, q.a0 + 64, q.a1 + k0);
+        for (int j = 0; j < q.nbox; ++j)
+            tc::tma_load_2d_pair(st + (2 + j) * BOX, tmB, fb, q.b0 + 64 * j, q.b1 + k0);
+    }
+    MOK_DEV void epilogue(int64_t u, int, uint32_t rank, uint32_t c, int q, int hw,
+                          int lane) const {
+        int g, mb, nb;
+        get(u, &g, &mb, &nb);
+        const int nn = N - nb * 256 < 256 ? N - nb * 256 : 256;
+        const bool any = count(g) > 0;
+        const int i = mb * 256 + (int)rank * 128 + q * 32 + lane;
+        for (int n0 = 32 * hw; n0 < nn; n0 += 64) {
+            float v[32];
+            ld32(c + n0, v);
+            if (i >= Kin) continue;
+            const int64_t o = ((int64_t)g * N + nb * 256 + n0) * ld + i;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (n0 + j < nn) st_val(dw, o + (int64_t)j * ld, any ? v[j] : 0.f, f32);
+        }
+    }
+};
+
+MOK_DEV bool lin_wait(uint64_t *bar, uint32_t parity, int *status, volatile int *abort) {
+    return tc::wait_bounded_cluster(bar, parity, status, abort, tc::WAIT_LIMIT_NS);
+}
+// bounded drain of a barrier phase on the way out
+MOK_DEV void lin_drain(uint64_t *bar, uint32_t parity) {
+    const uint64_t t0 = tc::globaltimer();
+    while (!tc::mbar_try_wait_cluster(bar, parity) && tc::globaltimer() - t0 < 100000000ull) {
+    }
+}
+
+template <class P>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tmA,
+                  const __grid_constant__ CUtensorMap tmB, const P p) {
+    constexpr int NS = LSTAGES, SB = LSTAGE_BYTES;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    LinSmem *sm = (LinSmem *)(base + NS * SB);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int64_t cid = tc::cluster_id_x(), ncl = tc::cluster_count_x();
+    const int64_t n_units = p.n_units();
+    const int segs = p.segs;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            tc::mbar_init(&sm->full[s], 1);
+            tc::mbar_init(&sm->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&sm->tmem_full[b], 1);
+            tc::mbar_init(&sm->tmem_empty[b], 2 * EPI_WARPS);
+        }
+        sm->abort = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_tmap(&tmA);
+        tc::prefetch_tmap(&tmB);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc_pair(&sm->tmem_base, TMEM_COLS);
+        tc::tmem_relinquish_pair();
+    }
+    // both CTAs' barriers exist and TMEM is allocated before either CTA touches the other
+    tc::tc_fence_before();
+    tc::cluster_sync();
+    tc::tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;
+    volatile int *abort = &sm->abort;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (tc::elect_one()) {
+            const uint32_t full0 = tc::cluster_addr(&sm->full[0], 0);  // rank 0's full[0]
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int64_t u = cid; u < n_units && ok; u += ncl)
+                for (int seg = 0; seg < segs && ok; ++seg) {
+                    const LinGeom g = p.geom(u, seg, rank);
+                    const uint32_t tx = p.tx(g);
+                    const int kblocks = (g.k_steps + 3) / 4;
+                    for (int kb = 0; kb < kblocks; ++kb) {
+                        if (!lin_wait(&sm->empty[s], ph ^ 1u, p.status, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&sm->full[s], 2 * tx);
+                        p.load(base + s * SB, full0 + (uint32_t)s * 8u, g, kb * BK, &tmA, &tmB);
+                        ++issued;
+                        if (++s == NS) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+            // do not leave while copies may still be landing: the MMAs that read the last
+            // stages have finished (bounded)
+            for (int q = 0; q < NS && q < issued; ++q) {
+                if (--s < 0) {
+                    s = NS - 1;
+                    ph ^= 1u;
+                }
+                lin_drain(&sm->empty[s], ph);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (rank 0)
+        if (rank == 0 && tc::elect_one()) {
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t a = 0;  // accumulations so far: number a uses set a % 2
+            bool ok = true;
+            for (int64_t u = cid; u < n_units && ok; u += ncl)
+                for (int seg = 0; seg < segs && ok; ++seg) {
+                    const LinGeom g = p.geom(u, seg, 0);
+                    const uint32_t idesc = tc::idesc_bf16(256, g.n_mma, P::A_MN, P::B_MN);
+                    const int ab = (int)(a & 1);
+                    const uint32_t use = (uint32_t)((a >> 1) & 1);
+                    if (!lin_wait(&sm->tmem_empty[ab], use ^ 1u, p.status, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)ab * SET_COLS;
+                    const int kblocks = (g.k_steps + 3) / 4;
+                    for (int kb = 0; kb < kblocks; ++kb) {
+                        if (!lin_wait(&sm->full[s], ph, p.status, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::tc_fence_after();
+                        const uint32_t sa = tc::smem_u32(base + s * SB);
+                        const uint32_t sb = sa + 2 * BOX;
+                        const int steps = g.k_steps - kb * 4 < 4 ? g.k_steps - kb * 4 : 4;
+                        for (int kk = 0; kk < steps; ++kk) {
+                            // MN-major: 16 K rows = 2 groups of eight 128-byte rows, blocks of
+                            // 64 M or N elements BOX apart; K-major: 32 bytes along the row
+                            const uint64_t da = P::A_MN
+                                                    ? tc::sdesc_sw128(sa + kk * 2048, BOX, 1024)
+                                                    : tc::sdesc_sw128(sa + kk * 32, 16, 1024);
+                            const uint64_t db = P::B_MN
+                                                    ? tc::sdesc_sw128(sb + kk * 2048, BOX, 1024)
+                                                    : tc::sdesc_sw128(sb + kk * 32, 16, 1024);
+                            tc::mma_f16_pair(d, da, db, idesc, kb > 0 || kk > 0 ? 1u : 0u);
+                        }
+                        tc::mma_commit_pair(&sm->empty[s], 3);  // frees the stage in both CTAs
+                        if (++s == NS) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    tc::mma_commit_pair(&sm->tmem_full[ab], 3);
+                    ++a;
+                }
+            // do not free TMEM under MMAs still in flight (bounded)
+            if (a > 0) {
+                const int lb = (int)((a - 1) & 1);
+                lin_drain(&sm->tmem_full[lb], (uint32_t)(((a - 1) >> 1) & 1));
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;          // TMEM lane quadrant this warp may access
+        const int hw = (warp - 2) >> 2;  // which alternate 32-column chunks it takes
+        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        const uint32_t empty0 = tc::cluster_addr(&sm->tmem_empty[0], 0);
+        int64_t a = 0;
+        bool ok = true;
+        for (int64_t u = cid; u < n_units && ok; u += ncl)
+            for (int seg = 0; seg < segs; ++seg, ++a) {
+                const int ab = (int)(a & 1);
+                if (!lin_wait(&sm->tmem_full[ab], (uint32_t)((a >> 1) & 1), p.status, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc::tc_fence_after();
+                p.epilogue(u, seg, rank, tmem + lane_base + (uint32_t)ab * SET_COLS, q, hw, lane);
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(empty0 + (uint32_t)ab * 8u);
+            }
+    }
+
+    // no MMA, copy or arrival of either CTA targets the other past this point
+    tc::tc_fence_before();
+    tc::cluster_sync();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc_pair(tmem, TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------- dz and the bias gradient
+// dz = dy act'(z) in bf16 (the products' operand), and per tile the column sums of the unrounded
+// dz. One block per (tile, 64 columns): 8 threads side by side on 8 columns each, 32 row
+// lanes; the sums of a column's 32 row lanes are added in lane order.
+template <bool DY32>
+__global__ void __launch_bounds__(256)
+    linear_dz_kernel(const void *__restrict__ dy, const uint16_t *__restrict__ z, Tiles tiles,
+                     int N, int64_t ld, int act, uint16_t *__restrict__ dz, int64_t ld_dz,
+                     float *__restrict__ part) {
+    __shared__ float red[32][65];
+    const int64_t t = blockIdx.x;
+    if (t >= tiles.count()) return;
+    int g;
+    int64_t r0, r1;
+    bool pad;
+    tiles.get(t, &g, &r0, &r1, &pad);
+    const int64_t rend = pad ? (r1 + 15) & ~(int64_t)15 : r1;
+    const int cv = threadIdx.x & 7, rl = threadIdx.x >> 3;
+    const int c = blockIdx.y * 64 + cv * 8;
+    float sum[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+    for (int64_t r = r0 + rl; r < rend; r += 32) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        const bool whole = c + 8 <= N;
+        if (r < r1 && c < N) {
+            const int64_t o = r * ld + c;
+            float zz[8];
+            if (whole) {
+                if (DY32) {
+                    const float4 *s = reinterpret_cast<const float4 *>(
+                        static_cast<const float *>(dy) + o);
+                    const float4 a = s[0], b = s[1];
+                    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+                } else {
+                    const uint4 a = ldg_nc_v4(static_cast<const uint16_t *>(dy) + o);
+                    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[2 * j] = bf16_lo(w[j]);
+                        v[2 * j + 1] = bf16_hi(w[j]);
+                    }
+                }
+                if (act != MOK_ACT_NONE) {
+                    const uint4 a = ldg_nc_v4(z + o);
+                    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        zz[2 * j] = bf16_lo(w[j]);
+                        zz[2 * j + 1] = bf16_hi(w[j]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool in = c + j < N;
+                    v[j] = !in ? 0.f
+                           : DY32 ? static_cast<const float *>(dy)[o + j]
+                                  : bf16_to_f32(static_cast<const uint16_t *>(dy)[o + j]);
+                    zz[j] = in && act != MOK_ACT_NONE ? bf16_to_f32(z[o + j]) : 0.f;
+                }
+            }
+            if (act != MOK_ACT_NONE) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= act_grad_f(zz[j], act);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += c + j < N ? v[j] : 0.f;
+        }
+        if (dz != nullptr && c < N) {
+            uint16_t *o = dz + r * ld_dz + c;  // ld_dz is a multiple of 8: whole vectors
+            *reinterpret_cast<uint4 *>(o) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        }
+    }
+    if (part == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[rl][cv * 8 + j] = sum[j];
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const int col = blockIdx.y * 64 + threadIdx.x;
+        float a = 0.f;
+        for (int i = 0; i < 32; ++i) a += red[i][threadIdx.x];
+        if (col < N) part[t * N + col] = a;
+    }
+}
+
+// db[g][n] = the sum of the tiles' parts in tile order (a group's tiles are consecutive)
+__global__ void __launch_bounds__(256)
+    linear_db_kernel(const float *__restrict__ part, Tiles tiles, int G, int N,
+                     float *__restrict__ db) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)G * N) return;
+    const int g = (int)(i / N), n = (int)(i % N);
+    const int64_t nt = tiles.count();
+    int64_t t = 0;
+    if (tiles.list != nullptr) {  // the group's first tile
+        int64_t lo = 0, hi = nt;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (tiles.list[4 * mid] < g) lo = mid + 1; else hi = mid;
+        }
+        t = lo;
+    }
+    float a = 0.f;
+    for (; t < nt && (tiles.list == nullptr || tiles.list[4 * t] == g); ++t) a += part[t * N + n];
+    db[i] = a;
+}
+
+// ---------------------------------------------------------------- host side
+// bf16 matrix of `rows` rows of `cols` elements, `ld` apart; boxes of 64 columns x box_rows
+cudaError_t map2d(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t ld,
+                  int box_rows) {
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides,
+                  box, es) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+// W [G][N][Kin]: (inputs, features, groups), boxes of 64 inputs x box_rows features
+cudaError_t map_w(CUtensorMap *m, const void *p, int64_t G, int64_t N, int64_t Kin, int64_t ld,
+                  int box_rows) {
+    cuuint64_t dims[3] = {(cuuint64_t)Kin, (cuuint64_t)N, (cuuint64_t)G};
+    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(N * ld * 2)};
+    cuuint32_t box[3] = {(cuuint32_t)BK, (cuuint32_t)box_rows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides,
+                  box, es) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+// pairs of SMs that run at once, one cluster of two per unit at most
+template <class P>
+cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const P &p,
+                          int64_t units_cap, cudaStream_t s) {
+    if (units_cap < 1) return cudaSuccess;
+    static std::atomic<uint64_t> attr_set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= MAX_DEV) return cudaErrorInvalidDevice;
+    const uint64_t bit = 1ull << dev;
+    if ((attr_set.load(std::memory_order_acquire) & bit) == 0) {
+        e = cudaFuncSetAttribute(linear_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 LIN_SMEM);
+        if (e != cudaSuccess) return e;
+        attr_set.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    const int64_t pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(2 * (units_cap < pairs ? units_cap : pairs)), 1, 1);
+    cfg.blockDim = dim3(NTHREADS, 1, 1);
+    cfg.dynamicSmemBytes = LIN_SMEM;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, linear_kernel<P>, ma, mb, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+bool grouped(const int32_t *starts) { return starts != nullptr; }
+
+// dense tiles of equal height
+Tiles dense_tiles(int64_t rows) {
+    const int64_t n = rows > 0 ? (rows + LTILE - 1) / LTILE : 1;
+    const int64_t h = round_up((rows + n - 1) / n, 16);
+    return Tiles{nullptr, (rows + h - 1) / (h > 0 ? h : 1), rows, (int)(h > 0 ? h : 16)};
+}
+
+struct LinWs {
+    int32_t *list;    // past its 16-byte header
+    int64_t cap;
+    int32_t *valid;   // [G]
+    uint16_t *dz;     // [rows][ld_dz]
+    int64_t ld_dz;
+    float *part;      // [tiles][N]
+};
+
+size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
+    size_t off = 0;
+    const auto take = [&](size_t bytes) {
+        off = (size_t)round_up((int64_t)off, 256);
+        void *p = ws != nullptr ? (char *)ws + off : nullptr;
+        off += bytes;
+        return p;
+    };
+    LinWs w = {};
+    w.cap = tiles_cap(c.rows, c.groups);
+    int32_t *l = (int32_t *)take(16 + (size_t)w.cap * 16);
+    w.list = l != nullptr ? l + 4 : nullptr;
+    w.valid = (int32_t *)take((size_t)c.groups * 4);
+    if (pass == MOK_LINEAR_BACKWARD) {
+        w.ld_dz = round_up(c.out_features, 8);
+        w.dz = (uint16_t *)take((size_t)c.rows * w.ld_dz * 2);
+        w.part = (float *)take((size_t)w.cap * c.out_features * 4);
+    }
+    if (o != nullptr) *o = w;
+    return off;
+}
+
+mok_status check_linear(const mok_linear_config *c, const int32_t *starts, const int32_t *counts,
+                        void *ws, size_t ws_bytes, int pass, int **status) {
+    mok_status st = mok_check_linear_config(c);
+    if (st != MOK_OK) return st;
+    if ((st = current_device_status_word(status)) != MOK_OK) return st;
+    if ((starts == nullptr) != (counts == nullptr)) return MOK_ERR_INVALID_ARG;
+    if (starts == nullptr && c->groups != 1) return MOK_ERR_INVALID_ARG;
+    if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 ||
+        ws_bytes < carve_linear(*c, pass, nullptr, nullptr))
+        return MOK_ERR_WORKSPACE;
+    return MOK_OK;
+}
+
+}  // namespace
+}  // namespace mok
+
+using namespace mok;
+
+extern "C" {
+
+mok_status mok_check_linear_config(const mok_linear_config *c) {
+    if (c == nullptr) return MOK_ERR_INVALID_ARG;
+    if (c->abi_version != MOK_ABI_VERSION) return MOK_ERR_ABI;
+    if (c->groups < 1 || c->groups > MAX_G) return MOK_ERR_INVALID_ARG;
+    const int32_t most = 1 << 20;
+    if (c->in_features < 1 || c->in_features > most || c->out_features < 1 ||
+        c->out_features > most)
+        return MOK_ERR_INVALID_ARG;
+    if (c->rows < 0 || c->rows >= ((int64_t)1 << 31) - 512) return MOK_ERR_INVALID_ARG;
+    const int64_t far = (int64_t)1 << 30;
+    const int64_t lds[] = {c->ld_in, c->ld_w, c->ld_out};
+    const int32_t widths[] = {c->in_features, c->in_features, c->out_features};
+    for (int i = 0; i < 3; ++i)
+        if (lds[i] < widths[i] || lds[i] % 8 != 0 || lds[i] > far) return MOK_ERR_INVALID_ARG;
+    if (c->act < MOK_ACT_NONE || c->act > MOK_ACT_GELU || c->reserved != 0)
+        return MOK_ERR_INVALID_ARG;
+    const int32_t dts[] = {c->out_dtype, c->grad_dtype};
+    for (int32_t d : dts)
+        if (d != MOK_DTYPE_BF16 && d != MOK_DTYPE_F32) return MOK_ERR_INVALID_ARG;
+    return MOK_OK;
+}
+
+size_t mok_linear_workspace_size(const mok_linear_config *c, int pass) {
+    if (mok_check_linear_config(c) != MOK_OK) return 0;
+    if (pass != MOK_LINEAR_FORWARD && pass != MOK_LINEAR_BACKWARD) return 0;
+    return carve_linear(*c, pass, nullptr, nullptr);
+}
+
+mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const void *w,
+                              const float *bias, const void *residual, const int32_t *starts,
+                              const int32_t *counts, void *y, void *z, void *ws, size_t ws_bytes,
+                              cudaStream_t stream) {
+    int *status;
+    mok_status st = check_linear(c, starts, counts, ws, ws_bytes, MOK_LINEAR_FORWARD, &status);
+    if (st != MOK_OK) return st;
+    if (c->rows == 0) return MOK_OK;
+    if (!x || !w || !y) return MOK_ERR_INVALID_ARG;
+    const void *ps[] = {x, w, bias, residual, starts, counts, y, z};
+    for (const void *p : ps)
+        if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    LinWs wk;
+    carve_linear(*c, MOK_LINEAR_FORWARD, ws, &wk);
+    if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
+    Tiles tiles = dense_tiles(c->rows);
+    if (grouped(starts)) {
+        tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
+        prof_begin(OP_LINEAR_TILES, stream);
+        linear_tiles_kernel<<<1, MAX_G, 0, stream>>>(starts, counts, c->groups, c->rows, wk.list,
+                                                     wk.cap, wk.valid, status);
+        prof_end(OP_LINEAR_TILES, stream, 1);
+        if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
+    }
+    CUtensorMap ma, mb;
+    if (map_w(&ma, w, c->groups, c->out_features, c->in_features, c->ld_w, 128) != cudaSuccess ||
+        map2d(&mb, x, c->rows, c->in_features, c->ld_in, 128) != cudaSuccess)
+        return MOK_ERR_CUDA;
+    const bool f32 = c->out_dtype == MOK_DTYPE_F32;
+    const int segs = f32 ? (c->in_features + SEG_K - 1) / SEG_K : 1;
+    const int n_mb = (c->out_features + 255) / 256;
+    Fwd p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias,
+          (const uint16_t *)residual, y, (uint16_t *)z, c->act, f32, status};
+    MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, p, tiles.cap * n_mb, stream));
+    return MOK_OK;
+}
+
+mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const void *w,
+                               const void *z, const void *dy, const int32_t *starts,
+                               const int32_t *counts, void *dx, void *dw, float *db, void *ws,
+                               size_t ws_bytes, cudaStream_t stream) {
+    int *status;
+    mok_status st = check_linear(c, starts, counts, ws, ws_bytes, MOK_LINEAR_BACKWARD, &status);
+    if (st != MOK_OK) return st;
+    if (!dx && !dw && !db) return MOK_ERR_INVALID_ARG;
+    const bool act = c->act != MOK_ACT_NONE, dy32 = c->out_dtype == MOK_DTYPE_F32;
+    if (c->rows > 0 && (!dy || (act && !z) || (dx && !w) || (dw && !x)))
+        return MOK_ERR_INVALID_ARG;
+    const void *ps[] = {x, w, z, dy, starts, counts, dx, dw, db};
+    for (const void *p : ps)
+        if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    const int G = c->groups, N = c->out_features, Kin = c->in_features;
+    const bool g32 = c->grad_dtype == MOK_DTYPE_F32;
+    if (c->rows == 0) {  // sums over nothing
+        const size_t es = g32 ? 4 : 2;
+        if (dw && cudaMemset2DAsync(dw, (size_t)c->ld_w * es, 0, (size_t)Kin * es, (size_t)G * N,
+                                    stream) != cudaSuccess)
+            return MOK_ERR_CUDA;
+        if (db && cudaMemsetAsync(db, 0, (size_t)G * N * 4, stream) != cudaSuccess)
+            return MOK_ERR_CUDA;
+        return MOK_OK;
+    }
+    LinWs wk;
+    carve_linear(*c, MOK_LINEAR_BACKWARD, ws, &wk);
+    if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
+    Tiles tiles = dense_tiles(c->rows);
+    if (grouped(starts)) {
+        tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
+        prof_begin(OP_LINEAR_TILES, stream);
+        linear_tiles_kernel<<<1, MAX_G, 0, stream>>>(starts, counts, G, c->rows, wk.list, wk.cap,
+                                                     wk.valid, status);
+        prof_end(OP_LINEAR_TILES, stream, 1);
+        if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
+    }
+    // without an activation a bf16 dy is dz
+    const bool direct = !act && !dy32;
+    const uint16_t *dz = direct ? (const uint16_t *)dy : wk.dz;
+    const int64_t ld_dz = direct ? c->ld_out : wk.ld_dz;
+    if (db || (!direct && (dx || dw))) {
+        uint16_t *dzo = direct || (!dx && !dw) ? nullptr : wk.dz;
+        float *part = db ? wk.part : nullptr;
+        const dim3 grid((unsigned)tiles.cap, (unsigned)((N + 63) / 64));
+        prof_begin(OP_LINEAR_DZ, stream);
+        if (dy32)
+            linear_dz_kernel<true><<<grid, 256, 0, stream>>>(dy, (const uint16_t *)z, tiles, N,
+                                                             c->ld_out, c->act, dzo, ld_dz, part);
+        else
+            linear_dz_kernel<false><<<grid, 256, 0, stream>>>(dy, (const uint16_t *)z, tiles, N,
+                                                              c->ld_out, c->act, dzo, ld_dz, part);
+        if (db)
+            linear_db_kernel<<<(unsigned)(((int64_t)G * N + 255) / 256), 256, 0, stream>>>(
+                wk.part, tiles, G, N, db);
+        prof_end(OP_LINEAR_DZ, stream, db ? 2 : 1);
+        if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
+    }
+    CUtensorMap ma, mb;
+    if (dx) {
+        if (map_w(&ma, w, G, N, Kin, c->ld_w, 64) != cudaSuccess ||
+            map2d(&mb, dz, c->rows, N, ld_dz, 128) != cudaSuccess)
+            return MOK_ERR_CUDA;
+        const int n_mb = (Kin + 255) / 256;
+        Dx p{tiles, n_mb, 1, Kin, N, c->ld_in, dx, g32, status};
+        MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, p, tiles.cap * n_mb, stream));
+    }
+    if (dw) {
+        if (map2d(&ma, x, c->rows, Kin, c->ld_in, 64) != cudaSuccess ||
+            map2d(&mb, dz, c->rows, N, ld_dz, 64) != cudaSuccess)
+            return MOK_ERR_CUDA;
+        const int n_mb = (Kin + 255) / 256, n_nb = (N + 255) / 256;
+        Dw p{starts, grouped(starts) ? wk.valid : nullptr, c->rows, G, n_mb, n_nb, 1, Kin, N,
+             c->ld_w, dw, g32, status};
+        MOK_OP_LAUNCH(OP_LINEAR_DW, 1,
+                      launch_linear(ma, mb, p, (int64_t)G * n_mb * n_nb, stream));
+    }
+    return MOK_OK;
+}
+
+}  // extern "C"

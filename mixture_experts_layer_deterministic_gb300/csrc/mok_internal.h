@@ -13,24 +13,12 @@ enum KernelKind {
     KK_ROUTE = 0, KK_SCHEDULE, KK_TILES, KK_GATHER, KK_GEMM_UP, KK_GEMM_DOWN, KK_COMBINE,
     KK_QUANTIZE, KK_PAD, KK_GATHER_BWD, KK_GEMM_G, KK_ROUTER_GRAD, KK_GEMM_DGRAD,
     KK_DX_REDUCE, KK_WGRAD13, KK_WGRAD2, KK_SCALE_ATOMS, KK_SHARED_UP, KK_SHARED_DOWN,
-    KK_SHARED_BWD, KK_RING_FWD, KK_ROW_MAP, KK_DISPATCH, KK_COMBINE_ROWS, KK_COMBINE_BWD,
-    KK_ADAMW, KK_COUNT
+    KK_SHARED_BWD, KK_RING_FWD, KK_COUNT
 };
 // while profiling is on: brackets the launches between begin and end with events
 void prof_begin(int kind, cudaStream_t s);
 void prof_end(int kind, cudaStream_t s, int n_kernels);
 bool prof_on();
-
-// a launch of `nk` kernels of one kind, bracketed by events while profiling is on
-#define MOK_LAUNCH(kind, nk, expr)                         \
-    do {                                                   \
-        prof_begin(kind, stream);                          \
-        cudaError_t _e = (expr);                           \
-        prof_end(kind, stream, nk);                        \
-        if (_e != cudaSuccess) return MOK_ERR_CUDA;        \
-    } while (0)
-
-inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // the entry points' device check (compute capability 10.3) and the device's status word
 mok_status current_device_status_word(int **status);
@@ -304,21 +292,5 @@ cudaError_t launch_wgrad_pair_tc(const int32_t *counts, const int32_t *poff, con
                                  const uint16_t *Bm, void *out, bool out_f32, int E, int M,
                                  int N, int64_t rows_a, int64_t rows_b, int *status,
                                  cudaStream_t s);
-
-// ---------------------------------------------------------------- token sort (rows.cu)
-cudaError_t launch_build_row_map(const mok_rows_config &c, const int32_t *idx,
-                                 const mok_schedule &sch, int32_t *map, int32_t *starts,
-                                 int32_t *kept, int *status, cudaStream_t s);
-cudaError_t launch_dispatch_rows(const mok_rows_config &c, const void *x, const int32_t *map,
-                                 const int32_t *starts, const int32_t *kept, void *xs,
-                                 int *status, cudaStream_t s);
-// y[t] = res[t] + sum_k w[t,k] rows[map[t*K + k]] (w, res nullable)
-cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, const int32_t *map,
-                                const float *w, const void *res, void *y, int *status,
-                                cudaStream_t s);
-cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const void *rows,
-                               const int32_t *map, const int32_t *starts, const int32_t *kept,
-                               const float *w, void *drows, float *dw, int *status,
-                               cudaStream_t s);
 
 }  // namespace mok

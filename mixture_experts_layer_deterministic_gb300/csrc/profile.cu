@@ -2,17 +2,18 @@
 #include <vector>
 
 #include "common.cuh"
-#include "mok_internal.h"
+#include "ops_internal.h"
 
 namespace mok {
 namespace {
 
-const char *const kNames[KK_COUNT] = {
+const char *const kNames[OP_COUNT] = {
     "route_topk", "schedule", "build_tiles", "gather", "gemm_up_swiglu", "gemm_down_push",
     "combine", "quantize_mxfp8", "pad_offsets", "gather_bwd", "gemm_g_swiglu_bwd",
     "router_grad", "gemm_dgrad_push", "dx_reduce", "wgrad_w13", "wgrad_w2", "scale_atoms",
     "shared_up_swiglu", "shared_down_add", "shared_backward", "ring_forward",
-    "row_map", "dispatch_rows", "combine_rows", "combine_rows_bwd", "adamw"};
+    "row_map", "dispatch_rows", "combine_rows", "combine_rows_bwd", "adamw",
+    "linear_tiles", "linear_forward", "linear_dz", "linear_dx", "linear_dw"};
 
 struct Rec {
     int kind;
@@ -69,8 +70,8 @@ extern "C" mok_status mok_profile_read(int32_t max, int32_t *n_kinds, const char
                                        int64_t *launches, double *ms) {
     using namespace mok;
     if (n_kinds == nullptr) return MOK_ERR_INVALID_ARG;
-    double tot[KK_COUNT] = {0};
-    int64_t cnt[KK_COUNT] = {0};
+    double tot[OP_COUNT] = {0};
+    int64_t cnt[OP_COUNT] = {0};
     for (const Rec &r : g_recs) {
         if (cudaEventSynchronize(g_events[r.ev + 1]) != cudaSuccess) return MOK_ERR_CUDA;
         float t = 0.f;
@@ -80,7 +81,7 @@ extern "C" mok_status mok_profile_read(int32_t max, int32_t *n_kinds, const char
         cnt[r.kind] += r.n;
     }
     int32_t n = 0;
-    for (int k = 0; k < KK_COUNT; ++k) {
+    for (int k = 0; k < OP_COUNT; ++k) {
         if (cnt[k] == 0) continue;
         if (n < max) {
             if (names) names[n] = kNames[k];

@@ -9,7 +9,7 @@
 // token and by column segment, so a row is read or written by whole warps, 16 bytes a lane.
 // Sums over k run in ascending k in fp32; dot products over H in a fixed tree: no atomics.
 #include "common.cuh"
-#include "mok_internal.h"
+#include "ops_internal.h"
 
 namespace mok {
 namespace {
@@ -520,8 +520,8 @@ mok_status mok_build_row_map(const mok_rows_config *c, const int32_t *topk_idx,
     if (c->T > 0 && (!topk_idx || !row_map || !sch->inv)) return MOK_ERR_INVALID_ARG;
     const void *ps[] = {topk_idx, row_map, starts, kept, sch->counts, sch->offsets, sch->inv};
     for (const void *p : ps)
-        if (p && !aligned16(p)) return MOK_ERR_INVALID_ARG;
-    MOK_LAUNCH(KK_ROW_MAP, 1,
+        if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    MOK_OP_LAUNCH(OP_ROW_MAP, 1,
                launch_build_row_map(*c, topk_idx, *sch, row_map, starts, kept, status, stream));
     return MOK_OK;
 }
@@ -538,8 +538,8 @@ mok_status mok_dispatch(const mok_rows_config *c, const void *x, const int32_t *
     if (!xs && c->n_rows > 0) return MOK_ERR_INVALID_ARG;
     const void *ps[] = {x, row_map, starts, kept, xs};
     for (const void *p : ps)
-        if (p && !aligned16(p)) return MOK_ERR_INVALID_ARG;
-    MOK_LAUNCH(KK_DISPATCH, 1,
+        if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    MOK_OP_LAUNCH(OP_DISPATCH, 1,
                launch_dispatch_rows(*c, x, row_map, starts, kept, xs, status, stream));
     return MOK_OK;
 }
@@ -554,8 +554,8 @@ mok_status mok_combine(const mok_rows_config *c, const void *rows, const int32_t
     if (c->T > 0 && (!row_map || !y || (!rows && c->n_rows > 0))) return MOK_ERR_INVALID_ARG;
     const void *ps[] = {rows, row_map, topk_w, residual, y};
     for (const void *p : ps)
-        if (p && !aligned16(p)) return MOK_ERR_INVALID_ARG;
-    MOK_LAUNCH(KK_COMBINE_ROWS, 1,
+        if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    MOK_OP_LAUNCH(OP_COMBINE, 1,
                launch_combine_rows(*c, rows, row_map, topk_w, residual, y, status, stream));
     return MOK_OK;
 }
@@ -579,8 +579,8 @@ mok_status mok_combine_backward(const mok_rows_config *c, const void *dy, const 
     if (c->T > 0 && d_topk_w && !rows && c->n_rows > 0) return MOK_ERR_INVALID_ARG;
     const void *ps[] = {dy, rows, row_map, starts, kept, topk_w, drows, d_topk_w};
     for (const void *p : ps)
-        if (p && !aligned16(p)) return MOK_ERR_INVALID_ARG;
-    MOK_LAUNCH(KK_COMBINE_BWD, 1,
+        if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    MOK_OP_LAUNCH(OP_COMBINE_BWD, 1,
                launch_combine_bwd(*c, dy, rows, row_map, starts, kept, topk_w, drows, d_topk_w,
                                   status, stream));
     return MOK_OK;

@@ -40,3 +40,24 @@ def test_adamw_config(kw, want):
     base = dict(lr=1e-3)
     base.update(kw)
     assert B.mok_check_adamw_config(B.make_adamw(**base)) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(), OK), (dict(rows=0), OK), (dict(in_features=1, out_features=1), OK),
+    (dict(groups=1024), OK), (dict(act=B.MOK_ACT_GELU), OK),
+    (dict(out_dtype=B.MOK_DTYPE_F32, grad_dtype=B.MOK_DTYPE_F32), OK),
+    (dict(ld_in=72, ld_w=80, ld_out=104), OK),
+    (dict(rows=-1), BAD), (dict(rows=(1 << 31) - 512), BAD), (dict(groups=0), BAD),
+    (dict(groups=1025), BAD), (dict(in_features=0), BAD), (dict(out_features=0), BAD),
+    (dict(in_features=(1 << 20) + 1), BAD), (dict(ld_in=56), BAD), (dict(ld_in=65), BAD),
+    (dict(ld_w=68), BAD), (dict(ld_out=90), BAD), (dict(act=5), BAD), (dict(act=-1), BAD),
+    (dict(out_dtype=2), BAD), (dict(grad_dtype=2), BAD), (dict(abi_version=3), B.MOK_ERR_ABI),
+])
+def test_linear_config(kw, want):
+    base = dict(rows=100, in_features=64, out_features=96)
+    base.update(kw)
+    c = B.make_linear(**base)
+    assert B.mok_check_linear_config(c) == want
+    for which in (B.MOK_LINEAR_FORWARD, B.MOK_LINEAR_BACKWARD):
+        assert (B.mok_linear_workspace_size(c, which) > 0) == (want == OK)
+    assert B.mok_linear_workspace_size(c, 2) == 0
