@@ -17,6 +17,8 @@
 // Per CTA, 320 threads: warp 0 loads (TMA, both CTAs), warp 1 issues the MMAs (rank 0), warps
 // 2-9 drain accumulators, two sets of 256 TMEM columns alternating between units. Every wait is
 // bounded (2 s), after which MOK_ERR_TIMEOUT is recorded and the launch ends.
+#include <type_traits>
+
 #include "gemm_tc_core.cuh"
 #include "ops_internal.h"
 
@@ -114,41 +116,61 @@ __global__ void __launch_bounds__(MAX_G)
 int64_t tiles_cap(int64_t rows, int G) { return G + rows / 16 / (LTILE / 16) + 1; }
 
 // ---------------------------------------------------------------- activations
-MOK_DEV float sigmoid_f(float x) { return 1.0f / (1.0f + expf(-x)); }
+// exp and the quotient to within 2^-20 of their values: far inside the bf16 rounding of y
+// and z, and of the size of the products' own error in fp32
+MOK_DEV float sigmoid_f(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 constexpr float GELU_C2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float GELU_A = 0.044715f;
 
 // 0.5 (1 + tanh u) = sigma(2u): gelu_tanh is z sigma(2 sqrt(2/pi) (z + a z^3))
-MOK_DEV float act_f(float z, int act) {
-    switch (act) {
-        case MOK_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
-        case MOK_ACT_SILU: return z * sigmoid_f(z);
-        case MOK_ACT_GELU_TANH: return z * sigmoid_f(GELU_C2 * fmaf(GELU_A * z * z, z, z));
-        case MOK_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
-    }
+template <int ACT>
+MOK_DEV float act_f(float z) {
+    if (ACT == MOK_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+    if (ACT == MOK_ACT_SILU) return z * sigmoid_f(z);
+    if (ACT == MOK_ACT_GELU_TANH) return z * sigmoid_f(GELU_C2 * fmaf(GELU_A * z * z, z, z));
+    if (ACT == MOK_ACT_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
     return z;
 }
-MOK_DEV float act_grad_f(float z, int act) {
-    switch (act) {
-        case MOK_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-        case MOK_ACT_SILU: {
-            const float s = sigmoid_f(z);
-            return s * fmaf(z, 1.0f - s, 1.0f);
-        }
-        case MOK_ACT_GELU_TANH: {
-            const float s = sigmoid_f(GELU_C2 * fmaf(GELU_A * z * z, z, z));
-            const float du = GELU_C2 * fmaf(3.0f * GELU_A * z, z, 1.0f);
-            return s * fmaf(z * (1.0f - s), du, 1.0f);
-        }
-        case MOK_ACT_GELU:
-            return fmaf(z, 0.3989422804014327f * expf(-0.5f * z * z),
-                        0.5f * erfcf(-0.70710678118654752f * z));
+template <int ACT>
+MOK_DEV float act_grad_f(float z) {
+    if (ACT == MOK_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if (ACT == MOK_ACT_SILU) {
+        const float s = sigmoid_f(z);
+        return s * fmaf(z, 1.0f - s, 1.0f);
     }
+    if (ACT == MOK_ACT_GELU_TANH) {
+        const float s = sigmoid_f(GELU_C2 * fmaf(GELU_A * z * z, z, z));
+        const float du = GELU_C2 * fmaf(3.0f * GELU_A * z, z, 1.0f);
+        return s * fmaf(z * (1.0f - s), du, 1.0f);
+    }
+    if (ACT == MOK_ACT_GELU)
+        return fmaf(z, 0.3989422804014327f * __expf(-0.5f * z * z),
+                    0.5f * erfcf(-0.70710678118654752f * z));
     return 1.f;
+}
+// the runtime activation as a template argument: f(std::integral_constant<int, ACT>)
+template <class F>
+MOK_DEV void with_act(int act, F &&f) {
+    switch (act) {
+        case MOK_ACT_RELU: f(std::integral_constant<int, MOK_ACT_RELU>{}); break;
+        case MOK_ACT_SILU: f(std::integral_constant<int, MOK_ACT_SILU>{}); break;
+        case MOK_ACT_GELU_TANH: f(std::integral_constant<int, MOK_ACT_GELU_TANH>{}); break;
+        case MOK_ACT_GELU: f(std::integral_constant<int, MOK_ACT_GELU>{}); break;
+        default: f(std::integral_constant<int, MOK_ACT_NONE>{}); break;
+    }
 }
 
 // ---------------------------------------------------------------- the engine
+// Outputs in bf16 leave through shared memory and TMA. A warp takes 32 columns of its 32 lanes
+// at a time in the 16x256b shape, in which a thread holds two neighbouring columns of a lane;
+// packed to bf16 pairs, stmatrix.trans turns them around into rows of 32 consecutive lanes
+// (64 bytes, 64-byte swizzle: no bank conflicts), and one thread hands the patch to TMA, which
+// drops what lies past the matrix. Against storing each element from its lane this took
+// dW of 64 x 1024 x 4096 from 378 us to a fraction of that (issue slots were the limit).
+constexpr int PATCH_BYTES = 32 * 64;  // 32 columns of 32 lanes in bf16
+constexpr int PATCHES = 2;            // per epilogue warp
+
 struct LinSmem {
     uint64_t full[LSTAGES];   // rank 0: both CTAs' copies of the stage have landed
     uint64_t empty[LSTAGES];  // each CTA: the MMAs that read the stage are done
@@ -157,7 +179,9 @@ struct LinSmem {
     uint32_t tmem_base;
     int abort;
 };
-constexpr int LIN_SMEM = LSTAGES * LSTAGE_BYTES + 1024 + (int)sizeof(LinSmem);
+constexpr int LIN_PATCHES = EPI_WARPS * PATCHES * PATCH_BYTES;
+constexpr int LIN_SMEM =
+    LSTAGES * LSTAGE_BYTES + LIN_PATCHES + 1024 + (int)sizeof(LinSmem);
 static_assert(LIN_SMEM <= 232448, "shared memory of a CTA");
 
 // one unit as one CTA of the pair loads and multiplies it
@@ -178,6 +202,121 @@ MOK_DEV void tma_load_3d_pair(void *smem_dst, const CUtensorMap *m, uint32_t bar
         : "memory");
 }
 
+// 32 columns of this warp's 32 lanes as pairs: v[h][b][..] are lane 16 h + t / 4 (first two)
+// and 8 lanes on (last two), columns 8 b + 2 (t % 4) and the next, t the thread
+MOK_DEV void ld_pairs(uint32_t c, float (&v)[2][4][4]) {
+    uint32_t r[2][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+            "%13,%14,%15}, [%16];"
+            : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]),
+              "=r"(r[h][5]), "=r"(r[h][6]), "=r"(r[h][7]), "=r"(r[h][8]), "=r"(r[h][9]),
+              "=r"(r[h][10]), "=r"(r[h][11]), "=r"(r[h][12]), "=r"(r[h][13]), "=r"(r[h][14]),
+              "=r"(r[h][15])
+            : "r"(c + ((uint32_t)(16 * h) << 16)));
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h][b][i] = __uint_as_float(r[h][4 * b + i]);
+}
+
+// byte of row n (a column of the accumulator), 16-byte piece i of a patch (64-byte swizzle)
+MOK_DEV uint32_t patch_at(int n, int i) { return (uint32_t)(n * 64 + ((i ^ ((n >> 1) & 3)) << 4)); }
+
+// The values of ld_pairs, rounded to bf16, into a patch: row n holds the 32 lanes of column n
+MOK_DEV void patch_write(uint32_t patch, const float (&v)[2][4][4], int lane) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const uint32_t at = patch + patch_at(8 * b + (lane & 7), lane >> 3);
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at),
+                     "r"(pack_bf16x2(v[0][b][0], v[0][b][1])),
+                     "r"(pack_bf16x2(v[0][b][2], v[0][b][3])),
+                     "r"(pack_bf16x2(v[1][b][0], v[1][b][1])),
+                     "r"(pack_bf16x2(v[1][b][2], v[1][b][3]))
+                     : "memory");
+    }
+}
+// the reverse: a patch's bf16 values in ld_pairs' order
+MOK_DEV void patch_read(uint32_t patch, float (&v)[2][4][4], int lane) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const uint32_t at = patch + patch_at(8 * b + (lane & 7), lane >> 3);
+        uint32_t r[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(at)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i >> 1][b][2 * (i & 1)] = bf16_lo(r[i]);
+            v[i >> 1][b][2 * (i & 1) + 1] = bf16_hi(r[i]);
+        }
+    }
+}
+
+// a bf16 output: matrices of `rows` x `cols`, rows ld apart
+struct OutRef {
+    uint16_t *p;
+    int64_t rows, ld;
+    int cols;
+};
+
+// What an epilogue warp has for its stores: its patches and the output maps.
+struct LinOut {
+    uint32_t patch;  // shared address of its two patches
+    const CUtensorMap *y, *z;
+    int lane;
+    int *turn;       // patch to fill next
+
+    // a patch that no earlier store is still reading
+    MOK_DEV uint32_t next() const {
+        if (lane == 0) tc::bulk_wait_read<PATCHES - 1>();
+        __syncwarp();
+        const uint32_t p = patch + (uint32_t)*turn * PATCH_BYTES;
+        *turn = (*turn + 1) % PATCHES;
+        return p;
+    }
+    // 16-row boxes (1 or 2) of a filled patch to columns x.. of rows y0.. of matrix g of o. TMA
+    // drops rows past o.rows and whole 16-byte pieces past o.cols; it writes the rest of a piece
+    // that the edge cuts, so such a patch is copied element by element.
+    MOK_DEV void store(const CUtensorMap *m, const OutRef &o, uint32_t p, int x, int64_t y0, int g,
+                       int boxes) const {
+        const bool cut = x + 32 > o.cols && (o.cols & 7) != 0;
+        if (!cut) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (cut) {
+            for (int n = lane; n < 16 * boxes && y0 + n < o.rows; n += 32) {
+                uint16_t *row = o.p + ((int64_t)g * o.rows + y0 + n) * o.ld + x;
+                for (int j = 0; x + j < o.cols && j < 32; ++j) {
+                    uint16_t e;
+                    asm volatile("ld.shared.u16 %0, [%1];"
+                                 : "=h"(e)
+                                 : "r"(p + patch_at(n, j >> 3) + 2 * (j & 7))
+                                 : "memory");
+                    row[j] = e;
+                }
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {
+            if (!cut && x < o.cols)
+                for (int i = 0; i < boxes; ++i)
+                    asm volatile(
+                        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}],"
+                        " [%4];" ::"l"((uint64_t)m),
+                        "r"(x), "r"((int)y0 + 16 * i), "r"(g),
+                        "r"(p + (uint32_t)i * (PATCH_BYTES / 2))
+                        : "memory");
+            tc::bulk_commit();
+        }
+    }
+};
+
 MOK_DEV void ld32(uint32_t c, float (&v)[32]) {
     float a[16], b[16];
     tc::tmem_ld16(c, a);
@@ -190,6 +329,7 @@ MOK_DEV void ld32(uint32_t c, float (&v)[32]) {
     }
 }
 
+template <bool F32>
 struct Fwd {
     static constexpr bool A_MN = false, B_MN = false;
     Tiles tiles;
@@ -202,7 +342,6 @@ struct Fwd {
     void *y;
     uint16_t *z;
     int act;
-    bool y_f32;
     int *status;
 
     MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
@@ -230,54 +369,154 @@ struct Fwd {
         tma_load_3d_pair(st, tmA, fb, q.a0 + k0, q.a1, q.a2);
         tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, q.b0 + k0, q.b1);
     }
-    MOK_DEV void epilogue(int64_t u, int seg, uint32_t rank, uint32_t c, int q, int hw,
-                          int lane) const {
+    MOK_DEV void epilogue(int64_t u, int seg, uint32_t rank, uint32_t c, int q, int hw, int lane,
+                          const LinOut &out) const {
         int g;
         int64_t r0, r1;
         bool pad;
         tiles.get(u / n_mb, &g, &r0, &r1, &pad);
         const int nr = (int)(r1 - r0);
         const int n_mma = (nr + 15) & ~15;
-        const int n_out = pad ? n_mma : nr;  // rows to write (the padding as zeros)
-        const int f = (int)(u % n_mb) * 256 + (int)rank * 128 + q * 32 + lane;
+        const int f0 = (int)(u % n_mb) * 256 + (int)rank * 128 + q * 32;  // the warp's features
+        if constexpr (F32)
+            direct(seg, c, hw, f0 + lane, g, r0, nr, pad ? n_mma : nr);
+        else
+            staged(c, hw, lane, f0, g, r0, nr, n_mma, out);
+    }
+    // bf16: 32 rows at a time through patches
+    MOK_DEV void staged(uint32_t c, int hw, int lane, int f0, int g, int64_t r0, int nr, int n_mma,
+                        const LinOut &out) const {
+        float b[2][2];  // this thread's four features
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int f = f0 + 8 * i + (lane >> 2);
+            b[i >> 1][i & 1] = bias != nullptr && f < N ? bias[(int64_t)g * N + f] : 0.f;
+        }
+        const OutRef yo{static_cast<uint16_t *>(y), tiles.rows, ld, N}, zo{z, tiles.rows, ld, N};
+        for (int n0 = 32 * hw; n0 < n_mma; n0 += 64) {
+            const int boxes = n_mma - n0 > 16 ? 2 : 1;
+            float v[2][4][4], rs[2][4][4];
+            if (res != nullptr) {
+                // rows of 64 bytes, four lanes each; through a patch into the pairs' order
+                uint4 t[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = 8 * i + (lane >> 2), f = f0 + 8 * (lane & 3);
+                    t[i] = make_uint4(0, 0, 0, 0);
+                    if (n0 + n < nr && f < N) {
+                        const uint16_t *p = res + (r0 + n0 + n) * ld + f;
+                        if (f + 8 <= N) {
+                            t[i] = *reinterpret_cast<const uint4 *>(p);
+                        } else {
+                            uint32_t e[4] = {0, 0, 0, 0};
+                            for (int j = 0; j < N - f; ++j)
+                                e[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+                            t[i] = make_uint4(e[0], e[1], e[2], e[3]);
+                        }
+                    }
+                }
+                const uint32_t p = out.next();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                     p + patch_at(8 * i + (lane >> 2), lane & 3)),
+                                 "r"(t[i].x), "r"(t[i].y), "r"(t[i].z), "r"(t[i].w)
+                                 : "memory");
+                __syncwarp();
+                patch_read(p, rs, lane);
+                if (lane == 0) tc::bulk_commit();  // an empty group: next() counts one a patch
+            }
+            ld_pairs(c + n0, v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[h][k][i] += b[h][i >> 1];
+            if (n0 + 32 > nr) {  // the padding's z is zero
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n0 + 8 * k + 2 * (lane & 3) + (i & 1) >= nr) v[0][k][i] = v[1][k][i] = 0.f;
+            }
+            if (z != nullptr) {
+                const uint32_t p = out.next();
+                patch_write(p, v, lane);
+                out.store(out.z, zo, p, f0, r0 + n0, 0, boxes);
+            }
+            if (act != MOK_ACT_NONE)
+                with_act(act, [&](auto a) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[h][k][i] = act_f<a.value>(v[h][k][i]);
+                });
+            if (res != nullptr) {  // act(0) and the residual's padding are zero
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[h][k][i] += rs[h][k][i];
+            }
+            const uint32_t p = out.next();
+            patch_write(p, v, lane);
+            out.store(out.y, yo, p, f0, r0 + n0, 0, boxes);
+        }
+    }
+    // fp32: from the lanes, 128 bytes a warp and row
+    MOK_DEV void direct(int seg, uint32_t c, int hw, int f, int g, int64_t r0, int nr,
+                        int n_out) const {
         const bool ok = f < N;
         const bool last = seg == segs - 1;
         const float b = bias != nullptr && ok ? bias[(int64_t)g * N + f] : 0.f;
-        for (int n0 = 32 * hw; n0 < n_mma; n0 += 64) {
+        for (int n0 = 32 * hw; n0 < ((nr + 15) & ~15); n0 += 64) {
             float v[32];
             ld32(c + n0, v);
             if (!ok) continue;
             const int64_t o = (r0 + n0) * ld + f;
+            float *yp = static_cast<float *>(y) + o;
             if (seg > 0) {  // the sum of the earlier segments, left in y by this thread
                 float a[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    a[j] = n0 + j < nr ? static_cast<const float *>(y)[o + (int64_t)j * ld] : 0.f;
+                for (int j = 0; j < 32; ++j) a[j] = n0 + j < nr ? yp[(int64_t)j * ld] : 0.f;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] += a[j];
             }
             if (!last) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    if (n0 + j < nr) static_cast<float *>(y)[o + (int64_t)j * ld] = v[j];
+                    if (n0 + j < nr) yp[(int64_t)j * ld] = v[j];
                 continue;
             }
-            float rs[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = n0 + j < nr ? v[j] + b : 0.f;
+            if (z != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (n0 + j < n_out) z[o + (int64_t)j * ld] = f32_to_bf16(v[j]);
+            }
+            if (act != MOK_ACT_NONE)
+                with_act(act, [&](auto a) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = act_f<a.value>(v[j]);
+                });
+            if (res != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (n0 + j < nr) v[j] += bf16_to_f32(res[o + (int64_t)j * ld]);
+            }
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                rs[j] = res != nullptr && n0 + j < nr ? bf16_to_f32(res[o + (int64_t)j * ld]) : 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                if (n0 + j >= n_out) continue;
-                const bool real = n0 + j < nr;
-                const float zv = real ? v[j] + b : 0.f;
-                if (z != nullptr) z[o + (int64_t)j * ld] = f32_to_bf16(zv);
-                st_val(y, o + (int64_t)j * ld, real ? act_f(zv, act) + rs[j] : 0.f, y_f32);
-            }
+                if (n0 + j < n_out) yp[(int64_t)j * ld] = v[j];
         }
     }
 };
 
+template <bool F32>
 struct Dx {
     static constexpr bool A_MN = true, B_MN = false;
     Tiles tiles;
@@ -286,7 +525,6 @@ struct Dx {
     int Kin, N;
     int64_t ld;   // row stride of dx
     void *dx;
-    bool f32;
     int *status;
 
     MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
@@ -314,28 +552,46 @@ struct Dx {
         tma_load_3d_pair(st + BOX, tmA, fb, q.a0 + 64, k0, q.a2);
         tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, k0, q.b1);
     }
-    MOK_DEV void epilogue(int64_t u, int, uint32_t rank, uint32_t c, int q, int hw,
-                          int lane) const {
+    MOK_DEV void epilogue(int64_t u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
+                          const LinOut &out) const {
         int g;
         int64_t r0, r1;
         bool pad;
         tiles.get(u / n_mb, &g, &r0, &r1, &pad);
         const int nr = (int)(r1 - r0);
         const int n_mma = (nr + 15) & ~15;
-        const int n_out = pad ? n_mma : nr;
-        const int i = (int)(u % n_mb) * 256 + (int)rank * 128 + q * 32 + lane;
+        const int i0 = (int)(u % n_mb) * 256 + (int)rank * 128 + q * 32;
         for (int n0 = 32 * hw; n0 < n_mma; n0 += 64) {
-            float v[32];
-            ld32(c + n0, v);
-            if (i >= Kin) continue;
-            const int64_t o = (r0 + n0) * ld + i;
+            if constexpr (F32) {
+                float v[32];
+                ld32(c + n0, v);
+                if (i0 + lane >= Kin) continue;
+                float *o = static_cast<float *>(dx) + (r0 + n0) * ld + i0 + lane;
+                const int n_out = (pad ? n_mma : nr) - n0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (n0 + j < n_out) st_val(dx, o + (int64_t)j * ld, n0 + j < nr ? v[j] : 0.f, f32);
+                for (int j = 0; j < 32; ++j)
+                    if (j < n_out) o[(int64_t)j * ld] = n0 + j < nr ? v[j] : 0.f;
+            } else {
+                float v[2][4][4];
+                ld_pairs(c + n0, v);
+                if (n0 + 32 > nr) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (n0 + 8 * k + 2 * (lane & 3) + (i & 1) >= nr)
+                                v[0][k][i] = v[1][k][i] = 0.f;
+                }
+                const uint32_t p = out.next();
+                patch_write(p, v, lane);
+                out.store(out.y, OutRef{static_cast<uint16_t *>(dx), tiles.rows, ld, Kin}, p, i0,
+                          r0 + n0, 0, n_mma - n0 > 16 ? 2 : 1);
+            }
         }
     }
 };
 
+template <bool F32>
 struct Dw {
     static constexpr bool A_MN = true, B_MN = true;
     const int32_t *starts, *valid;  // grouped: first row and row count of each group
@@ -345,7 +601,6 @@ struct Dw {
     int Kin, N;
     int64_t ld;                     // row stride of dW
     void *dw;
-    bool f32;
     int *status;
 
     MOK_DEV int64_t n_units() const { return (int64_t)G * n_mb * n_nb; }
@@ -380,21 +635,37 @@ struct Dw {
         for (int j = 0; j < q.nbox; ++j)
             tc::tma_load_2d_pair(st + (2 + j) * BOX, tmB, fb, q.b0 + 64 * j, q.b1 + k0);
     }
-    MOK_DEV void epilogue(int64_t u, int, uint32_t rank, uint32_t c, int q, int hw,
-                          int lane) const {
+    MOK_DEV void epilogue(int64_t u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
+                          const LinOut &out) const {
         int g, mb, nb;
         get(u, &g, &mb, &nb);
         const int nn = N - nb * 256 < 256 ? N - nb * 256 : 256;
         const bool any = count(g) > 0;
-        const int i = mb * 256 + (int)rank * 128 + q * 32 + lane;
+        const int i0 = mb * 256 + (int)rank * 128 + q * 32;
         for (int n0 = 32 * hw; n0 < nn; n0 += 64) {
-            float v[32];
-            ld32(c + n0, v);
-            if (i >= Kin) continue;
-            const int64_t o = ((int64_t)g * N + nb * 256 + n0) * ld + i;
+            if constexpr (F32) {
+                float v[32];
+                ld32(c + n0, v);
+                if (i0 + lane >= Kin) continue;
+                float *o = static_cast<float *>(dw) +
+                           ((int64_t)g * N + nb * 256 + n0) * ld + i0 + lane;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (n0 + j < nn) st_val(dw, o + (int64_t)j * ld, any ? v[j] : 0.f, f32);
+                for (int j = 0; j < 32; ++j)
+                    if (n0 + j < nn) o[(int64_t)j * ld] = any ? v[j] : 0.f;
+            } else {
+                float v[2][4][4];
+                ld_pairs(c + n0, v);
+                if (!any) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[0][k][i] = v[1][k][i] = 0.f;
+                }
+                const uint32_t p = out.next();
+                patch_write(p, v, lane);
+                out.store(out.y, OutRef{static_cast<uint16_t *>(dw), N, ld, Kin}, p, i0, nb * 256 + n0,
+                          g, nn - n0 > 16 ? 2 : 1);
+            }
         }
     }
 };
@@ -412,11 +683,13 @@ MOK_DEV void lin_drain(uint64_t *bar, uint32_t parity) {
 template <class P>
 __global__ void __launch_bounds__(NTHREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA,
-                  const __grid_constant__ CUtensorMap tmB, const P p) {
+                  const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmY,
+                  const __grid_constant__ CUtensorMap tmZ, const P p) {
     constexpr int NS = LSTAGES, SB = LSTAGE_BYTES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    LinSmem *sm = (LinSmem *)(base + NS * SB);
+    LinSmem *sm = (LinSmem *)(base + NS * SB + LIN_PATCHES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const int64_t cid = tc::cluster_id_x(), ncl = tc::cluster_count_x();
@@ -548,6 +821,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int hw = (warp - 2) >> 2;  // which alternate 32-column chunks it takes
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
         const uint32_t empty0 = tc::cluster_addr(&sm->tmem_empty[0], 0);
+        int turn = 0;
+        const LinOut out{tc::smem_u32(base + NS * SB) +
+                             (uint32_t)((warp - 2) * PATCHES * PATCH_BYTES),
+                         &tmY, &tmZ, lane, &turn};
         int64_t a = 0;
         bool ok = true;
         for (int64_t u = cid; u < n_units && ok; u += ncl)
@@ -558,11 +835,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     break;
                 }
                 tc::tc_fence_after();
-                p.epilogue(u, seg, rank, tmem + lane_base + (uint32_t)ab * SET_COLS, q, hw, lane);
+                p.epilogue(u, seg, rank, tmem + lane_base + (uint32_t)ab * SET_COLS, q, hw, lane,
+                           out);
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive_cluster(empty0 + (uint32_t)ab * 8u);
             }
+        if (lane == 0) tc::bulk_wait<0>();  // the stores' sources go with the CTA
     }
 
     // no MMA, copy or arrival of either CTA targets the other past this point
@@ -578,10 +857,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 // dz = dy act'(z) in bf16 (the products' operand), and per tile the column sums of the unrounded
 // dz. One block per (tile, 64 columns): 8 threads side by side on 8 columns each, 32 row
 // lanes; the sums of a column's 32 row lanes are added in lane order.
-template <bool DY32>
+template <bool DY32, int ACT>
 __global__ void __launch_bounds__(256)
     linear_dz_kernel(const void *__restrict__ dy, const uint16_t *__restrict__ z, Tiles tiles,
-                     int N, int64_t ld, int act, uint16_t *__restrict__ dz, int64_t ld_dz,
+                     int N, int64_t ld, uint16_t *__restrict__ dz, int64_t ld_dz,
                      float *__restrict__ part) {
     __shared__ float red[32][65];
     const int64_t t = blockIdx.x;
@@ -620,7 +899,7 @@ __global__ void __launch_bounds__(256)
                         v[2 * j + 1] = bf16_hi(w[j]);
                     }
                 }
-                if (act != MOK_ACT_NONE) {
+                if (ACT != MOK_ACT_NONE) {
                     const uint4 a = ldg_nc_v4(z + o);
                     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -636,12 +915,12 @@ __global__ void __launch_bounds__(256)
                     v[j] = !in ? 0.f
                            : DY32 ? static_cast<const float *>(dy)[o + j]
                                   : bf16_to_f32(static_cast<const uint16_t *>(dy)[o + j]);
-                    zz[j] = in && act != MOK_ACT_NONE ? bf16_to_f32(z[o + j]) : 0.f;
+                    zz[j] = in && ACT != MOK_ACT_NONE ? bf16_to_f32(z[o + j]) : 0.f;
                 }
             }
-            if (act != MOK_ACT_NONE) {
+            if (ACT != MOK_ACT_NONE) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] *= act_grad_f(zz[j], act);
+                for (int j = 0; j < 8; ++j) v[j] *= act_grad_f<ACT>(zz[j]);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[j] += c + j < N ? v[j] : 0.f;
@@ -704,7 +983,7 @@ cudaError_t map2d(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int
 cudaError_t map_w(CUtensorMap *m, const void *p, int64_t G, int64_t N, int64_t Kin, int64_t ld,
                   int box_rows) {
     cuuint64_t dims[3] = {(cuuint64_t)Kin, (cuuint64_t)N, (cuuint64_t)G};
-    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(N * ld * 2)};
+    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)((G > 1 ? N : 1) * ld * 2)};
     cuuint32_t box[3] = {(cuuint32_t)BK, (cuuint32_t)box_rows, 1};
     cuuint32_t es[3] = {1, 1, 1};
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides,
@@ -713,10 +992,24 @@ cudaError_t map_w(CUtensorMap *m, const void *p, int64_t G, int64_t N, int64_t K
                : cudaErrorInvalidValue;
 }
 
+// an output in bf16: [groups][rows][cols], boxes of 32 columns x 16 rows (patches)
+cudaError_t map_out(CUtensorMap *m, void *p, int64_t G, int64_t rows, int64_t cols, int64_t ld) {
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)G};
+    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)((G > 1 ? rows : 1) * ld * 2)};
+    cuuint32_t box[3] = {32, 16, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return g_encode.load(std::memory_order_acquire)(
+               m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 // pairs of SMs that run at once, one cluster of two per unit at most
 template <class P>
-cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const P &p,
-                          int64_t units_cap, cudaStream_t s) {
+cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &my,
+                          const CUtensorMap &mz, const P &p, int64_t units_cap, cudaStream_t s) {
     if (units_cap < 1) return cudaSuccess;
     static std::atomic<uint64_t> attr_set{0};
     int dev = 0;
@@ -743,8 +1036,32 @@ cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const P 
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, linear_kernel<P>, ma, mb, p);
+    e = cudaLaunchKernelEx(&cfg, linear_kernel<P>, ma, mb, my, mz, p);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool DY32>
+void launch_dz_act(int act, dim3 grid, const void *dy, const uint16_t *z, const Tiles &t, int N,
+                   int64_t ld, uint16_t *dz, int64_t ld_dz, float *part, cudaStream_t s) {
+#define MOK_DZ_CASE(A)                                                                      \
+    case A: linear_dz_kernel<DY32, A><<<grid, 256, 0, s>>>(dy, z, t, N, ld, dz, ld_dz, part); \
+        break
+    switch (act) {
+        MOK_DZ_CASE(MOK_ACT_RELU);
+        MOK_DZ_CASE(MOK_ACT_SILU);
+        MOK_DZ_CASE(MOK_ACT_GELU_TANH);
+        MOK_DZ_CASE(MOK_ACT_GELU);
+        default: linear_dz_kernel<DY32, MOK_ACT_NONE><<<grid, 256, 0, s>>>(dy, z, t, N, ld, dz,
+                                                                         ld_dz, part);
+    }
+#undef MOK_DZ_CASE
+}
+void launch_dz(int act, bool dy32, dim3 grid, const void *dy, const uint16_t *z, const Tiles &t,
+               int N, int64_t ld, uint16_t *dz, int64_t ld_dz, float *part, cudaStream_t s) {
+    if (dy32)
+        launch_dz_act<true>(act, grid, dy, z, t, N, ld, dz, ld_dz, part, s);
+    else
+        launch_dz_act<false>(act, grid, dy, z, t, N, ld, dz, ld_dz, part, s);
 }
 
 bool grouped(const int32_t *starts) { return starts != nullptr; }
@@ -859,16 +1176,28 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
         prof_end(OP_LINEAR_TILES, stream, 1);
         if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
     }
-    CUtensorMap ma, mb;
+    const bool f32 = c->out_dtype == MOK_DTYPE_F32;
+    CUtensorMap ma, mb, my, mz;
     if (map_w(&ma, w, c->groups, c->out_features, c->in_features, c->ld_w, 128) != cudaSuccess ||
         map2d(&mb, x, c->rows, c->in_features, c->ld_in, 128) != cudaSuccess)
         return MOK_ERR_CUDA;
-    const bool f32 = c->out_dtype == MOK_DTYPE_F32;
+    my = mz = mb;  // maps that nothing is stored through
+    if (!f32 &&
+        (map_out(&my, y, 1, c->rows, c->out_features, c->ld_out) != cudaSuccess ||
+         (z && map_out(&mz, z, 1, c->rows, c->out_features, c->ld_out) != cudaSuccess)))
+        return MOK_ERR_CUDA;
     const int segs = f32 ? (c->in_features + SEG_K - 1) / SEG_K : 1;
     const int n_mb = (c->out_features + 255) / 256;
-    Fwd p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias,
-          (const uint16_t *)residual, y, (uint16_t *)z, c->act, f32, status};
-    MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, p, tiles.cap * n_mb, stream));
+    const int64_t units = tiles.cap * n_mb;
+    if (f32) {
+        const Fwd<true> p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias,
+                          (const uint16_t *)residual, y, (uint16_t *)z, c->act, status};
+        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, my, mz, p, units, stream));
+    } else {
+        const Fwd<false> p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias,
+                           (const uint16_t *)residual, y, (uint16_t *)z, c->act, status};
+        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, my, mz, p, units, stream));
+    }
     return MOK_OK;
 }
 
@@ -918,36 +1247,49 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
         float *part = db ? wk.part : nullptr;
         const dim3 grid((unsigned)tiles.cap, (unsigned)((N + 63) / 64));
         prof_begin(OP_LINEAR_DZ, stream);
-        if (dy32)
-            linear_dz_kernel<true><<<grid, 256, 0, stream>>>(dy, (const uint16_t *)z, tiles, N,
-                                                             c->ld_out, c->act, dzo, ld_dz, part);
-        else
-            linear_dz_kernel<false><<<grid, 256, 0, stream>>>(dy, (const uint16_t *)z, tiles, N,
-                                                              c->ld_out, c->act, dzo, ld_dz, part);
+        launch_dz(c->act, dy32, grid, dy, (const uint16_t *)z, tiles, N, c->ld_out, dzo, ld_dz,
+                  part, stream);
         if (db)
             linear_db_kernel<<<(unsigned)(((int64_t)G * N + 255) / 256), 256, 0, stream>>>(
                 wk.part, tiles, G, N, db);
         prof_end(OP_LINEAR_DZ, stream, db ? 2 : 1);
         if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
     }
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, my;
+    const int n_kb = (Kin + 255) / 256;
     if (dx) {
         if (map_w(&ma, w, G, N, Kin, c->ld_w, 64) != cudaSuccess ||
             map2d(&mb, dz, c->rows, N, ld_dz, 128) != cudaSuccess)
             return MOK_ERR_CUDA;
-        const int n_mb = (Kin + 255) / 256;
-        Dx p{tiles, n_mb, 1, Kin, N, c->ld_in, dx, g32, status};
-        MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, p, tiles.cap * n_mb, stream));
+        my = mb;
+        if (!g32 && map_out(&my, dx, 1, c->rows, Kin, c->ld_in) != cudaSuccess)
+            return MOK_ERR_CUDA;
+        const int64_t units = tiles.cap * n_kb;
+        if (g32) {
+            const Dx<true> p{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status};
+            MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, my, my, p, units, stream));
+        } else {
+            const Dx<false> p{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status};
+            MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, my, my, p, units, stream));
+        }
     }
     if (dw) {
         if (map2d(&ma, x, c->rows, Kin, c->ld_in, 64) != cudaSuccess ||
             map2d(&mb, dz, c->rows, N, ld_dz, 64) != cudaSuccess)
             return MOK_ERR_CUDA;
-        const int n_mb = (Kin + 255) / 256, n_nb = (N + 255) / 256;
-        Dw p{starts, grouped(starts) ? wk.valid : nullptr, c->rows, G, n_mb, n_nb, 1, Kin, N,
-             c->ld_w, dw, g32, status};
-        MOK_OP_LAUNCH(OP_LINEAR_DW, 1,
-                      launch_linear(ma, mb, p, (int64_t)G * n_mb * n_nb, stream));
+        my = mb;
+        if (!g32 && map_out(&my, dw, G, N, Kin, c->ld_w) != cudaSuccess) return MOK_ERR_CUDA;
+        const int n_nb = (N + 255) / 256;
+        const int64_t units = (int64_t)G * n_kb * n_nb;
+        const int32_t *valid = grouped(starts) ? wk.valid : nullptr;
+        if (g32) {
+            const Dw<true> p{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw, status};
+            MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(ma, mb, my, my, p, units, stream));
+        } else {
+            const Dw<false> p{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw,
+                              status};
+            MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(ma, mb, my, my, p, units, stream));
+        }
     }
     return MOK_OK;
 }
