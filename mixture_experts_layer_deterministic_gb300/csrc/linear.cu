@@ -32,6 +32,8 @@ constexpr uint32_t SET_COLS = 256; // TMEM columns of one accumulator set
 constexpr int LTILE = 256;         // most rows of a tile
 constexpr int SEG_K = 1024;        // fp32 outputs: K elements per accumulation segment
 constexpr int MAX_G = 1024;
+constexpr int EPI = 8;             // epilogue warps: two per TMEM lane quadrant
+constexpr int LTHREADS = 64 + 32 * EPI;
 
 // ---------------------------------------------------------------- row tiles
 // A tile is up to `height` consecutive rows of one group. Dense: tile t covers rows
@@ -46,19 +48,11 @@ struct Tiles {
         if (list == nullptr) return (rows + height - 1) / height;
         return list[-4] < cap ? list[-4] : cap;
     }
-    // pad: whether the tile's last rows are followed by padding up to a multiple of 16
-    MOK_DEV void get(int64_t t, int *g, int64_t *r0, int64_t *r1, bool *pad) const {
-        if (list == nullptr) {
-            *g = 0;
-            *r0 = t * height;
-            *r1 = *r0 + height < rows ? *r0 + height : rows;
-            *pad = false;
-        } else {
-            *g = list[4 * t];
-            *r0 = list[4 * t + 1];
-            *r1 = list[4 * t + 2];
-            *pad = list[4 * t + 3] != 0;
-        }
+    // (group, first row, end row, whether padding up to a multiple of 16 follows)
+    MOK_DEV int4 get(int64_t t) const {
+        if (list != nullptr) return __ldg(reinterpret_cast<const int4 *>(list) + t);
+        const int64_t r0 = t * height, r1 = r0 + height < rows ? r0 + height : rows;
+        return make_int4(0, (int)r0, (int)r1, 0);
     }
 };
 
@@ -162,14 +156,14 @@ MOK_DEV void with_act(int act, F &&f) {
 }
 
 // ---------------------------------------------------------------- the engine
-// Outputs in bf16 leave through shared memory and TMA. A warp takes 32 columns of its 32 lanes
-// at a time in the 16x256b shape, in which a thread holds two neighbouring columns of a lane;
-// packed to bf16 pairs, stmatrix.trans turns them around into rows of 32 consecutive lanes
-// (64 bytes, 64-byte swizzle: no bank conflicts), and one thread hands the patch to TMA, which
-// drops what lies past the matrix. Against storing each element from its lane this took
-// dW of 64 x 1024 x 4096 from 378 us to a fraction of that (issue slots were the limit).
-constexpr int PATCH_BYTES = 32 * 64;  // 32 columns of 32 lanes in bf16
-constexpr int PATCHES = 2;            // per epilogue warp
+// Outputs in bf16 leave through shared memory. A warp takes 32 columns of its 32 lanes at a
+// time in the 16x256b shape, in which a thread holds two neighbouring columns of a lane;
+// packed to bf16 pairs, stmatrix.trans turns them around into rows of consecutive lanes. Two
+// warps of neighbouring lane quadrants share a patch of 32 rows of 64 lanes, so every row leaves
+// as one 128-byte line: an SM writes lines much faster than half lines (64 bytes a row, by
+// TMA or by the lanes, held dW of 64 x 1024 x 4096 at 3 TB/s, whatever the number of warps).
+constexpr int PATCH_BYTES = 32 * 128;  // 32 columns of 64 lanes in bf16
+constexpr int PATCHES = 2;             // per pair of warps, filled in turn
 
 struct LinSmem {
     uint64_t full[LSTAGES];   // rank 0: both CTAs' copies of the stage have landed
@@ -179,10 +173,16 @@ struct LinSmem {
     uint32_t tmem_base;
     int abort;
 };
-constexpr int LIN_PATCHES = EPI_WARPS * PATCHES * PATCH_BYTES;
+constexpr int LIN_PATCHES = EPI / 2 * PATCHES * PATCH_BYTES;
 constexpr int LIN_SMEM =
     LSTAGES * LSTAGE_BYTES + LIN_PATCHES + 1024 + (int)sizeof(LinSmem);
 static_assert(LIN_SMEM <= 232448, "shared memory of a CTA");
+
+// One unit: a tile of rows (or, for dW, the rows of a group), and which block of the output's
+// contiguous dimension (mb) and of dW's features (nb).
+struct Unit {
+    int g, r0, nr, pad, mb, nb;
+};
 
 // one unit as one CTA of the pair loads and multiplies it
 struct LinGeom {
@@ -225,98 +225,7 @@ MOK_DEV void ld_pairs(uint32_t c, float (&v)[2][4][4]) {
             for (int i = 0; i < 4; ++i) v[h][b][i] = __uint_as_float(r[h][4 * b + i]);
 }
 
-// byte of row n (a column of the accumulator), 16-byte piece i of a patch (64-byte swizzle)
-MOK_DEV uint32_t patch_at(int n, int i) { return (uint32_t)(n * 64 + ((i ^ ((n >> 1) & 3)) << 4)); }
-
-// The values of ld_pairs, rounded to bf16, into a patch: row n holds the 32 lanes of column n
-MOK_DEV void patch_write(uint32_t patch, const float (&v)[2][4][4], int lane) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const uint32_t at = patch + patch_at(8 * b + (lane & 7), lane >> 3);
-        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at),
-                     "r"(pack_bf16x2(v[0][b][0], v[0][b][1])),
-                     "r"(pack_bf16x2(v[0][b][2], v[0][b][3])),
-                     "r"(pack_bf16x2(v[1][b][0], v[1][b][1])),
-                     "r"(pack_bf16x2(v[1][b][2], v[1][b][3]))
-                     : "memory");
-    }
-}
-// the reverse: a patch's bf16 values in ld_pairs' order
-MOK_DEV void patch_read(uint32_t patch, float (&v)[2][4][4], int lane) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const uint32_t at = patch + patch_at(8 * b + (lane & 7), lane >> 3);
-        uint32_t r[4];
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                     : "r"(at)
-                     : "memory");
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i >> 1][b][2 * (i & 1)] = bf16_lo(r[i]);
-            v[i >> 1][b][2 * (i & 1) + 1] = bf16_hi(r[i]);
-        }
-    }
-}
-
-// a bf16 output: matrices of `rows` x `cols`, rows ld apart
-struct OutRef {
-    uint16_t *p;
-    int64_t rows, ld;
-    int cols;
-};
-
-// What an epilogue warp has for its stores: its patches and the output maps.
-struct LinOut {
-    uint32_t patch;  // shared address of its two patches
-    const CUtensorMap *y, *z;
-    int lane;
-    int *turn;       // patch to fill next
-
-    // a patch that no earlier store is still reading
-    MOK_DEV uint32_t next() const {
-        if (lane == 0) tc::bulk_wait_read<PATCHES - 1>();
-        __syncwarp();
-        const uint32_t p = patch + (uint32_t)*turn * PATCH_BYTES;
-        *turn = (*turn + 1) % PATCHES;
-        return p;
-    }
-    // 16-row boxes (1 or 2) of a filled patch to columns x.. of rows y0.. of matrix g of o. TMA
-    // drops rows past o.rows and whole 16-byte pieces past o.cols; it writes the rest of a piece
-    // that the edge cuts, so such a patch is copied element by element.
-    MOK_DEV void store(const CUtensorMap *m, const OutRef &o, uint32_t p, int x, int64_t y0, int g,
-                       int boxes) const {
-        const bool cut = x + 32 > o.cols && (o.cols & 7) != 0;
-        if (!cut) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (cut) {
-            for (int n = lane; n < 16 * boxes && y0 + n < o.rows; n += 32) {
-                uint16_t *row = o.p + ((int64_t)g * o.rows + y0 + n) * o.ld + x;
-                for (int j = 0; x + j < o.cols && j < 32; ++j) {
-                    uint16_t e;
-                    asm volatile("ld.shared.u16 %0, [%1];"
-                                 : "=h"(e)
-                                 : "r"(p + patch_at(n, j >> 3) + 2 * (j & 7))
-                                 : "memory");
-                    row[j] = e;
-                }
-            }
-            __syncwarp();
-        }
-        if (lane == 0) {
-            if (!cut && x < o.cols)
-                for (int i = 0; i < boxes; ++i)
-                    asm volatile(
-                        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}],"
-                        " [%4];" ::"l"((uint64_t)m),
-                        "r"(x), "r"((int)y0 + 16 * i), "r"(g),
-                        "r"(p + (uint32_t)i * (PATCH_BYTES / 2))
-                        : "memory");
-            tc::bulk_commit();
-        }
-    }
-};
-
+// 32 columns, one lane per thread
 MOK_DEV void ld32(uint32_t c, float (&v)[32]) {
     float a[16], b[16];
     tc::tmem_ld16(c, a);
@@ -327,6 +236,128 @@ MOK_DEV void ld32(uint32_t c, float (&v)[32]) {
         v[j] = a[j];
         v[16 + j] = b[j];
     }
+}
+
+// 8 columns of this warp's 32 lanes: v[h][..] as v[h][b][..] of ld_pairs
+MOK_DEV void ld_pairs8(uint32_t c, float (&v)[2][4]) {
+    uint32_t r[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3])
+                     : "r"(c + ((uint32_t)(16 * h) << 16)));
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[h][i] = __uint_as_float(r[h][i]);
+}
+
+// byte of row n (a column of the accumulator), 16-byte piece i of a patch: pieces are exchanged
+// by row, so that neither the matrices nor the rows collide on banks
+MOK_DEV uint32_t patch_at(int n, int i) { return (uint32_t)(n * 128 + ((i ^ (n & 7)) << 4)); }
+
+// 8 columns (rows 8 b .. of the patch) of this warp's lanes, rounded to bf16; half: which 64
+// bytes of a row are the warp's
+MOK_DEV void patch_write8(uint32_t patch, int half, int b, const float (&v)[2][4], int lane) {
+    const uint32_t at = patch + patch_at(8 * b + (lane & 7), 4 * half + (lane >> 3));
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at),
+                 "r"(pack_bf16x2(v[0][0], v[0][1])), "r"(pack_bf16x2(v[0][2], v[0][3])),
+                 "r"(pack_bf16x2(v[1][0], v[1][1])), "r"(pack_bf16x2(v[1][2], v[1][3]))
+                 : "memory");
+}
+// the reverse, added to v
+MOK_DEV void patch_add8(uint32_t patch, int half, int b, float (&v)[2][4], int lane) {
+    const uint32_t at = patch + patch_at(8 * b + (lane & 7), 4 * half + (lane >> 3));
+    uint32_t r[4];
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i >> 1][2 * (i & 1)] += bf16_lo(r[i]);
+        v[i >> 1][2 * (i & 1) + 1] += bf16_hi(r[i]);
+    }
+}
+
+// a bf16 output: matrices of `rows` x `cols`, rows ld apart
+struct OutRef {
+    uint16_t *p;
+    int64_t rows, ld;
+    int cols;
+};
+
+// An epilogue warp's place: its half of the shared patches, its pair's barrier, the patch to
+// fill next. A patch is refilled two turns later; the barrier of the turn between says that the
+// other warp has read it.
+struct Patches {
+    uint32_t base;
+    int bar, half, lane;
+    int turn;
+
+    // both warps' flags and-ed: they go on, or give up, together (neither may leave the other
+    // at a barrier)
+    MOK_DEV bool agree(bool ok) const {
+        uint32_t r;
+        asm volatile(
+            "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, 64, p;\n"
+            "selp.u32 %0, 1, 0, q;\n}\n"
+            : "=r"(r)
+            : "r"(ok ? 1u : 0u), "r"(bar)
+            : "memory");
+        return r != 0;
+    }
+    MOK_DEV uint32_t patch() const { return base + (uint32_t)turn * PATCH_BYTES; }
+    // both halves of the current patch are filled: rows [y0, y0 + 32) and below `end` of matrix
+    // g of o get columns x .. x + 63 (x of the pair), this warp storing 16 of the rows, eight
+    // lanes a row; element by element where the matrix's edge cuts 16 bytes
+    MOK_DEV void store(const OutRef &o, int x, int64_t y0, int64_t end, int g) {
+        asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+        const uint32_t p0 = patch();
+        turn ^= 1;
+        const int col = x + 8 * (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = 16 * half + 4 * i + (lane >> 3);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(p0 + patch_at(n, lane & 7))
+                         : "memory");
+            if (y0 + n >= end) continue;
+            uint16_t *p = o.p + ((int64_t)g * o.rows + y0 + n) * o.ld + col;
+            if (col + 8 <= o.cols) {
+                *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (col + j < o.cols) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+            }
+        }
+    }
+};
+
+// A chunk of an output with no arithmetic: 32 columns of the accumulator, rows from nr on (and
+// everything, with nr <= 0) as zeros
+MOK_DEV void emit_plain(Patches &pt, uint32_t c, int nr, const OutRef &o, int x, int64_t y0,
+                        int64_t end, int g) {
+    float v[2][4][4];
+    ld_pairs(c, v);
+    if (nr < 32) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (8 * k + 2 * (pt.lane & 3) + (i & 1) >= nr) v[0][k][i] = v[1][k][i] = 0.f;
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float w[2][4] = {{v[0][b][0], v[0][b][1], v[0][b][2], v[0][b][3]},
+                               {v[1][b][0], v[1][b][1], v[1][b][2], v[1][b][3]}};
+        patch_write8(pt.patch(), pt.half, b, w, pt.lane);
+    }
+    pt.store(o, x, y0, end, g);
 }
 
 template <bool F32>
@@ -345,18 +376,18 @@ struct Fwd {
     int *status;
 
     MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
-    MOK_DEV LinGeom geom(int64_t u, int seg, uint32_t rank) const {
-        int g;
-        int64_t r0, r1;
-        bool pad;
-        tiles.get(u / n_mb, &g, &r0, &r1, &pad);
+    MOK_DEV Unit unit(uint32_t u) const {
+        const int4 t = tiles.get(u / (uint32_t)n_mb);
+        return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0};
+    }
+    MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
         LinGeom q;
-        q.n_mma = (int)((r1 - r0 + 15) & ~15);
+        q.n_mma = (u.nr + 15) & ~15;
         q.a0 = seg * SEG_K;
-        q.a1 = (int)(u % n_mb) * 256 + (int)rank * 128;
-        q.a2 = g;
+        q.a1 = u.mb * 256 + (int)rank * 128;
+        q.a2 = u.g;
         q.b0 = q.a0;
-        q.b1 = (int32_t)r0 + (int)rank * (q.n_mma / 2);
+        q.b1 = u.r0 + (int)rank * (q.n_mma / 2);
         q.nbox = 1;
         const int k = segs > 1 && Kin - q.a0 > SEG_K ? SEG_K : Kin - q.a0;
         q.k_steps = (k + 15) / 16;
@@ -369,36 +400,39 @@ struct Fwd {
         tma_load_3d_pair(st, tmA, fb, q.a0 + k0, q.a1, q.a2);
         tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, q.b0 + k0, q.b1);
     }
-    MOK_DEV void epilogue(int64_t u, int seg, uint32_t rank, uint32_t c, int q, int hw, int lane,
-                          const LinOut &out) const {
-        int g;
-        int64_t r0, r1;
-        bool pad;
-        tiles.get(u / n_mb, &g, &r0, &r1, &pad);
-        const int nr = (int)(r1 - r0);
+    MOK_DEV void epilogue(const Unit &u, int seg, uint32_t rank, uint32_t c, int q, int hw, int lane,
+                          Patches &pt) const {
+        const int nr = u.nr, pad = u.pad;
+        const int64_t r0 = u.r0;
         const int n_mma = (nr + 15) & ~15;
-        const int f0 = (int)(u % n_mb) * 256 + (int)rank * 128 + q * 32;  // the warp's features
+        const int f0 = u.mb * 256 + (int)rank * 128 + q * 32;  // the warp's features
         if constexpr (F32)
-            direct(seg, c, hw, f0 + lane, g, r0, nr, pad ? n_mma : nr);
+            direct(seg, c, hw, f0 + lane, u.g, r0, nr, pad ? n_mma : nr);
         else
-            staged(c, hw, lane, f0, g, r0, nr, n_mma, out);
+            staged(c, hw, f0, u.g, r0, nr, pad ? n_mma : nr, pt);
     }
-    // bf16: 32 rows at a time through patches
-    MOK_DEV void staged(uint32_t c, int hw, int lane, int f0, int g, int64_t r0, int nr, int n_mma,
-                        const LinOut &out) const {
-        float b[2][2];  // this thread's four features
+    // bf16: 32 rows at a time through patches, 8 rows in registers at once
+    MOK_DEV void staged(uint32_t c, int hw, int f0, int g, int64_t r0, int nr, int n_out,
+                        Patches &pt) const {
+        const int lane = pt.lane;
+        float bs[2][2];  // this thread's four features
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int f = f0 + 8 * i + (lane >> 2);
-            b[i >> 1][i & 1] = bias != nullptr && f < N ? bias[(int64_t)g * N + f] : 0.f;
+            bs[i >> 1][i & 1] = bias != nullptr && f < N ? bias[(int64_t)g * N + f] : 0.f;
         }
-        const OutRef yo{static_cast<uint16_t *>(y), tiles.rows, ld, N}, zo{z, tiles.rows, ld, N};
-        for (int n0 = 32 * hw; n0 < n_mma; n0 += 64) {
-            const int boxes = n_mma - n0 > 16 ? 2 : 1;
-            float v[2][4][4], rs[2][4][4];
-            if (res != nullptr) {
-                // rows of 64 bytes, four lanes each; through a patch into the pairs' order
-                uint4 t[4];
+        const int x = f0 & ~63;
+        const auto z_of = [&](int n, float (&v)[2][4]) {  // rows n.. ; the padding's z is zero
+            ld_pairs8(c + n, v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[h][i] = n + 2 * (lane & 3) + (i & 1) < nr ? v[h][i] + bs[h][i >> 1] : 0.f;
+        };
+        for (int n0 = 32 * hw; n0 < n_out; n0 += 32 * (EPI / 4)) {
+            uint4 t[4];
+            if (res != nullptr) {  // rows of 64 bytes, four lanes each
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int n = 8 * i + (lane >> 2), f = f0 + 8 * (lane & 3);
@@ -409,62 +443,52 @@ struct Fwd {
                             t[i] = *reinterpret_cast<const uint4 *>(p);
                         } else {
                             uint32_t e[4] = {0, 0, 0, 0};
-                            for (int j = 0; j < N - f; ++j)
-                                e[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (f + j < N) e[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
                             t[i] = make_uint4(e[0], e[1], e[2], e[3]);
                         }
                     }
                 }
-                const uint32_t p = out.next();
+            }
+            if (z != nullptr) {
+#pragma unroll 2
+                for (int b = 0; b < 4; ++b) {
+                    float v[2][4];
+                    z_of(n0 + 8 * b, v);
+                    patch_write8(pt.patch(), pt.half, b, v, lane);
+                }
+                pt.store(OutRef{z, tiles.rows, ld, N}, x, r0 + n0, r0 + n_out, 0);
+            }
+            if (res != nullptr) {  // through the patch that y will fill, into the pairs' order
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                     p + patch_at(8 * i + (lane >> 2), lane & 3)),
+                                     pt.patch() +
+                                     patch_at(8 * i + (lane >> 2), 4 * pt.half + (lane & 3))),
                                  "r"(t[i].x), "r"(t[i].y), "r"(t[i].z), "r"(t[i].w)
                                  : "memory");
                 __syncwarp();
-                patch_read(p, rs, lane);
-                if (lane == 0) tc::bulk_commit();  // an empty group: next() counts one a patch
             }
-            ld_pairs(c + n0, v);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[h][k][i] += b[h][i >> 1];
-            if (n0 + 32 > nr) {  // the padding's z is zero
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (n0 + 8 * k + 2 * (lane & 3) + (i & 1) >= nr) v[0][k][i] = v[1][k][i] = 0.f;
-            }
-            if (z != nullptr) {
-                const uint32_t p = out.next();
-                patch_write(p, v, lane);
-                out.store(out.z, zo, p, f0, r0 + n0, 0, boxes);
-            }
-            if (act != MOK_ACT_NONE)
-                with_act(act, [&](auto a) {
+            with_act(act, [&](auto a) {
+#pragma unroll 2
+                for (int b = 0; b < 4; ++b) {
+                    float v[2][4];
+                    z_of(n0 + 8 * b, v);
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[h][k][i] = act_f<a.value>(v[h][k][i]);
-                });
-            if (res != nullptr) {  // act(0) and the residual's padding are zero
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[h][k][i] += rs[h][k][i];
-            }
-            const uint32_t p = out.next();
-            patch_write(p, v, lane);
-            out.store(out.y, yo, p, f0, r0 + n0, 0, boxes);
+                        for (int i = 0; i < 4; ++i) v[h][i] = act_f<a.value>(v[h][i]);
+                    // act(0) and the residual's padding are zero
+                    if (res != nullptr) {
+                        patch_add8(pt.patch(), pt.half, b, v, lane);
+                        __syncwarp();
+                    }
+                    patch_write8(pt.patch(), pt.half, b, v, lane);
+                }
+            });
+            pt.store(OutRef{static_cast<uint16_t *>(y), tiles.rows, ld, N}, x, r0 + n0, r0 + n_out,
+                     0);
         }
     }
     // fp32: from the lanes, 128 bytes a warp and row
@@ -473,7 +497,7 @@ struct Fwd {
         const bool ok = f < N;
         const bool last = seg == segs - 1;
         const float b = bias != nullptr && ok ? bias[(int64_t)g * N + f] : 0.f;
-        for (int n0 = 32 * hw; n0 < ((nr + 15) & ~15); n0 += 64) {
+        for (int n0 = 32 * hw; n0 < ((nr + 15) & ~15); n0 += 32 * (EPI / 4)) {
             float v[32];
             ld32(c + n0, v);
             if (!ok) continue;
@@ -528,18 +552,18 @@ struct Dx {
     int *status;
 
     MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
-    MOK_DEV LinGeom geom(int64_t u, int, uint32_t rank) const {
-        int g;
-        int64_t r0, r1;
-        bool pad;
-        tiles.get(u / n_mb, &g, &r0, &r1, &pad);
+    MOK_DEV Unit unit(uint32_t u) const {
+        const int4 t = tiles.get(u / (uint32_t)n_mb);
+        return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0};
+    }
+    MOK_DEV LinGeom geom(const Unit &u, int, uint32_t rank) const {
         LinGeom q;
-        q.n_mma = (int)((r1 - r0 + 15) & ~15);
-        q.a0 = (int)(u % n_mb) * 256 + (int)rank * 128;
+        q.n_mma = (u.nr + 15) & ~15;
+        q.a0 = u.mb * 256 + (int)rank * 128;
         q.a1 = 0;
-        q.a2 = g;
+        q.a2 = u.g;
         q.b0 = 0;
-        q.b1 = (int32_t)r0 + (int)rank * (q.n_mma / 2);
+        q.b1 = u.r0 + (int)rank * (q.n_mma / 2);
         q.nbox = 1;
         q.k_steps = (N + 15) / 16;
         return q;
@@ -552,16 +576,13 @@ struct Dx {
         tma_load_3d_pair(st + BOX, tmA, fb, q.a0 + 64, k0, q.a2);
         tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, k0, q.b1);
     }
-    MOK_DEV void epilogue(int64_t u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
-                          const LinOut &out) const {
-        int g;
-        int64_t r0, r1;
-        bool pad;
-        tiles.get(u / n_mb, &g, &r0, &r1, &pad);
-        const int nr = (int)(r1 - r0);
+    MOK_DEV void epilogue(const Unit &u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
+                          Patches &pt) const {
+        const int nr = u.nr, pad = u.pad;
+        const int64_t r0 = u.r0;
         const int n_mma = (nr + 15) & ~15;
-        const int i0 = (int)(u % n_mb) * 256 + (int)rank * 128 + q * 32;
-        for (int n0 = 32 * hw; n0 < n_mma; n0 += 64) {
+        const int i0 = u.mb * 256 + (int)rank * 128 + q * 32;
+        for (int n0 = 32 * hw; n0 < n_mma; n0 += 32 * (EPI / 4)) {
             if constexpr (F32) {
                 float v[32];
                 ld32(c + n0, v);
@@ -572,20 +593,8 @@ struct Dx {
                 for (int j = 0; j < 32; ++j)
                     if (j < n_out) o[(int64_t)j * ld] = n0 + j < nr ? v[j] : 0.f;
             } else {
-                float v[2][4][4];
-                ld_pairs(c + n0, v);
-                if (n0 + 32 > nr) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (n0 + 8 * k + 2 * (lane & 3) + (i & 1) >= nr)
-                                v[0][k][i] = v[1][k][i] = 0.f;
-                }
-                const uint32_t p = out.next();
-                patch_write(p, v, lane);
-                out.store(out.y, OutRef{static_cast<uint16_t *>(dx), tiles.rows, ld, Kin}, p, i0,
-                          r0 + n0, 0, n_mma - n0 > 16 ? 2 : 1);
+                emit_plain(pt, c + n0, nr - n0, OutRef{static_cast<uint16_t *>(dx), tiles.rows, ld, Kin},
+                           i0 & ~63, r0 + n0, r0 + (pad ? n_mma : nr), 0);
             }
         }
     }
@@ -604,27 +613,26 @@ struct Dw {
     int *status;
 
     MOK_DEV int64_t n_units() const { return (int64_t)G * n_mb * n_nb; }
-    MOK_DEV void get(int64_t u, int *g, int *mb, int *nb) const {
-        *g = (int)(u / ((int64_t)n_mb * n_nb));
-        const int rest = (int)(u % ((int64_t)n_mb * n_nb));
-        *nb = rest / n_mb;
-        *mb = rest % n_mb;
+    MOK_DEV Unit unit(uint32_t u) const {
+        const uint32_t per = (uint32_t)n_mb * (uint32_t)n_nb, rest = u % per;
+        const int g = (int)(u / per);
+        return Unit{g, starts != nullptr ? __ldg(starts + g) : 0,
+                    valid != nullptr ? __ldg(valid + g) : (int)rows, 0,
+                    (int)(rest % (uint32_t)n_mb), (int)(rest / (uint32_t)n_mb)};
     }
-    MOK_DEV int64_t count(int g) const { return valid != nullptr ? valid[g] : rows; }
-    MOK_DEV LinGeom geom(int64_t u, int, uint32_t rank) const {
-        int g, mb, nb;
-        get(u, &g, &mb, &nb);
+    MOK_DEV LinGeom geom(const Unit &u, int, uint32_t rank) const {
+        const int mb = u.mb, nb = u.nb;
         LinGeom q;
         // MN-major B comes in boxes of 64 columns per CTA: N of the MMA is 128 or 256, columns
         // past the matrix being zeros
         q.n_mma = N - nb * 256 <= 128 ? 128 : 256;
         q.nbox = q.n_mma / 128;
         q.a0 = mb * 256 + (int)rank * 128;
-        q.a1 = starts != nullptr ? starts[g] : 0;
+        q.a1 = u.r0;
         q.a2 = 0;
         q.b0 = nb * 256 + (int)rank * (q.n_mma / 2);
         q.b1 = q.a1;
-        q.k_steps = (int)((count(g) + 15) / 16);
+        q.k_steps = (u.nr + 15) / 16;
         return q;
     }
     MOK_DEV uint32_t tx(const LinGeom &q) const { return (2 + q.nbox) * BOX; }
@@ -635,14 +643,13 @@ struct Dw {
         for (int j = 0; j < q.nbox; ++j)
             tc::tma_load_2d_pair(st + (2 + j) * BOX, tmB, fb, q.b0 + 64 * j, q.b1 + k0);
     }
-    MOK_DEV void epilogue(int64_t u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
-                          const LinOut &out) const {
-        int g, mb, nb;
-        get(u, &g, &mb, &nb);
+    MOK_DEV void epilogue(const Unit &u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
+                          Patches &pt) const {
+        const int g = u.g, mb = u.mb, nb = u.nb;
         const int nn = N - nb * 256 < 256 ? N - nb * 256 : 256;
-        const bool any = count(g) > 0;
+        const bool any = u.nr > 0;
         const int i0 = mb * 256 + (int)rank * 128 + q * 32;
-        for (int n0 = 32 * hw; n0 < nn; n0 += 64) {
+        for (int n0 = 32 * hw; n0 < nn; n0 += 32 * (EPI / 4)) {
             if constexpr (F32) {
                 float v[32];
                 ld32(c + n0, v);
@@ -653,47 +660,57 @@ struct Dw {
                 for (int j = 0; j < 32; ++j)
                     if (n0 + j < nn) o[(int64_t)j * ld] = any ? v[j] : 0.f;
             } else {
-                float v[2][4][4];
-                ld_pairs(c + n0, v);
-                if (!any) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[0][k][i] = v[1][k][i] = 0.f;
-                }
-                const uint32_t p = out.next();
-                patch_write(p, v, lane);
-                out.store(out.y, OutRef{static_cast<uint16_t *>(dw), N, ld, Kin}, p, i0, nb * 256 + n0,
-                          g, nn - n0 > 16 ? 2 : 1);
+                emit_plain(pt, c + n0, any ? 32 : 0, OutRef{static_cast<uint16_t *>(dw), N, ld, Kin},
+                           i0 & ~63, nb * 256 + n0, N, g);
             }
         }
     }
 };
 
+// Arrive on a barrier of either CTA of the pair. CTA scope: what the barrier hands over lives in
+// TMEM, ordered by the tcgen05 fences. Cluster scope made the arriving thread wait for its
+// global stores to land, about 2 us a unit (dW of 64 x 1024 x 4096: 208 us instead of what the
+// DESIGN table shows).
+MOK_DEV void lin_arrive(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+                 : "memory");
+}
+// A bounded wait that takes the time only after many polls: the clock read costs more than
+// most waits here are long.
 MOK_DEV bool lin_wait(uint64_t *bar, uint32_t parity, int *status, volatile int *abort) {
-    return tc::wait_bounded_cluster(bar, parity, status, abort, tc::WAIT_LIMIT_NS);
+    uint64_t t0 = 0;
+    for (uint32_t n = 1; !tc::mbar_try_wait(bar, parity); ++n) {
+        if ((n & 255u) != 0) continue;
+        if (*abort) return false;
+        const uint64_t t = tc::globaltimer();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > tc::WAIT_LIMIT_NS) {
+            raise_status(status, MOK_ERR_TIMEOUT);
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
 }
 // bounded drain of a barrier phase on the way out
 MOK_DEV void lin_drain(uint64_t *bar, uint32_t parity) {
     const uint64_t t0 = tc::globaltimer();
-    while (!tc::mbar_try_wait_cluster(bar, parity) && tc::globaltimer() - t0 < 100000000ull) {
+    while (!tc::mbar_try_wait(bar, parity) && tc::globaltimer() - t0 < 100000000ull) {
     }
 }
 
 template <class P>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(LTHREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA,
-                  const __grid_constant__ CUtensorMap tmB,
-                  const __grid_constant__ CUtensorMap tmY,
-                  const __grid_constant__ CUtensorMap tmZ, const P p) {
+                  const __grid_constant__ CUtensorMap tmB, const P p) {
     constexpr int NS = LSTAGES, SB = LSTAGE_BYTES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     LinSmem *sm = (LinSmem *)(base + NS * SB + LIN_PATCHES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
-    const int64_t cid = tc::cluster_id_x(), ncl = tc::cluster_count_x();
-    const int64_t n_units = p.n_units();
+    const uint32_t cid = tc::cluster_id_x(), ncl = tc::cluster_count_x();
+    const uint32_t n_units = (uint32_t)p.n_units();
     const int segs = p.segs;
 
     if (threadIdx.x == 0) {
@@ -703,7 +720,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&sm->tmem_full[b], 1);
-            tc::mbar_init(&sm->tmem_empty[b], 2 * EPI_WARPS);
+            tc::mbar_init(&sm->tmem_empty[b], 2 * EPI);
         }
         sm->abort = 0;
         tc::fence_mbar_init();
@@ -729,9 +746,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             uint32_t ph = 0;
             int64_t issued = 0;
             bool ok = true;
-            for (int64_t u = cid; u < n_units && ok; u += ncl)
+            for (uint32_t u = cid; u < n_units && ok; u += ncl) {
+                const Unit cur = p.unit(u);
                 for (int seg = 0; seg < segs && ok; ++seg) {
-                    const LinGeom g = p.geom(u, seg, rank);
+                    const LinGeom g = p.geom(cur, seg, rank);
                     const uint32_t tx = p.tx(g);
                     const int kblocks = (g.k_steps + 3) / 4;
                     for (int kb = 0; kb < kblocks; ++kb) {
@@ -748,6 +766,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                     }
                 }
+            }
             // do not leave while copies may still be landing: the MMAs that read the last
             // stages have finished (bounded)
             for (int q = 0; q < NS && q < issued; ++q) {
@@ -765,9 +784,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             uint32_t ph = 0;
             int64_t a = 0;  // accumulations so far: number a uses set a % 2
             bool ok = true;
-            for (int64_t u = cid; u < n_units && ok; u += ncl)
+            for (uint32_t u = cid; u < n_units && ok; u += ncl) {
+                const Unit cur = p.unit(u);
                 for (int seg = 0; seg < segs && ok; ++seg) {
-                    const LinGeom g = p.geom(u, seg, 0);
+                    const LinGeom g = p.geom(cur, seg, 0);
                     const uint32_t idesc = tc::idesc_bf16(256, g.n_mma, P::A_MN, P::B_MN);
                     const int ab = (int)(a & 1);
                     const uint32_t use = (uint32_t)((a >> 1) & 1);
@@ -808,6 +828,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     tc::mma_commit_pair(&sm->tmem_full[ab], 3);
                     ++a;
                 }
+            }
             // do not free TMEM under MMAs still in flight (bounded)
             if (a > 0) {
                 const int lb = (int)((a - 1) & 1);
@@ -818,30 +839,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;          // TMEM lane quadrant this warp may access
-        const int hw = (warp - 2) >> 2;  // which alternate 32-column chunks it takes
+        const int hw = (warp - 2) >> 2;  // it takes every second chunk of 32 columns from this
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
         const uint32_t empty0 = tc::cluster_addr(&sm->tmem_empty[0], 0);
-        int turn = 0;
-        const LinOut out{tc::smem_u32(base + NS * SB) +
-                             (uint32_t)((warp - 2) * PATCHES * PATCH_BYTES),
-                         &tmY, &tmZ, lane, &turn};
+        const int pair = 2 * hw + (q >> 1);
+        Patches pt{tc::smem_u32(base + NS * SB) + (uint32_t)(pair * PATCHES * PATCH_BYTES),
+                   1 + pair, q & 1, lane, 0};
         int64_t a = 0;
         bool ok = true;
-        for (int64_t u = cid; u < n_units && ok; u += ncl)
+        for (uint32_t u = cid; u < n_units && ok; u += ncl) {
+            const Unit cur = p.unit(u);
             for (int seg = 0; seg < segs; ++seg, ++a) {
                 const int ab = (int)(a & 1);
-                if (!lin_wait(&sm->tmem_full[ab], (uint32_t)((a >> 1) & 1), p.status, abort)) {
-                    ok = false;
-                    break;
-                }
+                ok = pt.agree(
+                    lin_wait(&sm->tmem_full[ab], (uint32_t)((a >> 1) & 1), p.status, abort));
+                if (!ok) break;
                 tc::tc_fence_after();
-                p.epilogue(u, seg, rank, tmem + lane_base + (uint32_t)ab * SET_COLS, q, hw, lane,
-                           out);
+                p.epilogue(cur, seg, rank, tmem + lane_base + (uint32_t)ab * SET_COLS, q, hw, lane,
+                           pt);
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(empty0 + (uint32_t)ab * 8u);
+                if (lane == 0) lin_arrive(empty0 + (uint32_t)ab * 8u);
             }
-        if (lane == 0) tc::bulk_wait<0>();  // the stores' sources go with the CTA
+        }
     }
 
     // no MMA, copy or arrival of either CTA targets the other past this point
@@ -865,10 +885,9 @@ __global__ void __launch_bounds__(256)
     __shared__ float red[32][65];
     const int64_t t = blockIdx.x;
     if (t >= tiles.count()) return;
-    int g;
-    int64_t r0, r1;
-    bool pad;
-    tiles.get(t, &g, &r0, &r1, &pad);
+    const int4 tile = tiles.get(t);
+    const int64_t r0 = tile.y, r1 = tile.z;
+    const bool pad = tile.w != 0;
     const int64_t rend = pad ? (r1 + 15) & ~(int64_t)15 : r1;
     const int cv = threadIdx.x & 7, rl = threadIdx.x >> 3;
     const int c = blockIdx.y * 64 + cv * 8;
@@ -992,25 +1011,12 @@ cudaError_t map_w(CUtensorMap *m, const void *p, int64_t G, int64_t N, int64_t K
                : cudaErrorInvalidValue;
 }
 
-// an output in bf16: [groups][rows][cols], boxes of 32 columns x 16 rows (patches)
-cudaError_t map_out(CUtensorMap *m, void *p, int64_t G, int64_t rows, int64_t cols, int64_t ld) {
-    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)G};
-    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)((G > 1 ? rows : 1) * ld * 2)};
-    cuuint32_t box[3] = {32, 16, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return g_encode.load(std::memory_order_acquire)(
-               m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
-}
-
 // pairs of SMs that run at once, one cluster of two per unit at most
 template <class P>
-cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &my,
-                          const CUtensorMap &mz, const P &p, int64_t units_cap, cudaStream_t s) {
+cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const P &p,
+                          int64_t units_cap, cudaStream_t s) {
     if (units_cap < 1) return cudaSuccess;
+    if (units_cap > 0x7FFFFFFF) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> attr_set{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1031,12 +1037,12 @@ cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const CU
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(2 * (units_cap < pairs ? units_cap : pairs)), 1, 1);
-    cfg.blockDim = dim3(NTHREADS, 1, 1);
+    cfg.blockDim = dim3(LTHREADS, 1, 1);
     cfg.dynamicSmemBytes = LIN_SMEM;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, linear_kernel<P>, ma, mb, my, mz, p);
+    e = cudaLaunchKernelEx(&cfg, linear_kernel<P>, ma, mb, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1177,14 +1183,9 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
         if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
     }
     const bool f32 = c->out_dtype == MOK_DTYPE_F32;
-    CUtensorMap ma, mb, my, mz;
+    CUtensorMap ma, mb;
     if (map_w(&ma, w, c->groups, c->out_features, c->in_features, c->ld_w, 128) != cudaSuccess ||
         map2d(&mb, x, c->rows, c->in_features, c->ld_in, 128) != cudaSuccess)
-        return MOK_ERR_CUDA;
-    my = mz = mb;  // maps that nothing is stored through
-    if (!f32 &&
-        (map_out(&my, y, 1, c->rows, c->out_features, c->ld_out) != cudaSuccess ||
-         (z && map_out(&mz, z, 1, c->rows, c->out_features, c->ld_out) != cudaSuccess)))
         return MOK_ERR_CUDA;
     const int segs = f32 ? (c->in_features + SEG_K - 1) / SEG_K : 1;
     const int n_mb = (c->out_features + 255) / 256;
@@ -1192,11 +1193,11 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
     if (f32) {
         const Fwd<true> p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias,
                           (const uint16_t *)residual, y, (uint16_t *)z, c->act, status};
-        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, my, mz, p, units, stream));
+        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, p, units, stream));
     } else {
         const Fwd<false> p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias,
                            (const uint16_t *)residual, y, (uint16_t *)z, c->act, status};
-        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, my, mz, p, units, stream));
+        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, p, units, stream));
     }
     return MOK_OK;
 }
@@ -1255,40 +1256,35 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
         prof_end(OP_LINEAR_DZ, stream, db ? 2 : 1);
         if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
     }
-    CUtensorMap ma, mb, my;
+    CUtensorMap ma, mb;
     const int n_kb = (Kin + 255) / 256;
     if (dx) {
         if (map_w(&ma, w, G, N, Kin, c->ld_w, 64) != cudaSuccess ||
             map2d(&mb, dz, c->rows, N, ld_dz, 128) != cudaSuccess)
             return MOK_ERR_CUDA;
-        my = mb;
-        if (!g32 && map_out(&my, dx, 1, c->rows, Kin, c->ld_in) != cudaSuccess)
-            return MOK_ERR_CUDA;
         const int64_t units = tiles.cap * n_kb;
         if (g32) {
             const Dx<true> p{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status};
-            MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, my, my, p, units, stream));
+            MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, p, units, stream));
         } else {
             const Dx<false> p{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status};
-            MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, my, my, p, units, stream));
+            MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, p, units, stream));
         }
     }
     if (dw) {
         if (map2d(&ma, x, c->rows, Kin, c->ld_in, 64) != cudaSuccess ||
             map2d(&mb, dz, c->rows, N, ld_dz, 64) != cudaSuccess)
             return MOK_ERR_CUDA;
-        my = mb;
-        if (!g32 && map_out(&my, dw, G, N, Kin, c->ld_w) != cudaSuccess) return MOK_ERR_CUDA;
         const int n_nb = (N + 255) / 256;
         const int64_t units = (int64_t)G * n_kb * n_nb;
         const int32_t *valid = grouped(starts) ? wk.valid : nullptr;
         if (g32) {
             const Dw<true> p{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw, status};
-            MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(ma, mb, my, my, p, units, stream));
+            MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(ma, mb, p, units, stream));
         } else {
             const Dw<false> p{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw,
                               status};
-            MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(ma, mb, my, my, p, units, stream));
+            MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(ma, mb, p, units, stream));
         }
     }
     return MOK_OK;
