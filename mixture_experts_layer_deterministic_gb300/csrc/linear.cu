@@ -25,6 +25,14 @@
 namespace mok {
 namespace {
 
+// two fp32 values to bf16 in one conversion, lo in the low half (two single conversions run on
+// the slow pipe and held the epilogue: dW of 64 x 1024 x 4096 164 against 139 us)
+MOK_DEV uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 constexpr int BOX = 64 * 128;      // one 64 x 64 bf16 box (8 KB)
 constexpr int LSTAGES = 6;
 constexpr int LSTAGE_BYTES = 4 * BOX;
@@ -262,8 +270,8 @@ MOK_DEV uint32_t patch_at(int n, int i) { return (uint32_t)(n * 128 + ((i ^ (n &
 MOK_DEV void patch_write8(uint32_t patch, int half, int b, const float (&v)[2][4], int lane) {
     const uint32_t at = patch + patch_at(8 * b + (lane & 7), 4 * half + (lane >> 3));
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at),
-                 "r"(pack_bf16x2(v[0][0], v[0][1])), "r"(pack_bf16x2(v[0][2], v[0][3])),
-                 "r"(pack_bf16x2(v[1][0], v[1][1])), "r"(pack_bf16x2(v[1][2], v[1][3]))
+                 "r"(pack2(v[0][0], v[0][1])), "r"(pack2(v[0][2], v[0][3])),
+                 "r"(pack2(v[1][0], v[1][1])), "r"(pack2(v[1][2], v[1][3]))
                  : "memory");
 }
 // the reverse, added to v
@@ -316,23 +324,31 @@ struct Patches {
         asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
         const uint32_t p0 = patch();
         turn ^= 1;
-        const int col = x + 8 * (lane & 7);
+        const int col = x + 8 * (lane & 7), n0 = 16 * half + (lane >> 3);
+        uint16_t *p = o.p + ((int64_t)g * o.rows + y0 + n0) * o.ld + col;
+        uint32_t w[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = 16 * half + 4 * i + (lane >> 3);
-            uint32_t w[4];
+        for (int i = 0; i < 4; ++i)
             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(p0 + patch_at(n, lane & 7))
+                         : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                         : "r"(p0 + patch_at(n0 + 4 * i, lane & 7))
                          : "memory");
-            if (y0 + n >= end) continue;
-            uint16_t *p = o.p + ((int64_t)g * o.rows + y0 + n) * o.ld + col;
+        const int64_t step = 4 * o.ld;
+        if (y0 + 32 <= end && x + 64 <= o.cols) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i, p += step)
+                *reinterpret_cast<uint4 *>(p) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i, p += step) {
+            if (y0 + n0 + 4 * i >= end) continue;
             if (col + 8 <= o.cols) {
-                *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(p) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (col + j < o.cols) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+                    if (col + j < o.cols) p[j] = (uint16_t)(w[i][j >> 1] >> (16 * (j & 1)));
             }
         }
     }
@@ -780,6 +796,16 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (rank 0)
         if (rank == 0 && tc::elect_one()) {
+            // Descriptors of stage 0; a stage, and a K step of 16 elements, move only the address
+            // (in 16-byte units). MN-major: 16 K rows are two groups of eight 128-byte rows,
+            // blocks of 64 M or N elements BOX apart; K-major: 32 bytes along the row. The
+            // issuing thread's own instructions count here: with the descriptors built per
+            // step a K block took no less time at N = 160 than at 256.
+            constexpr uint32_t A_STEP = (P::A_MN ? 2048 : 32) >> 4;
+            constexpr uint32_t B_STEP = (P::B_MN ? 2048 : 32) >> 4;
+            const uint32_t s0 = tc::smem_u32(base);
+            const uint64_t da0 = tc::sdesc_sw128(s0, P::A_MN ? BOX : 16, 1024);
+            const uint64_t db0 = tc::sdesc_sw128(s0 + 2 * BOX, P::B_MN ? BOX : 16, 1024);
             int s = 0;
             uint32_t ph = 0;
             int64_t a = 0;  // accumulations so far: number a uses set a % 2
@@ -804,19 +830,17 @@ __global__ void __launch_bounds__(LTHREADS, 1)
                             break;
                         }
                         tc::tc_fence_after();
-                        const uint32_t sa = tc::smem_u32(base + s * SB);
-                        const uint32_t sb = sa + 2 * BOX;
-                        const int steps = g.k_steps - kb * 4 < 4 ? g.k_steps - kb * 4 : 4;
-                        for (int kk = 0; kk < steps; ++kk) {
-                            // MN-major: 16 K rows = 2 groups of eight 128-byte rows, blocks of
-                            // 64 M or N elements BOX apart; K-major: 32 bytes along the row
-                            const uint64_t da = P::A_MN
-                                                    ? tc::sdesc_sw128(sa + kk * 2048, BOX, 1024)
-                                                    : tc::sdesc_sw128(sa + kk * 32, 16, 1024);
-                            const uint64_t db = P::B_MN
-                                                    ? tc::sdesc_sw128(sb + kk * 2048, BOX, 1024)
-                                                    : tc::sdesc_sw128(sb + kk * 32, 16, 1024);
-                            tc::mma_f16_pair(d, da, db, idesc, kb > 0 || kk > 0 ? 1u : 0u);
+                        const uint64_t da = da0 + (uint64_t)(s * (SB >> 4));
+                        const uint64_t db = db0 + (uint64_t)(s * (SB >> 4));
+                        if (g.k_steps - kb * 4 >= 4) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc::mma_f16_pair(d, da + kk * A_STEP, db + kk * B_STEP, idesc,
+                                                 kk > 0 ? 1u : (kb > 0 ? 1u : 0u));
+                        } else {
+                            for (int kk = 0; kk < g.k_steps - kb * 4; ++kk)
+                                tc::mma_f16_pair(d, da + kk * A_STEP, db + kk * B_STEP, idesc,
+                                                 kb > 0 || kk > 0 ? 1u : 0u);
                         }
                         tc::mma_commit_pair(&sm->empty[s], 3);  // frees the stage in both CTAs
                         if (++s == NS) {
@@ -947,8 +971,8 @@ __global__ void __launch_bounds__(256)
         if (dz != nullptr && c < N) {
             uint16_t *o = dz + r * ld_dz + c;  // ld_dz is a multiple of 8: whole vectors
             *reinterpret_cast<uint4 *>(o) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]),
+                           pack2(v[4], v[5]), pack2(v[6], v[7]));
         }
     }
     if (part == nullptr) return;
