@@ -17,6 +17,17 @@ namespace {
 constexpr int TPB = 256;
 constexpr int WARPS = TPB / 32;
 constexpr int MAX_E = 1024;
+// 16-byte pieces per lane and row of an item: a warp reads a row in runs of 1 KB (16384 tokens x
+// 10 rows x 4096 bf16: combine 291 us at one piece, 246 us at two;
+// and its gradient 281 us at one, 241 us at two for 8192 tokens)
+constexpr int COMBINE_U = 2;
+constexpr int COMBINE_BWD_U = 2;
+// blocks per SM, looping over the items: dispatch holds few registers and wants many stores in
+// flight (16: 235 us, 4: 261 us); the other two hold 8 rows a lane in registers, two blocks an SM
+// are resident, and longer-lived blocks read neighbouring rows together (16: 247 and 242 us,
+// 4: 243 and 241 us)
+constexpr int DISPATCH_BLOCKS = 16;
+constexpr int COMBINE_BLOCKS = 4;
 
 inline unsigned grid_for(int64_t items, int per_block, int per_sm) {
     const int64_t cap = (int64_t)device_sm_count() * per_sm;
@@ -225,104 +236,140 @@ __global__ void __launch_bounds__(TPB)
 }
 
 // ---------------------------------------------------------------- combine
-// Work item: (token, segment of 32 vectors), one warp each. Lane k holds row and weight of
-// copy k; the K rows are read four at a time.
+// PER elements of a row from column c, as fp32; elements past H are zero
 template <bool F32, bool VEC>
+struct Piece {
+    static constexpr int PER = VEC ? Elem<F32>::PER : 1;
+    uint4 q;
+    float e;
+    // raw load: whole vectors only (VEC), or one element
+    MOK_DEV void load(const uint8_t *row, int c, bool in) {
+        if (VEC) {
+            q = make_uint4(0, 0, 0, 0);
+            if (in) q = ldg_nc_v4(row + (int64_t)c * Elem<F32>::BYTES);
+        } else {
+            e = in ? load_elem<F32>(row, c) : 0.f;
+        }
+    }
+    MOK_DEV void values(float (&v)[PER]) const {
+        if constexpr (VEC) unpack<F32>(q, v);
+        else v[0] = e;
+    }
+};
+
+// Work item: (token, segment of 32*U pieces of 16 bytes), one warp each. Lane k holds row and
+// weight of copy k. The K rows are read in rounds of equal size, at most 8 rows x U pieces a
+// lane, all loads of a round before the first is used: the rounds' memory latency is what
+// bounds a warp here. A dropped copy has weight zero and reads as zero.
+template <bool F32, bool VEC, int U>
 __global__ void __launch_bounds__(TPB)
     combine_rows_kernel(const void *__restrict__ rows, const int32_t *__restrict__ map,
                         const float *__restrict__ w, const void *res, int64_t T, int K, int H,
                         int64_t ld_tok, int64_t ld_row, int64_t n_rows, void *y, int *status) {
-    constexpr int B = Elem<F32>::BYTES, PER = VEC ? Elem<F32>::PER : 1;
+    using P = Piece<F32, VEC>;
+    constexpr int B = Elem<F32>::BYTES, PER = P::PER;
     const int lane = threadIdx.x & 31;
-    const int segs = (H + PER * 32 - 1) / (PER * 32);
+    const int segs = (H + PER * 32 * U - 1) / (PER * 32 * U);
+    const int rounds = (K + 7) / 8, per_round = (K + rounds - 1) / rounds;
     const int64_t items = T * segs;
     const int64_t nw = (int64_t)gridDim.x * WARPS;
     for (int64_t it = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); it < items; it += nw) {
-        const int64_t t = it / segs;
-        const int c = ((int)(it % segs) * 32 + lane) * PER;  // this lane's first column
+        const int64_t t = segs == 1 ? it : it / segs;
+        const int c0 = ((int)(it - t * segs) * 32 * U + lane) * PER;  // first column, step 32 PER
         const int32_t rk = lane < K ? row_of(map, t * K + lane, n_rows, status) : -1;
-        const float wk = lane < K ? (w != nullptr ? w[t * K + lane] : 1.0f) : 0.f;
+        const float wk = rk >= 0 ? (w != nullptr ? w[t * K + lane] : 1.0f) : 0.f;
+        float acc[U][PER];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int q = 0; q < PER; ++q) acc[u][q] = 0.f;
+        for (int k0 = 0; k0 < K; k0 += per_round) {
+            P b[8][U];
+            float s[8];
+            const int kn = K - k0 < per_round ? K - k0 : per_round;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j >= kn) break;
+                const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
+                s[j] = __shfl_sync(0xFFFFFFFFu, wk, k0 + j);
+                const uint8_t *p = static_cast<const uint8_t *>(rows) + r * ld_row * B;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    b[j][u].load(p, c0 + u * 32 * PER, r >= 0 && c0 + u * 32 * PER + PER <= H);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j >= kn) break;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float v[PER];
+                    b[j][u].values(v);
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) acc[u][q] = fmaf(s[j], v[q], acc[u][q]);
+                }
+            }
+        }
         const uint8_t *resp =
             res != nullptr ? static_cast<const uint8_t *>(res) + t * ld_tok * B : nullptr;
         uint8_t *yp = static_cast<uint8_t *>(y) + t * ld_tok * B;
-        const bool whole = VEC && c + PER <= H;
-        float acc[PER];
 #pragma unroll
-        for (int q = 0; q < PER; ++q) acc[q] = 0.f;
-        for (int k0 = 0; k0 < K; k0 += 4) {
-            uint4 b[4];
-            float e[4][VEC ? 1 : PER];
-            int32_t r[4];
-            float s[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = k0 + j;
-                r[j] = __shfl_sync(0xFFFFFFFFu, rk, k < K ? k : K - 1);
-                s[j] = __shfl_sync(0xFFFFFFFFu, wk, k < K ? k : K - 1);
-                if (k >= K) r[j] = -1;
-                if (r[j] < 0) continue;
-                const uint8_t *p = static_cast<const uint8_t *>(rows) + r[j] * ld_row * B;
-                if (VEC) {
-                    if (whole) b[j] = ldg_nc_v4(p + (int64_t)c * B);
-                } else if (c < H) {
-                    e[j][0] = load_elem<F32>(p, c);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (r[j] < 0) continue;
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 32 * PER;
+            if (c + PER <= H) {
                 if constexpr (VEC) {
-                    float v[PER];
-                    if (whole) {
-                        unpack<F32>(b[j], v);
-                    } else {
-                        const uint8_t *p = static_cast<const uint8_t *>(rows) + r[j] * ld_row * B;
+                    if (resp != nullptr) {
+                        float v[PER];
+                        unpack<F32>(*reinterpret_cast<const uint4 *>(resp + (int64_t)c * B), v);
 #pragma unroll
-                        for (int q = 0; q < PER; ++q)
-                            v[q] = c + q < H ? load_elem<F32>(p, c + q) : 0.f;
+                        for (int q = 0; q < PER; ++q) acc[u][q] += v[q];
                     }
-#pragma unroll
-                    for (int q = 0; q < PER; ++q) acc[q] = fmaf(s[j], v[q], acc[q]);
-                } else if (c < H) {
-                    acc[0] = fmaf(s[j], e[j][0], acc[0]);
+                    *reinterpret_cast<uint4 *>(yp + (int64_t)c * B) = pack<F32>(acc[u]);
+                } else {
+                    store_elem<F32>(yp, c,
+                                    acc[u][0] + (resp != nullptr ? load_elem<F32>(resp, c) : 0.f));
                 }
             }
         }
-        if constexpr (VEC) {
-            if (whole) {
-                if (resp != nullptr) {
-                    float v[PER];
-                    unpack<F32>(*reinterpret_cast<const uint4 *>(resp + (int64_t)c * B), v);
-#pragma unroll
-                    for (int q = 0; q < PER; ++q) acc[q] += v[q];
+        // the columns past the last whole vector, at most PER - 1: one a lane
+        if (VEC && H % PER != 0) {
+            const int c = H / PER * PER + lane;
+            const int seg_of_tail = (H / PER) / (32 * U);
+            if ((int)(it - t * segs) == seg_of_tail) {
+                float a = 0.f;
+                for (int k = 0; k < K; ++k) {
+                    const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
+                    const float s = __shfl_sync(0xFFFFFFFFu, wk, k);
+                    if (r >= 0 && c < H)
+                        a = fmaf(s, load_elem<F32>(static_cast<const uint8_t *>(rows) +
+                                                       r * ld_row * B, c), a);
                 }
-                *reinterpret_cast<uint4 *>(yp + (int64_t)c * B) = pack<F32>(acc);
-                continue;
+                if (c < H)
+                    store_elem<F32>(yp, c, a + (resp != nullptr ? load_elem<F32>(resp, c) : 0.f));
             }
         }
-#pragma unroll
-        for (int q = 0; q < PER; ++q)
-            if (c + q < H)
-                store_elem<F32>(yp, c + q,
-                                acc[q] + (resp != nullptr ? load_elem<F32>(resp, c + q) : 0.f));
     }
 }
 
 // ---------------------------------------------------------------- combine backward
-// One block per token; warp i takes the row's segments i, i + 8, ... of 32 vectors. Each warp
-// sums its part of the K dot products over its lanes by a butterfly, lane k keeping copy k's;
+// One block per token; warp i takes the row's segments i, i + 8, ... of 32*U pieces. The copies
+// go in rounds of equal size, at most 8: a round's rows are loaded before the first is used, and
+// each lane keeps its part of the round's dot products over all its segments. A butterfly that
+// halves the number of values at each step (9 shuffles for 8 sums, not 40) adds the lanes, and
 // the warps' parts are added in warp order. Blocks past the tokens' zero the pad rows.
-template <bool F32, bool VEC>
+template <bool F32, bool VEC, int U>
 __global__ void __launch_bounds__(TPB)
     combine_bwd_kernel(const void *__restrict__ dy, const void *__restrict__ rows,
                        const int32_t *__restrict__ map, const int32_t *__restrict__ starts,
                        const int32_t *__restrict__ kept, const float *__restrict__ w, int64_t T,
                        int K, int E, int H, int64_t ld_tok, int64_t ld_row, int64_t n_rows,
                        void *__restrict__ drows, float *__restrict__ dw, int *status) {
-    constexpr int B = Elem<F32>::BYTES, PER = VEC ? Elem<F32>::PER : 1;
+    using P = Piece<F32, VEC>;
+    constexpr int B = Elem<F32>::BYTES, PER = P::PER;
     __shared__ float part[WARPS][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool pads = starts != nullptr && drows != nullptr;
+    const int rounds = (K + 7) / 8, per_round = (K + rounds - 1) / rounds;
+    const int tail = H / PER * PER;  // the columns from here are taken one a lane, by warp 0
     const int64_t items = T + (pads ? (int64_t)E * 16 / WARPS : 0);
     for (int64_t t = blockIdx.x; t < items; t += gridDim.x) {
         if (t >= T) {
@@ -331,73 +378,110 @@ __global__ void __launch_bounds__(TPB)
             continue;
         }
         const int32_t rk = lane < K ? row_of(map, t * K + lane, n_rows, status) : -1;
-        const float wk = lane < K ? (w != nullptr ? w[t * K + lane] : 1.0f) : 0.f;
+        const float wk = rk >= 0 ? (w != nullptr ? w[t * K + lane] : 1.0f) : 0.f;
         const uint8_t *dyp = static_cast<const uint8_t *>(dy) + t * ld_tok * B;
-        float dot = 0.f;  // lane k: this warp's part of <rows[r_k], dy>
-        for (int c0 = warp * 32 * PER; c0 < H; c0 += WARPS * 32 * PER) {
-            const int c = c0 + lane * PER;
-            const bool whole = c + PER <= H;
-            float g[PER];
-            if constexpr (VEC) {
-                if (whole) {
-                    unpack<F32>(ldg_nc_v4(dyp + (int64_t)c * B), g);
-                } else {
+        for (int k0 = 0; k0 < K; k0 += per_round) {
+            const int kn = K - k0 < per_round ? K - k0 : per_round;
+            float acc[8];
 #pragma unroll
-                    for (int q = 0; q < PER; ++q) g[q] = c + q < H ? load_elem<F32>(dyp, c + q) : 0.f;
+            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+            for (int c0 = warp * 32 * PER * U; c0 < H; c0 += WARPS * 32 * PER * U) {
+                const int c = c0 + lane * PER;  // and U - 1 more pieces, 32 PER apart
+                P gp[U], b[8][U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    gp[u].load(dyp, c + u * 32 * PER, c + u * 32 * PER + PER <= H);
+                if (dw != nullptr) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (j >= kn) break;
+                        const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            b[j][u].load(static_cast<const uint8_t *>(rows) + r * ld_row * B,
+                                         c + u * 32 * PER,
+                                         r >= 0 && c + u * 32 * PER + PER <= H);
+                    }
                 }
-            } else {
-                g[0] = c < H ? load_elem<F32>(dyp, c) : 0.f;
+                float g[U][PER];
+#pragma unroll
+                for (int u = 0; u < U; ++u) gp[u].values(g[u]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j >= kn) break;
+                    if (drows != nullptr) {
+                        const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
+                        const float s = __shfl_sync(0xFFFFFFFFu, wk, k0 + j);
+                        uint8_t *o = static_cast<uint8_t *>(drows) + r * ld_row * B;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int cu = c + u * 32 * PER;
+                            if (r < 0 || cu + PER > H) continue;
+                            float d[PER];
+#pragma unroll
+                            for (int q = 0; q < PER; ++q) d[q] = s * g[u][q];
+                            if constexpr (VEC)
+                                *reinterpret_cast<uint4 *>(o + (int64_t)cu * B) = pack<F32>(d);
+                            else
+                                store_elem<F32>(o, cu, d[0]);
+                        }
+                    }
+                    if (dw != nullptr) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            float v[PER];
+                            b[j][u].values(v);
+#pragma unroll
+                            for (int q = 0; q < PER; ++q) acc[j] = fmaf(v[q], g[u][q], acc[j]);
+                        }
+                    }
+                }
             }
-            for (int k = 0; k < K; ++k) {
-                const int64_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
-                if (r < 0) continue;
-                const float s = __shfl_sync(0xFFFFFFFFu, wk, k);
-                float v[PER], d[PER];
+            if (VEC && warp == 0 && tail < H) {
+                const int c = tail + lane;
+                const float g = c < H ? load_elem<F32>(dyp, c) : 0.f;
 #pragma unroll
-                for (int q = 0; q < PER; ++q) v[q] = 0.f;
-                if (dw != nullptr) {
-                    const uint8_t *p = static_cast<const uint8_t *>(rows) + r * ld_row * B;
-                    if constexpr (VEC) {
-                        if (whole) {
-                            unpack<F32>(ldg_nc_v4(p + (int64_t)c * B), v);
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < PER; ++q)
-                                v[q] = c + q < H ? load_elem<F32>(p, c + q) : 0.f;
-                        }
-                    } else {
-                        v[0] = c < H ? load_elem<F32>(p, c) : 0.f;
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    if (j >= kn) break;
+                    const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
+                    const float s = __shfl_sync(0xFFFFFFFFu, wk, k0 + j);
+                    if (r < 0 || c >= H) continue;
+                    if (drows != nullptr)
+                        store_elem<F32>(static_cast<uint8_t *>(drows) + r * ld_row * B, c, s * g);
+                    if (dw != nullptr)
+                        acc[j] = fmaf(
+                            load_elem<F32>(static_cast<const uint8_t *>(rows) + r * ld_row * B, c),
+                            g, acc[j]);
                 }
-                if (drows != nullptr) {
-                    uint8_t *o = static_cast<uint8_t *>(drows) + r * ld_row * B;
+            }
+            if (dw != nullptr) {
+                // after the step with lane distance 16, 8, 4 a lane keeps the half of the values
+                // that its lane bit names; the last two add what is left of one value
+                float h4[4], h2[2], h1;
 #pragma unroll
-                    for (int q = 0; q < PER; ++q) d[q] = s * g[q];
-                    bool done = false;
-                    if constexpr (VEC) {
-                        if (whole) {
-                            *reinterpret_cast<uint4 *>(o + (int64_t)c * B) = pack<F32>(d);
-                            done = true;
-                        }
-                    }
-                    if (!done) {
-#pragma unroll
-                        for (int q = 0; q < PER; ++q)
-                            if (c + q < H) store_elem<F32>(o, c + q, d[q]);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const bool up = lane & 16;
+                    const float give = up ? acc[j] : acc[j + 4], keep = up ? acc[j + 4] : acc[j];
+                    h4[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 16);
                 }
-                if (dw != nullptr) {
-                    float a = 0.f;
 #pragma unroll
-                    for (int q = 0; q < PER; ++q) a = fmaf(v[q], g[q], a);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-                    if (lane == k) dot += a;
+                for (int j = 0; j < 2; ++j) {
+                    const bool up = lane & 8;
+                    const float give = up ? h4[j] : h4[j + 2], keep = up ? h4[j + 2] : h4[j];
+                    h2[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 8);
                 }
+                {
+                    const bool up = lane & 4;
+                    const float give = up ? h2[0] : h2[1], keep = up ? h2[1] : h2[0];
+                    h1 = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 4);
+                }
+                h1 += __shfl_xor_sync(0xFFFFFFFFu, h1, 2);
+                h1 += __shfl_xor_sync(0xFFFFFFFFu, h1, 1);
+                const int j = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+                if ((lane & 3) == 0 && j < kn) part[warp][k0 + j] = h1;
             }
         }
         if (dw != nullptr) {
-            part[warp][lane] = dot;
             __syncthreads();
             if (warp == 0 && lane < K) {
                 float a = 0.f;
@@ -450,7 +534,7 @@ cudaError_t launch_dispatch_rows(const mok_rows_config &c, const void *x, const 
     const int64_t items = c.T * segs + (starts != nullptr ? (int64_t)c.E * 16 : 0);
     if (items == 0) return cudaSuccess;
 #define CALL(F, V)                                                                        \
-    dispatch_kernel<F, V, U><<<grid_for(items, WARPS, 16), TPB, 0, s>>>(                  \
+    dispatch_kernel<F, V, U><<<grid_for(items, WARPS, DISPATCH_BLOCKS), TPB, 0, s>>>(                  \
         x, map, starts, kept, c.T, c.K, c.E, c.H, c.ld_tok, c.ld_row, c.n_rows, xs, status)
     MOK_ROWS_CASES(c, CALL);
 #undef CALL
@@ -462,9 +546,10 @@ cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, cons
                                 cudaStream_t s) {
     if (c.T == 0) return cudaSuccess;
     const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
-    const int64_t items = (int64_t)c.T * ((c.H + per * 32 - 1) / (per * 32));
+    constexpr int U = COMBINE_U;
+    const int64_t items = (int64_t)c.T * ((c.H + per * 32 * U - 1) / (per * 32 * U));
 #define CALL(F, V)                                                                       \
-    combine_rows_kernel<F, V><<<grid_for(items, WARPS, 16), TPB, 0, s>>>(                \
+    combine_rows_kernel<F, V, U><<<grid_for(items, WARPS, COMBINE_BLOCKS), TPB, 0, s>>>(             \
         rows, map, w, res, c.T, c.K, c.H, c.ld_tok, c.ld_row, c.n_rows, y, status)
     MOK_ROWS_CASES(c, CALL);
 #undef CALL
@@ -478,7 +563,7 @@ cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const v
     const int64_t items = c.T + (starts != nullptr && drows != nullptr ? (int64_t)c.E * 2 : 0);
     if (items == 0) return cudaSuccess;
 #define CALL(F, V)                                                                         \
-    combine_bwd_kernel<F, V><<<grid_for(items, 1, 16), TPB, 0, s>>>(                       \
+    combine_bwd_kernel<F, V, COMBINE_BWD_U><<<grid_for(items, 1, COMBINE_BLOCKS), TPB, 0, s>>>( \
         dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, c.ld_tok, c.ld_row, c.n_rows,  \
         drows, dw, status)
     MOK_ROWS_CASES(c, CALL);
