@@ -243,10 +243,26 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None  # handle of the current stream, without building a Stream object (3 us a call)
+
+
+def _current_stream():
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            torch.cuda.current_stream()  # CUDA is initialised before the handle is asked for
+            device = torch.cuda.current_device
+            _raw_stream = lambda: raw(device())  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

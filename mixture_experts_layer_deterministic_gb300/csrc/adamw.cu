@@ -54,7 +54,8 @@ struct Params {
     Scalars s;
     TensorDesc t[NT];
 };
-constexpr int NT_SMALL = 16, NT_LARGE = 400;
+// tensors of one launch: the parameters are copied at each launch, so short lists take less
+constexpr int NT_SMALL = 8, NT_MID = 64, NT_LARGE = 400;
 static_assert(sizeof(Params<NT_LARGE>) <= 32764, "kernel parameters");
 
 // the MurmurHash3 finaliser
@@ -458,6 +459,8 @@ mok_status mok_adamw_step(const mok_adamw_config *c, const mok_adamw_tensor *ten
         MOK_OP_LAUNCH(OP_ADAMW, 1,
                    t1 - t0 <= NT_SMALL
                        ? step_group<NT_SMALL>(*c, tensors, t0, t1, grad_scale, &base, stream)
+                   : t1 - t0 <= NT_MID
+                       ? step_group<NT_MID>(*c, tensors, t0, t1, grad_scale, &base, stream)
                        : step_group<NT_LARGE>(*c, tensors, t0, t1, grad_scale, &base, stream));
     }
     return MOK_OK;

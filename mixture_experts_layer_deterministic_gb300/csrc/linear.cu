@@ -40,8 +40,22 @@ constexpr uint32_t SET_COLS = 256; // TMEM columns of one accumulator set
 constexpr int LTILE = 256;         // most rows of a tile
 constexpr int SEG_K = 1024;        // fp32 outputs: K elements per accumulation segment
 constexpr int MAX_G = 1024;
-constexpr int EPI = 8;             // epilogue warps: two per TMEM lane quadrant
-constexpr int LTHREADS = 64 + 32 * EPI;
+
+// Epilogue warps: two per TMEM lane quadrant, or four where the warps keep a unit's sums in
+// registers between its segments (SUMS: 64 a thread, where two would need 128).
+template <bool SUMS>
+struct Epi {
+    static constexpr int WARPS = SUMS ? 16 : 8;
+    static constexpr int THREADS = 64 + 32 * WARPS;
+    static constexpr int STEP = 32 * (WARPS / 4);   // columns between a warp's chunks of 32
+    static constexpr int CHUNKS = LTILE / STEP;     // its chunks of a full tile
+};
+template <bool SUMS>
+struct Carry {};  // what a warp keeps between the segments of a unit
+template <>
+struct Carry<true> {
+    float v[2 * Epi<true>::CHUNKS][16];  // by 16 columns
+};
 
 // ---------------------------------------------------------------- row tiles
 // A tile is up to `height` consecutive rows of one group. Dense: tile t covers rows
@@ -181,7 +195,7 @@ struct LinSmem {
     uint32_t tmem_base;
     int abort;
 };
-constexpr int LIN_PATCHES = EPI / 2 * PATCHES * PATCH_BYTES;
+constexpr int LIN_PATCHES = Epi<false>::WARPS / 2 * PATCHES * PATCH_BYTES;
 constexpr int LIN_SMEM =
     LSTAGES * LSTAGE_BYTES + LIN_PATCHES + 1024 + (int)sizeof(LinSmem);
 static_assert(LIN_SMEM <= 232448, "shared memory of a CTA");
@@ -201,6 +215,14 @@ struct LinGeom {
     int k_steps;         // 16-element K steps
 };
 
+// values of tcgen05.ld instructions that a tmem_ld_wait before this covers: keeps their uses
+// behind the wait
+template <int N>
+MOK_DEV void loaded(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
 MOK_DEV void tma_load_3d_pair(void *smem_dst, const CUtensorMap *m, uint32_t bar_cluster,
                               int32_t x, int32_t y, int32_t z) {
     asm volatile(
@@ -213,24 +235,21 @@ MOK_DEV void tma_load_3d_pair(void *smem_dst, const CUtensorMap *m, uint32_t bar
 // 32 columns of this warp's 32 lanes as pairs: v[h][b][..] are lane 16 h + t / 4 (first two)
 // and 8 lanes on (last two), columns 8 b + 2 (t % 4) and the next, t the thread
 MOK_DEV void ld_pairs(uint32_t c, float (&v)[2][4][4]) {
-    uint32_t r[2][16];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
         asm volatile(
             "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
             "%13,%14,%15}, [%16];"
-            : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]),
-              "=r"(r[h][5]), "=r"(r[h][6]), "=r"(r[h][7]), "=r"(r[h][8]), "=r"(r[h][9]),
-              "=r"(r[h][10]), "=r"(r[h][11]), "=r"(r[h][12]), "=r"(r[h][13]), "=r"(r[h][14]),
-              "=r"(r[h][15])
+            : "=f"(v[h][0][0]), "=f"(v[h][0][1]), "=f"(v[h][0][2]), "=f"(v[h][0][3]),
+              "=f"(v[h][1][0]), "=f"(v[h][1][1]), "=f"(v[h][1][2]), "=f"(v[h][1][3]),
+              "=f"(v[h][2][0]), "=f"(v[h][2][1]), "=f"(v[h][2][2]), "=f"(v[h][2][3]),
+              "=f"(v[h][3][0]), "=f"(v[h][3][1]), "=f"(v[h][3][2]), "=f"(v[h][3][3])
             : "r"(c + ((uint32_t)(16 * h) << 16)));
     tc::tmem_ld_wait();
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[h][b][i] = __uint_as_float(r[h][4 * b + i]);
+        for (int b = 0; b < 4; ++b) loaded(v[h][b]);
 }
 
 // 32 columns, one lane per thread
@@ -239,6 +258,8 @@ MOK_DEV void ld32(uint32_t c, float (&v)[32]) {
     tc::tmem_ld16(c, a);
     tc::tmem_ld16(c + 16, b);
     tc::tmem_ld_wait();
+    loaded(a);
+    loaded(b);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         v[j] = a[j];
@@ -248,17 +269,14 @@ MOK_DEV void ld32(uint32_t c, float (&v)[32]) {
 
 // 8 columns of this warp's 32 lanes: v[h][..] as v[h][b][..] of ld_pairs
 MOK_DEV void ld_pairs8(uint32_t c, float (&v)[2][4]) {
-    uint32_t r[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3])
+                     : "=f"(v[h][0]), "=f"(v[h][1]), "=f"(v[h][2]), "=f"(v[h][3])
                      : "r"(c + ((uint32_t)(16 * h) << 16)));
     tc::tmem_ld_wait();
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[h][i] = __uint_as_float(r[h][i]);
+    loaded(v[0]);
+    loaded(v[1]);
 }
 
 // byte of row n (a column of the accumulator), 16-byte piece i of a patch: pieces are exchanged
@@ -376,8 +394,11 @@ MOK_DEV void emit_plain(Patches &pt, uint32_t c, int nr, const OutRef &o, int x,
     pt.store(o, x, y0, end, g);
 }
 
-template <bool F32>
+// PLAIN: only a bias after the product (no activation, residual or z)
+template <bool F32, bool PLAIN>
 struct Fwd {
+    using E = Epi<F32 && PLAIN>;
+    static constexpr bool F32_OUT = F32, SUMS = F32 && PLAIN;
     static constexpr bool A_MN = false, B_MN = false;
     Tiles tiles;
     int n_mb;      // ceil(N / 256)
@@ -417,15 +438,18 @@ struct Fwd {
         tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, q.b0 + k0, q.b1);
     }
     MOK_DEV void epilogue(const Unit &u, int seg, uint32_t rank, uint32_t c, int q, int hw, int lane,
-                          Patches &pt) const {
+                          Patches &pt, Carry<SUMS> &carry) const {
         const int nr = u.nr, pad = u.pad;
         const int64_t r0 = u.r0;
         const int n_mma = (nr + 15) & ~15;
         const int f0 = u.mb * 256 + (int)rank * 128 + q * 32;  // the warp's features
-        if constexpr (F32)
-            direct(seg, c, hw, f0 + lane, u.g, r0, nr, pad ? n_mma : nr);
+        const int n_out = pad ? n_mma : nr;
+        if constexpr (SUMS)
+            direct_sums(seg, c, hw, f0 + lane, u.g, r0, nr, n_out, carry.v);
+        else if constexpr (F32)
+            direct(seg, c, hw, f0 + lane, u.g, r0, nr, n_out);
         else
-            staged(c, hw, f0, u.g, r0, nr, pad ? n_mma : nr, pt);
+            staged(c, hw, f0, u.g, r0, nr, n_out, pt);
     }
     // bf16: 32 rows at a time through patches, 8 rows in registers at once
     MOK_DEV void staged(uint32_t c, int hw, int f0, int g, int64_t r0, int nr, int n_out,
@@ -446,7 +470,7 @@ struct Fwd {
                 for (int i = 0; i < 4; ++i)
                     v[h][i] = n + 2 * (lane & 3) + (i & 1) < nr ? v[h][i] + bs[h][i >> 1] : 0.f;
         };
-        for (int n0 = 32 * hw; n0 < n_out; n0 += 32 * (EPI / 4)) {
+        for (int n0 = 32 * hw; n0 < n_out; n0 += E::STEP) {
             uint4 t[4];
             if (res != nullptr) {  // rows of 64 bytes, four lanes each
 #pragma unroll
@@ -507,57 +531,84 @@ struct Fwd {
                      0);
         }
     }
-    // fp32: from the lanes, 128 bytes a warp and row
+    // fp32: from the lanes, 128 bytes a warp and row. The tensor cores' accumulation error grows
+    // with its length (router logits over 4096 inputs 3.9e-6 of their norm in one run, 8.9e-7 in
+    // runs of 1024), so a long K is cut into segments that are added in fp32 here: in registers,
+    // kept between the calls of a unit, where nothing but a bias follows ...
+    MOK_DEV void direct_sums(int seg, uint32_t c, int hw, int f, int g, int64_t r0, int nr,
+                             int n_out, float (&acc)[2 * E::CHUNKS][16]) const {
+        const bool last = seg == segs - 1;
+        const float b = last && bias != nullptr && f < N ? bias[(int64_t)g * N + f] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 2 * E::CHUNKS; ++k) {
+            const int n0 = 32 * hw + E::STEP * (k >> 1) + 16 * (k & 1);
+            if (n0 >= n_out) continue;
+            float v[16];
+            tc::tmem_ld16(c + n0, v);
+            tc::tmem_ld_wait();
+            loaded(v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[k][j] = (seg > 0 ? acc[k][j] : b) + v[j];
+            if (!last || f >= N) continue;
+            float *yp = static_cast<float *>(y) + (r0 + n0) * ld + f;
+            const float b1 = segs > 1 ? b : 0.f;  // a single segment began with it
+#pragma unroll
+            for (int j = 0; j < 16; ++j, yp += ld)
+                if (n0 + j < n_out) *yp = n0 + j < nr ? acc[k][j] + b1 : 0.f;
+        }
+    }
+    // ... or in y, each element by the thread that will finish it
     MOK_DEV void direct(int seg, uint32_t c, int hw, int f, int g, int64_t r0, int nr,
                         int n_out) const {
-        const bool ok = f < N;
-        const bool last = seg == segs - 1;
-        const float b = bias != nullptr && ok ? bias[(int64_t)g * N + f] : 0.f;
-        for (int n0 = 32 * hw; n0 < ((nr + 15) & ~15); n0 += 32 * (EPI / 4)) {
-            float v[32];
-            ld32(c + n0, v);
+        const bool ok = f < N, last = seg == segs - 1;
+        const float b = last && bias != nullptr && ok ? bias[(int64_t)g * N + f] : 0.f;
+        for (int n0 = 16 * hw; n0 < n_out; n0 += E::STEP / 2) {
+            float v[16];
+            tc::tmem_ld16(c + n0, v);
+            tc::tmem_ld_wait();
+            loaded(v);
             if (!ok) continue;
             const int64_t o = (r0 + n0) * ld + f;
+            const int left = nr - n0, out = n_out - n0;  // real rows, rows to write
             float *yp = static_cast<float *>(y) + o;
-            if (seg > 0) {  // the sum of the earlier segments, left in y by this thread
-                float a[32];
+            if (seg > 0) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) a[j] = n0 + j < nr ? yp[(int64_t)j * ld] : 0.f;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += a[j];
+                for (int j = 0; j < 16; ++j)
+                    if (j < left) v[j] += yp[(int64_t)j * ld];
             }
             if (!last) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (n0 + j < nr) yp[(int64_t)j * ld] = v[j];
+                for (int j = 0; j < 16; ++j)
+                    if (j < left) yp[(int64_t)j * ld] = v[j];
                 continue;
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = n0 + j < nr ? v[j] + b : 0.f;
+            for (int j = 0; j < 16; ++j) v[j] = j < left ? v[j] + b : 0.f;
             if (z != nullptr) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (n0 + j < n_out) z[o + (int64_t)j * ld] = f32_to_bf16(v[j]);
+                for (int j = 0; j < 16; ++j)
+                    if (j < out) z[o + (int64_t)j * ld] = (uint16_t)pack2(v[j], 0.f);
             }
-            if (act != MOK_ACT_NONE)
-                with_act(act, [&](auto a) {
+            with_act(act, [&](auto a) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = act_f<a.value>(v[j]);
-                });
+                for (int j = 0; j < 16; ++j) v[j] = act_f<a.value>(v[j]);
+            });
             if (res != nullptr) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (n0 + j < nr) v[j] += bf16_to_f32(res[o + (int64_t)j * ld]);
+                for (int j = 0; j < 16; ++j)
+                    if (j < left) v[j] += bf16_to_f32(res[o + (int64_t)j * ld]);
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (n0 + j < n_out) yp[(int64_t)j * ld] = v[j];
+            for (int j = 0; j < 16; ++j)
+                if (j < out) yp[(int64_t)j * ld] = v[j];
         }
     }
 };
 
 template <bool F32>
 struct Dx {
+    using E = Epi<false>;
+    static constexpr bool F32_OUT = F32, SUMS = false;
     static constexpr bool A_MN = true, B_MN = false;
     Tiles tiles;
     int n_mb;     // ceil(Kin / 256)
@@ -593,12 +644,12 @@ struct Dx {
         tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, k0, q.b1);
     }
     MOK_DEV void epilogue(const Unit &u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
-                          Patches &pt) const {
+                          Patches &pt, Carry<SUMS> &carry) const {
         const int nr = u.nr, pad = u.pad;
         const int64_t r0 = u.r0;
         const int n_mma = (nr + 15) & ~15;
         const int i0 = u.mb * 256 + (int)rank * 128 + q * 32;
-        for (int n0 = 32 * hw; n0 < n_mma; n0 += 32 * (EPI / 4)) {
+        for (int n0 = 32 * hw; n0 < n_mma; n0 += E::STEP) {
             if constexpr (F32) {
                 float v[32];
                 ld32(c + n0, v);
@@ -618,6 +669,8 @@ struct Dx {
 
 template <bool F32>
 struct Dw {
+    using E = Epi<false>;
+    static constexpr bool F32_OUT = F32, SUMS = false;
     static constexpr bool A_MN = true, B_MN = true;
     const int32_t *starts, *valid;  // grouped: first row and row count of each group
     int64_t rows;                   // dense
@@ -660,12 +713,12 @@ struct Dw {
             tc::tma_load_2d_pair(st + (2 + j) * BOX, tmB, fb, q.b0 + 64 * j, q.b1 + k0);
     }
     MOK_DEV void epilogue(const Unit &u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
-                          Patches &pt) const {
+                          Patches &pt, Carry<SUMS> &carry) const {
         const int g = u.g, mb = u.mb, nb = u.nb;
         const int nn = N - nb * 256 < 256 ? N - nb * 256 : 256;
         const bool any = u.nr > 0;
         const int i0 = mb * 256 + (int)rank * 128 + q * 32;
-        for (int n0 = 32 * hw; n0 < nn; n0 += 32 * (EPI / 4)) {
+        for (int n0 = 32 * hw; n0 < nn; n0 += E::STEP) {
             if constexpr (F32) {
                 float v[32];
                 ld32(c + n0, v);
@@ -716,7 +769,7 @@ MOK_DEV void lin_drain(uint64_t *bar, uint32_t parity) {
 }
 
 template <class P>
-__global__ void __launch_bounds__(LTHREADS, 1)
+__global__ void __launch_bounds__(P::E::THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA,
                   const __grid_constant__ CUtensorMap tmB, const P p) {
     constexpr int NS = LSTAGES, SB = LSTAGE_BYTES;
@@ -736,7 +789,7 @@ __global__ void __launch_bounds__(LTHREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&sm->tmem_full[b], 1);
-            tc::mbar_init(&sm->tmem_empty[b], 2 * EPI);
+            tc::mbar_init(&sm->tmem_empty[b], 2 * P::E::WARPS);
         }
         sm->abort = 0;
         tc::fence_mbar_init();
@@ -863,24 +916,25 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;          // TMEM lane quadrant this warp may access
-        const int hw = (warp - 2) >> 2;  // it takes every second chunk of 32 columns from this
+        const int hw = (warp - 2) >> 2;  // which of the quadrant's warps: it takes every so-manyth chunk
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
         const uint32_t empty0 = tc::cluster_addr(&sm->tmem_empty[0], 0);
         const int pair = 2 * hw + (q >> 1);
         Patches pt{tc::smem_u32(base + NS * SB) + (uint32_t)(pair * PATCHES * PATCH_BYTES),
                    1 + pair, q & 1, lane, 0};
+        Carry<P::SUMS> carry;
         int64_t a = 0;
         bool ok = true;
         for (uint32_t u = cid; u < n_units && ok; u += ncl) {
             const Unit cur = p.unit(u);
             for (int seg = 0; seg < segs; ++seg, ++a) {
                 const int ab = (int)(a & 1);
-                ok = pt.agree(
-                    lin_wait(&sm->tmem_full[ab], (uint32_t)((a >> 1) & 1), p.status, abort));
+                ok = lin_wait(&sm->tmem_full[ab], (uint32_t)((a >> 1) & 1), p.status, abort);
+                if constexpr (!P::F32_OUT) ok = pt.agree(ok);
                 if (!ok) break;
                 tc::tc_fence_after();
                 p.epilogue(cur, seg, rank, tmem + lane_base + (uint32_t)ab * SET_COLS, q, hw, lane,
-                           pt);
+                           pt, carry);
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) lin_arrive(empty0 + (uint32_t)ab * 8u);
@@ -897,83 +951,196 @@ __global__ void __launch_bounds__(LTHREADS, 1)
     }
 }
 
+// ---------------------------------------------------------------- few rows
+// Up to 8 dense rows (a decoded token, a small batch): the weights' bytes are all the work, and
+// the tensor-core kernel's 256-row tiles put them on too few SMs (16 of 76 pairs for 4096
+// features). Here a warp takes 4 features and one of KS parts of the inputs, lanes side by
+// side on 16-byte pieces; fp32 products and sums, lanes added by a butterfly, parts in order.
+constexpr int SMALL_ROWS = 8;
+constexpr int SMALL_F = 2;  // features per warp
+
+struct SmallArgs {
+    const uint16_t *x, *w, *res;
+    const float *bias;
+    void *y;
+    uint16_t *z;
+    int Kin, N, rows, act, parts;
+    int64_t ld_in, ld_w, ld_out;
+};
+
+// R rows (rows past a.rows repeat the last and are not stored), UN pieces a lane in flight
+template <int R, int UN, bool F32>
+__global__ void __launch_bounds__(256)
+    linear_small_kernel(const SmallArgs a) {
+    __shared__ float sh[8][SMALL_F * R];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = warp % a.parts, slot = warp / a.parts;
+    const int per_block = 8 / a.parts * SMALL_F;
+    const int f0 = blockIdx.x * per_block + slot * SMALL_F;
+    const int nv = a.Kin / 8;
+    const uint16_t *wp[SMALL_F], *xp[R];
+#pragma unroll
+    for (int f = 0; f < SMALL_F; ++f)
+        wp[f] = a.w + (int64_t)(f0 + f < a.N ? f0 + f : a.N - 1) * a.ld_w;
+#pragma unroll
+    for (int r = 0; r < R; ++r) xp[r] = a.x + (int64_t)(r < a.rows ? r : a.rows - 1) * a.ld_in;
+    float acc[SMALL_F][R];
+#pragma unroll
+    for (int f = 0; f < SMALL_F; ++f)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[f][r] = 0.f;
+    for (int v0 = part * 32 + lane; v0 < nv; v0 += a.parts * 32 * UN) {
+        uint4 wv[UN][SMALL_F];
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int f = 0; f < SMALL_F; ++f) {
+                const int v = v0 + u * a.parts * 32;
+                wv[u][f] = make_uint4(0, 0, 0, 0);
+                if (v < nv) wv[u][f] = ldg_nc_v4(wp[f] + (int64_t)v * 8);
+            }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int v = v0 + u * a.parts * 32;
+            if (v >= nv) break;
+            float xf[R][8];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint4 q = ldg_nc_v4(xp[r] + (int64_t)v * 8);
+                const uint32_t e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    xf[r][2 * j] = bf16_lo(e[j]);
+                    xf[r][2 * j + 1] = bf16_hi(e[j]);
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < SMALL_F; ++f) {
+                const uint32_t e[4] = {wv[u][f].x, wv[u][f].y, wv[u][f].z, wv[u][f].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float lo = bf16_lo(e[j]), hi = bf16_hi(e[j]);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        acc[f][r] = fmaf(hi, xf[r][2 * j + 1], fmaf(lo, xf[r][2 * j], acc[f][r]));
+                }
+            }
+        }
+    }
+    if (part == 0) {  // the inputs past the last whole piece
+        const int c = nv * 8 + lane;
+        if (c < a.Kin) {
+#pragma unroll
+            for (int f = 0; f < SMALL_F; ++f)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    acc[f][r] = fmaf(bf16_to_f32(wp[f][c]), bf16_to_f32(xp[r][c]), acc[f][r]);
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < SMALL_F; ++f)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float v = acc[f][r];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            if (lane == 0) sh[warp][f * R + r] = v;
+        }
+    __syncthreads();
+    // one thread per output of the block; features side by side
+    const int n = per_block * R;
+    if (threadIdx.x >= n) return;
+    const int r = threadIdx.x / per_block, fb = threadIdx.x % per_block;
+    const int f = blockIdx.x * per_block + fb;
+    if (f >= a.N || r >= a.rows) return;
+    float v = 0.f;
+    for (int k = 0; k < a.parts; ++k)
+        v += sh[fb / SMALL_F * a.parts + k][fb % SMALL_F * R + r];
+    if (a.bias != nullptr) v += a.bias[f];
+    const int64_t o = r * a.ld_out + f;
+    if (a.z != nullptr) a.z[o] = f32_to_bf16(v);
+    with_act(a.act, [&](auto act) { v = act_f<act.value>(v); });
+    if (a.res != nullptr) v += bf16_to_f32(a.res[o]);
+    st_val(a.y, o, v, F32);
+}
+
 // ---------------------------------------------------------------- dz and the bias gradient
-// dz = dy act'(z) in bf16 (the products' operand), and per tile the column sums of the unrounded
-// dz. One block per (tile, 64 columns): 8 threads side by side on 8 columns each, 32 row
-// lanes; the sums of a column's 32 row lanes are added in lane order.
+// dz = dy act'(z) in bf16 (the products' operand), and the column sums of the unrounded dz. One
+// block per 128 rows of a tile and 64 columns: 8 threads side by side on 8 columns each, 32
+// row lanes of 4 rows each, whose loads are all issued before the first is used (one row at a
+// time, 20480 x 1024 took 47 us); the sums of a column's 32 row lanes are added in lane order.
+constexpr int DZ_ROWS = 128;
+constexpr int DZ_PARTS = LTILE / DZ_ROWS;  // parts of a tile
+
 template <bool DY32, int ACT>
 __global__ void __launch_bounds__(256)
     linear_dz_kernel(const void *__restrict__ dy, const uint16_t *__restrict__ z, Tiles tiles,
                      int N, int64_t ld, uint16_t *__restrict__ dz, int64_t ld_dz,
                      float *__restrict__ part) {
     __shared__ float red[32][65];
-    const int64_t t = blockIdx.x;
+    const int64_t t = blockIdx.x / DZ_PARTS;
     if (t >= tiles.count()) return;
     const int4 tile = tiles.get(t);
-    const int64_t r0 = tile.y, r1 = tile.z;
-    const bool pad = tile.w != 0;
-    const int64_t rend = pad ? (r1 + 15) & ~(int64_t)15 : r1;
+    const int64_t r0 = tile.y + (int64_t)(blockIdx.x % DZ_PARTS) * DZ_ROWS;
+    const int64_t r1 = tile.z, rend = tile.w != 0 ? (r1 + 15) & ~(int64_t)15 : r1;
     const int cv = threadIdx.x & 7, rl = threadIdx.x >> 3;
     const int c = blockIdx.y * 64 + cv * 8;
+    constexpr int NR = DZ_ROWS / 32;
+    const bool whole = c + 8 <= N;
+    uint4 a[NR], a2[NR], q[NR];  // dy (fp32: two vectors), z
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int64_t r = r0 + rl + 32 * i, o = r * ld + c;
+            a[i] = a2[i] = q[i] = make_uint4(0, 0, 0, 0);
+            if (r < r1) {
+                if (DY32) {
+                    a[i] = ldg_nc_v4(static_cast<const float *>(dy) + o);
+                    a2[i] = ldg_nc_v4(static_cast<const float *>(dy) + o + 4);
+                } else {
+                    a[i] = ldg_nc_v4(static_cast<const uint16_t *>(dy) + o);
+                }
+                if (ACT != MOK_ACT_NONE) q[i] = ldg_nc_v4(z + o);
+            }
+        }
+    }
     float sum[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
-    for (int64_t r = r0 + rl; r < rend; r += 32) {
-        float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-        const bool whole = c + 8 <= N;
-        if (r < r1 && c < N) {
-            const int64_t o = r * ld + c;
-            float zz[8];
-            if (whole) {
-                if (DY32) {
-                    const float4 *s = reinterpret_cast<const float4 *>(
-                        static_cast<const float *>(dy) + o);
-                    const float4 a = s[0], b = s[1];
-                    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-                    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-                } else {
-                    const uint4 a = ldg_nc_v4(static_cast<const uint16_t *>(dy) + o);
-                    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    for (int i = 0; i < NR; ++i) {
+        const int64_t r = r0 + rl + 32 * i, o = r * ld + c;
+        if (r >= rend || c >= N) continue;
+        float v[8], zz[8];
+        if (whole) {
+            const uint32_t w[8] = {a[i].x, a[i].y, a[i].z, a[i].w,
+                                   a2[i].x, a2[i].y, a2[i].z, a2[i].w};
+            const uint32_t y[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        v[2 * j] = bf16_lo(w[j]);
-                        v[2 * j + 1] = bf16_hi(w[j]);
-                    }
-                }
-                if (ACT != MOK_ACT_NONE) {
-                    const uint4 a = ldg_nc_v4(z + o);
-                    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        zz[2 * j] = bf16_lo(w[j]);
-                        zz[2 * j + 1] = bf16_hi(w[j]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool in = c + j < N;
-                    v[j] = !in ? 0.f
-                           : DY32 ? static_cast<const float *>(dy)[o + j]
-                                  : bf16_to_f32(static_cast<const uint16_t *>(dy)[o + j]);
-                    zz[j] = in && ACT != MOK_ACT_NONE ? bf16_to_f32(z[o + j]) : 0.f;
-                }
+            for (int j = 0; j < 8; ++j) {
+                v[j] = DY32 ? __uint_as_float(w[j])
+                            : (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+                zz[j] = (j & 1) ? bf16_hi(y[j >> 1]) : bf16_lo(y[j >> 1]);
             }
-            if (ACT != MOK_ACT_NONE) {
+        } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] *= act_grad_f<ACT>(zz[j]);
+            for (int j = 0; j < 8; ++j) {
+                const bool in = c + j < N && r < r1;
+                v[j] = !in ? 0.f
+                       : DY32 ? static_cast<const float *>(dy)[o + j]
+                              : bf16_to_f32(static_cast<const uint16_t *>(dy)[o + j]);
+                zz[j] = in && ACT != MOK_ACT_NONE ? bf16_to_f32(z[o + j]) : 0.f;
             }
+        }
+        if (ACT != MOK_ACT_NONE) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += c + j < N ? v[j] : 0.f;
+            for (int j = 0; j < 8; ++j) v[j] *= act_grad_f<ACT>(zz[j]);
         }
-        if (dz != nullptr && c < N) {
-            uint16_t *o = dz + r * ld_dz + c;  // ld_dz is a multiple of 8: whole vectors
-            *reinterpret_cast<uint4 *>(o) =
-                make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]),
-                           pack2(v[4], v[5]), pack2(v[6], v[7]));
-        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];  // absent rows and columns are zero
+        if (dz != nullptr)  // ld_dz is a multiple of 8: whole vectors
+            *reinterpret_cast<uint4 *>(dz + r * ld_dz + c) = make_uint4(
+                pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
     }
     if (part == nullptr) return;
 #pragma unroll
@@ -981,9 +1148,10 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     if (threadIdx.x < 64) {
         const int col = blockIdx.y * 64 + threadIdx.x;
-        float a = 0.f;
-        for (int i = 0; i < 32; ++i) a += red[i][threadIdx.x];
-        if (col < N) part[t * N + col] = a;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
+        if (col < N) part[(int64_t)blockIdx.x * N + col] = s;
     }
 }
 
@@ -1004,8 +1172,19 @@ __global__ void __launch_bounds__(256)
         }
         t = lo;
     }
+    int64_t e = nt;  // one past the group's last tile
+    if (tiles.list != nullptr) {
+        int64_t lo = t, hi = nt;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (tiles.list[4 * mid] <= g) lo = mid + 1; else hi = mid;
+        }
+        e = lo;
+    }
     float a = 0.f;
-    for (; t < nt && (tiles.list == nullptr || tiles.list[4 * t] == g); ++t) a += part[t * N + n];
+    const float *p = part + t * DZ_PARTS * N + n;
+#pragma unroll 8
+    for (int64_t k = 0; k < (e - t) * DZ_PARTS; ++k) a += p[k * N];
     db[i] = a;
 }
 
@@ -1061,7 +1240,7 @@ cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const P 
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(2 * (units_cap < pairs ? units_cap : pairs)), 1, 1);
-    cfg.blockDim = dim3(LTHREADS, 1, 1);
+    cfg.blockDim = dim3(P::E::THREADS, 1, 1);
     cfg.dynamicSmemBytes = LIN_SMEM;
     cfg.stream = s;
     cfg.attrs = at;
@@ -1094,6 +1273,22 @@ void launch_dz(int act, bool dy32, dim3 grid, const void *dy, const uint16_t *z,
         launch_dz_act<false>(act, grid, dy, z, t, N, ld, dz, ld_dz, part, s);
 }
 
+template <bool F32>
+cudaError_t launch_small(SmallArgs a, cudaStream_t s) {
+    // as few parts as give two blocks an SM: a part fewer is a block of more features, which
+    // reads x less often
+    a.parts = 1;
+    while (a.parts < 8 && (int64_t)a.N * a.parts < (int64_t)2 * device_sm_count() * 8 * SMALL_F)
+        a.parts *= 2;
+    const int per_block = 8 / a.parts * SMALL_F;
+    const unsigned grid = (unsigned)((a.N + per_block - 1) / per_block);
+    if (a.rows == 1) linear_small_kernel<1, 4, F32><<<grid, 256, 0, s>>>(a);
+    else if (a.rows == 2) linear_small_kernel<2, 4, F32><<<grid, 256, 0, s>>>(a);
+    else if (a.rows <= 4) linear_small_kernel<4, 2, F32><<<grid, 256, 0, s>>>(a);
+    else linear_small_kernel<8, 2, F32><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
 bool grouped(const int32_t *starts) { return starts != nullptr; }
 
 // dense tiles of equal height
@@ -1109,7 +1304,7 @@ struct LinWs {
     int32_t *valid;   // [G]
     uint16_t *dz;     // [rows][ld_dz]
     int64_t ld_dz;
-    float *part;      // [tiles][N]
+    float *part;      // [tiles][DZ_PARTS][N]
 };
 
 size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
@@ -1128,7 +1323,7 @@ size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
     if (pass == MOK_LINEAR_BACKWARD) {
         w.ld_dz = round_up(c.out_features, 8);
         w.dz = (uint16_t *)take((size_t)c.rows * w.ld_dz * 2);
-        w.part = (float *)take((size_t)w.cap * c.out_features * 4);
+        w.part = (float *)take((size_t)w.cap * DZ_PARTS * c.out_features * 4);
     }
     if (o != nullptr) *o = w;
     return off;
@@ -1194,6 +1389,15 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
     const void *ps[] = {x, w, bias, residual, starts, counts, y, z};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    if (!grouped(starts) && c->rows <= SMALL_ROWS) {
+        const SmallArgs a{(const uint16_t *)x, (const uint16_t *)w, (const uint16_t *)residual, bias,
+                          y, (uint16_t *)z, c->in_features, c->out_features, (int)c->rows, c->act,
+                          1, c->ld_in, c->ld_w, c->ld_out};
+        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1,
+                      c->out_dtype == MOK_DTYPE_F32 ? launch_small<true>(a, stream)
+                                                    : launch_small<false>(a, stream));
+        return MOK_OK;
+    }
     LinWs wk;
     carve_linear(*c, MOK_LINEAR_FORWARD, ws, &wk);
     if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
@@ -1214,15 +1418,17 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
     const int segs = f32 ? (c->in_features + SEG_K - 1) / SEG_K : 1;
     const int n_mb = (c->out_features + 255) / 256;
     const int64_t units = tiles.cap * n_mb;
-    if (f32) {
-        const Fwd<true> p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias,
-                          (const uint16_t *)residual, y, (uint16_t *)z, c->act, status};
-        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, p, units, stream));
-    } else {
-        const Fwd<false> p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias,
-                           (const uint16_t *)residual, y, (uint16_t *)z, c->act, status};
-        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, p, units, stream));
-    }
+    const bool plain = c->act == MOK_ACT_NONE && !residual && !z;
+#define MOK_FWD(F, PL)                                                                          \
+    do {                                                                                        \
+        const Fwd<F, PL> p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias, \
+                           (const uint16_t *)residual, y, (uint16_t *)z, c->act, status};       \
+        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, p, units, stream));               \
+    } while (0)
+    if (!f32) MOK_FWD(false, false);
+    else if (plain) MOK_FWD(true, true);
+    else MOK_FWD(true, false);
+#undef MOK_FWD
     return MOK_OK;
 }
 
@@ -1270,7 +1476,7 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     if (db || (!direct && (dx || dw))) {
         uint16_t *dzo = direct || (!dx && !dw) ? nullptr : wk.dz;
         float *part = db ? wk.part : nullptr;
-        const dim3 grid((unsigned)tiles.cap, (unsigned)((N + 63) / 64));
+        const dim3 grid((unsigned)(tiles.cap * DZ_PARTS), (unsigned)((N + 63) / 64));
         prof_begin(OP_LINEAR_DZ, stream);
         launch_dz(c->act, dy32, grid, dy, (const uint16_t *)z, tiles, N, c->ld_out, dzo, ld_dz,
                   part, stream);
