@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(MAX_G)
     }
 }
 
-int64_t tiles_cap(int64_t rows, int G) { return G + rows / 16 / (LTILE / 16) + 1; }
+int64_t tiles_cap(int64_t rows, int G) { return G + rows / LTILE + 1; }
 
 // ---------------------------------------------------------------- activations
 // exp and the quotient to within 2^-20 of their values: far inside the bf16 rounding of y
@@ -210,7 +210,7 @@ struct Unit {
 struct LinGeom {
     int32_t a0, a1, a2;  // A coordinates (per policy)
     int32_t b0, b1;      // B coordinates
-    int nbox;            // MN-major B: 64-column boxes per CTA
+    int nbox;            // boxes of B per CTA: 64 columns (MN-major), 32 rows (K-major)
     int n_mma;           // N of each MMA
     int k_steps;         // 16-element K steps
 };
@@ -425,17 +425,18 @@ struct Fwd {
         q.a2 = u.g;
         q.b0 = q.a0;
         q.b1 = u.r0 + (int)rank * (q.n_mma / 2);
-        q.nbox = 1;
+        q.nbox = (q.n_mma / 2 + 31) / 32;
         const int k = segs > 1 && Kin - q.a0 > SEG_K ? SEG_K : Kin - q.a0;
         q.k_steps = (k + 15) / 16;
         return q;
     }
-    MOK_DEV uint32_t tx(const LinGeom &) const { return 4 * BOX; }
-    // A: 128 features x 64 inputs; B: 128 rows x 64 inputs, of which n_mma / 2 rows are used
+    MOK_DEV uint32_t tx(const LinGeom &q) const { return 2 * BOX + q.nbox * (BOX / 2); }
+    // A: 128 features x 64 inputs; B: the rows' 64 inputs in boxes of 32 rows
     MOK_DEV void load(uint8_t *st, uint32_t fb, const LinGeom &q, int k0, const CUtensorMap *tmA,
                       const CUtensorMap *tmB) const {
         tma_load_3d_pair(st, tmA, fb, q.a0 + k0, q.a1, q.a2);
-        tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, q.b0 + k0, q.b1);
+        for (int j = 0; j < q.nbox; ++j)
+            tc::tma_load_2d_pair(st + 2 * BOX + j * (BOX / 2), tmB, fb, q.b0 + k0, q.b1 + 32 * j);
     }
     MOK_DEV void epilogue(const Unit &u, int seg, uint32_t rank, uint32_t c, int q, int hw, int lane,
                           Patches &pt, Carry<SUMS> &carry) const {
@@ -631,17 +632,18 @@ struct Dx {
         q.a2 = u.g;
         q.b0 = 0;
         q.b1 = u.r0 + (int)rank * (q.n_mma / 2);
-        q.nbox = 1;
+        q.nbox = (q.n_mma / 2 + 31) / 32;
         q.k_steps = (N + 15) / 16;
         return q;
     }
-    MOK_DEV uint32_t tx(const LinGeom &) const { return 4 * BOX; }
-    // A: two boxes of 64 inputs x 64 features; B: 128 rows x 64 features of dz
+    MOK_DEV uint32_t tx(const LinGeom &q) const { return 2 * BOX + q.nbox * (BOX / 2); }
+    // A: two boxes of 64 inputs x 64 features; B: the rows' 64 features of dz in boxes of 32 rows
     MOK_DEV void load(uint8_t *st, uint32_t fb, const LinGeom &q, int k0, const CUtensorMap *tmA,
                       const CUtensorMap *tmB) const {
         tma_load_3d_pair(st, tmA, fb, q.a0, k0, q.a2);
         tma_load_3d_pair(st + BOX, tmA, fb, q.a0 + 64, k0, q.a2);
-        tc::tma_load_2d_pair(st + 2 * BOX, tmB, fb, k0, q.b1);
+        for (int j = 0; j < q.nbox; ++j)
+            tc::tma_load_2d_pair(st + 2 * BOX + j * (BOX / 2), tmB, fb, k0, q.b1 + 32 * j);
     }
     MOK_DEV void epilogue(const Unit &u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
                           Patches &pt, Carry<SUMS> &carry) const {
@@ -1291,11 +1293,24 @@ cudaError_t launch_small(SmallArgs a, cudaStream_t s) {
 
 bool grouped(const int32_t *starts) { return starts != nullptr; }
 
-// dense tiles of equal height
-Tiles dense_tiles(int64_t rows) {
-    const int64_t n = rows > 0 ? (rows + LTILE - 1) / LTILE : 1;
-    const int64_t h = round_up((rows + n - 1) / n, 16);
-    return Tiles{nullptr, (rows + h - 1) / (h > 0 ? h : 1), rows, (int)(h > 0 ? h : 16)};
+// Dense tiles of equal height: the height, up to 256 rows, at which `n_mb` blocks a tile take the
+// least time, as waves over the SM pairs times a K block's time. That is the larger of the MMAs'
+// (2 clocks a row) and the loads' (64 bytes a clock and SM: 256 clocks for the weights, 64 for
+// each box of 32 rows).
+Tiles dense_tiles(int64_t rows, int64_t n_mb) {
+    const int64_t pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
+    int64_t best_h = LTILE, best = INT64_MAX;
+    for (int64_t h0 = LTILE; h0 >= 16; h0 -= 16) {
+        const int64_t n = (rows + h0 - 1) / h0;
+        const int64_t h = n > 0 ? round_up((rows + n - 1) / n, 16) : 16;
+        const int64_t mma = 2 * h, load = 256 + 64 * ((h / 2 + 31) / 32);
+        const int64_t t = (n * n_mb + pairs - 1) / pairs * (mma > load ? mma : load);
+        if (t < best) {
+            best = t;
+            best_h = h;
+        }
+    }
+    return Tiles{nullptr, (rows + best_h - 1) / best_h, rows, (int)best_h};
 }
 
 struct LinWs {
@@ -1401,7 +1416,8 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
     LinWs wk;
     carve_linear(*c, MOK_LINEAR_FORWARD, ws, &wk);
     if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
-    Tiles tiles = dense_tiles(c->rows);
+    const int n_mb = (c->out_features + 255) / 256;
+    Tiles tiles = dense_tiles(c->rows, n_mb);
     if (grouped(starts)) {
         tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
         prof_begin(OP_LINEAR_TILES, stream);
@@ -1413,10 +1429,9 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
     const bool f32 = c->out_dtype == MOK_DTYPE_F32;
     CUtensorMap ma, mb;
     if (map_w(&ma, w, c->groups, c->out_features, c->in_features, c->ld_w, 128) != cudaSuccess ||
-        map2d(&mb, x, c->rows, c->in_features, c->ld_in, 128) != cudaSuccess)
+        map2d(&mb, x, c->rows, c->in_features, c->ld_in, 32) != cudaSuccess)
         return MOK_ERR_CUDA;
     const int segs = f32 ? (c->in_features + SEG_K - 1) / SEG_K : 1;
-    const int n_mb = (c->out_features + 255) / 256;
     const int64_t units = tiles.cap * n_mb;
     const bool plain = c->act == MOK_ACT_NONE && !residual && !z;
 #define MOK_FWD(F, PL)                                                                          \
@@ -1460,7 +1475,8 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     LinWs wk;
     carve_linear(*c, MOK_LINEAR_BACKWARD, ws, &wk);
     if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
-    Tiles tiles = dense_tiles(c->rows);
+    const int n_kb = (Kin + 255) / 256;
+    Tiles tiles = dense_tiles(c->rows, n_kb);
     if (grouped(starts)) {
         tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
         prof_begin(OP_LINEAR_TILES, stream);
@@ -1476,21 +1492,23 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     if (db || (!direct && (dx || dw))) {
         uint16_t *dzo = direct || (!dx && !dw) ? nullptr : wk.dz;
         float *part = db ? wk.part : nullptr;
-        const dim3 grid((unsigned)(tiles.cap * DZ_PARTS), (unsigned)((N + 63) / 64));
+        // dz has tiles of its own: full ones, whatever the products take
+        const Tiles dzt = grouped(starts) ? tiles
+                                          : Tiles{nullptr, (c->rows + LTILE - 1) / LTILE, c->rows, LTILE};
+        const dim3 grid((unsigned)(dzt.cap * DZ_PARTS), (unsigned)((N + 63) / 64));
         prof_begin(OP_LINEAR_DZ, stream);
-        launch_dz(c->act, dy32, grid, dy, (const uint16_t *)z, tiles, N, c->ld_out, dzo, ld_dz,
+        launch_dz(c->act, dy32, grid, dy, (const uint16_t *)z, dzt, N, c->ld_out, dzo, ld_dz,
                   part, stream);
         if (db)
             linear_db_kernel<<<(unsigned)(((int64_t)G * N + 255) / 256), 256, 0, stream>>>(
-                wk.part, tiles, G, N, db);
+                wk.part, dzt, G, N, db);
         prof_end(OP_LINEAR_DZ, stream, db ? 2 : 1);
         if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
     }
     CUtensorMap ma, mb;
-    const int n_kb = (Kin + 255) / 256;
     if (dx) {
         if (map_w(&ma, w, G, N, Kin, c->ld_w, 64) != cudaSuccess ||
-            map2d(&mb, dz, c->rows, N, ld_dz, 128) != cudaSuccess)
+            map2d(&mb, dz, c->rows, N, ld_dz, 32) != cudaSuccess)
             return MOK_ERR_CUDA;
         const int64_t units = tiles.cap * n_kb;
         if (g32) {
