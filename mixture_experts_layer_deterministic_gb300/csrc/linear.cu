@@ -79,11 +79,12 @@ struct Tiles {
 };
 
 // Each group's rows in tiles of equal height (a multiple of 16, at most LTILE); valid[g] gets
-// the group's row count, 0 where its layout breaks the rules.
+// the group's row count, 0 where its layout breaks the rules; first[g] its first tile (first[G]:
+// their number).
 __global__ void __launch_bounds__(MAX_G)
     linear_tiles_kernel(const int32_t *__restrict__ starts, const int32_t *__restrict__ counts,
                         int G, int64_t rows, int32_t *__restrict__ list, int64_t cap,
-                        int32_t *__restrict__ valid, int *status) {
+                        int32_t *__restrict__ valid, int32_t *__restrict__ first, int *status) {
     __shared__ int32_t wsum[MAX_G / 32];
     const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
     int64_t b = 0, n = 0, h = LTILE;
@@ -114,10 +115,11 @@ __global__ void __launch_bounds__(MAX_G)
     __syncthreads();
     int32_t at = v - nt;
     for (int w = 0; w < warp; ++w) at += wsum[w];
+    if (g < G) first[g] = (int32_t)(at < cap ? at : cap);
     if (g == MAX_G - 1) {
         // overlapping groups can ask for more tiles than there are rows for
         const int32_t total = at + nt;
-        list[-4] = (int32_t)(total < cap ? total : cap);
+        list[-4] = first[G] = (int32_t)(total < cap ? total : cap);
         if (total > cap) raise_status(status, MOK_ERR_DEVICE_INVARIANT);
     }
     for (int32_t i = 0; i < nt; ++i) {
@@ -669,6 +671,26 @@ struct Dx {
     }
 };
 
+// The bias gradient from the parts of the dz kernel: db[g][n] is the sum of the group's parts in
+// row order.
+constexpr int DZ_ROWS = 128;
+constexpr int DZ_PARTS = LTILE / DZ_ROWS;  // parts of a tile
+struct DbArgs {
+    const float *part;     // [tiles][DZ_PARTS][N]
+    const int32_t *first;  // grouped: first tile of each group
+    int64_t tiles;         // dense: all tiles
+    float *db;             // [G][N], or nullptr
+    MOK_DEV float sum(int g, int n, int N) const {
+        const int64_t t0 = first != nullptr ? __ldg(first + g) : 0;
+        const int64_t t1 = first != nullptr ? __ldg(first + g + 1) : tiles;
+        const float *p = part + t0 * DZ_PARTS * N + n;
+        float a = 0.f;
+#pragma unroll 8
+        for (int64_t k = 0; k < (t1 - t0) * DZ_PARTS; ++k) a += p[k * N];
+        return a;
+    }
+};
+
 template <bool F32>
 struct Dw {
     using E = Epi<false>;
@@ -682,6 +704,7 @@ struct Dw {
     int64_t ld;                     // row stride of dW
     void *dw;
     int *status;
+    DbArgs db;
 
     MOK_DEV int64_t n_units() const { return (int64_t)G * n_mb * n_nb; }
     MOK_DEV Unit unit(uint32_t u) const {
@@ -720,6 +743,10 @@ struct Dw {
         const int nn = N - nb * 256 < 256 ? N - nb * 256 : 256;
         const bool any = u.nr > 0;
         const int i0 = mb * 256 + (int)rank * 128 + q * 32;
+        if (db.db != nullptr && mb == 0 && rank == 0) {  // one thread per feature of the block
+            const int n = (4 * hw + q) * 32 + lane;
+            if (n < nn) db.db[(int64_t)g * N + nb * 256 + n] = db.sum(g, nb * 256 + n, N);
+        }
         for (int n0 = 32 * hw; n0 < nn; n0 += E::STEP) {
             if constexpr (F32) {
                 float v[32];
@@ -770,17 +797,16 @@ MOK_DEV void lin_drain(uint64_t *bar, uint32_t parity) {
     }
 }
 
+// the kernel's work on the units cid, cid + ncl, ... of p, as one CTA of a pair
 template <class P>
-__global__ void __launch_bounds__(P::E::THREADS, 1)
-    linear_kernel(const __grid_constant__ CUtensorMap tmA,
-                  const __grid_constant__ CUtensorMap tmB, const P p) {
+MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P &p,
+                         const uint32_t cid, const uint32_t ncl) {
     constexpr int NS = LSTAGES, SB = LSTAGE_BYTES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     LinSmem *sm = (LinSmem *)(base + NS * SB + LIN_PATCHES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
-    const uint32_t cid = tc::cluster_id_x(), ncl = tc::cluster_count_x();
     const uint32_t n_units = (uint32_t)p.n_units();
     const int segs = p.segs;
 
@@ -953,6 +979,28 @@ __global__ void __launch_bounds__(P::E::THREADS, 1)
     }
 }
 
+template <class P>
+__global__ void __launch_bounds__(P::E::THREADS, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tmA,
+                  const __grid_constant__ CUtensorMap tmB, const P p) {
+    linear_body(tmA, tmB, p, tc::cluster_id_x(), tc::cluster_count_x());
+}
+
+// two products at once: the first `split` pairs take the units of p, the others those of q
+template <class P, class Q>
+__global__ void __launch_bounds__(P::E::THREADS, 1)
+    linear_both_kernel(const __grid_constant__ CUtensorMap pA,
+                       const __grid_constant__ CUtensorMap pB, const P p,
+                       const __grid_constant__ CUtensorMap qA,
+                       const __grid_constant__ CUtensorMap qB, const Q q, const uint32_t split) {
+    static_assert(P::E::THREADS == Q::E::THREADS, "one launch shape");
+    const uint32_t c = tc::cluster_id_x();
+    if (c < split)
+        linear_body(pA, pB, p, c, split);
+    else
+        linear_body(qA, qB, q, c - split, tc::cluster_count_x() - split);
+}
+
 // ---------------------------------------------------------------- few rows
 // Up to 8 dense rows (a decoded token, a small batch): the weights' bytes are all the work, and
 // the tensor-core kernel's 256-row tiles put them on too few SMs (16 of 76 pairs for 4096
@@ -1071,9 +1119,6 @@ __global__ void __launch_bounds__(256)
 // block per 128 rows of a tile and 64 columns: 8 threads side by side on 8 columns each, 32
 // row lanes of 4 rows each, whose loads are all issued before the first is used (one row at a
 // time, 20480 x 1024 took 47 us); the sums of a column's 32 row lanes are added in lane order.
-constexpr int DZ_ROWS = 128;
-constexpr int DZ_PARTS = LTILE / DZ_ROWS;  // parts of a tile
-
 template <bool DY32, int ACT>
 __global__ void __launch_bounds__(256)
     linear_dz_kernel(const void *__restrict__ dy, const uint16_t *__restrict__ z, Tiles tiles,
@@ -1157,37 +1202,10 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// db[g][n] = the sum of the tiles' parts in tile order (a group's tiles are consecutive)
-__global__ void __launch_bounds__(256)
-    linear_db_kernel(const float *__restrict__ part, Tiles tiles, int G, int N,
-                     float *__restrict__ db) {
+// db where no dW is asked for (else the dW kernel adds the parts)
+__global__ void __launch_bounds__(256) linear_db_kernel(const DbArgs d, int G, int N) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)G * N) return;
-    const int g = (int)(i / N), n = (int)(i % N);
-    const int64_t nt = tiles.count();
-    int64_t t = 0;
-    if (tiles.list != nullptr) {  // the group's first tile
-        int64_t lo = 0, hi = nt;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (tiles.list[4 * mid] < g) lo = mid + 1; else hi = mid;
-        }
-        t = lo;
-    }
-    int64_t e = nt;  // one past the group's last tile
-    if (tiles.list != nullptr) {
-        int64_t lo = t, hi = nt;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (tiles.list[4 * mid] <= g) lo = mid + 1; else hi = mid;
-        }
-        e = lo;
-    }
-    float a = 0.f;
-    const float *p = part + t * DZ_PARTS * N + n;
-#pragma unroll 8
-    for (int64_t k = 0; k < (e - t) * DZ_PARTS; ++k) a += p[k * N];
-    db[i] = a;
+    if (i < (int64_t)G * N) d.db[i] = d.sum((int)(i / N), (int)(i % N), N);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1216,39 +1234,55 @@ cudaError_t map_w(CUtensorMap *m, const void *p, int64_t G, int64_t N, int64_t K
                : cudaErrorInvalidValue;
 }
 
-// pairs of SMs that run at once, one cluster of two per unit at most
-template <class P>
-cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const P &p,
-                          int64_t units_cap, cudaStream_t s) {
-    if (units_cap < 1) return cudaSuccess;
-    if (units_cap > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    static std::atomic<uint64_t> attr_set{0};
+int64_t sm_pairs() { return device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1; }
+
+// a launch of `pairs` clusters of two CTAs; the shared-memory opt-in is set once per device
+template <class... KA, class... A>
+cudaError_t launch_pairs(void (*kernel)(KA...), std::atomic<uint64_t> &attr_set, int threads,
+                         int64_t pairs, cudaStream_t s, const A &...args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= MAX_DEV) return cudaErrorInvalidDevice;
     const uint64_t bit = 1ull << dev;
     if ((attr_set.load(std::memory_order_acquire) & bit) == 0) {
-        e = cudaFuncSetAttribute(linear_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 LIN_SMEM);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LIN_SMEM);
         if (e != cudaSuccess) return e;
         attr_set.fetch_or(bit, std::memory_order_acq_rel);
     }
-    const int64_t pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = 2;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(2 * (units_cap < pairs ? units_cap : pairs)), 1, 1);
-    cfg.blockDim = dim3(P::E::THREADS, 1, 1);
+    cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = LIN_SMEM;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, linear_kernel<P>, ma, mb, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// one cluster per unit, at most the pairs of SMs that run at once
+template <class P>
+cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const P &p,
+                          int64_t units_cap, cudaStream_t s) {
+    if (units_cap < 1) return cudaSuccess;
+    if (units_cap > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> attr_set{0};
+    return launch_pairs(linear_kernel<P>, attr_set, P::E::THREADS,
+                        units_cap < sm_pairs() ? units_cap : sm_pairs(), s, ma, mb, p);
+}
+template <class P, class Q>
+cudaError_t launch_both(const CUtensorMap &pa, const CUtensorMap &pb, const P &p,
+                        const CUtensorMap &qa, const CUtensorMap &qb, const Q &q, int64_t split,
+                        int64_t pairs, cudaStream_t s) {
+    static std::atomic<uint64_t> attr_set{0};
+    return launch_pairs(linear_both_kernel<P, Q>, attr_set, P::E::THREADS, pairs, s, pa, pb, p, qa,
+                        qb, q, (uint32_t)split);
 }
 
 template <bool DY32>
@@ -1293,18 +1327,27 @@ cudaError_t launch_small(SmallArgs a, cudaStream_t s) {
 
 bool grouped(const int32_t *starts) { return starts != nullptr; }
 
+// clocks of a 64-element K block on tiles of h rows: the larger of the MMAs' (2 a row) and the
+// loads' (64 bytes a clock and SM: 256 for the weights, 64 for each box of 32 rows)
+int64_t block_clocks(int64_t h) {
+    const int64_t mma = 2 * h, load = 256 + 64 * ((h / 2 + 31) / 32);
+    return mma > load ? mma : load;
+}
+// clocks of a unit of `blocks` K blocks on h columns: its loads and MMAs, or its epilogue (about
+// 4500 clocks for 256 columns), whichever keeps the pair longer
+int64_t unit_clocks(int64_t blocks, int64_t h) {
+    const int64_t main = blocks * block_clocks(h), epi = 4500 * h / LTILE;
+    return main > epi ? main : epi;
+}
 // Dense tiles of equal height: the height, up to 256 rows, at which `n_mb` blocks a tile take the
-// least time, as waves over the SM pairs times a K block's time. That is the larger of the MMAs'
-// (2 clocks a row) and the loads' (64 bytes a clock and SM: 256 clocks for the weights, 64 for
-// each box of 32 rows).
+// least time, as waves over the SM pairs times a K block's clocks.
 Tiles dense_tiles(int64_t rows, int64_t n_mb) {
-    const int64_t pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
+    const int64_t pairs = sm_pairs();
     int64_t best_h = LTILE, best = INT64_MAX;
     for (int64_t h0 = LTILE; h0 >= 16; h0 -= 16) {
         const int64_t n = (rows + h0 - 1) / h0;
         const int64_t h = n > 0 ? round_up((rows + n - 1) / n, 16) : 16;
-        const int64_t mma = 2 * h, load = 256 + 64 * ((h / 2 + 31) / 32);
-        const int64_t t = (n * n_mb + pairs - 1) / pairs * (mma > load ? mma : load);
+        const int64_t t = (n * n_mb + pairs - 1) / pairs * block_clocks(h);
         if (t < best) {
             best = t;
             best_h = h;
@@ -1313,10 +1356,29 @@ Tiles dense_tiles(int64_t rows, int64_t n_mb) {
     return Tiles{nullptr, (rows + best_h - 1) / best_h, rows, (int)best_h};
 }
 
+// Whether two products of `a` and `b` equal units (ta, tb clocks each) run better side by side
+// than one after the other: *split pairs of SMs for the first and the rest of *pairs for the
+// second, or 0. Side by side there is one launch and one tail, but each has fewer pairs.
+void plan_both(int64_t a, int64_t ta, int64_t b, int64_t tb, int64_t *split, int64_t *pairs) {
+    const int64_t all = sm_pairs(), once = 12000;  // clocks of a launch, its fill and its drain
+    const auto waves = [](int64_t n, int64_t p) { return (n + p - 1) / p; };
+    int64_t best = waves(a, all) * ta + waves(b, all) * tb + once;
+    *split = *pairs = 0;
+    for (int64_t k = 1; k < all; ++k) {
+        const int64_t x = waves(a, k) * ta, y = waves(b, all - k) * tb;
+        if ((x > y ? x : y) < best) {
+            best = x > y ? x : y;
+            *split = k < a ? k : a;
+            *pairs = *split + (all - k < b ? all - k : b);
+        }
+    }
+}
+
 struct LinWs {
     int32_t *list;    // past its 16-byte header
     int64_t cap;
     int32_t *valid;   // [G]
+    int32_t *first;   // [G + 1]
     uint16_t *dz;     // [rows][ld_dz]
     int64_t ld_dz;
     float *part;      // [tiles][DZ_PARTS][N]
@@ -1335,6 +1397,7 @@ size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
     int32_t *l = (int32_t *)take(16 + (size_t)w.cap * 16);
     w.list = l != nullptr ? l + 4 : nullptr;
     w.valid = (int32_t *)take((size_t)c.groups * 4);
+    w.first = (int32_t *)take((size_t)(c.groups + 1) * 4);
     if (pass == MOK_LINEAR_BACKWARD) {
         w.ld_dz = round_up(c.out_features, 8);
         w.dz = (uint16_t *)take((size_t)c.rows * w.ld_dz * 2);
@@ -1422,7 +1485,7 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
         tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
         prof_begin(OP_LINEAR_TILES, stream);
         linear_tiles_kernel<<<1, MAX_G, 0, stream>>>(starts, counts, c->groups, c->rows, wk.list,
-                                                     wk.cap, wk.valid, status);
+                                                     wk.cap, wk.valid, wk.first, status);
         prof_end(OP_LINEAR_TILES, stream, 1);
         if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
     }
@@ -1481,7 +1544,7 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
         tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
         prof_begin(OP_LINEAR_TILES, stream);
         linear_tiles_kernel<<<1, MAX_G, 0, stream>>>(starts, counts, G, c->rows, wk.list, wk.cap,
-                                                     wk.valid, status);
+                                                     wk.valid, wk.first, status);
         prof_end(OP_LINEAR_TILES, stream, 1);
         if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
     }
@@ -1489,6 +1552,11 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     const bool direct = !act && !dy32;
     const uint16_t *dz = direct ? (const uint16_t *)dy : wk.dz;
     const int64_t ld_dz = direct ? c->ld_out : wk.ld_dz;
+    // The dW kernel adds the parts of db on the side, which saves a launch; with groups its
+    // epilogues are the bottleneck already (64 groups of 320 rows: dW 145 -> 168 us) and a
+    // launch of its own is shorter.
+    const bool db_in_dw = dw && !grouped(starts);
+    DbArgs dba{wk.part, grouped(starts) ? wk.first : nullptr, (c->rows + LTILE - 1) / LTILE, db};
     if (db || (!direct && (dx || dw))) {
         uint16_t *dzo = direct || (!dx && !dw) ? nullptr : wk.dz;
         float *part = db ? wk.part : nullptr;
@@ -1499,42 +1567,44 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
         prof_begin(OP_LINEAR_DZ, stream);
         launch_dz(c->act, dy32, grid, dy, (const uint16_t *)z, dzt, N, c->ld_out, dzo, ld_dz,
                   part, stream);
-        if (db)
-            linear_db_kernel<<<(unsigned)(((int64_t)G * N + 255) / 256), 256, 0, stream>>>(
-                wk.part, dzt, G, N, db);
-        prof_end(OP_LINEAR_DZ, stream, db ? 2 : 1);
+        if (db && !db_in_dw)
+            linear_db_kernel<<<(unsigned)(((int64_t)G * N + 255) / 256), 256, 0, stream>>>(dba, G, N);
+        prof_end(OP_LINEAR_DZ, stream, db && !db_in_dw ? 2 : 1);
         if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
     }
-    CUtensorMap ma, mb;
-    if (dx) {
-        if (map_w(&ma, w, G, N, Kin, c->ld_w, 64) != cudaSuccess ||
-            map2d(&mb, dz, c->rows, N, ld_dz, 32) != cudaSuccess)
-            return MOK_ERR_CUDA;
-        const int64_t units = tiles.cap * n_kb;
-        if (g32) {
-            const Dx<true> p{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status};
-            MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, p, units, stream));
-        } else {
-            const Dx<false> p{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status};
-            MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(ma, mb, p, units, stream));
-        }
-    }
-    if (dw) {
-        if (map2d(&ma, x, c->rows, Kin, c->ld_in, 64) != cudaSuccess ||
-            map2d(&mb, dz, c->rows, N, ld_dz, 64) != cudaSuccess)
-            return MOK_ERR_CUDA;
-        const int n_nb = (N + 255) / 256;
-        const int64_t units = (int64_t)G * n_kb * n_nb;
-        const int32_t *valid = grouped(starts) ? wk.valid : nullptr;
-        if (g32) {
-            const Dw<true> p{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw, status};
-            MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(ma, mb, p, units, stream));
-        } else {
-            const Dw<false> p{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw,
-                              status};
-            MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(ma, mb, p, units, stream));
-        }
-    }
+    CUtensorMap xa, xb, wa, wb;
+    if (dx && (map_w(&xa, w, G, N, Kin, c->ld_w, 64) != cudaSuccess ||
+               map2d(&xb, dz, c->rows, N, ld_dz, 32) != cudaSuccess))
+        return MOK_ERR_CUDA;
+    if (dw && (map2d(&wa, x, c->rows, Kin, c->ld_in, 64) != cudaSuccess ||
+               map2d(&wb, dz, c->rows, N, ld_dz, 64) != cudaSuccess))
+        return MOK_ERR_CUDA;
+    const int n_nb = (N + 255) / 256;
+    const int64_t x_units = dx ? tiles.cap * n_kb : 0;
+    const int64_t w_units = dw ? (int64_t)G * n_kb * n_nb : 0;
+    if (x_units > 0x7FFFFFFF || w_units > 0x7FFFFFFF) return MOK_ERR_INVALID_ARG;
+    const int32_t *valid = grouped(starts) ? wk.valid : nullptr;
+    int64_t split = 0, pairs = 0;  // pairs of SMs for dW, and in all, where both go in one launch
+    if (dx && dw && !grouped(starts))
+        plan_both(w_units, unit_clocks((c->rows + 63) / 64, LTILE), x_units,
+                  unit_clocks((N + 63) / 64, tiles.height), &split, &pairs);
+    DbArgs dwb = dba;
+    if (!db_in_dw) dwb.db = nullptr;
+#define MOK_BWD(F)                                                                              \
+    do {                                                                                        \
+        const Dx<F> px{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status};                           \
+        const Dw<F> pw{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw, status, dwb}; \
+        if (split > 0) {                                                                        \
+            MOK_OP_LAUNCH(OP_LINEAR_DX, 1,                                                      \
+                          launch_both(wa, wb, pw, xa, xb, px, split, pairs, stream));           \
+        } else {                                                                                \
+            if (dx) MOK_OP_LAUNCH(OP_LINEAR_DX, 1, launch_linear(xa, xb, px, x_units, stream)); \
+            if (dw) MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(wa, wb, pw, w_units, stream)); \
+        }                                                                                       \
+    } while (0)
+    if (g32) MOK_BWD(true);
+    else MOK_BWD(false);
+#undef MOK_BWD
     return MOK_OK;
 }
 
