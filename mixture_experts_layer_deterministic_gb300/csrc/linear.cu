@@ -57,6 +57,11 @@ struct Carry<true> {
     float v[2 * Epi<true>::CHUNKS][16];  // by 16 columns
 };
 
+// Launches of one call overlap at their edges: a kernel may be started while the one before it
+// in the stream drains, sets itself up, and waits here before it touches global memory.
+MOK_DEV void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+MOK_DEV void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- row tiles
 // A tile is up to `height` consecutive rows of one group. Dense: tile t covers rows
 // [t height, ..). Grouped: a list built on the device, int32 [cap][4] = (group, first row,
@@ -86,6 +91,8 @@ __global__ void __launch_bounds__(MAX_G)
                         int G, int64_t rows, int32_t *__restrict__ list, int64_t cap,
                         int32_t *__restrict__ valid, int32_t *__restrict__ first, int *status) {
     __shared__ int32_t wsum[MAX_G / 32];
+    let_next_start();
+    wait_for_previous();
     const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
     int64_t b = 0, n = 0, h = LTILE;
     int32_t nt = 0;
@@ -136,17 +143,28 @@ int64_t tiles_cap(int64_t rows, int G) { return G + rows / LTILE + 1; }
 // ---------------------------------------------------------------- activations
 // exp and the quotient to within 2^-20 of their values: far inside the bf16 rounding of y
 // and z, and of the size of the products' own error in fp32
-MOK_DEV float sigmoid_f(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+MOK_DEV float sigmoid2_f(float x) {  // sigma(-x log 2) = 1 / (1 + 2^x)
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+MOK_DEV float sigmoid_f(float x) { return sigmoid2_f(-LOG2E * x); }
 
 constexpr float GELU_C2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float GELU_A = 0.044715f;
 
+// sigma(2 sqrt(2/pi) (z + a z^3)), z2 = z z
+MOK_DEV float gelu_sigmoid(float z, float z2) {
+    return sigmoid2_f(z * fmaf(-LOG2E * GELU_C2 * GELU_A, z2, -LOG2E * GELU_C2));
+}
 // 0.5 (1 + tanh u) = sigma(2u): gelu_tanh is z sigma(2 sqrt(2/pi) (z + a z^3))
 template <int ACT>
 MOK_DEV float act_f(float z) {
     if (ACT == MOK_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
     if (ACT == MOK_ACT_SILU) return z * sigmoid_f(z);
-    if (ACT == MOK_ACT_GELU_TANH) return z * sigmoid_f(GELU_C2 * fmaf(GELU_A * z * z, z, z));
+    if (ACT == MOK_ACT_GELU_TANH) return z * gelu_sigmoid(z, z * z);
     if (ACT == MOK_ACT_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
     return z;
 }
@@ -158,8 +176,8 @@ MOK_DEV float act_grad_f(float z) {
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
     if (ACT == MOK_ACT_GELU_TANH) {
-        const float s = sigmoid_f(GELU_C2 * fmaf(GELU_A * z * z, z, z));
-        const float du = GELU_C2 * fmaf(3.0f * GELU_A * z, z, 1.0f);
+        const float z2 = z * z, s = gelu_sigmoid(z, z2);
+        const float du = fmaf(3.0f * GELU_A * GELU_C2, z2, GELU_C2);
         return s * fmaf(z * (1.0f - s), du, 1.0f);
     }
     if (ACT == MOK_ACT_GELU)
@@ -807,7 +825,6 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
     LinSmem *sm = (LinSmem *)(base + NS * SB + LIN_PATCHES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
-    const uint32_t n_units = (uint32_t)p.n_units();
     const int segs = p.segs;
 
     if (threadIdx.x == 0) {
@@ -834,6 +851,9 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
     tc::tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
     volatile int *abort = &sm->abort;
+    let_next_start();
+    wait_for_previous();
+    const uint32_t n_units = (uint32_t)p.n_units();
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
@@ -1023,6 +1043,8 @@ template <int R, int UN, bool F32>
 __global__ void __launch_bounds__(256)
     linear_small_kernel(const SmallArgs a) {
     __shared__ float sh[8][SMALL_F * R];
+    let_next_start();
+    wait_for_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = warp % a.parts, slot = warp / a.parts;
     const int per_block = 8 / a.parts * SMALL_F;
@@ -1116,7 +1138,7 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- dz and the bias gradient
 // dz = dy act'(z) in bf16 (the products' operand), and the column sums of the unrounded dz. One
-// block per 128 rows of a tile and 64 columns: 8 threads side by side on 8 columns each, 32
+// block per half tile (up to 128 rows) and 64 columns: 8 threads side by side on 8 columns each, 32
 // row lanes of 4 rows each, whose loads are all issued before the first is used (one row at a
 // time, 20480 x 1024 took 47 us); the sums of a column's 32 row lanes are added in lane order.
 template <bool DY32, int ACT>
@@ -1125,11 +1147,16 @@ __global__ void __launch_bounds__(256)
                      int N, int64_t ld, uint16_t *__restrict__ dz, int64_t ld_dz,
                      float *__restrict__ part) {
     __shared__ float red[32][65];
+    let_next_start();
+    wait_for_previous();
     const int64_t t = blockIdx.x / DZ_PARTS;
     if (t >= tiles.count()) return;
     const int4 tile = tiles.get(t);
-    const int64_t r0 = tile.y + (int64_t)(blockIdx.x % DZ_PARTS) * DZ_ROWS;
-    const int64_t r1 = tile.z, rend = tile.w != 0 ? (r1 + 15) & ~(int64_t)15 : r1;
+    // the tile in equal parts, multiples of 16 rows; the last takes the padding
+    const int per = ((tile.z - tile.y + DZ_PARTS - 1) / DZ_PARTS + 15) & ~15;
+    const int64_t r0 = tile.y + (int64_t)(blockIdx.x % DZ_PARTS) * per;
+    const int64_t all = tile.w != 0 ? (tile.z + 15) & ~15 : tile.z;  // one past the rows to write
+    const int64_t rend = r0 + per < all ? r0 + per : all, r1 = rend < tile.z ? rend : tile.z;
     const int cv = threadIdx.x & 7, rl = threadIdx.x >> 3;
     const int c = blockIdx.y * 64 + cv * 8;
     constexpr int NR = DZ_ROWS / 32;
@@ -1204,6 +1231,8 @@ __global__ void __launch_bounds__(256)
 
 // db where no dW is asked for (else the dW kernel adds the parts)
 __global__ void __launch_bounds__(256) linear_db_kernel(const DbArgs d, int G, int N) {
+    let_next_start();
+    wait_for_previous();
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < (int64_t)G * N) d.db[i] = d.sum((int)(i / N), (int)(i % N), N);
 }
@@ -1236,6 +1265,29 @@ cudaError_t map_w(CUtensorMap *m, const void *p, int64_t G, int64_t N, int64_t K
 
 int64_t sm_pairs() { return device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1; }
 
+// a launch that may start while the kernel before it drains (its kernel waits for that one
+// itself); cluster: CTAs per cluster
+template <class... KA, class... A>
+cudaError_t launch_edge(void (*kernel)(KA...), dim3 grid, int threads, int smem, int cluster,
+                        cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // a launch of `pairs` clusters of two CTAs; the shared-memory opt-in is set once per device
 template <class... KA, class... A>
 cudaError_t launch_pairs(void (*kernel)(KA...), std::atomic<uint64_t> &attr_set, int threads,
@@ -1250,20 +1302,7 @@ cudaError_t launch_pairs(void (*kernel)(KA...), std::atomic<uint64_t> &attr_set,
         if (e != cudaSuccess) return e;
         attr_set.fetch_or(bit, std::memory_order_acq_rel);
     }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.dynamicSmemBytes = LIN_SMEM;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_edge(kernel, dim3((unsigned)(2 * pairs)), threads, LIN_SMEM, 2, s, args...);
 }
 
 // one cluster per unit, at most the pairs of SMs that run at once
@@ -1286,27 +1325,21 @@ cudaError_t launch_both(const CUtensorMap &pa, const CUtensorMap &pb, const P &p
 }
 
 template <bool DY32>
-void launch_dz_act(int act, dim3 grid, const void *dy, const uint16_t *z, const Tiles &t, int N,
-                   int64_t ld, uint16_t *dz, int64_t ld_dz, float *part, cudaStream_t s) {
-#define MOK_DZ_CASE(A)                                                                      \
-    case A: linear_dz_kernel<DY32, A><<<grid, 256, 0, s>>>(dy, z, t, N, ld, dz, ld_dz, part); \
-        break
+cudaError_t launch_dz(int act, dim3 grid, const void *dy, const uint16_t *z, const Tiles &t, int N,
+                      int64_t ld, uint16_t *dz, int64_t ld_dz, float *part, cudaStream_t s) {
+#define MOK_DZ_CASE(A)                                                                         \
+    case A:                                                                                    \
+        return launch_edge(linear_dz_kernel<DY32, A>, grid, 256, 0, 1, s, dy, z, t, N, ld, dz, \
+                           ld_dz, part)
     switch (act) {
         MOK_DZ_CASE(MOK_ACT_RELU);
         MOK_DZ_CASE(MOK_ACT_SILU);
         MOK_DZ_CASE(MOK_ACT_GELU_TANH);
         MOK_DZ_CASE(MOK_ACT_GELU);
-        default: linear_dz_kernel<DY32, MOK_ACT_NONE><<<grid, 256, 0, s>>>(dy, z, t, N, ld, dz,
-                                                                         ld_dz, part);
+        MOK_DZ_CASE(MOK_ACT_NONE);
     }
 #undef MOK_DZ_CASE
-}
-void launch_dz(int act, bool dy32, dim3 grid, const void *dy, const uint16_t *z, const Tiles &t,
-               int N, int64_t ld, uint16_t *dz, int64_t ld_dz, float *part, cudaStream_t s) {
-    if (dy32)
-        launch_dz_act<true>(act, grid, dy, z, t, N, ld, dz, ld_dz, part, s);
-    else
-        launch_dz_act<false>(act, grid, dy, z, t, N, ld, dz, ld_dz, part, s);
+    return cudaErrorInvalidValue;
 }
 
 template <bool F32>
@@ -1318,11 +1351,10 @@ cudaError_t launch_small(SmallArgs a, cudaStream_t s) {
         a.parts *= 2;
     const int per_block = 8 / a.parts * SMALL_F;
     const unsigned grid = (unsigned)((a.N + per_block - 1) / per_block);
-    if (a.rows == 1) linear_small_kernel<1, 4, F32><<<grid, 256, 0, s>>>(a);
-    else if (a.rows == 2) linear_small_kernel<2, 4, F32><<<grid, 256, 0, s>>>(a);
-    else if (a.rows <= 4) linear_small_kernel<4, 2, F32><<<grid, 256, 0, s>>>(a);
-    else linear_small_kernel<8, 2, F32><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    if (a.rows == 1) return launch_edge(linear_small_kernel<1, 4, F32>, grid, 256, 0, 1, s, a);
+    if (a.rows == 2) return launch_edge(linear_small_kernel<2, 4, F32>, grid, 256, 0, 1, s, a);
+    if (a.rows <= 4) return launch_edge(linear_small_kernel<4, 2, F32>, grid, 256, 0, 1, s, a);
+    return launch_edge(linear_small_kernel<8, 2, F32>, grid, 256, 0, 1, s, a);
 }
 
 bool grouped(const int32_t *starts) { return starts != nullptr; }
@@ -1483,11 +1515,9 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
     Tiles tiles = dense_tiles(c->rows, n_mb);
     if (grouped(starts)) {
         tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
-        prof_begin(OP_LINEAR_TILES, stream);
-        linear_tiles_kernel<<<1, MAX_G, 0, stream>>>(starts, counts, c->groups, c->rows, wk.list,
-                                                     wk.cap, wk.valid, wk.first, status);
-        prof_end(OP_LINEAR_TILES, stream, 1);
-        if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
+        MOK_OP_LAUNCH(OP_LINEAR_TILES, 1,
+                      launch_edge(linear_tiles_kernel, 1, MAX_G, 0, 1, stream, starts, counts,
+                                  c->groups, c->rows, wk.list, wk.cap, wk.valid, wk.first, status));
     }
     const bool f32 = c->out_dtype == MOK_DTYPE_F32;
     CUtensorMap ma, mb;
@@ -1542,11 +1572,9 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     Tiles tiles = dense_tiles(c->rows, n_kb);
     if (grouped(starts)) {
         tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
-        prof_begin(OP_LINEAR_TILES, stream);
-        linear_tiles_kernel<<<1, MAX_G, 0, stream>>>(starts, counts, G, c->rows, wk.list, wk.cap,
-                                                     wk.valid, wk.first, status);
-        prof_end(OP_LINEAR_TILES, stream, 1);
-        if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
+        MOK_OP_LAUNCH(OP_LINEAR_TILES, 1,
+                      launch_edge(linear_tiles_kernel, 1, MAX_G, 0, 1, stream, starts, counts,
+                                  c->groups, c->rows, wk.list, wk.cap, wk.valid, wk.first, status));
     }
     // without an activation a bf16 dy is dz
     const bool direct = !act && !dy32;
@@ -1564,13 +1592,15 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
         const Tiles dzt = grouped(starts) ? tiles
                                           : Tiles{nullptr, (c->rows + LTILE - 1) / LTILE, c->rows, LTILE};
         const dim3 grid((unsigned)(dzt.cap * DZ_PARTS), (unsigned)((N + 63) / 64));
-        prof_begin(OP_LINEAR_DZ, stream);
-        launch_dz(c->act, dy32, grid, dy, (const uint16_t *)z, dzt, N, c->ld_out, dzo, ld_dz,
-                  part, stream);
+        MOK_OP_LAUNCH(OP_LINEAR_DZ, 1,
+                      dy32 ? launch_dz<true>(c->act, grid, dy, (const uint16_t *)z, dzt, N,
+                                             c->ld_out, dzo, ld_dz, part, stream)
+                           : launch_dz<false>(c->act, grid, dy, (const uint16_t *)z, dzt, N,
+                                              c->ld_out, dzo, ld_dz, part, stream));
         if (db && !db_in_dw)
-            linear_db_kernel<<<(unsigned)(((int64_t)G * N + 255) / 256), 256, 0, stream>>>(dba, G, N);
-        prof_end(OP_LINEAR_DZ, stream, db && !db_in_dw ? 2 : 1);
-        if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
+            MOK_OP_LAUNCH(OP_LINEAR_DZ, 1,
+                          launch_edge(linear_db_kernel, (unsigned)(((int64_t)G * N + 255) / 256), 256,
+                                      0, 1, stream, dba, G, N));
     }
     CUtensorMap xa, xb, wa, wb;
     if (dx && (map_w(&xa, w, G, N, Kin, c->ld_w, 64) != cudaSuccess ||
