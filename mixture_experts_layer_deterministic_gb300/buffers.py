@@ -1,5 +1,7 @@
 """Device-memory plumbing for the C ABI: torch allocates, the library computes.
 
+`TokenSort`, `Linear` and `AdamW` do the same for the operators around the layer.
+
 `MoELayer` owns the caller-side buffers of one configuration (schedule arrays and the
 three workspaces) and strings the entry points together in the order a user calls them:
 mok_route_topk -> mok_build_schedule -> mok_forward (-> mok_backward). Every method only
@@ -173,3 +175,149 @@ def quantize_mxfp8(src, stream=None):
     s = torch.empty(src.shape[:-1] + (cols // 32,), dtype=torch.uint8, device=src.device)
     B.check(B.mok_quantize_mxfp8(src, rows, cols, q, s, stream), "quantize")
     return q, s
+
+
+# ------------------------------------------------- operators around the layer (mok_ops.h)
+
+def _row_stride(t):
+    if t.stride(-1) != 1:
+        raise ValueError("rows must be contiguous along their last axis")
+    return t.stride(0)
+
+
+class TokenSort:
+    """Tokens sorted by expert and back: the row map of a schedule and the four passes over it.
+    Sorted arrays come from `rows()`: expert e owns rows starts[e] .. starts[e] + kept[e],
+    padded with zero rows to a multiple of 16."""
+
+    def __init__(self, T, K, E, H, dtype=torch.bfloat16, capacity=0, device="cuda"):
+        per = 4 if dtype == torch.float32 else 8
+        self.T, self.K, self.E, self.H, self.dtype = T, K, E, H, dtype
+        self.ld = (H + per - 1) // per * per
+        self.device = torch.device(device)
+        self.cfg = B.make_rows(T, K, E, H, capacity=capacity, ld_tok=self.ld, ld_row=self.ld,
+                               dtype=B.MOK_DTYPE_F32 if dtype == torch.float32
+                               else B.MOK_DTYPE_BF16)
+        B.check(B.mok_check_rows_config(self.cfg), "rows config")
+        self.n_rows = int(self.cfg.n_rows)
+        self.map = _empty(T * K, torch.int32, self.device)
+        self.starts = _empty(E + 1, torch.int32, self.device)
+        self.kept = _empty(E, torch.int32, self.device)
+
+    def rows(self, width=None):
+        """A zeroed sorted array [n_rows][width] whose rows start on 16-byte boundaries."""
+        w = self.H if width is None else width
+        per = 4 if self.dtype == torch.float32 else 8
+        return torch.zeros(self.n_rows, (w + per - 1) // per * per, dtype=self.dtype,
+                           device=self.device)[:, :w]
+
+    def _check(self, tokens=(), rows=()):
+        for t in (*tokens, *rows):
+            if t is not None and (t.dtype != self.dtype or _row_stride(t) != self.ld):
+                raise ValueError("tokens and rows are %s with %d elements between rows" %
+                                 (self.dtype, self.ld))
+
+    def build(self, idx, sched, stream=None):
+        """The row map of `sched` (a Schedule built from idx [T][K])."""
+        B.check(B.mok_build_row_map(self.cfg, idx, sched.struct, self.map, self.starts, self.kept,
+                                    stream), "row map")
+
+    def dispatch(self, x, xs, stream=None):
+        self._check((x,), (xs,))
+        B.check(B.mok_dispatch(self.cfg, x, self.map, self.starts, self.kept, xs, stream),
+                "dispatch")
+        return xs
+
+    def dispatch_backward(self, dxs, dx, stream=None):
+        self._check((dx,), (dxs,))
+        B.check(B.mok_dispatch_backward(self.cfg, dxs, self.map, dx, stream), "dispatch backward")
+        return dx
+
+    def combine(self, rows, topk_w, y, residual=None, stream=None):
+        self._check((y, residual), (rows,))
+        B.check(B.mok_combine(self.cfg, rows, self.map, topk_w, residual, y, stream), "combine")
+        return y
+
+    def combine_backward(self, dy, rows, topk_w, drows, d_topk_w, stream=None):
+        self._check((dy,), (rows, drows))
+        B.check(B.mok_combine_backward(self.cfg, dy, rows, self.map, self.starts, self.kept,
+                                       topk_w, drows, d_topk_w, stream), "combine backward")
+        return drows
+
+
+class Linear:
+    """A linear layer and its workspaces: one matrix, or with groups > 1 one per group of sorted
+    rows (forward and backward then take the TokenSort that sorted them). Weights are
+    [groups][out][in] bf16; rows of x, y, z, dy, dx start on 16-byte boundaries."""
+
+    def __init__(self, rows, in_features, out_features, groups=1, act=B.MOK_ACT_NONE,
+                 out_dtype=torch.bfloat16, grad_dtype=torch.bfloat16, device="cuda"):
+        dt = lambda t: B.MOK_DTYPE_F32 if t == torch.float32 else B.MOK_DTYPE_BF16  # noqa: E731
+        self.cfg = B.make_linear(rows, in_features, out_features, groups, act, dt(out_dtype),
+                                 dt(grad_dtype))
+        B.check(B.mok_check_linear_config(self.cfg), "linear config")
+        self.device = torch.device(device)
+        self.ws = [None, None]
+
+    def _ws(self, which):
+        if self.ws[which] is None:
+            n = B.mok_linear_workspace_size(self.cfg, which)
+            self.ws[which] = (_empty(n, torch.uint8, self.device), n)
+        return self.ws[which]
+
+    def _check(self, wide, out):
+        for t, ld in [(t, self.cfg.ld_in) for t in wide] + [(t, self.cfg.ld_out) for t in out]:
+            if t is not None and _row_stride(t) != ld:
+                raise ValueError("rows have %d elements between them, not %d" %
+                                 (_row_stride(t), ld))
+
+    def forward(self, x, w, y, bias=None, residual=None, z=None, sort=None, stream=None):
+        self._check((x,), (y, residual, z))
+        ws, n = self._ws(B.MOK_LINEAR_FORWARD)
+        B.check(B.mok_linear_forward(self.cfg, x, w, bias, residual, sort and sort.starts,
+                                     sort and sort.kept, y, z, ws, n, stream), "linear forward")
+        return y
+
+    def backward(self, x, w, dy, z=None, dx=None, dw=None, db=None, sort=None, stream=None):
+        self._check((x, dx), (dy, z))
+        ws, n = self._ws(B.MOK_LINEAR_BACKWARD)
+        B.check(B.mok_linear_backward(self.cfg, x, w, z, dy, sort and sort.starts,
+                                      sort and sort.kept, dx, dw, db, ws, n, stream),
+                "linear backward")
+        return dx
+
+
+class AdamW:
+    """AdamW over a list of parameters: dicts with p (fp32 or bf16), g (its gradient) and, where
+    they apply, copy (bf16 working weights of an fp32 p) and weight_decay. The states are fp32,
+    or MXFP8 with eight_bit. Parameters that share their types go in one launch."""
+
+    def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, eight_bit=False,
+                 stochastic=True, seed=0):
+        self.lr, self.betas, self.eps, self.seed, self.t = lr, betas, eps, seed, 0
+        self.state = B.MOK_STATE_MXFP8 if eight_bit else B.MOK_STATE_F32
+        self.flags = B.MOK_ADAMW_STOCHASTIC if stochastic else 0
+        groups = {}
+        for q in params:
+            e, p = dict(q), q["p"]
+            n = p.numel()
+            for t in (p, q["g"], q.get("copy")):
+                if t is not None and (t.numel() != n or not t.is_contiguous()):
+                    raise ValueError("parameters, gradients and copies are packed and of one size")
+            u8 = dict(dtype=torch.uint8, device=p.device)
+            for k in ("m", "v"):
+                e[k] = torch.zeros(n, **(u8 if eight_bit else
+                                         dict(dtype=torch.float32, device=p.device)))
+                if eight_bit:
+                    e[k + "_scale"] = torch.zeros((n + 31) // 32, **u8)
+            groups.setdefault((p.dtype, q["g"].dtype), []).append(dict(e, n=n))
+        self.lists = [(types, B.make_adamw_list(g)) for types, g in groups.items()]
+
+    def step(self, grad_scale=None, stream=None):
+        self.t += 1
+        dt = lambda t: B.MOK_DTYPE_F32 if t == torch.float32 else B.MOK_DTYPE_BF16  # noqa: E731
+        for k, ((p, g), tensors) in enumerate(self.lists):
+            cfg = B.make_adamw(self.lr, *self.betas, self.eps, self.t,
+                               (self.seed + self.t * len(self.lists) + k) & (2 ** 64 - 1), dt(p),
+                               dt(g), self.state, self.flags)
+            B.check(B.mok_adamw_step(cfg, tensors, grad_scale, stream), "adamw")
