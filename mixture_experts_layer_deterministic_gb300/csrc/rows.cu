@@ -29,11 +29,13 @@ constexpr int COMBINE_BWD_U = 2;
 constexpr int DISPATCH_BLOCKS = 16;
 constexpr int COMBINE_BLOCKS = 4;
 
+// blocks for `items` work items, `per_block` of them a block: looping blocks, per_sm on each SM,
+// where there are at least four rounds of them; below that one block per share of the items
+// (1.7 rounds of looping blocks would run as two)
 inline unsigned grid_for(int64_t items, int per_block, int per_sm) {
     const int64_t cap = (int64_t)device_sm_count() * per_sm;
-    int64_t b = (items + per_block - 1) / per_block;
-    if (b > cap) b = cap;
-    return (unsigned)(b < 1 ? 1 : b);
+    const int64_t b = (items + per_block - 1) / per_block;
+    return (unsigned)(b < 1 ? 1 : b > 4 * cap ? cap : b);
 }
 
 // ---------------------------------------------------------------- row map
@@ -336,12 +338,21 @@ __global__ void __launch_bounds__(TPB)
             const int seg_of_tail = (H / PER) / (32 * U);
             if ((int)(it - t * segs) == seg_of_tail) {
                 float a = 0.f;
-                for (int k = 0; k < K; ++k) {
-                    const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
-                    const float s = __shfl_sync(0xFFFFFFFFu, wk, k);
-                    if (r >= 0 && c < H)
-                        a = fmaf(s, load_elem<F32>(static_cast<const uint8_t *>(rows) +
-                                                       r * ld_row * B, c), a);
+                for (int k0 = 0; k0 < K; k0 += 8) {  // 8 loads in flight
+                    float e[8], s[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int k = k0 + j < K ? k0 + j : K - 1;
+                        const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
+                        s[j] = __shfl_sync(0xFFFFFFFFu, wk, k);
+                        e[j] = 0.f;
+                        if (k0 + j < K && r >= 0 && c < H)
+                            e[j] = load_elem<F32>(
+                                static_cast<const uint8_t *>(rows) + r * ld_row * B, c);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (k0 + j < K) a = fmaf(s[j], e[j], a);
                 }
                 if (c < H)
                     store_elem<F32>(yp, c, a + (resp != nullptr ? load_elem<F32>(resp, c) : 0.f));
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(TPB)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool pads = starts != nullptr && drows != nullptr;
     const int rounds = (K + 7) / 8, per_round = (K + rounds - 1) / rounds;
-    const int tail = H / PER * PER;  // the columns from here are taken one a lane, by warp 0
+    const int tail = H / PER * PER;  // the columns from here are taken one a lane, by one warp
     const int64_t items = T + (pads ? (int64_t)E * 16 / WARPS : 0);
     for (int64_t t = blockIdx.x; t < items; t += gridDim.x) {
         if (t >= T) {
@@ -437,21 +448,27 @@ __global__ void __launch_bounds__(TPB)
                     }
                 }
             }
-            if (VEC && warp == 0 && tail < H) {
+            if (VEC && warp == WARPS - 1 && tail < H) {  // the warp with the least else to do
                 const int c = tail + lane;
                 const float g = c < H ? load_elem<F32>(dyp, c) : 0.f;
+                float e[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j >= kn) break;
+                    const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
+                    e[j] = 0.f;
+                    if (dw != nullptr && r >= 0 && c < H)
+                        e[j] = load_elem<F32>(static_cast<const uint8_t *>(rows) + r * ld_row * B,
+                                              c);
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     if (j >= kn) break;
                     const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
                     const float s = __shfl_sync(0xFFFFFFFFu, wk, k0 + j);
-                    if (r < 0 || c >= H) continue;
-                    if (drows != nullptr)
+                    if (drows != nullptr && r >= 0 && c < H)
                         store_elem<F32>(static_cast<uint8_t *>(drows) + r * ld_row * B, c, s * g);
-                    if (dw != nullptr)
-                        acc[j] = fmaf(
-                            load_elem<F32>(static_cast<const uint8_t *>(rows) + r * ld_row * B, c),
-                            g, acc[j]);
+                    acc[j] = fmaf(e[j], g, acc[j]);
                 }
             }
             if (dw != nullptr) {
