@@ -433,6 +433,7 @@ struct Fwd {
     int *status;
 
     MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
+    MOK_DEV void side_work(uint32_t, uint32_t, int) const {}
     MOK_DEV Unit unit(uint32_t u) const {
         const int4 t = tiles.get(u / (uint32_t)n_mb);
         return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0};
@@ -640,6 +641,7 @@ struct Dx {
     int *status;
 
     MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
+    MOK_DEV void side_work(uint32_t, uint32_t, int) const {}
     MOK_DEV Unit unit(uint32_t u) const {
         const int4 t = tiles.get(u / (uint32_t)n_mb);
         return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0};
@@ -703,7 +705,7 @@ struct DbArgs {
         const int64_t t1 = first != nullptr ? __ldg(first + g + 1) : tiles;
         const float *p = part + t0 * DZ_PARTS * N + n;
         float a = 0.f;
-#pragma unroll 8
+#pragma unroll 16
         for (int64_t k = 0; k < (t1 - t0) * DZ_PARTS; ++k) a += p[k * N];
         return a;
     }
@@ -725,6 +727,12 @@ struct Dw {
     DbArgs db;
 
     MOK_DEV int64_t n_units() const { return (int64_t)G * n_mb * n_nb; }
+    // a share of db, by the one warp of a pair that has nothing else to do
+    MOK_DEV void side_work(uint32_t cid, uint32_t ncl, int lane) const {
+        if (db.db == nullptr) return;
+        for (int64_t i = (int64_t)cid * 32 + lane; i < (int64_t)G * N; i += (int64_t)ncl * 32)
+            db.db[i] = db.sum((int)(i / N), (int)(i % N), N);
+    }
     MOK_DEV Unit unit(uint32_t u) const {
         const uint32_t per = (uint32_t)n_mb * (uint32_t)n_nb, rest = u % per;
         const int g = (int)(u / per);
@@ -761,10 +769,6 @@ struct Dw {
         const int nn = N - nb * 256 < 256 ? N - nb * 256 : 256;
         const bool any = u.nr > 0;
         const int i0 = mb * 256 + (int)rank * 128 + q * 32;
-        if (db.db != nullptr && mb == 0 && rank == 0) {  // one thread per feature of the block
-            const int n = (4 * hw + q) * 32 + lane;
-            if (n < nn) db.db[(int64_t)g * N + nb * 256 + n] = db.sum(g, nb * 256 + n, N);
-        }
         for (int n0 = 32 * hw; n0 < nn; n0 += E::STEP) {
             if constexpr (F32) {
                 float v[32];
@@ -896,6 +900,7 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (rank 0)
+        if (rank == 1) p.side_work(cid, ncl, lane);
         if (rank == 0 && tc::elect_one()) {
             // Descriptors of stage 0; a stage, and a K step of 16 elements, move only the address
             // (in 16-byte units). MN-major: 16 K rows are two groups of eight 128-byte rows,
@@ -1580,10 +1585,9 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     const bool direct = !act && !dy32;
     const uint16_t *dz = direct ? (const uint16_t *)dy : wk.dz;
     const int64_t ld_dz = direct ? c->ld_out : wk.ld_dz;
-    // The dW kernel adds the parts of db on the side, which saves a launch; with groups its
-    // epilogues are the bottleneck already (64 groups of 320 rows: dW 145 -> 168 us) and a
-    // launch of its own is shorter.
-    const bool db_in_dw = dw && !grouped(starts);
+    // The dW kernel adds the parts of db on the side, in the warps of the second SMs that issue no
+    // MMAs, which saves a launch; with few inputs that kernel would end before its side work.
+    const bool db_in_dw = dw && Kin >= 256;
     DbArgs dba{wk.part, grouped(starts) ? wk.first : nullptr, (c->rows + LTILE - 1) / LTILE, db};
     if (db || (!direct && (dx || dw))) {
         uint16_t *dzo = direct || (!dx && !dw) ? nullptr : wk.dz;
