@@ -1027,12 +1027,16 @@ __global__ void __launch_bounds__(P::E::THREADS, 1)
 }
 
 // ---------------------------------------------------------------- few rows
-// Up to 8 dense rows (a decoded token, a small batch): the weights' bytes are all the work, and
-// the tensor-core kernel's 256-row tiles put them on too few SMs (16 of 76 pairs for 4096
-// features). Here a warp takes 4 features and one of KS parts of the inputs, lanes side by
-// side on 16-byte pieces; fp32 products and sums, lanes added by a butterfly, parts in order.
-constexpr int SMALL_ROWS = 8;
-constexpr int SMALL_F = 2;  // features per warp
+// Up to 32 dense rows (a decoded token, a small batch): the weights' bytes are all the work, and
+// the 256-row tiles above put them on too few SMs (16 of 76 pairs for 4096 features). Here a
+// warp takes 16 features and one of `parts` parts of the inputs with mma.sync (m16n8k16; its rate
+// does not matter at 8 rows a weight), straight from registers: over 32 inputs a thread of a
+// quad loads 8 consecutive ones of two features and of a row, 16 bytes each, and the
+// instruction's K slots are assigned to inputs in that order, the same for both operands, since
+// a sum does not care. Parts are added in order through shared memory.
+constexpr int SMALL_ROWS = 32;
+constexpr int SMALL_F = 16;  // features of a warp
+
 
 struct SmallArgs {
     const uint16_t *x, *w, *res;
@@ -1043,35 +1047,125 @@ struct SmallArgs {
     int64_t ld_in, ld_w, ld_out;
 };
 
-// R rows (rows past a.rows repeat the last and are not stored), UN pieces a lane in flight
-template <int R, int UN, bool F32>
+MOK_DEV void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                       uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 inputs from column c of a row, zeros past Kin
+MOK_DEV uint4 load_piece(const uint16_t *row, int c, int Kin) {
+    if (c + 8 <= Kin) return ldg_nc_v4(row + c);
+    uint32_t e[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (c + j < Kin) e[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
+    return make_uint4(e[0], e[1], e[2], e[3]);
+}
+
+// NT groups of 8 rows (rows past a.rows repeat the last and are not stored), UN steps of 32 inputs
+// in flight
+template <int NT, int UN, bool F32>
 __global__ void __launch_bounds__(256)
     linear_small_kernel(const SmallArgs a) {
-    __shared__ float sh[8][SMALL_F * R];
+    __shared__ float sh[8][SMALL_F][8 * NT + 1];
     let_next_start();
     wait_for_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = warp % a.parts, slot = warp / a.parts;
     const int per_block = 8 / a.parts * SMALL_F;
     const int f0 = blockIdx.x * per_block + slot * SMALL_F;
-    const int nv = a.Kin / 8;
-    const uint16_t *wp[SMALL_F], *xp[R];
+    const int q = lane >> 2, t = lane & 3;
+    const uint16_t *w0 = a.w + (int64_t)(f0 + q < a.N ? f0 + q : a.N - 1) * a.ld_w;
+    const uint16_t *w1 = a.w + (int64_t)(f0 + q + 8 < a.N ? f0 + q + 8 : a.N - 1) * a.ld_w;
+    const uint16_t *xp[NT];
 #pragma unroll
-    for (int f = 0; f < SMALL_F; ++f)
-        wp[f] = a.w + (int64_t)(f0 + f < a.N ? f0 + f : a.N - 1) * a.ld_w;
+    for (int i = 0; i < NT; ++i)
+        xp[i] = a.x + (int64_t)(8 * i + q < a.rows ? 8 * i + q : a.rows - 1) * a.ld_in;
+    float acc[NT][4];
 #pragma unroll
-    for (int r = 0; r < R; ++r) xp[r] = a.x + (int64_t)(r < a.rows ? r : a.rows - 1) * a.ld_in;
-    float acc[SMALL_F][R];
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int f = 0; f < SMALL_F; ++f)
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int k0 = part * 32 * UN; k0 < a.Kin; k0 += a.parts * 32 * UN) {
+        uint4 wa[UN], wb[UN], xv[UN][NT];
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[f][r] = 0.f;
-    for (int v0 = part * 32 + lane; v0 < nv; v0 += a.parts * 32 * UN) {
-        uint4 wv[UN][SMALL_F];
+        for (int u = 0; u < UN; ++u) {
+            const int c = k0 + 32 * u + 8 * t;
+            wa[u] = load_piece(w0, c, a.Kin);
+            wb[u] = load_piece(w1, c, a.Kin);
+        }
 #pragma unroll
         for (int u = 0; u < UN; ++u)
 #pragma unroll
-            for (int f = 0; f < SMALL_F; ++f) {
+            for (int i = 0; i < NT; ++i) xv[u][i] = load_piece(xp[i], k0 + 32 * u + 8 * t, a.Kin);
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                mma_16816(acc[i], wa[u].x, wb[u].x, wa[u].y, wb[u].y, xv[u][i].x, xv[u][i].y);
+                mma_16816(acc[i], wa[u].z, wb[u].z, wa[u].w, wb[u].w, xv[u][i].z, xv[u][i].w);
+            }
+    }
+    // acc[i]: features q and q + 8 (second pair), rows 8 i + 2 t and the next
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sh[warp][q + 8 * (j >> 1)][8 * i + 2 * t + (j & 1)] = acc[i][j];
+    __syncthreads();
+    for (int o = threadIdx.x; o < per_block * a.rows; o += 256) {  // features side by side
+        const int r = o / per_block, fb = o % per_block;
+        const int f = blockIdx.x * per_block + fb;
+        if (f >= a.N) continue;
+        float v = 0.f;
+        for (int k = 0; k < a.parts; ++k) v += sh[fb / SMALL_F * a.parts + k][fb % SMALL_F][r];
+        if (a.bias != nullptr) v += a.bias[f];
+        const int64_t at = r * a.ld_out + f;
+        if (a.z != nullptr) a.z[at] = f32_to_bf16(v);
+        with_act(a.act, [&](auto act) { v = act_f<act.value>(v); });
+        if (a.res != nullptr) v += bf16_to_f32(a.res[at]);
+        st_val(a.y, at, v, F32);
+    }
+}
+
+// One or two rows of up to 8192 features: half the features a warp, whole rows of W side by side
+// on the lanes, products on the fp32 units. Four times as many warps start on a narrow layer
+// (one row, 4096 inputs: 512 features 2.2 against 4.5 us, 4096 features 5.5 against 6.5 us),
+// where a wide one has enough of them (14336 features 32 against 18 us).
+constexpr int VEC_F = 2;  // features of a warp
+
+// UN pieces a lane in flight
+template <int R, int UN, bool F32>
+__global__ void __launch_bounds__(256)
+    linear_vector_kernel(const SmallArgs a) {
+    __shared__ float sh[8][VEC_F * R];
+    let_next_start();
+    wait_for_previous();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = warp % a.parts, slot = warp / a.parts;
+    const int per_block = 8 / a.parts * VEC_F;
+    const int f0 = blockIdx.x * per_block + slot * VEC_F;
+    const int nv = a.Kin / 8;
+    const uint16_t *wp[VEC_F], *xp[R];
+#pragma unroll
+    for (int f = 0; f < VEC_F; ++f)
+        wp[f] = a.w + (int64_t)(f0 + f < a.N ? f0 + f : a.N - 1) * a.ld_w;
+#pragma unroll
+    for (int r = 0; r < R; ++r) xp[r] = a.x + (int64_t)(r < a.rows ? r : a.rows - 1) * a.ld_in;
+    float acc[VEC_F][R];
+#pragma unroll
+    for (int f = 0; f < VEC_F; ++f)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[f][r] = 0.f;
+    for (int v0 = part * 32 + lane; v0 < nv; v0 += a.parts * 32 * UN) {
+        uint4 wv[UN][VEC_F];
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int f = 0; f < VEC_F; ++f) {
                 const int v = v0 + u * a.parts * 32;
                 wv[u][f] = make_uint4(0, 0, 0, 0);
                 if (v < nv) wv[u][f] = ldg_nc_v4(wp[f] + (int64_t)v * 8);
@@ -1092,7 +1186,7 @@ __global__ void __launch_bounds__(256)
                 }
             }
 #pragma unroll
-            for (int f = 0; f < SMALL_F; ++f) {
+            for (int f = 0; f < VEC_F; ++f) {
                 const uint32_t e[4] = {wv[u][f].x, wv[u][f].y, wv[u][f].z, wv[u][f].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -1108,14 +1202,14 @@ __global__ void __launch_bounds__(256)
         const int c = nv * 8 + lane;
         if (c < a.Kin) {
 #pragma unroll
-            for (int f = 0; f < SMALL_F; ++f)
+            for (int f = 0; f < VEC_F; ++f)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
                     acc[f][r] = fmaf(bf16_to_f32(wp[f][c]), bf16_to_f32(xp[r][c]), acc[f][r]);
         }
     }
 #pragma unroll
-    for (int f = 0; f < SMALL_F; ++f)
+    for (int f = 0; f < VEC_F; ++f)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float v = acc[f][r];
@@ -1132,7 +1226,7 @@ __global__ void __launch_bounds__(256)
     if (f >= a.N || r >= a.rows) return;
     float v = 0.f;
     for (int k = 0; k < a.parts; ++k)
-        v += sh[fb / SMALL_F * a.parts + k][fb % SMALL_F * R + r];
+        v += sh[fb / VEC_F * a.parts + k][fb % VEC_F * R + r];
     if (a.bias != nullptr) v += a.bias[f];
     const int64_t o = r * a.ld_out + f;
     if (a.z != nullptr) a.z[o] = f32_to_bf16(v);
@@ -1347,19 +1441,29 @@ cudaError_t launch_dz(int act, dim3 grid, const void *dy, const uint16_t *z, con
     return cudaErrorInvalidValue;
 }
 
+// whether a dense call of this size goes to the kernels for few rows: up to 8 rows, and up to 32
+// on layers of up to 8192 features (4096 inputs, 32 rows: 4096 features 12 against 16 us on tiles,
+// 14336 features 33 against 23 us)
+bool few_rows(int64_t rows, int64_t N) { return rows <= 8 || (rows <= SMALL_ROWS && N <= 8192); }
+
 template <bool F32>
 cudaError_t launch_small(SmallArgs a, cudaStream_t s) {
-    // as few parts as give two blocks an SM: a part fewer is a block of more features, which
-    // reads x less often
+    const bool vec = a.rows <= 2 && a.N <= 8192;
+    const int per_warp = vec ? VEC_F : SMALL_F;
+    // a warp's features in more parts until there are two blocks an SM, each part keeping a few
+    // steps
     a.parts = 1;
-    while (a.parts < 8 && (int64_t)a.N * a.parts < (int64_t)2 * device_sm_count() * 8 * SMALL_F)
+    while (a.parts < 8 && a.Kin / a.parts >= 256 &&
+           (int64_t)a.N * a.parts < (int64_t)2 * device_sm_count() * 8 * per_warp)
         a.parts *= 2;
-    const int per_block = 8 / a.parts * SMALL_F;
+    const int per_block = 8 / a.parts * per_warp;
     const unsigned grid = (unsigned)((a.N + per_block - 1) / per_block);
-    if (a.rows == 1) return launch_edge(linear_small_kernel<1, 4, F32>, grid, 256, 0, 1, s, a);
-    if (a.rows == 2) return launch_edge(linear_small_kernel<2, 4, F32>, grid, 256, 0, 1, s, a);
-    if (a.rows <= 4) return launch_edge(linear_small_kernel<4, 2, F32>, grid, 256, 0, 1, s, a);
-    return launch_edge(linear_small_kernel<8, 2, F32>, grid, 256, 0, 1, s, a);
+    if (vec && a.rows == 1)
+        return launch_edge(linear_vector_kernel<1, 4, F32>, grid, 256, 0, 1, s, a);
+    if (vec) return launch_edge(linear_vector_kernel<2, 4, F32>, grid, 256, 0, 1, s, a);
+    if (a.rows <= 8) return launch_edge(linear_small_kernel<1, 4, F32>, grid, 256, 0, 1, s, a);
+    if (a.rows <= 16) return launch_edge(linear_small_kernel<2, 4, F32>, grid, 256, 0, 1, s, a);
+    return launch_edge(linear_small_kernel<4, 2, F32>, grid, 256, 0, 1, s, a);
 }
 
 bool grouped(const int32_t *starts) { return starts != nullptr; }
@@ -1504,7 +1608,7 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
     const void *ps[] = {x, w, bias, residual, starts, counts, y, z};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    if (!grouped(starts) && c->rows <= SMALL_ROWS) {
+    if (!grouped(starts) && few_rows(c->rows, c->out_features)) {
         const SmallArgs a{(const uint16_t *)x, (const uint16_t *)w, (const uint16_t *)residual, bias,
                           y, (uint16_t *)z, c->in_features, c->out_features, (int)c->rows, c->act,
                           1, c->ld_in, c->ld_w, c->ld_out};

@@ -231,6 +231,13 @@ CASES = [
     dict(R=1, Kin=4096, N=513, act="silu"),
     dict(R=3, Kin=72, N=8, act="relu", bias=False),
     dict(R=8, Kin=1000, N=40, out="fp32"),
+    dict(R=2, Kin=515, N=130, act="gelu", out="fp32"),
+    dict(R=5, Kin=2050, N=300, act="silu"),
+    dict(R=2, Kin=72, N=8200),
+    dict(R=14, Kin=1301, N=77, act="gelu_tanh", extra=8),
+    dict(R=27, Kin=640, N=600, act="relu", out="fp32"),
+    dict(R=40, Kin=2100, N=300, out="fp32", res=False, z=False),
+    dict(R=5000, Kin=300, N=2600, act="silu"),
     dict(R=17, Kin=15, N=300, act="gelu"),
     dict(R=33, Kin=264, N=1030, act="gelu_tanh", extra=8),
     dict(R=255, Kin=129, N=127, act="silu", res=False),
