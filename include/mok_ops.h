@@ -70,7 +70,7 @@ mok_status mok_dispatch_backward(const mok_rows_config *cfg, const void *dxs,
 
 /* y[t] = residual[t] + sum over k, in order, of topk_w[t][k] * rows[row_map[t*K + k]], in fp32,
  * rounded once. topk_w fp32 [T][K], or NULL for weights of one; residual NULL or [T] rows
- * (may be y itself). */
+ * (may be y itself). rows must not overlap y. */
 mok_status mok_combine(const mok_rows_config *cfg, const void *rows, const int32_t *row_map,
                        const float *topk_w, const void *residual, void *y,
                        cudaStream_t stream);
@@ -104,7 +104,8 @@ mok_status mok_combine_backward(const mok_rows_config *cfg, const void *dy, cons
  * z^3))); gelu 0.5 z (1 + erf(z / sqrt 2)).
  *
  * Limits: 1 <= groups <= 1024, 1 <= in_features, out_features <= 2^20 (any number, odd ones
- * among them), 0 <= rows < 2^31 - 512; strides ld_in >= in, ld_w >= in, ld_out >= out are
+ * among them), 0 <= rows < 2^31 - 512, fewer than 2^31 blocks of 16 rows x 256 columns in an
+ * output (x, y or all of dW); strides ld_in >= in, ld_w >= in, ld_out >= out are
  * multiples of 8 elements. Columns past a matrix's width are neither read nor written. */
 typedef enum mok_activation {
     MOK_ACT_NONE = 0,

@@ -789,8 +789,7 @@ struct Dw {
 
 // Arrive on a barrier of either CTA of the pair. CTA scope: what the barrier hands over lives in
 // TMEM, ordered by the tcgen05 fences. Cluster scope made the arriving thread wait for its
-// global stores to land, about 2 us a unit (dW of 64 x 1024 x 4096: 208 us instead of what the
-// DESIGN table shows).
+// global stores to land, about 2 us a unit (dW of 64 x 1024 x 4096: 208 against 164 us).
 MOK_DEV void lin_arrive(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
                  : "memory");
@@ -1248,16 +1247,18 @@ __global__ void __launch_bounds__(256)
     __shared__ float red[32][65];
     let_next_start();
     wait_for_previous();
-    const int64_t t = blockIdx.x / DZ_PARTS;
+    // column blocks first: neighbours in time read neighbouring parts of the same rows
+    const uint32_t ncb = (uint32_t)(N + 63) / 64, part_id = blockIdx.x / ncb, cb = blockIdx.x % ncb;
+    const int64_t t = part_id / DZ_PARTS;
     if (t >= tiles.count()) return;
     const int4 tile = tiles.get(t);
     // the tile in equal parts, multiples of 16 rows; the last takes the padding
     const int per = ((tile.z - tile.y + DZ_PARTS - 1) / DZ_PARTS + 15) & ~15;
-    const int64_t r0 = tile.y + (int64_t)(blockIdx.x % DZ_PARTS) * per;
+    const int64_t r0 = tile.y + (int64_t)(part_id % DZ_PARTS) * per;
     const int64_t all = tile.w != 0 ? (tile.z + 15) & ~15 : tile.z;  // one past the rows to write
     const int64_t rend = r0 + per < all ? r0 + per : all, r1 = rend < tile.z ? rend : tile.z;
     const int cv = threadIdx.x & 7, rl = threadIdx.x >> 3;
-    const int c = blockIdx.y * 64 + cv * 8;
+    const int c = (int)cb * 64 + cv * 8;
     constexpr int NR = DZ_ROWS / 32;
     const bool whole = c + 8 <= N;
     uint4 a[NR], a2[NR], q[NR];  // dy (fp32: two vectors), z
@@ -1320,11 +1321,11 @@ __global__ void __launch_bounds__(256)
     for (int j = 0; j < 8; ++j) red[rl][cv * 8 + j] = sum[j];
     __syncthreads();
     if (threadIdx.x < 64) {
-        const int col = blockIdx.y * 64 + threadIdx.x;
+        const int col = (int)cb * 64 + threadIdx.x;
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
-        if (col < N) part[(int64_t)blockIdx.x * N + col] = s;
+        if (col < N) part[(int64_t)part_id * N + col] = s;
     }
 }
 
@@ -1582,6 +1583,12 @@ mok_status mok_check_linear_config(const mok_linear_config *c) {
     const int32_t widths[] = {c->in_features, c->in_features, c->out_features};
     for (int i = 0; i < 3; ++i)
         if (lds[i] < widths[i] || lds[i] % 8 != 0 || lds[i] > far) return MOK_ERR_INVALID_ARG;
+    // units of the products and blocks of the dz kernel are numbered in 31 bits
+    const int64_t G = c->groups, kb = (c->in_features + 255) / 256, nb = (c->out_features + 255) / 256;
+    const int64_t tiles = c->rows / 16 + G + 1, limit = 0x7FFFFFFF;
+    if (tiles * (kb > nb ? kb : nb) > limit || G * kb * nb > limit ||
+        (c->rows / DZ_ROWS + 2 * G + 4) * ((c->out_features + 63) / 64) > limit)
+        return MOK_ERR_INVALID_ARG;
     if (c->act < MOK_ACT_NONE || c->act > MOK_ACT_GELU || c->reserved != 0)
         return MOK_ERR_INVALID_ARG;
     const int32_t dts[] = {c->out_dtype, c->grad_dtype};
@@ -1699,7 +1706,8 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
         // dz has tiles of its own: full ones, whatever the products take
         const Tiles dzt = grouped(starts) ? tiles
                                           : Tiles{nullptr, (c->rows + LTILE - 1) / LTILE, c->rows, LTILE};
-        const dim3 grid((unsigned)(dzt.cap * DZ_PARTS), (unsigned)((N + 63) / 64));
+        const int64_t blocks = dzt.cap * DZ_PARTS * ((N + 63) / 64);
+        const dim3 grid((unsigned)blocks);
         MOK_OP_LAUNCH(OP_LINEAR_DZ, 1,
                       dy32 ? launch_dz<true>(c->act, grid, dy, (const uint16_t *)z, dzt, N,
                                              c->ld_out, dzo, ld_dz, part, stream)
@@ -1720,7 +1728,6 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     const int n_nb = (N + 255) / 256;
     const int64_t x_units = dx ? tiles.cap * n_kb : 0;
     const int64_t w_units = dw ? (int64_t)G * n_kb * n_nb : 0;
-    if (x_units > 0x7FFFFFFF || w_units > 0x7FFFFFFF) return MOK_ERR_INVALID_ARG;
     const int32_t *valid = grouped(starts) ? wk.valid : nullptr;
     int64_t split = 0, pairs = 0;  // pairs of SMs for dW, and in all, where both go in one launch
     if (dx && dw && !grouped(starts))

@@ -8,6 +8,8 @@
 // All of it is HBM traffic of R = T*K rows; every token row is touched once. Work is cut by
 // token and by column segment, so a row is read or written by whole warps, 16 bytes a lane.
 // Sums over k run in ascending k in fp32; dot products over H in a fixed tree: no atomics.
+#include <type_traits>
+
 #include "common.cuh"
 #include "ops_internal.h"
 
@@ -108,18 +110,21 @@ __global__ void __launch_bounds__(MAX_E)
 // strides do not keep rows 16-byte aligned.
 template <bool F32>
 struct Elem {
+    using Raw = typename std::conditional<F32, uint32_t, uint16_t>::type;
     static constexpr int BYTES = F32 ? 4 : 2;
     static constexpr int PER = 16 / BYTES;  // elements of a 16-byte vector
 };
 
 // the routed row of id f: a valid row index, or -1 (an index at or past n_rows is reported)
-MOK_DEV int32_t row_of(const int32_t *__restrict__ map, int64_t f, int64_t n_rows, int *status) {
-    int32_t r = map[f];
+MOK_DEV int32_t checked_row(int32_t r, int64_t n_rows, int *status) {
     if (r >= n_rows) {
         raise_status(status, MOK_ERR_DEVICE_INVARIANT);
         r = -1;
     }
     return r;
+}
+MOK_DEV int32_t row_of(const int32_t *__restrict__ map, int64_t f, int64_t n_rows, int *status) {
+    return checked_row(map[f], n_rows, status);
 }
 
 template <bool F32>
@@ -202,15 +207,16 @@ __global__ void __launch_bounds__(TPB)
         const int v0 = (int)(it % segs) * 32 * U + lane;
         const int32_t rk = lane < K ? row_of(map, t * K + lane, n_rows, status) : -1;
         const uint8_t *src = static_cast<const uint8_t *>(x) + t * ld_tok * B;
+        using Raw = typename Elem<F32>::Raw;  // elements are copied bit for bit
         if (VEC) {
             uint4 b[U];
-            float tail = 0.f;  // the columns past the last whole vector, at most PER - 1
+            Raw tail = 0;  // the columns past the last whole vector, at most PER - 1
             const int tc = nv * PER + lane;
             const bool has_tail = v0 - lane + 32 * U > nv && tc < H;
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (v0 + 32 * j < nv) b[j] = ldg_nc_v4(src + (int64_t)(v0 + 32 * j) * 16);
-            if (has_tail) tail = load_elem<F32>(src, tc);
+            if (has_tail) tail = reinterpret_cast<const Raw *>(src)[tc];
             for (int k = 0; k < K; ++k) {
                 const int64_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
                 if (r < 0) continue;
@@ -218,20 +224,20 @@ __global__ void __launch_bounds__(TPB)
 #pragma unroll
                 for (int j = 0; j < U; ++j)
                     if (v0 + 32 * j < nv) reinterpret_cast<uint4 *>(dst)[v0 + 32 * j] = b[j];
-                if (has_tail) store_elem<F32>(dst, tc, tail);
+                if (has_tail) reinterpret_cast<Raw *>(dst)[tc] = tail;
             }
         } else {
-            float b[U];
+            Raw b[U];
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                if (v0 + 32 * j < nv) b[j] = load_elem<F32>(src, v0 + 32 * j);
+                if (v0 + 32 * j < nv) b[j] = reinterpret_cast<const Raw *>(src)[v0 + 32 * j];
             for (int k = 0; k < K; ++k) {
                 const int64_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
                 if (r < 0) continue;
-                uint8_t *dst = static_cast<uint8_t *>(xs) + r * ld_row * B;
+                Raw *dst = reinterpret_cast<Raw *>(static_cast<uint8_t *>(xs) + r * ld_row * B);
 #pragma unroll
                 for (int j = 0; j < U; ++j)
-                    if (v0 + 32 * j < nv) store_elem<F32>(dst, v0 + 32 * j, b[j]);
+                    if (v0 + 32 * j < nv) dst[v0 + 32 * j] = b[j];
             }
         }
     }
@@ -275,11 +281,27 @@ __global__ void __launch_bounds__(TPB)
     const int rounds = (K + 7) / 8, per_round = (K + rounds - 1) / rounds;
     const int64_t items = T * segs;
     const int64_t nw = (int64_t)gridDim.x * WARPS;
-    for (int64_t it = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); it < items; it += nw) {
+    // row and weight of copy `lane` of item i's token; the next item's are fetched while this one's
+    // rows are on their way
+    const auto fetch = [&](int64_t i, int32_t &r, float &v) {
+        r = -1;
+        v = 0.f;
+        if (i < items && lane < K) {
+            const int64_t f = (segs == 1 ? i : i / segs) * K + lane;
+            r = map[f];
+            v = w != nullptr ? w[f] : 1.0f;
+        }
+    };
+    int64_t it = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
+    int32_t next_r;
+    float next_w;
+    fetch(it, next_r, next_w);
+    for (; it < items; it += nw) {
+        const int32_t rk = checked_row(next_r, n_rows, status);
+        const float wk = rk >= 0 ? next_w : 0.f;
+        fetch(it + nw, next_r, next_w);
         const int64_t t = segs == 1 ? it : it / segs;
         const int c0 = ((int)(it - t * segs) * 32 * U + lane) * PER;  // first column, step 32 PER
-        const int32_t rk = lane < K ? row_of(map, t * K + lane, n_rows, status) : -1;
-        const float wk = rk >= 0 ? (w != nullptr ? w[t * K + lane] : 1.0f) : 0.f;
         float acc[U][PER];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -382,14 +404,27 @@ __global__ void __launch_bounds__(TPB)
     const int rounds = (K + 7) / 8, per_round = (K + rounds - 1) / rounds;
     const int tail = H / PER * PER;  // the columns from here are taken one a lane, by one warp
     const int64_t items = T + (pads ? (int64_t)E * 16 / WARPS : 0);
+    // row and weight of copy `lane` of token i, the next token's ahead of time
+    const auto fetch = [&](int64_t i, int32_t &r, float &v) {
+        r = -1;
+        v = 0.f;
+        if (i < T && lane < K) {
+            r = map[i * K + lane];
+            v = w != nullptr ? w[i * K + lane] : 1.0f;
+        }
+    };
+    int32_t next_r;
+    float next_w;
+    fetch(blockIdx.x, next_r, next_w);
     for (int64_t t = blockIdx.x; t < items; t += gridDim.x) {
+        const int32_t rk = checked_row(next_r, n_rows, status);
+        const float wk = rk >= 0 ? next_w : 0.f;
+        fetch(t + gridDim.x, next_r, next_w);
         if (t >= T) {
             zero_pad_row<F32, VEC>((t - T) * WARPS + warp, starts, kept, n_rows, H, ld_row, drows,
                                    lane);
             continue;
         }
-        const int32_t rk = lane < K ? row_of(map, t * K + lane, n_rows, status) : -1;
-        const float wk = rk >= 0 ? (w != nullptr ? w[t * K + lane] : 1.0f) : 0.f;
         const uint8_t *dyp = static_cast<const uint8_t *>(dy) + t * ld_tok * B;
         for (int k0 = 0; k0 < K; k0 += per_round) {
             const int kn = K - k0 < per_round ? K - k0 : per_round;
@@ -511,11 +546,191 @@ __global__ void __launch_bounds__(TPB)
     }
 }
 
+// ---------------------------------------------------------------- narrow rows
+// Rows of at most 32 pieces (a piece is 16 bytes, or one element where rows are not aligned): a
+// warp a row would leave most of its lanes idle, so a row gets a group of 2^sh lanes, the least
+// power of two that covers its pieces, and a warp holds 32 / 2^sh rows.
+template <bool F32, bool VEC>
+MOK_DEV void get_piece(const void *p, int64_t row, int64_t ld, int c, int H,
+                       float (&v)[VEC ? Elem<F32>::PER : 1]) {
+    constexpr int PER = VEC ? Elem<F32>::PER : 1;
+    const uint8_t *r = static_cast<const uint8_t *>(p) + row * ld * Elem<F32>::BYTES;
+    if constexpr (VEC) {
+        if (c + PER <= H) {
+            unpack<F32>(*reinterpret_cast<const uint4 *>(r + (int64_t)c * Elem<F32>::BYTES), v);
+            return;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q) v[q] = c + q < H ? load_elem<F32>(r, c + q) : 0.f;
+}
+template <bool F32, bool VEC>
+MOK_DEV void put_piece(void *p, int64_t row, int64_t ld, int c, int H,
+                       const float (&v)[VEC ? Elem<F32>::PER : 1]) {
+    constexpr int PER = VEC ? Elem<F32>::PER : 1;
+    uint8_t *r = static_cast<uint8_t *>(p) + row * ld * Elem<F32>::BYTES;
+    if constexpr (VEC) {
+        if (c + PER <= H) {
+            *reinterpret_cast<uint4 *>(r + (int64_t)c * Elem<F32>::BYTES) = pack<F32>(v);
+            return;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+        if (c + q < H) store_elem<F32>(r, c + q, v[q]);
+}
+
+// a piece as it is, bit for bit
+template <bool F32, bool VEC>
+MOK_DEV void copy_piece(const void *src, int64_t from, int64_t ld_src, void *dst, int64_t to,
+                        int64_t ld_dst, int c, int H) {
+    constexpr int PER = VEC ? Elem<F32>::PER : 1, B = Elem<F32>::BYTES;
+    const uint8_t *a = static_cast<const uint8_t *>(src) + (from * ld_src + c) * B;
+    uint8_t *b = static_cast<uint8_t *>(dst) + (to * ld_dst + c) * B;
+    if constexpr (VEC) {
+        if (c + PER <= H) {
+            *reinterpret_cast<uint4 *>(b) = *reinterpret_cast<const uint4 *>(a);
+            return;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        if (c + q >= H) continue;
+        if (F32)
+            reinterpret_cast<uint32_t *>(b)[q] = reinterpret_cast<const uint32_t *>(a)[q];
+        else
+            reinterpret_cast<uint16_t *>(b)[q] = reinterpret_cast<const uint16_t *>(a)[q];
+    }
+}
+
+// the pad row of item i (see zero_pad_row), one piece
+template <bool F32, bool VEC>
+MOK_DEV void zero_pad_piece(int64_t item, const int32_t *starts, const int32_t *kept,
+                            int64_t n_rows, int c, int H, int64_t ld, void *out) {
+    const int e = (int)(item >> 4), j = (int)(item & 15);
+    const int64_t n = kept[e], row = starts[e] + n + j;
+    if (n + j >= ((n + 15) & ~(int64_t)15) || row < 0 || row >= n_rows) return;
+    float z[VEC ? Elem<F32>::PER : 1] = {};
+    put_piece<F32, VEC>(out, row, ld, c, H, z);
+}
+
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(TPB)
+    dispatch_narrow_kernel(const void *__restrict__ x, const int32_t *__restrict__ map,
+                           const int32_t *__restrict__ starts, const int32_t *__restrict__ kept,
+                           int64_t T, int K, int E, int H, int sh, int64_t ld_tok, int64_t ld_row,
+                           int64_t n_rows, void *__restrict__ xs, int *status) {
+    constexpr int PER = VEC ? Elem<F32>::PER : 1;
+    const int64_t i = (int64_t)blockIdx.x * TPB + threadIdx.x, f = i >> sh;
+    const int c = (int)(i & ((1 << sh) - 1)) * PER;
+    const int64_t R = T * K;
+    if (c >= H) return;
+    if (f >= R) {
+        if (starts != nullptr && f - R < (int64_t)E * 16)
+            zero_pad_piece<F32, VEC>(f - R, starts, kept, n_rows, c, H, ld_row, xs);
+        return;
+    }
+    const int32_t r = row_of(map, f, n_rows, status);
+    if (r < 0) return;
+    copy_piece<F32, VEC>(x, (uint32_t)f / (uint32_t)K, ld_tok, xs, r, ld_row, c, H);
+}
+
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(TPB)
+    combine_narrow_kernel(const void *__restrict__ rows, const int32_t *__restrict__ map,
+                          const float *__restrict__ w, const void *res, int64_t T, int K, int H,
+                          int sh, int64_t ld_tok, int64_t ld_row, int64_t n_rows, void *y,
+                          int *status) {
+    constexpr int PER = VEC ? Elem<F32>::PER : 1;
+    const int64_t i = (int64_t)blockIdx.x * TPB + threadIdx.x, t = i >> sh;
+    const int c = (int)(i & ((1 << sh) - 1)) * PER;
+    if (t >= T || c >= H) return;
+    float acc[PER] = {};
+    for (int k0 = 0; k0 < K; k0 += 4) {  // 4 rows in flight
+        float v[4][PER], s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int32_t r = k0 + j < K ? row_of(map, t * K + k0 + j, n_rows, status) : -1;
+            s[j] = r >= 0 ? (w != nullptr ? w[t * K + k0 + j] : 1.0f) : 0.f;
+            if (r >= 0) {
+                get_piece<F32, VEC>(rows, r, ld_row, c, H, v[j]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < PER; ++q) v[j][q] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int q = 0; q < PER; ++q) acc[q] = fmaf(s[j], v[j][q], acc[q]);
+    }
+    if (res != nullptr) {
+        float v[PER];
+        get_piece<F32, VEC>(res, t, ld_tok, c, H, v);
+#pragma unroll
+        for (int q = 0; q < PER; ++q) acc[q] += v[q];
+    }
+    put_piece<F32, VEC>(y, t, ld_tok, c, H, acc);
+}
+
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(TPB)
+    combine_bwd_narrow_kernel(const void *__restrict__ dy, const void *__restrict__ rows,
+                              const int32_t *__restrict__ map,
+                              const int32_t *__restrict__ starts,
+                              const int32_t *__restrict__ kept, const float *__restrict__ w,
+                              int64_t T, int K, int E, int H, int sh, int64_t ld_tok,
+                              int64_t ld_row, int64_t n_rows, void *__restrict__ drows,
+                              float *__restrict__ dw, int *status) {
+    constexpr int PER = VEC ? Elem<F32>::PER : 1;
+    const int64_t i = (int64_t)blockIdx.x * TPB + threadIdx.x, f = i >> sh;
+    const int v0 = (int)(i & ((1 << sh) - 1)), c = v0 * PER;
+    const int64_t R = T * K;
+    float dot = 0.f;
+    if (f < R && c < H) {
+        const int32_t r = row_of(map, f, n_rows, status);
+        if (r >= 0) {
+            float g[PER];
+            get_piece<F32, VEC>(dy, (uint32_t)f / (uint32_t)K, ld_tok, c, H, g);
+            if (dw != nullptr) {
+                float v[PER];
+                get_piece<F32, VEC>(rows, r, ld_row, c, H, v);
+#pragma unroll
+                for (int q = 0; q < PER; ++q) dot = fmaf(v[q], g[q], dot);
+            }
+            if (drows != nullptr) {
+                const float s = w != nullptr ? w[f] : 1.0f;
+#pragma unroll
+                for (int q = 0; q < PER; ++q) g[q] *= s;
+                put_piece<F32, VEC>(drows, r, ld_row, c, H, g);
+            }
+        }
+    } else if (f >= R && f - R < (int64_t)E * 16 && c < H && starts != nullptr &&
+               drows != nullptr) {
+        zero_pad_piece<F32, VEC>(f - R, starts, kept, n_rows, c, H, ld_row, drows);
+    }
+    if (dw != nullptr) {  // the group's lanes, all of the warp taking part
+        for (int o = (1 << sh) >> 1; o > 0; o >>= 1)
+            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+        if (v0 == 0 && f < R) dw[f] = dot;
+    }
+}
+
 // rows start on 16-byte boundaries: both strides are multiples of 16 bytes
 bool vectors(const mok_rows_config &c) {
     const int per = c.dtype == MOK_DTYPE_F32 ? 4 : 8;
     return c.ld_tok % per == 0 && c.ld_row % per == 0;
 }
+
+// lanes of a narrow row's group, as a shift; -1 for rows of more than 32 pieces
+int narrow_shift(const mok_rows_config &c) {
+    const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
+    const int pieces = (c.H + per - 1) / per;
+    int sh = 0;
+    while ((1 << sh) < pieces && sh < 6) ++sh;
+    return sh <= 5 ? sh : -1;
+}
+int64_t narrow_blocks(int64_t items, int sh) { return ((items << sh) + TPB - 1) / TPB; }
 
 }  // namespace
 
@@ -550,6 +765,18 @@ cudaError_t launch_dispatch_rows(const mok_rows_config &c, const void *x, const 
     const int64_t segs = (c.H + per * 32 * U - 1) / (per * 32 * U);
     const int64_t items = c.T * segs + (starts != nullptr ? (int64_t)c.E * 16 : 0);
     if (items == 0) return cudaSuccess;
+    if (const int sh = narrow_shift(c); sh >= 0) {
+        const int64_t rows = (int64_t)c.T * c.K + (starts != nullptr ? (int64_t)c.E * 16 : 0);
+        const int64_t blocks = narrow_blocks(rows, sh);
+        if (blocks <= 0x7FFFFFFF) {
+#define CALL(F, V)                                                                          \
+    dispatch_narrow_kernel<F, V><<<(unsigned)blocks, TPB, 0, s>>>(                          \
+        x, map, starts, kept, c.T, c.K, c.E, c.H, sh, c.ld_tok, c.ld_row, c.n_rows, xs, status)
+            MOK_ROWS_CASES(c, CALL);
+#undef CALL
+            return cudaGetLastError();
+        }
+    }
 #define CALL(F, V)                                                                        \
     dispatch_kernel<F, V, U><<<grid_for(items, WARPS, DISPATCH_BLOCKS), TPB, 0, s>>>(                  \
         x, map, starts, kept, c.T, c.K, c.E, c.H, c.ld_tok, c.ld_row, c.n_rows, xs, status)
@@ -563,6 +790,17 @@ cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, cons
                                 cudaStream_t s) {
     if (c.T == 0) return cudaSuccess;
     const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
+    if (const int sh = narrow_shift(c); sh >= 0) {
+        const int64_t blocks = narrow_blocks(c.T, sh);
+        if (blocks <= 0x7FFFFFFF) {
+#define CALL(F, V)                                                               \
+    combine_narrow_kernel<F, V><<<(unsigned)blocks, TPB, 0, s>>>(                \
+        rows, map, w, res, c.T, c.K, c.H, sh, c.ld_tok, c.ld_row, c.n_rows, y, status)
+            MOK_ROWS_CASES(c, CALL);
+#undef CALL
+            return cudaGetLastError();
+        }
+    }
     constexpr int U = COMBINE_U;
     const int64_t items = (int64_t)c.T * ((c.H + per * 32 * U - 1) / (per * 32 * U));
 #define CALL(F, V)                                                                       \
@@ -579,6 +817,20 @@ cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const v
                                cudaStream_t s) {
     const int64_t items = c.T + (starts != nullptr && drows != nullptr ? (int64_t)c.E * 2 : 0);
     if (items == 0) return cudaSuccess;
+    if (const int sh = narrow_shift(c); sh >= 0) {
+        const bool pads = starts != nullptr && drows != nullptr;
+        const int64_t n = (int64_t)c.T * c.K + (pads ? (int64_t)c.E * 16 : 0);
+        const int64_t blocks = narrow_blocks(n, sh);
+        if (blocks <= 0x7FFFFFFF) {
+#define CALL(F, V)                                                                            \
+    combine_bwd_narrow_kernel<F, V><<<(unsigned)blocks, TPB, 0, s>>>(                         \
+        dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, sh, c.ld_tok, c.ld_row, c.n_rows, \
+        drows, dw, status)
+            MOK_ROWS_CASES(c, CALL);
+#undef CALL
+            return cudaGetLastError();
+        }
+    }
 #define CALL(F, V)                                                                         \
     combine_bwd_kernel<F, V, COMBINE_BWD_U><<<grid_for(items, 1, COMBINE_BLOCKS), TPB, 0, s>>>( \
         dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, c.ld_tok, c.ld_row, c.n_rows,  \

@@ -108,6 +108,10 @@ CASES = [
     dict(T=64, K=2, E=9, H=100, dtype="fp32", ld_extra=3),
     dict(T=64, K=4, E=9, H=130, ld_extra=1),
     dict(T=90, K=4, E=8, H=264, hot=True),
+    dict(T=700, K=5, E=30, H=44, capacity=90, spare=8),
+    dict(T=130, K=3, E=5, H=31, ld_extra=1),
+    dict(T=130, K=3, E=5, H=250, hot=True),
+    dict(T=75, K=9, E=12, H=127, dtype="fp32"),
     dict(T=90, K=4, E=8, H=520, capacity=1),
     dict(T=300, K=8, E=64, H=2056, capacity=17, spare=40),
 ]
@@ -251,6 +255,20 @@ def test_side_stream_and_repeat():
         outs.append([t[..., :c.H] if t.dim() == 2 else t for t in (xs, y, drows, dw)])
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("H,extra", [(64, 0), (61, 0), (61, 1), (520, 0), (523, 3)])
+def test_dispatch_copies_every_bit_pattern(H, extra):
+    """bf16 patterns of every kind, NaN payloads among them, arrive unchanged."""
+    torch = _t()
+    c = Case(T=64, K=2, E=5, H=H, ld_extra=extra)
+    bits = torch.from_numpy(c.r.integers(-(1 << 15), 1 << 15, (64, c.ld)).astype(np.int16)).cuda()
+    bits[:, 0] = 0x7F81  # a signalling NaN
+    xs = torch.zeros(c.n_rows, c.ld, dtype=torch.int16, device="cuda")
+    B.check(B.mok_dispatch(c.cfg, bits, c.dev(c.map), None, None, xs))
+    f = torch.arange(c.T * c.K, device="cuda")
+    got = xs[torch.from_numpy(c.map).cuda().long(), :H]
+    assert torch.equal(got, bits[f // c.K, :H])
 
 
 def test_map_entries_out_of_range_are_reported_and_skipped():

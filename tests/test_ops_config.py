@@ -52,6 +52,7 @@ def test_adamw_config(kw, want):
     (dict(in_features=(1 << 20) + 1), BAD), (dict(ld_in=56), BAD), (dict(ld_in=65), BAD),
     (dict(ld_w=68), BAD), (dict(ld_out=90), BAD), (dict(act=5), BAD), (dict(act=-1), BAD),
     (dict(out_dtype=2), BAD), (dict(grad_dtype=2), BAD), (dict(abi_version=3), B.MOK_ERR_ABI),
+    (dict(rows=1 << 30, out_features=1 << 20), BAD),  # more tiles than 31 bits number
 ])
 def test_linear_config(kw, want):
     base = dict(rows=100, in_features=64, out_features=96)
