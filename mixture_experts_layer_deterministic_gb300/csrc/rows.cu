@@ -26,10 +26,10 @@ constexpr int COMBINE_U = 2;
 constexpr int COMBINE_BWD_U = 2;
 // blocks per SM, looping over the items: dispatch holds few registers and wants many stores in
 // flight (16: 235 us, 4: 261 us); the other two hold 8 rows a lane in registers, two blocks an SM
-// are resident, and longer-lived blocks read neighbouring rows together (16: 247 and 242 us,
-// 4: 243 and 241 us)
+// are resident, and longer-lived blocks read neighbouring rows together (2: 232 and 233 us,
+// 4: 236 and 234 us, 16: 247 and 242 us)
 constexpr int DISPATCH_BLOCKS = 16;
-constexpr int COMBINE_BLOCKS = 4;
+constexpr int COMBINE_BLOCKS = 2;
 
 // blocks for `items` work items, `per_block` of them a block: looping blocks, per_sm on each SM,
 // where there are at least four rounds of them; below that one block per share of the items
@@ -384,26 +384,32 @@ __global__ void __launch_bounds__(TPB)
 }
 
 // ---------------------------------------------------------------- combine backward
-// One block per token; warp i takes the row's segments i, i + 8, ... of 32*U pieces. The copies
-// go in rounds of equal size, at most 8: a round's rows are loaded before the first is used, and
-// each lane keeps its part of the round's dot products over all its segments. A butterfly that
-// halves the number of values at each step (9 shuffles for 8 sums, not 40) adds the lanes, and
-// the warps' parts are added in warp order. Blocks past the tokens' zero the pad rows.
-template <bool F32, bool VEC, int U>
+// 2^wsh warps per token, as many as the row has segments of 32*U pieces (at most 8, a block);
+// warp i of a token takes the segments i, i + 2^wsh, ... The copies go in rounds of equal size, at
+// most 8: a round's rows are loaded before the first is used, and each lane keeps its part of
+// the round's dot products over all its segments. A butterfly that halves the number of values
+// at each step (9 shuffles for 8 sums, not 40) adds the lanes, and the warps' parts are added
+// in warp order. Items past the tokens' are the pad rows.
+template <bool F32, bool VEC, int U, bool BLOCK>
 __global__ void __launch_bounds__(TPB)
     combine_bwd_kernel(const void *__restrict__ dy, const void *__restrict__ rows,
                        const int32_t *__restrict__ map, const int32_t *__restrict__ starts,
                        const int32_t *__restrict__ kept, const float *__restrict__ w, int64_t T,
-                       int K, int E, int H, int64_t ld_tok, int64_t ld_row, int64_t n_rows,
-                       void *__restrict__ drows, float *__restrict__ dw, int *status) {
+                       int K, int E, int H, int wsh_, int64_t ld_tok, int64_t ld_row,
+                       int64_t n_rows, void *__restrict__ drows, float *__restrict__ dw,
+                       int *status) {
     using P = Piece<F32, VEC>;
     constexpr int B = Elem<F32>::BYTES, PER = P::PER;
     __shared__ float part[WARPS][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int wsh = BLOCK ? 3 : wsh_;  // a token per block: known when compiling
+    const int wpt = 1 << wsh, warp = wid & (wpt - 1);  // warps of a token, this one among them
     const bool pads = starts != nullptr && drows != nullptr;
     const int rounds = (K + 7) / 8, per_round = (K + rounds - 1) / rounds;
     const int tail = H / PER * PER;  // the columns from here are taken one a lane, by one warp
-    const int64_t items = T + (pads ? (int64_t)E * 16 / WARPS : 0);
+    // items: tokens, then the pad rows (one warp each)
+    const int64_t items = T + (pads ? (((int64_t)E * 16 - 1) >> wsh) + 1 : 0);
+    const int64_t step = (int64_t)gridDim.x * (WARPS >> wsh);
     // row and weight of copy `lane` of token i, the next token's ahead of time
     const auto fetch = [&](int64_t i, int32_t &r, float &v) {
         r = -1;
@@ -415,23 +421,25 @@ __global__ void __launch_bounds__(TPB)
     };
     int32_t next_r;
     float next_w;
-    fetch(blockIdx.x, next_r, next_w);
-    for (int64_t t = blockIdx.x; t < items; t += gridDim.x) {
+    int64_t t = (int64_t)blockIdx.x * (WARPS >> wsh) + (wid >> wsh);
+    fetch(t, next_r, next_w);
+    // every warp of a block makes the same number of turns (they meet at barriers)
+    for (int64_t t0 = (int64_t)blockIdx.x * (WARPS >> wsh); t0 < items; t0 += step, t += step) {
         const int32_t rk = checked_row(next_r, n_rows, status);
         const float wk = rk >= 0 ? next_w : 0.f;
-        fetch(t + gridDim.x, next_r, next_w);
+        fetch(t + step, next_r, next_w);
         if (t >= T) {
-            zero_pad_row<F32, VEC>((t - T) * WARPS + warp, starts, kept, n_rows, H, ld_row, drows,
-                                   lane);
-            continue;
-        }
+            const int64_t pad = ((t - T) << wsh) + warp;
+            if (pads && pad < (int64_t)E * 16)
+                zero_pad_row<F32, VEC>(pad, starts, kept, n_rows, H, ld_row, drows, lane);
+        } else {
         const uint8_t *dyp = static_cast<const uint8_t *>(dy) + t * ld_tok * B;
         for (int k0 = 0; k0 < K; k0 += per_round) {
             const int kn = K - k0 < per_round ? K - k0 : per_round;
             float acc[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-            for (int c0 = warp * 32 * PER * U; c0 < H; c0 += WARPS * 32 * PER * U) {
+            for (int c0 = warp * 32 * PER * U; c0 < H; c0 += wpt * 32 * PER * U) {
                 const int c = c0 + lane * PER;  // and U - 1 more pieces, 32 PER apart
                 P gp[U], b[8][U];
 #pragma unroll
@@ -483,7 +491,7 @@ __global__ void __launch_bounds__(TPB)
                     }
                 }
             }
-            if (VEC && warp == WARPS - 1 && tail < H) {  // the warp with the least else to do
+            if (VEC && warp == wpt - 1 && tail < H) {  // the warp with the least else to do
                 const int c = tail + lane;
                 const float g = c < H ? load_elem<F32>(dyp, c) : 0.f;
                 float e[8];
@@ -530,26 +538,35 @@ __global__ void __launch_bounds__(TPB)
                 h1 += __shfl_xor_sync(0xFFFFFFFFu, h1, 2);
                 h1 += __shfl_xor_sync(0xFFFFFFFFu, h1, 1);
                 const int j = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-                if ((lane & 3) == 0 && j < kn) part[warp][k0 + j] = h1;
+                if ((lane & 3) == 0 && j < kn) part[wid][k0 + j] = h1;
             }
         }
+        }
         if (dw != nullptr) {
-            __syncthreads();
-            if (warp == 0 && lane < K) {
+            if (wsh > 0) __syncthreads();
+            else __syncwarp();
+            if (warp == 0 && lane < K && t < T) {
                 float a = 0.f;
-#pragma unroll
-                for (int i = 0; i < WARPS; ++i) a += part[i][lane];
+                for (int i = 0; i < wpt; ++i) a += part[wid + i][lane];
                 dw[t * K + lane] = a;
             }
-            __syncthreads();
+            if (wsh > 0) __syncthreads();
+            else __syncwarp();
         }
     }
 }
 
 // ---------------------------------------------------------------- narrow rows
-// Rows of at most 32 pieces (a piece is 16 bytes, or one element where rows are not aligned): a
+// Rows of at most 16 pieces (a piece is 16 bytes, or one element where rows are not aligned): a
 // warp a row would leave most of its lanes idle, so a row gets a group of 2^sh lanes, the least
 // power of two that covers its pieces, and a warp holds 32 / 2^sh rows.
+// Rows of 65536 tokens x 8 copies of 64 bf16: dispatch 22 us, combine 37, gradient 43; with a
+// warp a row 35, 69 and 125. Rows of 32 pieces are faster as whole rows (256 bf16, 32768 tokens x
+// 8: 29, 45 and 72 us, against 38, 55 and 78 in groups of 32 lanes), so groups end at 16 lanes.
+constexpr int NARROW = 4;  // rows of a dispatch thread, their loads in flight together (2: 41 us
+                           // against 37 for 65536 x 8 of 128 bf16); one row in the gradient,
+                           // whose loads fill the registers by themselves
+
 template <bool F32, bool VEC>
 MOK_DEV void get_piece(const void *p, int64_t row, int64_t ld, int c, int H,
                        float (&v)[VEC ? Elem<F32>::PER : 1]) {
@@ -621,18 +638,24 @@ __global__ void __launch_bounds__(TPB)
                            int64_t T, int K, int E, int H, int sh, int64_t ld_tok, int64_t ld_row,
                            int64_t n_rows, void *__restrict__ xs, int *status) {
     constexpr int PER = VEC ? Elem<F32>::PER : 1;
-    const int64_t i = (int64_t)blockIdx.x * TPB + threadIdx.x, f = i >> sh;
-    const int c = (int)(i & ((1 << sh) - 1)) * PER;
-    const int64_t R = T * K;
+    const int64_t R = T * K, i0 = (int64_t)blockIdx.x * TPB * NARROW + threadIdx.x;
+    const int c = (int)(i0 & ((1 << sh) - 1)) * PER;  // the same for all of the thread's rows
     if (c >= H) return;
-    if (f >= R) {
-        if (starts != nullptr && f - R < (int64_t)E * 16)
-            zero_pad_piece<F32, VEC>(f - R, starts, kept, n_rows, c, H, ld_row, xs);
-        return;
+    int32_t r[NARROW];
+#pragma unroll
+    for (int j = 0; j < NARROW; ++j) {  // the rows' lookups in flight together
+        const int64_t f = (i0 + j * TPB) >> sh;
+        r[j] = f < R ? map[f] : -1;
     }
-    const int32_t r = row_of(map, f, n_rows, status);
-    if (r < 0) return;
-    copy_piece<F32, VEC>(x, (uint32_t)f / (uint32_t)K, ld_tok, xs, r, ld_row, c, H);
+#pragma unroll
+    for (int j = 0; j < NARROW; ++j) {
+        const int64_t f = (i0 + j * TPB) >> sh;
+        const int32_t to = checked_row(r[j], n_rows, status);
+        if (to >= 0)
+            copy_piece<F32, VEC>(x, (uint32_t)f / (uint32_t)K, ld_tok, xs, to, ld_row, c, H);
+        else if (f >= R && starts != nullptr && f - R < (int64_t)E * 16)
+            zero_pad_piece<F32, VEC>(f - R, starts, kept, n_rows, c, H, ld_row, xs);
+    }
 }
 
 template <bool F32, bool VEC>
@@ -722,15 +745,17 @@ bool vectors(const mok_rows_config &c) {
     return c.ld_tok % per == 0 && c.ld_row % per == 0;
 }
 
-// lanes of a narrow row's group, as a shift; -1 for rows of more than 32 pieces
+// lanes of a narrow row's group, as a shift; -1 for rows of more than 16 pieces
 int narrow_shift(const mok_rows_config &c) {
     const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
     const int pieces = (c.H + per - 1) / per;
     int sh = 0;
-    while ((1 << sh) < pieces && sh < 6) ++sh;
-    return sh <= 5 ? sh : -1;
+    while ((1 << sh) < pieces && sh < 5) ++sh;
+    return sh <= 4 ? sh : -1;
 }
-int64_t narrow_blocks(int64_t items, int sh) { return ((items << sh) + TPB - 1) / TPB; }
+int64_t narrow_blocks(int64_t items, int sh, int per_thread) {
+    return ((items << sh) + TPB * per_thread - 1) / (TPB * per_thread);
+}
 
 }  // namespace
 
@@ -767,7 +792,7 @@ cudaError_t launch_dispatch_rows(const mok_rows_config &c, const void *x, const 
     if (items == 0) return cudaSuccess;
     if (const int sh = narrow_shift(c); sh >= 0) {
         const int64_t rows = (int64_t)c.T * c.K + (starts != nullptr ? (int64_t)c.E * 16 : 0);
-        const int64_t blocks = narrow_blocks(rows, sh);
+        const int64_t blocks = narrow_blocks(rows, sh, NARROW);
         if (blocks <= 0x7FFFFFFF) {
 #define CALL(F, V)                                                                          \
     dispatch_narrow_kernel<F, V><<<(unsigned)blocks, TPB, 0, s>>>(                          \
@@ -791,7 +816,7 @@ cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, cons
     if (c.T == 0) return cudaSuccess;
     const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
     if (const int sh = narrow_shift(c); sh >= 0) {
-        const int64_t blocks = narrow_blocks(c.T, sh);
+        const int64_t blocks = narrow_blocks(c.T, sh, 1);
         if (blocks <= 0x7FFFFFFF) {
 #define CALL(F, V)                                                               \
     combine_narrow_kernel<F, V><<<(unsigned)blocks, TPB, 0, s>>>(                \
@@ -815,12 +840,11 @@ cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const v
                                const int32_t *map, const int32_t *starts, const int32_t *kept,
                                const float *w, void *drows, float *dw, int *status,
                                cudaStream_t s) {
-    const int64_t items = c.T + (starts != nullptr && drows != nullptr ? (int64_t)c.E * 2 : 0);
-    if (items == 0) return cudaSuccess;
+    const bool has_pads = starts != nullptr && drows != nullptr;
+    if (c.T == 0 && !has_pads) return cudaSuccess;
     if (const int sh = narrow_shift(c); sh >= 0) {
-        const bool pads = starts != nullptr && drows != nullptr;
-        const int64_t n = (int64_t)c.T * c.K + (pads ? (int64_t)c.E * 16 : 0);
-        const int64_t blocks = narrow_blocks(n, sh);
+        const int64_t n = (int64_t)c.T * c.K + (has_pads ? (int64_t)c.E * 16 : 0);
+        const int64_t blocks = narrow_blocks(n, sh, 1);
         if (blocks <= 0x7FFFFFFF) {
 #define CALL(F, V)                                                                            \
     combine_bwd_narrow_kernel<F, V><<<(unsigned)blocks, TPB, 0, s>>>(                         \
@@ -831,10 +855,22 @@ cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const v
             return cudaGetLastError();
         }
     }
-#define CALL(F, V)                                                                         \
-    combine_bwd_kernel<F, V, COMBINE_BWD_U><<<grid_for(items, 1, COMBINE_BLOCKS), TPB, 0, s>>>( \
-        dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, c.ld_tok, c.ld_row, c.n_rows,  \
-        drows, dw, status)
+    const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
+    const int segs = (c.H + per * 32 * COMBINE_BWD_U - 1) / (per * 32 * COMBINE_BWD_U);
+    int wsh = 0;
+    while ((1 << wsh) < segs && (1 << wsh) < WARPS) ++wsh;
+    const int64_t items = c.T + (has_pads ? (((int64_t)c.E * 16 - 1) >> wsh) + 1 : 0);
+#define CALL(F, V)                                                                             \
+    if (wsh == 3)                                                                              \
+        combine_bwd_kernel<F, V, COMBINE_BWD_U, true>                                          \
+            <<<grid_for(items, 1, COMBINE_BLOCKS), TPB, 0, s>>>(                               \
+                dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, wsh, c.ld_tok, c.ld_row,   \
+                c.n_rows, drows, dw, status);                                                  \
+    else                                                                                       \
+        combine_bwd_kernel<F, V, COMBINE_BWD_U, false>                                         \
+            <<<grid_for(items, WARPS >> wsh, COMBINE_BLOCKS), TPB, 0, s>>>(                    \
+                dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, wsh, c.ld_tok, c.ld_row,   \
+                c.n_rows, drows, dw, status)
     MOK_ROWS_CASES(c, CALL);
 #undef CALL
     return cudaGetLastError();
