@@ -20,14 +20,20 @@ constexpr int TPB = 256;
 constexpr int WARPS = TPB / 32;
 constexpr int MAX_E = 1024;
 // 16-byte pieces per lane and row of an item: a warp reads a row in runs of 1 KB (16384 tokens x
-// 10 rows x 4096 bf16: combine 291 us at one piece, 246 us at two;
-// and its gradient 281 us at one, 241 us at two for 8192 tokens)
+// 10 rows x 4096 bf16: combine 321 us at one piece, 232 us at two;
+// and its gradient 273 us at one, 233 us at two for 8192 tokens)
 constexpr int COMBINE_U = 2;
 constexpr int COMBINE_BWD_U = 2;
+// with at most 4 copies a round of one segment leaves few loads in flight: longer segments for
+// combine, more blocks for its gradient (16384 tokens x 2 rows x 4096 bf16: 98 -> 76 us and
+// 156 -> 126 us; 8192 x 4: 69 -> 63 us and 113 -> 98 us)
+constexpr int FEW = 4;
+constexpr int FEW_U = 4;
+constexpr int FEW_BWD_BLOCKS = 3;
 // blocks per SM, looping over the items: dispatch holds few registers and wants many stores in
 // flight (16: 235 us, 4: 261 us); the other two hold 8 rows a lane in registers, two blocks an SM
 // are resident, and longer-lived blocks read neighbouring rows together (2: 232 and 233 us,
-// 4: 236 and 234 us, 16: 247 and 242 us)
+// 4: 236 and 234 us, 16: 247 and 242 us, the gradient over 8192 tokens)
 constexpr int DISPATCH_BLOCKS = 16;
 constexpr int COMBINE_BLOCKS = 2;
 
@@ -266,11 +272,11 @@ struct Piece {
 };
 
 // Work item: (token, segment of 32*U pieces of 16 bytes), one warp each. Lane k holds row and
-// weight of copy k. The K rows are read in rounds of equal size, at most 8 rows x U pieces a
+// weight of copy k. The K rows are read in rounds of equal size, at most J rows x U pieces a
 // lane, all loads of a round before the first is used: the rounds' memory latency is what
 // bounds a warp here. A dropped copy has weight zero and reads as zero.
-template <bool F32, bool VEC, int U>
-__global__ void __launch_bounds__(TPB)
+template <bool F32, bool VEC, int J, int U>
+__global__ void __launch_bounds__(TPB, COMBINE_BLOCKS)
     combine_rows_kernel(const void *__restrict__ rows, const int32_t *__restrict__ map,
                         const float *__restrict__ w, const void *res, int64_t T, int K, int H,
                         int64_t ld_tok, int64_t ld_row, int64_t n_rows, void *y, int *status) {
@@ -278,41 +284,51 @@ __global__ void __launch_bounds__(TPB)
     constexpr int B = Elem<F32>::BYTES, PER = P::PER;
     const int lane = threadIdx.x & 31;
     const int segs = (H + PER * 32 * U - 1) / (PER * 32 * U);
-    const int rounds = (K + 7) / 8, per_round = (K + rounds - 1) / rounds;
-    const int64_t items = T * segs;
+    const int rounds = (K + J - 1) / J, per_round = (K + rounds - 1) / rounds;
     const int64_t nw = (int64_t)gridDim.x * WARPS;
-    // row and weight of copy `lane` of item i's token; the next item's are fetched while this one's
-    // rows are on their way
+    // row and weight of copy `lane` of token i; the next item's are fetched while this one's rows
+    // are on their way
     const auto fetch = [&](int64_t i, int32_t &r, float &v) {
         r = -1;
         v = 0.f;
-        if (i < items && lane < K) {
-            const int64_t f = (segs == 1 ? i : i / segs) * K + lane;
-            r = map[f];
-            v = w != nullptr ? w[f] : 1.0f;
+        if (i < T && lane < K) {
+            r = map[i * K + lane];
+            v = w != nullptr ? w[i * K + lane] : 1.0f;
         }
     };
-    int64_t it = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
+    // this item's token and segment, and what a step of the grid adds to them: no division a turn
+    const int64_t it = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
+    int64_t next_t = it / segs;
+    int next_seg = (int)(it - next_t * segs);
+    const int64_t step_t = nw / segs;
+    const int step_seg = (int)(nw - step_t * segs);
     int32_t next_r;
     float next_w;
-    fetch(it, next_r, next_w);
-    for (; it < items; it += nw) {
+    fetch(next_t, next_r, next_w);
+    while (next_t < T) {
         const int32_t rk = checked_row(next_r, n_rows, status);
         const float wk = rk >= 0 ? next_w : 0.f;
-        fetch(it + nw, next_r, next_w);
-        const int64_t t = segs == 1 ? it : it / segs;
-        const int c0 = ((int)(it - t * segs) * 32 * U + lane) * PER;  // first column, step 32 PER
+        const int64_t t = next_t;
+        const int seg = next_seg;
+        next_t += step_t;
+        next_seg += step_seg;
+        if (next_seg >= segs) {
+            next_seg -= segs;
+            ++next_t;
+        }
+        fetch(next_t, next_r, next_w);
+        const int c0 = (seg * 32 * U + lane) * PER;  // first column, step 32 PER
         float acc[U][PER];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int q = 0; q < PER; ++q) acc[u][q] = 0.f;
         for (int k0 = 0; k0 < K; k0 += per_round) {
-            P b[8][U];
-            float s[8];
+            P b[J][U];
+            float s[J];
             const int kn = K - k0 < per_round ? K - k0 : per_round;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < J; ++j) {
                 if (j >= kn) break;
                 const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
                 s[j] = __shfl_sync(0xFFFFFFFFu, wk, k0 + j);
@@ -322,7 +338,7 @@ __global__ void __launch_bounds__(TPB)
                     b[j][u].load(p, c0 + u * 32 * PER, r >= 0 && c0 + u * 32 * PER + PER <= H);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < J; ++j) {
                 if (j >= kn) break;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -358,7 +374,7 @@ __global__ void __launch_bounds__(TPB)
         if (VEC && H % PER != 0) {
             const int c = H / PER * PER + lane;
             const int seg_of_tail = (H / PER) / (32 * U);
-            if ((int)(it - t * segs) == seg_of_tail) {
+            if (seg == seg_of_tail) {
                 float a = 0.f;
                 for (int k0 = 0; k0 < K; k0 += 8) {  // 8 loads in flight
                     float e[8], s[8];
@@ -386,12 +402,12 @@ __global__ void __launch_bounds__(TPB)
 // ---------------------------------------------------------------- combine backward
 // 2^wsh warps per token, as many as the row has segments of 32*U pieces (at most 8, a block);
 // warp i of a token takes the segments i, i + 2^wsh, ... The copies go in rounds of equal size, at
-// most 8: a round's rows are loaded before the first is used, and each lane keeps its part of
+// most J: a round's rows are loaded before the first is used, and each lane keeps its part of
 // the round's dot products over all its segments. A butterfly that halves the number of values
 // at each step (9 shuffles for 8 sums, not 40) adds the lanes, and the warps' parts are added
 // in warp order. Items past the tokens' are the pad rows.
-template <bool F32, bool VEC, int U, bool BLOCK>
-__global__ void __launch_bounds__(TPB)
+template <bool F32, bool VEC, int J, bool BLOCK>
+__global__ void __launch_bounds__(TPB, J == FEW ? FEW_BWD_BLOCKS : COMBINE_BLOCKS)
     combine_bwd_kernel(const void *__restrict__ dy, const void *__restrict__ rows,
                        const int32_t *__restrict__ map, const int32_t *__restrict__ starts,
                        const int32_t *__restrict__ kept, const float *__restrict__ w, int64_t T,
@@ -399,13 +415,13 @@ __global__ void __launch_bounds__(TPB)
                        int64_t n_rows, void *__restrict__ drows, float *__restrict__ dw,
                        int *status) {
     using P = Piece<F32, VEC>;
-    constexpr int B = Elem<F32>::BYTES, PER = P::PER;
+    constexpr int B = Elem<F32>::BYTES, PER = P::PER, U = COMBINE_BWD_U;
     __shared__ float part[WARPS][32];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int wsh = BLOCK ? 3 : wsh_;  // a token per block: known when compiling
     const int wpt = 1 << wsh, warp = wid & (wpt - 1);  // warps of a token, this one among them
     const bool pads = starts != nullptr && drows != nullptr;
-    const int rounds = (K + 7) / 8, per_round = (K + rounds - 1) / rounds;
+    const int rounds = (K + J - 1) / J, per_round = (K + rounds - 1) / rounds;
     const int tail = H / PER * PER;  // the columns from here are taken one a lane, by one warp
     // items: tokens, then the pad rows (one warp each)
     const int64_t items = T + (pads ? (((int64_t)E * 16 - 1) >> wsh) + 1 : 0);
@@ -433,114 +449,114 @@ __global__ void __launch_bounds__(TPB)
             if (pads && pad < (int64_t)E * 16)
                 zero_pad_row<F32, VEC>(pad, starts, kept, n_rows, H, ld_row, drows, lane);
         } else {
-        const uint8_t *dyp = static_cast<const uint8_t *>(dy) + t * ld_tok * B;
-        for (int k0 = 0; k0 < K; k0 += per_round) {
-            const int kn = K - k0 < per_round ? K - k0 : per_round;
-            float acc[8];
+            const uint8_t *dyp = static_cast<const uint8_t *>(dy) + t * ld_tok * B;
+            for (int k0 = 0; k0 < K; k0 += per_round) {
+                const int kn = K - k0 < per_round ? K - k0 : per_round;
+                float acc[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-            for (int c0 = warp * 32 * PER * U; c0 < H; c0 += wpt * 32 * PER * U) {
-                const int c = c0 + lane * PER;  // and U - 1 more pieces, 32 PER apart
-                P gp[U], b[8][U];
+                for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+                for (int c0 = warp * 32 * PER * U; c0 < H; c0 += wpt * 32 * PER * U) {
+                    const int c = c0 + lane * PER;  // and U - 1 more pieces, 32 PER apart
+                    P gp[U], b[J][U];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    gp[u].load(dyp, c + u * 32 * PER, c + u * 32 * PER + PER <= H);
-                if (dw != nullptr) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (j >= kn) break;
-                        const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
-#pragma unroll
-                        for (int u = 0; u < U; ++u)
-                            b[j][u].load(static_cast<const uint8_t *>(rows) + r * ld_row * B,
-                                         c + u * 32 * PER,
-                                         r >= 0 && c + u * 32 * PER + PER <= H);
-                    }
-                }
-                float g[U][PER];
-#pragma unroll
-                for (int u = 0; u < U; ++u) gp[u].values(g[u]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j >= kn) break;
-                    if (drows != nullptr) {
-                        const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
-                        const float s = __shfl_sync(0xFFFFFFFFu, wk, k0 + j);
-                        uint8_t *o = static_cast<uint8_t *>(drows) + r * ld_row * B;
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const int cu = c + u * 32 * PER;
-                            if (r < 0 || cu + PER > H) continue;
-                            float d[PER];
-#pragma unroll
-                            for (int q = 0; q < PER; ++q) d[q] = s * g[u][q];
-                            if constexpr (VEC)
-                                *reinterpret_cast<uint4 *>(o + (int64_t)cu * B) = pack<F32>(d);
-                            else
-                                store_elem<F32>(o, cu, d[0]);
-                        }
-                    }
+                    for (int u = 0; u < U; ++u)
+                        gp[u].load(dyp, c + u * 32 * PER, c + u * 32 * PER + PER <= H);
                     if (dw != nullptr) {
 #pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            float v[PER];
-                            b[j][u].values(v);
+                        for (int j = 0; j < J; ++j) {
+                            if (j >= kn) break;
+                            const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
 #pragma unroll
-                            for (int q = 0; q < PER; ++q) acc[j] = fmaf(v[q], g[u][q], acc[j]);
+                            for (int u = 0; u < U; ++u)
+                                b[j][u].load(static_cast<const uint8_t *>(rows) + r * ld_row * B,
+                                             c + u * 32 * PER,
+                                             r >= 0 && c + u * 32 * PER + PER <= H);
+                        }
+                    }
+                    float g[U][PER];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) gp[u].values(g[u]);
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        if (j >= kn) break;
+                        if (drows != nullptr) {
+                            const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
+                            const float s = __shfl_sync(0xFFFFFFFFu, wk, k0 + j);
+                            uint8_t *o = static_cast<uint8_t *>(drows) + r * ld_row * B;
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                const int cu = c + u * 32 * PER;
+                                if (r < 0 || cu + PER > H) continue;
+                                float d[PER];
+#pragma unroll
+                                for (int q = 0; q < PER; ++q) d[q] = s * g[u][q];
+                                if constexpr (VEC)
+                                    *reinterpret_cast<uint4 *>(o + (int64_t)cu * B) = pack<F32>(d);
+                                else
+                                    store_elem<F32>(o, cu, d[0]);
+                            }
+                        }
+                        if (dw != nullptr) {
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                float v[PER];
+                                b[j][u].values(v);
+#pragma unroll
+                                for (int q = 0; q < PER; ++q) acc[j] = fmaf(v[q], g[u][q], acc[j]);
+                            }
                         }
                     }
                 }
+                if (VEC && warp == wpt - 1 && tail < H) {  // the warp with the least else to do
+                    const int c = tail + lane;
+                    const float g = c < H ? load_elem<F32>(dyp, c) : 0.f;
+                    float e[J];
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        if (j >= kn) break;
+                        const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
+                        e[j] = 0.f;
+                        if (dw != nullptr && r >= 0 && c < H)
+                            e[j] = load_elem<F32>(static_cast<const uint8_t *>(rows) + r * ld_row * B,
+                                                  c);
+                    }
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        if (j >= kn) break;
+                        const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
+                        const float s = __shfl_sync(0xFFFFFFFFu, wk, k0 + j);
+                        if (drows != nullptr && r >= 0 && c < H)
+                            store_elem<F32>(static_cast<uint8_t *>(drows) + r * ld_row * B, c, s * g);
+                        acc[j] = fmaf(e[j], g, acc[j]);
+                    }
+                }
+                if (dw != nullptr) {
+                    // after the step with lane distance 16, 8, 4 a lane keeps the half of the values
+                    // that its lane bit names; the last two add what is left of one value
+                    float h4[4], h2[2], h1;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool up = lane & 16;
+                        const float give = up ? acc[j] : acc[j + 4], keep = up ? acc[j + 4] : acc[j];
+                        h4[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 16);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const bool up = lane & 8;
+                        const float give = up ? h4[j] : h4[j + 2], keep = up ? h4[j + 2] : h4[j];
+                        h2[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 8);
+                    }
+                    {
+                        const bool up = lane & 4;
+                        const float give = up ? h2[0] : h2[1], keep = up ? h2[1] : h2[0];
+                        h1 = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 4);
+                    }
+                    h1 += __shfl_xor_sync(0xFFFFFFFFu, h1, 2);
+                    h1 += __shfl_xor_sync(0xFFFFFFFFu, h1, 1);
+                    const int j = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+                    if ((lane & 3) == 0 && j < kn) part[wid][k0 + j] = h1;
+                }
             }
-            if (VEC && warp == wpt - 1 && tail < H) {  // the warp with the least else to do
-                const int c = tail + lane;
-                const float g = c < H ? load_elem<F32>(dyp, c) : 0.f;
-                float e[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j >= kn) break;
-                    const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
-                    e[j] = 0.f;
-                    if (dw != nullptr && r >= 0 && c < H)
-                        e[j] = load_elem<F32>(static_cast<const uint8_t *>(rows) + r * ld_row * B,
-                                              c);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j >= kn) break;
-                    const int32_t r = __shfl_sync(0xFFFFFFFFu, rk, k0 + j);
-                    const float s = __shfl_sync(0xFFFFFFFFu, wk, k0 + j);
-                    if (drows != nullptr && r >= 0 && c < H)
-                        store_elem<F32>(static_cast<uint8_t *>(drows) + r * ld_row * B, c, s * g);
-                    acc[j] = fmaf(e[j], g, acc[j]);
-                }
-            }
-            if (dw != nullptr) {
-                // after the step with lane distance 16, 8, 4 a lane keeps the half of the values
-                // that its lane bit names; the last two add what is left of one value
-                float h4[4], h2[2], h1;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool up = lane & 16;
-                    const float give = up ? acc[j] : acc[j + 4], keep = up ? acc[j + 4] : acc[j];
-                    h4[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 16);
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const bool up = lane & 8;
-                    const float give = up ? h4[j] : h4[j + 2], keep = up ? h4[j + 2] : h4[j];
-                    h2[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 8);
-                }
-                {
-                    const bool up = lane & 4;
-                    const float give = up ? h2[0] : h2[1], keep = up ? h2[1] : h2[0];
-                    h1 = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 4);
-                }
-                h1 += __shfl_xor_sync(0xFFFFFFFFu, h1, 2);
-                h1 += __shfl_xor_sync(0xFFFFFFFFu, h1, 1);
-                const int j = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-                if ((lane & 3) == 0 && j < kn) part[wid][k0 + j] = h1;
-            }
-        }
         }
         if (dw != nullptr) {
             if (wsh > 0) __syncthreads();
@@ -826,12 +842,20 @@ cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, cons
             return cudaGetLastError();
         }
     }
-    constexpr int U = COMBINE_U;
+    // rows that two pieces a lane cover gain nothing from longer segments (4 copies of 264 bf16:
+    // 41 us against 35 us)
+    const bool few = c.K <= FEW && c.H > per * 32 * COMBINE_U;
+    const int U = few ? FEW_U : COMBINE_U;
     const int64_t items = (int64_t)c.T * ((c.H + per * 32 * U - 1) / (per * 32 * U));
-#define CALL(F, V)                                                                       \
-    combine_rows_kernel<F, V, U><<<grid_for(items, WARPS, COMBINE_BLOCKS), TPB, 0, s>>>(             \
+    const unsigned grid = grid_for(items, WARPS, COMBINE_BLOCKS);
+#define ROWS(F, V, J, U)                                                               \
+    combine_rows_kernel<F, V, J, U><<<grid, TPB, 0, s>>>(                              \
         rows, map, w, res, c.T, c.K, c.H, c.ld_tok, c.ld_row, c.n_rows, y, status)
+#define CALL(F, V)                           \
+    if (few) ROWS(F, V, FEW, FEW_U);         \
+    else ROWS(F, V, 8, COMBINE_U)
     MOK_ROWS_CASES(c, CALL);
+#undef ROWS
 #undef CALL
     return cudaGetLastError();
 }
@@ -860,18 +884,22 @@ cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const v
     int wsh = 0;
     while ((1 << wsh) < segs && (1 << wsh) < WARPS) ++wsh;
     const int64_t items = c.T + (has_pads ? (((int64_t)c.E * 16 - 1) >> wsh) + 1 : 0);
-#define CALL(F, V)                                                                             \
-    if (wsh == 3)                                                                              \
-        combine_bwd_kernel<F, V, COMBINE_BWD_U, true>                                          \
-            <<<grid_for(items, 1, COMBINE_BLOCKS), TPB, 0, s>>>(                               \
-                dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, wsh, c.ld_tok, c.ld_row,   \
-                c.n_rows, drows, dw, status);                                                  \
-    else                                                                                       \
-        combine_bwd_kernel<F, V, COMBINE_BWD_U, false>                                         \
-            <<<grid_for(items, WARPS >> wsh, COMBINE_BLOCKS), TPB, 0, s>>>(                    \
-                dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, wsh, c.ld_tok, c.ld_row,   \
-                c.n_rows, drows, dw, status)
+    const bool few = c.K <= FEW;
+    const unsigned grid = grid_for(items, WARPS >> wsh, few ? FEW_BWD_BLOCKS : COMBINE_BLOCKS);
+#define BWD(F, V, J, BLOCK)                                                                    \
+    combine_bwd_kernel<F, V, J, BLOCK><<<grid, TPB, 0, s>>>(                                   \
+        dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, wsh, c.ld_tok, c.ld_row, c.n_rows, \
+        drows, dw, status)
+#define CALL(F, V)                           \
+    if (few) {                               \
+        if (wsh == 3) BWD(F, V, FEW, true);  \
+        else BWD(F, V, FEW, false);          \
+    } else {                                 \
+        if (wsh == 3) BWD(F, V, 8, true);    \
+        else BWD(F, V, 8, false);            \
+    }
     MOK_ROWS_CASES(c, CALL);
+#undef BWD
 #undef CALL
     return cudaGetLastError();
 }

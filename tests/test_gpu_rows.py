@@ -114,6 +114,11 @@ CASES = [
     dict(T=75, K=9, E=12, H=127, dtype="fp32"),
     dict(T=90, K=4, E=8, H=520, capacity=1),
     dict(T=300, K=8, E=64, H=2056, capacity=17, spare=40),
+    dict(T=50, K=1, E=3, H=2060, capacity=20),
+    dict(T=50, K=4, E=8, H=1100, dtype="fp32", hot=True),
+    dict(T=50, K=5, E=8, H=1300),
+    dict(T=50, K=2, E=8, H=515, dtype="fp32", ld_extra=2),
+    dict(T=5000, K=2, E=8, H=1027, capacity=1100),
 ]
 
 
