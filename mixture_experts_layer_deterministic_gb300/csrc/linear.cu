@@ -12,7 +12,8 @@
 //   Dx   A = W    (MN-major), B = dz  (K-major)   -> dx          [inputs x rows]
 //   Dw   A = x    (MN-major), B = dz  (MN-major)  -> dW          [inputs x features]
 // W is a 3D tensor map (inputs, features, groups), so a tile past a matrix's edge reads zeros,
-// not the next group's matrix. Every output element is one fixed-order fp32 sum.
+// not the next group's matrix. Every output element is one fp32 sum in an order that depends on the
+// call's sizes alone.
 //
 // Per CTA, 320 threads: warp 0 loads (TMA, both CTAs), warp 1 issues the MMAs (rank 0), warps
 // 2-9 drain accumulators, two sets of 256 TMEM columns alternating between units. Every wait is
@@ -224,6 +225,7 @@ static_assert(LIN_SMEM <= 232448, "shared memory of a CTA");
 // contiguous dimension (mb) and of dW's features (nb).
 struct Unit {
     int g, r0, nr, pad, mb, nb;
+    int part;  // of K, where it is cut
 };
 
 // one unit as one CTA of the pair loads and multiplies it
@@ -233,6 +235,32 @@ struct LinGeom {
     int nbox;            // boxes of B per CTA: 64 columns (MN-major), 32 rows (K-major)
     int n_mma;           // N of each MMA
     int k_steps;         // 16-element K steps
+    int k_first;         // K element to begin at
+};
+
+// Dense products with few units and a long K (dW of a narrow layer over many rows) leave most
+// SMs idle: K is then cut into equal parts, one unit each, which write their fp32 sums to the
+// workspace, and a join kernel adds them in order and finishes the output. Gradients of 16384
+// rows, 64 x 64, 60 us without and 30 us with it, of 4096 rows, 512 x 512, 24 and 14 us; forward
+// of 512 rows, 4096 -> 512, 15 and 10 us.
+struct KParts {
+    int parts;   // 1: K is whole and `out` not used
+    int per;     // 64-element K blocks a part
+    float *out;  // [parts][rows][ld]
+    int64_t ld, stride;
+
+    // number u of `units` times parts: the part, u becomes the unit's number
+    MOK_DEV int take(uint32_t &u, uint32_t units) const {
+        if (parts == 1) return 0;
+        const uint32_t p = u / units;
+        u -= p * units;
+        return (int)p;
+    }
+    MOK_DEV void cut(LinGeom &q, int part) const {
+        q.k_first = part * per * BK;
+        const int left = q.k_steps - part * per * (BK / 16);
+        q.k_steps = parts > 1 && left > per * (BK / 16) ? per * (BK / 16) : left;
+    }
 };
 
 // values of tcgen05.ld instructions that a tmem_ld_wait before this covers: keeps their uses
@@ -327,6 +355,26 @@ MOK_DEV void patch_add8(uint32_t patch, int half, int b, float (&v)[2][4], int l
     }
 }
 
+// `n` rows from `row` on of a part's sums, one of the columns a lane
+template <int STEP>
+MOK_DEV void emit_part(const KParts &kp, int part, uint32_t c, int hw, int64_t row, int n, int col,
+                       int cols) {
+    float *o = kp.out + part * kp.stride + row * kp.ld + col;
+    for (int n0 = 32 * hw; n0 < n; n0 += STEP) {
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+            float v[16];
+            tc::tmem_ld16(c + n0 + h, v);
+            tc::tmem_ld_wait();
+            loaded(v);
+            if (col >= cols) continue;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (n0 + h + j < n) o[(n0 + h + j) * kp.ld] = v[j];
+        }
+    }
+}
+
 // a bf16 output: matrices of `rows` x `cols`, rows ld apart
 struct OutRef {
     uint16_t *p;
@@ -414,11 +462,12 @@ MOK_DEV void emit_plain(Patches &pt, uint32_t c, int nr, const OutRef &o, int x,
     pt.store(o, x, y0, end, g);
 }
 
-// PLAIN: only a bias after the product (no activation, residual or z)
-template <bool F32, bool PLAIN>
+// PLAIN: only a bias after the product (no activation, residual or z); CUT: K is cut into parts
+// (a variant of its own: the code for parts cost the router's product 1.3 of 52 us)
+template <bool F32, bool PLAIN, bool CUT = false>
 struct Fwd {
     using E = Epi<F32 && PLAIN>;
-    static constexpr bool F32_OUT = F32, SUMS = F32 && PLAIN;
+    static constexpr bool F32_OUT = F32 || CUT, SUMS = F32 && PLAIN;
     static constexpr bool A_MN = false, B_MN = false;
     Tiles tiles;
     int n_mb;      // ceil(N / 256)
@@ -431,12 +480,14 @@ struct Fwd {
     uint16_t *z;
     int act;
     int *status;
+    KParts kp;
 
-    MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
+    MOK_DEV int64_t n_units() const { return tiles.count() * n_mb * (CUT ? kp.parts : 1); }
     MOK_DEV void side_work(uint32_t, uint32_t, int) const {}
     MOK_DEV Unit unit(uint32_t u) const {
+        const int part = CUT ? kp.take(u, (uint32_t)(tiles.cap * n_mb)) : 0;
         const int4 t = tiles.get(u / (uint32_t)n_mb);
-        return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0};
+        return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0, part};
     }
     MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
         LinGeom q;
@@ -449,6 +500,8 @@ struct Fwd {
         q.nbox = (q.n_mma / 2 + 31) / 32;
         const int k = segs > 1 && Kin - q.a0 > SEG_K ? SEG_K : Kin - q.a0;
         q.k_steps = (k + 15) / 16;
+        q.k_first = 0;
+        if constexpr (CUT) kp.cut(q, u.part);
         return q;
     }
     MOK_DEV uint32_t tx(const LinGeom &q) const { return 2 * BOX + q.nbox * (BOX / 2); }
@@ -466,7 +519,9 @@ struct Fwd {
         const int n_mma = (nr + 15) & ~15;
         const int f0 = u.mb * 256 + (int)rank * 128 + q * 32;  // the warp's features
         const int n_out = pad ? n_mma : nr;
-        if constexpr (SUMS)
+        if constexpr (CUT)
+            emit_part<E::STEP>(kp, u.part, c, hw, r0, nr, f0 + lane, N);
+        else if constexpr (SUMS)
             direct_sums(seg, c, hw, f0 + lane, u.g, r0, nr, n_out, carry.v);
         else if constexpr (F32)
             direct(seg, c, hw, f0 + lane, u.g, r0, nr, n_out);
@@ -627,7 +682,8 @@ struct Fwd {
     }
 };
 
-template <bool F32>
+// CUT: K may be cut into parts
+template <bool F32, bool CUT>
 struct Dx {
     using E = Epi<false>;
     static constexpr bool F32_OUT = F32, SUMS = false;
@@ -639,12 +695,14 @@ struct Dx {
     int64_t ld;   // row stride of dx
     void *dx;
     int *status;
+    KParts kp;
 
-    MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
+    MOK_DEV int64_t n_units() const { return tiles.count() * n_mb * (CUT ? kp.parts : 1); }
     MOK_DEV void side_work(uint32_t, uint32_t, int) const {}
     MOK_DEV Unit unit(uint32_t u) const {
+        const int part = CUT ? kp.take(u, (uint32_t)(tiles.cap * n_mb)) : 0;
         const int4 t = tiles.get(u / (uint32_t)n_mb);
-        return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0};
+        return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0, part};
     }
     MOK_DEV LinGeom geom(const Unit &u, int, uint32_t rank) const {
         LinGeom q;
@@ -656,6 +714,8 @@ struct Dx {
         q.b1 = u.r0 + (int)rank * (q.n_mma / 2);
         q.nbox = (q.n_mma / 2 + 31) / 32;
         q.k_steps = (N + 15) / 16;
+        q.k_first = 0;
+        if constexpr (CUT) kp.cut(q, u.part);
         return q;
     }
     MOK_DEV uint32_t tx(const LinGeom &q) const { return 2 * BOX + q.nbox * (BOX / 2); }
@@ -673,6 +733,10 @@ struct Dx {
         const int64_t r0 = u.r0;
         const int n_mma = (nr + 15) & ~15;
         const int i0 = u.mb * 256 + (int)rank * 128 + q * 32;
+        if (CUT && kp.parts > 1) {
+            emit_part<E::STEP>(kp, u.part, c, hw, r0, nr, i0 + lane, Kin);
+            return;
+        }
         for (int n0 = 32 * hw; n0 < n_mma; n0 += E::STEP) {
             if constexpr (F32) {
                 float v[32];
@@ -691,27 +755,61 @@ struct Dx {
     }
 };
 
-// The bias gradient from the parts of the dz kernel: db[g][n] is the sum of the group's parts in
-// row order.
+// The bias gradient from the parts of the dz kernel: db[g][n] is the sum of the group's parts, in
+// a fixed order.
 constexpr int DZ_ROWS = 128;
 constexpr int DZ_PARTS = LTILE / DZ_ROWS;  // parts of a tile
+constexpr int DB_SLICES = 8;               // sums that a feature's parts are added in
 struct DbArgs {
     const float *part;     // [tiles][DZ_PARTS][N]
     const int32_t *first;  // grouped: first tile of each group
     int64_t tiles;         // dense: all tiles
     float *db;             // [G][N], or nullptr
-    MOK_DEV float sum(int g, int n, int N) const {
+    // the group's parts: the first, and their number
+    MOK_DEV const float *parts(int g, int n, int N, int64_t *count) const {
         const int64_t t0 = first != nullptr ? __ldg(first + g) : 0;
         const int64_t t1 = first != nullptr ? __ldg(first + g + 1) : tiles;
-        const float *p = part + t0 * DZ_PARTS * N + n;
+        *count = (t1 - t0) * DZ_PARTS;
+        return part + t0 * DZ_PARTS * N + n;
+    }
+    // every DB_SLICES-th part from `slice` on
+    MOK_DEV float slice(int g, int n, int N, int slice) const {
+        int64_t count;
+        const float *p = parts(g, n, N, &count);
         float a = 0.f;
 #pragma unroll 16
-        for (int64_t k = 0; k < (t1 - t0) * DZ_PARTS; ++k) a += p[k * N];
+        for (int64_t k = slice; k < count; k += DB_SLICES) a += p[k * N];
         return a;
+    }
+    // all of them in one thread, to the same bits as its slices added in order
+    MOK_DEV float sum(int g, int n, int N) const {
+        int64_t count;
+        const float *p = parts(g, n, N, &count);
+        float a[DB_SLICES], all = 0.f;
+#pragma unroll
+        for (int j = 0; j < DB_SLICES; ++j) a[j] = 0.f;
+        int64_t k = 0;
+        for (; k + 2 * DB_SLICES <= count; k += 2 * DB_SLICES) {
+            float b[2 * DB_SLICES];
+#pragma unroll
+            for (int j = 0; j < 2 * DB_SLICES; ++j) b[j] = p[(k + j) * N];
+#pragma unroll
+            for (int j = 0; j < 2 * DB_SLICES; ++j) a[j % DB_SLICES] += b[j];
+        }
+        for (; k < count; k += DB_SLICES) {
+            float b[DB_SLICES];
+#pragma unroll
+            for (int j = 0; j < DB_SLICES; ++j) b[j] = k + j < count ? p[(k + j) * N] : 0.f;
+#pragma unroll
+            for (int j = 0; j < DB_SLICES; ++j) a[j] += b[j];
+        }
+#pragma unroll
+        for (int j = 0; j < DB_SLICES; ++j) all += a[j];
+        return all;
     }
 };
 
-template <bool F32>
+template <bool F32, bool CUT>
 struct Dw {
     using E = Epi<false>;
     static constexpr bool F32_OUT = F32, SUMS = false;
@@ -725,8 +823,9 @@ struct Dw {
     void *dw;
     int *status;
     DbArgs db;
+    KParts kp;
 
-    MOK_DEV int64_t n_units() const { return (int64_t)G * n_mb * n_nb; }
+    MOK_DEV int64_t n_units() const { return (int64_t)G * n_mb * n_nb * (CUT ? kp.parts : 1); }
     // a share of db, by the one warp of a pair that has nothing else to do
     MOK_DEV void side_work(uint32_t cid, uint32_t ncl, int lane) const {
         if (db.db == nullptr) return;
@@ -734,11 +833,12 @@ struct Dw {
             db.db[i] = db.sum((int)(i / N), (int)(i % N), N);
     }
     MOK_DEV Unit unit(uint32_t u) const {
-        const uint32_t per = (uint32_t)n_mb * (uint32_t)n_nb, rest = u % per;
-        const int g = (int)(u / per);
+        const uint32_t per = (uint32_t)n_mb * (uint32_t)n_nb;
+        const int part = CUT ? kp.take(u, (uint32_t)G * per) : 0, g = (int)(u / per);
+        const uint32_t rest = u % per;
         return Unit{g, starts != nullptr ? __ldg(starts + g) : 0,
                     valid != nullptr ? __ldg(valid + g) : (int)rows, 0,
-                    (int)(rest % (uint32_t)n_mb), (int)(rest / (uint32_t)n_mb)};
+                    (int)(rest % (uint32_t)n_mb), (int)(rest / (uint32_t)n_mb), part};
     }
     MOK_DEV LinGeom geom(const Unit &u, int, uint32_t rank) const {
         const int mb = u.mb, nb = u.nb;
@@ -753,6 +853,8 @@ struct Dw {
         q.b0 = nb * 256 + (int)rank * (q.n_mma / 2);
         q.b1 = q.a1;
         q.k_steps = (u.nr + 15) / 16;
+        q.k_first = 0;
+        if constexpr (CUT) kp.cut(q, u.part);
         return q;
     }
     MOK_DEV uint32_t tx(const LinGeom &q) const { return (2 + q.nbox) * BOX; }
@@ -769,6 +871,10 @@ struct Dw {
         const int nn = N - nb * 256 < 256 ? N - nb * 256 : 256;
         const bool any = u.nr > 0;
         const int i0 = mb * 256 + (int)rank * 128 + q * 32;
+        if (CUT && kp.parts > 1) {
+            emit_part<E::STEP>(kp, u.part, c, hw, nb * 256, nn, i0 + lane, Kin);
+            return;
+        }
         for (int n0 = 32 * hw; n0 < nn; n0 += E::STEP) {
             if constexpr (F32) {
                 float v[32];
@@ -878,7 +984,8 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
                             break;
                         }
                         if (rank == 0) tc::mbar_arrive_expect_tx(&sm->full[s], 2 * tx);
-                        p.load(base + s * SB, full0 + (uint32_t)s * 8u, g, kb * BK, &tmA, &tmB);
+                        p.load(base + s * SB, full0 + (uint32_t)s * 8u, g, g.k_first + kb * BK, &tmA,
+                               &tmB);
                         ++issued;
                         if (++s == NS) {
                             s = 0;
@@ -1023,6 +1130,88 @@ __global__ void __launch_bounds__(P::E::THREADS, 1)
         linear_body(pA, pB, p, c, split);
     else
         linear_body(qA, qB, q, c - split, tc::cluster_count_x() - split);
+}
+
+// ---------------------------------------------------------------- parts of K
+// The sums of the parts in order, for up to two outputs; bias, activation, residual and z (row
+// strides as the output's) belong to the first. A thread takes four columns, loading eight parts
+// at a time.
+struct JoinOut {
+    const float *part;
+    int64_t stride, ldp;  // of parts, of rows (a multiple of 4)
+    int parts, cols;
+    int64_t rows;
+    void *out;
+    int64_t ld;
+    uint32_t blocks;
+};
+struct JoinArgs {
+    JoinOut o[2];
+    const float *bias;
+    const uint16_t *res;
+    uint16_t *z;
+    int act;
+};
+constexpr int JOIN_TPB = 128;
+
+template <bool F32>
+__global__ void __launch_bounds__(JOIN_TPB) linear_join_kernel(const JoinArgs a) {
+    let_next_start();
+    wait_for_previous();
+    const bool second = blockIdx.x >= a.o[0].blocks;
+    const JoinOut &o = a.o[second];
+    const uint32_t i = (blockIdx.x - (second ? a.o[0].blocks : 0)) * JOIN_TPB + threadIdx.x;
+    const uint32_t nv = (uint32_t)(o.cols + 3) / 4, row = i / nv;
+    const int c = (int)(i - row * nv) * 4;
+    if (row >= o.rows) return;
+    const float *p = o.part + row * o.ldp + c;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < o.parts; k0 += 8) {
+        float4 b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < o.parts)
+                b[k] = *reinterpret_cast<const float4 *>(p + (k0 + k) * o.stride);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < o.parts) {
+                v[0] += b[k].x;
+                v[1] += b[k].y;
+                v[2] += b[k].z;
+                v[3] += b[k].w;
+            }
+    }
+    const int64_t at = row * o.ld + c;
+    const int n = o.cols - c < 4 ? o.cols - c : 4;  // columns past the matrix hold anything
+    if (!second) {
+        if (a.bias != nullptr)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) v[j] += a.bias[c + j];
+        if (a.z != nullptr)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) a.z[at + j] = f32_to_bf16(v[j]);
+        with_act(a.act, [&](auto act) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = act_f<act.value>(v[j]);
+        });
+        if (a.res != nullptr)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) v[j] += bf16_to_f32(a.res[at + j]);
+    }
+    if (F32 && n == 4) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(o.out) + at) =
+            make_float4(v[0], v[1], v[2], v[3]);
+    } else if (n == 4) {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o.out) + at) =
+            make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n) st_val(o.out, at + j, v[j], F32);
+    }
 }
 
 // ---------------------------------------------------------------- few rows
@@ -1329,12 +1518,24 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// db where no dW is asked for (else the dW kernel adds the parts)
-__global__ void __launch_bounds__(256) linear_db_kernel(const DbArgs d, int G, int N) {
+// db where the dW kernel does not add the parts: a block takes 32 features, each warp a slice of
+// their parts (narrow layers have many rows and few features: dx, dW and db of 16384 rows x 64 x 64
+// 30 us with a thread a feature, 17 us so)
+__global__ void __launch_bounds__(32 * DB_SLICES)
+    linear_db_kernel(const DbArgs d, int G, int N) {
+    __shared__ float sh[DB_SLICES][32];
     let_next_start();
     wait_for_previous();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < (int64_t)G * N) d.db[i] = d.sum((int)(i / N), (int)(i % N), N);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+    const bool in = i < (int64_t)G * N;
+    sh[warp][lane] = in ? d.slice((int)(i / N), (int)(i % N), N, warp) : 0.f;
+    __syncthreads();
+    if (warp != 0 || !in) return;
+    float a = 0.f;
+#pragma unroll
+    for (int k = 0; k < DB_SLICES; ++k) a += sh[k][lane];
+    d.db[i] = a;
 }
 
 // ---------------------------------------------------------------- host side
@@ -1467,6 +1668,12 @@ cudaError_t launch_small(SmallArgs a, cudaStream_t s) {
     return launch_edge(linear_small_kernel<4, 2, F32>, grid, 256, 0, 1, s, a);
 }
 
+cudaError_t launch_join(bool f32, const JoinArgs &j, cudaStream_t s) {
+    const dim3 grid(j.o[0].blocks + j.o[1].blocks);
+    return launch_edge(f32 ? linear_join_kernel<true> : linear_join_kernel<false>, grid, JOIN_TPB, 0,
+                       1, s, j);
+}
+
 bool grouped(const int32_t *starts) { return starts != nullptr; }
 
 // clocks of a 64-element K block on tiles of h rows: the larger of the MMAs' (2 a row) and the
@@ -1482,9 +1689,8 @@ int64_t unit_clocks(int64_t blocks, int64_t h) {
     return main > epi ? main : epi;
 }
 // Dense tiles of equal height: the height, up to 256 rows, at which `n_mb` blocks a tile take the
-// least time, as waves over the SM pairs times a K block's clocks.
-Tiles dense_tiles(int64_t rows, int64_t n_mb) {
-    const int64_t pairs = sm_pairs();
+// least time, as waves over the SM pairs times a K block's clocks (*clocks).
+int dense_height(int64_t rows, int64_t n_mb, int64_t pairs, int64_t *clocks) {
     int64_t best_h = LTILE, best = INT64_MAX;
     for (int64_t h0 = LTILE; h0 >= 16; h0 -= 16) {
         const int64_t n = (rows + h0 - 1) / h0;
@@ -1495,7 +1701,87 @@ Tiles dense_tiles(int64_t rows, int64_t n_mb) {
             best_h = h;
         }
     }
-    return Tiles{nullptr, (rows + best_h - 1) / best_h, rows, (int)best_h};
+    *clocks = best;
+    return (int)best_h;
+}
+Tiles dense_tiles(int64_t rows, int height) {
+    return Tiles{nullptr, (rows + height - 1) / height, rows, height};
+}
+
+// How a dense product is cut along K. The plan (and with it every rounding) depends on the sizes
+// alone, so it counts the GB300's pairs of SMs, not the device's.
+constexpr int64_t PLAN_PAIRS = 76;
+constexpr int64_t MAX_PART_BYTES = 32 << 20;  // of all parts: they stay in L2
+struct Cut {
+    int parts, per, height;  // height: of the tiles the parts run on
+};
+// `rows` rows in tiles (of any height, or of `fixed` rows) by n_mb blocks of the other dimension
+// on `pairs` pairs of SMs, K blocks `blocks` long, parts at most max_per of them; `cols` columns
+// of output.
+Cut plan_parts(int64_t rows, int64_t n_mb, int64_t blocks, int64_t cols, int64_t pairs,
+               int64_t max_per, int fixed) {
+    Cut best{1, (int)(blocks < INT32_MAX ? blocks : INT32_MAX), 0};
+    if (rows * n_mb > pairs * 2 * LTILE || blocks < 4) return best;  // enough units as it is
+    int64_t whole;
+    if (fixed > 0)
+        whole = ((rows + fixed - 1) / fixed * n_mb + pairs - 1) / pairs * block_clocks(fixed);
+    else
+        dense_height(rows, n_mb, pairs, &whole);
+    // a part has to save more than the join kernel costs: about 5000 clocks, and the parts' bytes
+    // written and read at 2500 a clock
+    const int64_t join = 5000, bytes = rows * round_up(cols, 4) * 4;
+    int64_t least = whole * blocks - 1000;
+    if (least <= join) return best;
+    for (int64_t h0 = fixed > 0 ? fixed : LTILE; h0 >= 16; h0 -= 16) {
+        const int64_t n = (rows + h0 - 1) / h0;
+        const int64_t h = fixed > 0 ? fixed : round_up((rows + n - 1) / n, 16);
+        const int64_t units = n * n_mb, most = pairs / units;
+        // 2, 3, 5, 8, 12, .. parts and as many as there are pairs for
+        for (int64_t want = 2, next = 0; want <= most; want = next) {
+            next = want * 3 / 2 + want % 2;
+            if (want < most && next > most) next = most;
+            const int64_t per = (blocks + want - 1) / want, parts = (blocks + per - 1) / per;
+            if (parts < 2 || per > max_per || parts * bytes > MAX_PART_BYTES) continue;
+            const int64_t t = per * block_clocks(h) + join + parts * bytes * 2 / 2500;
+            if (t < least) {
+                least = t;
+                best = Cut{(int)parts, (int)per, (int)h};
+            }
+        }
+        if (fixed > 0) break;
+    }
+    return best;
+}
+Cut forward_cut(const mok_linear_config &c) {
+    return plan_parts(c.rows, (c.out_features + 255) / 256, (c.in_features + BK - 1) / BK,
+                      c.out_features, PLAN_PAIRS,
+                      c.out_dtype == MOK_DTYPE_F32 ? SEG_K / BK : INT32_MAX, 0);
+}
+// dx and dW side by side, each with its share of the SMs by its work (whether or not a call asks
+// for both: its bits do not depend on that)
+void backward_cuts(const mok_linear_config &c, Cut *x, Cut *w) {
+    const int64_t kb = (c.in_features + 255) / 256, nb = (c.out_features + 255) / 256;
+    const int64_t x_blocks = (c.out_features + BK - 1) / BK, w_blocks = (c.rows + BK - 1) / BK;
+    const int fixed = c.out_features <= 128 ? 128 : LTILE;
+    int64_t per_block;
+    dense_height(c.rows, kb, PLAN_PAIRS, &per_block);
+    const int64_t cx = per_block * x_blocks;
+    const int64_t cw = (kb * nb + PLAN_PAIRS - 1) / PLAN_PAIRS * block_clocks(fixed) * w_blocks;
+    int64_t px = PLAN_PAIRS * cx / (cx + cw > 0 ? cx + cw : 1);
+    px = px < 1 ? 1 : px > PLAN_PAIRS - 1 ? PLAN_PAIRS - 1 : px;
+    *x = plan_parts(c.rows, kb, x_blocks, c.in_features, px, INT32_MAX, 0);
+    *w = plan_parts(c.out_features, kb, w_blocks, c.in_features, PLAN_PAIRS - px, INT32_MAX, fixed);
+}
+size_t part_bytes(const Cut &c, int64_t rows, int64_t cols) {
+    return c.parts > 1 ? (size_t)c.parts * rows * round_up(cols, 4) * 4 : 0;
+}
+KParts k_parts(const Cut &c, float *out, int64_t rows, int64_t cols) {
+    return KParts{c.parts, c.per, out, round_up(cols, 4), rows * round_up(cols, 4)};
+}
+JoinOut join_out(const KParts &k, int64_t rows, int cols, void *out, int64_t ld) {
+    const int64_t n = rows * ((cols + 3) / 4);
+    return JoinOut{k.out, k.stride, k.ld, k.parts, cols, rows, out, ld,
+                   (uint32_t)((n + JOIN_TPB - 1) / JOIN_TPB)};
 }
 
 // Whether two products of `a` and `b` equal units (ta, tb clocks each) run better side by side
@@ -1524,6 +1810,7 @@ struct LinWs {
     uint16_t *dz;     // [rows][ld_dz]
     int64_t ld_dz;
     float *part;      // [tiles][DZ_PARTS][N]
+    float *kp[2];     // parts of K: y, or dx and dW
 };
 
 size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
@@ -1544,6 +1831,14 @@ size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
         w.ld_dz = round_up(c.out_features, 8);
         w.dz = (uint16_t *)take((size_t)c.rows * w.ld_dz * 2);
         w.part = (float *)take((size_t)w.cap * DZ_PARTS * c.out_features * 4);
+    }
+    if (c.groups == 1 && pass == MOK_LINEAR_BACKWARD) {
+        Cut x, y;
+        backward_cuts(c, &x, &y);
+        w.kp[0] = (float *)take(part_bytes(x, c.rows, c.in_features));
+        w.kp[1] = (float *)take(part_bytes(y, c.out_features, c.in_features));
+    } else if (c.groups == 1) {
+        w.kp[0] = (float *)take(part_bytes(forward_cut(c), c.rows, c.out_features));
     }
     if (o != nullptr) *o = w;
     return off;
@@ -1628,31 +1923,48 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
     carve_linear(*c, MOK_LINEAR_FORWARD, ws, &wk);
     if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
     const int n_mb = (c->out_features + 255) / 256;
-    Tiles tiles = dense_tiles(c->rows, n_mb);
+    Tiles tiles;
+    Cut cut{1, 0, 0};
     if (grouped(starts)) {
         tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
         MOK_OP_LAUNCH(OP_LINEAR_TILES, 1,
                       launch_edge(linear_tiles_kernel, 1, MAX_G, 0, 1, stream, starts, counts,
                                   c->groups, c->rows, wk.list, wk.cap, wk.valid, wk.first, status));
+    } else {
+        cut = forward_cut(*c);
+        int64_t t;
+        tiles = dense_tiles(c->rows, cut.parts > 1 ? cut.height
+                                                   : dense_height(c->rows, n_mb, sm_pairs(), &t));
     }
+    const KParts kp = k_parts(cut, wk.kp[0], c->rows, c->out_features);
     const bool f32 = c->out_dtype == MOK_DTYPE_F32;
     CUtensorMap ma, mb;
     if (map_w(&ma, w, c->groups, c->out_features, c->in_features, c->ld_w, 128) != cudaSuccess ||
         map2d(&mb, x, c->rows, c->in_features, c->ld_in, 32) != cudaSuccess)
         return MOK_ERR_CUDA;
-    const int segs = f32 ? (c->in_features + SEG_K - 1) / SEG_K : 1;
-    const int64_t units = tiles.cap * n_mb;
+    const int segs = f32 && cut.parts == 1 ? (c->in_features + SEG_K - 1) / SEG_K : 1;
+    const int64_t units = tiles.cap * n_mb * cut.parts;
     const bool plain = c->act == MOK_ACT_NONE && !residual && !z;
-#define MOK_FWD(F, PL)                                                                          \
+#define MOK_FWD(...)                                                                            \
     do {                                                                                        \
-        const Fwd<F, PL> p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias, \
-                           (const uint16_t *)residual, y, (uint16_t *)z, c->act, status};       \
+        const Fwd<__VA_ARGS__> p{tiles, n_mb, segs, c->in_features, c->out_features, c->ld_out, bias, \
+                           (const uint16_t *)residual, y, (uint16_t *)z, c->act, status, kp};   \
         MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_linear(ma, mb, p, units, stream));               \
     } while (0)
-    if (!f32) MOK_FWD(false, false);
+    if (cut.parts > 1) MOK_FWD(false, false, true);
+    else if (!f32) MOK_FWD(false, false);
     else if (plain) MOK_FWD(true, true);
     else MOK_FWD(true, false);
 #undef MOK_FWD
+    if (cut.parts > 1) {
+        JoinArgs j = {};
+        j.o[0] = join_out(kp, c->rows, c->out_features, y, c->ld_out);
+        j.bias = bias;
+        j.res = (const uint16_t *)residual;
+        j.z = (uint16_t *)z;
+        j.act = c->act;
+        MOK_OP_LAUNCH(OP_LINEAR_FWD, 1, launch_join(f32, j, stream));
+    }
     return MOK_OK;
 }
 
@@ -1685,13 +1997,20 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     carve_linear(*c, MOK_LINEAR_BACKWARD, ws, &wk);
     if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
     const int n_kb = (Kin + 255) / 256;
-    Tiles tiles = dense_tiles(c->rows, n_kb);
+    Tiles tiles;
+    Cut xc{1, 0, 0}, wc{1, 0, 0};
     if (grouped(starts)) {
         tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
         MOK_OP_LAUNCH(OP_LINEAR_TILES, 1,
                       launch_edge(linear_tiles_kernel, 1, MAX_G, 0, 1, stream, starts, counts,
                                   c->groups, c->rows, wk.list, wk.cap, wk.valid, wk.first, status));
+    } else {
+        backward_cuts(*c, &xc, &wc);
+        int64_t t;
+        tiles = dense_tiles(c->rows, xc.parts > 1 ? xc.height
+                                                  : dense_height(c->rows, n_kb, sm_pairs(), &t));
     }
+    const KParts xk = k_parts(xc, wk.kp[0], c->rows, Kin), wkp = k_parts(wc, wk.kp[1], N, Kin);
     // without an activation a bf16 dy is dz
     const bool direct = !act && !dy32;
     const uint16_t *dz = direct ? (const uint16_t *)dy : wk.dz;
@@ -1715,8 +2034,8 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
                                               c->ld_out, dzo, ld_dz, part, stream));
         if (db && !db_in_dw)
             MOK_OP_LAUNCH(OP_LINEAR_DZ, 1,
-                          launch_edge(linear_db_kernel, (unsigned)(((int64_t)G * N + 255) / 256), 256,
-                                      0, 1, stream, dba, G, N));
+                          launch_edge(linear_db_kernel, (unsigned)(((int64_t)G * N + 31) / 32),
+                                      32 * DB_SLICES, 0, 1, stream, dba, G, N));
     }
     CUtensorMap xa, xb, wa, wb;
     if (dx && (map_w(&xa, w, G, N, Kin, c->ld_w, 64) != cudaSuccess ||
@@ -1726,19 +2045,20 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
                map2d(&wb, dz, c->rows, N, ld_dz, 64) != cudaSuccess))
         return MOK_ERR_CUDA;
     const int n_nb = (N + 255) / 256;
-    const int64_t x_units = dx ? tiles.cap * n_kb : 0;
-    const int64_t w_units = dw ? (int64_t)G * n_kb * n_nb : 0;
+    const int64_t x_units = dx ? tiles.cap * n_kb * xc.parts : 0;
+    const int64_t w_units = dw ? (int64_t)G * n_kb * n_nb * wc.parts : 0;
     const int32_t *valid = grouped(starts) ? wk.valid : nullptr;
     int64_t split = 0, pairs = 0;  // pairs of SMs for dW, and in all, where both go in one launch
     if (dx && dw && !grouped(starts))
-        plan_both(w_units, unit_clocks((c->rows + 63) / 64, LTILE), x_units,
-                  unit_clocks((N + 63) / 64, tiles.height), &split, &pairs);
+        plan_both(w_units, unit_clocks(wc.parts > 1 ? wc.per : (c->rows + 63) / 64, LTILE), x_units,
+                  unit_clocks(xc.parts > 1 ? xc.per : (N + 63) / 64, tiles.height), &split, &pairs);
     DbArgs dwb = dba;
     if (!db_in_dw) dwb.db = nullptr;
-#define MOK_BWD(F)                                                                              \
+#define MOK_BWD(F, CUT)                                                                         \
     do {                                                                                        \
-        const Dx<F> px{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status};                           \
-        const Dw<F> pw{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw, status, dwb}; \
+        const Dx<F, CUT> px{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status, xk};                       \
+        const Dw<F, CUT> pw{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw, status, dwb, \
+                        wkp};                                                                   \
         if (split > 0) {                                                                        \
             MOK_OP_LAUNCH(OP_LINEAR_DX, 1,                                                      \
                           launch_both(wa, wb, pw, xa, xb, px, split, pairs, stream));           \
@@ -1747,9 +2067,17 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
             if (dw) MOK_OP_LAUNCH(OP_LINEAR_DW, 1, launch_linear(wa, wb, pw, w_units, stream)); \
         }                                                                                       \
     } while (0)
-    if (g32) MOK_BWD(true);
-    else MOK_BWD(false);
+    const bool cut = xc.parts > 1 || wc.parts > 1;
+    if (g32 && cut) MOK_BWD(true, true);
+    else if (g32) MOK_BWD(true, false);
+    else if (cut) MOK_BWD(false, true);
+    else MOK_BWD(false, false);
 #undef MOK_BWD
+    JoinArgs j = {};
+    int n = 0;
+    if (dx && xc.parts > 1) j.o[n++] = join_out(xk, c->rows, Kin, dx, c->ld_in);
+    if (dw && wc.parts > 1) j.o[n++] = join_out(wkp, N, Kin, dw, c->ld_w);
+    if (n > 0) MOK_OP_LAUNCH(dx ? OP_LINEAR_DX : OP_LINEAR_DW, 1, launch_join(g32, j, stream));
     return MOK_OK;
 }
 

@@ -252,6 +252,13 @@ CASES = [
     dict(G=40, R=900, Kin=128, N=128, act="relu", out="fp32"),
     dict(G=1, grouped=True, counts=[50], Kin=64, N=64, act="silu", spare=16),
     dict(G=1024, R=2000, Kin=16, N=24, act="gelu"),
+    dict(R=9001, Kin=70, N=61, act="silu"),
+    dict(R=16384, Kin=64, N=64, act="gelu_tanh", grad="fp32"),
+    dict(R=150, Kin=8200, N=140, act="relu", extra=8),
+    dict(R=100, Kin=5000, N=90, out="fp32", res=False, z=False),
+    dict(R=40, Kin=4097, N=515, out="fp32", act="silu"),
+    dict(R=90, Kin=130, N=6001, act="gelu"),
+    dict(R=3000, Kin=520, N=300, grad="fp32", bias=False),
 ]
 ID = lambda k: "-".join("%s%s" % i for i in k.items()).replace(" ", "")  # noqa: E731
 
@@ -396,3 +403,16 @@ def test_refusals():
     assert bwd(z=None) == bad and bwd(dy=None) == bad and bwd(w=None) == bad
     assert bwd(x=None, dx=None, dw=y) == bad
     assert device_ok()
+
+
+@pytest.mark.parametrize("kw", [dict(R=9001, Kin=70, N=61, act="silu"),
+                                dict(R=3000, Kin=520, N=300),
+                                dict(G=5, counts=[1, 0, 3000, 16, 257], Kin=300, N=136)])
+def test_each_gradient_alone_has_the_same_bits(kw):
+    torch = _t()
+    c = Lin(**kw)
+    whole = c.backward()
+    for i in range(3):
+        alone = c.backward(*[i == j for j in range(3)])
+        assert [g is not None for g in alone] == [i == j for j in range(3)]
+        assert torch.equal(alone[i].view(torch.uint8), whole[i].view(torch.uint8))
