@@ -62,6 +62,15 @@ struct Carry<true> {
 // in the stream drains, sets itself up, and waits here before it touches global memory.
 MOK_DEV void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 MOK_DEV void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// So what a kernel reads may still be written while it exists: loads go the ordinary way, not the
+// read-only one.
+MOK_DEV uint4 ld_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 
 // ---------------------------------------------------------------- row tiles
 // A tile is up to `height` consecutive rows of one group. Dense: tile t covers rows
@@ -78,7 +87,10 @@ struct Tiles {
     }
     // (group, first row, end row, whether padding up to a multiple of 16 follows)
     MOK_DEV int4 get(int64_t t) const {
-        if (list != nullptr) return __ldg(reinterpret_cast<const int4 *>(list) + t);
+        if (list != nullptr) {
+            const uint4 v = ld_v4(list + 4 * t);
+            return make_int4((int)v.x, (int)v.y, (int)v.z, (int)v.w);
+        }
         const int64_t r0 = t * height, r1 = r0 + height < rows ? r0 + height : rows;
         return make_int4(0, (int)r0, (int)r1, 0);
     }
@@ -88,9 +100,8 @@ struct Tiles {
 // the group's row count, 0 where its layout breaks the rules; first[g] its first tile (first[G]:
 // their number).
 __global__ void __launch_bounds__(MAX_G)
-    linear_tiles_kernel(const int32_t *__restrict__ starts, const int32_t *__restrict__ counts,
-                        int G, int64_t rows, int32_t *__restrict__ list, int64_t cap,
-                        int32_t *__restrict__ valid, int32_t *__restrict__ first, int *status) {
+    linear_tiles_kernel(const int32_t *starts, const int32_t *counts, int G, int64_t rows,
+                        int32_t *list, int64_t cap, int32_t *valid, int32_t *first, int *status) {
     __shared__ int32_t wsum[MAX_G / 32];
     let_next_start();
     wait_for_previous();
@@ -767,8 +778,8 @@ struct DbArgs {
     float *db;             // [G][N], or nullptr
     // the group's parts: the first, and their number
     MOK_DEV const float *parts(int g, int n, int N, int64_t *count) const {
-        const int64_t t0 = first != nullptr ? __ldg(first + g) : 0;
-        const int64_t t1 = first != nullptr ? __ldg(first + g + 1) : tiles;
+        const int64_t t0 = first != nullptr ? first[g] : 0;
+        const int64_t t1 = first != nullptr ? first[g + 1] : tiles;
         *count = (t1 - t0) * DZ_PARTS;
         return part + t0 * DZ_PARTS * N + n;
     }
@@ -836,8 +847,8 @@ struct Dw {
         const uint32_t per = (uint32_t)n_mb * (uint32_t)n_nb;
         const int part = CUT ? kp.take(u, (uint32_t)G * per) : 0, g = (int)(u / per);
         const uint32_t rest = u % per;
-        return Unit{g, starts != nullptr ? __ldg(starts + g) : 0,
-                    valid != nullptr ? __ldg(valid + g) : (int)rows, 0,
+        return Unit{g, starts != nullptr ? starts[g] : 0,
+                    valid != nullptr ? valid[g] : (int)rows, 0,
                     (int)(rest % (uint32_t)n_mb), (int)(rest / (uint32_t)n_mb), part};
     }
     MOK_DEV LinGeom geom(const Unit &u, int, uint32_t rank) const {
@@ -1246,7 +1257,7 @@ MOK_DEV void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
 
 // 8 inputs from column c of a row, zeros past Kin
 MOK_DEV uint4 load_piece(const uint16_t *row, int c, int Kin) {
-    if (c + 8 <= Kin) return ldg_nc_v4(row + c);
+    if (c + 8 <= Kin) return ld_v4(row + c);
     uint32_t e[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -1356,7 +1367,7 @@ __global__ void __launch_bounds__(256)
             for (int f = 0; f < VEC_F; ++f) {
                 const int v = v0 + u * a.parts * 32;
                 wv[u][f] = make_uint4(0, 0, 0, 0);
-                if (v < nv) wv[u][f] = ldg_nc_v4(wp[f] + (int64_t)v * 8);
+                if (v < nv) wv[u][f] = ld_v4(wp[f] + (int64_t)v * 8);
             }
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
@@ -1365,7 +1376,7 @@ __global__ void __launch_bounds__(256)
             float xf[R][8];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const uint4 q = ldg_nc_v4(xp[r] + (int64_t)v * 8);
+                const uint4 q = ld_v4(xp[r] + (int64_t)v * 8);
                 const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -1430,9 +1441,8 @@ __global__ void __launch_bounds__(256)
 // time, 20480 x 1024 took 47 us); the sums of a column's 32 row lanes are added in lane order.
 template <bool DY32, int ACT>
 __global__ void __launch_bounds__(256)
-    linear_dz_kernel(const void *__restrict__ dy, const uint16_t *__restrict__ z, Tiles tiles,
-                     int N, int64_t ld, uint16_t *__restrict__ dz, int64_t ld_dz,
-                     float *__restrict__ part) {
+    linear_dz_kernel(const void *dy, const uint16_t *z, Tiles tiles, int N, int64_t ld, uint16_t *dz,
+                     int64_t ld_dz, float *part) {
     __shared__ float red[32][65];
     let_next_start();
     wait_for_previous();
@@ -1458,12 +1468,12 @@ __global__ void __launch_bounds__(256)
             a[i] = a2[i] = q[i] = make_uint4(0, 0, 0, 0);
             if (r < r1) {
                 if (DY32) {
-                    a[i] = ldg_nc_v4(static_cast<const float *>(dy) + o);
-                    a2[i] = ldg_nc_v4(static_cast<const float *>(dy) + o + 4);
+                    a[i] = ld_v4(static_cast<const float *>(dy) + o);
+                    a2[i] = ld_v4(static_cast<const float *>(dy) + o + 4);
                 } else {
-                    a[i] = ldg_nc_v4(static_cast<const uint16_t *>(dy) + o);
+                    a[i] = ld_v4(static_cast<const uint16_t *>(dy) + o);
                 }
-                if (ACT != MOK_ACT_NONE) q[i] = ldg_nc_v4(z + o);
+                if (ACT != MOK_ACT_NONE) q[i] = ld_v4(z + o);
             }
         }
     }
