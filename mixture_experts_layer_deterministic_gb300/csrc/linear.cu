@@ -58,20 +58,6 @@ struct Carry<true> {
     float v[2 * Epi<true>::CHUNKS][16];  // by 16 columns
 };
 
-// Launches of one call overlap at their edges: a kernel may be started while the one before it
-// in the stream drains, sets itself up, and waits here before it touches global memory.
-MOK_DEV void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-MOK_DEV void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-// So what a kernel reads may still be written while it exists: loads go the ordinary way, not the
-// read-only one.
-MOK_DEV uint4 ld_v4(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 // ---------------------------------------------------------------- row tiles
 // A tile is up to `height` consecutive rows of one group. Dense: tile t covers rows
 // [t height, ..). Grouped: a list built on the device, int32 [cap][4] = (group, first row,
@@ -1575,29 +1561,6 @@ cudaError_t map_w(CUtensorMap *m, const void *p, int64_t G, int64_t N, int64_t K
 }
 
 int64_t sm_pairs() { return device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1; }
-
-// a launch that may start while the kernel before it drains (its kernel waits for that one
-// itself); cluster: CTAs per cluster
-template <class... KA, class... A>
-cudaError_t launch_edge(void (*kernel)(KA...), dim3 grid, int threads, int smem, int cluster,
-                        cudaStream_t s, const A &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)cluster;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
 
 // a launch of `pairs` clusters of two CTAs; the shared-memory opt-in is set once per device
 template <class... KA, class... A>

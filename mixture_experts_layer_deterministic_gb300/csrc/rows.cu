@@ -50,10 +50,12 @@ inline unsigned grid_for(int64_t items, int per_block, int per_sm) {
 // Every block scans the experts' kept rows for itself (E <= 1024: ten steps in shared
 // memory), then maps its share of the ids: one launch, no order between blocks.
 __global__ void __launch_bounds__(MAX_E)
-    row_map_kernel(const int32_t *__restrict__ idx, const int32_t *__restrict__ counts,
-                   const int32_t *__restrict__ offsets, const int32_t *__restrict__ inv,
-                   int64_t R, int E, int capacity, int64_t n_rows, int32_t *__restrict__ map,
-                   int32_t *__restrict__ starts, int32_t *__restrict__ kept, int *status) {
+    row_map_kernel(const int32_t *idx, const int32_t *counts,
+                   const int32_t *offsets, const int32_t *inv,
+                   int64_t R, int E, int capacity, int64_t n_rows, int32_t *map,
+                   int32_t *starts, int32_t *kept, int *status) {
+    let_next_start();
+    wait_for_previous();
     __shared__ int64_t warp_sum[MAX_E / 32];
     __shared__ int32_t s_start[MAX_E], s_kept[MAX_E], s_off[MAX_E];
     const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
@@ -129,7 +131,7 @@ MOK_DEV int32_t checked_row(int32_t r, int64_t n_rows, int *status) {
     }
     return r;
 }
-MOK_DEV int32_t row_of(const int32_t *__restrict__ map, int64_t f, int64_t n_rows, int *status) {
+MOK_DEV int32_t row_of(const int32_t *map, int64_t f, int64_t n_rows, int *status) {
     return checked_row(map[f], n_rows, status);
 }
 
@@ -170,9 +172,9 @@ MOK_DEV uint4 pack(const float (&v)[Elem<F32>::PER]) {
 // zero rows of the sorted array after each expert's own: item (e, j), row kept[e] + j below
 // the next multiple of 16; one warp per item
 template <bool F32, bool VEC>
-MOK_DEV void zero_pad_row(int64_t item, const int32_t *__restrict__ starts,
-                          const int32_t *__restrict__ kept, int64_t n_rows, int H, int64_t ld,
-                          void *__restrict__ out, int lane) {
+MOK_DEV void zero_pad_row(int64_t item, const int32_t *starts,
+                          const int32_t *kept, int64_t n_rows, int H, int64_t ld,
+                          void *out, int lane) {
     const int e = (int)(item >> 4), j = (int)(item & 15);
     const int64_t n = kept[e];
     if (n + j >= ((n + 15) & ~(int64_t)15)) return;
@@ -193,10 +195,12 @@ MOK_DEV void zero_pad_row(int64_t item, const int32_t *__restrict__ starts,
 // written to the rows of its K copies. Items past the tokens' are the pad rows.
 template <bool F32, bool VEC, int U>
 __global__ void __launch_bounds__(TPB)
-    dispatch_kernel(const void *__restrict__ x, const int32_t *__restrict__ map,
-                    const int32_t *__restrict__ starts, const int32_t *__restrict__ kept,
+    dispatch_kernel(const void *x, const int32_t *map,
+                    const int32_t *starts, const int32_t *kept,
                     int64_t T, int K, int E, int H, int64_t ld_tok, int64_t ld_row,
-                    int64_t n_rows, void *__restrict__ xs, int *status) {
+                    int64_t n_rows, void *xs, int *status) {
+    let_next_start();
+    wait_for_previous();
     constexpr int B = Elem<F32>::BYTES, PER = VEC ? Elem<F32>::PER : 1;
     const int lane = threadIdx.x & 31;
     const int nv = H / PER;                          // whole vectors of a row
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(TPB)
             const bool has_tail = v0 - lane + 32 * U > nv && tc < H;
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                if (v0 + 32 * j < nv) b[j] = ldg_nc_v4(src + (int64_t)(v0 + 32 * j) * 16);
+                if (v0 + 32 * j < nv) b[j] = ld_v4(src + (int64_t)(v0 + 32 * j) * 16);
             if (has_tail) tail = reinterpret_cast<const Raw *>(src)[tc];
             for (int k = 0; k < K; ++k) {
                 const int64_t r = __shfl_sync(0xFFFFFFFFu, rk, k);
@@ -260,7 +264,7 @@ struct Piece {
     MOK_DEV void load(const uint8_t *row, int c, bool in) {
         if (VEC) {
             q = make_uint4(0, 0, 0, 0);
-            if (in) q = ldg_nc_v4(row + (int64_t)c * Elem<F32>::BYTES);
+            if (in) q = ld_v4(row + (int64_t)c * Elem<F32>::BYTES);
         } else {
             e = in ? load_elem<F32>(row, c) : 0.f;
         }
@@ -277,9 +281,11 @@ struct Piece {
 // bounds a warp here. A dropped copy has weight zero and reads as zero.
 template <bool F32, bool VEC, int J, int U>
 __global__ void __launch_bounds__(TPB, COMBINE_BLOCKS)
-    combine_rows_kernel(const void *__restrict__ rows, const int32_t *__restrict__ map,
-                        const float *__restrict__ w, const void *res, int64_t T, int K, int H,
+    combine_rows_kernel(const void *rows, const int32_t *map,
+                        const float *w, const void *res, int64_t T, int K, int H,
                         int64_t ld_tok, int64_t ld_row, int64_t n_rows, void *y, int *status) {
+    let_next_start();
+    wait_for_previous();
     using P = Piece<F32, VEC>;
     constexpr int B = Elem<F32>::BYTES, PER = P::PER;
     const int lane = threadIdx.x & 31;
@@ -408,12 +414,14 @@ __global__ void __launch_bounds__(TPB, COMBINE_BLOCKS)
 // in warp order. Items past the tokens' are the pad rows.
 template <bool F32, bool VEC, int J, bool BLOCK>
 __global__ void __launch_bounds__(TPB, J == FEW ? FEW_BWD_BLOCKS : COMBINE_BLOCKS)
-    combine_bwd_kernel(const void *__restrict__ dy, const void *__restrict__ rows,
-                       const int32_t *__restrict__ map, const int32_t *__restrict__ starts,
-                       const int32_t *__restrict__ kept, const float *__restrict__ w, int64_t T,
+    combine_bwd_kernel(const void *dy, const void *rows,
+                       const int32_t *map, const int32_t *starts,
+                       const int32_t *kept, const float *w, int64_t T,
                        int K, int E, int H, int wsh_, int64_t ld_tok, int64_t ld_row,
-                       int64_t n_rows, void *__restrict__ drows, float *__restrict__ dw,
+                       int64_t n_rows, void *drows, float *dw,
                        int *status) {
+    let_next_start();
+    wait_for_previous();
     using P = Piece<F32, VEC>;
     constexpr int B = Elem<F32>::BYTES, PER = P::PER, U = COMBINE_BWD_U;
     __shared__ float part[WARPS][32];
@@ -649,10 +657,12 @@ MOK_DEV void zero_pad_piece(int64_t item, const int32_t *starts, const int32_t *
 
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(TPB)
-    dispatch_narrow_kernel(const void *__restrict__ x, const int32_t *__restrict__ map,
-                           const int32_t *__restrict__ starts, const int32_t *__restrict__ kept,
+    dispatch_narrow_kernel(const void *x, const int32_t *map,
+                           const int32_t *starts, const int32_t *kept,
                            int64_t T, int K, int E, int H, int sh, int64_t ld_tok, int64_t ld_row,
-                           int64_t n_rows, void *__restrict__ xs, int *status) {
+                           int64_t n_rows, void *xs, int *status) {
+    let_next_start();
+    wait_for_previous();
     constexpr int PER = VEC ? Elem<F32>::PER : 1;
     const int64_t R = T * K, i0 = (int64_t)blockIdx.x * TPB * NARROW + threadIdx.x;
     const int c = (int)(i0 & ((1 << sh) - 1)) * PER;  // the same for all of the thread's rows
@@ -676,10 +686,12 @@ __global__ void __launch_bounds__(TPB)
 
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(TPB)
-    combine_narrow_kernel(const void *__restrict__ rows, const int32_t *__restrict__ map,
-                          const float *__restrict__ w, const void *res, int64_t T, int K, int H,
+    combine_narrow_kernel(const void *rows, const int32_t *map,
+                          const float *w, const void *res, int64_t T, int K, int H,
                           int sh, int64_t ld_tok, int64_t ld_row, int64_t n_rows, void *y,
                           int *status) {
+    let_next_start();
+    wait_for_previous();
     constexpr int PER = VEC ? Elem<F32>::PER : 1;
     const int64_t i = (int64_t)blockIdx.x * TPB + threadIdx.x, t = i >> sh;
     const int c = (int)(i & ((1 << sh) - 1)) * PER;
@@ -714,13 +726,15 @@ __global__ void __launch_bounds__(TPB)
 
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(TPB)
-    combine_bwd_narrow_kernel(const void *__restrict__ dy, const void *__restrict__ rows,
-                              const int32_t *__restrict__ map,
-                              const int32_t *__restrict__ starts,
-                              const int32_t *__restrict__ kept, const float *__restrict__ w,
+    combine_bwd_narrow_kernel(const void *dy, const void *rows,
+                              const int32_t *map,
+                              const int32_t *starts,
+                              const int32_t *kept, const float *w,
                               int64_t T, int K, int E, int H, int sh, int64_t ld_tok,
-                              int64_t ld_row, int64_t n_rows, void *__restrict__ drows,
-                              float *__restrict__ dw, int *status) {
+                              int64_t ld_row, int64_t n_rows, void *drows,
+                              float *dw, int *status) {
+    let_next_start();
+    wait_for_previous();
     constexpr int PER = VEC ? Elem<F32>::PER : 1;
     const int64_t i = (int64_t)blockIdx.x * TPB + threadIdx.x, f = i >> sh;
     const int v0 = (int)(i & ((1 << sh) - 1)), c = v0 * PER;
@@ -792,15 +806,14 @@ cudaError_t launch_build_row_map(const mok_rows_config &c, const int32_t *idx,
                                  const mok_schedule &sch, int32_t *map, int32_t *starts,
                                  int32_t *kept, int *status, cudaStream_t s) {
     const int64_t R = (int64_t)c.T * c.K;
-    row_map_kernel<<<grid_for(R, MAX_E, 1), MAX_E, 0, s>>>(
-        idx, sch.counts, sch.offsets, sch.inv, R, c.E, c.capacity, c.n_rows, map, starts, kept,
-        status);
-    return cudaGetLastError();
+    return launch_edge(row_map_kernel, grid_for(R, MAX_E, 1), MAX_E, 0, 1, s, idx, sch.counts,
+                       sch.offsets, sch.inv, R, c.E, c.capacity, c.n_rows, map, starts, kept, status);
 }
 
 cudaError_t launch_dispatch_rows(const mok_rows_config &c, const void *x, const int32_t *map,
                                  const int32_t *starts, const int32_t *kept, void *xs,
                                  int *status, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     constexpr int U = 4;
     const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
     const int64_t segs = (c.H + per * 32 * U - 1) / (per * 32 * U);
@@ -811,35 +824,37 @@ cudaError_t launch_dispatch_rows(const mok_rows_config &c, const void *x, const 
         const int64_t blocks = narrow_blocks(rows, sh, NARROW);
         if (blocks <= 0x7FFFFFFF) {
 #define CALL(F, V)                                                                          \
-    dispatch_narrow_kernel<F, V><<<(unsigned)blocks, TPB, 0, s>>>(                          \
+    e = launch_edge(dispatch_narrow_kernel<F, V>, (unsigned)blocks, TPB, 0, 1, s, \\
         x, map, starts, kept, c.T, c.K, c.E, c.H, sh, c.ld_tok, c.ld_row, c.n_rows, xs, status)
             MOK_ROWS_CASES(c, CALL);
 #undef CALL
-            return cudaGetLastError();
+            return e;
         }
     }
 #define CALL(F, V)                                                                        \
-    dispatch_kernel<F, V, U><<<grid_for(items, WARPS, DISPATCH_BLOCKS), TPB, 0, s>>>(                  \
-        x, map, starts, kept, c.T, c.K, c.E, c.H, c.ld_tok, c.ld_row, c.n_rows, xs, status)
+    e = launch_edge(dispatch_kernel<F, V, U>, grid_for(items, WARPS, DISPATCH_BLOCKS), TPB, 0, 1, \
+                    s, x, map, starts, kept, c.T, c.K, c.E, c.H, c.ld_tok, c.ld_row, c.n_rows,    \
+                    xs, status)
     MOK_ROWS_CASES(c, CALL);
 #undef CALL
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, const int32_t *map,
                                 const float *w, const void *res, void *y, int *status,
                                 cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     if (c.T == 0) return cudaSuccess;
     const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
     if (const int sh = narrow_shift(c); sh >= 0) {
         const int64_t blocks = narrow_blocks(c.T, sh, 1);
         if (blocks <= 0x7FFFFFFF) {
 #define CALL(F, V)                                                               \
-    combine_narrow_kernel<F, V><<<(unsigned)blocks, TPB, 0, s>>>(                \
+    e = launch_edge(combine_narrow_kernel<F, V>, (unsigned)blocks, TPB, 0, 1, s, \\
         rows, map, w, res, c.T, c.K, c.H, sh, c.ld_tok, c.ld_row, c.n_rows, y, status)
             MOK_ROWS_CASES(c, CALL);
 #undef CALL
-            return cudaGetLastError();
+            return e;
         }
     }
     // rows that two pieces a lane cover gain nothing from longer segments (4 copies of 264 bf16:
@@ -849,7 +864,7 @@ cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, cons
     const int64_t items = (int64_t)c.T * ((c.H + per * 32 * U - 1) / (per * 32 * U));
     const unsigned grid = grid_for(items, WARPS, COMBINE_BLOCKS);
 #define ROWS(F, V, J, U)                                                               \
-    combine_rows_kernel<F, V, J, U><<<grid, TPB, 0, s>>>(                              \
+    e = launch_edge(combine_rows_kernel<F, V, J, U>, grid, TPB, 0, 1, s, \
         rows, map, w, res, c.T, c.K, c.H, c.ld_tok, c.ld_row, c.n_rows, y, status)
 #define CALL(F, V)                           \
     if (few) ROWS(F, V, FEW, FEW_U);         \
@@ -857,13 +872,14 @@ cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, cons
     MOK_ROWS_CASES(c, CALL);
 #undef ROWS
 #undef CALL
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const void *rows,
                                const int32_t *map, const int32_t *starts, const int32_t *kept,
                                const float *w, void *drows, float *dw, int *status,
                                cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     const bool has_pads = starts != nullptr && drows != nullptr;
     if (c.T == 0 && !has_pads) return cudaSuccess;
     if (const int sh = narrow_shift(c); sh >= 0) {
@@ -871,12 +887,12 @@ cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const v
         const int64_t blocks = narrow_blocks(n, sh, 1);
         if (blocks <= 0x7FFFFFFF) {
 #define CALL(F, V)                                                                            \
-    combine_bwd_narrow_kernel<F, V><<<(unsigned)blocks, TPB, 0, s>>>(                         \
+    e = launch_edge(combine_bwd_narrow_kernel<F, V>, (unsigned)blocks, TPB, 0, 1, s, \\
         dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, sh, c.ld_tok, c.ld_row, c.n_rows, \
         drows, dw, status)
             MOK_ROWS_CASES(c, CALL);
 #undef CALL
-            return cudaGetLastError();
+            return e;
         }
     }
     const int per = vectors(c) ? (c.dtype == MOK_DTYPE_F32 ? 4 : 8) : 1;
@@ -887,7 +903,7 @@ cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const v
     const bool few = c.K <= FEW;
     const unsigned grid = grid_for(items, WARPS >> wsh, few ? FEW_BWD_BLOCKS : COMBINE_BLOCKS);
 #define BWD(F, V, J, BLOCK)                                                                    \
-    combine_bwd_kernel<F, V, J, BLOCK><<<grid, TPB, 0, s>>>(                                   \
+    e = launch_edge(combine_bwd_kernel<F, V, J, BLOCK>, grid, TPB, 0, 1, s, \
         dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, wsh, c.ld_tok, c.ld_row, c.n_rows, \
         drows, dw, status)
 #define CALL(F, V)                           \
@@ -901,7 +917,7 @@ cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const v
     MOK_ROWS_CASES(c, CALL);
 #undef BWD
 #undef CALL
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace mok
