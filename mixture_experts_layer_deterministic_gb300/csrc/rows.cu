@@ -824,7 +824,7 @@ cudaError_t launch_dispatch_rows(const mok_rows_config &c, const void *x, const 
         const int64_t blocks = narrow_blocks(rows, sh, NARROW);
         if (blocks <= 0x7FFFFFFF) {
 #define CALL(F, V)                                                                          \
-    e = launch_edge(dispatch_narrow_kernel<F, V>, (unsigned)blocks, TPB, 0, 1, s, \\
+    e = launch_edge(dispatch_narrow_kernel<F, V>, (unsigned)blocks, TPB, 0, 1, s, \
         x, map, starts, kept, c.T, c.K, c.E, c.H, sh, c.ld_tok, c.ld_row, c.n_rows, xs, status)
             MOK_ROWS_CASES(c, CALL);
 #undef CALL
@@ -850,7 +850,7 @@ cudaError_t launch_combine_rows(const mok_rows_config &c, const void *rows, cons
         const int64_t blocks = narrow_blocks(c.T, sh, 1);
         if (blocks <= 0x7FFFFFFF) {
 #define CALL(F, V)                                                               \
-    e = launch_edge(combine_narrow_kernel<F, V>, (unsigned)blocks, TPB, 0, 1, s, \\
+    e = launch_edge(combine_narrow_kernel<F, V>, (unsigned)blocks, TPB, 0, 1, s, \
         rows, map, w, res, c.T, c.K, c.H, sh, c.ld_tok, c.ld_row, c.n_rows, y, status)
             MOK_ROWS_CASES(c, CALL);
 #undef CALL
@@ -887,7 +887,7 @@ cudaError_t launch_combine_bwd(const mok_rows_config &c, const void *dy, const v
         const int64_t blocks = narrow_blocks(n, sh, 1);
         if (blocks <= 0x7FFFFFFF) {
 #define CALL(F, V)                                                                            \
-    e = launch_edge(combine_bwd_narrow_kernel<F, V>, (unsigned)blocks, TPB, 0, 1, s, \\
+    e = launch_edge(combine_bwd_narrow_kernel<F, V>, (unsigned)blocks, TPB, 0, 1, s, \
         dy, rows, map, starts, kept, w, c.T, c.K, c.E, c.H, sh, c.ld_tok, c.ld_row, c.n_rows, \
         drows, dw, status)
             MOK_ROWS_CASES(c, CALL);
