@@ -82,17 +82,17 @@ struct Tiles {
     }
 };
 
-// Each group's rows in tiles of equal height (a multiple of 16, at most LTILE); valid[g] gets
+// Each group's rows in tiles of equal height (a multiple of 16, at most `most`); valid[g] gets
 // the group's row count, 0 where its layout breaks the rules; first[g] its first tile (first[G]:
 // their number).
 __global__ void __launch_bounds__(MAX_G)
     linear_tiles_kernel(const int32_t *starts, const int32_t *counts, int G, int64_t rows,
-                        int32_t *list, int64_t cap, int32_t *valid, int32_t *first, int *status) {
+                        int most, int32_t *list, int64_t cap, int32_t *valid, int32_t *first, int *status) {
     __shared__ int32_t wsum[MAX_G / 32];
     let_next_start();
     wait_for_previous();
     const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
-    int64_t b = 0, n = 0, h = LTILE;
+    int64_t b = 0, n = 0, h = most;
     int32_t nt = 0;
     if (g < G) {
         b = starts[g];
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(MAX_G)
         }
         valid[g] = (int32_t)n;
         if (n > 0) {
-            const int64_t n0 = (n + LTILE - 1) / LTILE;
+            const int64_t n0 = (n + most - 1) / most;
             h = ((n + n0 - 1) / n0 + 15) & ~(int64_t)15;
             nt = (int32_t)((n + h - 1) / h);
         }
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(MAX_G)
     }
 }
 
-int64_t tiles_cap(int64_t rows, int G) { return G + rows / LTILE + 1; }
+int64_t tiles_cap(int64_t rows, int G, int most) { return G + rows / most + 1; }
 
 // ---------------------------------------------------------------- activations
 // exp and the quotient to within 2^-20 of their values: far inside the bf16 rounding of y
@@ -1681,9 +1681,28 @@ Tiles dense_tiles(int64_t rows, int height) {
     return Tiles{nullptr, (rows + height - 1) / height, rows, height};
 }
 
+// The most rows of a tile of a grouped product: fewer than 256 where the groups' tiles by n_mb
+// blocks would leave pairs of SMs idle, by the waves of evenly filled groups (4 groups of 256 rows,
+// 4096 -> 256: 24 us with tiles of up to 256 rows, 17 us of 32). Counted for the GB300's pairs, since
+// the order of db's sum follows the tiles.
+constexpr int64_t PLAN_PAIRS = 76;
+int group_height(int64_t rows, int G, int64_t n_mb) {
+    const int64_t per = rows / G > 0 ? rows / G : 1;
+    int64_t best = INT64_MAX;
+    int best_h = LTILE;
+    for (int h0 = LTILE; h0 >= 32; h0 /= 2) {
+        const int64_t n = (per + h0 - 1) / h0, h = round_up((per + n - 1) / n, 16);
+        const int64_t t = (G * n * n_mb + PLAN_PAIRS - 1) / PLAN_PAIRS * block_clocks(h);
+        if (best == INT64_MAX || t < best * 9 / 10) {
+            best = t;
+            best_h = h0;
+        }
+    }
+    return best_h;
+}
+
 // How a dense product is cut along K. The plan (and with it every rounding) depends on the sizes
 // alone, so it counts the GB300's pairs of SMs, not the device's.
-constexpr int64_t PLAN_PAIRS = 76;
 constexpr int64_t MAX_PART_BYTES = 32 << 20;  // of all parts: they stay in L2
 struct Cut {
     int parts, per, height;  // height: of the tiles the parts run on
@@ -1778,6 +1797,7 @@ void plan_both(int64_t a, int64_t ta, int64_t b, int64_t tb, int64_t *split, int
 struct LinWs {
     int32_t *list;    // past its 16-byte header
     int64_t cap;
+    int height;       // most rows of a tile in it
     int32_t *valid;   // [G]
     int32_t *first;   // [G + 1]
     uint16_t *dz;     // [rows][ld_dz]
@@ -1795,7 +1815,9 @@ size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
         return p;
     };
     LinWs w = {};
-    w.cap = tiles_cap(c.rows, c.groups);
+    const int across = pass == MOK_LINEAR_BACKWARD ? c.in_features : c.out_features;
+    w.height = group_height(c.rows, c.groups, (across + 255) / 256);
+    w.cap = tiles_cap(c.rows, c.groups, w.height);
     int32_t *l = (int32_t *)take(16 + (size_t)w.cap * 16);
     w.list = l != nullptr ? l + 4 : nullptr;
     w.valid = (int32_t *)take((size_t)c.groups * 4);
@@ -1899,10 +1921,11 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
     Tiles tiles;
     Cut cut{1, 0, 0};
     if (grouped(starts)) {
-        tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
+        tiles = Tiles{wk.list, wk.cap, c->rows, wk.height};
         MOK_OP_LAUNCH(OP_LINEAR_TILES, 1,
                       launch_edge(linear_tiles_kernel, 1, MAX_G, 0, 1, stream, starts, counts,
-                                  c->groups, c->rows, wk.list, wk.cap, wk.valid, wk.first, status));
+                                  c->groups, c->rows, wk.height, wk.list, wk.cap, wk.valid, wk.first,
+                                  status));
     } else {
         cut = forward_cut(*c);
         int64_t t;
@@ -1973,10 +1996,11 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     Tiles tiles;
     Cut xc{1, 0, 0}, wc{1, 0, 0};
     if (grouped(starts)) {
-        tiles = Tiles{wk.list, wk.cap, c->rows, LTILE};
+        tiles = Tiles{wk.list, wk.cap, c->rows, wk.height};
         MOK_OP_LAUNCH(OP_LINEAR_TILES, 1,
                       launch_edge(linear_tiles_kernel, 1, MAX_G, 0, 1, stream, starts, counts,
-                                  c->groups, c->rows, wk.list, wk.cap, wk.valid, wk.first, status));
+                                  c->groups, c->rows, wk.height, wk.list, wk.cap, wk.valid, wk.first,
+                                  status));
     } else {
         backward_cuts(*c, &xc, &wc);
         int64_t t;

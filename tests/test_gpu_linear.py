@@ -259,6 +259,8 @@ CASES = [
     dict(R=40, Kin=4097, N=515, out="fp32", act="silu"),
     dict(R=90, Kin=130, N=6001, act="gelu"),
     dict(R=3000, Kin=520, N=300, grad="fp32", bias=False),
+    dict(G=2, counts=[700, 41], Kin=300, N=200, act="silu", out="fp32"),
+    dict(G=3, counts=[0, 1, 600], Kin=2000, N=90, act="gelu_tanh", spare=64),
 ]
 ID = lambda k: "-".join("%s%s" % i for i in k.items()).replace(" ", "")  # noqa: E731
 
