@@ -1222,7 +1222,6 @@ __global__ void __launch_bounds__(JOIN_TPB) linear_join_kernel(const JoinArgs a)
 constexpr int SMALL_ROWS = 32;
 constexpr int SMALL_F = 16;  // features of a warp
 
-
 struct SmallArgs {
     const uint16_t *x, *w, *res;
     const float *bias;
@@ -1316,41 +1315,41 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// One or two rows of up to 8192 features: half the features a warp, whole rows of W side by side
-// on the lanes, products on the fp32 units. Four times as many warps start on a narrow layer
-// (one row, 4096 inputs: 512 features 2.2 against 4.5 us, 4096 features 5.5 against 6.5 us),
-// where a wide one has enough of them (14336 features 32 against 18 us).
-constexpr int VEC_F = 2;  // features of a warp
-
-// UN pieces a lane in flight
-template <int R, int UN, bool F32>
+// One or two rows, and up to four of few features: whole rows of W side by side on the lanes,
+// products on the fp32 units, few features a warp. More warps start on a narrow layer than with 16
+// features a warp (4096 inputs, weights from HBM: one row 512 features 3.2 against 6.0 us, 4096
+// features 7.7 against 9.2, 16384 24 against 29). Two rows read x as often as W with two features
+// a warp, so wide layers take eight (2 rows, 4096 -> 8192: 14.8 against 20.5 us; 4096 -> 512: 4.1
+// against 3.3).
+// F features a warp, UN pieces a lane in flight
+template <int R, int F, int UN, bool F32>
 __global__ void __launch_bounds__(256)
     linear_vector_kernel(const SmallArgs a) {
-    __shared__ float sh[8][VEC_F * R];
+    __shared__ float sh[8][F * R];
     let_next_start();
     wait_for_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = warp % a.parts, slot = warp / a.parts;
-    const int per_block = 8 / a.parts * VEC_F;
-    const int f0 = blockIdx.x * per_block + slot * VEC_F;
+    const int per_block = 8 / a.parts * F;
+    const int f0 = blockIdx.x * per_block + slot * F;
     const int nv = a.Kin / 8;
-    const uint16_t *wp[VEC_F], *xp[R];
+    const uint16_t *wp[F], *xp[R];
 #pragma unroll
-    for (int f = 0; f < VEC_F; ++f)
+    for (int f = 0; f < F; ++f)
         wp[f] = a.w + (int64_t)(f0 + f < a.N ? f0 + f : a.N - 1) * a.ld_w;
 #pragma unroll
     for (int r = 0; r < R; ++r) xp[r] = a.x + (int64_t)(r < a.rows ? r : a.rows - 1) * a.ld_in;
-    float acc[VEC_F][R];
+    float acc[F][R];
 #pragma unroll
-    for (int f = 0; f < VEC_F; ++f)
+    for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[f][r] = 0.f;
     for (int v0 = part * 32 + lane; v0 < nv; v0 += a.parts * 32 * UN) {
-        uint4 wv[UN][VEC_F];
+        uint4 wv[UN][F];
 #pragma unroll
         for (int u = 0; u < UN; ++u)
 #pragma unroll
-            for (int f = 0; f < VEC_F; ++f) {
+            for (int f = 0; f < F; ++f) {
                 const int v = v0 + u * a.parts * 32;
                 wv[u][f] = make_uint4(0, 0, 0, 0);
                 if (v < nv) wv[u][f] = ld_v4(wp[f] + (int64_t)v * 8);
@@ -1371,7 +1370,7 @@ __global__ void __launch_bounds__(256)
                 }
             }
 #pragma unroll
-            for (int f = 0; f < VEC_F; ++f) {
+            for (int f = 0; f < F; ++f) {
                 const uint32_t e[4] = {wv[u][f].x, wv[u][f].y, wv[u][f].z, wv[u][f].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -1387,14 +1386,14 @@ __global__ void __launch_bounds__(256)
         const int c = nv * 8 + lane;
         if (c < a.Kin) {
 #pragma unroll
-            for (int f = 0; f < VEC_F; ++f)
+            for (int f = 0; f < F; ++f)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
                     acc[f][r] = fmaf(bf16_to_f32(wp[f][c]), bf16_to_f32(xp[r][c]), acc[f][r]);
         }
     }
 #pragma unroll
-    for (int f = 0; f < VEC_F; ++f)
+    for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float v = acc[f][r];
@@ -1411,7 +1410,7 @@ __global__ void __launch_bounds__(256)
     if (f >= a.N || r >= a.rows) return;
     float v = 0.f;
     for (int k = 0; k < a.parts; ++k)
-        v += sh[fb / VEC_F * a.parts + k][fb % VEC_F * R + r];
+        v += sh[fb / F * a.parts + k][fb % F * R + r];
     if (a.bias != nullptr) v += a.bias[f];
     const int64_t o = r * a.ld_out + f;
     if (a.z != nullptr) a.z[o] = f32_to_bf16(v);
@@ -1616,26 +1615,43 @@ cudaError_t launch_dz(int act, dim3 grid, const void *dy, const uint16_t *z, con
     return cudaErrorInvalidValue;
 }
 
-// whether a dense call of this size goes to the kernels for few rows: up to 8 rows, and up to 32
-// on layers of up to 8192 features (4096 inputs, 32 rows: 4096 features 12 against 16 us on tiles,
-// 14336 features 33 against 23 us)
-bool few_rows(int64_t rows, int64_t N) { return rows <= 8 || (rows <= SMALL_ROWS && N <= 8192); }
+// Whether a dense call of this size goes to the kernels for few rows; us with weights from HBM,
+// these against the tiles (their K cut):
+//   one row always, two but for wide layers with few inputs (one row, 4096 -> 4096: 7.7 against
+//   10.1; 14336 -> 512: 5.6 against 9.8), up to four of few features (4096 -> 512: 3.8 against
+//   7.5), all on the fp32 units;
+//   up to 16 rows, but for wide layers (4 rows, 4096 -> 16384: 30 against 26) and for few features
+//   over a long K, where the tiles' parts use more SMs (4 rows, 8192 -> 512: 10.2 against 8.3);
+//   up to 32 rows on small layers (1024 -> 1024: 5.3 against 6.5; 4096 -> 4096: 16 against 12).
+// Two rows, 1024 -> 4096: 5.1 on the fp32 units, 3.9 with mma.sync.
+bool vector_rows(int64_t rows, int64_t Kin, int64_t N) {
+    return rows == 1 || (rows == 2 && (N <= 2048 || Kin >= 2048)) || (rows <= 4 && N <= 1024);
+}
+bool few_rows(int64_t rows, int64_t Kin, int64_t N) {
+    if (vector_rows(rows, Kin, N)) return true;
+    if (rows <= 16) return !(N >= 8192 && Kin >= 1024) && !(Kin >= 8192 && N <= 2048);
+    return rows <= SMALL_ROWS && Kin <= 1024 && N <= 4096;
+}
 
 template <bool F32>
 cudaError_t launch_small(SmallArgs a, cudaStream_t s) {
-    const bool vec = a.rows <= 2 && a.N <= 8192;
-    const int per_warp = vec ? VEC_F : SMALL_F;
-    // a warp's features in more parts until there are two blocks an SM, each part keeping a few
-    // steps
+    const bool vec = vector_rows(a.rows, a.Kin, a.N), wide = vec && a.rows == 2 && a.N >= 2048;
+    const int per_warp = vec ? (wide ? 8 : 2) : SMALL_F;
+    // a warp's features in more parts until there are two blocks an SM; on the fp32 units each part
+    // keeps a few steps. With mma.sync also where parts stay empty: a block with fewer features has
+    // fewer outputs to write (32 rows, 64 -> 512: 2.6 us, 7.8 with one part)
     a.parts = 1;
-    while (a.parts < 8 && a.Kin / a.parts >= 256 &&
+    while (a.parts < 8 && (!vec || a.Kin / a.parts >= 256) &&
            (int64_t)a.N * a.parts < (int64_t)2 * device_sm_count() * 8 * per_warp)
         a.parts *= 2;
     const int per_block = 8 / a.parts * per_warp;
     const unsigned grid = (unsigned)((a.N + per_block - 1) / per_block);
     if (vec && a.rows == 1)
-        return launch_edge(linear_vector_kernel<1, 4, F32>, grid, 256, 0, 1, s, a);
-    if (vec) return launch_edge(linear_vector_kernel<2, 4, F32>, grid, 256, 0, 1, s, a);
+        return launch_edge(linear_vector_kernel<1, 2, 4, F32>, grid, 256, 0, 1, s, a);
+    if (wide) return launch_edge(linear_vector_kernel<2, 8, 1, F32>, grid, 256, 0, 1, s, a);
+    if (vec && a.rows == 2)
+        return launch_edge(linear_vector_kernel<2, 2, 4, F32>, grid, 256, 0, 1, s, a);
+    if (vec) return launch_edge(linear_vector_kernel<4, 2, 4, F32>, grid, 256, 0, 1, s, a);
     if (a.rows <= 8) return launch_edge(linear_small_kernel<1, 4, F32>, grid, 256, 0, 1, s, a);
     if (a.rows <= 16) return launch_edge(linear_small_kernel<2, 4, F32>, grid, 256, 0, 1, s, a);
     return launch_edge(linear_small_kernel<4, 2, F32>, grid, 256, 0, 1, s, a);
@@ -1803,7 +1819,8 @@ struct LinWs {
     uint16_t *dz;     // [rows][ld_dz]
     int64_t ld_dz;
     float *part;      // [tiles][DZ_PARTS][N]
-    float *kp[2];     // parts of K: y, or dx and dW
+    Cut cut[2];       // along K: y, or dx and dW (dense)
+    float *kp[2];     // their parts
 };
 
 size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
@@ -1827,27 +1844,26 @@ size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
         w.dz = (uint16_t *)take((size_t)c.rows * w.ld_dz * 2);
         w.part = (float *)take((size_t)w.cap * DZ_PARTS * c.out_features * 4);
     }
-    if (c.groups == 1 && pass == MOK_LINEAR_BACKWARD) {
-        Cut x, y;
-        backward_cuts(c, &x, &y);
-        w.kp[0] = (float *)take(part_bytes(x, c.rows, c.in_features));
-        w.kp[1] = (float *)take(part_bytes(y, c.out_features, c.in_features));
-    } else if (c.groups == 1) {
-        w.kp[0] = (float *)take(part_bytes(forward_cut(c), c.rows, c.out_features));
-    }
+    const Cut whole{1, 0, 0};
+    w.cut[0] = w.cut[1] = whole;
+    if (c.groups == 1 && pass == MOK_LINEAR_BACKWARD)
+        backward_cuts(c, &w.cut[0], &w.cut[1]);
+    else if (c.groups == 1 && !few_rows(c.rows, c.in_features, c.out_features))
+        w.cut[0] = forward_cut(c);
+    w.kp[0] = (float *)take(part_bytes(w.cut[0], c.rows, across));
+    w.kp[1] = (float *)take(part_bytes(w.cut[1], c.out_features, c.in_features));
     if (o != nullptr) *o = w;
     return off;
 }
 
 mok_status check_linear(const mok_linear_config *c, const int32_t *starts, const int32_t *counts,
-                        void *ws, size_t ws_bytes, int pass, int **status) {
+                        void *ws, size_t ws_bytes, int pass, int **status, LinWs *wk) {
     mok_status st = mok_check_linear_config(c);
     if (st != MOK_OK) return st;
     if ((st = current_device_status_word(status)) != MOK_OK) return st;
     if ((starts == nullptr) != (counts == nullptr)) return MOK_ERR_INVALID_ARG;
     if (starts == nullptr && c->groups != 1) return MOK_ERR_INVALID_ARG;
-    if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 ||
-        ws_bytes < carve_linear(*c, pass, nullptr, nullptr))
+    if (carve_linear(*c, pass, ws, wk) > ws_bytes || ws == nullptr || ((uintptr_t)ws & 255u) != 0)
         return MOK_ERR_WORKSPACE;
     return MOK_OK;
 }
@@ -1898,14 +1914,16 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
                               const int32_t *counts, void *y, void *z, void *ws, size_t ws_bytes,
                               cudaStream_t stream) {
     int *status;
-    mok_status st = check_linear(c, starts, counts, ws, ws_bytes, MOK_LINEAR_FORWARD, &status);
+    LinWs wk;
+    mok_status st =
+        check_linear(c, starts, counts, ws, ws_bytes, MOK_LINEAR_FORWARD, &status, &wk);
     if (st != MOK_OK) return st;
     if (c->rows == 0) return MOK_OK;
     if (!x || !w || !y) return MOK_ERR_INVALID_ARG;
     const void *ps[] = {x, w, bias, residual, starts, counts, y, z};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    if (!grouped(starts) && few_rows(c->rows, c->out_features)) {
+    if (!grouped(starts) && few_rows(c->rows, c->in_features, c->out_features)) {
         const SmallArgs a{(const uint16_t *)x, (const uint16_t *)w, (const uint16_t *)residual, bias,
                           y, (uint16_t *)z, c->in_features, c->out_features, (int)c->rows, c->act,
                           1, c->ld_in, c->ld_w, c->ld_out};
@@ -1914,8 +1932,6 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
                                                     : launch_small<false>(a, stream));
         return MOK_OK;
     }
-    LinWs wk;
-    carve_linear(*c, MOK_LINEAR_FORWARD, ws, &wk);
     if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
     const int n_mb = (c->out_features + 255) / 256;
     Tiles tiles;
@@ -1927,7 +1943,7 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
                                   c->groups, c->rows, wk.height, wk.list, wk.cap, wk.valid, wk.first,
                                   status));
     } else {
-        cut = forward_cut(*c);
+        cut = wk.cut[0];
         int64_t t;
         tiles = dense_tiles(c->rows, cut.parts > 1 ? cut.height
                                                    : dense_height(c->rows, n_mb, sm_pairs(), &t));
@@ -1969,7 +1985,9 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
                                const int32_t *counts, void *dx, void *dw, float *db, void *ws,
                                size_t ws_bytes, cudaStream_t stream) {
     int *status;
-    mok_status st = check_linear(c, starts, counts, ws, ws_bytes, MOK_LINEAR_BACKWARD, &status);
+    LinWs wk;
+    mok_status st =
+        check_linear(c, starts, counts, ws, ws_bytes, MOK_LINEAR_BACKWARD, &status, &wk);
     if (st != MOK_OK) return st;
     if (!dx && !dw && !db) return MOK_ERR_INVALID_ARG;
     const bool act = c->act != MOK_ACT_NONE, dy32 = c->out_dtype == MOK_DTYPE_F32;
@@ -1989,8 +2007,6 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
             return MOK_ERR_CUDA;
         return MOK_OK;
     }
-    LinWs wk;
-    carve_linear(*c, MOK_LINEAR_BACKWARD, ws, &wk);
     if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
     const int n_kb = (Kin + 255) / 256;
     Tiles tiles;
@@ -2002,7 +2018,8 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
                                   c->groups, c->rows, wk.height, wk.list, wk.cap, wk.valid, wk.first,
                                   status));
     } else {
-        backward_cuts(*c, &xc, &wc);
+        xc = wk.cut[0];
+        wc = wk.cut[1];
         int64_t t;
         tiles = dense_tiles(c->rows, xc.parts > 1 ? xc.height
                                                   : dense_height(c->rows, n_kb, sm_pairs(), &t));

@@ -234,6 +234,12 @@ CASES = [
     dict(R=2, Kin=515, N=130, act="gelu", out="fp32"),
     dict(R=5, Kin=2050, N=300, act="silu"),
     dict(R=2, Kin=72, N=8200),
+    dict(R=2, Kin=1029, N=2051, act="gelu", extra=8),
+    dict(R=4, Kin=2070, N=77, act="silu"),
+    dict(R=3, Kin=40, N=1024, out="fp32"),
+    dict(R=30, Kin=500, N=500, act="silu"),
+    dict(R=12, Kin=8200, N=100, act="relu"),
+    dict(R=7, Kin=1030, N=8200),
     dict(R=14, Kin=1301, N=77, act="gelu_tanh", extra=8),
     dict(R=27, Kin=640, N=600, act="relu", out="fp32"),
     dict(R=40, Kin=2100, N=300, out="fp32", res=False, z=False),
