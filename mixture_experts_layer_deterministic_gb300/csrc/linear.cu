@@ -15,9 +15,12 @@
 // not the next group's matrix. Every output element is one fp32 sum in an order that depends on the
 // call's sizes alone.
 //
+// A few rows go to kernels of their own, few tiles over a long K to parts of K that a join adds.
+//
 // Per CTA, 320 threads: warp 0 loads (TMA, both CTAs), warp 1 issues the MMAs (rank 0), warps
-// 2-9 drain accumulators, two sets of 256 TMEM columns alternating between units. Every wait is
-// bounded (2 s), after which MOK_ERR_TIMEOUT is recorded and the launch ends.
+// 2-9 drain accumulators (16 warps where sums stay in registers), two sets of 256 TMEM columns
+// alternating between units. Every wait is bounded (2 s), after which MOK_ERR_TIMEOUT is
+// recorded and the launch ends.
 #include <type_traits>
 
 #include "gemm_tc_core.cuh"
@@ -84,7 +87,8 @@ struct Tiles {
 
 // Each group's rows in tiles of equal height (a multiple of 16, at most `most`); valid[g] gets
 // the group's row count, 0 where its layout breaks the rules; first[g] its first tile (first[G]:
-// their number).
+// their number). One block, a scan over the groups: about 2 us, most of them under the kernel
+// before and after.
 __global__ void __launch_bounds__(MAX_G)
     linear_tiles_kernel(const int32_t *starts, const int32_t *counts, int G, int64_t rows,
                         int most, int32_t *list, int64_t cap, int32_t *valid, int32_t *first, int *status) {
@@ -459,6 +463,9 @@ MOK_DEV void emit_plain(Patches &pt, uint32_t c, int nr, const OutRef &o, int x,
     pt.store(o, x, y0, end, g);
 }
 
+// The product. 8192 x 4096 x 4096 137 us, the measured MMA peak; 64 groups of 320 rows, 4096 ->
+// 1024 with GELU and z 140 us (5.6 TB/s and 1230 TFLOP/s: 6.7 waves of tiles of 160 rows, whose
+// operands come slower than their MMAs run).
 // PLAIN: only a bias after the product (no activation, residual or z); CUT: K is cut into parts
 // (a variant of its own: the code for parts cost the router's product 1.3 of 52 us)
 template <bool F32, bool PLAIN, bool CUT = false>
@@ -679,7 +686,8 @@ struct Fwd {
     }
 };
 
-// CUT: K may be cut into parts
+// The input gradient; CUT: K may be cut into parts. 64 groups of 320 rows, 1024 -> 4096: 126 us,
+// 5.9 TB/s (W is most of it); tiles of 160 rows take longer to load than to multiply.
 template <bool F32, bool CUT>
 struct Dx {
     using E = Epi<false>;
@@ -806,6 +814,8 @@ struct DbArgs {
     }
 };
 
+// The weight gradient, K along the group's rows. 64 groups of 320 rows, 1024 x 4096: 139 us,
+// bound by writing 537 MB (132 us at the write-only rate of a memset, 4.06 TB/s).
 template <bool F32, bool CUT>
 struct Dw {
     using E = Epi<false>;
@@ -1132,7 +1142,7 @@ __global__ void __launch_bounds__(P::E::THREADS, 1)
 // ---------------------------------------------------------------- parts of K
 // The sums of the parts in order, for up to two outputs; bias, activation, residual and z (row
 // strides as the output's) belong to the first. A thread takes four columns, loading eight parts
-// at a time.
+// at a time; the parts are still in L2, so launch and latency are what it costs, about 3 us.
 struct JoinOut {
     const float *part;
     int64_t stride, ldp;  // of parts, of rows (a multiple of 4)
@@ -1423,7 +1433,8 @@ __global__ void __launch_bounds__(256)
 // dz = dy act'(z) in bf16 (the products' operand), and the column sums of the unrounded dz. One
 // block per half tile (up to 128 rows) and 64 columns: 8 threads side by side on 8 columns each, 32
 // row lanes of 4 rows each, whose loads are all issued before the first is used (one row at a
-// time, 20480 x 1024 took 47 us); the sums of a column's 32 row lanes are added in lane order.
+// time, 20480 x 1024 took 47 us, so 27; 126 MB are 19 at the copy rate); the sums of a column's 32
+// row lanes are added in lane order.
 template <bool DY32, int ACT>
 __global__ void __launch_bounds__(256)
     linear_dz_kernel(const void *dy, const uint16_t *z, Tiles tiles, int N, int64_t ld, uint16_t *dz,
@@ -1615,6 +1626,9 @@ cudaError_t launch_dz(int act, dim3 grid, const void *dy, const uint16_t *z, con
     return cudaErrorInvalidValue;
 }
 
+// Plans that a result's rounding depends on count the GB300's pairs of SMs, not the device's.
+constexpr int64_t PLAN_PAIRS = 76;
+
 // Whether a dense call of this size goes to the kernels for few rows; us with weights from HBM,
 // these against the tiles (their K cut):
 //   one row always, two but for wide layers with few inputs (one row, 4096 -> 4096: 7.7 against
@@ -1642,7 +1656,7 @@ cudaError_t launch_small(SmallArgs a, cudaStream_t s) {
     // fewer outputs to write (32 rows, 64 -> 512: 2.6 us, 7.8 with one part)
     a.parts = 1;
     while (a.parts < 8 && (!vec || a.Kin / a.parts >= 256) &&
-           (int64_t)a.N * a.parts < (int64_t)2 * device_sm_count() * 8 * per_warp)
+           (int64_t)a.N * a.parts < 2 * (2 * PLAN_PAIRS) * 8 * per_warp)
         a.parts *= 2;
     const int per_block = 8 / a.parts * per_warp;
     const unsigned grid = (unsigned)((a.N + per_block - 1) / per_block);
@@ -1699,9 +1713,8 @@ Tiles dense_tiles(int64_t rows, int height) {
 
 // The most rows of a tile of a grouped product: fewer than 256 where the groups' tiles by n_mb
 // blocks would leave pairs of SMs idle, by the waves of evenly filled groups (4 groups of 256 rows,
-// 4096 -> 256: 24 us with tiles of up to 256 rows, 17 us of 32). Counted for the GB300's pairs, since
-// the order of db's sum follows the tiles.
-constexpr int64_t PLAN_PAIRS = 76;
+// 4096 -> 256: 24 us with tiles of up to 256 rows, 17 us of 32). The order of db's sum follows the
+// tiles.
 int group_height(int64_t rows, int G, int64_t n_mb) {
     const int64_t per = rows / G > 0 ? rows / G : 1;
     int64_t best = INT64_MAX;
@@ -1717,8 +1730,7 @@ int group_height(int64_t rows, int G, int64_t n_mb) {
     return best_h;
 }
 
-// How a dense product is cut along K. The plan (and with it every rounding) depends on the sizes
-// alone, so it counts the GB300's pairs of SMs, not the device's.
+// How a dense product is cut along K, by the sizes alone.
 constexpr int64_t MAX_PART_BYTES = 32 << 20;  // of all parts: they stay in L2
 struct Cut {
     int parts, per, height;  // height: of the tiles the parts run on

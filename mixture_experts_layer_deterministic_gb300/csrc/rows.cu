@@ -192,7 +192,8 @@ MOK_DEV void zero_pad_row(int64_t item, const int32_t *starts,
 
 // ---------------------------------------------------------------- dispatch
 // Work item: (token, segment of 32*U vectors), one warp each; a token's row is read once and
-// written to the rows of its K copies. Items past the tokens' are the pad rows.
+// written to the rows of its K copies. Items past the tokens' are the pad rows. Bound by the
+// writes: 16384 tokens x 10 copies x 4096 bf16 224 us, 6.6 TB/s.
 template <bool F32, bool VEC, int U>
 __global__ void __launch_bounds__(TPB)
     dispatch_kernel(const void *x, const int32_t *map,
@@ -277,7 +278,8 @@ struct Piece {
 
 // Work item: (token, segment of 32*U pieces of 16 bytes), one warp each. Lane k holds row and
 // weight of copy k. The K rows are read in rounds of equal size, at most J rows x U pieces a
-// lane, all loads of a round before the first is used: the rounds' memory latency is what
+// lane, all loads of a round before the first is used (16384 tokens x 10 rows x 4096 bf16 230 us,
+// 6.4 TB/s): the rounds' memory latency is what
 // bounds a warp here. A dropped copy has weight zero and reads as zero.
 template <bool F32, bool VEC, int J, int U>
 __global__ void __launch_bounds__(TPB, COMBINE_BLOCKS)
@@ -411,7 +413,8 @@ __global__ void __launch_bounds__(TPB, COMBINE_BLOCKS)
 // most J: a round's rows are loaded before the first is used, and each lane keeps its part of
 // the round's dot products over all its segments. A butterfly that halves the number of values
 // at each step (9 shuffles for 8 sums, not 40) adds the lanes, and the warps' parts are added
-// in warp order. Items past the tokens' are the pad rows.
+// in warp order. Items past the tokens' are the pad rows. 8192 tokens x 10 rows x 4096 bf16 233 us,
+// 6.1 TB/s; a block a token at any width took 415 us for 32768 x 8 x 264, this 83.
 template <bool F32, bool VEC, int J, bool BLOCK>
 __global__ void __launch_bounds__(TPB, J == FEW ? FEW_BWD_BLOCKS : COMBINE_BLOCKS)
     combine_bwd_kernel(const void *dy, const void *rows,
