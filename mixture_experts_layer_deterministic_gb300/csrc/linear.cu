@@ -72,7 +72,7 @@ struct Tiles {
     int height;
     MOK_DEV int64_t count() const {
         if (list == nullptr) return (rows + height - 1) / height;
-        return list[-4] < cap ? list[-4] : cap;
+        return list[-4];
     }
     // (group, first row, end row, whether padding up to a multiple of 16 follows)
     MOK_DEV int4 get(int64_t t) const {
@@ -87,23 +87,44 @@ struct Tiles {
 
 // Each group's rows in tiles of equal height (a multiple of 16, at most `most`); valid[g] gets
 // the group's row count, 0 where its layout breaks the rules; first[g] its first tile (first[G]:
-// their number). One block, a scan over the groups: about 2 us, most of them under the kernel
-// before and after.
+// their number). One block, two scans over the groups: about 2 us, most of them under the kernel
+// before and after. Groups that count lie apart inside `rows`, so their tiles number at most
+// tiles_cap and fit 31 bits.
 __global__ void __launch_bounds__(MAX_G)
     linear_tiles_kernel(const int32_t *starts, const int32_t *counts, int G, int64_t rows,
-                        int most, int32_t *list, int64_t cap, int32_t *valid, int32_t *first, int *status) {
+                        int most, int32_t *list, int32_t *valid, int32_t *first, int *status) {
     __shared__ int32_t wsum[MAX_G / 32];
+    __shared__ int64_t wend[MAX_G / 32];
     let_next_start();
     wait_for_previous();
     const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
-    int64_t b = 0, n = 0, h = most;
+    int64_t b = 0, n = 0, h = most, end = 0;  // end: of the group's rows and their padding
     int32_t nt = 0;
-    if (g < G) {
+    bool ok = g < G;
+    if (ok) {
         b = starts[g];
         n = counts[g];
         const int64_t e = starts[g + 1];
         // the padding after the rows is written too, so it has to lie inside the group
-        if (n < 0 || b < 0 || (b & 15) != 0 || b + ((n + 15) & ~(int64_t)15) > e || e > rows) {
+        ok = n >= 0 && b >= 0 && (b & 15) == 0 && b + ((n + 15) & ~(int64_t)15) <= e && e <= rows;
+        if (ok) end = b + ((n + 15) & ~(int64_t)15);
+    }
+    // the largest end of the groups before this one: a group that begins below it would write
+    // rows that are another's already
+    int64_t before = end;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o && u > before) before = u;
+    }
+    if (lane == 31) wend[warp] = before;
+    before = __shfl_up_sync(0xFFFFFFFFu, before, 1);
+    if (lane == 0) before = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w)
+        if (wend[w] > before) before = wend[w];
+    if (g < G) {
+        if (!ok || b < before) {
             raise_status(status, MOK_ERR_DEVICE_INVARIANT);
             n = 0;
         }
@@ -124,18 +145,11 @@ __global__ void __launch_bounds__(MAX_G)
     __syncthreads();
     int32_t at = v - nt;
     for (int w = 0; w < warp; ++w) at += wsum[w];
-    if (g < G) first[g] = (int32_t)(at < cap ? at : cap);
-    if (g == MAX_G - 1) {
-        // overlapping groups can ask for more tiles than there are rows for
-        const int32_t total = at + nt;
-        list[-4] = first[G] = (int32_t)(total < cap ? total : cap);
-        if (total > cap) raise_status(status, MOK_ERR_DEVICE_INVARIANT);
-    }
+    if (g < G) first[g] = at;
+    if (g == MAX_G - 1) list[-4] = first[G] = at + nt;
     for (int32_t i = 0; i < nt; ++i) {
-        const int64_t s = (int64_t)at + i;
-        if (s >= cap) break;
         const int64_t r0 = b + i * h, r1 = r0 + h < b + n ? r0 + h : b + n;
-        reinterpret_cast<int4 *>(list)[s] =
+        reinterpret_cast<int4 *>(list)[at + i] =
             make_int4(g, (int32_t)r0, (int32_t)r1, i == nt - 1 ? 1 : 0);
     }
 }
@@ -1952,7 +1966,7 @@ mok_status mok_linear_forward(const mok_linear_config *c, const void *x, const v
         tiles = Tiles{wk.list, wk.cap, c->rows, wk.height};
         MOK_OP_LAUNCH(OP_LINEAR_TILES, 1,
                       launch_edge(linear_tiles_kernel, 1, MAX_G, 0, 1, stream, starts, counts,
-                                  c->groups, c->rows, wk.height, wk.list, wk.cap, wk.valid, wk.first,
+                                  c->groups, c->rows, wk.height, wk.list, wk.valid, wk.first,
                                   status));
     } else {
         cut = wk.cut[0];
@@ -2027,7 +2041,7 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
         tiles = Tiles{wk.list, wk.cap, c->rows, wk.height};
         MOK_OP_LAUNCH(OP_LINEAR_TILES, 1,
                       launch_edge(linear_tiles_kernel, 1, MAX_G, 0, 1, stream, starts, counts,
-                                  c->groups, c->rows, wk.height, wk.list, wk.cap, wk.valid, wk.first,
+                                  c->groups, c->rows, wk.height, wk.list, wk.valid, wk.first,
                                   status));
     } else {
         xc = wk.cut[0];

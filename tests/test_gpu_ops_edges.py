@@ -1,0 +1,75 @@
+"""The operators around the layer at the edges of their definitions: layouts that break the rules,
+schedules that do not fit, non-finite values, long sums kept in fp32.
+
+Tolerances are those of test_gpu_linear.py and test_gpu_rows.py, and for fp32 gradients: dz enters
+a product as two bf16 values, each rounded to nearest, so within 2^-17 of itself; a sum in
+segments of 1024 terms is within 2^-19 of its norm (twice the 8.9e-7 that 4096 terms of one sign
+pattern after another gave in four segments; one run of 4096 terms gave 3.9e-6, and the error of
+a run grows with its length)."""
+import pytest
+
+from mixture_experts_layer_deterministic_gb300 import binding as B
+from test_gpu_linear import Lin, check_forward, dot_rel
+
+pytestmark = pytest.mark.gpu
+
+
+def _t():
+    import torch
+    return torch
+
+
+def i32(a):
+    return _t().tensor(a, dtype=_t().int32, device="cuda")
+
+
+def norm_rel(got, ref):
+    return float((got.double() - ref).norm() / ref.norm())
+
+
+def test_a_group_that_overlaps_an_earlier_one_counts_as_empty():
+    """starts that fall: the third group's rows are the first one's. It is reported and takes no
+    part, so no row has two writers."""
+    torch = _t()
+    c = Lin(G=3, counts=[20, 0, 20], Kin=64, N=40)
+    clean = check_forward(c)[0]
+    c.d_starts, c.d_counts = i32([0, 32, 0, 32]), i32([20, 5, 20])
+    y, _ = c.forward()
+    assert B.mok_read_device_status()[1] == B.MOK_ERR_DEVICE_INVARIANT
+    B.mok_clear_device_status()
+    assert torch.equal(y[:32, :40], clean[:32, :40])
+    assert bool((y[32:] == 7).all())
+    _, dw, db = c.backward()
+    assert B.mok_read_device_status()[1] == B.MOK_ERR_DEVICE_INVARIANT
+    B.mok_clear_device_status()
+    assert bool((dw[:40, :64] != 0).any())
+    assert bool((dw[40:, :64] == 0).all()) and bool((db[40:120] == 0).all())
+
+
+def test_falling_starts_over_more_than_2_to_the_30_rows():
+    """Every other group asks for all of 2^30 rows and more: the first has them, the others count
+    as empty, and no tile is counted twice. Arrays of more than 2^31 elements."""
+    torch = _t()
+    rows, G = (1 << 30) + 4096, 1024
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    cfg = B.make_linear(rows, 8, 8, G)
+    assert B.mok_check_linear_config(cfg) == B.MOK_OK
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, y = torch.zeros(rows, 8, **bf), torch.full((rows, 8), 7.0, **bf)
+    w = torch.randn(G, 8, 8, device="cuda").to(torch.bfloat16)
+    live = [slice(0, 300), slice((1 << 30) - 150, (1 << 30) + 150), slice(rows - 300, rows)]
+    for s in live:
+        x[s] = torch.randn(300, 8, device="cuda").to(torch.bfloat16)
+    starts, counts = i32([0, rows] * (G // 2) + [0]), i32([rows, 0] * (G // 2))
+    n = B.mok_linear_workspace_size(cfg, B.MOK_LINEAR_FORWARD)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    B.check(B.mok_linear_forward(cfg, x, w, None, None, starts, counts, y, None, ws, n))
+    assert B.mok_read_device_status()[1] == B.MOK_ERR_DEVICE_INVARIANT
+    B.mok_clear_device_status()
+    for s in live:
+        ref = x[s].double() @ w[0].double().T
+        mag = x[s].double().abs() @ w[0].double().abs().T
+        assert bool(((y[s].double() - ref).abs() <= dot_rel(8) * mag + 2.0 ** -8 * ref.abs()).all())
+        y[s] = 0
+    assert int(torch.count_nonzero(y)) == 0
