@@ -179,6 +179,39 @@ def quantize_mxfp8(src, stream=None):
 
 # ------------------------------------------------- operators around the layer (mok_ops.h)
 
+def _mok_dtype(dtype):
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("fp32 or bf16, not %s" % dtype)
+    return B.MOK_DTYPE_F32 if dtype == torch.float32 else B.MOK_DTYPE_BF16
+
+
+def _check_kind(name, t, dtype, device):
+    if t.dtype != dtype or t.device.type != device.type:
+        raise ValueError("%s: %s on %s, not %s on %s" % (name, dtype, device.type, t.dtype,
+                                                         t.device.type))
+
+
+def _check_matrix(name, t, dtype, device, rows, cols, ld):
+    """`rows` rows of `cols` elements, `ld` apart (more of either does not matter); None passes."""
+    if t is None:
+        return
+    _check_kind(name, t, dtype, device)
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols or \
+            (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != ld):
+        raise ValueError("%s: [%d][%d] with %d elements between rows, not %s with strides %s" %
+                         (name, rows, cols, ld, list(t.shape), list(t.stride())))
+
+
+def _check_vector(name, t, dtype, device, n):
+    """`n` packed elements of any shape; None passes."""
+    if t is None:
+        return
+    _check_kind(name, t, dtype, device)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s: %d packed elements, not %s with strides %s" %
+                         (name, n, list(t.shape), list(t.stride())))
+
+
 def _row_stride(t):
     if t.stride(-1) != 1:
         raise ValueError("rows must be contiguous along their last axis")
@@ -248,16 +281,27 @@ class TokenSort:
 class Linear:
     """A linear layer and its workspaces: one matrix, or with groups > 1 one per group of sorted
     rows (forward and backward then take the TokenSort that sorted them). Weights are
-    [groups][out][in] bf16; rows of x, y, z, dy, dx start on 16-byte boundaries."""
+    [groups][out][in] bf16; rows of x, y, z, dy, dx and of the weights start on 16-byte
+    boundaries, which packed rows do where their width is a multiple of 8 (`weights()` makes an
+    array for any width). y and dy have out_dtype, dx and dw grad_dtype, bias and db are fp32,
+    everything else is bf16. Arrays that do not fit raise ValueError before anything is
+    launched."""
 
     def __init__(self, rows, in_features, out_features, groups=1, act=B.MOK_ACT_NONE,
                  out_dtype=torch.bfloat16, grad_dtype=torch.bfloat16, device="cuda"):
-        dt = lambda t: B.MOK_DTYPE_F32 if t == torch.float32 else B.MOK_DTYPE_BF16  # noqa: E731
-        self.cfg = B.make_linear(rows, in_features, out_features, groups, act, dt(out_dtype),
-                                 dt(grad_dtype))
+        self.cfg = B.make_linear(rows, in_features, out_features, groups, act,
+                                 _mok_dtype(out_dtype), _mok_dtype(grad_dtype))
         B.check(B.mok_check_linear_config(self.cfg), "linear config")
+        self.out_dtype, self.grad_dtype = out_dtype, grad_dtype
         self.device = torch.device(device)
         self.ws = [None, None]
+
+    def weights(self, dtype=torch.bfloat16):
+        """Zeros [groups][out][in] whose rows lie as the layer reads them: a view of a packed
+        [groups][out][ld_w] array."""
+        c = self.cfg
+        return torch.zeros(c.groups, c.out_features, c.ld_w, dtype=dtype,
+                           device=self.device)[..., :c.in_features]
 
     def _ws(self, which):
         if self.ws[which] is None:
@@ -265,21 +309,54 @@ class Linear:
             self.ws[which] = (_empty(n, torch.uint8, self.device), n)
         return self.ws[which]
 
-    def _check(self, wide, out):
-        for t, ld in [(t, self.cfg.ld_in) for t in wide] + [(t, self.cfg.ld_out) for t in out]:
-            if t is not None and _row_stride(t) != ld:
-                raise ValueError("rows have %d elements between them, not %d" %
-                                 (_row_stride(t), ld))
+    def _check_rows(self, **arrays):
+        """name=(array or None, dtype): arrays of the layer's rows, x and dx of its inputs, the
+        others of its outputs."""
+        c = self.cfg
+        for name, (t, dtype) in arrays.items():
+            inputs = name in ("x", "dx")
+            _check_matrix(name, t, dtype, self.device, c.rows,
+                          c.in_features if inputs else c.out_features,
+                          c.ld_in if inputs else c.ld_out)
+
+    def _check_weights(self, **arrays):
+        c = self.cfg
+        for name, (t, dtype) in arrays.items():
+            rows = c.groups * c.out_features
+            if t is not None and t.dim() == 3:
+                if t.shape[0] != c.groups or t.shape[1] != c.out_features or \
+                        (c.groups > 1 and t.stride(0) != c.out_features * c.ld_w):
+                    raise ValueError("%s: [%d][%d][%d] with %d elements between rows, not %s with "
+                                     "strides %s" % (name, c.groups, c.out_features,
+                                                     c.in_features, c.ld_w, list(t.shape),
+                                                     list(t.stride())))
+                t, rows = t[0], c.out_features  # the groups follow one another
+            _check_matrix(name, t, dtype, self.device, rows, c.in_features, c.ld_w)
+
+    def _check_sort(self, sort):
+        if sort is None and self.cfg.groups > 1:
+            raise ValueError("%d groups of rows need the TokenSort that made them" %
+                             self.cfg.groups)
+        if sort is not None and sort.E != self.cfg.groups:
+            raise ValueError("the sort has %d groups, the layer %d" % (sort.E, self.cfg.groups))
 
     def forward(self, x, w, y, bias=None, residual=None, z=None, sort=None, stream=None):
-        self._check((x,), (y, residual, z))
+        bf, n = torch.bfloat16, self.cfg.groups * self.cfg.out_features
+        self._check_rows(x=(x, bf), y=(y, self.out_dtype), residual=(residual, bf), z=(z, bf))
+        self._check_weights(w=(w, bf))
+        _check_vector("bias", bias, torch.float32, self.device, n)
+        self._check_sort(sort)
         ws, n = self._ws(B.MOK_LINEAR_FORWARD)
         B.check(B.mok_linear_forward(self.cfg, x, w, bias, residual, sort and sort.starts,
                                      sort and sort.kept, y, z, ws, n, stream), "linear forward")
         return y
 
     def backward(self, x, w, dy, z=None, dx=None, dw=None, db=None, sort=None, stream=None):
-        self._check((x, dx), (dy, z))
+        bf, n = torch.bfloat16, self.cfg.groups * self.cfg.out_features
+        self._check_rows(x=(x, bf), dy=(dy, self.out_dtype), z=(z, bf), dx=(dx, self.grad_dtype))
+        self._check_weights(w=(w, bf), dw=(dw, self.grad_dtype))
+        _check_vector("db", db, torch.float32, self.device, n)
+        self._check_sort(sort)
         ws, n = self._ws(B.MOK_LINEAR_BACKWARD)
         B.check(B.mok_linear_backward(self.cfg, x, w, z, dy, sort and sort.starts,
                                       sort and sort.kept, dx, dw, db, ws, n, stream),

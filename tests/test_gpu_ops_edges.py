@@ -9,7 +9,7 @@ a run grows with its length)."""
 import pytest
 
 from mixture_experts_layer_deterministic_gb300 import binding as B
-from test_gpu_linear import Lin, check_forward, dot_rel
+from test_gpu_linear import Lin, check_forward, device_ok, dot_rel
 
 pytestmark = pytest.mark.gpu
 
@@ -21,10 +21,6 @@ def _t():
 
 def i32(a):
     return _t().tensor(a, dtype=_t().int32, device="cuda")
-
-
-def norm_rel(got, ref):
-    return float((got.double() - ref).norm() / ref.norm())
 
 
 def test_a_group_that_overlaps_an_earlier_one_counts_as_empty():
@@ -73,3 +69,25 @@ def test_falling_starts_over_more_than_2_to_the_30_rows():
         assert bool(((y[s].double() - ref).abs() <= dot_rel(8) * mag + 2.0 ** -8 * ref.abs()).all())
         y[s] = 0
     assert int(torch.count_nonzero(y)) == 0
+
+
+def test_linear_helper_with_an_odd_width():
+    """1001 inputs: weights and their gradient in rows 1008 apart, as weights() makes them."""
+    torch = _t()
+    from mixture_experts_layer_deterministic_gb300.buffers import Linear
+    lin = Linear(70, 1001, 77, grad_dtype=torch.float32)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, y = torch.randn(70, 1008, **bf)[:, :1001], torch.zeros(70, 80, **bf)[:, :77]
+    w, dw, dx = lin.weights(), lin.weights(torch.float32), torch.zeros(70, 1008, device="cuda")
+    w.copy_(torch.randn(77, 1001, device="cuda") / 32)
+    dy = torch.randn(70, 80, **bf)[:, :77]
+    lin.forward(x, w, y)
+    lin.backward(x, w, dy, dx=dx, dw=dw)
+    assert device_ok()
+    xd, wd, dyd = x.double(), w[0].double(), dy.double()
+    for got, a, b, n, u in ((y, xd, wd.T, 1001, 2.0 ** -8), (dx[:, :1001], dyd, wd, 77, 0.0),
+                            (dw[0], dyd.T, xd, 70, 0.0)):
+        e = dot_rel(n) * (a.abs() @ b.abs())
+        assert bool(((got.double() - a @ b).abs() <= e + u * ((a @ b).abs() + e)).all())
+    with pytest.raises(ValueError):
+        lin.forward(x, torch.zeros(1, 77, 1001, **bf), y)
