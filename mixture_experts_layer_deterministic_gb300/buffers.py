@@ -212,25 +212,21 @@ def _check_vector(name, t, dtype, device, n):
                          (name, n, list(t.shape), list(t.stride())))
 
 
-def _row_stride(t):
-    if t.stride(-1) != 1:
-        raise ValueError("rows must be contiguous along their last axis")
-    return t.stride(0)
-
-
 class TokenSort:
     """Tokens sorted by expert and back: the row map of a schedule and the four passes over it.
     Sorted arrays come from `rows()`: expert e owns rows starts[e] .. starts[e] + kept[e],
-    padded with zero rows to a multiple of 16."""
+    padded with zero rows to a multiple of 16. Tokens and rows are bf16 or fp32 (`dtype`) in rows
+    that start on 16-byte boundaries, ids int32, weights fp32. Arrays that do not fit raise
+    ValueError before anything is launched."""
 
     def __init__(self, T, K, E, H, dtype=torch.bfloat16, capacity=0, device="cuda"):
+        kind = _mok_dtype(dtype)
         per = 4 if dtype == torch.float32 else 8
         self.T, self.K, self.E, self.H, self.dtype = T, K, E, H, dtype
         self.ld = (H + per - 1) // per * per
         self.device = torch.device(device)
         self.cfg = B.make_rows(T, K, E, H, capacity=capacity, ld_tok=self.ld, ld_row=self.ld,
-                               dtype=B.MOK_DTYPE_F32 if dtype == torch.float32
-                               else B.MOK_DTYPE_BF16)
+                               dtype=kind)
         B.check(B.mok_check_rows_config(self.cfg), "rows config")
         self.n_rows = int(self.cfg.n_rows)
         self.map = _empty(T * K, torch.int32, self.device)
@@ -244,35 +240,50 @@ class TokenSort:
         return torch.zeros(self.n_rows, (w + per - 1) // per * per, dtype=self.dtype,
                            device=self.device)[:, :w]
 
-    def _check(self, tokens=(), rows=()):
-        for t in (*tokens, *rows):
-            if t is not None and (t.dtype != self.dtype or _row_stride(t) != self.ld):
-                raise ValueError("tokens and rows are %s with %d elements between rows" %
-                                 (self.dtype, self.ld))
+    def _check(self, n, /, **arrays):
+        for name, t in arrays.items():
+            _check_matrix(name, t, self.dtype, self.device, n, self.H, self.ld)
+
+    def _check_ids(self, name, t, dtype):
+        """One value per routed id (the helpers' own arrays have one where there are no ids)."""
+        if t is not None and self.T * self.K == 0:
+            return _check_kind(name, t, dtype, self.device)
+        _check_vector(name, t, dtype, self.device, self.T * self.K)
 
     def build(self, idx, sched, stream=None):
         """The row map of `sched` (a Schedule built from idx [T][K])."""
+        self._check_ids("idx", idx, torch.int32)
+        if sched.R != self.T * self.K or sched.counts.numel() != self.E:
+            raise ValueError("the schedule has %d ids of %d experts, the sort %d of %d" %
+                             (sched.R, sched.counts.numel(), self.T * self.K, self.E))
         B.check(B.mok_build_row_map(self.cfg, idx, sched.struct, self.map, self.starts, self.kept,
                                     stream), "row map")
 
     def dispatch(self, x, xs, stream=None):
-        self._check((x,), (xs,))
+        self._check(self.T, x=x)
+        self._check(self.n_rows, xs=xs)
         B.check(B.mok_dispatch(self.cfg, x, self.map, self.starts, self.kept, xs, stream),
                 "dispatch")
         return xs
 
     def dispatch_backward(self, dxs, dx, stream=None):
-        self._check((dx,), (dxs,))
+        self._check(self.T, dx=dx)
+        self._check(self.n_rows, dxs=dxs)
         B.check(B.mok_dispatch_backward(self.cfg, dxs, self.map, dx, stream), "dispatch backward")
         return dx
 
     def combine(self, rows, topk_w, y, residual=None, stream=None):
-        self._check((y, residual), (rows,))
+        self._check(self.T, y=y, residual=residual)
+        self._check(self.n_rows, rows=rows)
+        self._check_ids("topk_w", topk_w, torch.float32)
         B.check(B.mok_combine(self.cfg, rows, self.map, topk_w, residual, y, stream), "combine")
         return y
 
     def combine_backward(self, dy, rows, topk_w, drows, d_topk_w, stream=None):
-        self._check((dy,), (rows, drows))
+        self._check(self.T, dy=dy)
+        self._check(self.n_rows, rows=rows, drows=drows)
+        self._check_ids("topk_w", topk_w, torch.float32)
+        self._check_ids("d_topk_w", d_topk_w, torch.float32)
         B.check(B.mok_combine_backward(self.cfg, dy, rows, self.map, self.starts, self.kept,
                                        topk_w, drows, d_topk_w, stream), "combine backward")
         return drows

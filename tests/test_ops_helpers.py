@@ -5,7 +5,7 @@ import pytest
 from mixture_experts_layer_deterministic_gb300 import binding as B
 
 torch = pytest.importorskip("torch")
-from mixture_experts_layer_deterministic_gb300.buffers import Linear  # noqa: E402
+from mixture_experts_layer_deterministic_gb300.buffers import Linear, TokenSort  # noqa: E402
 
 F32, BF, F16 = torch.float32, torch.bfloat16, torch.float16
 
@@ -14,7 +14,8 @@ F32, BF, F16 = torch.float32, torch.bfloat16, torch.float16
 def calls(monkeypatch):
     """Names of the entry points that were reached, which do nothing."""
     seen = []
-    for name in ("mok_linear_forward", "mok_linear_backward"):
+    for name in ("mok_linear_forward", "mok_linear_backward", "mok_build_row_map", "mok_dispatch",
+                 "mok_dispatch_backward", "mok_combine", "mok_combine_backward"):
         monkeypatch.setattr(B, name, lambda *a, _n=name: seen.append(_n) or B.MOK_OK)
     return seen
 
@@ -117,3 +118,64 @@ def test_linear_refuses_other_types_and_a_sort_of_other_groups(calls):
     sort.E = 3
     a.lin.forward(**a.fwd, sort=sort)
     a.lin.backward(**a.bwd, sort=sort)
+
+
+class Sorted:
+    """A TokenSort of 20 tokens with 3 of 7 experts, 101 columns, and arrays that fit it."""
+
+    def __init__(self, dtype, T=20):
+        self.sort = TokenSort(T, 3, 7, 101, dtype=dtype, device="cpu")
+        ld = 104
+        tok = lambda: torch.zeros(T, ld, dtype=dtype)[:, :101]  # noqa: E731
+        r, w = self.sort.rows, lambda: torch.zeros(T, 3)  # noqa: E731
+        self.sched = type("Sched", (), dict(R=3 * T, counts=torch.zeros(7), struct=None))()
+        self.args = dict(dispatch=dict(x=tok(), xs=r()), dispatch_backward=dict(dxs=r(), dx=tok()),
+                         combine=dict(rows=r(), topk_w=w(), y=tok(), residual=tok()),
+                         combine_backward=dict(dy=tok(), rows=r(), topk_w=w(), drows=r(),
+                                               d_topk_w=w()))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [20, 1])
+def test_sort_takes_what_fits(calls, dtype, T):
+    s = Sorted(dtype, T)
+    s.sort.build(torch.zeros(3 * T, dtype=torch.int32), s.sched)
+    for name, args in s.args.items():
+        getattr(s.sort, name)(**args)
+    s.sort.combine(s.sort.rows(), None, s.args["combine"]["y"])  # weights of one, no residual
+    s.sort.combine_backward(s.args["combine"]["y"], None, None, s.sort.rows(), None)
+    if T == 1:  # one row has no stride
+        s.sort.dispatch(torch.zeros(1, 101, dtype=dtype), s.sort.rows())
+    assert len(calls) == (8 if T == 1 else 7)
+    empty = TokenSort(0, 3, 7, 101, dtype=dtype, device="cpu")
+    empty.combine(empty.rows(), torch.zeros(1), torch.zeros(0, 104, dtype=dtype)[:, :101])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sort_refuses_arrays_that_do_not_fit(calls, dtype):
+    s = Sorted(dtype)
+    for name, args in s.args.items():
+        call = getattr(s.sort, name)
+        for k, t in args.items():
+            other = F32 if t.dtype == BF else BF
+            wrong = [t.to(other), t.to(F16), t.to(torch.float64), t[:-1], t.to("meta"),
+                     torch.zeros(t.shape[0], 2 * t.shape[1], dtype=t.dtype)[:, ::2]]
+            if "topk_w" not in k:
+                wrong += [torch.zeros(t.shape[0], 112, dtype=dtype)[:, :101],
+                          torch.zeros(t.shape[0], 104, dtype=dtype)[:, :100],
+                          torch.zeros(t.shape[0], 101, dtype=dtype), t[0]]
+            for w in wrong:
+                refused(calls, call, **dict(args, **{k: w}))
+    ids = torch.zeros(60, dtype=torch.int32)
+    for idx in (ids.long(), ids[:-1], ids.float(), ids.to("meta"),
+                torch.zeros(120, dtype=torch.int32)[::2]):
+        refused(calls, s.sort.build, idx, s.sched)
+    for kw in (dict(R=59), dict(counts=torch.zeros(8))):
+        sched = type("Sched", (), dict(vars(type(s.sched)), **kw))()
+        refused(calls, s.sort.build, ids, sched)
+
+
+def test_sort_refuses_other_types():
+    for dt in (F16, torch.float64, torch.int32):
+        with pytest.raises(ValueError):
+            TokenSort(20, 3, 7, 101, dtype=dt, device="cpu")
