@@ -376,36 +376,42 @@ class Linear:
 
 
 class AdamW:
-    """AdamW over a list of parameters: dicts with p (fp32 or bf16), g (its gradient) and, where
-    they apply, copy (bf16 working weights of an fp32 p) and weight_decay. The states are fp32,
-    or MXFP8 with eight_bit. Parameters that share their types go in one launch."""
+    """AdamW over a list of parameters: dicts with p (fp32 or bf16), g (its gradient, fp32 or
+    bf16) and, where they apply, copy (bf16 working weights of an fp32 p) and weight_decay. All
+    are packed and stay where they are: a step reads the gradients at the addresses they had when
+    the list was given. The states are fp32, or MXFP8 with eight_bit. Parameters that share their
+    types go in one launch. Arrays that do not fit raise ValueError."""
 
     def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, eight_bit=False,
-                 stochastic=True, seed=0):
+                 stochastic=True, seed=0, device="cuda"):
         self.lr, self.betas, self.eps, self.seed, self.t = lr, betas, eps, seed, 0
         self.state = B.MOK_STATE_MXFP8 if eight_bit else B.MOK_STATE_F32
         self.flags = B.MOK_ADAMW_STOCHASTIC if stochastic else 0
-        groups = {}
+        device, groups = torch.device(device), {}
         for q in params:
             e, p = dict(q), q["p"]
-            n = p.numel()
-            for t in (p, q["g"], q.get("copy")):
-                if t is not None and (t.numel() != n or not t.is_contiguous()):
-                    raise ValueError("parameters, gradients and copies are packed and of one size")
+            n, kinds = p.numel(), (_mok_dtype(p.dtype), _mok_dtype(q["g"].dtype))
+            for k in ("p", "g"):
+                _check_vector(k, q[k], q[k].dtype, device, n)
+            _check_vector("copy", q.get("copy"), torch.bfloat16, device, n)
+            if q.get("copy") is not None and p.dtype != torch.float32:
+                raise ValueError("copy: only fp32 parameters have one")
             u8 = dict(dtype=torch.uint8, device=p.device)
             for k in ("m", "v"):
                 e[k] = torch.zeros(n, **(u8 if eight_bit else
                                          dict(dtype=torch.float32, device=p.device)))
                 if eight_bit:
                     e[k + "_scale"] = torch.zeros((n + 31) // 32, **u8)
-            groups.setdefault((p.dtype, q["g"].dtype), []).append(dict(e, n=n))
-        self.lists = [(types, B.make_adamw_list(g)) for types, g in groups.items()]
+            groups.setdefault(kinds, []).append(dict(e, n=n))
+        self.lists = [(kinds, B.make_adamw_list(g)) for kinds, g in groups.items()]
+        self.device = device
 
     def step(self, grad_scale=None, stream=None):
+        if grad_scale is not None:
+            _check_vector("grad_scale", grad_scale, torch.float32, self.device, 1)
         self.t += 1
-        dt = lambda t: B.MOK_DTYPE_F32 if t == torch.float32 else B.MOK_DTYPE_BF16  # noqa: E731
         for k, ((p, g), tensors) in enumerate(self.lists):
             cfg = B.make_adamw(self.lr, *self.betas, self.eps, self.t,
-                               (self.seed + self.t * len(self.lists) + k) & (2 ** 64 - 1), dt(p),
-                               dt(g), self.state, self.flags)
+                               (self.seed + self.t * len(self.lists) + k) & (2 ** 64 - 1), p, g,
+                               self.state, self.flags)
             B.check(B.mok_adamw_step(cfg, tensors, grad_scale, stream), "adamw")

@@ -5,7 +5,7 @@ import pytest
 from mixture_experts_layer_deterministic_gb300 import binding as B
 
 torch = pytest.importorskip("torch")
-from mixture_experts_layer_deterministic_gb300.buffers import Linear, TokenSort  # noqa: E402
+from mixture_experts_layer_deterministic_gb300.buffers import AdamW, Linear, TokenSort  # noqa: E402
 
 F32, BF, F16 = torch.float32, torch.bfloat16, torch.float16
 
@@ -15,7 +15,8 @@ def calls(monkeypatch):
     """Names of the entry points that were reached, which do nothing."""
     seen = []
     for name in ("mok_linear_forward", "mok_linear_backward", "mok_build_row_map", "mok_dispatch",
-                 "mok_dispatch_backward", "mok_combine", "mok_combine_backward"):
+                 "mok_dispatch_backward", "mok_combine", "mok_combine_backward",
+                 "mok_adamw_step"):
         monkeypatch.setattr(B, name, lambda *a, _n=name: seen.append(_n) or B.MOK_OK)
     return seen
 
@@ -179,3 +180,35 @@ def test_sort_refuses_other_types():
     for dt in (F16, torch.float64, torch.int32):
         with pytest.raises(ValueError):
             TokenSort(20, 3, 7, 101, dtype=dt, device="cpu")
+
+
+@pytest.mark.parametrize("eight_bit", [False, True])
+def test_adamw_takes_what_fits(calls, eight_bit):
+    mk = lambda *s, dt=F32: torch.zeros(*s, dtype=dt)  # noqa: E731
+    opt = AdamW([dict(p=mk(3, 40), g=mk(3, 40, dt=BF), copy=mk(3, 40, dt=BF)),
+                 dict(p=mk(7), g=mk(7), weight_decay=0.1), dict(p=mk(5, dt=BF), g=mk(5, dt=BF)),
+                 dict(p=mk(9, dt=BF), g=mk(9)), dict(p=mk(2), g=mk(2))], lr=1e-3,
+                eight_bit=eight_bit, device="cpu")
+    opt.step()
+    opt.step(grad_scale=torch.ones(1))
+    assert [k for k, _ in opt.lists] == [(B.MOK_DTYPE_F32, B.MOK_DTYPE_BF16),
+                                         (B.MOK_DTYPE_F32, B.MOK_DTYPE_F32),
+                                         (B.MOK_DTYPE_BF16, B.MOK_DTYPE_BF16),
+                                         (B.MOK_DTYPE_BF16, B.MOK_DTYPE_F32)]
+    assert len(calls) == 8 and opt.t == 2
+
+
+def test_adamw_refuses_arrays_that_do_not_fit(calls):
+    mk = lambda n, dt=F32: torch.zeros(n, dtype=dt)  # noqa: E731
+    good = dict(p=mk(40), g=mk(40, BF), copy=mk(40, BF))
+    for kw in [dict(p=mk(40, dt)) for dt in (F16, torch.float64, torch.int8)] + \
+              [dict(g=mk(40, dt)) for dt in (F16, torch.float64, torch.uint8)] + \
+              [dict(copy=mk(40, dt)) for dt in (F32, F16, torch.uint8)] + \
+              [dict(g=mk(39)), dict(copy=mk(39, BF)), dict(p=mk(41)), dict(p=mk(80)[::2]),
+               dict(g=mk(80)[::2]), dict(copy=mk(80, BF)[::2]), dict(p=mk(40, BF)),
+               dict(g=mk(40).to("meta")), dict(copy=mk(40, BF).to("meta"))]:
+        refused(calls, AdamW, [dict(good, **kw)], lr=1e-3, device="cpu")
+    opt = AdamW([good], lr=1e-3, device="cpu")
+    for gs in (mk(1, BF), mk(2), mk(1).to("meta")):
+        refused(calls, opt.step, gs)
+    assert opt.t == 0
