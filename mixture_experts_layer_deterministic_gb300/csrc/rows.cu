@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(MAX_E)
     let_next_start();
     wait_for_previous();
     __shared__ int64_t warp_sum[MAX_E / 32];
-    __shared__ int32_t s_start[MAX_E], s_kept[MAX_E], s_off[MAX_E];
+    __shared__ int32_t s_start[MAX_E], s_count[MAX_E], s_kept[MAX_E], s_off[MAX_E];
     const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
     int32_t n = 0;
     if (e < E) {
@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(MAX_E)
             raise_status(status, MOK_ERR_DEVICE_INVARIANT);
             n = 0;
         }
+        s_count[e] = n;
         if (capacity > 0 && n > capacity) n = capacity;
     }
     int64_t v = ((int64_t)n + 15) & ~(int64_t)15;
@@ -103,7 +104,8 @@ __global__ void __launch_bounds__(MAX_E)
             raise_status(status, MOK_ERR_DEVICE_INVARIANT);
         } else {
             const int64_t rank = (int64_t)inv[f] - s_off[x];
-            if (rank < 0 || rank >= R) {
+            // past the count the schedule is of other ids; from the capacity on an id is dropped
+            if (rank < 0 || rank >= s_count[x]) {
                 raise_status(status, MOK_ERR_DEVICE_INVARIANT);
             } else if (rank < s_kept[x] && (int64_t)s_start[x] + rank < n_rows) {
                 row = (int32_t)(s_start[x] + rank);

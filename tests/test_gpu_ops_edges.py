@@ -6,10 +6,12 @@ a product as two bf16 values, each rounded to nearest, so within 2^-17 of itself
 segments of 1024 terms is within 2^-19 of its norm (twice the 8.9e-7 that 4096 terms of one sign
 pattern after another gave in four segments; one run of 4096 terms gave 3.9e-6, and the error of
 a run grows with its length)."""
+import numpy as np
 import pytest
 
 from mixture_experts_layer_deterministic_gb300 import binding as B
 from test_gpu_linear import Lin, check_forward, device_ok, dot_rel
+from test_gpu_rows import Case, clean_status
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +93,34 @@ def test_linear_helper_with_an_odd_width():
         assert bool(((got.double() - a @ b).abs() <= e + u * ((a @ b).abs() + e)).all())
     with pytest.raises(ValueError):
         lin.forward(x, torch.zeros(1, 77, 1001, **bf), y)
+
+
+@pytest.mark.parametrize("capacity", [0, 3])
+def test_a_schedule_of_other_ids_is_reported(capacity):
+    """The schedule of 12 ids of expert 0 and 4 of expert 1, used with ids the other way round:
+    expert 1 then holds ranks 4 to 15, of which it counted four."""
+    c = Case(T=16, K=1, E=2, H=16, capacity=capacity)
+    idx = np.array([0] * 12 + [1] * 4, np.int32)
+    c.counts, c.offsets = np.array([12, 4], np.int32), np.array([0, 12, 16], np.int32)
+    c.perm = c.inv = np.arange(16, dtype=np.int32)
+    m, starts, kept = i32([7] * 16), i32([0] * 3), i32([0] * 2)
+
+    def build(ids):
+        B.check(B.mok_build_row_map(c.cfg, c.dev(ids), c.sched(), m, starts, kept))
+        return clean_status(), m.cpu().numpy()
+
+    status, got = build(idx)
+    assert status == B.MOK_OK
+    keep = capacity or 16
+    first1 = 16
+    want = [f if f < keep else -1 for f in range(12)] + [first1 + r if r < keep else -1
+                                                         for r in range(4)]
+    assert got.tolist() == want
+    # ids that the schedule did not see: id 12 (rank 12 of expert 0, which counted 12) is past the
+    # count, with and without a capacity below it
+    other = idx.copy()
+    other[12] = 0
+    status, got = build(other)
+    assert status == B.MOK_ERR_DEVICE_INVARIANT
+    want[12] = -1
+    assert got.tolist() == want
