@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(TPB, J == FEW ? FEW_BWD_BLOCKS : COMBINE_BLOCK
             if (warp == 0 && lane < K && t < T) {
                 float a = 0.f;
                 for (int i = 0; i < wpt; ++i) a += part[wid + i][lane];
-                dw[t * K + lane] = a;
+                dw[t * K + lane] = rk >= 0 ? a : 0.f;  // dropped: zero, whatever dy holds
             }
             if (wsh > 0) __syncthreads();
             else __syncwarp();

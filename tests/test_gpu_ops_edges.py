@@ -124,3 +124,21 @@ def test_a_schedule_of_other_ids_is_reported(capacity):
     assert status == B.MOK_ERR_DEVICE_INVARIANT
     want[12] = -1
     assert got.tolist() == want
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("H,extra", [(64, 0), (61, 3), (264, 0), (1030, 0), (4100, 1)])
+def test_dropped_copies_have_zero_gradients_whatever_dy_holds(H, extra, dtype):
+    torch = _t()
+    c = Case(T=40, K=3, E=6, H=H, capacity=15, dtype=dtype, ld_extra=extra)
+    rows, dy = c.array(c.n_rows), c.array(c.T)
+    dy[:, 0] = float("inf")
+    dy[:, H - 1] = float("nan")
+    drows, dw = c.array(c.n_rows, fill=9.0), torch.full((c.T * c.K,), 9.0, device="cuda")
+    B.check(B.mok_combine_backward(c.cfg, dy, rows, c.dev(c.map), c.dev(c.starts), c.dev(c.kept),
+                                   c.dev(c.w), drows, dw))
+    dropped = torch.from_numpy(c.map < 0).cuda()
+    assert int(dropped.sum()) > 0
+    assert bool((dw[dropped] == 0).all())
+    assert bool(dw[~dropped].isnan().all())
+    assert clean_status() == B.MOK_OK
