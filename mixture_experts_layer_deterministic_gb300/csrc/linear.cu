@@ -184,6 +184,14 @@ MOK_DEV float act_f(float z) {
     if (ACT == MOK_ACT_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
     return z;
 }
+// the nearest value of [-16, 16]; NaN stays NaN
+MOK_DEV float within16(float z) {
+    float r;
+    asm("{\n.reg .f32 t;\nmin.NaN.f32 t, %1, %2;\nmax.NaN.f32 %0, t, %3;\n}\n"
+        : "=f"(r)
+        : "f"(z), "f"(16.0f), "f"(-16.0f));
+    return r;
+}
 template <int ACT>
 MOK_DEV float act_grad_f(float z) {
     if (ACT == MOK_ACT_RELU) return z > 0.f ? 1.f : 0.f;
@@ -192,9 +200,10 @@ MOK_DEV float act_grad_f(float z) {
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
     if (ACT == MOK_ACT_GELU_TANH) {
-        const float z2 = z * z, s = gelu_sigmoid(z, z2);
+        const float c = within16(z);  // s is 0 or 1 past it, and z^3 must not meet that 0
+        const float z2 = c * c, s = gelu_sigmoid(c, z2);
         const float du = fmaf(3.0f * GELU_A * GELU_C2, z2, GELU_C2);
-        return s * fmaf(z * (1.0f - s), du, 1.0f);
+        return s * fmaf(c * (1.0f - s), du, 1.0f);
     }
     if (ACT == MOK_ACT_GELU)
         return fmaf(z, 0.3989422804014327f * __expf(-0.5f * z * z),

@@ -142,3 +142,27 @@ def test_dropped_copies_have_zero_gradients_whatever_dy_holds(H, extra, dtype):
     assert bool((dw[dropped] == 0).all())
     assert bool(dw[~dropped].isnan().all())
     assert clean_status() == B.MOK_OK
+
+
+def test_activations_and_slopes_far_from_zero():
+    """Finite z of any size: the slopes are 0 or 1 there, and act(z) is z or 0."""
+    torch = _t()
+    far = torch.tensor([3.0e38, 1e30, 1e20, 1e14, 1e8, 200.0, 30.0], device="cuda")
+    zs = torch.cat([far, -far]).to(torch.bfloat16)
+    for act in ("relu", "silu", "gelu_tanh", "gelu"):
+        for R in (1, 300):
+            c = Lin(R=R, Kin=16, N=14, act=act, grad="fp32")
+            c.z[:R, :14] = zs
+            dx, dw, db = c.backward()
+            assert device_ok()
+            want = torch.where(zs > 0, c.dy[:R, :14].float(), 0.0).sum(0)
+            mag = c.dy[:R, :14].float().abs().sum(0)
+            # exp(-30) z is below 2^-38; the sums are fp32
+            assert bool(((db[:14] - want).abs() <= (R + 8) * 2.0 ** -24 * mag + 1e-10).all()), act
+            assert bool(dx[:R, :16].isfinite().all()) and bool(dw[:14, :16].isfinite().all())
+        c = Lin(R=3, Kin=1, N=14, act=act, out="fp32", res=False, bias=False)
+        c.x[:3, :1], c.w[:14, 0] = 1.0, zs
+        y, z = c.forward()
+        assert device_ok() and torch.equal(z[:3, :14], zs.expand(3, 14))
+        want = zs.float().clamp(min=0)
+        assert bool(((y[:3, :14] - want).abs() <= 2.0 ** -20 * want + 1e-10).all()), act
