@@ -42,7 +42,7 @@ constexpr int LSTAGES = 6;
 constexpr int LSTAGE_BYTES = 4 * BOX;
 constexpr uint32_t SET_COLS = 256; // TMEM columns of one accumulator set
 constexpr int LTILE = 256;         // most rows of a tile
-constexpr int SEG_K = 1024;        // fp32 outputs: K elements per accumulation segment
+constexpr int SEG_K = 1024;        // fp32 outputs and gradients: K elements per accumulation segment
 constexpr int MAX_G = 1024;
 
 // Epilogue warps: two per TMEM lane quadrant, or four where the warps keep a unit's sums in
@@ -260,6 +260,19 @@ struct LinGeom {
     int n_mma;           // N of each MMA
     int k_steps;         // 16-element K steps
     int k_first;         // K element to begin at
+    int half;            // of dz, where it comes as two bf16 values
+
+    // cut to segment `seg` of a sum that is kept in registers: SEG_K of its K, by one of the
+    // halves of dz
+    MOK_DEV void segment(int seg, int halves) {
+        const int first = seg / halves * (SEG_K / 16);
+        half = seg % halves;
+        k_first += first * 16;
+        k_steps = k_steps - first < SEG_K / 16 ? k_steps - first : SEG_K / 16;
+    }
+    MOK_DEV int segments(int halves) const {
+        return k_steps > SEG_K / 16 ? (k_steps + SEG_K / 16 - 1) / (SEG_K / 16) * halves : halves;
+    }
 };
 
 // Dense products with few units and a long K (dW of a narrow layer over many rows) leave most
@@ -399,6 +412,24 @@ MOK_DEV void emit_part(const KParts &kp, int part, uint32_t c, int hw, int64_t r
     }
 }
 
+// 16 columns at a time below column n of this warp's lanes: a unit's segments so far added up in
+// registers, and after the last out(first column, sums)
+template <class F>
+MOK_DEV void sum_segments(uint32_t c, int hw, int n, bool first, bool last, Carry<true> &s, F &&out) {
+#pragma unroll
+    for (int k = 0; k < 2 * Epi<true>::CHUNKS; ++k) {
+        const int n0 = 32 * hw + Epi<true>::STEP * (k >> 1) + 16 * (k & 1);
+        if (n0 >= n) continue;
+        float v[16];
+        tc::tmem_ld16(c + n0, v);
+        tc::tmem_ld_wait();
+        loaded(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s.v[k][j] = first ? v[j] : s.v[k][j] + v[j];
+        if (last) out(n0, s.v[k]);
+    }
+}
+
 // a bf16 output: matrices of `rows` x `cols`, rows ld apart
 struct OutRef {
     uint16_t *p;
@@ -516,6 +547,7 @@ struct Fwd {
         const int4 t = tiles.get(u / (uint32_t)n_mb);
         return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0, part};
     }
+    MOK_DEV int segments(const Unit &) const { return segs; }
     MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
         LinGeom q;
         q.n_mma = (u.nr + 15) & ~15;
@@ -539,8 +571,8 @@ struct Fwd {
         for (int j = 0; j < q.nbox; ++j)
             tc::tma_load_2d_pair(st + 2 * BOX + j * (BOX / 2), tmB, fb, q.b0 + k0, q.b1 + 32 * j);
     }
-    MOK_DEV void epilogue(const Unit &u, int seg, uint32_t rank, uint32_t c, int q, int hw, int lane,
-                          Patches &pt, Carry<SUMS> &carry) const {
+    MOK_DEV void epilogue(const Unit &u, int seg, bool, uint32_t rank, uint32_t c, int q, int hw,
+                          int lane, Patches &pt, Carry<SUMS> &carry) const {
         const int nr = u.nr, pad = u.pad;
         const int64_t r0 = u.r0;
         const int n_mma = (nr + 15) & ~15;
@@ -711,14 +743,16 @@ struct Fwd {
 
 // The input gradient; CUT: K may be cut into parts. 64 groups of 320 rows, 1024 -> 4096: 126 us,
 // 5.9 TB/s (W is most of it); tiles of 160 rows take longer to load than to multiply.
+// F32: dz comes as `halves` planes of bf16 that add up to it, and the sums of segments of K, for
+// the accuracy of a long sum, are added in registers (see Fwd).
 template <bool F32, bool CUT>
 struct Dx {
-    using E = Epi<false>;
-    static constexpr bool F32_OUT = F32, SUMS = false;
+    using E = Epi<F32>;
+    static constexpr bool F32_OUT = F32, SUMS = F32;
     static constexpr bool A_MN = true, B_MN = false;
     Tiles tiles;
     int n_mb;     // ceil(Kin / 256)
-    int segs;     // 1
+    int halves;   // planes of dz: 2 for fp32 gradients of a dz that bf16 does not hold
     int Kin, N;
     int64_t ld;   // row stride of dx
     void *dx;
@@ -732,8 +766,17 @@ struct Dx {
         const int4 t = tiles.get(u / (uint32_t)n_mb);
         return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0, part};
     }
-    MOK_DEV LinGeom geom(const Unit &u, int, uint32_t rank) const {
+    MOK_DEV LinGeom k_range(const Unit &u) const {
         LinGeom q;
+        q.k_steps = (N + 15) / 16;
+        q.k_first = q.half = 0;
+        if constexpr (CUT) kp.cut(q, u.part);
+        return q;
+    }
+    MOK_DEV int segments(const Unit &u) const { return F32 ? k_range(u).segments(halves) : 1; }
+    MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
+        LinGeom q = k_range(u);
+        if constexpr (F32) q.segment(seg, halves);
         q.n_mma = (u.nr + 15) & ~15;
         q.a0 = u.mb * 256 + (int)rank * 128;
         q.a1 = 0;
@@ -741,9 +784,6 @@ struct Dx {
         q.b0 = 0;
         q.b1 = u.r0 + (int)rank * (q.n_mma / 2);
         q.nbox = (q.n_mma / 2 + 31) / 32;
-        q.k_steps = (N + 15) / 16;
-        q.k_first = 0;
-        if constexpr (CUT) kp.cut(q, u.part);
         return q;
     }
     MOK_DEV uint32_t tx(const LinGeom &q) const { return 2 * BOX + q.nbox * (BOX / 2); }
@@ -752,33 +792,39 @@ struct Dx {
                       const CUtensorMap *tmB) const {
         tma_load_3d_pair(st, tmA, fb, q.a0, k0, q.a2);
         tma_load_3d_pair(st + BOX, tmA, fb, q.a0 + 64, k0, q.a2);
-        for (int j = 0; j < q.nbox; ++j)
-            tc::tma_load_2d_pair(st + 2 * BOX + j * (BOX / 2), tmB, fb, k0, q.b1 + 32 * j);
+        for (int j = 0; j < q.nbox; ++j) {
+            uint8_t *b = st + 2 * BOX + j * (BOX / 2);
+            if constexpr (F32)
+                tma_load_3d_pair(b, tmB, fb, k0, q.b1 + 32 * j, q.half);
+            else
+                tc::tma_load_2d_pair(b, tmB, fb, k0, q.b1 + 32 * j);
+        }
     }
-    MOK_DEV void epilogue(const Unit &u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
-                          Patches &pt, Carry<SUMS> &carry) const {
+    MOK_DEV void epilogue(const Unit &u, int seg, bool last, uint32_t rank, uint32_t c, int q, int hw,
+                          int lane, Patches &pt, Carry<SUMS> &carry) const {
         const int nr = u.nr, pad = u.pad;
         const int64_t r0 = u.r0;
         const int n_mma = (nr + 15) & ~15;
         const int i0 = u.mb * 256 + (int)rank * 128 + q * 32;
-        if (CUT && kp.parts > 1) {
-            emit_part<E::STEP>(kp, u.part, c, hw, r0, nr, i0 + lane, Kin);
-            return;
-        }
-        for (int n0 = 32 * hw; n0 < n_mma; n0 += E::STEP) {
-            if constexpr (F32) {
-                float v[32];
-                ld32(c + n0, v);
-                if (i0 + lane >= Kin) continue;
-                float *o = static_cast<float *>(dx) + (r0 + n0) * ld + i0 + lane;
-                const int n_out = (pad ? n_mma : nr) - n0;
+        const bool part = CUT && kp.parts > 1;
+        if constexpr (F32) {
+            float *o = part ? kp.out + u.part * kp.stride + r0 * kp.ld
+                            : static_cast<float *>(dx) + r0 * ld;
+            const int64_t ldo = part ? kp.ld : ld;
+            const int n_out = pad && !part ? n_mma : nr;
+            sum_segments(c, hw, n_mma, seg == 0, last, carry, [&](int n0, const float (&v)[16]) {
+                if (i0 + lane >= Kin) return;
+                float *p = o + n0 * ldo + i0 + lane;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j < n_out) o[(int64_t)j * ld] = n0 + j < nr ? v[j] : 0.f;
-            } else {
+                for (int j = 0; j < 16; ++j)
+                    if (n0 + j < n_out) p[j * ldo] = n0 + j < nr ? v[j] : 0.f;
+            });
+        } else if (part) {
+            emit_part<E::STEP>(kp, u.part, c, hw, r0, nr, i0 + lane, Kin);
+        } else {
+            for (int n0 = 32 * hw; n0 < n_mma; n0 += E::STEP)
                 emit_plain(pt, c + n0, nr - n0, OutRef{static_cast<uint16_t *>(dx), tiles.rows, ld, Kin},
                            i0 & ~63, r0 + n0, r0 + (pad ? n_mma : nr), 0);
-            }
         }
     }
 };
@@ -841,13 +887,13 @@ struct DbArgs {
 // bound by writing 537 MB (132 us at the write-only rate of a memset, 4.06 TB/s).
 template <bool F32, bool CUT>
 struct Dw {
-    using E = Epi<false>;
-    static constexpr bool F32_OUT = F32, SUMS = false;
+    using E = Epi<F32>;
+    static constexpr bool F32_OUT = F32, SUMS = F32;
     static constexpr bool A_MN = true, B_MN = true;
     const int32_t *starts, *valid;  // grouped: first row and row count of each group
     int64_t rows;                   // dense
     int G, n_mb, n_nb;              // ceil(Kin / 256), ceil(N / 256)
-    int segs;                       // 1
+    int halves;                     // planes of dz (F32; see Dx)
     int Kin, N;
     int64_t ld;                     // row stride of dW
     void *dw;
@@ -870,9 +916,18 @@ struct Dw {
                     valid != nullptr ? valid[g] : (int)rows, 0,
                     (int)(rest % (uint32_t)n_mb), (int)(rest / (uint32_t)n_mb), part};
     }
-    MOK_DEV LinGeom geom(const Unit &u, int, uint32_t rank) const {
-        const int mb = u.mb, nb = u.nb;
+    MOK_DEV LinGeom k_range(const Unit &u) const {
         LinGeom q;
+        q.k_steps = (u.nr + 15) / 16;
+        q.k_first = q.half = 0;
+        if constexpr (CUT) kp.cut(q, u.part);
+        return q;
+    }
+    MOK_DEV int segments(const Unit &u) const { return F32 ? k_range(u).segments(halves) : 1; }
+    MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
+        const int mb = u.mb, nb = u.nb;
+        LinGeom q = k_range(u);
+        if constexpr (F32) q.segment(seg, halves);
         // MN-major B comes in boxes of 64 columns per CTA: N of the MMA is 128 or 256, columns
         // past the matrix being zeros
         q.n_mma = N - nb * 256 <= 128 ? 128 : 256;
@@ -882,9 +937,6 @@ struct Dw {
         q.a2 = 0;
         q.b0 = nb * 256 + (int)rank * (q.n_mma / 2);
         q.b1 = q.a1;
-        q.k_steps = (u.nr + 15) / 16;
-        q.k_first = 0;
-        if constexpr (CUT) kp.cut(q, u.part);
         return q;
     }
     MOK_DEV uint32_t tx(const LinGeom &q) const { return (2 + q.nbox) * BOX; }
@@ -892,33 +944,38 @@ struct Dw {
                       const CUtensorMap *tmB) const {
         tc::tma_load_2d_pair(st, tmA, fb, q.a0, q.a1 + k0);
         tc::tma_load_2d_pair(st + BOX, tmA, fb, q.a0 + 64, q.a1 + k0);
-        for (int j = 0; j < q.nbox; ++j)
-            tc::tma_load_2d_pair(st + (2 + j) * BOX, tmB, fb, q.b0 + 64 * j, q.b1 + k0);
+        for (int j = 0; j < q.nbox; ++j) {
+            uint8_t *b = st + (2 + j) * BOX;
+            if constexpr (F32)
+                tma_load_3d_pair(b, tmB, fb, q.b0 + 64 * j, q.b1 + k0, q.half);
+            else
+                tc::tma_load_2d_pair(b, tmB, fb, q.b0 + 64 * j, q.b1 + k0);
+        }
     }
-    MOK_DEV void epilogue(const Unit &u, int, uint32_t rank, uint32_t c, int q, int hw, int lane,
-                          Patches &pt, Carry<SUMS> &carry) const {
+    MOK_DEV void epilogue(const Unit &u, int seg, bool last, uint32_t rank, uint32_t c, int q, int hw,
+                          int lane, Patches &pt, Carry<SUMS> &carry) const {
         const int g = u.g, mb = u.mb, nb = u.nb;
         const int nn = N - nb * 256 < 256 ? N - nb * 256 : 256;
         const bool any = u.nr > 0;
         const int i0 = mb * 256 + (int)rank * 128 + q * 32;
-        if (CUT && kp.parts > 1) {
-            emit_part<E::STEP>(kp, u.part, c, hw, nb * 256, nn, i0 + lane, Kin);
-            return;
-        }
-        for (int n0 = 32 * hw; n0 < nn; n0 += E::STEP) {
-            if constexpr (F32) {
-                float v[32];
-                ld32(c + n0, v);
-                if (i0 + lane >= Kin) continue;
-                float *o = static_cast<float *>(dw) +
-                           ((int64_t)g * N + nb * 256 + n0) * ld + i0 + lane;
+        const bool part = CUT && kp.parts > 1;
+        if constexpr (F32) {
+            float *o = part ? kp.out + u.part * kp.stride + nb * 256 * kp.ld
+                            : static_cast<float *>(dw) + ((int64_t)g * N + nb * 256) * ld;
+            const int64_t ldo = part ? kp.ld : ld;
+            sum_segments(c, hw, nn, seg == 0, last, carry, [&](int n0, const float (&v)[16]) {
+                if (i0 + lane >= Kin) return;
+                float *p = o + n0 * ldo + i0 + lane;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (n0 + j < nn) o[(int64_t)j * ld] = any ? v[j] : 0.f;
-            } else {
+                for (int j = 0; j < 16; ++j)
+                    if (n0 + j < nn) p[j * ldo] = any ? v[j] : 0.f;
+            });
+        } else if (part) {
+            emit_part<E::STEP>(kp, u.part, c, hw, nb * 256, nn, i0 + lane, Kin);
+        } else {
+            for (int n0 = 32 * hw; n0 < nn; n0 += E::STEP)
                 emit_plain(pt, c + n0, any ? 32 : 0, OutRef{static_cast<uint16_t *>(dw), N, ld, Kin},
                            i0 & ~63, nb * 256 + n0, N, g);
-            }
         }
     }
 };
@@ -964,7 +1021,6 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
     LinSmem *sm = (LinSmem *)(base + NS * SB + LIN_PATCHES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
-    const int segs = p.segs;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -1004,6 +1060,7 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
             bool ok = true;
             for (uint32_t u = cid; u < n_units && ok; u += ncl) {
                 const Unit cur = p.unit(u);
+                const int segs = p.segments(cur);
                 for (int seg = 0; seg < segs && ok; ++seg) {
                     const LinGeom g = p.geom(cur, seg, rank);
                     const uint32_t tx = p.tx(g);
@@ -1054,6 +1111,7 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
             bool ok = true;
             for (uint32_t u = cid; u < n_units && ok; u += ncl) {
                 const Unit cur = p.unit(u);
+                const int segs = p.segments(cur);
                 for (int seg = 0; seg < segs && ok; ++seg) {
                     const LinGeom g = p.geom(cur, seg, 0);
                     const uint32_t idesc = tc::idesc_bf16(256, g.n_mma, P::A_MN, P::B_MN);
@@ -1116,14 +1174,15 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
         bool ok = true;
         for (uint32_t u = cid; u < n_units && ok; u += ncl) {
             const Unit cur = p.unit(u);
+            const int segs = p.segments(cur);
             for (int seg = 0; seg < segs; ++seg, ++a) {
                 const int ab = (int)(a & 1);
                 ok = lin_wait(&sm->tmem_full[ab], (uint32_t)((a >> 1) & 1), p.status, abort);
                 if constexpr (!P::F32_OUT) ok = pt.agree(ok);
                 if (!ok) break;
                 tc::tc_fence_after();
-                p.epilogue(cur, seg, rank, tmem + lane_base + (uint32_t)ab * SET_COLS, q, hw, lane,
-                           pt, carry);
+                p.epilogue(cur, seg, seg == segs - 1, rank, tmem + lane_base + (uint32_t)ab * SET_COLS,
+                           q, hw, lane, pt, carry);
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) lin_arrive(empty0 + (uint32_t)ab * 8u);
@@ -1458,10 +1517,12 @@ __global__ void __launch_bounds__(256)
 // row lanes of 4 rows each, whose loads are all issued before the first is used (one row at a
 // time, 20480 x 1024 took 47 us, so 27; 126 MB are 19 at the copy rate); the sums of a column's 32
 // row lanes are added in lane order.
-template <bool DY32, int ACT>
+// LO: what bf16 leaves of dz goes to a second plane, `plane` elements on, in bf16 again: the two
+// are within 2^-17 of dz. Nothing where dz is not finite in bf16.
+template <bool DY32, int ACT, bool LO>
 __global__ void __launch_bounds__(256)
     linear_dz_kernel(const void *dy, const uint16_t *z, Tiles tiles, int N, int64_t ld, uint16_t *dz,
-                     int64_t ld_dz, float *part) {
+                     int64_t ld_dz, int64_t plane, float *part) {
     __shared__ float red[32][65];
     let_next_start();
     wait_for_previous();
@@ -1530,9 +1591,21 @@ __global__ void __launch_bounds__(256)
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] += v[j];  // absent rows and columns are zero
-        if (dz != nullptr)  // ld_dz is a multiple of 8: whole vectors
-            *reinterpret_cast<uint4 *>(dz + r * ld_dz + c) = make_uint4(
-                pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+        if (dz != nullptr) {  // ld_dz is a multiple of 8: whole vectors
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = pack2(v[2 * j], v[2 * j + 1]);
+            *reinterpret_cast<uint4 *>(dz + r * ld_dz + c) = make_uint4(h[0], h[1], h[2], h[3]);
+            if constexpr (LO) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float a = bf16_lo(h[j]), b = bf16_hi(h[j]);
+                    h[j] = pack2(isfinite(a) ? v[2 * j] - a : 0.f, isfinite(b) ? v[2 * j + 1] - b : 0.f);
+                }
+                *reinterpret_cast<uint4 *>(dz + plane + r * ld_dz + c) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
     }
     if (part == nullptr) return;
 #pragma unroll
@@ -1580,7 +1653,8 @@ cudaError_t map2d(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int
                ? cudaSuccess
                : cudaErrorInvalidValue;
 }
-// W [G][N][Kin]: (inputs, features, groups), boxes of 64 inputs x box_rows features
+// W [G][N][Kin]: (inputs, features, groups), boxes of 64 inputs x box_rows features; or the planes
+// of dz
 cudaError_t map_w(CUtensorMap *m, const void *p, int64_t G, int64_t N, int64_t Kin, int64_t ld,
                   int box_rows) {
     cuuint64_t dims[3] = {(cuuint64_t)Kin, (cuuint64_t)N, (cuuint64_t)G};
@@ -1631,13 +1705,13 @@ cudaError_t launch_both(const CUtensorMap &pa, const CUtensorMap &pb, const P &p
                         qb, q, (uint32_t)split);
 }
 
-template <bool DY32>
+template <bool DY32, bool LO>
 cudaError_t launch_dz(int act, dim3 grid, const void *dy, const uint16_t *z, const Tiles &t, int N,
                       int64_t ld, uint16_t *dz, int64_t ld_dz, float *part, cudaStream_t s) {
-#define MOK_DZ_CASE(A)                                                                         \
-    case A:                                                                                    \
-        return launch_edge(linear_dz_kernel<DY32, A>, grid, 256, 0, 1, s, dy, z, t, N, ld, dz, \
-                           ld_dz, part)
+#define MOK_DZ_CASE(A)                                                                          \
+    case A:                                                                                     \
+        return launch_edge(linear_dz_kernel<DY32, A, LO>, grid, 256, 0, 1, s, dy, z, t, N, ld,  \
+                           dz, ld_dz, t.rows * ld_dz, part)
     switch (act) {
         MOK_DZ_CASE(MOK_ACT_RELU);
         MOK_DZ_CASE(MOK_ACT_SILU);
@@ -1851,12 +1925,22 @@ struct LinWs {
     int height;       // most rows of a tile in it
     int32_t *valid;   // [G]
     int32_t *first;   // [G + 1]
-    uint16_t *dz;     // [rows][ld_dz]
+    uint16_t *dz;     // [halves][rows][ld_dz]
     int64_t ld_dz;
     float *part;      // [tiles][DZ_PARTS][N]
     Cut cut[2];       // along K: y, or dx and dW (dense)
     float *kp[2];     // their parts
 };
+
+// without an activation a bf16 dy is dz
+bool dz_is_dy(const mok_linear_config &c) {
+    return c.act == MOK_ACT_NONE && c.out_dtype == MOK_DTYPE_BF16;
+}
+// bf16 values that dz enters a product as: fp32 gradients take what one leaves as a second
+// (16384 rows, 4096 -> 512: see Dx)
+int dz_halves(const mok_linear_config &c) {
+    return c.grad_dtype == MOK_DTYPE_F32 && !dz_is_dy(c) ? 2 : 1;
+}
 
 size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
     size_t off = 0;
@@ -1876,7 +1960,7 @@ size_t carve_linear(const mok_linear_config &c, int pass, void *ws, LinWs *o) {
     w.first = (int32_t *)take((size_t)(c.groups + 1) * 4);
     if (pass == MOK_LINEAR_BACKWARD) {
         w.ld_dz = round_up(c.out_features, 8);
-        w.dz = (uint16_t *)take((size_t)c.rows * w.ld_dz * 2);
+        w.dz = (uint16_t *)take((size_t)c.rows * w.ld_dz * 2 * dz_halves(c));
         w.part = (float *)take((size_t)w.cap * DZ_PARTS * c.out_features * 4);
     }
     const Cut whole{1, 0, 0};
@@ -2060,8 +2144,8 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
                                                   : dense_height(c->rows, n_kb, sm_pairs(), &t));
     }
     const KParts xk = k_parts(xc, wk.kp[0], c->rows, Kin), wkp = k_parts(wc, wk.kp[1], N, Kin);
-    // without an activation a bf16 dy is dz
-    const bool direct = !act && !dy32;
+    const bool direct = dz_is_dy(*c);
+    const int halves = dz_halves(*c);
     const uint16_t *dz = direct ? (const uint16_t *)dy : wk.dz;
     const int64_t ld_dz = direct ? c->ld_out : wk.ld_dz;
     // The dW kernel adds the parts of db on the side, in the warps of the second SMs that issue no
@@ -2077,21 +2161,27 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
         const int64_t blocks = dzt.cap * DZ_PARTS * ((N + 63) / 64);
         const dim3 grid((unsigned)blocks);
         MOK_OP_LAUNCH(OP_LINEAR_DZ, 1,
-                      dy32 ? launch_dz<true>(c->act, grid, dy, (const uint16_t *)z, dzt, N,
-                                             c->ld_out, dzo, ld_dz, part, stream)
-                           : launch_dz<false>(c->act, grid, dy, (const uint16_t *)z, dzt, N,
-                                              c->ld_out, dzo, ld_dz, part, stream));
+                      (halves == 2 ? dy32 ? launch_dz<true, true> : launch_dz<false, true>
+                       : dy32      ? launch_dz<true, false>
+                                   : launch_dz<false, false>)(c->act, grid, dy, (const uint16_t *)z,
+                                                              dzt, N, c->ld_out, dzo, ld_dz, part,
+                                                              stream));
         if (db && !db_in_dw)
             MOK_OP_LAUNCH(OP_LINEAR_DZ, 1,
                           launch_edge(linear_db_kernel, (unsigned)(((int64_t)G * N + 31) / 32),
                                       32 * DB_SLICES, 0, 1, stream, dba, G, N));
     }
+    // for fp32 gradients dz is a stack of planes
+    const auto map_dz = [&](CUtensorMap *m, int box_rows) {
+        return g32 ? map_w(m, dz, halves, c->rows, N, ld_dz, box_rows)
+                   : map2d(m, dz, c->rows, N, ld_dz, box_rows);
+    };
     CUtensorMap xa, xb, wa, wb;
     if (dx && (map_w(&xa, w, G, N, Kin, c->ld_w, 64) != cudaSuccess ||
-               map2d(&xb, dz, c->rows, N, ld_dz, 32) != cudaSuccess))
+               map_dz(&xb, 32) != cudaSuccess))
         return MOK_ERR_CUDA;
     if (dw && (map2d(&wa, x, c->rows, Kin, c->ld_in, 64) != cudaSuccess ||
-               map2d(&wb, dz, c->rows, N, ld_dz, 64) != cudaSuccess))
+               map_dz(&wb, 64) != cudaSuccess))
         return MOK_ERR_CUDA;
     const int n_nb = (N + 255) / 256;
     const int64_t x_units = dx ? tiles.cap * n_kb * xc.parts : 0;
@@ -2099,14 +2189,15 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     const int32_t *valid = grouped(starts) ? wk.valid : nullptr;
     int64_t split = 0, pairs = 0;  // pairs of SMs for dW, and in all, where both go in one launch
     if (dx && dw && !grouped(starts))
-        plan_both(w_units, unit_clocks(wc.parts > 1 ? wc.per : (c->rows + 63) / 64, LTILE), x_units,
-                  unit_clocks(xc.parts > 1 ? xc.per : (N + 63) / 64, tiles.height), &split, &pairs);
+        plan_both(w_units, unit_clocks((wc.parts > 1 ? wc.per : (c->rows + 63) / 64) * halves, LTILE),
+                  x_units, unit_clocks((xc.parts > 1 ? xc.per : (N + 63) / 64) * halves, tiles.height),
+                  &split, &pairs);
     DbArgs dwb = dba;
     if (!db_in_dw) dwb.db = nullptr;
 #define MOK_BWD(F, CUT)                                                                         \
     do {                                                                                        \
-        const Dx<F, CUT> px{tiles, n_kb, 1, Kin, N, c->ld_in, dx, status, xk};                       \
-        const Dw<F, CUT> pw{starts, valid, c->rows, G, n_kb, n_nb, 1, Kin, N, c->ld_w, dw, status, dwb, \
+        const Dx<F, CUT> px{tiles, n_kb, halves, Kin, N, c->ld_in, dx, status, xk};                       \
+        const Dw<F, CUT> pw{starts, valid, c->rows, G, n_kb, n_nb, halves, Kin, N, c->ld_w, dw, status, dwb, \
                         wkp};                                                                   \
         if (split > 0) {                                                                        \
             MOK_OP_LAUNCH(OP_LINEAR_DX, 1,                                                      \

@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 
 from mixture_experts_layer_deterministic_gb300 import binding as B
-from test_gpu_linear import Lin, check_forward, device_ok, dot_rel
+from test_gpu_linear import Lin, act64, check_backward, check_forward, device_ok, dot_rel
 from test_gpu_rows import Case, clean_status
 
 pytestmark = pytest.mark.gpu
@@ -23,6 +23,10 @@ def _t():
 
 def i32(a):
     return _t().tensor(a, dtype=_t().int32, device="cuda")
+
+
+def norm_rel(got, ref):
+    return float((got.double() - ref).norm() / ref.norm())
 
 
 def test_a_group_that_overlaps_an_earlier_one_counts_as_empty():
@@ -166,3 +170,44 @@ def test_activations_and_slopes_far_from_zero():
         assert device_ok() and torch.equal(z[:3, :14], zs.expand(3, 14))
         want = zs.float().clamp(min=0)
         assert bool(((y[:3, :14] - want).abs() <= 2.0 ** -20 * want + 1e-10).all()), act
+
+
+@pytest.mark.parametrize("kw", [
+    dict(R=16384, Kin=2048, N=2048),                     # no cut along K, dz = dy
+    dict(R=16384, Kin=64, N=64),                         # parts of K
+    dict(R=16384, Kin=64, N=64, act="gelu_tanh"),
+    dict(R=3000, Kin=1200, N=2600, act="silu"),
+    dict(R=3000, Kin=1200, N=2600, out="fp32"),
+    dict(R=700, Kin=520, N=300, act="gelu", out="fp32", extra=8),
+    dict(R=1, Kin=40, N=24, act="relu"),
+    dict(R=33, Kin=15, N=17, act="silu"),
+    dict(G=4, counts=[5000, 0, 17, 3001], Kin=300, N=200, spare=16),
+    dict(G=4, counts=[5000, 0, 17, 3001], Kin=300, N=2100, act="gelu_tanh", out="fp32", spare=16),
+    dict(G=3, counts=[0, 0, 0], Kin=64, N=64, act="silu", spare=16),
+], ids=lambda k: "-".join("%s%s" % i for i in k.items()).replace(" ", ""))
+def test_fp32_gradients_are_fp32(kw):
+    torch = _t()
+    c = Lin(grad="fp32", z=True, res=False, **kw)
+    dx, dw, db = check_backward(c)
+    k, N, u = c.Kin, c.N, 2.0 ** -17
+    exact_dz = c.act == "none" and c.out_dt == torch.bfloat16
+    for g, (a, b) in enumerate(c.spans()):
+        if b == a:
+            continue
+        x, w = c.x[a:b, :k].double(), c.w[g * N:(g + 1) * N, :k].double()
+        dz = c.dy[a:b, :N].double()
+        edz = torch.zeros_like(dz)
+        if c.act != "none":
+            zz = c.z[a:b, :N].double()
+            edz = dz.abs() * 2.0 ** -20 * (1 + zz.abs())
+            dz = dz * act64(zz, c.act)[1]
+        e = edz + (0.0 if exact_dz else u * (dz.abs() + edz))
+        for got, ref, err, mag, n in (
+                (dx[a:b, :k], dz @ w, e @ w.abs(), dz.abs() @ w.abs(), N),
+                (dw[g * N:(g + 1) * N, :k], dz.T @ x, e.T @ x.abs(), dz.abs().T @ x.abs(), b - a)):
+            assert bool(((got.double() - ref).abs() <= err + dot_rel(n) * (mag + err)).all())
+            assert norm_rel(got, ref) <= 2.0 ** -19 + (0.0 if exact_dz else u)
+    # the bits of a gradient do not depend on what else is asked for, and repeat
+    for i in range(3):
+        alone = c.backward(*[i == j for j in range(3)])
+        assert torch.equal(alone[i].view(torch.uint8), (dx, dw, db)[i].view(torch.uint8))
