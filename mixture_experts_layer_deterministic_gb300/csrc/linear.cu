@@ -93,13 +93,13 @@ struct Tiles {
 __global__ void __launch_bounds__(MAX_G)
     linear_tiles_kernel(const int32_t *starts, const int32_t *counts, int G, int64_t rows,
                         int most, int32_t *list, int32_t *valid, int32_t *first, int *status) {
-    __shared__ int32_t wsum[MAX_G / 32];
-    __shared__ int64_t wend[MAX_G / 32];
+    __shared__ int32_t wsum[32], wend[32];
+    static_assert(MAX_G == 32 * 32, "a warp total a lane");
     let_next_start();
     wait_for_previous();
     const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
-    int64_t b = 0, n = 0, h = most, end = 0;  // end: of the group's rows and their padding
-    int32_t nt = 0;
+    int64_t b = 0, n = 0, h = most;
+    int32_t nt = 0, end = 0;  // end: of the group's rows and their padding
     bool ok = g < G;
     if (ok) {
         b = starts[g];
@@ -107,22 +107,22 @@ __global__ void __launch_bounds__(MAX_G)
         const int64_t e = starts[g + 1];
         // the padding after the rows is written too, so it has to lie inside the group
         ok = n >= 0 && b >= 0 && (b & 15) == 0 && b + ((n + 15) & ~(int64_t)15) <= e && e <= rows;
-        if (ok) end = b + ((n + 15) & ~(int64_t)15);
+        if (ok) end = (int32_t)(b + ((n + 15) & ~(int64_t)15));
     }
     // the largest end of the groups before this one: a group that begins below it would write
     // rows that are another's already
-    int64_t before = end;
+    int32_t before = end;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        const int32_t u = __shfl_up_sync(0xFFFFFFFFu, before, o);
         if (lane >= o && u > before) before = u;
     }
     if (lane == 31) wend[warp] = before;
     before = __shfl_up_sync(0xFFFFFFFFu, before, 1);
     if (lane == 0) before = 0;
     __syncthreads();
-    for (int w = 0; w < warp; ++w)
-        if (wend[w] > before) before = wend[w];
+    // the earlier warps', one a lane
+    before = max(before, __reduce_max_sync(0xFFFFFFFFu, lane < warp ? wend[lane] : 0));
     if (g < G) {
         if (!ok || b < before) {
             raise_status(status, MOK_ERR_DEVICE_INVARIANT);
@@ -143,8 +143,7 @@ __global__ void __launch_bounds__(MAX_G)
     }
     if (lane == 31) wsum[warp] = v;
     __syncthreads();
-    int32_t at = v - nt;
-    for (int w = 0; w < warp; ++w) at += wsum[w];
+    const int32_t at = v - nt + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wsum[lane] : 0);
     if (g < G) first[g] = at;
     if (g == MAX_G - 1) list[-4] = first[G] = at + nt;
     for (int32_t i = 0; i < nt; ++i) {
