@@ -7,7 +7,7 @@
     gradients       the same operators in reverse
     update          AdamW over every weight and bias
 
-Run it on a GPU: python examples/gelu_experts.py [--steps N] [--eight-bit]
+Run it on a GPU: python examples/gelu_experts.py [--steps N] [--eight-bit] [--graph]
 """
 import argparse
 import os
@@ -25,7 +25,8 @@ from mixture_experts_layer_deterministic_gb300.buffers import (  # noqa: E402
 class GeluExperts:
     """y = x + sum_k w[t,k] (W2[e] gelu(W1[e] x + b1[e]) + b2[e]), e the k-th expert of token t."""
 
-    def __init__(self, T, H, I, E, K, capacity=0, seed=0, lr=1e-3, eight_bit=False):
+    def __init__(self, T, H, I, E, K, capacity=0, seed=0, lr=1e-3, eight_bit=False,
+                 capturable=False):
         gen = torch.Generator("cuda").manual_seed(seed)
         bf, f32 = dict(dtype=torch.bfloat16, device="cuda"), dict(device="cuda")
         self.T, self.H, self.I, self.E, self.K = T, H, I, E, K
@@ -46,7 +47,7 @@ class GeluExperts:
         self.opt = AdamW([dict(p=self.p[k], g=self.g[k],
                                copy=None if k[0] == "b" else self.w[k],
                                weight_decay=0.0 if k[0] == "b" else 0.01) for k in shapes],
-                         lr=lr, eight_bit=eight_bit)
+                         lr=lr, eight_bit=eight_bit, capturable=capturable)
         self.logits = torch.zeros(T, E, **f32)
         self.y, self.dx = torch.zeros(T, H, **bf), torch.zeros(T, H, **bf)
         self.dx_gate = torch.zeros(T, H, **bf)
@@ -88,20 +89,35 @@ class GeluExperts:
         self.opt.step()
         return loss
 
+    def capture(self, x, target):
+        """A training step as a graph to replay (of a `capturable` model, after a first step): the
+        graph, and the loss that each replay writes."""
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            loss = self.step(x, target)
+        return graph, loss
+
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=50)
     ap.add_argument("--eight-bit", action="store_true", help="MXFP8 optimizer states")
+    ap.add_argument("--graph", action="store_true", help="replay the steps from a CUDA graph")
     a = ap.parse_args()
     torch.manual_seed(0)
-    m = GeluExperts(T=1024, H=512, I=1024, E=8, K=2, eight_bit=a.eight_bit)
+    m = GeluExperts(T=1024, H=512, I=1024, E=8, K=2, eight_bit=a.eight_bit, capturable=a.graph)
     x = torch.randn(1024, 512, device="cuda").to(torch.bfloat16)
     target = x.float() + 0.5 * torch.tanh(x.float().roll(1, 1))
+    graph = None
     for k in range(a.steps):
-        loss = m.step(x, target)
+        if graph is not None:
+            graph.replay()
+        else:
+            loss = m.step(x, target)
         if k % 10 == 0 or k == a.steps - 1:
             print("step %3d  loss %.5f" % (k, loss.item()))
+        if a.graph and graph is None:
+            graph, loss = m.capture(x, target)
     print("device status:", B.status_string(B.mok_read_device_status()[1]))
 
 

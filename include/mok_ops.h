@@ -215,6 +215,29 @@ mok_status mok_check_adamw_config(const mok_adamw_config *cfg);
 mok_status mok_adamw_step(const mok_adamw_config *cfg, const mok_adamw_tensor *tensors,
                           int32_t n_tensors, const float *grad_scale, cudaStream_t stream);
 
+/* The step for programs that capture it in a CUDA graph and replay it. mok_adamw_step takes
+ * step, lr and seed from the host, so a replayed graph would repeat one step's bias correction
+ * and random bits; here they are in device memory, 16-byte aligned, and move with each replay.
+ * Once per step mok_adamw_advance adds one to clock->step and fills in what follows from it
+ * (cfg's betas); mok_adamw_step_at then updates a list of tensors (as often as there are lists)
+ * with that step, clock->lr, and the seed cfg->seed + clock->step * clock->seed_stride. cfg's
+ * step and lr have to be valid but are not used. A step below one, or an lr that is negative or
+ * not finite, raises MOK_ERR_DEVICE_INVARIANT and leaves the parameters as they are. */
+typedef struct mok_adamw_clock {
+    int64_t step;         /* steps taken */
+    uint64_t seed_stride; /* what the seed moves by from step to step */
+    double lr;
+    float step_lr, step_size, inv_root; /* lr, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t): of the
+                                           step, written by mok_adamw_advance */
+    float reserved;
+} mok_adamw_clock;
+
+mok_status mok_adamw_advance(const mok_adamw_config *cfg, mok_adamw_clock *clock,
+                             cudaStream_t stream);
+mok_status mok_adamw_step_at(const mok_adamw_config *cfg, const mok_adamw_tensor *tensors,
+                             int32_t n_tensors, const mok_adamw_clock *clock,
+                             const float *grad_scale, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

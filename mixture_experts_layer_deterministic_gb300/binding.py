@@ -89,7 +89,7 @@ EXPORTED = [
     "mok_check_rows_config", "mok_build_row_map", "mok_dispatch", "mok_dispatch_backward",
     "mok_combine", "mok_combine_backward", "mok_check_adamw_config", "mok_adamw_step",
     "mok_check_linear_config", "mok_linear_workspace_size", "mok_linear_forward",
-    "mok_linear_backward",
+    "mok_linear_backward", "mok_adamw_advance", "mok_adamw_step_at",
 ]
 
 # bytes of the fixed scratch array behind mok_build_schedule_noalloc
@@ -224,6 +224,9 @@ def lib():
             "mok_check_adamw_config": ([adamp], ctypes.c_int),
             "mok_adamw_step": ([adamp, ctypes.POINTER(MokAdamwTensor), i32, p, p],
                                ctypes.c_int),
+            "mok_adamw_advance": ([adamp, p, p], ctypes.c_int),
+            "mok_adamw_step_at": ([adamp, ctypes.POINTER(MokAdamwTensor), i32, p, p, p],
+                                  ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -527,3 +530,17 @@ def mok_adamw_step(cfg, tensors, grad_scale=None, stream=None) -> int:
     """One step over an AdamwList (make_adamw_list)."""
     return lib().mok_adamw_step(ctypes.byref(cfg), tensors.array, tensors.n, _ptr(grad_scale),
                                 _stream(stream))
+
+
+# words of 8 bytes of a mok_adamw_clock: step, seed_stride (int64), lr (float64), written scalars
+ADAMW_CLOCK_WORDS = 5
+
+
+def mok_adamw_advance(cfg, clock, stream=None) -> int:
+    return lib().mok_adamw_advance(ctypes.byref(cfg), _ptr(clock), _stream(stream))
+
+
+def mok_adamw_step_at(cfg, tensors, clock, grad_scale=None, stream=None) -> int:
+    """One step over an AdamwList, its number, lr and seed from the clock."""
+    return lib().mok_adamw_step_at(ctypes.byref(cfg), tensors.array, tensors.n, _ptr(clock),
+                                   _ptr(grad_scale), _stream(stream))

@@ -380,10 +380,14 @@ class AdamW:
     bf16) and, where they apply, copy (bf16 working weights of an fp32 p) and weight_decay. All
     are packed and stay where they are: a step reads the gradients at the addresses they had when
     the list was given. The states are fp32, or MXFP8 with eight_bit. Parameters that share their
-    types go in one launch. Arrays that do not fit raise ValueError."""
+    types go in one launch. Arrays that do not fit raise ValueError.
+
+    A step takes its number t, lr and seed from this object, so a CUDA graph that captured one
+    would replay that step. With `capturable` they are on the device and move with each replay
+    (one more launch a step): set_lr changes lr, and t does not count replays."""
 
     def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, eight_bit=False,
-                 stochastic=True, seed=0, device="cuda"):
+                 stochastic=True, seed=0, device="cuda", capturable=False):
         self.lr, self.betas, self.eps, self.seed, self.t = lr, betas, eps, seed, 0
         self.state = B.MOK_STATE_MXFP8 if eight_bit else B.MOK_STATE_F32
         self.flags = B.MOK_ADAMW_STOCHASTIC if stochastic else 0
@@ -404,14 +408,34 @@ class AdamW:
                     e[k + "_scale"] = torch.zeros((n + 31) // 32, **u8)
             groups.setdefault(kinds, []).append(dict(e, n=n))
         self.lists = [(kinds, B.make_adamw_list(g)) for kinds, g in groups.items()]
-        self.device = device
+        self.device, self.clock = device, None
+        if capturable:
+            self.clock = torch.zeros(B.ADAMW_CLOCK_WORDS, dtype=torch.int64, device=device)
+            self.clock[1] = len(self.lists)
+            self.set_lr(lr)
+
+    def set_lr(self, lr):
+        """The learning rate from the next step on."""
+        self.lr = lr
+        if self.clock is not None:
+            self.clock.view(torch.float64)[2] = lr
 
     def step(self, grad_scale=None, stream=None):
         if grad_scale is not None:
             _check_vector("grad_scale", grad_scale, torch.float32, self.device, 1)
         self.t += 1
+        if self.clock is not None:
+            return self._step_at(grad_scale, stream)
         for k, ((p, g), tensors) in enumerate(self.lists):
             cfg = B.make_adamw(self.lr, *self.betas, self.eps, self.t,
                                (self.seed + self.t * len(self.lists) + k) & (2 ** 64 - 1), p, g,
                                self.state, self.flags)
             B.check(B.mok_adamw_step(cfg, tensors, grad_scale, stream), "adamw")
+
+    def _step_at(self, grad_scale, stream):
+        for k, ((p, g), tensors) in enumerate(self.lists):
+            cfg = B.make_adamw(self.lr, *self.betas, self.eps, 1,
+                               (self.seed + k) & (2 ** 64 - 1), p, g, self.state, self.flags)
+            if k == 0:
+                B.check(B.mok_adamw_advance(cfg, self.clock, stream), "adamw clock")
+            B.check(B.mok_adamw_step_at(cfg, tensors, self.clock, grad_scale, stream), "adamw")

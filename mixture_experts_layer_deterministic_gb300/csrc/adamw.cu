@@ -35,7 +35,7 @@ struct TensorDesc {
     int64_t n;
     int64_t base;    // element number of the tensor's first element
     uint32_t first;  // its first chunk
-    float decay;     // 1 - lr weight_decay
+    float decay;     // 1 - lr weight_decay (weight_decay where a clock has lr)
 };
 
 struct Scalars {
@@ -47,6 +47,7 @@ struct Scalars {
     int n_tensors;
     uint32_t n_chunks;
     const float *gscale;
+    const mok_adamw_clock *clock;  // nullptr, or where step, inv_root, lr and the seed's step are
 };
 
 template <int NT>
@@ -238,7 +239,7 @@ MOK_DEV uint2 encode8(const float (&x)[PER], const uint32_t (&r16)[PER], uint32_
 
 // this thread's 8 elements from element i of tensor t
 template <bool PF32, bool GF32, bool S8, bool SR, bool FULL>
-MOK_DEV void update8(const Scalars &S, const TensorDesc &t, int64_t i, float gs) {
+MOK_DEV void update8(const Scalars &S, const TensorDesc &t, float decay, int64_t i, float gs) {
     const int64_t n = t.n;
     float p[PER], g[PER], m[PER], v[PER];
     load8<PF32, FULL>(t.p, i, n, p);
@@ -289,7 +290,7 @@ MOK_DEV void update8(const Scalars &S, const TensorDesc &t, int64_t i, float gs)
         m[j] = fmaf(S.a1, gj, m[j]);
         v[j] = fmaf(S.a2, gj * gj, v[j]);
         s[j] = sqrt_approx(v[j]);
-        p[j] = fmaf(p[j], t.decay, -S.step * __fdividef(m[j], fmaf(s[j], S.inv_root, S.eps)));
+        p[j] = fmaf(p[j], decay, -S.step * __fdividef(m[j], fmaf(s[j], S.inv_root, S.eps)));
     }
     if (PF32) {
         store8_f32<FULL>(t.p, i, n, p);
@@ -328,38 +329,60 @@ MOK_DEV void update8(const Scalars &S, const TensorDesc &t, int64_t i, float gs)
     }
 }
 
-template <int NT, bool PF32, bool GF32, bool S8, bool SR>
+// The step that follows: one thread, in 64 bits as the host has it.
+__global__ void advance_kernel(mok_adamw_clock *c, double b1, double b2, int *status) {
+    const int64_t t = c->step + 1;
+    const double lr = c->lr;
+    const bool ok = t >= 1 && lr >= 0 && isfinite(lr);
+    if (!ok) raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+    c->step = t;
+    c->step_lr = ok ? (float)lr : 0.f;  // a step of nothing
+    c->step_size = ok ? (float)(lr / (1.0 - pow(b1, (double)t))) : 0.f;
+    c->inv_root = ok ? (float)(1.0 / sqrt(1.0 - pow(b2, (double)t))) : 1.f;
+}
+
+template <int NT, bool PF32, bool GF32, bool S8, bool SR, bool CLOCK>
 __global__ void __launch_bounds__(TPB)
     adamw_kernel(const __grid_constant__ Params<NT> P) {
-    const Scalars &S = P.s;
-    const float gs = S.gscale != nullptr ? *S.gscale : 1.0f;
+    const float gs = P.s.gscale != nullptr ? *P.s.gscale : 1.0f;
     const uint32_t c = blockIdx.x;
-    int lo = 0, hi = S.n_tensors - 1;  // the last tensor whose first chunk is <= c
+    int lo = 0, hi = P.s.n_tensors - 1;  // the last tensor whose first chunk is <= c
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (P.t[mid].first <= c) lo = mid; else hi = mid - 1;
     }
     const TensorDesc &t = P.t[lo];
     const int64_t i0 = (int64_t)(c - t.first) * CHUNK, i = i0 + (int64_t)threadIdx.x * PER;
-    if (i0 + CHUNK <= t.n)
-        update8<PF32, GF32, S8, SR, true>(S, t, i, gs);
-    else
-        update8<PF32, GF32, S8, SR, false>(S, t, i, gs);
+    const auto update = [&](const Scalars &S, float decay) {
+        if (i0 + CHUNK <= t.n)
+            update8<PF32, GF32, S8, SR, true>(S, t, decay, i, gs);
+        else
+            update8<PF32, GF32, S8, SR, false>(S, t, decay, i, gs);
+    };
+    if constexpr (CLOCK) {
+        Scalars S = P.s;
+        const mok_adamw_clock k = *S.clock;
+        S.step = k.step_size;
+        S.inv_root = k.inv_root;
+        const uint64_t seed = ((uint64_t)S.seed_hi << 32 | S.seed_lo) + (uint64_t)k.step * k.seed_stride;
+        S.seed_lo = (uint32_t)seed;
+        S.seed_hi = (uint32_t)(seed >> 32);
+        update(S, fmaf(-k.step_lr, t.decay, 1.0f));
+    } else {
+        update(P.s, t.decay);
+    }
 }
 
-template <int NT, bool PF32, bool GF32, bool S8, bool SR>
-cudaError_t launch(const Params<NT> &P, cudaStream_t s) {
-    adamw_kernel<NT, PF32, GF32, S8, SR><<<P.s.n_chunks, TPB, 0, s>>>(P);
-    return cudaGetLastError();
-}
-
-template <int NT>
+template <bool CLOCK, int NT>
 cudaError_t launch_group(const mok_adamw_config &c, Params<NT> &P, cudaStream_t s) {
     const bool pf = c.p_dtype == MOK_DTYPE_F32, gf = c.g_dtype == MOK_DTYPE_F32;
     const bool s8 = c.state == MOK_STATE_MXFP8;
     const bool sr = (c.flags & MOK_ADAMW_STOCHASTIC) != 0 && (s8 || !pf);
-#define MOK_ADAMW_CASE(p_, g_, s_, r_) \
-    if (pf == p_ && gf == g_ && s8 == s_ && sr == r_) return launch<NT, p_, g_, s_, r_>(P, s)
+#define MOK_ADAMW_CASE(p_, g_, s_, r_)                                                          \
+    if (pf == p_ && gf == g_ && s8 == s_ && sr == r_) {                                         \
+        adamw_kernel<NT, p_, g_, s_, r_, CLOCK><<<P.s.n_chunks, TPB, 0, s>>>(P);                \
+        return cudaGetLastError();                                                              \
+    }
     MOK_ADAMW_CASE(true, true, false, false);
     MOK_ADAMW_CASE(true, false, false, false);
     MOK_ADAMW_CASE(true, true, true, false);
@@ -379,9 +402,10 @@ cudaError_t launch_group(const mok_adamw_config &c, Params<NT> &P, cudaStream_t 
 }
 
 // tensors [t0, t1) as one launch; *base: element number of the first, advanced past the last
-template <int NT>
+template <bool CLOCK, int NT>
 cudaError_t step_group(const mok_adamw_config &c, const mok_adamw_tensor *ts, int t0, int t1,
-                       const float *gscale, int64_t *base, cudaStream_t s) {
+                       const mok_adamw_clock *clock, const float *gscale, int64_t *base,
+                       cudaStream_t s) {
     Params<NT> P;
     const double bc1 = 1.0 - pow(c.beta1, (double)c.step);
     const double bc2 = 1.0 - pow(c.beta2, (double)c.step);
@@ -395,13 +419,15 @@ cudaError_t step_group(const mok_adamw_config &c, const mok_adamw_tensor *ts, in
     P.s.seed_lo = (uint32_t)c.seed;
     P.s.seed_hi = (uint32_t)(c.seed >> 32);
     P.s.gscale = gscale;
+    P.s.clock = clock;
     int n = 0;
     int64_t chunks = 0;
     for (int i = t0; i < t1; ++i) {
         const mok_adamw_tensor &t = ts[i];
         if (t.n == 0) continue;
+        const float decay = (float)(CLOCK ? t.weight_decay : 1.0 - c.lr * t.weight_decay);
         P.t[n++] = TensorDesc{t.p, t.copy, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, *base,
-                              (uint32_t)chunks, (float)(1.0 - c.lr * t.weight_decay)};
+                              (uint32_t)chunks, decay};
         chunks += (t.n + CHUNK - 1) / CHUNK;
         *base += (t.n + 31) & ~(int64_t)31;
     }
@@ -409,7 +435,29 @@ cudaError_t step_group(const mok_adamw_config &c, const mok_adamw_tensor *ts, in
     if (chunks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     P.s.n_tensors = n;
     P.s.n_chunks = (uint32_t)chunks;
-    return launch_group<NT>(c, P, s);
+    return launch_group<CLOCK, NT>(c, P, s);
+}
+
+mok_status check_step(const mok_adamw_config *c, const mok_adamw_tensor *tensors,
+                      int32_t n_tensors, int **status) {
+    mok_status st = mok_check_adamw_config(c);
+    if (st != MOK_OK) return st;
+    if ((st = current_device_status_word(status)) != MOK_OK) return st;
+    if (n_tensors < 0 || (n_tensors > 0 && tensors == nullptr)) return MOK_ERR_INVALID_ARG;
+    const bool s8 = c->state == MOK_STATE_MXFP8;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const mok_adamw_tensor &t = tensors[i];
+        if (t.n < 0 || t.n > ((int64_t)1 << 40) || !std::isfinite(t.weight_decay))
+            return MOK_ERR_INVALID_ARG;
+        if (t.copy != nullptr && c->p_dtype != MOK_DTYPE_F32) return MOK_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (!t.p || !t.g || !t.m || !t.v || (s8 && (!t.m_scale || !t.v_scale)))
+            return MOK_ERR_INVALID_ARG;
+        const void *ps[] = {t.p, t.copy, t.g, t.m, t.v};
+        for (const void *p : ps)
+            if (!op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    }
+    return MOK_OK;
 }
 
 }  // namespace
@@ -435,33 +483,46 @@ mok_status mok_check_adamw_config(const mok_adamw_config *c) {
 
 mok_status mok_adamw_step(const mok_adamw_config *c, const mok_adamw_tensor *tensors,
                           int32_t n_tensors, const float *grad_scale, cudaStream_t stream) {
+    int *status;
+    const mok_status st = check_step(c, tensors, n_tensors, &status);
+    if (st != MOK_OK) return st;
+    int64_t base = 0;
+    for (int t0 = 0; t0 < n_tensors; t0 += NT_LARGE) {
+        const int t1 = n_tensors - t0 < NT_LARGE ? n_tensors : t0 + NT_LARGE, n = t1 - t0;
+        MOK_OP_LAUNCH(OP_ADAMW, 1,
+                      (n <= NT_SMALL ? step_group<false, NT_SMALL>
+                       : n <= NT_MID ? step_group<false, NT_MID>
+                                     : step_group<false, NT_LARGE>)(*c, tensors, t0, t1, nullptr,
+                                                                    grad_scale, &base, stream));
+    }
+    return MOK_OK;
+}
+
+mok_status mok_adamw_advance(const mok_adamw_config *c, mok_adamw_clock *clock,
+                             cudaStream_t stream) {
     mok_status st = mok_check_adamw_config(c);
     if (st != MOK_OK) return st;
     int *status;
     if ((st = current_device_status_word(&status)) != MOK_OK) return st;
-    if (n_tensors < 0 || (n_tensors > 0 && tensors == nullptr)) return MOK_ERR_INVALID_ARG;
-    const bool s8 = c->state == MOK_STATE_MXFP8;
-    for (int32_t i = 0; i < n_tensors; ++i) {
-        const mok_adamw_tensor &t = tensors[i];
-        if (t.n < 0 || t.n > ((int64_t)1 << 40) || !std::isfinite(t.weight_decay))
-            return MOK_ERR_INVALID_ARG;
-        if (t.copy != nullptr && c->p_dtype != MOK_DTYPE_F32) return MOK_ERR_INVALID_ARG;
-        if (t.n == 0) continue;
-        if (!t.p || !t.g || !t.m || !t.v || (s8 && (!t.m_scale || !t.v_scale)))
-            return MOK_ERR_INVALID_ARG;
-        const void *ps[] = {t.p, t.copy, t.g, t.m, t.v};
-        for (const void *p : ps)
-            if (!op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    }
+    if (clock == nullptr || !op_aligned16(clock)) return MOK_ERR_INVALID_ARG;
+    MOK_OP_LAUNCH(OP_ADAMW, 1,
+                  (advance_kernel<<<1, 1, 0, stream>>>(clock, c->beta1, c->beta2, status),
+                   cudaGetLastError()));
+    return MOK_OK;
+}
+
+mok_status mok_adamw_step_at(const mok_adamw_config *c, const mok_adamw_tensor *tensors,
+                             int32_t n_tensors, const mok_adamw_clock *clock,
+                             const float *grad_scale, cudaStream_t stream) {
+    int *status;
+    const mok_status st = check_step(c, tensors, n_tensors, &status);
+    if (st != MOK_OK) return st;
+    if (clock == nullptr || !op_aligned16(clock)) return MOK_ERR_INVALID_ARG;
     int64_t base = 0;
-    for (int t0 = 0; t0 < n_tensors; t0 += NT_LARGE) {
-        const int t1 = n_tensors - t0 < NT_LARGE ? n_tensors : t0 + NT_LARGE;
+    for (int t0 = 0; t0 < n_tensors; t0 += NT_MID) {
+        const int t1 = n_tensors - t0 < NT_MID ? n_tensors : t0 + NT_MID;
         MOK_OP_LAUNCH(OP_ADAMW, 1,
-                   t1 - t0 <= NT_SMALL
-                       ? step_group<NT_SMALL>(*c, tensors, t0, t1, grad_scale, &base, stream)
-                   : t1 - t0 <= NT_MID
-                       ? step_group<NT_MID>(*c, tensors, t0, t1, grad_scale, &base, stream)
-                       : step_group<NT_LARGE>(*c, tensors, t0, t1, grad_scale, &base, stream));
+                      (step_group<true, NT_MID>)(*c, tensors, t0, t1, clock, grad_scale, &base, stream));
     }
     return MOK_OK;
 }
