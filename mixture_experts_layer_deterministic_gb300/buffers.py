@@ -185,31 +185,33 @@ def _mok_dtype(dtype):
     return B.MOK_DTYPE_F32 if dtype == torch.float32 else B.MOK_DTYPE_BF16
 
 
-def _check_kind(name, t, dtype, device):
-    if t.dtype != dtype or t.device.type != device.type:
-        raise ValueError("%s: %s on %s, not %s on %s" % (name, dtype, device.type, t.dtype,
-                                                         t.device.type))
+def _here(device):
+    """`device` with its index, as tensors on it name it."""
+    return torch.empty(0, device=device).device
 
 
 def _check_matrix(name, t, dtype, device, rows, cols, ld):
     """`rows` rows of `cols` elements, `ld` apart (more of either does not matter); None passes."""
     if t is None:
         return
-    _check_kind(name, t, dtype, device)
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols or \
-            (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != ld):
-        raise ValueError("%s: [%d][%d] with %d elements between rows, not %s with strides %s" %
-                         (name, rows, cols, ld, list(t.shape), list(t.stride())))
+    shape = t.shape
+    if t.dtype is dtype and t.device == device and len(shape) == 2 and shape[0] >= rows and \
+            shape[1] >= cols:
+        step = t.stride()
+        if (step[1] == 1 or cols == 1) and (step[0] == ld or rows <= 1):
+            return
+    raise ValueError("%s: %s [%d][%d] with %d elements between rows on %s, not %s %s with strides "
+                     "%s on %s" % (name, dtype, rows, cols, ld, device, t.dtype, list(shape),
+                                   list(t.stride()), t.device))
 
 
 def _check_vector(name, t, dtype, device, n):
     """`n` packed elements of any shape; None passes."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.device == device and t.numel() == n and
+                     t.is_contiguous()):
         return
-    _check_kind(name, t, dtype, device)
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError("%s: %d packed elements, not %s with strides %s" %
-                         (name, n, list(t.shape), list(t.stride())))
+    raise ValueError("%s: %d packed elements of %s on %s, not %s %s with strides %s on %s" %
+                     (name, n, dtype, device, t.dtype, list(t.shape), list(t.stride()), t.device))
 
 
 class TokenSort:
@@ -232,6 +234,7 @@ class TokenSort:
         self.map = _empty(T * K, torch.int32, self.device)
         self.starts = _empty(E + 1, torch.int32, self.device)
         self.kept = _empty(E, torch.int32, self.device)
+        self.here = self.map.device
 
     def rows(self, width=None):
         """A zeroed sorted array [n_rows][width] whose rows start on 16-byte boundaries."""
@@ -240,15 +243,13 @@ class TokenSort:
         return torch.zeros(self.n_rows, (w + per - 1) // per * per, dtype=self.dtype,
                            device=self.device)[:, :w]
 
-    def _check(self, n, /, **arrays):
-        for name, t in arrays.items():
-            _check_matrix(name, t, self.dtype, self.device, n, self.H, self.ld)
+    def _check(self, name, t, n):
+        _check_matrix(name, t, self.dtype, self.here, n, self.H, self.ld)
 
     def _check_ids(self, name, t, dtype):
         """One value per routed id (the helpers' own arrays have one where there are no ids)."""
-        if t is not None and self.T * self.K == 0:
-            return _check_kind(name, t, dtype, self.device)
-        _check_vector(name, t, dtype, self.device, self.T * self.K)
+        n = self.T * self.K
+        _check_vector(name, t, dtype, self.here, n if n or t is None else t.numel())
 
     def build(self, idx, sched, stream=None):
         """The row map of `sched` (a Schedule built from idx [T][K])."""
@@ -260,28 +261,30 @@ class TokenSort:
                                     stream), "row map")
 
     def dispatch(self, x, xs, stream=None):
-        self._check(self.T, x=x)
-        self._check(self.n_rows, xs=xs)
+        self._check("x", x, self.T)
+        self._check("xs", xs, self.n_rows)
         B.check(B.mok_dispatch(self.cfg, x, self.map, self.starts, self.kept, xs, stream),
                 "dispatch")
         return xs
 
     def dispatch_backward(self, dxs, dx, stream=None):
-        self._check(self.T, dx=dx)
-        self._check(self.n_rows, dxs=dxs)
+        self._check("dx", dx, self.T)
+        self._check("dxs", dxs, self.n_rows)
         B.check(B.mok_dispatch_backward(self.cfg, dxs, self.map, dx, stream), "dispatch backward")
         return dx
 
     def combine(self, rows, topk_w, y, residual=None, stream=None):
-        self._check(self.T, y=y, residual=residual)
-        self._check(self.n_rows, rows=rows)
+        self._check("y", y, self.T)
+        self._check("residual", residual, self.T)
+        self._check("rows", rows, self.n_rows)
         self._check_ids("topk_w", topk_w, torch.float32)
         B.check(B.mok_combine(self.cfg, rows, self.map, topk_w, residual, y, stream), "combine")
         return y
 
     def combine_backward(self, dy, rows, topk_w, drows, d_topk_w, stream=None):
-        self._check(self.T, dy=dy)
-        self._check(self.n_rows, rows=rows, drows=drows)
+        self._check("dy", dy, self.T)
+        self._check("rows", rows, self.n_rows)
+        self._check("drows", drows, self.n_rows)
         self._check_ids("topk_w", topk_w, torch.float32)
         self._check_ids("d_topk_w", d_topk_w, torch.float32)
         B.check(B.mok_combine_backward(self.cfg, dy, rows, self.map, self.starts, self.kept,
@@ -305,7 +308,12 @@ class Linear:
         B.check(B.mok_check_linear_config(self.cfg), "linear config")
         self.out_dtype, self.grad_dtype = out_dtype, grad_dtype
         self.device = torch.device(device)
+        self.here = _here(self.device)
         self.ws = [None, None]
+        self.groups = groups
+        self.wide = (rows, in_features, int(self.cfg.ld_in))    # x, dx
+        self.out = (rows, out_features, int(self.cfg.ld_out))   # y, dy, z, residual
+        self.of_w = (out_features, in_features, int(self.cfg.ld_w))
 
     def weights(self, dtype=torch.bfloat16):
         """Zeros [groups][out][in] whose rows lie as the layer reads them: a view of a packed
@@ -320,42 +328,38 @@ class Linear:
             self.ws[which] = (_empty(n, torch.uint8, self.device), n)
         return self.ws[which]
 
-    def _check_rows(self, **arrays):
-        """name=(array or None, dtype): arrays of the layer's rows, x and dx of its inputs, the
-        others of its outputs."""
-        c = self.cfg
-        for name, (t, dtype) in arrays.items():
-            inputs = name in ("x", "dx")
-            _check_matrix(name, t, dtype, self.device, c.rows,
-                          c.in_features if inputs else c.out_features,
-                          c.ld_in if inputs else c.ld_out)
-
-    def _check_weights(self, **arrays):
-        c = self.cfg
-        for name, (t, dtype) in arrays.items():
-            rows = c.groups * c.out_features
-            if t is not None and t.dim() == 3:
-                if t.shape[0] != c.groups or t.shape[1] != c.out_features or \
-                        (c.groups > 1 and t.stride(0) != c.out_features * c.ld_w):
-                    raise ValueError("%s: [%d][%d][%d] with %d elements between rows, not %s with "
-                                     "strides %s" % (name, c.groups, c.out_features,
-                                                     c.in_features, c.ld_w, list(t.shape),
-                                                     list(t.stride())))
-                t, rows = t[0], c.out_features  # the groups follow one another
-            _check_matrix(name, t, dtype, self.device, rows, c.in_features, c.ld_w)
+    def _check_weights(self, name, t, dtype):
+        """[groups][out][in], or [groups * out][in]."""
+        if t is None:
+            return
+        n, k, ld = self.of_w
+        shape = t.shape
+        if len(shape) == 3 and shape[0] == self.groups and shape[1] == n and \
+                (self.groups == 1 or t.stride(0) == n * ld) and (n == 1 or t.stride(1) == ld) and \
+                (k == 1 or t.stride(2) == 1) and shape[2] >= k and t.dtype is dtype and \
+                t.device == self.here:
+            return
+        if len(shape) == 3:
+            raise ValueError("%s: %s [%d][%d][%d] with %d elements between rows on %s, not %s %s "
+                             "with strides %s on %s" % (name, dtype, self.groups, n, k, ld,
+                                                        self.here, t.dtype, list(shape),
+                                                        list(t.stride()), t.device))
+        _check_matrix(name, t, dtype, self.here, self.groups * n, k, ld)
 
     def _check_sort(self, sort):
-        if sort is None and self.cfg.groups > 1:
-            raise ValueError("%d groups of rows need the TokenSort that made them" %
-                             self.cfg.groups)
-        if sort is not None and sort.E != self.cfg.groups:
-            raise ValueError("the sort has %d groups, the layer %d" % (sort.E, self.cfg.groups))
+        if sort is None and self.groups > 1:
+            raise ValueError("%d groups of rows need the TokenSort that made them" % self.groups)
+        if sort is not None and sort.E != self.groups:
+            raise ValueError("the sort has %d groups, the layer %d" % (sort.E, self.groups))
 
     def forward(self, x, w, y, bias=None, residual=None, z=None, sort=None, stream=None):
-        bf, n = torch.bfloat16, self.cfg.groups * self.cfg.out_features
-        self._check_rows(x=(x, bf), y=(y, self.out_dtype), residual=(residual, bf), z=(z, bf))
-        self._check_weights(w=(w, bf))
-        _check_vector("bias", bias, torch.float32, self.device, n)
+        bf, here = torch.bfloat16, self.here
+        _check_matrix("x", x, bf, here, *self.wide)
+        _check_matrix("y", y, self.out_dtype, here, *self.out)
+        _check_matrix("residual", residual, bf, here, *self.out)
+        _check_matrix("z", z, bf, here, *self.out)
+        self._check_weights("w", w, bf)
+        _check_vector("bias", bias, torch.float32, here, self.groups * self.of_w[0])
         self._check_sort(sort)
         ws, n = self._ws(B.MOK_LINEAR_FORWARD)
         B.check(B.mok_linear_forward(self.cfg, x, w, bias, residual, sort and sort.starts,
@@ -363,10 +367,14 @@ class Linear:
         return y
 
     def backward(self, x, w, dy, z=None, dx=None, dw=None, db=None, sort=None, stream=None):
-        bf, n = torch.bfloat16, self.cfg.groups * self.cfg.out_features
-        self._check_rows(x=(x, bf), dy=(dy, self.out_dtype), z=(z, bf), dx=(dx, self.grad_dtype))
-        self._check_weights(w=(w, bf), dw=(dw, self.grad_dtype))
-        _check_vector("db", db, torch.float32, self.device, n)
+        bf, here = torch.bfloat16, self.here
+        _check_matrix("x", x, bf, here, *self.wide)
+        _check_matrix("dy", dy, self.out_dtype, here, *self.out)
+        _check_matrix("z", z, bf, here, *self.out)
+        _check_matrix("dx", dx, self.grad_dtype, here, *self.wide)
+        self._check_weights("w", w, bf)
+        self._check_weights("dw", dw, self.grad_dtype)
+        _check_vector("db", db, torch.float32, here, self.groups * self.of_w[0])
         self._check_sort(sort)
         ws, n = self._ws(B.MOK_LINEAR_BACKWARD)
         B.check(B.mok_linear_backward(self.cfg, x, w, z, dy, sort and sort.starts,
@@ -391,7 +399,7 @@ class AdamW:
         self.lr, self.betas, self.eps, self.seed, self.t = lr, betas, eps, seed, 0
         self.state = B.MOK_STATE_MXFP8 if eight_bit else B.MOK_STATE_F32
         self.flags = B.MOK_ADAMW_STOCHASTIC if stochastic else 0
-        device, groups = torch.device(device), {}
+        device, groups = _here(device), {}
         for q in params:
             e, p = dict(q), q["p"]
             n, kinds = p.numel(), (_mok_dtype(p.dtype), _mok_dtype(q["g"].dtype))
