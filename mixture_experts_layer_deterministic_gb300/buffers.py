@@ -214,6 +214,13 @@ def _check_vector(name, t, dtype, device, n):
                      (name, n, dtype, device, t.dtype, list(t.shape), list(t.stride()), t.device))
 
 
+def _torch_stream(stream):
+    """The torch stream that an entry point's `stream` argument names."""
+    if stream is None:
+        return torch.cuda.current_stream()
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream)
+
+
 class TokenSort:
     """Tokens sorted by expert and back: the row map of a schedule and the four passes over it.
     Sorted arrays come from `rows()`: expert e owns rows starts[e] .. starts[e] + kept[e],
@@ -297,7 +304,8 @@ class Linear:
     rows (forward and backward then take the TokenSort that sorted them). Weights are
     [groups][out][in] bf16; rows of x, y, z, dy, dx and of the weights start on 16-byte
     boundaries, which packed rows do where their width is a multiple of 8 (`weights()` makes an
-    array for any width). y and dy have out_dtype, dx and dw grad_dtype, bias and db are fp32,
+    array for any width). Calls of one Linear share its workspaces, so calls on several streams
+    have to be ordered by the caller. y and dy have out_dtype, dx and dw grad_dtype, bias and db are fp32,
     everything else is bf16. Arrays that do not fit raise ValueError before anything is
     launched."""
 
@@ -322,11 +330,19 @@ class Linear:
         return torch.zeros(c.groups, c.out_features, c.ld_w, dtype=dtype,
                            device=self.device)[..., :c.in_features]
 
-    def _ws(self, which):
+    def _ws(self, which, stream):
+        """The workspace of a pass, its size and the stream's handle. It comes from the memory of the stream that first
+        runs the pass, whose earlier work is then done with it; other streams are recorded, so it
+        is not given away under their work."""
+        handle = B._stream(stream) if self.here.type == "cuda" else 0
         if self.ws[which] is None:
             n = B.mok_linear_workspace_size(self.cfg, which)
-            self.ws[which] = (_empty(n, torch.uint8, self.device), n)
-        return self.ws[which]
+            with torch.cuda.stream(None if stream is None else _torch_stream(stream)):
+                self.ws[which] = (_empty(n, torch.uint8, self.here), n, handle)
+        ws, n, first = self.ws[which]
+        if handle != first:
+            ws.record_stream(_torch_stream(stream))
+        return ws, n, handle
 
     def _check_weights(self, name, t, dtype):
         """[groups][out][in], or [groups * out][in]."""
@@ -361,9 +377,9 @@ class Linear:
         self._check_weights("w", w, bf)
         _check_vector("bias", bias, torch.float32, here, self.groups * self.of_w[0])
         self._check_sort(sort)
-        ws, n = self._ws(B.MOK_LINEAR_FORWARD)
+        ws, n, handle = self._ws(B.MOK_LINEAR_FORWARD, stream)
         B.check(B.mok_linear_forward(self.cfg, x, w, bias, residual, sort and sort.starts,
-                                     sort and sort.kept, y, z, ws, n, stream), "linear forward")
+                                     sort and sort.kept, y, z, ws, n, handle), "linear forward")
         return y
 
     def backward(self, x, w, dy, z=None, dx=None, dw=None, db=None, sort=None, stream=None):
@@ -376,9 +392,9 @@ class Linear:
         self._check_weights("dw", dw, self.grad_dtype)
         _check_vector("db", db, torch.float32, here, self.groups * self.of_w[0])
         self._check_sort(sort)
-        ws, n = self._ws(B.MOK_LINEAR_BACKWARD)
+        ws, n, handle = self._ws(B.MOK_LINEAR_BACKWARD, stream)
         B.check(B.mok_linear_backward(self.cfg, x, w, z, dy, sort and sort.starts,
-                                      sort and sort.kept, dx, dw, db, ws, n, stream),
+                                      sort and sort.kept, dx, dw, db, ws, n, handle),
                 "linear backward")
         return dx
 

@@ -99,6 +99,39 @@ def test_linear_helper_with_an_odd_width():
         lin.forward(x, torch.zeros(1, 77, 1001, **bf), y)
 
 
+def test_workspaces_belong_to_the_stream_that_uses_them():
+    """A Linear's workspace comes from the memory of the stream of the pass (other memory may still
+    be in use by the current stream's earlier work), and the passes run on either kind of handle."""
+    torch = _t()
+    from mixture_experts_layer_deterministic_gb300.buffers import Linear
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, dy = torch.randn(300, 64, **bf), torch.randn(300, 48, **bf)
+    y, dx = torch.zeros(300, 48, **bf), torch.zeros(300, 64, **bf)
+    s = torch.cuda.Stream()
+
+    def owner(t):
+        for seg in torch.cuda.memory_snapshot():
+            if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+                return seg["stream"]
+
+    for handle in (s, s.cuda_stream, None):
+        lin = Linear(300, 64, 48, act=B.MOK_ACT_SILU)
+        w = lin.weights()
+        w.normal_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s if handle is None else None):
+            lin.forward(x, w, y, stream=handle)
+            lin.backward(x, w, dy, z=dy, dx=dx, stream=handle)
+        s.synchronize()
+        assert [owner(ws[0]) for ws in lin.ws] == [s.cuda_stream] * 2
+        a, b = y.clone(), dx.clone()
+        torch.cuda.synchronize()
+        lin.forward(x, w, y)  # and on another stream than its own
+        lin.backward(x, w, dy, z=dy, dx=dx)
+        torch.cuda.synchronize()
+        assert torch.equal(a, y) and torch.equal(b, dx) and device_ok()
+
+
 @pytest.mark.parametrize("capacity", [0, 3])
 def test_a_schedule_of_other_ids_is_reported(capacity):
     """The schedule of 12 ids of expert 0 and 4 of expert 1, used with ids the other way round:
@@ -170,6 +203,29 @@ def test_activations_and_slopes_far_from_zero():
         assert device_ok() and torch.equal(z[:3, :14], zs.expand(3, 14))
         want = zs.float().clamp(min=0)
         assert bool(((y[:3, :14] - want).abs() <= 2.0 ** -20 * want + 1e-10).all()), act
+
+
+@pytest.mark.parametrize("kw", [
+    dict(R=10000, Kin=2100, N=1030, res=False, z=False),
+    dict(R=10000, Kin=2100, N=1030, act="silu"),
+    dict(R=10000, Kin=2100, N=1030, res=True, z=False),
+    dict(G=4, counts=[900, 0, 17, 300], Kin=2500, N=300, res=False, z=False, spare=16),
+    dict(G=4, counts=[900, 0, 17, 300], Kin=2500, N=300, act="gelu_tanh", spare=16),
+], ids=lambda k: "-".join("%s%s" % i for i in k.items()).replace(" ", ""))
+def test_fp32_outputs_over_several_segments(kw):
+    c = Lin(out="fp32", **kw)
+    y, _ = check_forward(c)
+    k = c.Kin
+    for g, (a, b) in enumerate(c.spans()):
+        if b == a:
+            continue
+        ref = c.x[a:b, :k].double() @ c.w[g * c.N:(g + 1) * c.N, :k].double().T
+        if c.b is not None:
+            ref = ref + c.b[g * c.N:(g + 1) * c.N].double()
+        ref, _ = act64(ref, c.act)
+        if c.res is not None:
+            ref = ref + c.res[a:b, :c.N].double()
+        assert norm_rel(y[a:b, :c.N], ref) <= 2.0 ** -19
 
 
 @pytest.mark.parametrize("kw", [
