@@ -547,6 +547,7 @@ struct Fwd {
         return Unit{t.x, t.y, t.z - t.y, t.w, (int)(u % (uint32_t)n_mb), 0, part};
     }
     MOK_DEV int segments(const Unit &) const { return segs; }
+    MOK_DEV int long_steps(const Unit &) const { return 0; }  // K is at most 2^20
     MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
         LinGeom q;
         q.n_mma = (u.nr + 15) & ~15;
@@ -773,6 +774,7 @@ struct Dx {
         return q;
     }
     MOK_DEV int segments(const Unit &u) const { return F32 ? k_range(u).segments(halves) : 1; }
+    MOK_DEV int long_steps(const Unit &) const { return 0; }
     MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
         LinGeom q = k_range(u);
         if constexpr (F32) q.segment(seg, halves);
@@ -923,6 +925,7 @@ struct Dw {
         return q;
     }
     MOK_DEV int segments(const Unit &u) const { return F32 ? k_range(u).segments(halves) : 1; }
+    MOK_DEV int long_steps(const Unit &u) const { return F32 ? 0 : (u.nr + 15) / 16; }
     MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
         const int mb = u.mb, nb = u.nb;
         LinGeom q = k_range(u);
@@ -987,21 +990,26 @@ MOK_DEV void lin_arrive(uint32_t bar_cluster) {
                  : "memory");
 }
 // A bounded wait that takes the time only after many polls: the clock read costs more than
-// most waits here are long.
-MOK_DEV bool lin_wait(uint64_t *bar, uint32_t parity, int *status, volatile int *abort) {
+// most waits here are long. steps(): K steps that may run during it, a microsecond each on top of
+// the limit (a step takes about 0.05 us; dW of a group of 2^30 rows is one sum of some seconds).
+template <class F>
+MOK_DEV bool lin_wait(uint64_t *bar, uint32_t parity, int *status, volatile int *abort, F &&steps) {
     uint64_t t0 = 0;
     for (uint32_t n = 1; !tc::mbar_try_wait(bar, parity); ++n) {
         if ((n & 255u) != 0) continue;
         if (*abort) return false;
         const uint64_t t = tc::globaltimer();
         if (t0 == 0) t0 = t;
-        if (t - t0 > tc::WAIT_LIMIT_NS) {
+        if (t - t0 > tc::WAIT_LIMIT_NS && t - t0 > tc::WAIT_LIMIT_NS + 1000ull * (uint32_t)steps()) {
             raise_status(status, MOK_ERR_TIMEOUT);
             *abort = 1;
             return false;
         }
     }
     return true;
+}
+MOK_DEV bool lin_wait(uint64_t *bar, uint32_t parity, int *status, volatile int *abort) {
+    return lin_wait(bar, parity, status, abort, [] { return 0; });
 }
 // bounded drain of a barrier phase on the way out
 MOK_DEV void lin_drain(uint64_t *bar, uint32_t parity) {
@@ -1176,7 +1184,8 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
             const int segs = p.segments(cur);
             for (int seg = 0; seg < segs; ++seg, ++a) {
                 const int ab = (int)(a & 1);
-                ok = lin_wait(&sm->tmem_full[ab], (uint32_t)((a >> 1) & 1), p.status, abort);
+                ok = lin_wait(&sm->tmem_full[ab], (uint32_t)((a >> 1) & 1), p.status, abort,
+                              [&] { return p.long_steps(cur); });
                 if constexpr (!P::F32_OUT) ok = pt.agree(ok);
                 if (!ok) break;
                 tc::tc_fence_after();

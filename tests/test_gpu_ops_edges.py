@@ -77,6 +77,29 @@ def test_falling_starts_over_more_than_2_to_the_30_rows():
     assert int(torch.count_nonzero(y)) == 0
 
 
+def test_a_group_whose_sum_takes_seconds():
+    """dW of a group of 2^30 rows: one sum of some seconds, longer than a wait for anything else
+    may take."""
+    torch = _t()
+    rows = 1 << 30
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    cfg = B.make_linear(rows, 8, 8, 1, grad_dtype=B.MOK_DTYPE_BF16)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, dy, dw = torch.zeros(rows, 8, **bf), torch.zeros(rows, 8, **bf), torch.zeros(8, 8, **bf)
+    live = [slice(0, 300), slice(rows // 2, rows // 2 + 300), slice(rows - 300, rows)]
+    for s in live:
+        x[s], dy[s] = torch.randn(300, 8, device="cuda"), torch.randn(300, 8, device="cuda")
+    n = B.mok_linear_workspace_size(cfg, B.MOK_LINEAR_BACKWARD)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    B.check(B.mok_linear_backward(cfg, x, None, None, dy, i32([0, rows]), i32([rows]), None, dw,
+                                  None, ws, n))
+    assert device_ok()
+    xs, ds = (torch.cat([t[s] for s in live]).double() for t in (x, dy))
+    e = dot_rel(900) * (ds.abs().T @ xs.abs())
+    assert bool(((dw.double() - ds.T @ xs).abs() <= e + 2.0 ** -8 * ((ds.T @ xs).abs() + e)).all())
+
+
 def test_linear_helper_with_an_odd_width():
     """1001 inputs: weights and their gradient in rows 1008 apart, as weights() makes them."""
     torch = _t()
