@@ -290,3 +290,165 @@ def test_fp32_gradients_are_fp32(kw):
     for i in range(3):
         alone = c.backward(*[i == j for j in range(3)])
         assert torch.equal(alone[i].view(torch.uint8), (dx, dw, db)[i].view(torch.uint8))
+
+
+@pytest.mark.parametrize("kw", [dict(R=2, Kin=200, N=130), dict(R=12, Kin=520, N=40, act="silu"),
+                                dict(R=300, Kin=200, N=130, act="gelu_tanh"),
+                                dict(R=100, Kin=5000, N=90, out="fp32"),
+                                dict(R=10000, Kin=1100, N=1030, out="fp32"),
+                                dict(G=4, counts=[900, 0, 17, 300], Kin=200, N=72, act="gelu")],
+                         ids=lambda k: "-".join("%s%s" % i for i in k.items()).replace(" ", ""))
+def test_non_finite_values_stay_in_their_rows_and_features(kw):
+    """A NaN in a row of x reaches that row of y and dx alone, an infinity in a feature of W that
+    feature alone; a sum past the range is infinite, and its neighbours keep their bits."""
+    torch = _t()
+    c = Lin(z=True, **kw)
+    a, b = c.spans()[0]
+    clean, clean_z = c.forward()
+    dx0, dw0, db0 = c.backward()
+    r, f, N, k = b - 1, 3, c.N, c.Kin
+    x, w, dy = c.x.clone(), c.w.clone(), c.dy.clone()
+    c.x[r, 1] = float("nan")
+    c.w[f, 0] = float("inf")
+    y, z = c.forward()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[a:b, f] = keep[r, :N] = False
+    assert torch.equal(y[keep].isnan(), clean[keep].isnan())
+    assert torch.equal(y[keep].nan_to_num(), clean[keep].nan_to_num())
+    assert bool(y[r, :N].isnan().all()) and bool(z[r, :N].isnan().all())
+    assert not bool(z[a:b, f].isfinite().any())
+    # gradients: dx of the row takes the NaN of its dy, dW of the feature, db too
+    c.x.copy_(x)
+    c.w.copy_(w)
+    c.dy[r, f] = float("nan")
+    dx, dw, db = c.backward()
+    keep = torch.ones_like(dx, dtype=torch.bool)
+    keep[r, :k] = False
+    assert torch.equal(dx[keep], dx0[keep]) and bool(dx[r, :k].isnan().all())
+    keep = torch.ones_like(dw, dtype=torch.bool)
+    keep[f, :k] = False
+    assert torch.equal(dw[keep], dw0[keep]) and bool(dw[f, :k].isnan().all())
+    assert bool(db[f].isnan()) and torch.equal(db[f + 1:], db0[f + 1:]) and device_ok()
+    # a sum past the largest value of its type
+    c.dy.copy_(dy)
+    c.x[r, :k], c.w[f, :k] = 2.0 ** 100, 2.0 ** 60
+    y, z = c.forward()
+    assert bool((y[r, f] == float("inf")).all()) and bool((z[r, f] == float("inf")).all())
+    assert torch.equal(z[a:r, :f], clean_z[a:r, :f]) and device_ok()
+
+
+def test_sort_of_more_than_2_to_the_31_elements():
+    """Rows past 2^31 elements of their array, against the plain passes on the GPU."""
+    torch = _t()
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    T, K, E, H = 8192, 32, 64, 8250
+    c = Case(T=T, K=K, E=E, H=H)
+    assert c.n_rows * c.ld > 1 << 31
+    gen = torch.Generator("cuda").manual_seed(1)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    x, xs = torch.zeros(T, c.ld, **bf), torch.full((c.n_rows, c.ld), 9.0, **bf)
+    x.normal_(generator=gen)
+    m, st, kp, w = c.dev(c.map), c.dev(c.starts), c.dev(c.kept), c.dev(c.w)
+    B.check(B.mok_dispatch(c.cfg, x, m, st, kp, xs))
+    for k in range(K):
+        assert torch.equal(xs[m.view(T, K)[:, k].long(), :H], x[:, :H])
+    assert bool((xs[:, H:] == 9).all())
+    y = torch.zeros(T, c.ld, **bf)
+    B.check(B.mok_combine(c.cfg, xs, m, w, None, y))
+    ws = w.view(T, K).double()
+    ref = x[:, :H].double() * ws.sum(1, keepdim=True)
+    assert bool(((y[:, :H].double() - ref).abs() <=
+                 (2.0 ** -8 + (K + 2) * 2.0 ** -23) * ref.abs()).all())
+    drows, dw = torch.full((c.n_rows, c.ld), 9.0, **bf), torch.zeros(T * K, device="cuda")
+    B.check(B.mok_combine_backward(c.cfg, x, xs, m, st, kp, w, drows, dw))
+    for k in range(K):
+        ref = (x[:, :H].float() * w.view(T, K)[:, k:k + 1]).to(torch.bfloat16)
+        assert torch.equal(drows[m.view(T, K)[:, k].long(), :H], ref)
+    sq = x[:, :H].double().square().sum(1, keepdim=True)
+    assert bool(((dw.view(T, K).double() - sq).abs() <= (H + 1) * 2.0 ** -24 * sq).all())
+    assert clean_status() == B.MOK_OK
+
+
+def test_weights_of_more_than_2_to_the_31_elements():
+    """1024 groups of 1024 x 2056: the last groups' matrices lie past 2^31 elements."""
+    torch = _t()
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    G, K, N = 1024, 2056, 1024
+    assert G * N * K > 1 << 31
+    rows, bf = 16 * G, dict(dtype=torch.bfloat16, device="cuda")
+    cfg = B.make_linear(rows, K, N, G)
+    gen = torch.Generator("cuda").manual_seed(1)
+    x, w = torch.zeros(rows, K, **bf), torch.zeros(G, N, K, **bf)
+    x.normal_(generator=gen)
+    w.normal_(generator=gen)
+    dy, y = torch.zeros(rows, N, **bf), torch.full((rows, N), 7.0, **bf)
+    dy.normal_(generator=gen)
+    starts, counts = i32(list(range(0, rows + 1, 16))), i32([16] * G)
+    ws = torch.empty(max(B.mok_linear_workspace_size(cfg, i) for i in (0, 1)), dtype=torch.uint8,
+                     device="cuda")
+    B.check(B.mok_linear_forward(cfg, x, w, None, None, starts, counts, y, None, ws, ws.numel()))
+    dx, dw = torch.full_like(x, 7.0), torch.full_like(w, 7.0)
+    B.check(B.mok_linear_backward(cfg, x, w, None, dy, starts, counts, dx, dw, None, ws,
+                                  ws.numel()))
+    assert device_ok()
+    for g in (0, 1, 511, 1019, 1020, 1022, 1023):
+        s = slice(16 * g, 16 * g + 16)
+        xd, wd, dd = x[s].double(), w[g].double(), dy[s].double()
+        for got, p, q, n in ((y[s], xd, wd.T, K), (dx[s], dd, wd, N), (dw[g], dd.T, xd, 16)):
+            e = dot_rel(n) * (p.abs() @ q.abs())
+            assert bool(((got.double() - p @ q).abs() <= e + 2.0 ** -8 * ((p @ q).abs() + e)).all())
+
+
+def test_two_host_threads_on_two_streams():
+    """Passes issued by two threads at once, each on a stream of its own, give the bits that each
+    gives alone."""
+    import threading
+    torch = _t()
+    jobs = [Lin(G=5, counts=[1, 0, 300, 16, 257], Kin=200, N=136, act="silu"),
+            Lin(R=700, Kin=520, N=300, act="gelu_tanh", grad="fp32")]
+    sorts = [Case(T=300, K=4, E=16, H=264, seed=i) for i in range(2)]
+    alone, kept, failed = [], [[], []], []
+
+    def work(i, stream):
+        c, s = jobs[i], sorts[i]
+        y, z = c.forward(stream=stream)
+        keep = c._keep
+        grads = c.backward(stream=stream)
+        out = s.out
+        B.check(B.mok_dispatch(s.cfg, s.x, s.m, s.st, s.kp, out[0], stream))
+        B.check(B.mok_combine(s.cfg, out[0], s.m, s.dw, s.x, out[1], stream))
+        return (y, z, *grads), (keep, c._keep)
+
+    for s in sorts:
+        s.x, s.m, s.st, s.kp, s.dw = (s.array(s.T), s.dev(s.map), s.dev(s.starts), s.dev(s.kept),
+                                      s.dev(s.w))
+        s.out = [s.array(s.n_rows, fill=1.0), s.array(s.T, fill=1.0)]
+    for i in range(2):
+        got, _ = work(i, None)
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in (*got, *sorts[i].out)])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+
+    def loop(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                for _ in range(20):
+                    kept[i].append(work(i, streams[i]))
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and device_ok()
+    for i in range(2):
+        for got, _ in kept[i]:
+            for a, b in zip(got, alone[i]):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        for a, b in zip(sorts[i].out, alone[i][5:]):
+            assert torch.equal(a.nan_to_num(), b.nan_to_num())
