@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 
 from mixture_experts_layer_deterministic_gb300 import binding as B
+from test_gpu_adamw import Tensors, config
 from test_gpu_linear import Lin, act64, check_backward, check_forward, device_ok, dot_rel
 from test_gpu_rows import Case, clean_status
 
@@ -452,3 +453,15 @@ def test_two_host_threads_on_two_streams():
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
         for a, b in zip(sorts[i].out, alone[i][5:]):
             assert torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
+@pytest.mark.parametrize("g", ["bf16", "fp32"])
+def test_first_moment_is_the_formula_in_fp32(g):
+    """beta1 m + (1 - beta1) g with each operation rounded to fp32, bit for bit."""
+    t = Tensors([100000], "fp32", g, "fp32", seed=6)
+    d, n = t.t[0], 100000
+    f = np.float32
+    m0, g0 = d["m"][:n].cpu().numpy(), d["g"][:n].float().cpu().numpy() * f(0.5)
+    B.check(B.mok_adamw_step(config(t), t.list(), t.gs))
+    want = m0 * f(0.9) + g0 * f(1 - 0.9)
+    assert np.array_equal(d["m"][:n].cpu().numpy(), want)
