@@ -30,9 +30,9 @@ typedef enum mok_dtype { MOK_DTYPE_BF16 = 0, MOK_DTYPE_F32 = 1 } mok_dtype;
  * is -1 or a row of its own below n_rows; an entry at or past n_rows raises
  * MOK_ERR_DEVICE_INVARIANT and is treated as dropped.
  *
- * Shapes: T tokens (T >= 0), 1 <= K <= 32 experts per token, 1 <= E <= 1024 experts, H >= 1
- * columns of any number; ld_tok, ld_row >= H; T*K, n_rows < 2^31. Columns past H of a row are
- * neither read nor written. Rows are copied 16 bytes at a time where both ld are multiples of
+ * Shapes: T tokens (T >= 0), 1 <= K <= 32 experts per token, 1 <= E <= 1024 experts,
+ * 1 <= H <= 2^24 columns, any number; H <= ld_tok, ld_row <= 2^30; T*K, n_rows < 2^31. Columns
+ * past H of a row are neither read nor written. Rows are copied 16 bytes at a time where both ld are multiples of
  * 16 bytes, else element by element. */
 typedef struct mok_rows_config {
     uint32_t abi_version; /* MOK_ABI_VERSION */
@@ -50,8 +50,8 @@ mok_status mok_check_rows_config(const mok_rows_config *cfg);
 /* The row map of a schedule (mok_build_schedule; its counts, offsets and inv are read, the
  * other arrays may be NULL).
  *   topk_idx [T][K]; row_map [T*K] int32 out; starts [E+1] int32 out; kept [E] int32 out.
- * An expert id out of range, or a rank outside its expert's count, maps to -1 and raises
- * MOK_ERR_DEVICE_INVARIANT, as does starts[E] > n_rows. */
+ * An expert id out of range, or a rank outside its expert's count (the schedule is of other ids),
+ * maps to -1 and raises MOK_ERR_DEVICE_INVARIANT, as does starts[E] > n_rows. */
 mok_status mok_build_row_map(const mok_rows_config *cfg, const int32_t *topk_idx,
                              const mok_schedule *sched, int32_t *row_map, int32_t *starts,
                              int32_t *kept, cudaStream_t stream);
@@ -77,7 +77,8 @@ mok_status mok_combine(const mok_rows_config *cfg, const void *rows, const int32
 
 /* The gradients of mok_combine, with r = row_map[t*K + k]:
  *   drows[r] = topk_w[t][k] * dy[t], rounded once (zero rows as in mok_dispatch);
- *   d_topk_w[t][k] = <rows[r], dy[t]> in fp32, in a fixed order (0 where dropped).
+ *   d_topk_w[t][k] = <rows[r], dy[t]> in fp32, in a fixed order (0 where dropped, whatever dy
+ *   holds).
  * The residual's gradient is dy. Either output may be NULL (then rows is not read where
  * d_topk_w is NULL and may be NULL too), not both. drows must not overlap rows. */
 mok_status mok_combine_backward(const mok_rows_config *cfg, const void *dy, const void *rows,
@@ -98,15 +99,17 @@ mok_status mok_combine_backward(const mok_rows_config *cfg, const void *dy, cons
  *    of 16 are padding: written as zeros in y, z and dx, and read (as zeros) in x and, without
  *    an activation, dy by the weight gradient, so they must hold zeros there, as mok_dispatch
  *    and mok_combine_backward write them. Rows past that are neither read nor written. A group
- *    that breaks these rules raises MOK_ERR_DEVICE_INVARIANT and counts as empty.
+ *    that breaks these rules, or begins before the rows and padding of an earlier group end,
+ *    raises MOK_ERR_DEVICE_INVARIANT and counts as empty.
  *
  * Activations: none; relu; silu z sigma(z); gelu_tanh 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715
- * z^3))); gelu 0.5 z (1 + erf(z / sqrt 2)).
+ * z^3))); gelu 0.5 z (1 + erf(z / sqrt 2)). They and their slopes are computed to within
+ * 2^-20 (1 + |z|); for finite z far from zero the slopes are 0 or 1.
  *
  * Limits: 1 <= groups <= 1024, 1 <= in_features, out_features <= 2^20 (any number, odd ones
  * among them), 0 <= rows < 2^31 - 512, fewer than 2^31 blocks of 16 rows x 256 columns in an
  * output (x, y or all of dW); strides ld_in >= in, ld_w >= in, ld_out >= out are
- * multiples of 8 elements. Columns past a matrix's width are neither read nor written. */
+ * multiples of 8 elements, at most 2^30. Columns past a matrix's width are neither read nor written. */
 typedef enum mok_activation {
     MOK_ACT_NONE = 0,
     MOK_ACT_RELU = 1,
@@ -147,8 +150,14 @@ mok_status mok_linear_forward(const mok_linear_config *cfg, const void *x, const
 
 /* Backward, with dz = dy act'(z) (relu'(0) = 0):
  *   dx = dz W        dW[g] = sum over the group's rows of dz^T x        db[g] = sum of dz
- * dz is rounded to bf16 where it enters a product (exact where there is no activation and dy is
- * bf16); db is the fp32 sum of the unrounded dz in a fixed order. The residual's gradient is dy.
+ * How dz enters the products follows the gradients' type (it is exact where there is no activation
+ * and dy is bf16):
+ *   bf16 gradients: rounded to bf16, as the gradients are themselves. Their error is then 2.3e-3
+ *     of their norm, where rounding the results alone gives 1.7e-3;
+ *   fp32 gradients: as two bf16 values that add up to within 2^-17 of it, and sums run in
+ *     segments of 1024 terms that are added in fp32: 2.6e-6 of the norm (1.0e-6 where dz is
+ *     exact), for twice the matrix work.
+ * db is the fp32 sum of the unrounded dz in a fixed order. The residual's gradient is dy.
  *   z    [rows][out] bf16 from the forward, or NULL without an activation
  *   dx   NULL or [rows][in] out; dw NULL or [groups][out][in] out (zero for an empty group);
  *   db   NULL or [groups][out] fp32 out. At least one of the three. */
@@ -176,8 +185,10 @@ mok_status mok_linear_backward(const mok_linear_config *cfg, const void *x, cons
  *
  * Rounding: to nearest even; with MOK_ADAMW_STOCHASTIC the 8-bit states and bf16 parameters are
  * rounded up or down with probability proportional to the distance, so that changes smaller
- * than a step (v moves by 1/1000 of itself at beta2 = 0.999, E4M3 steps are 1/16 or more) are
- * kept on average. The random bits are a function of the seed and the element's number alone:
+ * than a step (sqrt(v) moves by 1/2000 of itself at beta2 = 0.999, E4M3 steps are 1/16 or more) are
+ * kept on average. It is m and sqrt(v) whose mean is kept: their rounding spreads sqrt(v) by some
+ * 15% from element to element, and v, its square, gains that variance: 2% (beta2 = 0.9) to 5%
+ * (0.999) above the fp32 state's mean in a simulation of unit normal gradients. The random bits are a function of the seed and the element's number alone:
  * with the tensors numbered one after another, each beginning at the next multiple of 32,
  * element i gets h = mix(lo32(i) ^ mix(mix(hi32(i) ^ lo32(seed)) ^ hi32(seed))), mix being
  * h ^= h>>16, h *= 0x85EBCA6B, h ^= h>>13, h *= 0xC2B2AE35, h ^= h>>16 (the MurmurHash3
