@@ -140,7 +140,9 @@ mok_status mok_check_linear_config(const mok_linear_config *cfg);
  * invalid configuration. */
 size_t mok_linear_workspace_size(const mok_linear_config *cfg, int pass);
 
-/* Forward. x, w bf16; bias NULL or fp32; residual NULL or [rows][out] bf16 (may be y where y
+/* Forward. A sum over many inputs runs on the tensor cores 1024 of them at a time where y is
+ * fp32, and the runs are added in fp32: y is then within about 1e-6 of its norm.
+ * x, w bf16; bias NULL or fp32; residual NULL or [rows][out] bf16 (may be y where y
  * is bf16); y [rows][out]; z NULL or [rows][out] bf16 out: the value before the activation,
  * which the backward needs where there is one. */
 mok_status mok_linear_forward(const mok_linear_config *cfg, const void *x, const void *w,
