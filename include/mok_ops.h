@@ -1,6 +1,7 @@
 /*
  * mok_ops.h -- operators around the expert layer of mok.h (included by it): the token sort
- * on its own, a linear layer for one matrix or one per expert, and the optimizer step.
+ * on its own, a linear layer for one matrix or one per expert, the optimizer step, a router with
+ * scores, bias and groups, layer and RMS norms, and the loss over a vocabulary.
  *
  * The conventions of mok.h hold: device pointers owned by the caller and 16-byte aligned,
  * row-major; scratch from the caller's workspace; asynchronous on `stream`; arguments
@@ -250,6 +251,176 @@ mok_status mok_adamw_advance(const mok_adamw_config *cfg, mok_adamw_clock *clock
 mok_status mok_adamw_step_at(const mok_adamw_config *cfg, const mok_adamw_tensor *tensors,
                              int32_t n_tensors, const mok_adamw_clock *clock,
                              const float *grad_scale, cudaStream_t stream);
+
+/* ---- router ---------------------------------------------------------------------------
+ *
+ * mok_route_topk takes the largest logits and a softmax over them. Here the choice of experts and
+ * their weights go by scores of all experts, a bias balances the experts' loads without a gradient,
+ * and experts may come from a few groups only. For a token with logits l[0 .. E-1]:
+ *   s = softmax(l) over all E, or sigmoid(l)              the scores
+ *   c = s + bias                                          what the choice goes by
+ *   groups > 1: group g holds experts g E/groups ..; its score is the sum of its group_top (1 or 2)
+ *   largest c, and only the topk_groups groups of largest score are kept
+ *   topk_idx  the K experts of largest c in the kept groups, c descending
+ *   topk_w    scale * s of them, with `renormalize` divided by their sum
+ * Ties, of experts and of groups, go to the lower id.
+ *
+ * The choice is that of exact arithmetic as far as 64 bits hold it: where two scores, or sums of
+ * scores, are closer than 32 bits can tell, the token is done again in 64. Without a bias experts
+ * are compared by their logits.
+ *
+ * A logit of -inf masks an expert out: its score is 0, it adds nothing to its group, and it is
+ * chosen only where the kept groups have too few others (then the lowest ids, with weight 0); a
+ * group of masked experts is kept only where there are too few others. A row of nothing else has
+ * weights and gradients of 0. Logits of NaN or +inf give unspecified ids in range, each once, and
+ * unspecified weights and gradients of that token. Bias values are finite.
+ *
+ * Limits: T >= 0, 1 <= E <= 1024, 1 <= K <= min(32, topk_groups E / groups), 1 <= topk_groups <=
+ * groups <= 32, groups divides E, T K < 2^31; E <= ld <= 2^30, any number. Columns past E of a row are
+ * neither read nor written. */
+typedef enum mok_score { MOK_SCORE_SOFTMAX = 0, MOK_SCORE_SIGMOID = 1 } mok_score;
+
+typedef struct mok_router_config {
+    uint32_t abi_version; /* MOK_ABI_VERSION */
+    int32_t T, E, K;
+    int32_t dtype;       /* mok_dtype of logits and d_logits */
+    int32_t score;       /* mok_score */
+    int32_t groups;      /* 1: every expert may be chosen */
+    int32_t topk_groups; /* groups kept */
+    int32_t group_top;   /* experts whose c make a group's score: 1 or 2 */
+    int32_t renormalize; /* 0 or 1 */
+    float scale;         /* finite, above 0 */
+    int32_t reserved;    /* 0 */
+    int64_t ld;          /* row stride of logits and d_logits */
+} mok_router_config;
+
+mok_status mok_check_router_config(const mok_router_config *cfg);
+
+/* Bytes of workspace of mok_router_forward where counts or score_sum are asked for (256-byte
+ * aligned, contents on entry do not matter); 0 for an invalid configuration. */
+size_t mok_router_workspace_size(const mok_router_config *cfg);
+
+/* logits [T][E]; bias NULL or fp32 [E]; topk_idx [T][K] int32 out, topk_w [T][K] fp32 out.
+ * counts NULL or [E] int32 out: tokens that chose each expert. score_sum NULL or [E] fp32 out: the
+ * sum over all tokens of each expert's score, in a fixed order (times counts it makes a balance
+ * loss). ws may be NULL where both are. */
+mok_status mok_router_forward(const mok_router_config *cfg, const void *logits, const float *bias,
+                              int32_t *topk_idx, float *topk_w, int32_t *counts, float *score_sum,
+                              void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* d_logits = the gradient of sum(d_topk_w topk_w) + sum(d_score_sum score_sum) for the chosen
+ * topk_idx (the bias has none), rounded once; zero for masked experts. d_topk_w fp32 [T][K];
+ * d_score_sum NULL or fp32 [E]. An id out of range raises MOK_ERR_DEVICE_INVARIANT and takes no part.
+ * d_logits may be logits itself. */
+mok_status mok_router_backward(const mok_router_config *cfg, const void *logits,
+                               const int32_t *topk_idx, const float *d_topk_w,
+                               const float *d_score_sum, void *d_logits, cudaStream_t stream);
+
+/* new_bias[e] = bias[e] + rate * sign(T K / E - counts[e]): up for an expert that fewer than an
+ * average number of tokens chose. rate finite; new_bias may be bias. */
+mok_status mok_router_update_bias(const mok_router_config *cfg, const int32_t *counts, float rate,
+                                  const float *bias, float *new_bias, cudaStream_t stream);
+
+/* ---- layer norm and RMS norm ----------------------------------------------------------
+ *
+ *   h = x + residual (rounded to its type)
+ *   MOK_NORM_LAYER: mean = mean(h), rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+ *   MOK_NORM_RMS:   mean = 0,       rstd = 1 / sqrt(mean(h^2) + eps)
+ *   y = (h - mean) rstd weight + bias
+ * over each row, statistics of the rounded h, everything in fp32, each output rounded once.
+ *
+ * Limits: 0 <= rows < 2^31 - 512, 1 <= H <= 2^20 (any number); strides ld_x, ld_y >= H are multiples
+ * of 8 elements, at most 2^30. Columns past H are neither read nor written. */
+typedef enum mok_norm_kind { MOK_NORM_LAYER = 0, MOK_NORM_RMS = 1 } mok_norm_kind;
+
+typedef struct mok_norm_config {
+    uint32_t abi_version; /* MOK_ABI_VERSION */
+    int32_t H;
+    int64_t rows;
+    int64_t ld_x;     /* row stride of x, residual, h, dh, dx */
+    int64_t ld_y;     /* row stride of y, dy */
+    int32_t kind;     /* mok_norm_kind */
+    int32_t x_dtype;  /* mok_dtype of x, residual, h, dh, dx */
+    int32_t y_dtype;  /* mok_dtype of y, dy */
+    float eps;        /* finite, above 0 */
+} mok_norm_config;
+
+mok_status mok_check_norm_config(const mok_norm_config *cfg);
+
+/* Bytes of workspace of mok_norm_backward where dw or db are asked for (256-byte aligned, contents on
+ * entry do not matter); 0 for an invalid configuration. */
+size_t mok_norm_workspace_size(const mok_norm_config *cfg);
+
+/* x [rows][H]; residual NULL or [rows][H]; weight, bias NULL (one, zero) or fp32 [H]; h NULL or
+ * [rows][H] out (with a residual; may be x or residual); y [rows][H] out (may be x where the types
+ * and strides are the same and h is not x); mean, rstd NULL or fp32 [rows] out, for the backward
+ * (mean of MOK_NORM_LAYER only). */
+mok_status mok_norm_forward(const mok_norm_config *cfg, const void *x, const void *residual,
+                            const float *weight, const float *bias, void *h, void *y, float *mean,
+                            float *rstd, cudaStream_t stream);
+
+/* Backward, with n = (h - mean) rstd and g = dy weight:
+ *   dx = dh + rstd (g - n mean(g n) - mean(g))   (the last mean of MOK_NORM_LAYER only)
+ *   dw = sum over the rows of dy n               db = sum of dy
+ * in fp32, the sums over rows in a fixed order. It is the gradient of x and of the residual.
+ *   h     [rows][H]: h, or x where there was no residual; mean (MOK_NORM_LAYER), rstd of the forward
+ *   dh    NULL or [rows][H]: the gradient that reaches h beside the norm (may be dx)
+ *   dx    NULL or [rows][H] out (may be dy where the types and strides are the same); dw, db NULL or
+ *         fp32 [H] out. At least one of the three; ws may be NULL without dw and db. */
+mok_status mok_norm_backward(const mok_norm_config *cfg, const void *h, const float *mean,
+                             const float *rstd, const float *weight, const void *dy, const void *dh,
+                             void *dx, float *dw, float *db, void *ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/* ---- loss over a vocabulary -----------------------------------------------------------
+ *
+ *   l = x W^T       lse = log sum_v exp(l_v)       loss = lse - l_target + z_loss lse^2
+ * for rows of x [rows][H] and the vocabulary's W [V][H], bf16 with fp32 accumulation. The logits are
+ * never in memory: the forward keeps running maxima and sums, the backward makes the gradient of the
+ * logits for a piece of the vocabulary at a time. A target below 0 takes no part (loss and gradients
+ * 0); one at or past V raises MOK_ERR_DEVICE_INVARIANT and counts as below 0.
+ *
+ * Limits: 0 <= rows < 2^31 - 512, 1 <= H <= 2^20, 1 <= V <= 2^24, any numbers, fewer than 2^31 blocks
+ * of 16 rows x 256 columns in rows x V, rows x H and V x H; strides ld_x, ld_w >= H are multiples of 8
+ * elements, at most 2^30. Columns past H are neither read nor written. */
+typedef struct mok_vocab_loss_config {
+    uint32_t abi_version; /* MOK_ABI_VERSION */
+    int32_t H, V;
+    int32_t grad_dtype;   /* mok_dtype of dx and dW */
+    int64_t rows;
+    int64_t ld_x;         /* row stride of x and dx */
+    int64_t ld_w;         /* row stride of W and dW */
+    float z_loss;         /* finite, >= 0 */
+    int32_t piece;        /* vocabulary entries of a piece, a multiple of 256; 0: as many as keep the
+                             gradient of a piece's logits within 1 GiB */
+} mok_vocab_loss_config;
+
+typedef enum mok_vocab_loss_pass {
+    MOK_VOCAB_LOSS_FORWARD = 0,
+    MOK_VOCAB_LOSS_BACKWARD = 1
+} mok_vocab_loss_pass;
+
+mok_status mok_check_vocab_loss_config(const mok_vocab_loss_config *cfg);
+
+/* Bytes of workspace of a pass (256-byte aligned, contents on entry do not matter); 0 for an
+ * invalid configuration. */
+size_t mok_vocab_loss_workspace_size(const mok_vocab_loss_config *cfg, int pass);
+
+/* targets int32 [rows]; loss NULL or fp32 [rows] out, lse fp32 [rows] out (of every row, whatever its
+ * target). */
+mok_status mok_vocab_loss_forward(const mok_vocab_loss_config *cfg, const void *x, const void *w,
+                                  const int32_t *targets, float *loss, float *lse, void *ws,
+                                  size_t ws_bytes, cudaStream_t stream);
+
+/* With d_loss fp32 [rows] and lse from the forward:
+ *   dl_v = d_loss ((1 + 2 z_loss lse) exp(l_v - lse) - [v == target])
+ *   dx = dl W            dW = dl^T x
+ * dl enters the products rounded to bf16 for bf16 gradients (as the linear layer's dz does), as three
+ * bf16 values that add up to it for fp32 ones. dx NULL or [rows][H] out, dw NULL or [V][H] out; one of them at least. */
+mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *cfg, const void *x, const void *w,
+                                   const int32_t *targets, const float *lse, const float *d_loss,
+                                   void *dx, void *dw, void *ws, size_t ws_bytes,
+                                   cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -3,7 +3,7 @@ hand-written CUDA kernels and a thin Python binding.
 
     binding   the C entry points by name (ctypes; marshalling only)
     buffers   torch-allocated schedule arrays and workspaces, a small MoELayer helper, and
-              TokenSort, Linear and AdamW for the operators around the layer
+              TokenSort, Linear, AdamW, Router, Norm and VocabLoss for the operators around the layer
 """
 from . import binding  # noqa: F401
 from .binding import (  # noqa: F401

@@ -61,6 +61,14 @@ MOK_STATE_F32 = 0
 MOK_STATE_MXFP8 = 1
 MOK_ADAMW_STOCHASTIC = 1
 
+# mok_score, mok_norm_kind, mok_vocab_loss_pass
+MOK_SCORE_SOFTMAX = 0
+MOK_SCORE_SIGMOID = 1
+MOK_NORM_LAYER = 0
+MOK_NORM_RMS = 1
+MOK_VOCAB_LOSS_FORWARD = 0
+MOK_VOCAB_LOSS_BACKWARD = 1
+
 # mok_ws_item
 MOK_ITEM_X_RING = 0
 MOK_ITEM_X_RING_SCALE = 1
@@ -90,6 +98,11 @@ EXPORTED = [
     "mok_combine", "mok_combine_backward", "mok_check_adamw_config", "mok_adamw_step",
     "mok_check_linear_config", "mok_linear_workspace_size", "mok_linear_forward",
     "mok_linear_backward", "mok_adamw_advance", "mok_adamw_step_at",
+    "mok_check_router_config", "mok_router_workspace_size", "mok_router_forward",
+    "mok_router_backward", "mok_router_update_bias", "mok_check_norm_config",
+    "mok_norm_workspace_size", "mok_norm_forward", "mok_norm_backward",
+    "mok_check_vocab_loss_config", "mok_vocab_loss_workspace_size", "mok_vocab_loss_forward",
+    "mok_vocab_loss_backward",
 ]
 
 # bytes of the fixed scratch array behind mok_build_schedule_noalloc
@@ -124,6 +137,26 @@ class MokLinearConfig(ctypes.Structure):
                 ("ld_out", ctypes.c_int64), ("act", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class MokRouterConfig(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("T", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("dtype", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("ld", ctypes.c_int64)]
+
+
+class MokNormConfig(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("H", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("kind", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class MokVocabLossConfig(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("H", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("rows", ctypes.c_int64), ("ld_x", ctypes.c_int64),
+                ("ld_w", ctypes.c_int64), ("z_loss", ctypes.c_float), ("piece", ctypes.c_int32)]
 
 
 class MokAdamwConfig(ctypes.Structure):
@@ -178,6 +211,9 @@ def lib():
         rowsp = ctypes.POINTER(MokRowsConfig)
         linp = ctypes.POINTER(MokLinearConfig)
         adamp = ctypes.POINTER(MokAdamwConfig)
+        routp = ctypes.POINTER(MokRouterConfig)
+        normp = ctypes.POINTER(MokNormConfig)
+        vocp = ctypes.POINTER(MokVocabLossConfig)
         sig = {
             "mok_abi_version": ([], ctypes.c_uint32),
             "mok_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -224,6 +260,19 @@ def lib():
             "mok_check_adamw_config": ([adamp], ctypes.c_int),
             "mok_adamw_step": ([adamp, ctypes.POINTER(MokAdamwTensor), i32, p, p],
                                ctypes.c_int),
+            "mok_check_router_config": ([routp], ctypes.c_int),
+            "mok_router_workspace_size": ([routp], sz),
+            "mok_router_forward": ([routp, p, p, p, p, p, p, p, sz, p], ctypes.c_int),
+            "mok_router_backward": ([routp, p, p, p, p, p, p], ctypes.c_int),
+            "mok_router_update_bias": ([routp, p, ctypes.c_float, p, p, p], ctypes.c_int),
+            "mok_check_norm_config": ([normp], ctypes.c_int),
+            "mok_norm_workspace_size": ([normp], sz),
+            "mok_norm_forward": ([normp, p, p, p, p, p, p, p, p, p], ctypes.c_int),
+            "mok_norm_backward": ([normp, p, p, p, p, p, p, p, p, p, p, sz, p], ctypes.c_int),
+            "mok_check_vocab_loss_config": ([vocp], ctypes.c_int),
+            "mok_vocab_loss_workspace_size": ([vocp, ctypes.c_int], sz),
+            "mok_vocab_loss_forward": ([vocp, p, p, p, p, p, p, sz, p], ctypes.c_int),
+            "mok_vocab_loss_backward": ([vocp, p, p, p, p, p, p, p, p, sz, p], ctypes.c_int),
             "mok_adamw_advance": ([adamp, p, p], ctypes.c_int),
             "mok_adamw_step_at": ([adamp, ctypes.POINTER(MokAdamwTensor), i32, p, p, p],
                                   ctypes.c_int),
@@ -300,6 +349,31 @@ def make_linear(rows, in_features, out_features, groups=1, act=MOK_ACT_NONE,
                            up8(in_features) if ld_w is None else ld_w,
                            up8(out_features) if ld_out is None else ld_out, act, out_dtype,
                            grad_dtype, 0)
+
+
+def make_router(T, E, K, score=MOK_SCORE_SOFTMAX, groups=1, topk_groups=1, group_top=1,
+                renormalize=True, scale=1.0, dtype=MOK_DTYPE_F32, ld=None,
+                abi_version=MOK_ABI_VERSION) -> MokRouterConfig:
+    """Configuration of a router; rows packed unless given."""
+    return MokRouterConfig(abi_version, T, E, K, dtype, score, groups, topk_groups, group_top,
+                           int(renormalize), scale, 0, E if ld is None else ld)
+
+
+def make_norm(rows, H, kind=MOK_NORM_LAYER, eps=1e-5, x_dtype=MOK_DTYPE_BF16,
+              y_dtype=MOK_DTYPE_BF16, ld_x=None, ld_y=None,
+              abi_version=MOK_ABI_VERSION) -> MokNormConfig:
+    """Configuration of a norm; rows at the next multiple of 8 elements unless given."""
+    up8 = (H + 7) // 8 * 8
+    return MokNormConfig(abi_version, H, rows, up8 if ld_x is None else ld_x,
+                         up8 if ld_y is None else ld_y, kind, x_dtype, y_dtype, eps)
+
+
+def make_vocab_loss(rows, H, V, z_loss=0.0, grad_dtype=MOK_DTYPE_BF16, piece=0, ld_x=None,
+                    ld_w=None, abi_version=MOK_ABI_VERSION) -> MokVocabLossConfig:
+    """Configuration of a vocabulary loss; rows at the next multiple of 8 elements unless given."""
+    up8 = (H + 7) // 8 * 8
+    return MokVocabLossConfig(abi_version, H, V, grad_dtype, rows, up8 if ld_x is None else ld_x,
+                              up8 if ld_w is None else ld_w, z_loss, piece)
 
 
 def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0, p_dtype=MOK_DTYPE_F32,
@@ -456,7 +530,7 @@ def mok_profile_enable(on) -> int:
     return lib().mok_profile_enable(1 if on else 0)
 
 
-def mok_profile_read(max_kinds=32):
+def mok_profile_read(max_kinds=64):
     """{kernel kind: (launches, total ms)} recorded since mok_profile_enable(1)."""
     n = ctypes.c_int32(0)
     names = (ctypes.c_char_p * max_kinds)()
@@ -544,3 +618,73 @@ def mok_adamw_step_at(cfg, tensors, clock, grad_scale=None, stream=None) -> int:
     """One step over an AdamwList, its number, lr and seed from the clock."""
     return lib().mok_adamw_step_at(ctypes.byref(cfg), tensors.array, tensors.n, _ptr(clock),
                                    _ptr(grad_scale), _stream(stream))
+
+
+def mok_check_router_config(cfg) -> int:
+    return lib().mok_check_router_config(ctypes.byref(cfg))
+
+
+def mok_router_workspace_size(cfg) -> int:
+    return int(lib().mok_router_workspace_size(ctypes.byref(cfg)))
+
+
+def mok_router_forward(cfg, logits, bias, topk_idx, topk_w, counts=None, score_sum=None, ws=None,
+                       ws_bytes=0, stream=None) -> int:
+    return lib().mok_router_forward(ctypes.byref(cfg), _ptr(logits), _ptr(bias), _ptr(topk_idx),
+                                    _ptr(topk_w), _ptr(counts), _ptr(score_sum), _ptr(ws),
+                                    int(ws_bytes), _stream(stream))
+
+
+def mok_router_backward(cfg, logits, topk_idx, d_topk_w, d_score_sum, d_logits,
+                        stream=None) -> int:
+    return lib().mok_router_backward(ctypes.byref(cfg), _ptr(logits), _ptr(topk_idx),
+                                     _ptr(d_topk_w), _ptr(d_score_sum), _ptr(d_logits),
+                                     _stream(stream))
+
+
+def mok_router_update_bias(cfg, counts, rate, bias, new_bias, stream=None) -> int:
+    return lib().mok_router_update_bias(ctypes.byref(cfg), _ptr(counts), float(rate), _ptr(bias),
+                                        _ptr(new_bias), _stream(stream))
+
+
+def mok_check_norm_config(cfg) -> int:
+    return lib().mok_check_norm_config(ctypes.byref(cfg))
+
+
+def mok_norm_workspace_size(cfg) -> int:
+    return int(lib().mok_norm_workspace_size(ctypes.byref(cfg)))
+
+
+def mok_norm_forward(cfg, x, residual, weight, bias, h, y, mean=None, rstd=None,
+                     stream=None) -> int:
+    return lib().mok_norm_forward(ctypes.byref(cfg), _ptr(x), _ptr(residual), _ptr(weight),
+                                  _ptr(bias), _ptr(h), _ptr(y), _ptr(mean), _ptr(rstd),
+                                  _stream(stream))
+
+
+def mok_norm_backward(cfg, h, mean, rstd, weight, dy, dh, dx, dw=None, db=None, ws=None,
+                      ws_bytes=0, stream=None) -> int:
+    return lib().mok_norm_backward(ctypes.byref(cfg), _ptr(h), _ptr(mean), _ptr(rstd),
+                                   _ptr(weight), _ptr(dy), _ptr(dh), _ptr(dx), _ptr(dw), _ptr(db),
+                                   _ptr(ws), int(ws_bytes), _stream(stream))
+
+
+def mok_check_vocab_loss_config(cfg) -> int:
+    return lib().mok_check_vocab_loss_config(ctypes.byref(cfg))
+
+
+def mok_vocab_loss_workspace_size(cfg, which) -> int:
+    return int(lib().mok_vocab_loss_workspace_size(ctypes.byref(cfg), int(which)))
+
+
+def mok_vocab_loss_forward(cfg, x, w, targets, loss, lse, ws, ws_bytes, stream=None) -> int:
+    return lib().mok_vocab_loss_forward(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(targets),
+                                        _ptr(loss), _ptr(lse), _ptr(ws), int(ws_bytes),
+                                        _stream(stream))
+
+
+def mok_vocab_loss_backward(cfg, x, w, targets, lse, d_loss, dx, dw, ws, ws_bytes,
+                            stream=None) -> int:
+    return lib().mok_vocab_loss_backward(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(targets),
+                                         _ptr(lse), _ptr(d_loss), _ptr(dx), _ptr(dw), _ptr(ws),
+                                         int(ws_bytes), _stream(stream))

@@ -1,6 +1,7 @@
 """Device-memory plumbing for the C ABI: torch allocates, the library computes.
 
-`TokenSort`, `Linear` and `AdamW` do the same for the operators around the layer.
+`TokenSort`, `Linear`, `AdamW`, `Router`, `Norm` and `VocabLoss` do the same for the operators
+around the layer.
 
 `MoELayer` owns the caller-side buffers of one configuration (schedule arrays and the
 three workspaces) and strings the entry points together in the order a user calls them:
@@ -463,3 +464,178 @@ class AdamW:
             if k == 0:
                 B.check(B.mok_adamw_advance(cfg, self.clock, stream), "adamw clock")
             B.check(B.mok_adamw_step_at(cfg, tensors, self.clock, grad_scale, stream), "adamw")
+
+
+class _Workspace:
+    """A pass's workspace, from the memory of the stream that first runs the pass, whose earlier work
+    is then done with it; other streams are recorded, so it is not given away under their work."""
+
+    def __init__(self, device):
+        self.device = device
+        self.made = None
+
+    def get(self, size, stream):
+        """(workspace, its size, the stream's handle)."""
+        handle = B._stream(stream) if self.device.type == "cuda" else 0
+        if self.made is None:
+            with torch.cuda.stream(None if stream is None else _torch_stream(stream)):
+                self.made = (_empty(size, torch.uint8, self.device), size, handle)
+        ws, n, first = self.made
+        if handle != first:
+            ws.record_stream(_torch_stream(stream))
+        return ws, n, handle
+
+
+class Router:
+    """Choice of experts by scores of their logits, with a balance bias and groups, and its
+    gradient. Logits [T][E] and their gradient are fp32 or bf16 (`dtype`) in rows that start on
+    16-byte boundaries, ids int32 and weights fp32 [T][K], per-expert vectors fp32 (counts int32). What it
+    gives feeds `TokenSort` and `MoELayer` as their own router's does. Calls of one Router share its
+    workspace, so calls on several streams have to be ordered by the caller. Arrays that do not fit
+    raise ValueError before anything is launched."""
+
+    def __init__(self, T, E, K, score=B.MOK_SCORE_SOFTMAX, groups=1, topk_groups=1, group_top=1,
+                 renormalize=True, scale=1.0, dtype=torch.float32, device="cuda"):
+        kind, per = _mok_dtype(dtype), 4 if dtype == torch.float32 else 8
+        self.T, self.E, self.K, self.dtype = T, E, K, dtype
+        self.ld = (E + per - 1) // per * per
+        self.cfg = B.make_router(T, E, K, score, groups, topk_groups, group_top, renormalize, scale,
+                                 kind, self.ld)
+        B.check(B.mok_check_router_config(self.cfg), "router config")
+        self.here = _here(torch.device(device))
+        self.ws = _Workspace(self.here)
+
+    def _check(self, logits, idx, w_name, w):
+        n = self.T * self.K
+        _check_vector("idx", idx, torch.int32, self.here, n if n else idx.numel())
+        _check_vector(w_name, w, torch.float32, self.here, n if n else w.numel())
+        _check_matrix("logits", logits, self.dtype, self.here, self.T, self.E, self.ld)
+
+    def forward(self, logits, idx, topk_w, bias=None, counts=None, score_sum=None, stream=None):
+        self._check(logits, idx, "topk_w", topk_w)
+        _check_vector("bias", bias, torch.float32, self.here, self.E)
+        _check_vector("counts", counts, torch.int32, self.here, self.E)
+        _check_vector("score_sum", score_sum, torch.float32, self.here, self.E)
+        ws, n, handle = None, 0, stream
+        if counts is not None or score_sum is not None:
+            ws, n, handle = self.ws.get(B.mok_router_workspace_size(self.cfg), stream)
+        B.check(B.mok_router_forward(self.cfg, logits, bias, idx, topk_w, counts, score_sum, ws, n,
+                                     handle), "router")
+        return idx, topk_w
+
+    def backward(self, logits, idx, d_topk_w, d_logits, d_score_sum=None, stream=None):
+        self._check(logits, idx, "d_topk_w", d_topk_w)
+        _check_matrix("d_logits", d_logits, self.dtype, self.here, self.T, self.E, self.ld)
+        _check_vector("d_score_sum", d_score_sum, torch.float32, self.here, self.E)
+        B.check(B.mok_router_backward(self.cfg, logits, idx, d_topk_w, d_score_sum, d_logits,
+                                      stream), "router backward")
+        return d_logits
+
+    def update_bias(self, counts, rate, bias, new_bias=None, stream=None):
+        """bias (or new_bias) one step towards equal loads."""
+        new_bias = bias if new_bias is None else new_bias
+        _check_vector("counts", counts, torch.int32, self.here, self.E)
+        _check_vector("bias", bias, torch.float32, self.here, self.E)
+        _check_vector("new_bias", new_bias, torch.float32, self.here, self.E)
+        B.check(B.mok_router_update_bias(self.cfg, counts, rate, bias, new_bias, stream),
+                "router bias")
+        return new_bias
+
+
+class Norm:
+    """Layer norm or RMS norm of rows of H, of a residual sum where there is one, and its gradients.
+    x, residual, h, dh and dx have x_dtype, y and dy y_dtype (fp32 or bf16), in rows that start on
+    16-byte boundaries; weight, bias, dw, db and the statistics are fp32. Calls of one Norm share its
+    workspace, so backward calls on several streams have to be ordered by the caller. Arrays that do
+    not fit raise ValueError before anything is launched."""
+
+    def __init__(self, rows, H, kind=B.MOK_NORM_LAYER, eps=1e-5, x_dtype=torch.bfloat16,
+                 y_dtype=torch.bfloat16, device="cuda"):
+        self.cfg = B.make_norm(rows, H, kind, eps, _mok_dtype(x_dtype), _mok_dtype(y_dtype))
+        B.check(B.mok_check_norm_config(self.cfg), "norm config")
+        self.rows, self.H, self.x_dtype, self.y_dtype = rows, H, x_dtype, y_dtype
+        self.layer = kind == B.MOK_NORM_LAYER
+        self.here = _here(torch.device(device))
+        self.ws = _Workspace(self.here)
+
+    def _check(self, x=(), y=(), stats=(), weights=()):
+        """(name, array) pairs of each kind."""
+        c = self.cfg
+        for name, t in x:
+            _check_matrix(name, t, self.x_dtype, self.here, self.rows, self.H, c.ld_x)
+        for name, t in y:
+            _check_matrix(name, t, self.y_dtype, self.here, self.rows, self.H, c.ld_y)
+        for name, t in stats:
+            _check_vector(name, t, torch.float32, self.here, self.rows if self.rows or t is None
+                          else t.numel())
+        for name, t in weights:
+            _check_vector(name, t, torch.float32, self.here, self.H)
+
+    def forward(self, x, weight, y, bias=None, residual=None, h=None, mean=None, rstd=None,
+                stream=None):
+        self._check(x=(("x", x), ("residual", residual), ("h", h)), y=(("y", y),),
+                    stats=(("mean", mean), ("rstd", rstd)),
+                    weights=(("weight", weight), ("bias", bias)))
+        B.check(B.mok_norm_forward(self.cfg, x, residual, weight, bias, h, y, mean, rstd, stream),
+                "norm")
+        return y
+
+    def backward(self, h, weight, dy, rstd, mean=None, dh=None, dx=None, dw=None, db=None,
+                 stream=None):
+        self._check(x=(("h", h), ("dh", dh), ("dx", dx)), y=(("dy", dy),),
+                    stats=(("mean", mean), ("rstd", rstd)),
+                    weights=(("weight", weight), ("dw", dw), ("db", db)))
+        ws, n, handle = None, 0, stream
+        if dw is not None or db is not None:
+            ws, n, handle = self.ws.get(B.mok_norm_workspace_size(self.cfg), stream)
+        B.check(B.mok_norm_backward(self.cfg, h, mean, rstd, weight, dy, dh, dx, dw, db, ws, n,
+                                    handle), "norm backward")
+        return dx
+
+
+class VocabLoss:
+    """Softmax cross entropy of rows of x over a vocabulary's W [V][H], and its gradients, the logits
+    never in memory. x, W are bf16, dx and dw grad_dtype, in rows that start on 16-byte boundaries
+    (`weights()` makes an array for any H); targets int32, loss, lse and d_loss fp32, one a row. Calls of
+    one VocabLoss share its workspaces, so calls on several streams have to be ordered by the
+    caller. Arrays that do not fit raise ValueError before anything is launched."""
+
+    def __init__(self, rows, H, V, z_loss=0.0, grad_dtype=torch.bfloat16, piece=0, device="cuda"):
+        self.cfg = B.make_vocab_loss(rows, H, V, z_loss, _mok_dtype(grad_dtype), piece)
+        B.check(B.mok_check_vocab_loss_config(self.cfg), "vocabulary loss config")
+        self.rows, self.grad_dtype = rows, grad_dtype
+        self.here = _here(torch.device(device))
+        self.of_x = (rows, H, int(self.cfg.ld_x))
+        self.of_w = (V, H, int(self.cfg.ld_w))
+        self.ws = [_Workspace(self.here), _Workspace(self.here)]
+
+    def weights(self, dtype=torch.bfloat16):
+        """Zeros [V][H] whose rows lie as the loss reads them."""
+        V, H, ld = self.of_w
+        return torch.zeros(V, ld, dtype=dtype, device=self.here)[:, :H]
+
+    def _check(self, x, w, targets, values):
+        _check_matrix("x", x, torch.bfloat16, self.here, *self.of_x)
+        _check_matrix("w", w, torch.bfloat16, self.here, *self.of_w)
+        for name, t, dtype in (("targets", targets, torch.int32),) + values:
+            _check_vector(name, t, dtype, self.here, self.rows if self.rows or t is None
+                          else t.numel())
+
+    def _ws(self, which, stream):
+        return self.ws[which].get(B.mok_vocab_loss_workspace_size(self.cfg, which), stream)
+
+    def forward(self, x, w, targets, loss, lse, stream=None):
+        self._check(x, w, targets, (("loss", loss, torch.float32), ("lse", lse, torch.float32)))
+        ws, n, handle = self._ws(B.MOK_VOCAB_LOSS_FORWARD, stream)
+        B.check(B.mok_vocab_loss_forward(self.cfg, x, w, targets, loss, lse, ws, n, handle),
+                "vocabulary loss")
+        return loss
+
+    def backward(self, x, w, targets, lse, d_loss, dx=None, dw=None, stream=None):
+        self._check(x, w, targets, (("lse", lse, torch.float32), ("d_loss", d_loss, torch.float32)))
+        _check_matrix("dx", dx, self.grad_dtype, self.here, *self.of_x)
+        _check_matrix("dw", dw, self.grad_dtype, self.here, *self.of_w)
+        ws, n, handle = self._ws(B.MOK_VOCAB_LOSS_BACKWARD, stream)
+        B.check(B.mok_vocab_loss_backward(self.cfg, x, w, targets, lse, d_loss, dx, dw, ws, n,
+                                          handle), "vocabulary loss backward")
+        return dx

@@ -463,7 +463,7 @@ struct Dx {
         const int64_t r0 = u.r0;
         const int n_mma = (nr + 15) & ~15;
         const int i0 = u.mb * 256 + (int)rank * 128 + q * 32;
-        const bool part = CUT && kp.parts > 1;
+        const bool part = CUT && kp.out != nullptr;
         if constexpr (F32) {
             float *o = part ? kp.out + u.part * kp.stride + r0 * kp.ld
                             : static_cast<float *>(dx) + r0 * ld;
@@ -472,9 +472,10 @@ struct Dx {
             sum_segments(c, hw, n_mma, seg == 0, last, carry, [&](int n0, const float (&v)[16]) {
                 if (i0 + lane >= Kin) return;
                 float *p = o + n0 * ldo + i0 + lane;
+                const bool add = CUT && kp.add;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (n0 + j < n_out) p[j * ldo] = n0 + j < nr ? v[j] : 0.f;
+                    if (n0 + j < n_out) p[j * ldo] = n0 + j < nr ? (add ? p[j * ldo] : 0.f) + v[j] : 0.f;
             });
         } else if (part) {
             emit_part<E::STEP>(kp, u.part, c, hw, r0, nr, i0 + lane, Kin);
@@ -616,7 +617,7 @@ struct Dw {
         const int nn = N - nb * 256 < 256 ? N - nb * 256 : 256;
         const bool any = u.nr > 0;
         const int i0 = mb * 256 + (int)rank * 128 + q * 32;
-        const bool part = CUT && kp.parts > 1;
+        const bool part = CUT && kp.out != nullptr;
         if constexpr (F32) {
             float *o = part ? kp.out + u.part * kp.stride + nb * 256 * kp.ld
                             : static_cast<float *>(dw) + ((int64_t)g * N + nb * 256) * ld;
@@ -1211,7 +1212,8 @@ size_t part_bytes(const Cut &c, int64_t rows, int64_t cols) {
     return c.parts > 1 ? (size_t)c.parts * rows * round_up(cols, 4) * 4 : 0;
 }
 KParts k_parts(const Cut &c, float *out, int64_t rows, int64_t cols) {
-    return KParts{c.parts, c.per, out, round_up(cols, 4), rows * round_up(cols, 4)};
+    return KParts{c.parts, c.per, c.parts > 1 ? out : nullptr, round_up(cols, 4),
+                  rows * round_up(cols, 4), false};
 }
 JoinOut join_out(const KParts &k, int64_t rows, int cols, void *out, int64_t ld) {
     const int64_t n = rows * ((cols + 3) / 4);
@@ -1304,7 +1306,53 @@ mok_status check_linear(const mok_linear_config *c, const int32_t *starts, const
     return MOK_OK;
 }
 
+template <bool F, bool CUT>
+cudaError_t dense_grads(const DenseGrads &a, const KParts &kp, const CUtensorMap &xa,
+                        const CUtensorMap &xb, const CUtensorMap &wa, const CUtensorMap &wb,
+                        int *status, cudaStream_t s) {
+    const int n_kb = (a.Kin + 255) / 256, n_nb = (a.N + 255) / 256;
+    int64_t clocks, split = 0, pairs = 0;
+    const Tiles tiles = dense_tiles(a.rows, dense_height(a.rows, n_kb, sm_pairs(), &clocks));
+    const Dx<F, CUT> px{tiles, n_kb, a.halves, a.Kin, a.N, a.ld_x, a.dx, status, kp};
+    const Dw<F, CUT> pw{nullptr, nullptr, a.rows, 1, n_kb, n_nb, a.halves, a.Kin, a.N, a.ld_w, a.dw,
+                        status, DbArgs{nullptr, nullptr, 0, nullptr},
+                        KParts{1, 0, nullptr, 0, 0, false}};
+    const int64_t x_units = a.dx ? tiles.cap * n_kb : 0, w_units = a.dw ? (int64_t)n_kb * n_nb : 0;
+    if (a.dx && a.dw)
+        plan_both(w_units, unit_clocks((a.rows + 63) / 64 * a.halves, LTILE), x_units,
+                  unit_clocks((a.N + 63) / 64 * a.halves, tiles.height), &split, &pairs);
+    if (split > 0) return launch_both(wa, wb, pw, xa, xb, px, split, pairs, s);
+    cudaError_t e = cudaSuccess;
+    if (a.dx) e = launch_linear(xa, xb, px, x_units, s);
+    if (e == cudaSuccess && a.dw) e = launch_linear(wa, wb, pw, w_units, s);
+    return e;
+}
+
 }  // namespace
+
+cudaError_t launch_dense_grads(const DenseGrads &a, int *status, cudaStream_t s) {
+    cudaError_t e = init_host();
+    if (e != cudaSuccess) return e;
+    CUtensorMap xa = {}, xb = {}, wa = {}, wb = {};
+    const auto map_dz = [&](CUtensorMap *m, int box_rows) {
+        return a.f32 ? map_w(m, a.dz, a.halves, a.rows, a.N, a.ld_dz, box_rows)
+                     : map2d(m, a.dz, a.rows, a.N, a.ld_dz, box_rows);
+    };
+    if (a.dx && ((e = map_w(&xa, a.w, 1, a.N, a.Kin, a.ld_w, 64)) != cudaSuccess ||
+                 (e = map_dz(&xb, 32)) != cudaSuccess))
+        return e;
+    if (a.dw && ((e = map2d(&wa, a.x, a.rows, a.Kin, a.ld_x, 64)) != cudaSuccess ||
+                 (e = map_dz(&wb, 64)) != cudaSuccess))
+        return e;
+    const KParts kp{1, 0, a.dx_sum, round_up(a.Kin, 4), 0, a.add};
+    const bool cut = a.dx_sum != nullptr || a.add;
+    if (a.f32)
+        return cut ? dense_grads<true, true>(a, kp, xa, xb, wa, wb, status, s)
+                   : dense_grads<true, false>(a, kp, xa, xb, wa, wb, status, s);
+    return cut ? dense_grads<false, true>(a, kp, xa, xb, wa, wb, status, s)
+               : dense_grads<false, false>(a, kp, xa, xb, wa, wb, status, s);
+}
+
 }  // namespace mok
 
 using namespace mok;

@@ -130,8 +130,9 @@ struct LinGeom {
 struct KParts {
     int parts;   // 1: K is whole and `out` not used
     int per;     // 64-element K blocks a part
-    float *out;  // [parts][rows][ld]
+    float *out;  // [parts][rows][ld]; nullptr: sums go to the output itself
     int64_t ld, stride;
+    bool add;    // to what `out` (or an fp32 output) holds: a product in pieces of K, a launch each
 
     // number u of `units` times parts: the part, u becomes the unit's number
     MOK_DEV int take(uint32_t &u, uint32_t units) const {
@@ -252,6 +253,11 @@ MOK_DEV void emit_part(const KParts &kp, int part, uint32_t c, int hw, int64_t r
             tc::tmem_ld_wait();
             loaded(v);
             if (col >= cols) continue;
+            if (kp.add) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (n0 + h + j < n) v[j] += o[(n0 + h + j) * kp.ld];
+            }
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 if (n0 + h + j < n) o[(n0 + h + j) * kp.ld] = v[j];

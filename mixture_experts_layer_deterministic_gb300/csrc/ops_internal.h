@@ -12,13 +12,30 @@ namespace mok {
 // profiling kinds, numbered after the layer's KernelKind
 enum OpKind {
     OP_ROW_MAP = KK_COUNT, OP_DISPATCH, OP_COMBINE, OP_COMBINE_BWD, OP_ADAMW, OP_LINEAR_TILES,
-    OP_LINEAR_FWD, OP_LINEAR_DZ, OP_LINEAR_DX, OP_LINEAR_DW, OP_COUNT
+    OP_LINEAR_FWD, OP_LINEAR_DZ, OP_LINEAR_DX, OP_LINEAR_DW, OP_ROUTER, OP_ROUTER_BWD, OP_NORM,
+    OP_NORM_BWD, OP_VOCAB_FWD, OP_VOCAB_DL, OP_VOCAB_GRADS, OP_COUNT
 };
 
 inline bool op_aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // rounding up to a multiple
 inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+
+// The products of a dense layer's backward, dx = dz W and dW = dz^T x, with dz made elsewhere: bf16
+// [rows][N] rows ld_dz apart, or for fp32 gradients `halves` such planes that add up to it.
+struct DenseGrads {
+    const uint16_t *x, *w, *dz;  // [rows][Kin], [N][Kin], [halves][rows][N]
+    int64_t rows;
+    int N, Kin, halves;
+    int64_t ld_x, ld_w, ld_dz;   // of x and dx, of w and dw, of dz
+    void *dx, *dw;               // one of them may be nullptr
+    bool f32;                    // their type
+    // where N is a piece of the layer's: dx goes to dx_sum in fp32 (rows round_up(Kin, 4) apart;
+    // nullptr where dx is fp32 itself), and adds to it from the second piece on
+    float *dx_sum;
+    bool add;
+};
+cudaError_t launch_dense_grads(const DenseGrads &a, int *status, cudaStream_t s);
 
 #ifdef __CUDACC__
 // The operators' launches overlap at their edges: a kernel may be started while the one before it

@@ -13,7 +13,9 @@ const char *const kNames[OP_COUNT] = {
     "router_grad", "gemm_dgrad_push", "dx_reduce", "wgrad_w13", "wgrad_w2", "scale_atoms",
     "shared_up_swiglu", "shared_down_add", "shared_backward", "ring_forward",
     "row_map", "dispatch_rows", "combine_rows", "combine_rows_bwd", "adamw",
-    "linear_tiles", "linear_forward", "linear_dz", "linear_dx", "linear_dw"};
+    "linear_tiles", "linear_forward", "linear_dz", "linear_dx", "linear_dw",
+    "router", "router_backward", "norm", "norm_backward", "vocab_loss_forward", "vocab_loss_dl",
+    "vocab_loss_grads"};
 
 struct Rec {
     int kind;

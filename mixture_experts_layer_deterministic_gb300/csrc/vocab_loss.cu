@@ -1,0 +1,471 @@
+// vocab_loss.cu -- softmax cross entropy over the projection of rows on a vocabulary, and its
+// gradients, without the logits in memory.
+//
+//   forward   l = x W^T, lse = log sum_v exp(l_v), loss = lse - l_target + z lse^2
+//   backward  dl_v = d ((1 + 2 z lse) exp(l_v - lse) - [v == target]), dx = dl W, dW = dl^T x
+//
+// The products run on the linear layer's engine (linear_core.cuh): pairs of SMs, operands by TMA,
+// accumulators in TMEM.
+//   VocabFwd  A = x, B = W, so a TMEM lane is a row and a thread takes the maximum and the sum of
+//             exponentials of its row's columns without talking to others; each tile of 256 vocabulary
+//             entries leaves a (maximum, sum) per row and warp, and a second kernel joins them in
+//             order.
+//   VocabDl   A = W, B = x, as the linear layer's forward, with dl for an epilogue: bf16 rows of a
+//             piece of the vocabulary in the workspace.
+//   dx, dW    the linear layer's gradient products, with dl for dz.
+#include "linear_core.cuh"
+
+namespace mok {
+namespace {
+
+constexpr float LOG2E_F = 1.4426950408889634f, LN2_F = 0.6931471805599453f;
+constexpr float LOWEST = -3.0e38f;  // below any logit; differences with it stay finite or -inf
+
+MOK_DEV float exp2_hw(float x) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+    return e;
+}
+
+// Running maximum and sum of exponentials, in powers of two.
+struct MaxSum {
+    float m, s;
+    MOK_DEV void join(const MaxSum &o) {
+        const float t = fmaxf(m, o.m);
+        s = s * exp2_hw((m - t) * LOG2E_F) + o.s * exp2_hw((o.m - t) * LOG2E_F);
+        m = t;
+    }
+};
+
+// ---------------------------------------------------------------- forward
+struct VocabFwd {
+    using E = Epi<true>;
+    static constexpr bool F32_OUT = true, SUMS = true, A_MN = false, B_MN = false;
+    static constexpr int BAND = 16;  // row blocks that take a tile of W one after another: 4096
+                                     // rows of x stay in L2 while W passes by
+    int64_t rows;
+    int n_rb, n_vt;   // row blocks and vocabulary tiles of 256
+    int segs;         // of H
+    int H, V;
+    const int32_t *targets;
+    float2 *part;     // [4 n_vt][rows]: (maximum, sum) of a warp's columns of a tile
+    float *hit;       // [rows]: the target's logit
+    int *status;
+
+    MOK_DEV int64_t n_units() const { return (int64_t)n_rb * n_vt; }
+    MOK_DEV void side_work(uint32_t, uint32_t, int) const {}
+    MOK_DEV Unit unit(uint32_t u) const {
+        const uint32_t per = (uint32_t)BAND * (uint32_t)n_vt, band = u / per, rest = u - band * per;
+        const uint32_t left = (uint32_t)n_rb - band * BAND, nb = left < BAND ? left : BAND;
+        return Unit{0, 0, 0, 0, (int)(band * BAND + rest % nb), (int)(rest / nb), 0};
+    }
+    MOK_DEV int segments(const Unit &) const { return segs; }
+    MOK_DEV int long_steps(const Unit &) const { return 0; }
+    MOK_DEV int cols(const Unit &u) const {
+        const int left = V - u.nb * 256;
+        return left < 256 ? left : 256;
+    }
+    MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
+        LinGeom q;
+        q.n_mma = (cols(u) + 15) & ~15;
+        q.a0 = seg * SEG_K;
+        q.a1 = u.mb * 256 + (int)rank * 128;
+        q.a2 = 0;
+        q.b0 = q.a0;
+        q.b1 = u.nb * 256 + (int)rank * (q.n_mma / 2);
+        q.nbox = (q.n_mma / 2 + 31) / 32;
+        const int k = H - q.a0 > SEG_K ? SEG_K : H - q.a0;
+        q.k_steps = (k + 15) / 16;
+        q.k_first = q.half = 0;
+        return q;
+    }
+    MOK_DEV uint32_t tx(const LinGeom &q) const { return 2 * BOX + q.nbox * (BOX / 2); }
+    MOK_DEV void load(uint8_t *st, uint32_t fb, const LinGeom &q, int k0, const CUtensorMap *tmA,
+                      const CUtensorMap *tmB) const {
+        tma_load_3d_pair(st, tmA, fb, q.a0 + k0, q.a1, q.a2);
+        for (int j = 0; j < q.nbox; ++j)
+            tc::tma_load_2d_pair(st + 2 * BOX + j * (BOX / 2), tmB, fb, q.b0 + k0, q.b1 + 32 * j);
+    }
+    MOK_DEV void epilogue(const Unit &u, int seg, bool last, uint32_t rank, uint32_t c, int q, int hw,
+                          int lane, Patches &, Carry<true> &carry) const {
+        const int64_t row = (int64_t)u.mb * 256 + rank * 128 + q * 32 + lane;
+        const int n = cols(u);
+        MaxSum a{LOWEST, 0.0f};
+        int target = -1;
+        if (last && row < rows) target = targets[row];
+        target -= u.nb * 256;
+        sum_segments(c, hw, n, seg == 0, last, carry, [&](int n0, const float (&v)[16]) {
+            float t = a.m;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (n0 + j < n) t = fmaxf(t, v[j]);
+            a.s *= exp2_hw((a.m - t) * LOG2E_F);
+            a.m = t;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (n0 + j < n) a.s += exp2_hw((v[j] - t) * LOG2E_F);
+            if (target >= n0 && target < n0 + 16) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (target == n0 + j && n0 + j < n) hit[row] = v[j];
+            }
+        });
+        if (last && row < rows) part[((int64_t)u.nb * 4 + hw) * rows + row] = make_float2(a.m, a.s);
+    }
+};
+
+// A block joins the parts of 32 rows, each warp a slice of them, then the slices in order.
+constexpr int FINISH_SLICES = 32;
+__global__ void __launch_bounds__(32 * FINISH_SLICES)
+    vocab_finish_kernel(const float2 *part, const float *hit, int64_t rows, int parts, int V,
+                        const int32_t *targets, float z, float *loss, float *lse, int *status) {
+    __shared__ float2 sh[FINISH_SLICES][32];
+    let_next_start();
+    wait_for_previous();
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    MaxSum a{LOWEST, 0.0f};
+    if (row < rows)
+#pragma unroll 4
+        for (int p = slice; p < parts; p += FINISH_SLICES) {
+            const float2 v = part[(int64_t)p * rows + row];
+            a.join(MaxSum{v.x, v.y});
+        }
+    sh[slice][lane] = make_float2(a.m, a.s);
+    __syncthreads();
+    if (slice != 0 || row >= rows) return;
+#pragma unroll
+    for (int k = 1; k < FINISH_SLICES; ++k) a.join(MaxSum{sh[k][lane].x, sh[k][lane].y});
+    const float l = a.m + log2f(a.s) * LN2_F;
+    lse[row] = l;
+    if (loss == nullptr) return;
+    const int t = targets[row];
+    if (t >= V) raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+    loss[row] = t >= 0 && t < V ? (l - hit[row]) + z * l * l : 0.0f;
+}
+
+// ---------------------------------------------------------------- backward
+// what dl needs of a row
+struct alignas(16) RowGrad {
+    float lse, p;    // p: d (1 + 2 z lse), the factor of the probabilities
+    float d;
+    int32_t target;  // -1: the row takes no part
+};
+
+__global__ void vocab_rows_kernel(const float *lse, const float *d_loss, const int32_t *targets,
+                                  int64_t rows, int V, float z, RowGrad *out, int *status) {
+    let_next_start();
+    wait_for_previous();
+    const int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (r >= rows) return;
+    const int t = targets[r];
+    if (t >= V) raise_status(status, MOK_ERR_DEVICE_INVARIANT);
+    const bool in = t >= 0 && t < V;
+    const float l = lse[r], d = in ? d_loss[r] : 0.0f;
+    out[r] = RowGrad{l, in ? d * fmaf(2.0f * z, l, 1.0f) : 0.0f, d, in ? t : -1};
+}
+
+MOK_DEV float dl_of(const RowGrad &g, float l, int v) {
+    const float p = g.p * exp2_hw((l - g.lse) * LOG2E_F);
+    return g.target < 0 ? 0.0f : v == g.target ? p - g.d : p;
+}
+
+// bf16 planes that dl comes in for fp32 gradients: each takes what the ones before it leave. Two
+// would do as for the linear layer's dz (rms 2.7e-6 of it), but dl has no rounding of its own that
+// this would hide behind: gradients of 1001 rows, 1000 x 5003, are 2.7e-6 of their norm off with two
+// and 1.2e-6 with three, plain fp32 products 1.3e-6.
+constexpr int PLANES = 3;
+
+// The gradient of the logits for vocabulary entries [v0, v0 + N), in bf16 (F32: in planes, from logits
+// whose segments of H were added in fp32).
+template <bool F32>
+struct VocabDl {
+    using E = Epi<F32>;
+    static constexpr bool F32_OUT = F32, SUMS = F32, A_MN = false, B_MN = false;
+    Tiles tiles;
+    int n_mb;        // ceil(N / 256)
+    int segs;
+    int H, v0, N;
+    const RowGrad *rows;
+    uint16_t *dl;
+    int64_t ld, plane;
+    int *status;
+
+    MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
+    MOK_DEV void side_work(uint32_t, uint32_t, int) const {}
+    MOK_DEV Unit unit(uint32_t u) const {
+        const int4 t = tiles.get(u / (uint32_t)n_mb);
+        return Unit{0, t.y, t.z - t.y, 0, (int)(u % (uint32_t)n_mb), 0, 0};
+    }
+    MOK_DEV int segments(const Unit &) const { return segs; }
+    MOK_DEV int long_steps(const Unit &) const { return 0; }
+    MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
+        LinGeom q;
+        q.n_mma = (u.nr + 15) & ~15;
+        q.a0 = seg * SEG_K;
+        q.a1 = v0 + u.mb * 256 + (int)rank * 128;
+        q.a2 = 0;
+        q.b0 = q.a0;
+        q.b1 = u.r0 + (int)rank * (q.n_mma / 2);
+        q.nbox = (q.n_mma / 2 + 31) / 32;
+        const int k = segs > 1 && H - q.a0 > SEG_K ? SEG_K : H - q.a0;
+        q.k_steps = (k + 15) / 16;
+        q.k_first = q.half = 0;
+        return q;
+    }
+    MOK_DEV uint32_t tx(const LinGeom &q) const { return 2 * BOX + q.nbox * (BOX / 2); }
+    MOK_DEV void load(uint8_t *st, uint32_t fb, const LinGeom &q, int k0, const CUtensorMap *tmA,
+                      const CUtensorMap *tmB) const {
+        tma_load_3d_pair(st, tmA, fb, q.a0 + k0, q.a1, q.a2);
+        for (int j = 0; j < q.nbox; ++j)
+            tc::tma_load_2d_pair(st + 2 * BOX + j * (BOX / 2), tmB, fb, q.b0 + k0, q.b1 + 32 * j);
+    }
+    MOK_DEV void epilogue(const Unit &u, int seg, bool last, uint32_t rank, uint32_t c, int q, int hw,
+                          int lane, Patches &pt, Carry<SUMS> &carry) const {
+        const int64_t r0 = u.r0;
+        const int f0 = u.mb * 256 + (int)rank * 128 + q * 32;  // the warp's entries of the piece
+        if constexpr (F32) {
+            const int f = f0 + lane;
+            sum_segments(c, hw, u.nr, seg == 0, last, carry, [&](int n0, const float (&v)[16]) {
+                if (f >= N) return;
+                uint16_t *p = dl + (r0 + n0) * ld + f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if (n0 + j >= u.nr) continue;
+                    float g = dl_of(rows[r0 + n0 + j], v[j], v0 + f);
+#pragma unroll
+                    for (int k = 0; k < PLANES; ++k) {
+                        const uint16_t b = f32_to_bf16(g);
+                        p[k * plane + j * ld] = b;
+                        g = isfinite(bf16_to_f32(b)) ? g - bf16_to_f32(b) : 0.0f;
+                    }
+                }
+            });
+        } else {
+            for (int n0 = 32 * hw; n0 < u.nr; n0 += E::STEP) {
+#pragma unroll 2
+                for (int b = 0; b < 4; ++b) {
+                    float v[2][4];
+                    ld_pairs8(c + n0 + 8 * b, v);
+                    RowGrad g[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int n = n0 + 8 * b + 2 * (lane & 3) + i;
+                        g[i] = rows[r0 + (n < u.nr ? n : u.nr - 1)];
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[h][i] = dl_of(g[i & 1], v[h][i],
+                                            v0 + f0 + 16 * h + 8 * (i >> 1) + (lane >> 2));
+                    patch_write8(pt.patch(), pt.half, b, v, lane);
+                }
+                pt.store(OutRef{dl, tiles.rows, ld, N}, f0 & ~63, r0 + n0, r0 + u.nr, 0);
+            }
+        }
+    }
+};
+
+// dx of several pieces, from fp32 sums
+__global__ void __launch_bounds__(256)
+    vocab_round_kernel(const float *sum, int64_t ld_sum, int64_t rows, int H, uint16_t *dx, int64_t ld) {
+    let_next_start();
+    wait_for_previous();
+    const int64_t n = rows * (ld_sum / 4);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / (ld_sum / 4);
+        const int c = (int)(i - r * (ld_sum / 4)) * 4;
+        const float4 v = *reinterpret_cast<const float4 *>(sum + r * ld_sum + c);
+        uint16_t *p = dx + r * ld + c;
+        if (c + 4 <= H) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+        } else {
+            const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < H) p[j] = f32_to_bf16(e[j]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int64_t DL_BYTES = (int64_t)1 << 30;  // of a piece's dl, where the caller does not say
+
+struct VocabWs {
+    float2 *part;
+    float *hit;
+    RowGrad *rows;
+    uint16_t *dl;
+    float *dx_sum;
+    int piece, pieces;
+    int64_t ld_dl;
+};
+
+size_t carve_vocab(const mok_vocab_loss_config &c, int pass, void *ws, VocabWs *o) {
+    size_t off = 0;
+    const auto take = [&](size_t bytes) {
+        off = (size_t)round_up((int64_t)off, 256);
+        void *p = ws != nullptr ? (char *)ws + off : nullptr;
+        off += bytes;
+        return p;
+    };
+    VocabWs w = {};
+    if (pass == MOK_VOCAB_LOSS_FORWARD) {
+        w.part = (float2 *)take((size_t)c.rows * 4 * ((c.V + 255) / 256) * 8);
+        w.hit = (float *)take((size_t)c.rows * 4);
+    } else {
+        const int64_t planes = c.grad_dtype == MOK_DTYPE_F32 ? PLANES : 1;
+        const int64_t all = round_up(c.V, 256), row = 2 * planes * (c.rows > 0 ? c.rows : 1);
+        int64_t piece = c.piece;
+        if (piece == 0) {
+            int64_t most = DL_BYTES / row / 256 * 256;
+            if (most < 256) most = 256;
+            const int64_t n = (all + most - 1) / most;
+            piece = round_up((c.V + n - 1) / n, 256);
+        }
+        if (piece > all) piece = all;
+        w.piece = (int)piece;
+        w.pieces = (int)((c.V + piece - 1) / piece);
+        w.ld_dl = w.pieces > 1 ? piece : round_up(c.V, 8);
+        w.rows = (RowGrad *)take((size_t)c.rows * sizeof(RowGrad));
+        w.dl = (uint16_t *)take((size_t)planes * c.rows * w.ld_dl * 2);
+        if (w.pieces > 1 && c.grad_dtype == MOK_DTYPE_BF16)
+            w.dx_sum = (float *)take((size_t)c.rows * round_up(c.H, 4) * 4);
+    }
+    if (o != nullptr) *o = w;
+    return off > 0 ? off : 256;
+}
+
+mok_status check_vocab(const mok_vocab_loss_config *c, int pass, void *ws, size_t ws_bytes,
+                       int **status, VocabWs *w) {
+    mok_status st = mok_check_vocab_loss_config(c);
+    if (st != MOK_OK) return st;
+    if ((st = current_device_status_word(status)) != MOK_OK) return st;
+    if (carve_vocab(*c, pass, ws, w) > ws_bytes || ws == nullptr || ((uintptr_t)ws & 255u) != 0)
+        return MOK_ERR_WORKSPACE;
+    return MOK_OK;
+}
+
+}  // namespace
+}  // namespace mok
+
+using namespace mok;
+
+extern "C" {
+
+mok_status mok_check_vocab_loss_config(const mok_vocab_loss_config *c) {
+    if (c == nullptr) return MOK_ERR_INVALID_ARG;
+    if (c->abi_version != MOK_ABI_VERSION) return MOK_ERR_ABI;
+    if (c->H < 1 || c->H > (1 << 20) || c->V < 1 || c->V > (1 << 24)) return MOK_ERR_INVALID_ARG;
+    if (c->rows < 0 || c->rows >= ((int64_t)1 << 31) - 512) return MOK_ERR_INVALID_ARG;
+    const int64_t lds[] = {c->ld_x, c->ld_w};
+    for (int64_t ld : lds)
+        if (ld < c->H || ld % 8 != 0 || ld > ((int64_t)1 << 30)) return MOK_ERR_INVALID_ARG;
+    // units of the products are numbered in 31 bits
+    const int64_t tiles = c->rows / 16 + 1, vb = (c->V + 255) / 256, hb = (c->H + 255) / 256;
+    if (tiles * vb > INT32_MAX || tiles * hb > INT32_MAX || vb * 16 * hb > INT32_MAX)
+        return MOK_ERR_INVALID_ARG;
+    if (c->grad_dtype != MOK_DTYPE_BF16 && c->grad_dtype != MOK_DTYPE_F32) return MOK_ERR_INVALID_ARG;
+    if (!(c->z_loss >= 0.0f && c->z_loss <= 3.402823466e38f)) return MOK_ERR_INVALID_ARG;
+    if (c->piece < 0 || c->piece % 256 != 0) return MOK_ERR_INVALID_ARG;
+    return MOK_OK;
+}
+
+size_t mok_vocab_loss_workspace_size(const mok_vocab_loss_config *c, int pass) {
+    if (mok_check_vocab_loss_config(c) != MOK_OK) return 0;
+    if (pass != MOK_VOCAB_LOSS_FORWARD && pass != MOK_VOCAB_LOSS_BACKWARD) return 0;
+    return carve_vocab(*c, pass, nullptr, nullptr);
+}
+
+mok_status mok_vocab_loss_forward(const mok_vocab_loss_config *c, const void *x, const void *w,
+                                  const int32_t *targets, float *loss, float *lse, void *ws,
+                                  size_t ws_bytes, cudaStream_t stream) {
+    int *status;
+    VocabWs wk;
+    mok_status st = check_vocab(c, MOK_VOCAB_LOSS_FORWARD, ws, ws_bytes, &status, &wk);
+    if (st != MOK_OK) return st;
+    if (c->rows == 0) return MOK_OK;
+    if (!x || !w || !targets || !lse) return MOK_ERR_INVALID_ARG;
+    const void *ps[] = {x, w, targets, loss, lse};
+    for (const void *p : ps)
+        if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
+    CUtensorMap ma, mb;
+    if (map_w(&ma, x, 1, c->rows, c->H, c->ld_x, 128) != cudaSuccess ||
+        map2d(&mb, w, c->V, c->H, c->ld_w, 32) != cudaSuccess)
+        return MOK_ERR_CUDA;
+    const int n_rb = (int)((c->rows + 255) / 256), n_vt = (c->V + 255) / 256;
+    const VocabFwd p{c->rows, n_rb, n_vt, (c->H + SEG_K - 1) / SEG_K, c->H, c->V, targets, wk.part,
+                     wk.hit, status};
+    MOK_OP_LAUNCH(OP_VOCAB_FWD, 1, launch_linear(ma, mb, p, (int64_t)n_rb * n_vt, stream));
+    MOK_OP_LAUNCH(OP_VOCAB_FWD, 1,
+                  launch_edge(vocab_finish_kernel, (unsigned)((c->rows + 31) / 32),
+                              32 * FINISH_SLICES, 0, 1, stream, (const float2 *)wk.part,
+                              (const float *)wk.hit, c->rows, 4 * n_vt, c->V, targets, c->z_loss,
+                              loss, lse, status));
+    return MOK_OK;
+}
+
+mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x, const void *w,
+                                   const int32_t *targets, const float *lse, const float *d_loss,
+                                   void *dx, void *dw, void *ws, size_t ws_bytes,
+                                   cudaStream_t stream) {
+    int *status;
+    VocabWs wk;
+    mok_status st = check_vocab(c, MOK_VOCAB_LOSS_BACKWARD, ws, ws_bytes, &status, &wk);
+    if (st != MOK_OK) return st;
+    if (!dx && !dw) return MOK_ERR_INVALID_ARG;
+    if (c->rows > 0 && (!x || !w || !targets || !lse || !d_loss)) return MOK_ERR_INVALID_ARG;
+    const void *ps[] = {x, w, targets, lse, d_loss, dx, dw};
+    for (const void *p : ps)
+        if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
+    const bool f32 = c->grad_dtype == MOK_DTYPE_F32;
+    const size_t es = f32 ? 4 : 2;
+    if (c->rows == 0) {  // sums over nothing
+        if (dw && cudaMemset2DAsync(dw, (size_t)c->ld_w * es, 0, (size_t)c->H * es, (size_t)c->V,
+                                    stream) != cudaSuccess)
+            return MOK_ERR_CUDA;
+        return MOK_OK;
+    }
+    if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
+    CUtensorMap ma, mb;
+    if (map_w(&ma, w, 1, c->V, c->H, c->ld_w, 128) != cudaSuccess ||
+        map2d(&mb, x, c->rows, c->H, c->ld_x, 32) != cudaSuccess)
+        return MOK_ERR_CUDA;
+    MOK_OP_LAUNCH(OP_VOCAB_DL, 1,
+                  launch_edge(vocab_rows_kernel, (unsigned)((c->rows + 255) / 256), 256, 0, 1, stream,
+                              lse, d_loss, targets, c->rows, c->V, c->z_loss, wk.rows, status));
+    for (int k = 0; k < wk.pieces; ++k) {
+        const int v0 = k * wk.piece, n = c->V - v0 < wk.piece ? c->V - v0 : wk.piece;
+        const int n_mb = (n + 255) / 256;
+        int64_t clocks;
+        const Tiles tiles = dense_tiles(c->rows, dense_height(c->rows, n_mb, sm_pairs(), &clocks));
+        const int64_t units = tiles.cap * n_mb, plane = c->rows * wk.ld_dl;
+        if (f32) {
+            const VocabDl<true> p{tiles, n_mb, (c->H + SEG_K - 1) / SEG_K, c->H, v0, n, wk.rows,
+                                  wk.dl, wk.ld_dl, plane, status};
+            MOK_OP_LAUNCH(OP_VOCAB_DL, 1, launch_linear(ma, mb, p, units, stream));
+        } else {
+            const VocabDl<false> p{tiles, n_mb, 1, c->H, v0, n, wk.rows, wk.dl, wk.ld_dl, plane,
+                                   status};
+            MOK_OP_LAUNCH(OP_VOCAB_DL, 1, launch_linear(ma, mb, p, units, stream));
+        }
+        const DenseGrads g{(const uint16_t *)x, (const uint16_t *)w + v0 * c->ld_w, wk.dl, c->rows, n,
+                           c->H, f32 ? PLANES : 1, c->ld_x, c->ld_w, wk.ld_dl, dx,
+                           dw ? (char *)dw + v0 * c->ld_w * es : nullptr, f32,
+                           dx ? wk.dx_sum : nullptr, dx && k > 0};
+        MOK_OP_LAUNCH(OP_VOCAB_GRADS, 1, launch_dense_grads(g, status, stream));
+    }
+    if (dx && wk.dx_sum != nullptr) {
+        const int64_t n = c->rows * (round_up(c->H, 4) / 4), blocks = (n + 255) / 256;
+        const int64_t most = (int64_t)device_sm_count() * 32;
+        MOK_OP_LAUNCH(OP_VOCAB_GRADS, 1,
+                      launch_edge(vocab_round_kernel, (unsigned)(blocks < most ? blocks : most), 256,
+                                  0, 1, stream, (const float *)wk.dx_sum, round_up(c->H, 4), c->rows,
+                                  c->H, (uint16_t *)dx, c->ld_x));
+    }
+    return MOK_OK;
+}
+
+}  // extern "C"
