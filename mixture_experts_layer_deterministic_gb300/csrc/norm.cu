@@ -3,20 +3,25 @@
 //   h = x + residual, n = (h - mean) rstd, y = n w + b
 //   g = dy w, dx = dh + rstd (g - n mean(g n) - mean(g)), dw = sum dy n, db = sum dy
 //
-// All of it is HBM traffic. A row belongs to a power of two of threads, whose vectors of 8 elements
-// stay in registers between the passes over it; rows longer than that are read again. The mean is
-// taken in two steps (of h, then of h less the first), so that rows far from zero keep their
-// digits; the variance is that of h less the mean.
+// All of it is HBM traffic. A row belongs to a team, a power of two of threads that hold NV vectors
+// of 8 elements each; blocks walk over the rows, and where registers allow it (AHEAD) a team's next
+// row is on its way while it works on the last, so that the loads never pause. Rows too long for a
+// team are read again instead. The mean is taken in two steps (of h, then of h less the first), so
+// that rows far from zero keep their digits; the variance is that of h less the mean.
 #include "ops_internal.h"
 
 namespace mok {
 namespace {
 
-constexpr int NORM_TPB = 256;
-constexpr int NORM_VECS = 4;  // vectors of 8 a thread at most
+constexpr int NORM_TPB = 512;
 // blocks whose column sums are added in order: not of the device, the sums' bits depend on it
-constexpr int64_t NORM_PARTS = 2 * 152;
+constexpr int64_t NORM_PARTS = 152;
 
+// 8 elements as they lie in memory
+template <bool F32>
+struct Raw {
+    uint4 v[F32 ? 2 : 1];
+};
 // 8 elements from column c on, zeros past H (F32: two vectors)
 template <bool F32>
 MOK_DEV void load8(const void *row, int c, int H, float (&v)[8]) {
@@ -80,7 +85,7 @@ MOK_DEV float rounded(float v) {
 struct NormShape {
     int64_t rows, ld_x, ld_y;
     int H;
-    int tpr;  // threads of a row: a power of two
+    int tpr;  // threads of a team: a power of two
     bool layer;
     float eps;
 };
@@ -94,25 +99,59 @@ MOK_DEV void *row_of(void *p, int64_t r, int64_t ld) {
     return static_cast<char *>(p) + r * ld * (F32 ? 4 : 2);
 }
 
-// sums of a and b over the tpr threads of a row, the same in all of them. More than a warp's: through
-// sh, which the threads of every row of the block call together.
-struct RowSum {
-    float2 *sh;  // [warps of the block]
-    int tpr;
-    MOK_DEV void operator()(float &a, float &b) const {
+// 8 elements from column c on, zeros past H; whole vectors without a branch between their loads
+template <bool F32>
+MOK_DEV void load_raw(const void *row, int c, int H, Raw<F32> &q) {
+    if (c + 8 <= H) {
+        if (F32) {
+            q.v[0] = ld_v4(static_cast<const float *>(row) + c);
+            q.v[F32 ? 1 : 0] = ld_v4(static_cast<const float *>(row) + c + 4);
+        } else {
+            q.v[0] = ld_v4(static_cast<const uint16_t *>(row) + c);
+        }
+    } else {
+        uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (c + j >= H) continue;
+            if (F32)
+                e[j] = static_cast<const uint32_t *>(row)[c + j];
+            else
+                e[j >> 1] |= (uint32_t)static_cast<const uint16_t *>(row)[c + j] << (16 * (j & 1));
+        }
+        q.v[0] = make_uint4(e[0], e[1], e[2], e[3]);
+        if (F32) q.v[F32 ? 1 : 0] = make_uint4(e[4], e[5], e[6], e[7]);
+    }
+}
+template <bool F32>
+MOK_DEV void unpack(const Raw<F32> &q, float (&v)[8]) {
+    const uint4 b = q.v[F32 ? 1 : 0];
+    const uint32_t w[8] = {q.v[0].x, q.v[0].y, q.v[0].z, q.v[0].w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = F32 ? __uint_as_float(w[j]) : (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+}
+
+// sums of a and b over a team, the same in all of its threads. Teams of more than a warp: through
+// sh [2][warps of the block], its halves in turn, so that one barrier of the team is enough.
+struct TeamSum {
+    float2 *sh;
+    int tpr, turn;
+    MOK_DEV void operator()(float &a, float &b) {
         const int w = tpr < 32 ? tpr : 32;
         for (int o = 1; o < w; o <<= 1) {
             a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
             b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
         }
         if (tpr <= 32) return;
-        const int warp = threadIdx.x >> 5, n = tpr / 32, first = warp / n * n;
-        __syncthreads();  // the last sums have been read
-        if ((threadIdx.x & 31) == 0) sh[warp] = make_float2(a, b);
-        __syncthreads();
+        const int warp = threadIdx.x >> 5, n = tpr / 32, team = warp / n;
+        float2 *s = sh + turn * 32;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) s[warp] = make_float2(a, b);
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(tpr) : "memory");
         a = b = 0.0f;
         for (int k = 0; k < n; ++k) {
-            const float2 v = sh[first + k];
+            const float2 v = s[team * n + k];
             a += v.x;
             b += v.y;
         }
@@ -127,15 +166,13 @@ struct NormFwd {
     float *mean, *rstd;
 };
 
-// h of 8 columns, stored where asked for
-template <bool X32>
-MOK_DEV void load_h(const NormFwd &a, int64_t r, int c, float (&v)[8]) {
-    load8<X32>(row_of<X32>(a.x, r, a.s.ld_x), c, a.s.H, v);
-    if (a.res == nullptr) return;
-    float q[8];
-    load8<X32>(row_of<X32>(a.res, r, a.s.ld_x), c, a.s.H, q);
+// columns past H of a vector are zeros: they add to no sum but that of (0 - mean)^2
+MOK_DEV float square_from(const float (&v)[8], float mean, int n) {
+    float q = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = rounded<X32>(v[j] + q[j]);
+    for (int j = 0; j < 8; ++j)
+        if (j < n) q = fmaf(v[j] - mean, v[j] - mean, q);
+    return q;
 }
 
 template <bool Y32>
@@ -157,79 +194,106 @@ MOK_DEV void store_y(const NormFwd &a, int64_t r, int c, float mean, float rest,
     store8<Y32>(row_of<Y32>(a.y, r, a.s.ld_y), c, a.s.H, v);
 }
 
-// columns past H of a vector are zeros: they add to no sum but that of (0 - mean)^2
-MOK_DEV float square_from(const float (&v)[8], float mean, int n) {
-    float q = 0.0f;
+// the vectors of one row that a thread holds
+template <int NV, bool X32>
+struct NormRow {
+    Raw<X32> x[NV], res[NV];
+    MOK_DEV void load(const NormFwd &a, int64_t r, int i) {
+        const void *px = row_of<X32>(a.x, r, a.s.ld_x), *pr = row_of<X32>(a.res, r, a.s.ld_x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < n) q = fmaf(v[j] - mean, v[j] - mean, q);
-    return q;
-}
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (i + k * a.s.tpr);
+            x[k].v[0] = x[k].v[X32] = make_uint4(0, 0, 0, 0);
+            res[k].v[0] = res[k].v[X32] = make_uint4(0, 0, 0, 0);
+            if (r < a.s.rows && c < a.s.H) {
+                load_raw<X32>(px, c, a.s.H, x[k]);
+                if (a.res != nullptr) load_raw<X32>(pr, c, a.s.H, res[k]);
+            }
+        }
+    }
+};
 
-// NV vectors a thread: rows of at most 8 NV tpr elements
-template <int NV, bool X32, bool Y32>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormFwd a) {
-    __shared__ float2 sh[32];
+template <int NV, bool X32, bool Y32, bool AHEAD, int MOST>
+__global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const NormFwd a) {
+    __shared__ float2 sh[64];
     const NormShape &s = a.s;
-    const RowSum row_sum{sh, s.tpr};
+    TeamSum team_sum{sh, s.tpr, 0};
     let_next_start();
     wait_for_previous();
-    const int i = threadIdx.x % s.tpr;
-    const int64_t r = (int64_t)blockIdx.x * (blockDim.x / s.tpr) + threadIdx.x / s.tpr;
-    const bool in = r < s.rows;
-    float v[NV][8];
-    float sum = 0.0f, rest = 0.0f, sq = 0.0f;
+    const int i = threadIdx.x % s.tpr, slot = threadIdx.x / s.tpr, slots = blockDim.x / s.tpr;
+    const int64_t step = (int64_t)gridDim.x * slots;
+    NormRow<NV, X32> row;
+    row.load(a, (int64_t)blockIdx.x * slots + slot, i);
+    for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += step) {
+        const int64_t r = r0 + slot;
+        float v[NV][8];
+        float sum = 0.0f, rest = 0.0f, sq = 0.0f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = 8 * (i + k * s.tpr);
-        if (in && c < s.H) {
-            load_h<X32>(a, r, c, v[k]);
-        } else {
+        for (int k = 0; k < NV; ++k) {
+            unpack<X32>(row.x[k], v[k]);
+            if (a.res != nullptr) {
+                float q[8];
+                unpack<X32>(row.res[k], q);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+                for (int j = 0; j < 8; ++j) v[k][j] = rounded<X32>(v[k][j] + q[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += v[k][j];
         }
+        if (AHEAD && r0 + step < s.rows) row.load(a, r + step, i);
+        float mean = 0.0f;
+        if (s.layer) {
+            team_sum(sum, rest);
+            mean = sum / s.H;
+        }
+        rest = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += v[k][j];
-    }
-    float mean = 0.0f;
-    if (s.layer) {
-        row_sum(sum, rest);
-        mean = sum / s.H;
-    }
-    rest = 0.0f;
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (i + k * s.tpr), n = c < s.H ? s.H - c : 0;
+            sq += square_from(v[k], mean, n);
+            if (s.layer)
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = 8 * (i + k * s.tpr), n = in && c < s.H ? s.H - c : 0;
-        sq += square_from(v[k], mean, n);
-        if (s.layer)
+                for (int j = 0; j < 8; ++j)
+                    if (j < n) rest += v[k][j] - mean;
+        }
+        team_sum(sq, rest);
+        rest /= s.H;  // what the mean's rounding left
+        const float var = fmaxf(sq / s.H - rest * rest, 0.0f);
+        const float rstd = 1.0f / sqrtf(var + s.eps);
+        if (r < s.rows) {
+            if (i == 0) {
+                if (a.mean != nullptr) a.mean[r] = mean + rest;
+                if (a.rstd != nullptr) a.rstd[r] = rstd;
+            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) rest += v[k][j] - mean;
+            for (int k = 0; k < NV; ++k) {
+                const int c = 8 * (i + k * s.tpr);
+                if (c >= s.H) continue;
+                if (a.h != nullptr) store8<X32>(row_of<X32>(a.h, r, s.ld_x), c, s.H, v[k]);
+                store_y<Y32>(a, r, c, mean, rest, rstd, v[k]);
+            }
+        }
+        if (!AHEAD && r0 + step < s.rows) row.load(a, r + step, i);
     }
-    row_sum(sq, rest);
-    rest /= s.H;  // what the mean's rounding left
-    const float var = fmaxf(sq / s.H - rest * rest, 0.0f);
-    const float rstd = 1.0f / sqrtf(var + s.eps);
-    if (!in) return;
-    if (i == 0) {
-        if (a.mean != nullptr) a.mean[r] = mean + rest;
-        if (a.rstd != nullptr) a.rstd[r] = rstd;
-    }
+}
+
+// h of 8 columns
+template <bool X32>
+MOK_DEV void load_h(const NormFwd &a, int64_t r, int c, float (&v)[8]) {
+    load8<X32>(row_of<X32>(a.x, r, a.s.ld_x), c, a.s.H, v);
+    if (a.res == nullptr) return;
+    float q[8];
+    load8<X32>(row_of<X32>(a.res, r, a.s.ld_x), c, a.s.H, q);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = 8 * (i + k * s.tpr);
-        if (c >= s.H) continue;
-        if (a.h != nullptr) store8<X32>(row_of<X32>(a.h, r, s.ld_x), c, s.H, v[k]);
-        store_y<Y32>(a, r, c, mean, rest, rstd, v[k]);
-    }
+    for (int j = 0; j < 8; ++j) v[j] = rounded<X32>(v[j] + q[j]);
 }
 
 // longer rows: one a block, read three times (h is written last, so x or the residual may be h)
 template <bool X32, bool Y32>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormFwd a) {
-    __shared__ float2 sh[32];
+    __shared__ float2 sh[64];
     const NormShape &s = a.s;
-    const RowSum row_sum{sh, 1024};
+    TeamSum row_sum{sh, 1024, 0};
     let_next_start();
     wait_for_previous();
     const int64_t r = blockIdx.x;
@@ -310,51 +374,96 @@ MOK_DEV void store_dx(const NormBwd &a, int64_t r, int c, float rstd, float mg, 
     store8<X32>(row_of<X32>(a.dx, r, a.s.ld_x), c, a.s.H, v);
 }
 
-// Block b takes rows b, b + blocks, .. (a row to each tpr of its threads at a time), keeps its
-// columns' sums in registers and adds its rows' threads in order at the end.
+// the vectors of one row that a thread holds
 template <int NV, bool X32, bool Y32>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBwd a) {
+struct NormBwdRow {
+    Raw<X32> h[NV], dh[NV];
+    Raw<Y32> dy[NV];
+    float mean, rstd;
+    MOK_DEV void load(const NormBwd &a, int64_t r, int i) {
+        const NormShape &s = a.s;
+        const bool in = r < s.rows;
+        const void *ph = row_of<X32>(a.h, r, s.ld_x), *pd = row_of<X32>(a.dh, r, s.ld_x);
+        const void *py = row_of<Y32>(a.dy, r, s.ld_y);
+        mean = in && s.layer ? a.mean[r] : 0.0f;
+        rstd = in ? a.rstd[r] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (i + k * s.tpr);
+            h[k].v[0] = h[k].v[X32] = dh[k].v[0] = dh[k].v[X32] = make_uint4(0, 0, 0, 0);
+            dy[k].v[0] = dy[k].v[Y32] = make_uint4(0, 0, 0, 0);
+            if (in && c < s.H) {
+                load_raw<X32>(ph, c, s.H, h[k]);
+                load_raw<Y32>(py, c, s.H, dy[k]);
+                if (a.dh != nullptr) load_raw<X32>(pd, c, s.H, dh[k]);
+            }
+        }
+    }
+};
+
+// Block b's teams take the b-th, (b + blocks)-th, .. rows, keep their columns' sums in registers and
+// add them in order at the end.
+template <int NV, bool X32, bool Y32, bool AHEAD>
+__global__ void __launch_bounds__(NORM_TPB) norm_backward_kernel(const NormBwd a) {
     extern __shared__ float norm_smem[];
-    __shared__ float2 sh[32];
+    __shared__ float2 sh[64];
     const NormShape &s = a.s;
-    const RowSum row_sum{sh, s.tpr};
+    TeamSum team_sum{sh, s.tpr, 0};
     let_next_start();
     wait_for_previous();
     const int i = threadIdx.x % s.tpr, slot = threadIdx.x / s.tpr, slots = blockDim.x / s.tpr;
+    const int64_t step = (int64_t)gridDim.x * slots;
     float dw[NV][8], db[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
-    for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += (int64_t)gridDim.x * slots) {
+    NormBwdRow<NV, X32, Y32> next;
+    next.load(a, (int64_t)blockIdx.x * slots + slot, i);
+    for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += step) {
         const int64_t r = r0 + slot;
-        const bool in = r < s.rows;
-        const float mean = in && s.layer ? a.mean[r] : 0.0f, rstd = in ? a.rstd[r] : 0.0f;
-        float n[NV][8], dy[NV][8], sg = 0.0f, sgn = 0.0f;
+        const NormBwdRow<NV, X32, Y32> row = next;
+        if (AHEAD && r0 + step < s.rows) next.load(a, r + step, i);
+        float sg = 0.0f, sgn = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = 8 * (i + k * s.tpr);
-            if (in && c < s.H) {
-                load_ng<X32, Y32>(a, r, c, mean, rstd, n[k], dy[k], sg, sgn);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) n[k][j] = dy[k][j] = 0.0f;
-            }
+            float n[8], dy[8], w[8];
+            unpack<X32>(row.h[k], n);
+            unpack<Y32>(row.dy[k], dy);
+            if (a.w != nullptr && c < s.H) load8<true>(a.w, c, s.H, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                dw[k][j] = fmaf(dy[k][j], n[k][j], dw[k][j]);
-                db[k][j] += dy[k][j];
+                // past H dy is zero, so n does not matter there
+                n[j] = (n[j] - row.mean) * row.rstd;
+                const float g = a.w != nullptr && c < s.H ? dy[j] * w[j] : dy[j];
+                sg += g;
+                sgn = fmaf(g, n[j], sgn);
+                dw[k][j] = fmaf(dy[j], n[j], dw[k][j]);
+                db[k][j] += dy[j];
             }
         }
-        if (a.dx == nullptr) continue;
-        row_sum(sgn, sg);
-        if (!in) continue;
+        if (a.dx != nullptr) {
+            team_sum(sgn, sg);
+            const float mg = s.layer ? sg / s.H : 0.0f, mgn = sgn / s.H;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (i + k * s.tpr);
-            if (c < s.H)
-                store_dx<X32>(a, r, c, rstd, s.layer ? sg / s.H : 0.0f, sgn / s.H, n[k], dy[k]);
+            for (int k = 0; k < NV; ++k) {
+                const int c = 8 * (i + k * s.tpr);
+                if (r >= s.rows || c >= s.H) continue;
+                float n[8], dy[8], w[8], v[8];
+                unpack<X32>(row.h[k], n);
+                unpack<Y32>(row.dy[k], dy);
+                unpack<X32>(row.dh[k], v);
+                if (a.w != nullptr) load8<true>(a.w, c, s.H, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float g = a.w != nullptr ? dy[j] * w[j] : dy[j];
+                    v[j] += row.rstd * (g - (n[j] - row.mean) * row.rstd * mgn - mg);
+                }
+                store8<X32>(row_of<X32>(a.dx, r, s.ld_x), c, s.H, v);
+            }
         }
+        if (!AHEAD && r0 + step < s.rows) next.load(a, r + step, i);
     }
     for (int part = 0; part < 2; ++part) {
         float *out = part == 0 ? a.dw_part : a.db_part;
@@ -379,9 +488,9 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBwd a) {
 // longer rows: dx by a block a row, read twice
 template <bool X32, bool Y32>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBwd a) {
-    __shared__ float2 sh[32];
+    __shared__ float2 sh[64];
     const NormShape &s = a.s;
-    const RowSum row_sum{sh, 1024};
+    TeamSum row_sum{sh, 1024, 0};
     let_next_start();
     wait_for_previous();
     const int64_t r = blockIdx.x;
@@ -396,12 +505,13 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBwd 
     }
 }
 // ... and the column sums by a thread per 8 columns and part of the rows
+constexpr int COLUMNS_TPB = 256;
 template <bool X32, bool Y32>
-__global__ void __launch_bounds__(NORM_TPB) norm_columns_kernel(const NormBwd a) {
+__global__ void __launch_bounds__(COLUMNS_TPB) norm_columns_kernel(const NormBwd a) {
     const NormShape &s = a.s;
     let_next_start();
     wait_for_previous();
-    const int c = 8 * (blockIdx.x * NORM_TPB + threadIdx.x);
+    const int c = 8 * (blockIdx.x * COLUMNS_TPB + threadIdx.x);
     if (c >= s.H) return;
     float dw[8], db[8], n[8], dy[8], unused = 0.0f;
 #pragma unroll
@@ -466,75 +576,88 @@ int pow2_up(int n) {
     return p;
 }
 
+// How rows are held. Two vectors a thread where both types are bf16, one otherwise, is what the
+// registers hold twice: a row, and the next on its way. Longer rows have twice as many vectors a
+// thread and load a row when the last is done; yet longer ones are read again.
 struct NormPlan {
-    bool whole;      // rows fit the registers of 1024 threads
-    int nv, tpr;     // vectors a thread, threads a row
-    int64_t parts;   // of the backward's column sums
+    int nv, tpr, tpb;  // vectors a thread, threads of a team and of a block; nv 0: read again
+    bool ahead;
+    int64_t groups;    // of rows that a block takes at a time
+    int64_t parts;     // of the backward's column sums
 };
-NormPlan norm_plan(const mok_norm_config &c) {
-    const int vecs = (c.H + 7) / 8;
+NormPlan norm_plan(const mok_norm_config &c, bool backward) {
+    const int vecs = (c.H + 7) / 8, most = backward ? NORM_TPB : 1024;
+    const bool small = c.x_dtype == MOK_DTYPE_BF16 && c.y_dtype == MOK_DTYPE_BF16;
     NormPlan p = {};
-    p.whole = vecs <= 1024 * NORM_VECS;
-    p.nv = vecs <= 32 ? 1 : vecs <= 1024 ? 2 : NORM_VECS;
+    p.nv = small ? 2 : 1;
+    p.ahead = vecs <= p.nv * most;
+    if (!p.ahead && (backward || !small)) p.nv *= 2;
+    if (vecs > p.nv * most) {
+        p.nv = 0;
+        p.groups = c.rows;
+        p.parts = c.rows < 32 ? c.rows : 32;
+        return p;
+    }
     p.tpr = pow2_up((vecs + p.nv - 1) / p.nv);
-    if (p.tpr > 1024) p.tpr = 1024;
-    const int slots = p.tpr < NORM_TPB ? NORM_TPB / p.tpr : 1;
-    const int64_t groups = p.whole ? (c.rows + slots - 1) / slots : c.rows;
-    p.parts = groups < NORM_PARTS ? groups : NORM_PARTS;
-    if (!p.whole && p.parts > 32) p.parts = 32;
+    // few rows: smaller blocks, on more SMs
+    p.tpb = p.tpr > NORM_TPB ? p.tpr : NORM_TPB;
+    while (p.tpb > 128 && p.tpb > p.tpr && c.rows * p.tpr < NORM_PARTS * p.tpb) p.tpb /= 2;
+    p.groups = (c.rows + p.tpb / p.tpr - 1) / (p.tpb / p.tpr);
+    p.parts = p.groups < NORM_PARTS ? p.groups : NORM_PARTS;
     return p;
 }
 size_t norm_part_bytes(const mok_norm_config &c) {
-    return (size_t)round_up(norm_plan(c).parts * c.H * 4, 256);
+    return (size_t)round_up(norm_plan(c, true).parts * c.H * 4, 256);
 }
 
-#define MOK_NORM_TYPES(F)                                   \
-    (x32 ? (y32 ? F(true, true) : F(true, false))           \
-         : (y32 ? F(false, true) : F(false, false)))
+// f by the types of x and y
+#define MOK_NORM_TYPES(f, ...)                                                              \
+    (c->x_dtype == MOK_DTYPE_F32                                                            \
+         ? (c->y_dtype == MOK_DTYPE_F32 ? f<true, true>(__VA_ARGS__) : f<true, false>(__VA_ARGS__)) \
+         : (c->y_dtype == MOK_DTYPE_F32 ? f<false, true>(__VA_ARGS__)                       \
+                                        : f<false, false>(__VA_ARGS__)))
 
-cudaError_t launch_norm(NormFwd a, const NormPlan &p, bool x32, bool y32, cudaStream_t s) {
+template <bool X32, bool Y32>
+cudaError_t launch_norm(NormFwd a, const NormPlan &p, cudaStream_t s) {
+    constexpr int NV = X32 || Y32 ? 1 : 2;
     a.s.tpr = p.tpr;
-    const int tpb = p.tpr < NORM_TPB ? NORM_TPB : p.tpr;
-    const unsigned grid = (unsigned)((a.s.rows + tpb / p.tpr - 1) / (tpb / p.tpr));
-#define MOK_F(X, Y)                                                                 \
-    (!p.whole    ? launch_edge(norm_long_kernel<X, Y>, (unsigned)a.s.rows, 1024, 0, 1, s, a) \
-     : p.nv == 1 ? launch_edge(norm_kernel<1, X, Y>, grid, tpb, 0, 1, s, a)         \
-     : p.nv == 2 ? launch_edge(norm_kernel<2, X, Y>, grid, tpb, 0, 1, s, a)         \
-                 : launch_edge(norm_kernel<NORM_VECS, X, Y>, grid, tpb, 0, 1, s, a))
-    return MOK_NORM_TYPES(MOK_F);
-#undef MOK_F
+    if (p.nv == 0)
+        return launch_edge(norm_long_kernel<X32, Y32>, (unsigned)a.s.rows, 1024, 0, 1, s, a);
+    const int64_t most = (int64_t)device_sm_count() * (1024 / p.tpb);
+    const unsigned grid = (unsigned)(p.groups < most ? p.groups : most);
+    if constexpr (NV == 1)
+        if (!p.ahead)
+            return launch_edge(norm_kernel<2 * NV, X32, Y32, false, 1024>, grid, p.tpb, 0, 1, s, a);
+    if (p.tpb > NORM_TPB)
+        return launch_edge(norm_kernel<NV, X32, Y32, true, 1024>, grid, p.tpb, 0, 1, s, a);
+    return launch_edge(norm_kernel<NV, X32, Y32, true, NORM_TPB>, grid, p.tpb, 0, 1, s, a);
 }
 
-cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, bool x32, bool y32, cudaStream_t s) {
+template <bool X32, bool Y32>
+cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, cudaStream_t s) {
+    constexpr int NV = X32 || Y32 ? 1 : 2;
     a.s.tpr = p.tpr;
     const bool sums = a.dw_part != nullptr || a.db_part != nullptr;
-    if (!p.whole) {
-        const dim3 cols((unsigned)((a.s.H + 8 * NORM_TPB - 1) / (8 * NORM_TPB)), (unsigned)p.parts);
+    if (p.nv == 0) {
+        const dim3 cols((unsigned)((a.s.H + 8 * COLUMNS_TPB - 1) / (8 * COLUMNS_TPB)),
+                        (unsigned)p.parts);
         cudaError_t e = cudaSuccess;
-#define MOK_F(X, Y) launch_edge(norm_columns_kernel<X, Y>, cols, NORM_TPB, 0, 1, s, a)
-        if (sums) e = MOK_NORM_TYPES(MOK_F);
-#undef MOK_F
+        if (sums) e = launch_edge(norm_columns_kernel<X32, Y32>, cols, COLUMNS_TPB, 0, 1, s, a);
         if (e != cudaSuccess || a.dx == nullptr) return e;
-#define MOK_F(X, Y) \
-    launch_edge(norm_backward_long_kernel<X, Y>, (unsigned)a.s.rows, 1024, 0, 1, s, a)
-        return MOK_NORM_TYPES(MOK_F);
-#undef MOK_F
+        return launch_edge(norm_backward_long_kernel<X32, Y32>, (unsigned)a.s.rows, 1024, 0, 1, s, a);
     }
-    const int tpb = p.tpr < NORM_TPB ? NORM_TPB : p.tpr;
-    const int smem = sums ? tpb / p.tpr * a.s.H * 4 : 0;
+    // the teams' sums of a block: at most 8 nv floats a thread
+    const int smem = sums ? p.tpb / p.tpr * a.s.H * 4 : 0;
     const unsigned grid = (unsigned)p.parts;
-#define MOK_G(K)                                                                                    \
-    (smem <= 48 * 1024 ||                                                                           \
-             cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess \
-         ? launch_edge(K, grid, tpb, smem, 1, s, a)                                                 \
-         : cudaErrorInvalidValue)
-#define MOK_F(X, Y)                                                      \
-    (p.nv == 1   ? MOK_G((norm_backward_kernel<1, X, Y>))                \
-     : p.nv == 2 ? MOK_G((norm_backward_kernel<2, X, Y>))                \
-                 : MOK_G((norm_backward_kernel<NORM_VECS, X, Y>)))
-    return MOK_NORM_TYPES(MOK_F);
-#undef MOK_F
-#undef MOK_G
+    if (p.ahead)
+        return launch_edge(norm_backward_kernel<NV, X32, Y32, true>, grid, p.tpb, smem, 1, s, a);
+    const auto wide = norm_backward_kernel<2 * NV, X32, Y32, false>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            wide, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * 2 * NV * NORM_TPB * 4);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_edge(wide, grid, p.tpb, smem, 1, s, a);
 }
 
 }  // namespace
@@ -582,8 +705,7 @@ mok_status mok_norm_forward(const mok_norm_config *c, const void *x, const void 
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
     const NormFwd a{norm_shape(*c), x, residual, weight, bias, h, y, mean, rstd};
     MOK_OP_LAUNCH(OP_NORM, 1,
-                  launch_norm(a, norm_plan(*c), c->x_dtype == MOK_DTYPE_F32,
-                              c->y_dtype == MOK_DTYPE_F32, stream));
+                  MOK_NORM_TYPES(launch_norm, a, norm_plan(*c, false), stream));
     return MOK_OK;
 }
 
@@ -606,14 +728,13 @@ mok_status mok_norm_backward(const mok_norm_config *c, const void *h, const floa
     const void *ps[] = {h, mean, rstd, weight, dy, dh, dx, dw, db};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    const NormPlan plan = norm_plan(*c);
+    const NormPlan plan = norm_plan(*c, true);
     float *wp = dw ? (float *)ws : nullptr;
     float *bp = db ? (float *)((char *)ws + norm_part_bytes(*c)) : nullptr;
     if (c->rows > 0) {
         const NormBwd a{norm_shape(*c), h, dy, dh, mean, rstd, weight, dx, wp, bp};
         MOK_OP_LAUNCH(OP_NORM_BWD, 1,
-                      launch_norm_backward(a, plan, c->x_dtype == MOK_DTYPE_F32,
-                                           c->y_dtype == MOK_DTYPE_F32, stream));
+                      MOK_NORM_TYPES(launch_norm_backward, a, plan, stream));
     }
     if (sums)
         MOK_OP_LAUNCH(OP_NORM_BWD, 1,
