@@ -23,9 +23,9 @@ struct Raw {
     uint4 v[F32 ? 2 : 1];
 };
 // 8 elements from column c on, zeros past H (F32: two vectors)
-template <bool F32>
+template <bool F32, bool WHOLE = false>
 MOK_DEV void load8(const void *row, int c, int H, float (&v)[8]) {
-    if (c + 8 <= H) {
+    if (WHOLE || c + 8 <= H) {
         if (F32) {
             const uint4 a = ld_v4(static_cast<const float *>(row) + c);
             const uint4 b = ld_v4(static_cast<const float *>(row) + c + 4);
@@ -41,22 +41,22 @@ MOK_DEV void load8(const void *row, int c, int H, float (&v)[8]) {
                 v[2 * j + 1] = bf16_hi(w[j]);
             }
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = c + j >= H ? 0.0f
-               : F32      ? static_cast<const float *>(row)[c + j]
-                          : bf16_to_f32(static_cast<const uint16_t *>(row)[c + j]);
+        for (int j = 0; j < 8; ++j)
+            v[j] = c + j >= H ? 0.0f
+                   : F32      ? static_cast<const float *>(row)[c + j]
+                              : bf16_to_f32(static_cast<const uint16_t *>(row)[c + j]);
+    }
 }
 MOK_DEV uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-template <bool F32>
+template <bool F32, bool WHOLE = false>
 MOK_DEV void store8(void *row, int c, int H, const float (&v)[8]) {
-    if (c + 8 <= H) {
+    if (WHOLE || c + 8 <= H) {
         if (F32) {
             float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(row) + c);
             p[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -65,21 +65,49 @@ MOK_DEV void store8(void *row, int c, int H, const float (&v)[8]) {
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + c) = make_uint4(
                 pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (c + j >= H) continue;
-        if (F32)
-            static_cast<float *>(row)[c + j] = v[j];
-        else
-            static_cast<uint16_t *>(row)[c + j] = f32_to_bf16(v[j]);
+        for (int j = 0; j < 8; ++j) {
+            if (c + j >= H) continue;
+            if (F32)
+                static_cast<float *>(row)[c + j] = v[j];
+            else
+                static_cast<uint16_t *>(row)[c + j] = f32_to_bf16(v[j]);
+        }
     }
 }
 // as it will be read back
 template <bool F32>
 MOK_DEV float rounded(float v) {
     return F32 ? v : bf16_to_f32(f32_to_bf16(v));
+}
+
+// two fp32 values in one register pair, and the pipe's instructions on both at once
+typedef unsigned long long f32x2;
+MOK_DEV f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+MOK_DEV float2 both(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+MOK_DEV f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+MOK_DEV f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+MOK_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 struct NormShape {
@@ -99,10 +127,10 @@ MOK_DEV void *row_of(void *p, int64_t r, int64_t ld) {
     return static_cast<char *>(p) + r * ld * (F32 ? 4 : 2);
 }
 
-// 8 elements from column c on, zeros past H; whole vectors without a branch between their loads
-template <bool F32>
+// 8 elements from column c on, zeros past H; where rows are WHOLE vectors there is nothing past H
+template <bool F32, bool WHOLE>
 MOK_DEV void load_raw(const void *row, int c, int H, Raw<F32> &q) {
-    if (c + 8 <= H) {
+    if (WHOLE || c + 8 <= H) {
         if (F32) {
             q.v[0] = ld_v4(static_cast<const float *>(row) + c);
             q.v[F32 ? 1 : 0] = ld_v4(static_cast<const float *>(row) + c + 4);
@@ -122,6 +150,15 @@ MOK_DEV void load_raw(const void *row, int c, int H, Raw<F32> &q) {
         q.v[0] = make_uint4(e[0], e[1], e[2], e[3]);
         if (F32) q.v[F32 ? 1 : 0] = make_uint4(e[4], e[5], e[6], e[7]);
     }
+}
+template <bool F32>
+MOK_DEV void unpack(const Raw<F32> &q, f32x2 (&v)[4]) {
+    const uint4 b = q.v[F32 ? 1 : 0];
+    const uint32_t w[8] = {q.v[0].x, q.v[0].y, q.v[0].z, q.v[0].w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        v[j] = F32 ? pair(__uint_as_float(w[F32 ? 2 * j : j]), __uint_as_float(w[F32 ? 2 * j + 1 : j]))
+                   : pair(bf16_lo(w[j]), bf16_hi(w[j]));
 }
 template <bool F32>
 MOK_DEV void unpack(const Raw<F32> &q, float (&v)[8]) {
@@ -175,27 +212,27 @@ MOK_DEV float square_from(const float (&v)[8], float mean, int n) {
     return q;
 }
 
-template <bool Y32>
+template <bool Y32, bool WHOLE = false>
 MOK_DEV void store_y(const NormFwd &a, int64_t r, int c, float mean, float rest, float rstd,
                      float (&v)[8]) {
     float p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (v[j] - mean - rest) * rstd;
     if (a.w != nullptr) {
-        load8<true>(a.w, c, a.s.H, p);
+        load8<true, WHOLE>(a.w, c, a.s.H, p);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= p[j];
     }
     if (a.b != nullptr) {
-        load8<true>(a.b, c, a.s.H, p);
+        load8<true, WHOLE>(a.b, c, a.s.H, p);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += p[j];
     }
-    store8<Y32>(row_of<Y32>(a.y, r, a.s.ld_y), c, a.s.H, v);
+    store8<Y32, WHOLE>(row_of<Y32>(a.y, r, a.s.ld_y), c, a.s.H, v);
 }
 
 // the vectors of one row that a thread holds
-template <int NV, bool X32>
+template <int NV, bool X32, bool WHOLE>
 struct NormRow {
     Raw<X32> x[NV], res[NV];
     MOK_DEV void load(const NormFwd &a, int64_t r, int i) {
@@ -206,14 +243,14 @@ struct NormRow {
             x[k].v[0] = x[k].v[X32] = make_uint4(0, 0, 0, 0);
             res[k].v[0] = res[k].v[X32] = make_uint4(0, 0, 0, 0);
             if (r < a.s.rows && c < a.s.H) {
-                load_raw<X32>(px, c, a.s.H, x[k]);
-                if (a.res != nullptr) load_raw<X32>(pr, c, a.s.H, res[k]);
+                load_raw<X32, WHOLE>(px, c, a.s.H, x[k]);
+                if (a.res != nullptr) load_raw<X32, WHOLE>(pr, c, a.s.H, res[k]);
             }
         }
     }
 };
 
-template <int NV, bool X32, bool Y32, bool AHEAD, int MOST>
+template <int NV, bool X32, bool Y32, bool WHOLE, bool AHEAD, int MOST>
 __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const NormFwd a) {
     __shared__ float2 sh[64];
     const NormShape &s = a.s;
@@ -222,7 +259,7 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const NormFwd a
     wait_for_previous();
     const int i = threadIdx.x % s.tpr, slot = threadIdx.x / s.tpr, slots = blockDim.x / s.tpr;
     const int64_t step = (int64_t)gridDim.x * slots;
-    NormRow<NV, X32> row;
+    NormRow<NV, X32, WHOLE> row;
     row.load(a, (int64_t)blockIdx.x * slots + slot, i);
     for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += step) {
         const int64_t r = r0 + slot;
@@ -249,7 +286,7 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const NormFwd a
         rest = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (i + k * s.tpr), n = c < s.H ? s.H - c : 0;
+            const int c = 8 * (i + k * s.tpr), n = c >= s.H ? 0 : WHOLE ? 8 : s.H - c;
             sq += square_from(v[k], mean, n);
             if (s.layer)
 #pragma unroll
@@ -269,8 +306,8 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const NormFwd a
             for (int k = 0; k < NV; ++k) {
                 const int c = 8 * (i + k * s.tpr);
                 if (c >= s.H) continue;
-                if (a.h != nullptr) store8<X32>(row_of<X32>(a.h, r, s.ld_x), c, s.H, v[k]);
-                store_y<Y32>(a, r, c, mean, rest, rstd, v[k]);
+                if (a.h != nullptr) store8<X32, WHOLE>(row_of<X32>(a.h, r, s.ld_x), c, s.H, v[k]);
+                store_y<Y32, WHOLE>(a, r, c, mean, rest, rstd, v[k]);
             }
         }
         if (!AHEAD && r0 + step < s.rows) row.load(a, r + step, i);
@@ -375,7 +412,7 @@ MOK_DEV void store_dx(const NormBwd &a, int64_t r, int c, float rstd, float mg, 
 }
 
 // the vectors of one row that a thread holds
-template <int NV, bool X32, bool Y32>
+template <int NV, bool X32, bool Y32, bool WHOLE>
 struct NormBwdRow {
     Raw<X32> h[NV], dh[NV];
     Raw<Y32> dy[NV];
@@ -393,9 +430,9 @@ struct NormBwdRow {
             h[k].v[0] = h[k].v[X32] = dh[k].v[0] = dh[k].v[X32] = make_uint4(0, 0, 0, 0);
             dy[k].v[0] = dy[k].v[Y32] = make_uint4(0, 0, 0, 0);
             if (in && c < s.H) {
-                load_raw<X32>(ph, c, s.H, h[k]);
-                load_raw<Y32>(py, c, s.H, dy[k]);
-                if (a.dh != nullptr) load_raw<X32>(pd, c, s.H, dh[k]);
+                load_raw<X32, WHOLE>(ph, c, s.H, h[k]);
+                load_raw<Y32, WHOLE>(py, c, s.H, dy[k]);
+                if (a.dh != nullptr) load_raw<X32, WHOLE>(pd, c, s.H, dh[k]);
             }
         }
     }
@@ -403,7 +440,7 @@ struct NormBwdRow {
 
 // Block b's teams take the b-th, (b + blocks)-th, .. rows, keep their columns' sums in registers and
 // add them in order at the end.
-template <int NV, bool X32, bool Y32, bool AHEAD>
+template <int NV, bool X32, bool Y32, bool WHOLE, bool AHEAD>
 __global__ void __launch_bounds__(NORM_TPB) norm_backward_kernel(const NormBwd a) {
     extern __shared__ float norm_smem[];
     __shared__ float2 sh[64];
@@ -413,54 +450,69 @@ __global__ void __launch_bounds__(NORM_TPB) norm_backward_kernel(const NormBwd a
     wait_for_previous();
     const int i = threadIdx.x % s.tpr, slot = threadIdx.x / s.tpr, slots = blockDim.x / s.tpr;
     const int64_t step = (int64_t)gridDim.x * slots;
-    float dw[NV][8], db[NV][8];
+    f32x2 dw[NV][4], db[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
-    NormBwdRow<NV, X32, Y32> next;
+        for (int j = 0; j < 4; ++j) dw[k][j] = db[k][j] = 0;
+    // the weights of vector k, ones without them and past the row
+    const auto weights = [&](int c, f32x2 (&w)[4]) {
+        Raw<true> q;
+        q.v[0] = q.v[1] = make_uint4(0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u);
+        if (a.w != nullptr && c < s.H) load_raw<true, WHOLE>(a.w, c, s.H, q);
+        unpack<true>(q, w);
+    };
+    NormBwdRow<NV, X32, Y32, WHOLE> next;
     next.load(a, (int64_t)blockIdx.x * slots + slot, i);
     for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += step) {
         const int64_t r = r0 + slot;
-        const NormBwdRow<NV, X32, Y32> row = next;
+        const NormBwdRow<NV, X32, Y32, WHOLE> row = next;
         if (AHEAD && r0 + step < s.rows) next.load(a, r + step, i);
-        float sg = 0.0f, sgn = 0.0f;
+        // with t = h - mean: n = t rstd, so sum(g n) = rstd sum(g t). Past H dy is zero, so t does not
+        // matter there
+        const f32x2 mean = pair(-row.mean, -row.mean), rstd = pair(row.rstd, row.rstd);
+        f32x2 sg2 = 0, sgt2 = 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (i + k * s.tpr);
-            float n[8], dy[8], w[8];
-            unpack<X32>(row.h[k], n);
+            f32x2 t[4], dy[4], w[4];
+            unpack<X32>(row.h[k], t);
             unpack<Y32>(row.dy[k], dy);
-            if (a.w != nullptr && c < s.H) load8<true>(a.w, c, s.H, w);
+            weights(8 * (i + k * s.tpr), w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // past H dy is zero, so n does not matter there
-                n[j] = (n[j] - row.mean) * row.rstd;
-                const float g = a.w != nullptr && c < s.H ? dy[j] * w[j] : dy[j];
-                sg += g;
-                sgn = fmaf(g, n[j], sgn);
-                dw[k][j] = fmaf(dy[j], n[j], dw[k][j]);
-                db[k][j] += dy[j];
+            for (int j = 0; j < 4; ++j) {
+                t[j] = add2(t[j], mean);
+                const f32x2 g = mul2(dy[j], w[j]);
+                sg2 = add2(sg2, g);
+                sgt2 = fma2(g, t[j], sgt2);
+                dw[k][j] = fma2(mul2(dy[j], rstd), t[j], dw[k][j]);
+                db[k][j] = add2(db[k][j], dy[j]);
             }
         }
         if (a.dx != nullptr) {
-            team_sum(sgn, sg);
-            const float mg = s.layer ? sg / s.H : 0.0f, mgn = sgn / s.H;
+            float sg = both(sg2).x + both(sg2).y, sgt = both(sgt2).x + both(sgt2).y;
+            team_sum(sgt, sg);
+            // dx = dh - rstd mean(g) + g rstd - t rstd^2 mean(g n)
+            const float c0 = s.layer ? -row.rstd * (sg / s.H) : 0.0f;
+            const float c1 = -row.rstd * row.rstd * (row.rstd * (sgt / s.H));
+            const f32x2 a0 = pair(c0, c0), a1 = pair(c1, c1);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int c = 8 * (i + k * s.tpr);
                 if (r >= s.rows || c >= s.H) continue;
-                float n[8], dy[8], w[8], v[8];
-                unpack<X32>(row.h[k], n);
+                f32x2 t[4], dy[4], w[4], v[4];
+                unpack<X32>(row.h[k], t);
                 unpack<Y32>(row.dy[k], dy);
                 unpack<X32>(row.dh[k], v);
-                if (a.w != nullptr) load8<true>(a.w, c, s.H, w);
+                weights(c, w);
+                float o[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float g = a.w != nullptr ? dy[j] * w[j] : dy[j];
-                    v[j] += row.rstd * (g - (n[j] - row.mean) * row.rstd * mgn - mg);
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = fma2(mul2(dy[j], w[j]), rstd, add2(v[j], a0));
+                    v[j] = fma2(add2(t[j], mean), a1, v[j]);
+                    o[2 * j] = both(v[j]).x;
+                    o[2 * j + 1] = both(v[j]).y;
                 }
-                store8<X32>(row_of<X32>(a.dx, r, s.ld_x), c, s.H, v);
+                store8<X32, WHOLE>(row_of<X32>(a.dx, r, s.ld_x), c, s.H, o);
             }
         }
         if (!AHEAD && r0 + step < s.rows) next.load(a, r + step, i);
@@ -473,8 +525,10 @@ __global__ void __launch_bounds__(NORM_TPB) norm_backward_kernel(const NormBwd a
         for (int k = 0; k < NV; ++k) {
             const int c = 8 * (i + k * s.tpr);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < s.H) norm_smem[slot * s.H + c + j] = part == 0 ? dw[k][j] : db[k][j];
+            for (int j = 0; j < 8; ++j) {
+                const float2 v = both(part == 0 ? dw[k][j >> 1] : db[k][j >> 1]);
+                if (c + j < s.H) norm_smem[slot * s.H + c + j] = (j & 1) ? v.y : v.x;
+            }
         }
         __syncthreads();
         for (int c = threadIdx.x; c < s.H; c += blockDim.x) {
@@ -610,14 +664,17 @@ size_t norm_part_bytes(const mok_norm_config &c) {
     return (size_t)round_up(norm_plan(c, true).parts * c.H * 4, 256);
 }
 
-// f by the types of x and y
-#define MOK_NORM_TYPES(f, ...)                                                              \
-    (c->x_dtype == MOK_DTYPE_F32                                                            \
-         ? (c->y_dtype == MOK_DTYPE_F32 ? f<true, true>(__VA_ARGS__) : f<true, false>(__VA_ARGS__)) \
-         : (c->y_dtype == MOK_DTYPE_F32 ? f<false, true>(__VA_ARGS__)                       \
-                                        : f<false, false>(__VA_ARGS__)))
+// f by the types of x and y, and whether rows are whole vectors
+#define MOK_NORM_WHOLE(f, X, Y, ...) \
+    (c->H % 8 == 0 ? f<X, Y, true>(__VA_ARGS__) : f<X, Y, false>(__VA_ARGS__))
+#define MOK_NORM_TYPES(f, ...)                                                           \
+    (c->x_dtype == MOK_DTYPE_F32                                                         \
+         ? (c->y_dtype == MOK_DTYPE_F32 ? MOK_NORM_WHOLE(f, true, true, __VA_ARGS__)     \
+                                        : MOK_NORM_WHOLE(f, true, false, __VA_ARGS__))   \
+         : (c->y_dtype == MOK_DTYPE_F32 ? MOK_NORM_WHOLE(f, false, true, __VA_ARGS__)    \
+                                        : MOK_NORM_WHOLE(f, false, false, __VA_ARGS__)))
 
-template <bool X32, bool Y32>
+template <bool X32, bool Y32, bool WHOLE>
 cudaError_t launch_norm(NormFwd a, const NormPlan &p, cudaStream_t s) {
     constexpr int NV = X32 || Y32 ? 1 : 2;
     a.s.tpr = p.tpr;
@@ -627,13 +684,13 @@ cudaError_t launch_norm(NormFwd a, const NormPlan &p, cudaStream_t s) {
     const unsigned grid = (unsigned)(p.groups < most ? p.groups : most);
     if constexpr (NV == 1)
         if (!p.ahead)
-            return launch_edge(norm_kernel<2 * NV, X32, Y32, false, 1024>, grid, p.tpb, 0, 1, s, a);
+            return launch_edge(norm_kernel<2 * NV, X32, Y32, WHOLE, false, 1024>, grid, p.tpb, 0, 1, s, a);
     if (p.tpb > NORM_TPB)
-        return launch_edge(norm_kernel<NV, X32, Y32, true, 1024>, grid, p.tpb, 0, 1, s, a);
-    return launch_edge(norm_kernel<NV, X32, Y32, true, NORM_TPB>, grid, p.tpb, 0, 1, s, a);
+        return launch_edge(norm_kernel<NV, X32, Y32, WHOLE, true, 1024>, grid, p.tpb, 0, 1, s, a);
+    return launch_edge(norm_kernel<NV, X32, Y32, WHOLE, true, NORM_TPB>, grid, p.tpb, 0, 1, s, a);
 }
 
-template <bool X32, bool Y32>
+template <bool X32, bool Y32, bool WHOLE>
 cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, cudaStream_t s) {
     constexpr int NV = X32 || Y32 ? 1 : 2;
     a.s.tpr = p.tpr;
@@ -650,8 +707,8 @@ cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, cudaStream_t s) {
     const int smem = sums ? p.tpb / p.tpr * a.s.H * 4 : 0;
     const unsigned grid = (unsigned)p.parts;
     if (p.ahead)
-        return launch_edge(norm_backward_kernel<NV, X32, Y32, true>, grid, p.tpb, smem, 1, s, a);
-    const auto wide = norm_backward_kernel<2 * NV, X32, Y32, false>;
+        return launch_edge(norm_backward_kernel<NV, X32, Y32, WHOLE, true>, grid, p.tpb, smem, 1, s, a);
+    const auto wide = norm_backward_kernel<2 * NV, X32, Y32, WHOLE, false>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(
             wide, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * 2 * NV * NORM_TPB * 4);
