@@ -598,13 +598,21 @@ __global__ void __launch_bounds__(32 * NORM_SLICES)
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.0f, t = 0.0f;
-    if (c < H) {
-        if (dw != nullptr)
-#pragma unroll 8
-            for (int p = slice; p < parts; p += NORM_SLICES) s += dw_part[(int64_t)p * H + c];
-        if (db != nullptr)
-#pragma unroll 8
-            for (int p = slice; p < parts; p += NORM_SLICES) t += db_part[(int64_t)p * H + c];
+    // a batch of loads at a time, the last one too
+    for (int p0 = slice; p0 < parts; p0 += 10 * NORM_SLICES) {
+        float v[10], u[10];
+#pragma unroll
+        for (int k = 0; k < 10; ++k) {
+            const int p = p0 + k * NORM_SLICES;
+            const bool in = p < parts && c < H;
+            v[k] = in && dw != nullptr ? dw_part[(int64_t)p * H + c] : 0.0f;
+            u[k] = in && db != nullptr ? db_part[(int64_t)p * H + c] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 10; ++k) {
+            s += v[k];
+            t += u[k];
+        }
     }
     sh[0][slice][lane] = s;
     sh[1][slice][lane] = t;

@@ -3,35 +3,41 @@
 //
 //   s = softmax(l) or sigmoid(l), c = s + bias; the K largest c of the kept groups; weights from s
 //
-// One warp per token. With one group, lane l holds experts l, l + 32, ..; with more, each group has
-// L lanes of its own (a power of two) and lane i of group g holds experts g E/groups + i, + L, ..
-// A choice takes K rounds: the warp's largest key by one integer reduction over order-preserving
-// images, the lowest id that holds it by a second; the lane that held it looks for its next.
+// One warp per token, whose logits stay in registers. Each group of experts has a power of two of
+// lanes (32 where there is one group), which hold its experts in turn, four at a time where rows
+// allow 16-byte loads. A choice takes K rounds: the warp's largest key by one integer reduction over
+// order-preserving images, the lowest id that holds it where several do; the lane that held it goes on
+// to its second, and looks for its next two when both are gone.
 //
-// The choice has to be that of exact scores. fp32 scores are off by at most a few units in their
-// last place (bounds at score_error), so a choice is settled unless two neighbours in the order of
-// the chosen, or the last kept and the first other group, are closer than both errors allow; such a
-// token (about one in several hundred with a bias and spread logits) is done again in 64 bits.
-// Experts whose logits and biases are the same numbers are ties, not close calls.
+// The choice has to be that of exact scores. fp32 scores are off by a few units in their last place
+// (bounds at score_error), so a choice is settled unless two neighbours in the order of the chosen,
+// or the last kept and the first other group, are closer than both errors allow. Then 64 bits decide:
+// between the chosen and those that are as close to the last of them, one a lane, or, for groups and
+// long runs of close scores, over all experts (with a bias and spread logits about one token in 4000
+// needs the former, one in 50000 the latter). Experts whose logits and biases are the same numbers
+// are ties, not close calls.
+#include <type_traits>
+
 #include "ops_internal.h"
 
 namespace mok {
 namespace {
 
 constexpr int ROUTER_WARPS = 8;
-// blocks whose loads are added in order: not of the device, the sums' bits depend on it
-constexpr int64_t ROUTER_BLOCKS = 4 * 152;
+// Blocks of a SM by the experts a lane holds (the registers' share), and all of them: their loads are
+// added in order, so their number is not the device's (16384 x 512: 23.4 us in one wave, 26.6 in 1.3;
+// 100000 x 60: 50 us at 4 blocks a SM, 75 at 3)
+constexpr int per_sm(int held) { return held <= 4 ? 6 : held <= 8 ? 4 : held <= 16 ? 3 : held <= 32 ? 2 : 1; }
+constexpr int64_t SMS = 152;
 constexpr int MAX_E = 1024, MAX_GROUPS = 32;
 
 // order-preserving image of a float; -0 as +0. Everything, NaN of either sign too, maps above 0
 MOK_DEV uint32_t order_of(float v) {
-    uint32_t u = __float_as_uint(v);
-    if (u == 0x80000000u) u = 0u;
-    u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return u > 0u ? u : 1u;
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return max(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u), 1u);
 }
 MOK_DEV float of_order(uint32_t o) {
-    return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+    return __uint_as_float(o ^ (~(uint32_t)((int32_t)o >> 31) | 0x80000000u));
 }
 constexpr uint32_t ORDER_MASKED = 0x007FFFFFu;  // of -inf
 
@@ -52,23 +58,19 @@ struct RouterShape {
     float scale;
 };
 
-// which experts a lane holds: first, first + step, .. (n of them); its group, and place in it
+// Which experts a lane holds, VEC consecutive ones at a time: number j is first + (j / VEC) step +
+// j % VEC, for j < n (n is a multiple of VEC); and its group.
+template <int VEC>
 struct Held {
     int first, step, n, g;
     MOK_DEV Held(const RouterShape &c, int lane) {
-        if (c.G == 1) {
-            first = lane;
-            step = 32;
-            n = lane < c.E ? (c.E - lane + 31) / 32 : 0;
-            g = 0;
-        } else {
-            const int i = lane % c.lanes;
-            g = lane / c.lanes;
-            first = g * c.per + i;
-            step = c.lanes;
-            n = g < c.G && i < c.per ? (c.per - i + c.lanes - 1) / c.lanes : 0;
-        }
+        const int i = VEC * (lane % c.lanes);
+        g = lane / c.lanes;
+        first = g * c.per + i;
+        step = VEC * c.lanes;
+        n = g < c.G && i < c.per ? (c.per - i + step - 1) / step * VEC : 0;
     }
+    MOK_DEV int id(int j) const { return first + j / VEC * step + j % VEC; }
 };
 
 template <bool BF16>
@@ -76,59 +78,162 @@ MOK_DEV float load_logit(const void *row, int e) {
     return BF16 ? bf16_to_f32(static_cast<const uint16_t *>(row)[e])
                 : static_cast<const float *>(row)[e];
 }
-
-MOK_DEV float sigmoid32(float l) { return 1.0f / (1.0f + expf(-l)); }
-// e^x in softmaxes whose largest x is 0; -inf gives 0
-MOK_DEV float exp_below(float l, float top) { return expf(l - (isinf(top) ? 0.0f : top)); }
-
-// Bound of the error of an fp32 score, relative to the row's largest.
-// sigmoid: expf 2 ulp (2^-22), the sum and the quotient half an ulp each: below 2^-21.
-// softmax: expf 2^-22, its argument's rounding 2^-24 |x| e^x <= 0.37 2^-24, the sum over up to 64
-// values a lane and 5 steps across lanes 69 x 2^-24 and its terms' own 2^-22 + 7 x 2^-24, the
-// reciprocal and the product 2^-23: below 96 x 2^-24 < 2^-17.
-MOK_DEV float score_error(const RouterShape &c) {
-    return c.softmax ? 7.62939453125e-6f : 4.76837158203125e-7f;
-}
-
-// the better of two (key, id), the lower id among equals
-MOK_DEV void better(double &k, int &id, double k2, int id2) {
-    if (k2 > k || (k2 == k && id2 < id)) {
-        k = k2;
-        id = id2;
-    }
-}
-
-// The choice in 64 bits: lane k < K gets the k-th expert's id.
-template <int PER, bool BF16>
-__device__ __noinline__ int choose_exact(const RouterShape &c, const void *row, const float *bias,
-                                         int lane) {
-    const Held h(c, lane);
-    double key[PER];
-    double b1 = -INFINITY, b2 = -INFINITY;  // the lane's two largest s + bias
-    double inv = 1.0;
-    float top = -INFINITY;
-    if (c.softmax) {
-        for (int j = 0; j < h.n; ++j) top = fmaxf(top, load_logit<BF16>(row, h.first + j * h.step));
-        top = warp_max(top);
-        double den = 0.0;
-        for (int j = 0; j < h.n; ++j) {
-            const float l = load_logit<BF16>(row, h.first + j * h.step);
-            if (l > -INFINITY) den += exp((double)l - (double)top);
+// a lane's logits, -inf past its last
+template <int PER, int VEC, bool BF16>
+MOK_DEV void load_logits(const void *row, const Held<VEC> &h, float (&v)[PER]) {
+#pragma unroll
+    for (int j = 0; j < PER; j += VEC) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j + i] = -INFINITY;
+        if (j >= h.n) continue;
+        const int e = h.id(j);
+        if (VEC == 1) {
+            v[j] = load_logit<BF16>(row, e);
+        } else if (BF16) {
+            const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + e);
+            v[j] = bf16_lo(q.x);
+            v[j + VEC / 4] = bf16_hi(q.x);
+            v[j + VEC / 2] = bf16_lo(q.y);
+            v[j + VEC - 1] = bf16_hi(q.y);
+        } else {
+            const float4 q = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e);
+            v[j] = q.x;
+            v[j + VEC / 4] = q.y;
+            v[j + VEC / 2] = q.z;
+            v[j + VEC - 1] = q.w;
         }
-        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, o);
-        inv = 1.0 / den;
     }
+}
+
+// weights are exact to fp32; scores that only order experts or enter sums take the hardware's 2^x
+// and reciprocal
+MOK_DEV float sigmoid32(float l) { return 1.0f / (1.0f + expf(-l)); }
+constexpr float LOG2E_R = 1.4426950408889634f;
+MOK_DEV float exp2_hw(float x) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+    return e;
+}
+MOK_DEV float sigmoid_hw(float l) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_hw(-LOG2E_R * l)));
+    return r;
+}
+// e^x in softmaxes whose largest x is `top`; -inf gives 0
+MOK_DEV float finite_top(float top) { return isinf(top) ? 0.0f : top; }
+
+// The lane's scores of a softmax (v becomes them) and 1 / their sum's e^-top: 0 for a row of -inf
+template <int PER>
+MOK_DEV float softmax_scores(float (&v)[PER], float &top) {
+    top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) top = fmaxf(top, v[j]);
+    top = warp_max(top);
+    const float shift = finite_top(top);
+    float den = 0.0f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        v[j] = exp2_hw((v[j] - shift) * LOG2E_R);
+        den += v[j];
+    }
+    den = warp_sum(den);
+    const float inv = den > 0.0f ? 1.0f / den : den == 0.0f ? 0.0f : den;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) v[j] *= inv;
+    return inv;
+}
+
+// Bound of the error of a score of a row whose largest is `most`. u = 2^-24, x the exponent:
+//   sigmoid: 2^x is off by 4u + 1.5 |x| u of itself, which moves s by s (1 - s) times that, at most
+//     (1 + 0.34) u; the sum and the reciprocal add s (u + 2u): below 4.5 u. Where s is small that is
+//     s (7 + 1.5 |x|) u: 32 u s down to s = u, and less than 32 u^2 below
+//   softmax: 2^x by 4u + 1.5 |x| u of itself (|x| e^x <= 0.37), the sum over up to 64 values a lane
+//     and 5 steps across lanes 69 u and its terms' own 15 u, the reciprocal and product 2u: below
+//     96 u of the largest
+MOK_DEV float score_error(const RouterShape &c, float most) {
+    constexpr float u = 5.9604644775390625e-8f;
+    return c.softmax ? 96.0f * u * most : fminf(4.5f * u, 32.0f * u * (most + u));
+}
+
+// order-preserving image of a double that is no NaN, as two words
+struct Key64 {
+    uint32_t hi, lo;
+    MOK_DEV bool operator>(const Key64 &o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
+};
+MOK_DEV Key64 key64(double v) {
+    v += 0.0;  // -0 as 0
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint64_t k = (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+    return Key64{(uint32_t)(k >> 32), (uint32_t)k};
+}
+// the warp's largest, of lanes whose key is not 0
+MOK_DEV Key64 warp_max(const Key64 &k) {
+    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, k.hi);
+    return Key64{hi, __reduce_max_sync(0xFFFFFFFFu, k.hi == hi ? k.lo : 0u)};
+}
+
+// a score in 64 bits; top and den of a softmax
+MOK_DEV double score64(const RouterShape &c, float l, double top, double den) {
+    return c.softmax ? exp((double)l - top) / den : 1.0 / (1.0 + exp(-(double)l));
+}
+// the denominator of a softmax in 64 bits
+template <int VEC, bool BF16>
+MOK_DEV double denominator64(const RouterShape &c, const Held<VEC> &h, const void *row, float top) {
+    double den = 0.0;
+#pragma unroll 1
     for (int j = 0; j < h.n; ++j) {
-        const int e = h.first + j * h.step;
+        const float l = load_logit<BF16>(row, h.id(j));
+        if (l > -INFINITY) den += exp((double)l - (double)top);
+    }
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, o);
+    return den;
+}
+// what experts are ordered by in 64 bits; a masked one, or one without a number (of a logit of
+// +inf), has to be taken by someone, last
+MOK_DEV double order64(float l, double s, const float *bias, int e) {
+    const double v = bias != nullptr ? s + (double)bias[e] : (double)l;
+    return l > -INFINITY && v == v ? v : -1e300;
+}
+
+// The choice between `many` experts, one a lane: lane k < K gets the id of the k-th.
+template <int VEC, bool BF16>
+__device__ __noinline__ int choose_among(const RouterShape &c, const void *row, const float *bias,
+                                         float top, int id, int many, int lane) {
+    const Held<VEC> h(c, lane);
+    const double den = c.softmax ? denominator64<VEC, BF16>(c, h, row, top) : 1.0;
+    const float l = load_logit<BF16>(row, id);
+    Key64 k{0u, 0u};
+    if (lane < many) k = key64(order64(l, score64(c, l, (double)top, den), bias, id));
+    int rank = 0;
+    for (int o = 0; o < many; ++o) {
+        const Key64 other{__shfl_sync(0xFFFFFFFFu, k.hi, o), __shfl_sync(0xFFFFFFFFu, k.lo, o)};
+        const int oid = __shfl_sync(0xFFFFFFFFu, id, o);
+        if (other > k || (!(k > other) && oid < id)) ++rank;
+    }
+    int mine = 0;
+    for (int o = 0; o < many; ++o) {
+        const int r = __shfl_sync(0xFFFFFFFFu, rank, o), oid = __shfl_sync(0xFFFFFFFFu, id, o);
+        if (r == lane) mine = oid;
+    }
+    return mine;
+}
+
+// The choice in 64 bits from all experts: lane k < K gets the k-th expert's id.
+template <int PER, int VEC, bool BF16>
+__device__ __noinline__ int choose_exact(const RouterShape &c, const void *row, const float *bias,
+                                         float top, int lane) {
+    const Held<VEC> h(c, lane);
+    const double den = c.softmax ? denominator64<VEC, BF16>(c, h, row, top) : 1.0;
+    Key64 key[PER];
+    double b1 = -INFINITY, b2 = -INFINITY;  // the lane's two largest s + bias
+#pragma unroll 1
+    for (int j = 0; j < h.n; ++j) {
+        const int e = h.id(j);
         const float l = load_logit<BF16>(row, e);
-        const bool off = !(l > -INFINITY);
-        const double s = off         ? 0.0
-                         : c.softmax ? exp((double)l - (double)top) * inv
-                                     : 1.0 / (1.0 + exp(-(double)l));
+        const double s = score64(c, l, (double)top, den);
+        key[j] = key64(order64(l, s, bias, e));
         const double v = s + (bias != nullptr ? (double)bias[e] : 0.0);
-        // a score that is no number (of a logit of +inf) has to be taken by someone, last
-        key[j] = off || v != v ? -1e300 : bias != nullptr ? v : (double)l;
-        if (!off) {
+        if (l > -INFINITY) {
             if (v > b1) {
                 b2 = b1;
                 b1 = v;
@@ -155,23 +260,22 @@ __device__ __noinline__ int choose_exact(const RouterShape &c, const void *row, 
         kept = kept && rank < c.keep;
     }
     int mine = 0;
-    uint64_t taken = 0;  // the lane's chosen
+    uint64_t taken = kept ? 0 : ~0ull;
     for (int k = 0; k < c.K; ++k) {
-        double best = -INFINITY;
-        int id = INT32_MAX, at = 0;
-        if (kept)
-            for (int j = 0; j < h.n; ++j)
-                if (((taken >> j) & 1u) == 0 && key[j] > best) {
-                    best = key[j];
-                    id = h.first + j * h.step;
-                    at = j;
-                }
-        const int own = id;
-        for (int o = 16; o > 0; o >>= 1)
-            better(best, id, __shfl_xor_sync(0xFFFFFFFFu, best, o),
-                   __shfl_xor_sync(0xFFFFFFFFu, id, o));
-        if (own == id && id != INT32_MAX) taken |= 1ull << at;
-        if (lane == k) mine = id == INT32_MAX ? 0 : id;
+        Key64 best{0u, 0u};
+        int at = 0;
+#pragma unroll 1
+        for (int j = 0; j < h.n; ++j)
+            if (((taken >> j) & 1u) == 0 && key[j] > best) {
+                best = key[j];
+                at = j;
+            }
+        const Key64 most = warp_max(best);
+        const bool has = best.hi == most.hi && best.lo == most.lo && (best.hi | best.lo) != 0u;
+        const uint32_t cand = has ? (uint32_t)h.id(at) : 0xFFFFFFFFu;
+        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, cand);
+        if (has && cand == e) taken |= 1ull << at;
+        if (lane == k) mine = e < (uint32_t)c.E ? (int)e : 0;
     }
     return mine;
 }
@@ -182,7 +286,7 @@ __device__ __noinline__ int choose_exact(const RouterShape &c, const void *row, 
 MOK_DEV float chosen_weight(const RouterShape &c, int lane, float l, float top, float inv) {
     const bool in = lane < c.K && l > -INFINITY;
     if (!c.renorm)
-        return !in ? 0.0f : c.softmax ? exp_below(l, top) * inv : sigmoid32(l);
+        return !in ? 0.0f : c.softmax ? expf(l - finite_top(top)) * inv : sigmoid32(l);
     const float most = warp_max(in ? l : -INFINITY);
     float a = 0.0f;
     if (in) {
@@ -194,7 +298,7 @@ MOK_DEV float chosen_weight(const RouterShape &c, int lane, float l, float top, 
         }
     }
     const float total = warp_sum(a);
-    return total > 0.0f ? a / total : total == 0.0f ? 0.0f : total;
+    return total > 0.0f ? __fdividef(a, total) : total == 0.0f ? 0.0f : total;
 }
 
 struct RouterFwd {
@@ -205,12 +309,62 @@ struct RouterFwd {
     float *w;
     int32_t *count_part;  // [blocks][E], or nullptr
     float *sum_part;      // [blocks][E], or nullptr
-    int64_t chunk;        // tokens of a block
 };
 
-// PER experts a lane
-template <int PER, bool BF16>
-__global__ void __launch_bounds__(32 * ROUTER_WARPS) router_kernel(const RouterFwd a) {
+// key j, j not a constant
+template <int PER>
+MOK_DEV uint32_t key_of(const uint32_t (&key)[PER], int j) {
+    uint32_t u = 0u;
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+        if (k == j) u = key[k];
+    return u;
+}
+
+// What a lane has left to offer: its two largest keys that are not taken, with their experts.
+template <int PER, int VEC>
+struct Offer {
+    std::conditional_t<(PER > 32), uint64_t, uint32_t> taken;
+    uint32_t k0, k1;
+    int j0, j1;
+    // the two largest of what is left (at first nothing is taken)
+    MOK_DEV void look(const uint32_t (&key)[PER], bool first) {
+        k0 = k1 = 0u;
+        j0 = j1 = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const uint32_t u = !first && ((taken >> j) & 1u) != 0 ? 0u : key[j];
+            const bool best = u > k0, second = u > k1;
+            k1 = best ? k0 : second ? u : k1;
+            j1 = best ? j0 : second ? j : j1;
+            k0 = best ? u : k0;
+            j0 = best ? j : j0;
+        }
+    }
+    // the warp's next: its key (0: none left) and expert, taken where `take`
+    MOK_DEV uint32_t next(const uint32_t (&key)[PER], const Held<VEC> &h, bool take, int &e) {
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, k0);
+        const uint32_t holds = __ballot_sync(0xFFFFFFFFu, k0 == top);
+        const int mine = h.id(j0);
+        if ((holds & (holds - 1)) == 0)
+            e = __shfl_sync(0xFFFFFFFFu, mine, __ffs(holds) - 1);
+        else
+            e = (int)__reduce_min_sync(0xFFFFFFFFu, k0 == top ? (uint32_t)mine : 0xFFFFFFFFu);
+        if (take && k0 == top && e == mine) {  // k0 is not 0: as many are left as are taken
+            taken |= (decltype(taken))1 << j0;
+            k0 = k1;
+            j0 = j1;
+            k1 = 0u;
+            if (k0 == 0u) look(key, false);
+        }
+        return top;
+    }
+};
+
+// PER experts a lane. Scores are needed for the choice (SCORED: with a bias, or groups by the sum of
+// two), for the sums or for weights out of all of a softmax.
+template <int PER, int VEC, bool BF16, bool SCORED>
+__global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(const RouterFwd a) {
     extern __shared__ uint32_t router_smem[];
     const RouterShape &c = a.c;
     int32_t *hist = reinterpret_cast<int32_t *>(router_smem);            // [E]
@@ -222,64 +376,62 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS) router_kernel(const RouterF
         for (int e = threadIdx.x; e < c.E; e += blockDim.x) hist[e] = 0;
         __syncthreads();
     }
-    const Held h(c, lane);
-    const bool scored = a.bias != nullptr || (c.G > 1 && c.top == 2);  // the choice goes by scores
-    const bool row_scores = scored || a.sum_part != nullptr || (c.softmax && !c.renorm);
+    const Held<VEC> h(c, lane);
+    const bool biased = SCORED && a.bias != nullptr;
+    const bool row_scores = SCORED || a.sum_part != nullptr || (c.softmax && !c.renorm);
+    float largest_bias = 0.0f;
+    if (biased) {
+        for (int j = 0; j < h.n; ++j) largest_bias = fmaxf(largest_bias, fabsf(a.bias[h.id(j)]));
+        largest_bias = warp_max(largest_bias);
+    }
     float acc[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) acc[j] = 0.0f;
-    const int64_t t1 = (blockIdx.x + 1) * a.chunk < c.T ? (blockIdx.x + 1) * a.chunk : c.T;
-    for (int64_t t = blockIdx.x * a.chunk + warp; t < t1; t += ROUTER_WARPS) {
+    const int64_t step = (int64_t)gridDim.x * ROUTER_WARPS;
+    for (int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + warp; t < c.T; t += step) {
         const void *row = static_cast<const char *>(a.logits) + t * c.ld * (BF16 ? 2 : 4);
         float v[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            v[j] = j < h.n ? load_logit<BF16>(row, h.first + j * h.step) : -INFINITY;
+        load_logits<PER, VEC, BF16>(row, h, v);
         // scores, and what the choice goes by
         float top = -INFINITY, inv = 0.0f, most = 0.0f;
-        uint32_t key[PER];
-        float b1 = -INFINITY, b2 = -INFINITY;
+        float b1 = -INFINITY, b2 = -INFINITY;  // the lane's two largest: of s + bias, or logits
         if (row_scores) {
             float s[PER];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) s[j] = v[j];
             if (c.softmax) {
-#pragma unroll
-                for (int j = 0; j < PER; ++j) top = fmaxf(top, v[j]);
-                top = warp_max(top);
-                float den = 0.0f;
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    s[j] = exp_below(v[j], top);
-                    den += s[j];
-                }
-                den = warp_sum(den);
-                inv = den > 0.0f ? 1.0f / den : den == 0.0f ? 0.0f : den;
-#pragma unroll
-                for (int j = 0; j < PER; ++j) s[j] *= inv;
+                inv = softmax_scores(s, top);
             } else {
 #pragma unroll
-                for (int j = 0; j < PER; ++j) s[j] = sigmoid32(v[j]);
+                for (int j = 0; j < PER; ++j) s[j] = sigmoid_hw(s[j]);
             }
 #pragma unroll
             for (int j = 0; j < PER; ++j) acc[j] += s[j];
-            if (scored) {
+            if (SCORED) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j) most = fmaxf(most, s[j]);
+                most = warp_max(most);
+                if (biased) {
+                    float b[PER];
+                    load_logits<PER, VEC, false>(a.bias, h, b);
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) s[j] += b[j];
+                }
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
-                    most = fmaxf(most, s[j]);
-                    if (a.bias != nullptr && j < h.n) s[j] += a.bias[h.first + j * h.step];
                     if (v[j] == -INFINITY) s[j] = -INFINITY;
                     b2 = fmaxf(b2, fminf(b1, s[j]));
                     b1 = fmaxf(b1, s[j]);
-                    if (a.bias != nullptr) v[j] = s[j];
+                    if (biased) v[j] = s[j];
                 }
-                most = warp_max(most);
             }
         }
-        if (!scored) {
+        if (!SCORED && c.G > 1) {
 #pragma unroll
             for (int j = 0; j < PER; ++j) b1 = fmaxf(b1, v[j]);
         }
-        bool close = false, kept = h.n > 0;
-        const float err = scored ? score_error(c) * most : 0.0f;
+        const float err = SCORED ? score_error(c, most) : 0.0f, size = most + largest_bias;
+        bool exact = false, kept = h.n > 0;
         if (c.G > 1) {
             for (int o = 1; o < c.lanes; o <<= 1) {
                 const float o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
@@ -287,70 +439,83 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS) router_kernel(const RouterF
                 b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
                 b1 = fmaxf(b1, o1);
             }
-            const float score = c.top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+            const float score = SCORED && c.top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
             int rank = 0;
             for (int g = 0; g < c.G; ++g) {
                 const float other = __shfl_sync(0xFFFFFFFFu, score, g * c.lanes);
-                if (other > score || (other == score && g < h.g)) ++rank;
+                rank += other > score || (other == score && g < h.g) ? 1 : 0;
             }
             kept = kept && rank < c.keep;
-            if (scored && c.keep < c.G) {
-                // the least kept and the largest other score
+            if (SCORED && c.keep < c.G) {
+                // The least kept and the largest other score, each of at most two c, which are at most
+                // `size`: off by 2 err, the rounding of both c and of their sum, 4 x 2^-24 size
                 const uint32_t o = order_of(score);
                 const float low = of_order(__reduce_min_sync(0xFFFFFFFFu, kept ? o : 0xFFFFFFFFu));
                 const float high = of_order(__reduce_max_sync(
                     0xFFFFFFFFu, h.n > 0 && !kept ? o : ORDER_MASKED));
-                close = high > -INFINITY &&
-                        !(low - high > 4.0f * err + 4.76837158203125e-7f * fmaxf(fabsf(low), fabsf(high)));
+                exact = high > -INFINITY && !(low - high > 4.0f * err + 4.76837158203125e-7f * size);
             }
         }
+        uint32_t key[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) key[j] = kept && j < h.n ? order_of(v[j]) : 0u;
-        uint32_t best = 0u;
-        int bj = 0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (key[j] > best) {
-                best = key[j];
-                bj = j;
+        Offer<PER, VEC> left;
+        left.taken = 0;
+        left.look(key, true);
+        uint32_t sel = 0u;  // lane k: the k-th key and expert
+        int id = 0, e = 0;
+        for (int k = 0; k < c.K; ++k) {
+            const uint32_t top_key = left.next(key, h, true, e);
+            if (lane == k) {
+                sel = top_key;
+                id = e;
             }
-        uint32_t sel = 0u, next = 0u;  // lane k: the k-th key, and the one after it
-        int id = 0, next_id = 0;
-        // with a bias one round more, for the distance between the last chosen and the first left
-        const int rounds = a.bias != nullptr ? c.K + 1 : c.K;
-        for (int k = 0; k < rounds; ++k) {
-            const uint32_t most_key = __reduce_max_sync(0xFFFFFFFFu, best);
-            if (k > 0 && lane == k - 1) next = most_key;
-            if (most_key == 0u) break;  // fewer experts than rounds
-            const uint32_t cand =
-                best == most_key ? (uint32_t)(h.first + bj * h.step) : 0xFFFFFFFFu;
-            const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, cand);
-            if (k > 0 && lane == k - 1) next_id = (int)e;
-            if (lane == k && k < c.K) {
-                sel = most_key;
-                id = (int)e;
-            }
-            if (cand == e) {
-#pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    if (j == bj) key[j] = 0u;
-                best = 0u;
-                bj = 0;
-#pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    if (key[j] > best) {
-                        best = key[j];
-                        bj = j;
+        }
+        if (biased) {
+            // neighbours in the order, the first that was not chosen among them, that the scores' errors
+            // and the rounding of their sums with the bias could exchange
+            const float tol = 2.0f * err + 1.1920928955078125e-7f * size;
+            uint32_t after = __shfl_down_sync(0xFFFFFFFFu, sel, 1);
+            const uint32_t rest = __reduce_max_sync(0xFFFFFFFFu, left.k0);
+            if (lane == c.K - 1) after = rest;
+            const auto near = [&](uint32_t x, uint32_t y) {
+                return y > ORDER_MASKED && !(of_order(x) - of_order(y) > tol);
+            };
+            const auto alike = [&](int x, int y) {  // a tie, not a close call
+                return load_logit<BF16>(row, x) == load_logit<BF16>(row, y) && a.bias[x] == a.bias[y];
+            };
+            if (!exact && __any_sync(0xFFFFFFFFu, lane < c.K && near(sel, after))) {
+                // go on as long as the next is too close to the last to tell them apart
+                int many = c.K;
+                for (; many < 32; ++many) {
+                    const uint32_t last = __shfl_sync(0xFFFFFFFFu, sel, many - 1);
+                    const uint32_t rest_key = left.next(key, h, false, e);
+                    if (rest_key == 0u || !near(last, rest_key)) break;
+                    left.next(key, h, true, e);
+                    if (lane == many) {
+                        sel = rest_key;
+                        id = e;
                     }
+                }
+                after = __shfl_down_sync(0xFFFFFFFFu, sel, 1);
+                const int other = __shfl_down_sync(0xFFFFFFFFu, id, 1);
+                const bool close = lane < many - 1 && near(sel, after) && !alike(id, other);
+                if (many == 32) {  // no lane left: is any of the rest close, and no tie?
+                    const uint32_t last = __shfl_sync(0xFFFFFFFFu, sel, 31);
+                    const int of_last = __shfl_sync(0xFFFFFFFFu, id, 31);
+                    for (int j = 0; j < h.n; ++j) {
+                        const int i = h.id(j);
+                        const uint32_t u = kept && ((left.taken >> j) & 1u) == 0 ? key_of(key, j) : 0u;
+                        exact = exact || (near(last, u) && !alike(of_last, i));
+                    }
+                    exact = __any_sync(0xFFFFFFFFu, exact);
+                }
+                if (!exact && __any_sync(0xFFFFFFFFu, close))
+                    id = choose_among<VEC, BF16>(c, row, a.bias, finite_top(top), id, many, lane);
             }
         }
-        if (a.bias != nullptr && lane < c.K && next > ORDER_MASKED) {
-            const float x = of_order(sel), y = of_order(next);
-            if (!(x - y > 2.0f * err + 2.384185791015625e-7f * fmaxf(fabsf(x), fabsf(y))))
-                close = close || load_logit<BF16>(row, id) != load_logit<BF16>(row, next_id) ||
-                        a.bias[id] != a.bias[next_id];
-        }
-        if (__any_sync(0xFFFFFFFFu, close)) id = choose_exact<PER, BF16>(c, row, a.bias, lane);
+        if (SCORED && __any_sync(0xFFFFFFFFu, exact))
+            id = choose_exact<PER, VEC, BF16>(c, row, a.bias, finite_top(top), lane);
         const float l = lane < c.K ? load_logit<BF16>(row, id) : 0.0f;
         const float wt = chosen_weight(c, lane, l, top, inv);
         if (lane < c.K) {
@@ -362,7 +527,7 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS) router_kernel(const RouterF
     if (a.sum_part != nullptr) {
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-            if (j < h.n) sums[warp * c.E + h.first + j * h.step] = acc[j];
+            if (j < h.n) sums[warp * c.E + h.id(j)] = acc[j];
     }
     if (a.sum_part == nullptr && a.count_part == nullptr) return;
     __syncthreads();
@@ -378,44 +543,48 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS) router_kernel(const RouterF
     }
 }
 
-// The blocks' counts and sums, added in order: 32 experts a block, each warp a slice of the parts.
-constexpr int LOAD_SLICES = 16;
+// The blocks' counts (y = 0) and sums (y = 1), added in order: 32 experts a block, each warp a slice
+// of the parts.
+constexpr int LOAD_SLICES = 32;
+template <class V>
+MOK_DEV void add_parts(const V *part, int parts, int E, V *out, V (*sh)[32]) {
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane;
+    V s = 0;
+    // a batch of loads at a time, the last one too (an unrolled loop's rest is one after another)
+    for (int p0 = slice; p0 < parts; p0 += 20 * LOAD_SLICES) {
+        V v[20];
+#pragma unroll
+        for (int k = 0; k < 20; ++k) {
+            const int p = p0 + k * LOAD_SLICES;
+            v[k] = p < parts && e < E ? part[(int64_t)p * E + e] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 20; ++k) s += v[k];
+    }
+    sh[slice][lane] = s;
+    __syncthreads();
+    if (slice != 0 || e >= E) return;
+    s = 0;
+#pragma unroll
+    for (int k = 0; k < LOAD_SLICES; ++k) s += sh[k][lane];
+    out[e] = s;
+}
 __global__ void __launch_bounds__(32 * LOAD_SLICES)
     router_load_kernel(const int32_t *count_part, const float *sum_part, int parts, int E,
                        int32_t *counts, float *score_sum) {
-    __shared__ float fs[LOAD_SLICES][32];
-    __shared__ int32_t is[LOAD_SLICES][32];
+    __shared__ int32_t sh[LOAD_SLICES][32];
     let_next_start();
     wait_for_previous();
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int e = blockIdx.x * 32 + lane;
-    float s = 0.0f;
-    int32_t n = 0;
-    if (e < E) {
-        if (counts != nullptr)
-#pragma unroll 8
-            for (int p = slice; p < parts; p += LOAD_SLICES) n += count_part[(int64_t)p * E + e];
-        if (score_sum != nullptr)
-#pragma unroll 8
-            for (int p = slice; p < parts; p += LOAD_SLICES) s += sum_part[(int64_t)p * E + e];
+    if (blockIdx.y == 0) {
+        if (counts != nullptr) add_parts(count_part, parts, E, counts, sh);
+    } else if (score_sum != nullptr) {
+        add_parts(sum_part, parts, E, score_sum, reinterpret_cast<float(*)[32]>(sh));
     }
-    fs[slice][lane] = s;
-    is[slice][lane] = n;
-    __syncthreads();
-    if (slice != 0 || e >= E) return;
-    s = 0.0f;
-    n = 0;
-#pragma unroll
-    for (int k = 0; k < LOAD_SLICES; ++k) {
-        s += fs[k][lane];
-        n += is[k][lane];
-    }
-    if (counts != nullptr) counts[e] = n;
-    if (score_sum != nullptr) score_sum[e] = s;
 }
 
 struct RouterBwd {
-    RouterShape c;
+    RouterShape c;  // of one group: lanes hold experts of the whole row
     const void *logits;
     const int32_t *idx;
     const float *dw, *dsum;
@@ -430,109 +599,110 @@ MOK_DEV void store_logit(void *row, int e, float v) {
     else
         static_cast<float *>(row)[e] = v;
 }
+template <int PER, int VEC, bool BF16>
+MOK_DEV void store_logits(void *row, const Held<VEC> &h, const float (&v)[PER]) {
+#pragma unroll
+    for (int j = 0; j < PER; j += VEC) {
+        if (j >= h.n) continue;
+        const int e = h.id(j);
+        if (VEC == 1) {
+            store_logit<BF16>(row, e, v[j]);
+        } else if (BF16) {
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(row) + e) = make_uint2(
+                pack_bf16x2(v[j], v[j + VEC / 4]), pack_bf16x2(v[j + VEC / 2], v[j + VEC - 1]));
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(row) + e) =
+                make_float4(v[j], v[j + VEC / 4], v[j + VEC / 2], v[j + VEC - 1]);
+        }
+    }
+}
 
-// One warp per token, experts l, l + 32, .. of a lane. The row is written as if nothing were chosen,
-// then the chosen entries again, each from all that it gets, by the lane that holds it.
-template <int PER, bool BF16>
+// One warp per token at a time, walking over the tokens with the gradient of the sums in registers.
+// The row is written as if nothing were chosen, then the chosen entries again, each from all that it
+// gets, by the lane that holds it. DENSE: every logit of a row gets something.
+template <int PER, int VEC, bool BF16, bool DENSE>
 __global__ void __launch_bounds__(32 * ROUTER_WARPS) router_backward_kernel(const RouterBwd a) {
     const RouterShape &c = a.c;
     const int lane = threadIdx.x & 31;
     let_next_start();
     wait_for_previous();
-    const int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + (threadIdx.x >> 5);
-    if (t >= c.T) return;
-    const int64_t at = t * c.ld * (BF16 ? 2 : 4);
-    const void *row = static_cast<const char *>(a.logits) + at;
-    void *out = static_cast<char *>(a.dlogits) + at;
-    int id = -1;
-    float dw = 0.0f, l = -INFINITY;
-    if (lane < c.K) {
-        id = a.idx[t * c.K + lane];
-        dw = a.dw[t * c.K + lane];
-        if (id < 0 || id >= c.E) {
-            raise_status(a.status, MOK_ERR_DEVICE_INVARIANT);
-            id = -1;
-        } else {
-            l = load_logit<BF16>(row, id);
+    const Held<VEC> h(c, lane);
+    float ds[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        ds[j] = DENSE && a.dsum != nullptr && j < h.n ? a.dsum[h.id(j)] : 0.0f;
+    const int64_t step = (int64_t)gridDim.x * ROUTER_WARPS;
+    for (int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + (threadIdx.x >> 5); t < c.T; t += step) {
+        const int64_t at = t * c.ld * (BF16 ? 2 : 4);
+        const void *row = static_cast<const char *>(a.logits) + at;
+        void *out = static_cast<char *>(a.dlogits) + at;
+        float s[PER];
+        if (DENSE) load_logits<PER, VEC, BF16>(row, h, s);
+        int id = -1;
+        float dw = 0.0f, l = -INFINITY;
+        if (lane < c.K) {
+            id = a.idx[t * c.K + lane];
+            dw = a.dw[t * c.K + lane];
+            if (id < 0 || id >= c.E) {
+                raise_status(a.status, MOK_ERR_DEVICE_INVARIANT);
+                id = -1;
+            } else {
+                l = load_logit<BF16>(row, id);
+            }
         }
-    }
-    const bool dense = a.dsum != nullptr || (c.softmax && !c.renorm);
-    float s[PER];
-    float top = -INFINITY, inv = 0.0f, mean = 0.0f;  // mean: of dsum under the scores
-    if (dense) {
+        float top = -INFINITY, inv = 0.0f, mean = 0.0f;  // mean: of dsum under the scores
+        if (DENSE && c.softmax) {
+            inv = softmax_scores(s, top);
+            if (a.dsum != nullptr) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j) mean = fmaf(s[j], ds[j], mean);
+                mean = warp_sum(mean);
+            }
+        }
+        const float wt = chosen_weight(c, lane, l, top, inv);
+        // what a chosen logit gets through its weight; a masked one nothing, whatever dw holds
+        const bool live = l > -INFINITY;
+        const float m = warp_sum(live ? dw * wt : 0.0f);
+        float add = 0.0f;
+        if (live) {
+            add = c.scale * wt * (c.renorm ? dw - m : dw);
+            if (!c.softmax) add *= 1.0f / (1.0f + expf(l));  // 1 - s
+        }
+        // a softmax's chosen weights take from all
+        const float all = c.softmax && !c.renorm ? c.scale * m + mean : mean;
+        // the same id twice: the first of its lanes adds up
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, id < 0 ? -1 - lane : id);
+        if (__any_sync(0xFFFFFFFFu, (peers & (peers - 1)) != 0)) {
+            float sum = 0.0f;
+            for (int k = 0; k < 32; ++k) {
+                const float other = __shfl_sync(0xFFFFFFFFu, add, k);
+                if ((peers >> k) & 1u) sum += other;
+            }
+            add = sum;
+            if (lane != __ffs(peers) - 1) id = -1;
+        }
+        if (DENSE && id >= 0 && live) {
+            const float d = a.dsum != nullptr ? a.dsum[id] : 0.0f;
+            add += c.softmax ? expf(l - finite_top(top)) * inv * (d - all)
+                             : d * sigmoid32(l) * (1.0f / (1.0f + expf(l)));
+        }
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int e = lane + 32 * j;
-            s[j] = e < c.E ? load_logit<BF16>(row, e) : -INFINITY;
-        }
-        if (c.softmax) {
-#pragma unroll
-            for (int j = 0; j < PER; ++j) top = fmaxf(top, s[j]);
-            top = warp_max(top);
-            float den = 0.0f;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                s[j] = exp_below(s[j], top);
-                den += s[j];
+            if (!DENSE) {
+                s[j] = 0.0f;
+            } else if (c.softmax) {
+                s[j] *= ds[j] - all;
+            } else {
+                // s (1 - s) = e / (1 + e)^2, e = 2^-|x|; nothing for a masked expert
+                const float e = exp2_hw(-LOG2E_R * fabsf(s[j]));
+                s[j] = __fdividef(ds[j] * e, (1.0f + e) * (1.0f + e));
             }
-            den = warp_sum(den);
-            inv = den > 0.0f ? 1.0f / den : den == 0.0f ? 0.0f : den;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                s[j] *= inv;
-                const int e = lane + 32 * j;
-                if (a.dsum != nullptr && e < c.E) mean = fmaf(s[j], a.dsum[e], mean);
-            }
-            mean = warp_sum(mean);
         }
+        __syncwarp();  // d_logits may be logits: all of the row has been read
+        store_logits<PER, VEC, BF16>(out, h, s);
+        __syncwarp();
+        if (id >= 0) store_logit<BF16>(out, id, add);
     }
-    const float wt = chosen_weight(c, lane, l, top, inv);
-    // what a chosen logit gets through its weight; a masked one nothing, whatever dw holds
-    float add = 0.0f;
-    const bool live = l > -INFINITY;
-    const float m = warp_sum(live ? dw * wt : 0.0f);
-    if (live) {
-        if (c.softmax) {
-            add = c.scale * wt * (c.renorm ? dw - m : dw);
-        } else {
-            const float rest = 1.0f / (1.0f + expf(l));  // 1 - s
-            add = c.scale * wt * rest * (c.renorm ? dw - m : dw);
-        }
-    }
-    // a softmax's chosen weights take from all
-    const float all = c.softmax && !c.renorm ? c.scale * m + mean : mean;
-    const auto base = [&](float score, float logit, int e) {
-        if (c.softmax) return score * ((a.dsum != nullptr ? a.dsum[e] : 0.0f) - all);
-        return logit > -INFINITY ? a.dsum[e] * score * (1.0f / (1.0f + expf(logit))) : 0.0f;
-    };
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int e = lane + 32 * j;
-        if (e < c.E)
-            s[j] = !dense ? 0.0f : c.softmax ? base(s[j], 0.0f, e) : base(sigmoid32(s[j]), s[j], e);
-    }
-    // the same id twice: the first of its lanes adds up
-    const uint32_t peers = __match_any_sync(0xFFFFFFFFu, id < 0 ? -1 - lane : id);
-    if (__any_sync(0xFFFFFFFFu, (peers & (peers - 1)) != 0)) {
-        float sum = 0.0f;
-        for (int k = 0; k < 32; ++k) {
-            const float other = __shfl_sync(0xFFFFFFFFu, add, k);
-            if ((peers >> k) & 1u) sum += other;
-        }
-        add = sum;
-        if (lane != __ffs(peers) - 1) id = -1;
-    }
-    if (dense && id >= 0)
-        add += c.softmax ? (live ? base(exp_below(l, top) * inv, l, id) : 0.0f)
-                         : base(sigmoid32(l), l, id);
-    __syncwarp();  // d_logits may be logits: all of the row has been read
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int e = lane + 32 * j;
-        if (e < c.E) store_logit<BF16>(out, e, s[j]);
-    }
-    __syncwarp();
-    if (id >= 0) store_logit<BF16>(out, id, add);
 }
 
 __global__ void router_bias_kernel(const int32_t *counts, int64_t routed, int E, float rate,
@@ -545,69 +715,98 @@ __global__ void router_bias_kernel(const int32_t *counts, int64_t routed, int E,
     out[e] = bias[e] + (less > 0 ? rate : less < 0 ? -rate : 0.0f);
 }
 
-RouterShape shape_of(const mok_router_config &c) {
+RouterShape shape_of(const mok_router_config &c, int groups) {
     RouterShape s = {};
     s.T = c.T;
     s.ld = c.ld;
     s.E = c.E;
     s.K = c.K;
-    s.G = c.groups;
+    s.G = groups;
     s.keep = c.topk_groups;
     s.top = c.group_top;
-    s.per = c.E / c.groups;
+    s.per = c.E / groups;
     s.lanes = 32;
-    while (s.lanes * c.groups > 32) s.lanes /= 2;
+    while (s.lanes * groups > 32) s.lanes /= 2;
     s.softmax = c.score == MOK_SCORE_SOFTMAX;
     s.renorm = c.renormalize != 0;
     s.scale = c.scale;
     return s;
 }
 
-// experts a lane
+// experts a load (four where groups and rows allow it), experts a lane
+bool loads_four(const RouterShape &s) { return s.per % 4 == 0 && s.ld % 4 == 0; }
 int held_of(const RouterShape &s) {
-    return s.G == 1 ? (s.E + 31) / 32 : (s.per + s.lanes - 1) / s.lanes;
+    const int n = loads_four(s) ? (s.per / 4 + s.lanes - 1) / s.lanes * 4
+                                : (s.per + s.lanes - 1) / s.lanes;
+    const int sizes[] = {2, 4, 8, 16, 32};
+    for (int k : sizes)
+        if (n <= k && (k != 2 || !loads_four(s))) return k;
+    return 64;  // only with many groups: 17 of 60 experts have one lane each
+}
+int64_t blocks_of(const RouterShape &s) {
+    const int64_t n = (s.T + ROUTER_WARPS - 1) / ROUTER_WARPS, most = SMS * per_sm(held_of(s));
+    return n < most ? n : most;
 }
 
-int64_t chunk_of(int64_t T) {
-    const int64_t n = (T + ROUTER_BLOCKS - 1) / ROUTER_BLOCKS;
-    return round_up(n > 1 ? n : 1, ROUTER_WARPS);
+// f(experts a lane, experts a load) as constants
+template <class F>
+cudaError_t with_held(const RouterShape &s, F &&f) {
+    using std::integral_constant;
+    const int n = held_of(s);
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 4> four;
+#define MOK_HELD(N) \
+    if (n == N) return loads_four(s) ? f(integral_constant<int, N>{}, four) : f(integral_constant<int, N>{}, one)
+    if (n == 2) return f(integral_constant<int, 2>{}, one);
+    MOK_HELD(4);
+    MOK_HELD(8);
+    MOK_HELD(16);
+    MOK_HELD(32);
+    return loads_four(s) ? f(integral_constant<int, 64>{}, four) : f(integral_constant<int, 64>{}, one);
+#undef MOK_HELD
 }
-int64_t blocks_of(int64_t T) { return (T + chunk_of(T) - 1) / chunk_of(T); }
-
-#define MOK_ROUTER_PER(per, F, MOST)            \
-    (per <= 1    ? F(1)                         \
-     : per <= 2  ? F(2)                         \
-     : per <= 4  ? F(4)                         \
-     : per <= 8  ? F(8)                         \
-     : per <= 16 ? F(16)                        \
-     : per <= 32 ? F(32)                        \
-                 : F(MOST))
 
 cudaError_t launch_router(const RouterFwd &a, bool bf16, cudaStream_t s) {
-    const int per = held_of(a.c);
-    const unsigned grid = (unsigned)blocks_of(a.c.T);
+    const unsigned grid = (unsigned)blocks_of(a.c);
     const int smem = a.sum_part != nullptr     ? (1 + ROUTER_WARPS) * a.c.E * 4
                      : a.count_part != nullptr ? a.c.E * 4
                                                : 0;
-#define MOK_F(P)                                                                             \
-    (bf16 ? launch_edge(router_kernel<P, true>, grid, 32 * ROUTER_WARPS, smem, 1, s, a)      \
-          : launch_edge(router_kernel<P, false>, grid, 32 * ROUTER_WARPS, smem, 1, s, a))
-    return MOK_ROUTER_PER(per, MOK_F, 64);  // 17 groups of 60 experts: one lane a group
-#undef MOK_F
+    const bool scored = a.bias != nullptr || (a.c.G > 1 && a.c.top == 2);
+    return with_held(a.c, [&](auto per, auto vec) {
+        const auto go = [&](auto *kernel) {
+            return launch_edge(kernel, grid, 32 * ROUTER_WARPS, smem, 1, s, a);
+        };
+        if (scored)
+            return bf16 ? go(router_kernel<per.value, vec.value, true, true>)
+                        : go(router_kernel<per.value, vec.value, false, true>);
+        return bf16 ? go(router_kernel<per.value, vec.value, true, false>)
+                    : go(router_kernel<per.value, vec.value, false, false>);
+    });
 }
 
 cudaError_t launch_router_backward(const RouterBwd &a, bool bf16, cudaStream_t s) {
-    const int per = (a.c.E + 31) / 32;
-    const unsigned grid = (unsigned)((a.c.T + ROUTER_WARPS - 1) / ROUTER_WARPS);
-#define MOK_F(P)                                                                                  \
-    (bf16 ? launch_edge(router_backward_kernel<P, true>, grid, 32 * ROUTER_WARPS, 0, 1, s, a)     \
-          : launch_edge(router_backward_kernel<P, false>, grid, 32 * ROUTER_WARPS, 0, 1, s, a))
-    return MOK_ROUTER_PER(per, MOK_F, 32);
-#undef MOK_F
+    const int64_t blocks = (a.c.T + ROUTER_WARPS - 1) / ROUTER_WARPS;
+    const int64_t most = (int64_t)device_sm_count() * 8;
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    const bool dense = a.dsum != nullptr || (a.c.softmax && !a.c.renorm);
+    return with_held(a.c, [&](auto per, auto vec) {
+        const auto go = [&](auto *kernel) {
+            return launch_edge(kernel, grid, 32 * ROUTER_WARPS, 0, 1, s, a);
+        };
+        if constexpr (per.value > 32) {
+            return cudaErrorInvalidValue;  // one group of 1024 experts has 32 a lane
+        } else {
+            if (dense)
+                return bf16 ? go(router_backward_kernel<per.value, vec.value, true, true>)
+                            : go(router_backward_kernel<per.value, vec.value, false, true>);
+            return bf16 ? go(router_backward_kernel<per.value, vec.value, true, false>)
+                        : go(router_backward_kernel<per.value, vec.value, false, false>);
+        }
+    });
 }
 
 size_t part_bytes(const mok_router_config &c) {
-    return (size_t)round_up(blocks_of(c.T) * c.E * 4, 256);
+    return (size_t)round_up(blocks_of(shape_of(c, c.groups)) * c.E * 4, 256);
 }
 
 }  // namespace
@@ -655,16 +854,16 @@ mok_status mok_router_forward(const mok_router_config *c, const void *logits, co
     const void *ps[] = {logits, bias, topk_idx, topk_w, counts, score_sum};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    const int parts = (int)blocks_of(c->T);
+    const int parts = (int)blocks_of(shape_of(*c, c->groups));
     int32_t *cp = counts != nullptr ? (int32_t *)ws : nullptr;
     float *sp = score_sum != nullptr ? (float *)((char *)ws + part_bytes(*c)) : nullptr;
     if (c->T > 0) {
-        const RouterFwd a{shape_of(*c), logits, bias, topk_idx, topk_w, cp, sp, chunk_of(c->T)};
+        const RouterFwd a{shape_of(*c, c->groups), logits, bias, topk_idx, topk_w, cp, sp};
         MOK_OP_LAUNCH(OP_ROUTER, 1, launch_router(a, c->dtype == MOK_DTYPE_BF16, stream));
     }
     if (load)
         MOK_OP_LAUNCH(OP_ROUTER, 1,
-                      launch_edge(router_load_kernel, (unsigned)((c->E + 31) / 32), 32 * LOAD_SLICES,
+                      launch_edge(router_load_kernel, dim3((unsigned)((c->E + 31) / 32), 2), 32 * LOAD_SLICES,
                                   0, 1, stream, (const int32_t *)cp, (const float *)sp, parts, c->E,
                                   counts, score_sum));
     return MOK_OK;
@@ -682,7 +881,7 @@ mok_status mok_router_backward(const mok_router_config *c, const void *logits,
     const void *ps[] = {logits, topk_idx, d_topk_w, d_score_sum, d_logits};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    const RouterBwd a{shape_of(*c), logits, topk_idx, d_topk_w, d_score_sum, d_logits, status};
+    const RouterBwd a{shape_of(*c, 1), logits, topk_idx, d_topk_w, d_score_sum, d_logits, status};
     MOK_OP_LAUNCH(OP_ROUTER_BWD, 1, launch_router_backward(a, c->dtype == MOK_DTYPE_BF16, stream));
     return MOK_OK;
 }

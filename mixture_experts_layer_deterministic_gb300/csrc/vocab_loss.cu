@@ -125,12 +125,18 @@ __global__ void __launch_bounds__(32 * FINISH_SLICES)
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * 32 + lane;
     MaxSum a{LOWEST, 0.0f};
-    if (row < rows)
-#pragma unroll 4
-        for (int p = slice; p < parts; p += FINISH_SLICES) {
-            const float2 v = part[(int64_t)p * rows + row];
-            a.join(MaxSum{v.x, v.y});
+    // a batch of loads at a time, the last one too
+    for (int p0 = slice; p0 < parts; p0 += 8 * FINISH_SLICES) {
+        float2 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int p = p0 + k * FINISH_SLICES;
+            v[k] = make_float2(LOWEST, 0.0f);
+            if (p < parts && row < rows) v[k] = part[(int64_t)p * rows + row];
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a.join(MaxSum{v[k].x, v[k].y});
+    }
     sh[slice][lane] = make_float2(a.m, a.s);
     __syncthreads();
     if (slice != 0 || row >= rows) return;
