@@ -1306,21 +1306,35 @@ mok_status check_linear(const mok_linear_config *c, const int32_t *starts, const
     return MOK_OK;
 }
 
+mok_linear_config dense_config(int64_t rows, int N, int Kin) {
+    mok_linear_config c = {};
+    c.groups = 1;
+    c.rows = rows;
+    c.in_features = Kin;
+    c.out_features = N;
+    return c;
+}
+
 template <bool F, bool CUT>
-cudaError_t dense_grads(const DenseGrads &a, const KParts &kp, const CUtensorMap &xa,
-                        const CUtensorMap &xb, const CUtensorMap &wa, const CUtensorMap &wb,
-                        int *status, cudaStream_t s) {
+cudaError_t dense_grads(const DenseGrads &a, const Cut &xc, const KParts &xk, const Cut &wc,
+                        const KParts &wk, const CUtensorMap &xa, const CUtensorMap &xb,
+                        const CUtensorMap &wa, const CUtensorMap &wb, int *status, int *launches,
+                        cudaStream_t s) {
     const int n_kb = (a.Kin + 255) / 256, n_nb = (a.N + 255) / 256;
     int64_t clocks, split = 0, pairs = 0;
-    const Tiles tiles = dense_tiles(a.rows, dense_height(a.rows, n_kb, sm_pairs(), &clocks));
-    const Dx<F, CUT> px{tiles, n_kb, a.halves, a.Kin, a.N, a.ld_x, a.dx, status, kp};
+    const Tiles tiles = dense_tiles(
+        a.rows, xc.parts > 1 ? xc.height : dense_height(a.rows, n_kb, sm_pairs(), &clocks));
+    const Dx<F, CUT> px{tiles, n_kb, a.halves, a.Kin, a.N, a.ld_x, a.dx, status, xk};
     const Dw<F, CUT> pw{nullptr, nullptr, a.rows, 1, n_kb, n_nb, a.halves, a.Kin, a.N, a.ld_w, a.dw,
-                        status, DbArgs{nullptr, nullptr, 0, nullptr},
-                        KParts{1, 0, nullptr, 0, 0, false}};
-    const int64_t x_units = a.dx ? tiles.cap * n_kb : 0, w_units = a.dw ? (int64_t)n_kb * n_nb : 0;
+                        status, DbArgs{nullptr, nullptr, 0, nullptr}, wk};
+    const int64_t x_units = a.dx ? tiles.cap * n_kb * xc.parts : 0;
+    const int64_t w_units = a.dw ? (int64_t)n_kb * n_nb * wc.parts : 0;
     if (a.dx && a.dw)
-        plan_both(w_units, unit_clocks((a.rows + 63) / 64 * a.halves, LTILE), x_units,
-                  unit_clocks((a.N + 63) / 64 * a.halves, tiles.height), &split, &pairs);
+        plan_both(w_units, unit_clocks((wc.parts > 1 ? wc.per : (a.rows + 63) / 64) * a.halves, LTILE),
+                  x_units,
+                  unit_clocks((xc.parts > 1 ? xc.per : (a.N + 63) / 64) * a.halves, tiles.height),
+                  &split, &pairs);
+    *launches = split > 0 ? 1 : (a.dx != nullptr) + (a.dw != nullptr);
     if (split > 0) return launch_both(wa, wb, pw, xa, xb, px, split, pairs, s);
     cudaError_t e = cudaSuccess;
     if (a.dx) e = launch_linear(xa, xb, px, x_units, s);
@@ -1330,7 +1344,13 @@ cudaError_t dense_grads(const DenseGrads &a, const KParts &kp, const CUtensorMap
 
 }  // namespace
 
-cudaError_t launch_dense_grads(const DenseGrads &a, int *status, cudaStream_t s) {
+size_t dense_grads_bytes(int64_t rows, int N, int Kin) {
+    Cut x, w;
+    backward_cuts(dense_config(rows, N, Kin), &x, &w);
+    return (size_t)round_up((int64_t)part_bytes(x, rows, Kin), 256) + part_bytes(w, N, Kin);
+}
+
+cudaError_t launch_dense_grads(const DenseGrads &a, int *status, int *launches, cudaStream_t s) {
     cudaError_t e = init_host();
     if (e != cudaSuccess) return e;
     CUtensorMap xa = {}, xb = {}, wa = {}, wb = {};
@@ -1344,13 +1364,24 @@ cudaError_t launch_dense_grads(const DenseGrads &a, int *status, cudaStream_t s)
     if (a.dw && ((e = map2d(&wa, a.x, a.rows, a.Kin, a.ld_x, 64)) != cudaSuccess ||
                  (e = map_dz(&wb, 64)) != cudaSuccess))
         return e;
-    const KParts kp{1, 0, a.dx_sum, round_up(a.Kin, 4), 0, a.add};
-    const bool cut = a.dx_sum != nullptr || a.add;
-    if (a.f32)
-        return cut ? dense_grads<true, true>(a, kp, xa, xb, wa, wb, status, s)
-                   : dense_grads<true, false>(a, kp, xa, xb, wa, wb, status, s);
-    return cut ? dense_grads<false, true>(a, kp, xa, xb, wa, wb, status, s)
-               : dense_grads<false, false>(a, kp, xa, xb, wa, wb, status, s);
+    Cut xc{1, 0, 0}, wc{1, 0, 0};
+    if (a.ws != nullptr) backward_cuts(dense_config(a.rows, a.N, a.Kin), &xc, &wc);
+    float *parts = static_cast<float *>(a.ws);
+    KParts xk = k_parts(xc, parts, a.rows, a.Kin);
+    const KParts wk = k_parts(
+        wc, parts + round_up((int64_t)part_bytes(xc, a.rows, a.Kin), 256) / 4, a.N, a.Kin);
+    if (a.dx_sum != nullptr || a.add) xk = KParts{1, 0, a.dx_sum, round_up(a.Kin, 4), 0, a.add};
+    const bool cut = xk.out != nullptr || xk.add || wk.out != nullptr;
+    e = (a.f32 ? (cut ? dense_grads<true, true> : dense_grads<true, false>)
+               : (cut ? dense_grads<false, true> : dense_grads<false, false>))(
+        a, xc, xk, wc, wk, xa, xb, wa, wb, status, launches, s);
+    if (e != cudaSuccess) return e;
+    JoinArgs j = {};
+    int n = 0;
+    if (a.dx && xc.parts > 1) j.o[n++] = join_out(xk, a.rows, a.Kin, a.dx, a.ld_x);
+    if (a.dw && wc.parts > 1) j.o[n++] = join_out(wk, a.N, a.Kin, a.dw, a.ld_w);
+    *launches += n > 0;
+    return n > 0 ? launch_join(a.f32, j, s) : cudaSuccess;
 }
 
 }  // namespace mok

@@ -6,7 +6,11 @@
 //   A_MN, B_MN     operands that lie along M or N in memory (else along K)
 //   n_units(), unit(u), segments(unit), geom(unit, segment, rank), tx(geom), load(...), epilogue(...)
 //   long_steps(unit), side_work(...)
+// and, where a warp keeps more than a unit's sums from unit to unit:
+//   State, start(state), finish(state, cluster, rank, ...)
 #pragma once
+
+#include <type_traits>
 
 #include "gemm_tc_core.cuh"
 #include "ops_internal.h"
@@ -406,6 +410,18 @@ MOK_DEV void lin_drain(uint64_t *bar, uint32_t parity) {
     }
 }
 
+// what an epilogue warp of P keeps
+template <class P, class = void>
+struct StateOf {
+    using Type = Carry<P::SUMS>;
+    static constexpr bool LASTS = false;
+};
+template <class P>
+struct StateOf<P, std::void_t<typename P::State>> {
+    using Type = typename P::State;
+    static constexpr bool LASTS = true;
+};
+
 // the kernel's work on the units cid, cid + ncl, ... of p, as one CTA of a pair
 template <class P>
 MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P &p,
@@ -564,7 +580,8 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
         const int pair = 2 * hw + (q >> 1);
         Patches pt{tc::smem_u32(base + NS * SB) + (uint32_t)(pair * PATCHES * PATCH_BYTES),
                    1 + pair, q & 1, lane, 0};
-        Carry<P::SUMS> carry;
+        typename StateOf<P>::Type carry;
+        if constexpr (StateOf<P>::LASTS) p.start(carry);
         int64_t a = 0;
         bool ok = true;
         for (uint32_t u = cid; u < n_units && ok; u += ncl) {
@@ -584,6 +601,8 @@ MOK_DEV void linear_body(const CUtensorMap &tmA, const CUtensorMap &tmB, const P
                 if (lane == 0) lin_arrive(empty0 + (uint32_t)ab * 8u);
             }
         }
+        if constexpr (StateOf<P>::LASTS)
+            if (ok) p.finish(carry, cid, rank, q, hw, lane);
     }
 
     // no MMA, copy or arrival of either CTA targets the other past this point
@@ -663,15 +682,15 @@ cudaError_t launch_pairs(void (*kernel)(KA...), std::atomic<uint64_t> &attr_set,
     return launch_edge(kernel, dim3((unsigned)(2 * pairs)), threads, LIN_SMEM, 2, s, args...);
 }
 
-// one cluster per unit, at most the pairs of SMs that run at once
+// one cluster per unit, at most `most` (the pairs of SMs that run at once)
 template <class P>
 cudaError_t launch_linear(const CUtensorMap &ma, const CUtensorMap &mb, const P &p,
-                          int64_t units_cap, cudaStream_t s) {
+                          int64_t units_cap, cudaStream_t s, int64_t most = sm_pairs()) {
     if (units_cap < 1) return cudaSuccess;
     if (units_cap > 0x7FFFFFFF) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> attr_set{0};
     return launch_pairs(linear_kernel<P>, attr_set, P::E::THREADS,
-                        units_cap < sm_pairs() ? units_cap : sm_pairs(), s, ma, mb, p);
+                        units_cap < most ? units_cap : most, s, ma, mb, p);
 }
 template <class P, class Q>
 cudaError_t launch_both(const CUtensorMap &pa, const CUtensorMap &pb, const P &p,

@@ -34,8 +34,11 @@ struct DenseGrads {
     // nullptr where dx is fp32 itself), and adds to it from the second piece on
     float *dx_sum;
     bool add;
+    void *ws;                    // dense_grads_bytes; nullptr: K is not cut into parts (see linear.cu)
 };
-cudaError_t launch_dense_grads(const DenseGrads &a, int *status, cudaStream_t s);
+size_t dense_grads_bytes(int64_t rows, int N, int Kin);
+// *launches: how many it took
+cudaError_t launch_dense_grads(const DenseGrads &a, int *status, int *launches, cudaStream_t s);
 
 #ifdef __CUDACC__
 // The operators' launches overlap at their edges: a kernel may be started while the one before it

@@ -11,10 +11,10 @@
 //
 // The choice has to be that of exact scores. fp32 scores are off by a few units in their last place
 // (bounds at score_error), so a choice is settled unless two neighbours in the order of the chosen,
-// or the last kept and the first other group, are closer than both errors allow. Then 64 bits decide:
-// between the chosen and those that are as close to the last of them, one a lane, or, for groups and
-// long runs of close scores, over all experts (with a bias and spread logits about one token in 4000
-// needs the former, one in 50000 the latter). Experts whose logits and biases are the same numbers
+// or the last kept and the first other group, are closer than both errors allow. Then 64 bits decide,
+// between the experts and groups in question alone, one a lane (64-bit arithmetic is slow here, and
+// a launch waits for its slowest token); with a bias and spread logits that is about one token in
+// 4000. Only runs of more than 32 close scores take all experts. Experts whose logits and biases are the same numbers
 // are ties, not close calls.
 #include <type_traits>
 
@@ -143,6 +143,12 @@ MOK_DEV float softmax_scores(float (&v)[PER], float &top) {
     return inv;
 }
 
+// a score as the choice takes it; -inf for a masked expert
+MOK_DEV float unbiased_score(const RouterShape &c, float l, float top, float inv) {
+    if (l == -INFINITY) return l;
+    return c.softmax ? exp2_hw((l - finite_top(top)) * LOG2E_R) * inv : sigmoid_hw(l);
+}
+
 // Bound of the error of a score of a row whose largest is `most`. u = 2^-24, x the exponent:
 //   sigmoid: 2^x is off by 4u + 1.5 |x| u of itself, which moves s by s (1 - s) times that, at most
 //     (1 + 0.34) u; the sum and the reciprocal add s (u + 2u): below 4.5 u. Where s is small that is
@@ -218,46 +224,18 @@ __device__ __noinline__ int choose_among(const RouterShape &c, const void *row, 
     return mine;
 }
 
-// The choice in 64 bits from all experts: lane k < K gets the k-th expert's id.
+// The choice in 64 bits from all experts of the kept groups: lane k < K gets the k-th expert's id.
 template <int PER, int VEC, bool BF16>
 __device__ __noinline__ int choose_exact(const RouterShape &c, const void *row, const float *bias,
-                                         float top, int lane) {
+                                         float top, bool kept, int lane) {
     const Held<VEC> h(c, lane);
     const double den = c.softmax ? denominator64<VEC, BF16>(c, h, row, top) : 1.0;
     Key64 key[PER];
-    double b1 = -INFINITY, b2 = -INFINITY;  // the lane's two largest s + bias
 #pragma unroll 1
     for (int j = 0; j < h.n; ++j) {
         const int e = h.id(j);
         const float l = load_logit<BF16>(row, e);
-        const double s = score64(c, l, (double)top, den);
-        key[j] = key64(order64(l, s, bias, e));
-        const double v = s + (bias != nullptr ? (double)bias[e] : 0.0);
-        if (l > -INFINITY) {
-            if (v > b1) {
-                b2 = b1;
-                b1 = v;
-            } else if (v > b2) {
-                b2 = v;
-            }
-        }
-    }
-    bool kept = h.n > 0;
-    if (c.G > 1) {
-        for (int o = 1; o < c.lanes; o <<= 1) {
-            const double o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
-            const double o2 = __shfl_xor_sync(0xFFFFFFFFu, b2, o);
-            const double lo = b1 < o1 ? b1 : o1, hi = b2 > o2 ? b2 : o2;
-            b1 = b1 > o1 ? b1 : o1;
-            b2 = lo > hi ? lo : hi;
-        }
-        const double score = c.top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
-        int rank = 0;
-        for (int g = 0; g < c.G; ++g) {
-            const double other = __shfl_sync(0xFFFFFFFFu, score, g * c.lanes);
-            if (other > score || (other == score && g < h.g)) ++rank;
-        }
-        kept = kept && rank < c.keep;
+        key[j] = key64(order64(l, score64(c, l, (double)top, den), bias, e));
     }
     int mine = 0;
     uint64_t taken = kept ? 0 : ~0ull;
@@ -278,6 +256,48 @@ __device__ __noinline__ int choose_exact(const RouterShape &c, const void *row, 
         if (lane == k) mine = e < (uint32_t)c.E ? (int)e : 0;
     }
     return mine;
+}
+
+// Which groups are kept, in 64 bits, among those too close to the border to tell: `among` of them take
+// what the others leave. cand: the experts of a lane that may be one of its group's two largest. True
+// for the lanes of a group that is kept.
+template <int VEC, bool BF16>
+__device__ __noinline__ bool keep_exact(const RouterShape &c, const void *row, const float *bias,
+                                        float top, bool among, uint64_t cand, int left, int lane) {
+    const Held<VEC> h(c, lane);
+    const double den = c.softmax ? denominator64<VEC, BF16>(c, h, row, top) : 1.0;
+    double b1 = -INFINITY, b2 = -INFINITY;
+    if (!among) cand = 0;
+    while (__any_sync(0xFFFFFFFFu, cand != 0)) {  // one a lane at a time, most often one in all
+        if (cand == 0) continue;
+        const int e = h.id(__ffsll((long long)cand) - 1);
+        cand &= cand - 1;
+        const float l = load_logit<BF16>(row, e);
+        if (!(l > -INFINITY)) continue;
+        const double v = score64(c, l, (double)top, den) + (bias != nullptr ? (double)bias[e] : 0.0);
+        if (v > b1) {
+            b2 = b1;
+            b1 = v;
+        } else if (v > b2) {
+            b2 = v;
+        }
+    }
+    for (int o = 1; o < c.lanes; o <<= 1) {
+        const double o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
+        const double o2 = __shfl_xor_sync(0xFFFFFFFFu, b2, o);
+        const double lo = b1 < o1 ? b1 : o1, hi = b2 > o2 ? b2 : o2;
+        b1 = b1 > o1 ? b1 : o1;
+        b2 = lo > hi ? lo : hi;
+    }
+    const Key64 mine = key64(c.top == 2 && b2 > -INFINITY ? b1 + b2 : b1);
+    int rank = 0;
+    for (int g = 0; g < c.G; ++g) {
+        const int from = g * c.lanes;
+        const Key64 other{__shfl_sync(0xFFFFFFFFu, mine.hi, from), __shfl_sync(0xFFFFFFFFu, mine.lo, from)};
+        const bool in = __shfl_sync(0xFFFFFFFFu, (int)among, from) != 0;
+        if (in && (other > mine || (!(mine > other) && g < h.g))) ++rank;
+    }
+    return among && rank < left;
 }
 
 // Unscaled weight of a chosen logit among the K chosen (lane k < K holds the k-th): its score, or
@@ -431,7 +451,7 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
             for (int j = 0; j < PER; ++j) b1 = fmaxf(b1, v[j]);
         }
         const float err = SCORED ? score_error(c, most) : 0.0f, size = most + largest_bias;
-        bool exact = false, kept = h.n > 0;
+        bool kept = h.n > 0;
         if (c.G > 1) {
             for (int o = 1; o < c.lanes; o <<= 1) {
                 const float o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
@@ -449,11 +469,25 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
             if (SCORED && c.keep < c.G) {
                 // The least kept and the largest other score, each of at most two c, which are at most
                 // `size`: off by 2 err, the rounding of both c and of their sum, 4 x 2^-24 size
+                const float tol = 4.0f * err + 4.76837158203125e-7f * size;
                 const uint32_t o = order_of(score);
                 const float low = of_order(__reduce_min_sync(0xFFFFFFFFu, kept ? o : 0xFFFFFFFFu));
                 const float high = of_order(__reduce_max_sync(
                     0xFFFFFFFFu, h.n > 0 && !kept ? o : ORDER_MASKED));
-                exact = high > -INFINITY && !(low - high > 4.0f * err + 4.76837158203125e-7f * size);
+                if (high > -INFINITY && !(low - high > tol)) {
+                    // groups that clearly lie on their side of the border stay there
+                    const bool among = h.n > 0 && (kept ? !(score - high > tol) : !(low - score > tol));
+                    const uint32_t sure = __ballot_sync(0xFFFFFFFFu, kept && !among && lane % c.lanes == 0);
+                    uint64_t cand = 0;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const float s = biased ? v[j] : unbiased_score(c, v[j], top, inv);
+                        if (j < h.n && !((c.top == 2 ? b2 : b1) - s > tol)) cand |= 1ull << j;
+                    }
+                    const bool now = keep_exact<VEC, BF16>(c, row, a.bias, finite_top(top), among, cand,
+                                                           c.keep - __popc(sure), lane);
+                    kept = among ? now : kept;
+                }
             }
         }
         uint32_t key[PER];
@@ -471,6 +505,7 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
                 id = e;
             }
         }
+        bool exact = false;
         if (biased) {
             // neighbours in the order, the first that was not chosen among them, that the scores' errors
             // and the rounding of their sums with the bias could exchange
@@ -484,7 +519,7 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
             const auto alike = [&](int x, int y) {  // a tie, not a close call
                 return load_logit<BF16>(row, x) == load_logit<BF16>(row, y) && a.bias[x] == a.bias[y];
             };
-            if (!exact && __any_sync(0xFFFFFFFFu, lane < c.K && near(sel, after))) {
+            if (__any_sync(0xFFFFFFFFu, lane < c.K && near(sel, after))) {
                 // go on as long as the next is too close to the last to tell them apart
                 int many = c.K;
                 for (; many < 32; ++many) {
@@ -515,7 +550,7 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
             }
         }
         if (SCORED && __any_sync(0xFFFFFFFFu, exact))
-            id = choose_exact<PER, VEC, BF16>(c, row, a.bias, finite_top(top), lane);
+            id = choose_exact<PER, VEC, BF16>(c, row, a.bias, finite_top(top), kept, lane);
         const float l = lane < c.K ? load_logit<BF16>(row, id) : 0.0f;
         const float wt = chosen_weight(c, lane, l, top, inv);
         if (lane < c.K) {

@@ -10,6 +10,9 @@
 //             exponentials of its row's columns without talking to others; each tile of 256 vocabulary
 //             entries leaves a (maximum, sum) per row and warp, and a second kernel joins them in
 //             order.
+//   VocabFew  a few rows: A = W, B = x, so no tile is mostly padding (with 4 rows of x on M an SM
+//             writes as many zeros to shared memory as it loads of W). A lane is a vocabulary
+//             entry and keeps each row's maximum and sum from tile to tile; lanes are joined at the end.
 //   VocabDl   A = W, B = x, as the linear layer's forward, with dl for an epilogue: bf16 rows of a
 //             piece of the vocabulary in the workspace.
 //   dx, dW    the linear layer's gradient products, with dl for dz.
@@ -114,40 +117,133 @@ struct VocabFwd {
     }
 };
 
-// A block joins the parts of 32 rows, each warp a slice of them, then the slices in order.
-constexpr int FINISH_SLICES = 32;
-__global__ void __launch_bounds__(32 * FINISH_SLICES)
-    vocab_finish_kernel(const float2 *part, const float *hit, int64_t rows, int parts, int V,
-                        const int32_t *targets, float z, float *loss, float *lse, int *status) {
-    __shared__ float2 sh[FINISH_SLICES][32];
+// up to 64 rows: a warp takes 16 of them, four warps a TMEM lane quadrant
+constexpr int FEW_ROWS = 64;
+struct VocabFew {
+    using E = Epi<true>;
+    static constexpr bool F32_OUT = true, A_MN = false, B_MN = false;
+    struct State {
+        float v[16];      // the segments of H so far
+        MaxSum a[16];
+    };
+    int rows, n_vt;
+    int segs;
+    int H, V;
+    const int32_t *targets;
+    float2 *part;     // [8 clusters][rows]
+    float *hit;
+    int *status;
+
+    MOK_DEV int64_t n_units() const { return n_vt; }
+    MOK_DEV void side_work(uint32_t, uint32_t, int) const {}
+    MOK_DEV Unit unit(uint32_t u) const { return Unit{0, 0, rows, 0, (int)u, 0, 0}; }
+    MOK_DEV int segments(const Unit &) const { return segs; }
+    MOK_DEV int long_steps(const Unit &) const { return 0; }
+    MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
+        LinGeom q;
+        q.n_mma = (rows + 15) & ~15;
+        q.a0 = seg * SEG_K;
+        q.a1 = u.mb * 256 + (int)rank * 128;
+        q.a2 = 0;
+        q.b0 = q.a0;
+        q.b1 = (int)rank * (q.n_mma / 2);
+        q.nbox = (q.n_mma / 2 + 31) / 32;
+        const int k = H - q.a0 > SEG_K ? SEG_K : H - q.a0;
+        q.k_steps = (k + 15) / 16;
+        q.k_first = q.half = 0;
+        return q;
+    }
+    MOK_DEV uint32_t tx(const LinGeom &q) const { return 2 * BOX + q.nbox * (BOX / 2); }
+    MOK_DEV void load(uint8_t *st, uint32_t fb, const LinGeom &q, int k0, const CUtensorMap *tmA,
+                      const CUtensorMap *tmB) const {
+        tma_load_3d_pair(st, tmA, fb, q.a0 + k0, q.a1, q.a2);
+        for (int j = 0; j < q.nbox; ++j)
+            tc::tma_load_2d_pair(st + 2 * BOX + j * (BOX / 2), tmB, fb, q.b0 + k0, q.b1 + 32 * j);
+    }
+    MOK_DEV void start(State &k) const {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) k.a[j] = MaxSum{LOWEST, 0.0f};
+    }
+    MOK_DEV void epilogue(const Unit &u, int seg, bool last, uint32_t rank, uint32_t c, int q, int hw,
+                          int lane, Patches &, State &k) const {
+        const int r0 = 16 * hw;
+        if (r0 >= rows) return;
+        float v[16];
+        tc::tmem_ld16(c + r0, v);
+        tc::tmem_ld_wait();
+        loaded(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) k.v[j] = seg > 0 ? k.v[j] + v[j] : v[j];
+        const int f = u.mb * 256 + (int)rank * 128 + q * 32 + lane;
+        if (!last || f >= V) return;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (r0 + j >= rows) continue;
+            MaxSum &a = k.a[j];
+            const float t = fmaxf(a.m, k.v[j]);
+            a.s = a.s * exp2_hw((a.m - t) * LOG2E_F) + exp2_hw((k.v[j] - t) * LOG2E_F);
+            a.m = t;
+            if (targets[r0 + j] == f) hit[r0 + j] = k.v[j];
+        }
+    }
+    MOK_DEV void finish(State &k, uint32_t cluster, uint32_t rank, int q, int hw, int lane) const {
+        const int r0 = 16 * hw;
+        if (r0 >= rows) return;
+        const int64_t p = (int64_t)(cluster * 2 + rank) * 4 + q;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            MaxSum a = k.a[j];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                a.join(MaxSum{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o)});
+            if (lane == 0 && r0 + j < rows) part[p * rows + r0 + j] = make_float2(a.m, a.s);
+        }
+    }
+};
+
+// A block joins the parts of up to 32 rows: `across` lanes (a power of two) on rows, the other lanes and
+// the warps on slices of the parts (with one row a part a lane), then lanes and warps by halves.
+constexpr int FINISH_WARPS = 32;
+__global__ void __launch_bounds__(32 * FINISH_WARPS)
+    vocab_finish_kernel(const float2 *part, const float *hit, int64_t rows, int across, int parts,
+                        int V, const int32_t *targets, float z, float *loss, float *lse, int *status) {
+    __shared__ float2 sh[FINISH_WARPS][32];
     let_next_start();
     wait_for_previous();
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row0 = (int64_t)blockIdx.x * across, row = row0 + lane % across;
+    const int slices = FINISH_WARPS * (32 / across);
     MaxSum a{LOWEST, 0.0f};
     // a batch of loads at a time, the last one too
-    for (int p0 = slice; p0 < parts; p0 += 8 * FINISH_SLICES) {
+    for (int p0 = warp * (32 / across) + lane / across; p0 < parts; p0 += 8 * slices) {
         float2 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int p = p0 + k * FINISH_SLICES;
+            const int p = p0 + k * slices;
             v[k] = make_float2(LOWEST, 0.0f);
             if (p < parts && row < rows) v[k] = part[(int64_t)p * rows + row];
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) a.join(MaxSum{v[k].x, v[k].y});
     }
-    sh[slice][lane] = make_float2(a.m, a.s);
+    for (int o = 16; o >= across; o >>= 1)
+        a.join(MaxSum{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o)});
+    sh[warp][lane] = make_float2(a.m, a.s);
     __syncthreads();
-    if (slice != 0 || row >= rows) return;
+    // warp w joins the warps' values of row w
+    const int64_t r = row0 + warp;
+    if (warp >= across || r >= rows) return;
+    a = MaxSum{sh[lane][warp].x, sh[lane][warp].y};
 #pragma unroll
-    for (int k = 1; k < FINISH_SLICES; ++k) a.join(MaxSum{sh[k][lane].x, sh[k][lane].y});
+    for (int o = 16; o > 0; o >>= 1)
+        a.join(MaxSum{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o)});
+    if (lane != 0) return;
     const float l = a.m + log2f(a.s) * LN2_F;
-    lse[row] = l;
+    lse[r] = l;
     if (loss == nullptr) return;
-    const int t = targets[row];
+    const int t = targets[r];
     if (t >= V) raise_status(status, MOK_ERR_DEVICE_INVARIANT);
-    loss[row] = t >= 0 && t < V ? (l - hit[row]) + z * l * l : 0.0f;
+    loss[r] = t >= 0 && t < V ? (l - hit[r]) + z * l * l : 0.0f;
 }
 
 // ---------------------------------------------------------------- backward
@@ -182,13 +278,16 @@ MOK_DEV float dl_of(const RowGrad &g, float l, int v) {
 // and 1.2e-6 with three, plain fp32 products 1.3e-6.
 constexpr int PLANES = 3;
 
-// The gradient of the logits for vocabulary entries [v0, v0 + N), in bf16 (F32: in planes, from logits
-// whose segments of H were added in fp32).
-template <bool F32>
+// The gradient of the logits for vocabulary entries [v0, v0 + N), in N_PLANES planes of bf16. SEGS: of
+// logits whose segments of H were added in fp32 (for planes where H is long). Row tiles come first:
+// a band of 4096 rows of x stays in L2 while W passes by once (the other way round W passes by for
+// every tile, 4096 rows, 4096 x 65536: 1450 against 1200 us under the profiler).
+template <int N_PLANES, bool SEGS>
 struct VocabDl {
-    using E = Epi<F32>;
-    static constexpr bool F32_OUT = F32, SUMS = F32, A_MN = false, B_MN = false;
+    using E = Epi<SEGS>;
+    static constexpr bool F32_OUT = SEGS, SUMS = SEGS, A_MN = false, B_MN = false;
     Tiles tiles;
+    int band;        // tiles that take a block of W one after another
     int n_mb;        // ceil(N / 256)
     int segs;
     int H, v0, N;
@@ -200,8 +299,10 @@ struct VocabDl {
     MOK_DEV int64_t n_units() const { return tiles.count() * n_mb; }
     MOK_DEV void side_work(uint32_t, uint32_t, int) const {}
     MOK_DEV Unit unit(uint32_t u) const {
-        const int4 t = tiles.get(u / (uint32_t)n_mb);
-        return Unit{0, t.y, t.z - t.y, 0, (int)(u % (uint32_t)n_mb), 0, 0};
+        const uint32_t per = (uint32_t)band * (uint32_t)n_mb, b = u / per, rest = u - b * per;
+        const uint32_t left = (uint32_t)tiles.cap - b * band, nt = left < (uint32_t)band ? left : band;
+        const int4 t = tiles.get(b * band + rest % nt);
+        return Unit{0, t.y, t.z - t.y, 0, (int)(rest / nt), 0, 0};
     }
     MOK_DEV int segments(const Unit &) const { return segs; }
     MOK_DEV int long_steps(const Unit &) const { return 0; }
@@ -230,7 +331,7 @@ struct VocabDl {
                           int lane, Patches &pt, Carry<SUMS> &carry) const {
         const int64_t r0 = u.r0;
         const int f0 = u.mb * 256 + (int)rank * 128 + q * 32;  // the warp's entries of the piece
-        if constexpr (F32) {
+        if constexpr (SEGS) {
             const int f = f0 + lane;
             sum_segments(c, hw, u.nr, seg == 0, last, carry, [&](int n0, const float (&v)[16]) {
                 if (f >= N) return;
@@ -240,7 +341,7 @@ struct VocabDl {
                     if (n0 + j >= u.nr) continue;
                     float g = dl_of(rows[r0 + n0 + j], v[j], v0 + f);
 #pragma unroll
-                    for (int k = 0; k < PLANES; ++k) {
+                    for (int k = 0; k < N_PLANES; ++k) {
                         const uint16_t b = f32_to_bf16(g);
                         p[k * plane + j * ld] = b;
                         g = isfinite(bf16_to_f32(b)) ? g - bf16_to_f32(b) : 0.0f;
@@ -249,10 +350,11 @@ struct VocabDl {
             });
         } else {
             for (int n0 = 32 * hw; n0 < u.nr; n0 += E::STEP) {
-#pragma unroll 2
+                float v[4][2][4];
+#pragma unroll(N_PLANES > 1 ? 4 : 2)
                 for (int b = 0; b < 4; ++b) {
-                    float v[2][4];
-                    ld_pairs8(c + n0 + 8 * b, v);
+                    float w[2][4];
+                    ld_pairs8(c + n0 + 8 * b, w);
                     RowGrad g[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -263,11 +365,28 @@ struct VocabDl {
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            v[h][i] = dl_of(g[i & 1], v[h][i],
+                            w[h][i] = dl_of(g[i & 1], w[h][i],
                                             v0 + f0 + 16 * h + 8 * (i >> 1) + (lane >> 2));
-                    patch_write8(pt.patch(), pt.half, b, v, lane);
+                    patch_write8(pt.patch(), pt.half, b, w, lane);
+                    if (N_PLANES > 1)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[b][i >> 2][i & 3] = w[i >> 2][i & 3];
                 }
                 pt.store(OutRef{dl, tiles.rows, ld, N}, f0 & ~63, r0 + n0, r0 + u.nr, 0);
+#pragma unroll
+                for (int k = 1; k < N_PLANES; ++k) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float &g = v[b][i >> 2][i & 3];
+                            const float r = bf16_to_f32(f32_to_bf16(g));
+                            g = isfinite(r) ? g - r : 0.0f;
+                        }
+                        patch_write8(pt.patch(), pt.half, b, v[b], lane);
+                    }
+                    pt.store(OutRef{dl + k * plane, tiles.rows, ld, N}, f0 & ~63, r0 + n0, r0 + u.nr, 0);
+                }
             }
         }
     }
@@ -304,6 +423,8 @@ struct VocabWs {
     RowGrad *rows;
     uint16_t *dl;
     float *dx_sum;
+    void *grads;      // parts of the gradient products
+    int clusters;     // of a few rows' forward
     int piece, pieces;
     int64_t ld_dl;
 };
@@ -318,7 +439,9 @@ size_t carve_vocab(const mok_vocab_loss_config &c, int pass, void *ws, VocabWs *
     };
     VocabWs w = {};
     if (pass == MOK_VOCAB_LOSS_FORWARD) {
-        w.part = (float2 *)take((size_t)c.rows * 4 * ((c.V + 255) / 256) * 8);
+        const int n_vt = (c.V + 255) / 256;
+        w.clusters = n_vt < PLAN_PAIRS ? n_vt : (int)PLAN_PAIRS;
+        w.part = (float2 *)take((size_t)c.rows * (c.rows <= FEW_ROWS ? 8 * w.clusters : 4 * n_vt) * 8);
         w.hit = (float *)take((size_t)c.rows * 4);
     } else {
         const int64_t planes = c.grad_dtype == MOK_DTYPE_F32 ? PLANES : 1;
@@ -338,9 +461,28 @@ size_t carve_vocab(const mok_vocab_loss_config &c, int pass, void *ws, VocabWs *
         w.dl = (uint16_t *)take((size_t)planes * c.rows * w.ld_dl * 2);
         if (w.pieces > 1 && c.grad_dtype == MOK_DTYPE_BF16)
             w.dx_sum = (float *)take((size_t)c.rows * round_up(c.H, 4) * 4);
+        if (w.pieces == 1) w.grads = take(dense_grads_bytes(c.rows, c.V, c.H));
     }
     if (o != nullptr) *o = w;
     return off > 0 ? off : 256;
+}
+
+// Rows of dl's tiles: as waves over the SM pairs, each as long as its loads and MMAs or its epilogue
+// (about 6000 clocks for 256 rows, 15000 with planes), and a first load and a last epilogue alone.
+int dl_height(int64_t rows, int64_t n_mb, int H, bool planes) {
+    const int64_t blocks = (H + BK - 1) / BK, pairs = sm_pairs();
+    int64_t best = INT64_MAX, best_h = LTILE;
+    for (int64_t h0 = LTILE; h0 >= 32; h0 -= 16) {
+        const int64_t n = (rows + h0 - 1) / h0, h = round_up((rows + n - 1) / n, 16);
+        const int64_t main = blocks * block_clocks(h), epi = (planes ? 15000 : 6000) * h / LTILE;
+        const int64_t waves = (n * n_mb + pairs - 1) / pairs;
+        const int64_t t = (waves - 1) * (main > epi ? main : epi) + main + epi;
+        if (t < best) {
+            best = t;
+            best_h = h;
+        }
+    }
+    return (int)best_h;
 }
 
 mok_status check_vocab(const mok_vocab_loss_config *c, int pass, void *ws, size_t ws_bytes,
@@ -398,17 +540,29 @@ mok_status mok_vocab_loss_forward(const mok_vocab_loss_config *c, const void *x,
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
     if (init_host() != cudaSuccess) return MOK_ERR_CUDA;
     CUtensorMap ma, mb;
-    if (map_w(&ma, x, 1, c->rows, c->H, c->ld_x, 128) != cudaSuccess ||
-        map2d(&mb, w, c->V, c->H, c->ld_w, 32) != cudaSuccess)
-        return MOK_ERR_CUDA;
     const int n_rb = (int)((c->rows + 255) / 256), n_vt = (c->V + 255) / 256;
-    const VocabFwd p{c->rows, n_rb, n_vt, (c->H + SEG_K - 1) / SEG_K, c->H, c->V, targets, wk.part,
-                     wk.hit, status};
-    MOK_OP_LAUNCH(OP_VOCAB_FWD, 1, launch_linear(ma, mb, p, (int64_t)n_rb * n_vt, stream));
+    const int segs = (c->H + SEG_K - 1) / SEG_K;
+    int parts = 4 * n_vt;
+    if (c->rows <= FEW_ROWS) {
+        parts = 8 * wk.clusters;
+        if (map_w(&ma, w, 1, c->V, c->H, c->ld_w, 128) != cudaSuccess ||
+            map2d(&mb, x, c->rows, c->H, c->ld_x, 32) != cudaSuccess)
+            return MOK_ERR_CUDA;
+        const VocabFew p{(int)c->rows, n_vt, segs, c->H, c->V, targets, wk.part, wk.hit, status};
+        MOK_OP_LAUNCH(OP_VOCAB_FWD, 1, launch_linear(ma, mb, p, n_vt, stream, PLAN_PAIRS));
+    } else {
+        if (map_w(&ma, x, 1, c->rows, c->H, c->ld_x, 128) != cudaSuccess ||
+            map2d(&mb, w, c->V, c->H, c->ld_w, 32) != cudaSuccess)
+            return MOK_ERR_CUDA;
+        const VocabFwd p{c->rows, n_rb, n_vt, segs, c->H, c->V, targets, wk.part, wk.hit, status};
+        MOK_OP_LAUNCH(OP_VOCAB_FWD, 1, launch_linear(ma, mb, p, (int64_t)n_rb * n_vt, stream));
+    }
+    int across = 1;
+    while (across < 32 && across < c->rows) across *= 2;
     MOK_OP_LAUNCH(OP_VOCAB_FWD, 1,
-                  launch_edge(vocab_finish_kernel, (unsigned)((c->rows + 31) / 32),
-                              32 * FINISH_SLICES, 0, 1, stream, (const float2 *)wk.part,
-                              (const float *)wk.hit, c->rows, 4 * n_vt, c->V, targets, c->z_loss,
+                  launch_edge(vocab_finish_kernel, (unsigned)((c->rows + across - 1) / across),
+                              32 * FINISH_WARPS, 0, 1, stream, (const float2 *)wk.part,
+                              (const float *)wk.hit, c->rows, across, parts, c->V, targets, c->z_loss,
                               loss, lse, status));
     return MOK_OK;
 }
@@ -445,23 +599,26 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
     for (int k = 0; k < wk.pieces; ++k) {
         const int v0 = k * wk.piece, n = c->V - v0 < wk.piece ? c->V - v0 : wk.piece;
         const int n_mb = (n + 255) / 256;
-        int64_t clocks;
-        const Tiles tiles = dense_tiles(c->rows, dense_height(c->rows, n_mb, sm_pairs(), &clocks));
+        const Tiles tiles = dense_tiles(c->rows, dl_height(c->rows, n_mb, c->H, f32));
+        const int band = 4096 / tiles.height;
         const int64_t units = tiles.cap * n_mb, plane = c->rows * wk.ld_dl;
-        if (f32) {
-            const VocabDl<true> p{tiles, n_mb, (c->H + SEG_K - 1) / SEG_K, c->H, v0, n, wk.rows,
-                                  wk.dl, wk.ld_dl, plane, status};
-            MOK_OP_LAUNCH(OP_VOCAB_DL, 1, launch_linear(ma, mb, p, units, stream));
-        } else {
-            const VocabDl<false> p{tiles, n_mb, 1, c->H, v0, n, wk.rows, wk.dl, wk.ld_dl, plane,
-                                   status};
-            MOK_OP_LAUNCH(OP_VOCAB_DL, 1, launch_linear(ma, mb, p, units, stream));
-        }
+        const int segs = f32 ? (c->H + SEG_K - 1) / SEG_K : 1;
+#define MOK_DL(...)                                                                              \
+    do {                                                                                         \
+        const VocabDl<__VA_ARGS__> p{tiles, band, n_mb, segs, c->H, v0, n, wk.rows, wk.dl, wk.ld_dl, \
+                                     plane, status};                                             \
+        MOK_OP_LAUNCH(OP_VOCAB_DL, 1, launch_linear(ma, mb, p, units, stream));                  \
+    } while (0)
+        if (!f32) MOK_DL(1, false);
+        else if (segs == 1) MOK_DL(PLANES, false);
+        else MOK_DL(PLANES, true);
+#undef MOK_DL
         const DenseGrads g{(const uint16_t *)x, (const uint16_t *)w + v0 * c->ld_w, wk.dl, c->rows, n,
                            c->H, f32 ? PLANES : 1, c->ld_x, c->ld_w, wk.ld_dl, dx,
                            dw ? (char *)dw + v0 * c->ld_w * es : nullptr, f32,
-                           dx ? wk.dx_sum : nullptr, dx && k > 0};
-        MOK_OP_LAUNCH(OP_VOCAB_GRADS, 1, launch_dense_grads(g, status, stream));
+                           dx ? wk.dx_sum : nullptr, dx && k > 0, wk.grads};
+        int launches = 0;
+        MOK_OP_LAUNCH(OP_VOCAB_GRADS, launches, launch_dense_grads(g, status, &launches, stream));
     }
     if (dx && wk.dx_sum != nullptr) {
         const int64_t n = c->rows * (round_up(c->H, 4) / 4), blocks = (n + 255) / 256;
