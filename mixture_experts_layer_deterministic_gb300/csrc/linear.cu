@@ -1148,9 +1148,7 @@ int group_height(int64_t rows, int G, int64_t n_mb) {
 
 // How a dense product is cut along K, by the sizes alone.
 constexpr int64_t MAX_PART_BYTES = 32 << 20;  // of all parts: they stay in L2
-struct Cut {
-    int parts, per, height;  // height: of the tiles the parts run on
-};
+using Cut = GradCut;  // height: of the tiles the parts run on
 // `rows` rows in tiles (of any height, or of `fixed` rows) by n_mb blocks of the other dimension
 // on `pairs` pairs of SMs, K blocks `blocks` long, parts at most max_per of them; `cols` columns
 // of output.
@@ -1306,48 +1304,90 @@ mok_status check_linear(const mok_linear_config *c, const int32_t *starts, const
     return MOK_OK;
 }
 
-mok_linear_config dense_config(int64_t rows, int N, int Kin) {
-    mok_linear_config c = {};
-    c.groups = 1;
-    c.rows = rows;
-    c.in_features = Kin;
-    c.out_features = N;
-    return c;
+// clocks of a product of `rows` rows in tiles (of `fixed` rows, or any) by n_mb blocks, `blocks` K blocks
+// long, on `pairs` pairs, whole or in parts (with the join), whichever is shorter
+int64_t grad_clocks(int64_t rows, int64_t n_mb, int64_t blocks, int64_t cols, int64_t pairs, int fixed,
+                    int64_t most_parts, Cut *best) {
+    int64_t least = INT64_MAX;
+    const int heights[] = {256, 192, 160, 128, 96, 64, 32};
+    for (int h0 : heights) {
+        if (fixed > 0) h0 = fixed;
+        const int64_t n = (rows + h0 - 1) / h0;
+        const int64_t h = fixed > 0 ? fixed : round_up((rows + n - 1) / n, 16), units = n * n_mb;
+        for (int64_t p = 1; p <= most_parts; p += (p + 1) / 2) {
+            const int64_t per = (blocks + p - 1) / p, parts = (blocks + per - 1) / per;
+            const int64_t bytes = parts > 1 ? parts * rows * round_up(cols, 4) * 4 : 0;
+            if (parts > 1 && (per < 4 || bytes > MAX_PART_BYTES)) break;
+            // a wave's epilogue runs beside the next one's loads; the last one's stands alone
+            const int64_t t = (units * parts + pairs - 1) / pairs * unit_clocks(per, h) +
+                              4500 * h / LTILE + (parts > 1 ? 5000 + bytes * 2 / 2500 : 0);
+            if (t < least) {
+                least = t;
+                *best = Cut{(int)parts, (int)per, (int)h};
+            }
+        }
+        if (fixed > 0) break;
+    }
+    return least;
 }
-
 template <bool F, bool CUT>
-cudaError_t dense_grads(const DenseGrads &a, const Cut &xc, const KParts &xk, const Cut &wc,
-                        const KParts &wk, const CUtensorMap &xa, const CUtensorMap &xb,
-                        const CUtensorMap &wa, const CUtensorMap &wb, int *status, int *launches,
-                        cudaStream_t s) {
+cudaError_t dense_grads(const DenseGrads &a, const GradPlan &plan, const KParts &xk, const KParts &wk,
+                        const CUtensorMap &xa, const CUtensorMap &xb, const CUtensorMap &wa,
+                        const CUtensorMap &wb, int *status, int *launches, cudaStream_t s) {
     const int n_kb = (a.Kin + 255) / 256, n_nb = (a.N + 255) / 256;
-    int64_t clocks, split = 0, pairs = 0;
-    const Tiles tiles = dense_tiles(
-        a.rows, xc.parts > 1 ? xc.height : dense_height(a.rows, n_kb, sm_pairs(), &clocks));
+    const bool both = a.dx && a.dw && plan.split > 0;
+    const Tiles tiles = dense_tiles(a.rows, both ? plan.height : plan.alone);
     const Dx<F, CUT> px{tiles, n_kb, a.halves, a.Kin, a.N, a.ld_x, a.dx, status, xk};
     const Dw<F, CUT> pw{nullptr, nullptr, a.rows, 1, n_kb, n_nb, a.halves, a.Kin, a.N, a.ld_w, a.dw,
                         status, DbArgs{nullptr, nullptr, 0, nullptr}, wk};
-    const int64_t x_units = a.dx ? tiles.cap * n_kb * xc.parts : 0;
-    const int64_t w_units = a.dw ? (int64_t)n_kb * n_nb * wc.parts : 0;
-    if (a.dx && a.dw)
-        plan_both(w_units, unit_clocks((wc.parts > 1 ? wc.per : (a.rows + 63) / 64) * a.halves, LTILE),
-                  x_units,
-                  unit_clocks((xc.parts > 1 ? xc.per : (a.N + 63) / 64) * a.halves, tiles.height),
-                  &split, &pairs);
-    *launches = split > 0 ? 1 : (a.dx != nullptr) + (a.dw != nullptr);
-    if (split > 0) return launch_both(wa, wb, pw, xa, xb, px, split, pairs, s);
+    *launches = both ? 1 : (a.dx != nullptr) + (a.dw != nullptr);
+    if (both) return launch_both(wa, wb, pw, xa, xb, px, plan.split, plan.pairs, s);
     cudaError_t e = cudaSuccess;
-    if (a.dx) e = launch_linear(xa, xb, px, x_units, s);
-    if (e == cudaSuccess && a.dw) e = launch_linear(wa, wb, pw, w_units, s);
+    if (a.dx) e = launch_linear(xa, xb, px, tiles.cap * n_kb * plan.x.parts, s);
+    if (e == cudaSuccess && a.dw)
+        e = launch_linear(wa, wb, pw, (int64_t)n_kb * n_nb * plan.w.parts, s);
     return e;
 }
 
 }  // namespace
 
-size_t dense_grads_bytes(int64_t rows, int N, int Kin) {
-    Cut x, w;
-    backward_cuts(dense_config(rows, N, Kin), &x, &w);
-    return (size_t)round_up((int64_t)part_bytes(x, rows, Kin), 256) + part_bytes(w, N, Kin);
+GradPlan plan_dense_grads(int64_t rows, int N, int Kin, int halves, bool cut) {
+    const int64_t kb = (Kin + 255) / 256, nb = (N + 255) / 256, all = PLAN_PAIRS;
+    const int64_t x_blocks = (N + BK - 1) / BK, w_blocks = (rows + BK - 1) / BK;
+    const int fixed = N <= 128 ? 128 : LTILE;
+    // in K blocks of the products themselves: the halves of dz follow each other in a unit
+    const auto clocks = [&](bool x, int64_t pairs, Cut *c) {
+        const int64_t most = cut ? 16 : 1;
+        return halves * (x ? grad_clocks(rows, kb, x_blocks, Kin, pairs, 0, most, c)
+                           : grad_clocks(N, kb, w_blocks, Kin, pairs, fixed, most, c));
+    };
+    GradPlan p = {}, q = {};
+    const int64_t tx = clocks(true, all, &p.x), tw = clocks(false, all, &p.w);
+    p.alone = p.x.height;
+    int64_t least = tx + tw + 12000;  // a launch, its fill and its drain
+    const int64_t share = all * tw / (tx + tw);
+    for (int64_t k = share - 16; k <= share + 16; k += 8) {
+        if (k < 1 || k >= all) continue;
+        const int64_t x = clocks(true, all - k, &q.x), w = clocks(false, k, &q.w);
+        const int64_t t = x > w ? x : w;
+        if (t >= least) continue;
+        least = t;
+        p.x = q.x;
+        p.w = q.w;
+        p.split = k;
+        p.height = q.x.height;
+    }
+    if (p.split > 0) {
+        // of the parts that were taken, what each product keeps busy
+        const int64_t xu = (rows + p.height - 1) / p.height * kb * p.x.parts, wu = nb * kb * p.w.parts;
+        p.split = p.split < wu ? p.split : wu;
+        p.pairs = p.split + (all - p.split < xu ? all - p.split : xu);
+    }
+    return p;
+}
+
+size_t dense_grads_bytes(const GradPlan &p, int64_t rows, int N, int Kin) {
+    return (size_t)round_up((int64_t)part_bytes(p.x, rows, Kin), 256) + part_bytes(p.w, N, Kin);
 }
 
 cudaError_t launch_dense_grads(const DenseGrads &a, int *status, int *launches, cudaStream_t s) {
@@ -1364,22 +1404,21 @@ cudaError_t launch_dense_grads(const DenseGrads &a, int *status, int *launches, 
     if (a.dw && ((e = map2d(&wa, a.x, a.rows, a.Kin, a.ld_x, 64)) != cudaSuccess ||
                  (e = map_dz(&wb, 64)) != cudaSuccess))
         return e;
-    Cut xc{1, 0, 0}, wc{1, 0, 0};
-    if (a.ws != nullptr) backward_cuts(dense_config(a.rows, a.N, a.Kin), &xc, &wc);
+    const GradPlan &plan = a.plan;
     float *parts = static_cast<float *>(a.ws);
-    KParts xk = k_parts(xc, parts, a.rows, a.Kin);
+    KParts xk = k_parts(plan.x, parts, a.rows, a.Kin);
     const KParts wk = k_parts(
-        wc, parts + round_up((int64_t)part_bytes(xc, a.rows, a.Kin), 256) / 4, a.N, a.Kin);
+        plan.w, parts + round_up((int64_t)part_bytes(plan.x, a.rows, a.Kin), 256) / 4, a.N, a.Kin);
     if (a.dx_sum != nullptr || a.add) xk = KParts{1, 0, a.dx_sum, round_up(a.Kin, 4), 0, a.add};
     const bool cut = xk.out != nullptr || xk.add || wk.out != nullptr;
     e = (a.f32 ? (cut ? dense_grads<true, true> : dense_grads<true, false>)
                : (cut ? dense_grads<false, true> : dense_grads<false, false>))(
-        a, xc, xk, wc, wk, xa, xb, wa, wb, status, launches, s);
+        a, plan, xk, wk, xa, xb, wa, wb, status, launches, s);
     if (e != cudaSuccess) return e;
     JoinArgs j = {};
     int n = 0;
-    if (a.dx && xc.parts > 1) j.o[n++] = join_out(xk, a.rows, a.Kin, a.dx, a.ld_x);
-    if (a.dw && wc.parts > 1) j.o[n++] = join_out(wk, a.N, a.Kin, a.dw, a.ld_w);
+    if (a.dx && plan.x.parts > 1) j.o[n++] = join_out(xk, a.rows, a.Kin, a.dx, a.ld_x);
+    if (a.dw && plan.w.parts > 1) j.o[n++] = join_out(wk, a.N, a.Kin, a.dw, a.ld_w);
     *launches += n > 0;
     return n > 0 ? launch_join(a.f32, j, s) : cudaSuccess;
 }

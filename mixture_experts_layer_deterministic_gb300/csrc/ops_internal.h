@@ -21,6 +21,19 @@ inline bool op_aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 // rounding up to a multiple
 inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
+// How these run: parts of K, `per` 64-element blocks each, by the sizes alone (the bits depend on them);
+// the pairs of SMs that dW gets of a launch of both (0: one after the other), and of both; the height
+// of dx's tiles beside dW, and with all pairs to itself.
+struct GradCut {
+    int parts, per, height;
+};
+struct GradPlan {
+    GradCut x, w;
+    int64_t split, pairs;
+    int height, alone;
+};
+GradPlan plan_dense_grads(int64_t rows, int N, int Kin, int halves, bool cut);
+
 // The products of a dense layer's backward, dx = dz W and dW = dz^T x, with dz made elsewhere: bf16
 // [rows][N] rows ld_dz apart, or for fp32 gradients `halves` such planes that add up to it.
 struct DenseGrads {
@@ -34,9 +47,10 @@ struct DenseGrads {
     // nullptr where dx is fp32 itself), and adds to it from the second piece on
     float *dx_sum;
     bool add;
-    void *ws;                    // dense_grads_bytes; nullptr: K is not cut into parts (see linear.cu)
+    GradPlan plan;
+    void *ws;  // dense_grads_bytes, where the plan cuts K
 };
-size_t dense_grads_bytes(int64_t rows, int N, int Kin);
+size_t dense_grads_bytes(const GradPlan &p, int64_t rows, int N, int Kin);
 // *launches: how many it took
 cudaError_t launch_dense_grads(const DenseGrads &a, int *status, int *launches, cudaStream_t s);
 

@@ -41,9 +41,11 @@ struct MaxSum {
 };
 
 // ---------------------------------------------------------------- forward
+// SEGS: H in segments that are added in registers; else the sums are in TMEM whole.
+template <bool SEGS>
 struct VocabFwd {
     using E = Epi<true>;
-    static constexpr bool F32_OUT = true, SUMS = true, A_MN = false, B_MN = false;
+    static constexpr bool F32_OUT = true, SUMS = SEGS, A_MN = false, B_MN = false;
     static constexpr int BAND = 16;  // row blocks that take a tile of W one after another: 4096
                                      // rows of x stay in L2 while W passes by
     int64_t rows;
@@ -89,30 +91,44 @@ struct VocabFwd {
         for (int j = 0; j < q.nbox; ++j)
             tc::tma_load_2d_pair(st + 2 * BOX + j * (BOX / 2), tmB, fb, q.b0 + k0, q.b1 + 32 * j);
     }
+    // columns n0 .. n0 + N - 1 of a tile, those below `n` of the vocabulary
+    template <int N>
+    MOK_DEV void take(MaxSum &a, int n0, int n, const float (&v)[N], int target, int64_t row) const {
+        const bool whole = N > 16 && n0 + N <= n;  // (registers are short among segments)
+        float t = a.m;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (whole || n0 + j < n) t = fmaxf(t, v[j]);
+        a.s *= exp2_hw((a.m - t) * LOG2E_F);
+        a.m = t;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (whole || n0 + j < n) a.s += exp2_hw((v[j] - t) * LOG2E_F);
+        if (target >= n0 && target < n0 + N) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (target == n0 + j && n0 + j < n) hit[row] = v[j];
+        }
+    }
     MOK_DEV void epilogue(const Unit &u, int seg, bool last, uint32_t rank, uint32_t c, int q, int hw,
-                          int lane, Patches &, Carry<true> &carry) const {
+                          int lane, Patches &, Carry<SEGS> &carry) const {
         const int64_t row = (int64_t)u.mb * 256 + rank * 128 + q * 32 + lane;
         const int n = cols(u);
         MaxSum a{LOWEST, 0.0f};
         int target = -1;
         if (last && row < rows) target = targets[row];
         target -= u.nb * 256;
-        sum_segments(c, hw, n, seg == 0, last, carry, [&](int n0, const float (&v)[16]) {
-            float t = a.m;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (n0 + j < n) t = fmaxf(t, v[j]);
-            a.s *= exp2_hw((a.m - t) * LOG2E_F);
-            a.m = t;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (n0 + j < n) a.s += exp2_hw((v[j] - t) * LOG2E_F);
-            if (target >= n0 && target < n0 + 16) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (target == n0 + j && n0 + j < n) hit[row] = v[j];
+        if constexpr (SEGS) {
+            sum_segments(c, hw, n, seg == 0, last, carry, [&](int n0, const float (&v)[16]) {
+                take(a, n0, n, v, target, row);
+            });
+        } else {
+            for (int n0 = 32 * hw; n0 < n; n0 += 128) {
+                float v[32];
+                ld32(c + n0, v);
+                take(a, n0, n, v, target, row);
             }
-        });
+        }
         if (last && row < rows) part[((int64_t)u.nb * 4 + hw) * rows + row] = make_float2(a.m, a.s);
     }
 };
@@ -350,27 +366,26 @@ struct VocabDl {
             });
         } else {
             for (int n0 = 32 * hw; n0 < u.nr; n0 += E::STEP) {
-                float v[4][2][4];
-#pragma unroll(N_PLANES > 1 ? 4 : 2)
-                for (int b = 0; b < 4; ++b) {
-                    float w[2][4];
-                    ld_pairs8(c + n0 + 8 * b, w);
-                    RowGrad g[2];
+                // 32 rows: what they need first, so that its latency and the columns' run together
+                RowGrad g[4][2];
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int n = n0 + 8 * b + 2 * (lane & 3) + i;
-                        g[i] = rows[r0 + (n < u.nr ? n : u.nr - 1)];
+                        g[b][i] = rows[r0 + (n < u.nr ? n : u.nr - 1)];
                     }
+                float w[2][4][4], v[4][2][4];
+                ld_pairs(c + n0, w);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            w[h][i] = dl_of(g[i & 1], w[h][i],
-                                            v0 + f0 + 16 * h + 8 * (i >> 1) + (lane >> 2));
-                    patch_write8(pt.patch(), pt.half, b, w, lane);
-                    if (N_PLANES > 1)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[b][i >> 2][i & 3] = w[i >> 2][i & 3];
+                            v[b][h][i] = dl_of(g[b][i & 1], w[h][b][i],
+                                               v0 + f0 + 16 * h + 8 * (i >> 1) + (lane >> 2));
+                    patch_write8(pt.patch(), pt.half, b, v[b], lane);
                 }
                 pt.store(OutRef{dl, tiles.rows, ld, N}, f0 & ~63, r0 + n0, r0 + u.nr, 0);
 #pragma unroll
@@ -423,7 +438,8 @@ struct VocabWs {
     RowGrad *rows;
     uint16_t *dl;
     float *dx_sum;
-    void *grads;      // parts of the gradient products
+    GradPlan plan;    // of the gradient products, where the vocabulary is one piece
+    void *grads;      // their parts
     int clusters;     // of a few rows' forward
     int piece, pieces;
     int64_t ld_dl;
@@ -461,7 +477,10 @@ size_t carve_vocab(const mok_vocab_loss_config &c, int pass, void *ws, VocabWs *
         w.dl = (uint16_t *)take((size_t)planes * c.rows * w.ld_dl * 2);
         if (w.pieces > 1 && c.grad_dtype == MOK_DTYPE_BF16)
             w.dx_sum = (float *)take((size_t)c.rows * round_up(c.H, 4) * 4);
-        if (w.pieces == 1) w.grads = take(dense_grads_bytes(c.rows, c.V, c.H));
+        if (w.pieces == 1) {
+            w.plan = plan_dense_grads(c.rows, c.V, c.H, (int)planes, true);
+            w.grads = take(dense_grads_bytes(w.plan, c.rows, c.V, c.H));
+        }
     }
     if (o != nullptr) *o = w;
     return off > 0 ? off : 256;
@@ -554,8 +573,14 @@ mok_status mok_vocab_loss_forward(const mok_vocab_loss_config *c, const void *x,
         if (map_w(&ma, x, 1, c->rows, c->H, c->ld_x, 128) != cudaSuccess ||
             map2d(&mb, w, c->V, c->H, c->ld_w, 32) != cudaSuccess)
             return MOK_ERR_CUDA;
-        const VocabFwd p{c->rows, n_rb, n_vt, segs, c->H, c->V, targets, wk.part, wk.hit, status};
-        MOK_OP_LAUNCH(OP_VOCAB_FWD, 1, launch_linear(ma, mb, p, (int64_t)n_rb * n_vt, stream));
+        const int64_t units = (int64_t)n_rb * n_vt;
+        if (segs > 1) {
+            const VocabFwd<true> p{c->rows, n_rb, n_vt, segs, c->H, c->V, targets, wk.part, wk.hit, status};
+            MOK_OP_LAUNCH(OP_VOCAB_FWD, 1, launch_linear(ma, mb, p, units, stream));
+        } else {
+            const VocabFwd<false> p{c->rows, n_rb, n_vt, segs, c->H, c->V, targets, wk.part, wk.hit, status};
+            MOK_OP_LAUNCH(OP_VOCAB_FWD, 1, launch_linear(ma, mb, p, units, stream));
+        }
     }
     int across = 1;
     while (across < 32 && across < c->rows) across *= 2;
@@ -616,7 +641,10 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
         const DenseGrads g{(const uint16_t *)x, (const uint16_t *)w + v0 * c->ld_w, wk.dl, c->rows, n,
                            c->H, f32 ? PLANES : 1, c->ld_x, c->ld_w, wk.ld_dl, dx,
                            dw ? (char *)dw + v0 * c->ld_w * es : nullptr, f32,
-                           dx ? wk.dx_sum : nullptr, dx && k > 0, wk.grads};
+                           dx ? wk.dx_sum : nullptr, dx && k > 0,
+                           wk.pieces == 1 ? wk.plan
+                                          : plan_dense_grads(c->rows, n, c->H, f32 ? PLANES : 1, false),
+                           wk.grads};
         int launches = 0;
         MOK_OP_LAUNCH(OP_VOCAB_GRADS, launches, launch_dense_grads(g, status, &launches, stream));
     }
