@@ -3,12 +3,14 @@
 //   h = x + residual, n = (h - mean) rstd, y = n w + b
 //   g = dy w, dx = dh + rstd (g - n mean(g n) - mean(g)), dw = sum dy n, db = sum dy
 //
-// All of it is HBM traffic. A row belongs to a team, a power of two of threads that hold NV vectors
-// of 8 elements each; blocks walk over the rows, and where registers allow it (AHEAD) a team's next
-// row is on its way while it works on the last, so that the loads never pause. Rows too long for a
-// team are read again instead. The mean is taken in two steps (of h, then of h less the first), so
+// All of it is HBM traffic. A row belongs to a team, a power of two of threads up to a warp or some
+// warps of a block, that hold NV vectors of 8 elements each; long rows are cut over the blocks of a
+// cluster, which exchange their sums through each other's shared memory. Blocks walk over the rows, and
+// a team's next row is on its way while it works on the last, so that the loads never pause. Rows too
+// long for a cluster are read again instead. The mean is taken in two steps (of h, then of h less the first), so
 // that rows far from zero keep their digits; the variance is that of h less the mean.
 #include "ops_internal.h"
+#include "tc.cuh"
 
 namespace mok {
 namespace {
@@ -113,9 +115,11 @@ MOK_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 struct NormShape {
     int64_t rows, ld_x, ld_y;
     int H;
-    int tpr;  // threads of a team: a power of two
+    int tpr;      // threads of a team
+    int cluster;  // blocks of a row
     bool layer;
     float eps;
+    int *status;
 };
 
 template <bool F32>
@@ -169,11 +173,48 @@ MOK_DEV void unpack(const Raw<F32> &q, float (&v)[8]) {
         v[j] = F32 ? __uint_as_float(w[j]) : (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
 }
 
-// sums of a and b over a team, the same in all of its threads. Teams of more than a warp: through
-// sh [2][warps of the block], its halves in turn, so that one barrier of the team is enough.
+// Where a thread's vectors lie: number k is column 8 (first + k tpr).
+struct Place {
+    int first, slot, slots;  // slot: the team's number in its block
+    MOK_DEV Place(const NormShape &s, int nv, uint32_t rank) {
+        slot = threadIdx.x / s.tpr;
+        slots = blockDim.x / s.tpr;
+        first = threadIdx.x - slot * s.tpr + (int)rank * nv * s.tpr;
+    }
+};
+
+// Sums of a and b over a team, the same in all of its threads. Teams of more than a warp: through sh
+// [2][warps of the block], its halves in turn, so that one barrier of the team is enough. CLUSTER: then
+// over the blocks of the cluster, each sending its sums to all of them (across [2][blocks]), where they
+// are counted in by a barrier in shared memory. (A barrier of the cluster would have to wait for the
+// stores of the row before: 2000 rows of 16384 fp32 in four blocks 241 us with one.) A half is sent to
+// again only by blocks that have this block's next sums, which it sends when all of it has read.
+constexpr int MOST_BLOCKS = 8;  // of a cluster
+struct NormShared {
+    float2 warps[2][32];
+    float2 across[2][MOST_BLOCKS];
+    uint64_t arrived[2];
+    int gave_up;
+};
+template <bool CLUSTER>
 struct TeamSum {
-    float2 *sh;
-    int tpr, turn;
+    NormShared *sh;
+    int tpr, blocks;
+    uint32_t rank;
+    int *status;
+    uint32_t calls;
+    MOK_DEV TeamSum(NormShared *shared, const NormShape &s, uint32_t r)
+        : sh(shared), tpr(s.tpr), blocks(s.cluster), rank(r), status(s.status), calls(0) {
+        if constexpr (CLUSTER) {
+            if (threadIdx.x == 0) {
+                tc::mbar_init(&sh->arrived[0], 1);
+                tc::mbar_init(&sh->arrived[1], 1);
+                sh->gave_up = 0;
+                tc::fence_mbar_init();
+            }
+            together();  // all blocks are there to be sent to
+        }
+    }
     MOK_DEV void operator()(float &a, float &b) {
         const int w = tpr < 32 ? tpr : 32;
         for (int o = 1; o < w; o <<= 1) {
@@ -182,8 +223,8 @@ struct TeamSum {
         }
         if (tpr <= 32) return;
         const int warp = threadIdx.x >> 5, n = tpr / 32, team = warp / n;
-        float2 *s = sh + turn * 32;
-        turn ^= 1;
+        const uint32_t turn = calls & 1;
+        float2 *s = sh->warps[turn];
         if ((threadIdx.x & 31) == 0) s[warp] = make_float2(a, b);
         asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(tpr) : "memory");
         a = b = 0.0f;
@@ -192,8 +233,67 @@ struct TeamSum {
             a += v.x;
             b += v.y;
         }
+        if constexpr (CLUSTER) {
+            uint64_t *bar = &sh->arrived[turn];
+            if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)blocks * 8u);
+            if (threadIdx.x < blocks) {
+                uint32_t to, at;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                             : "=r"(to)
+                             : "r"(tc::smem_u32(&sh->across[turn][rank])), "r"(threadIdx.x));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                             : "=r"(at)
+                             : "r"(tc::smem_u32(bar)), "r"(threadIdx.x));
+                asm volatile(
+                    "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::
+                        "r"(to), "f"(a), "f"(b), "r"(at)
+                    : "memory");
+            }
+            wait(bar, (calls >> 1) & 1);
+            a = b = 0.0f;
+            for (int k = 0; k < blocks; ++k) {
+                const float2 v = sh->across[turn][k];
+                a += v.x;
+                b += v.y;
+            }
+        }
+        ++calls;
+    }
+    // until the blocks' sums are here: bounded, once for all
+    MOK_DEV void wait(uint64_t *bar, uint32_t parity) {
+        uint64_t t0 = 0;
+        for (uint32_t n = 1;; ++n) {
+            uint32_t ok;
+            asm volatile(
+                "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+                "selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(ok)
+                : "r"(tc::smem_u32(bar)), "r"(parity)
+                : "memory");
+            if (ok) return;
+            if ((n & 63u) != 0) continue;
+            if (*(volatile int *)&sh->gave_up) return;
+            const uint64_t t = tc::globaltimer();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > tc::WAIT_LIMIT_NS) {
+                raise_status(status, MOK_ERR_TIMEOUT);
+                *(volatile int *)&sh->gave_up = 1;
+                return;
+            }
+        }
+    }
+    // all blocks of the cluster
+    MOK_DEV void together() const {
+        if constexpr (CLUSTER)
+            asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
     }
 };
+template <bool CLUSTER>
+MOK_DEV uint32_t block_of_cluster() {
+    uint32_t r = 0;
+    if (CLUSTER) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
 
 struct NormFwd {
     NormShape s;
@@ -235,6 +335,7 @@ MOK_DEV void store_y(const NormFwd &a, int64_t r, int c, float mean, float rest,
 template <int NV, bool X32, bool WHOLE>
 struct NormRow {
     Raw<X32> x[NV], res[NV];
+    // i: the first of the thread's vectors
     MOK_DEV void load(const NormFwd &a, int64_t r, int i) {
         const void *px = row_of<X32>(a.x, r, a.s.ld_x), *pr = row_of<X32>(a.res, r, a.s.ld_x);
 #pragma unroll
@@ -250,19 +351,22 @@ struct NormRow {
     }
 };
 
-template <int NV, bool X32, bool Y32, bool WHOLE, bool AHEAD, int MOST>
-__global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const NormFwd a) {
-    __shared__ float2 sh[64];
+template <int NV, bool X32, bool Y32, bool WHOLE, bool CLUSTER>
+__global__ void __launch_bounds__(NORM_TPB, 2) norm_kernel(const NormFwd a) {
+    __shared__ NormShared sh;
     const NormShape &s = a.s;
-    TeamSum team_sum{sh, s.tpr, 0};
+    const uint32_t rank = block_of_cluster<CLUSTER>();
+    TeamSum<CLUSTER> team_sum(&sh, s, rank);
     let_next_start();
     wait_for_previous();
-    const int i = threadIdx.x % s.tpr, slot = threadIdx.x / s.tpr, slots = blockDim.x / s.tpr;
-    const int64_t step = (int64_t)gridDim.x * slots;
+    const Place at(s, NV, rank);
+    const int i = at.first;
+    const int64_t walkers = CLUSTER ? gridDim.x / s.cluster : gridDim.x;
+    const int64_t walker = CLUSTER ? blockIdx.x / s.cluster : blockIdx.x, step = walkers * at.slots;
     NormRow<NV, X32, WHOLE> row;
-    row.load(a, (int64_t)blockIdx.x * slots + slot, i);
-    for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += step) {
-        const int64_t r = r0 + slot;
+    row.load(a, walker * at.slots + at.slot, i);
+    for (int64_t r0 = walker * at.slots; r0 < s.rows; r0 += step) {
+        const int64_t r = r0 + at.slot;
         float v[NV][8];
         float sum = 0.0f, rest = 0.0f, sq = 0.0f;
 #pragma unroll
@@ -277,7 +381,7 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const NormFwd a
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum += v[k][j];
         }
-        if (AHEAD && r0 + step < s.rows) row.load(a, r + step, i);
+        if (r0 + step < s.rows) row.load(a, r + step, i);
         float mean = 0.0f;
         if (s.layer) {
             team_sum(sum, rest);
@@ -310,8 +414,8 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) norm_kernel(const NormFwd a
                 store_y<Y32, WHOLE>(a, r, c, mean, rest, rstd, v[k]);
             }
         }
-        if (!AHEAD && r0 + step < s.rows) row.load(a, r + step, i);
     }
+    team_sum.together();  // nobody sends to a block that has left
 }
 
 // h of 8 columns
@@ -328,9 +432,9 @@ MOK_DEV void load_h(const NormFwd &a, int64_t r, int c, float (&v)[8]) {
 // longer rows: one a block, read three times (h is written last, so x or the residual may be h)
 template <bool X32, bool Y32>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormFwd a) {
-    __shared__ float2 sh[64];
+    __shared__ NormShared sh;
     const NormShape &s = a.s;
-    TeamSum row_sum{sh, 1024, 0};
+    TeamSum<false> row_sum(&sh, s, 0);
     let_next_start();
     wait_for_previous();
     const int64_t r = blockIdx.x;
@@ -438,18 +542,21 @@ struct NormBwdRow {
     }
 };
 
-// Block b's teams take the b-th, (b + blocks)-th, .. rows, keep their columns' sums in registers and
-// add them in order at the end.
-template <int NV, bool X32, bool Y32, bool WHOLE, bool AHEAD>
+// The teams of block (or cluster) b take the b-th, (b + blocks)-th, .. rows, keep their columns' sums in
+// registers and add them in order at the end.
+template <int NV, bool X32, bool Y32, bool WHOLE, bool CLUSTER>
 __global__ void __launch_bounds__(NORM_TPB) norm_backward_kernel(const NormBwd a) {
     extern __shared__ float norm_smem[];
-    __shared__ float2 sh[64];
+    __shared__ NormShared sh;
     const NormShape &s = a.s;
-    TeamSum team_sum{sh, s.tpr, 0};
+    const uint32_t rank = block_of_cluster<CLUSTER>();
+    TeamSum<CLUSTER> team_sum(&sh, s, rank);
     let_next_start();
     wait_for_previous();
-    const int i = threadIdx.x % s.tpr, slot = threadIdx.x / s.tpr, slots = blockDim.x / s.tpr;
-    const int64_t step = (int64_t)gridDim.x * slots;
+    const Place at(s, NV, rank);
+    const int i = at.first;
+    const int64_t walkers = CLUSTER ? gridDim.x / s.cluster : gridDim.x;
+    const int64_t walker = CLUSTER ? blockIdx.x / s.cluster : blockIdx.x, step = walkers * at.slots;
     f32x2 dw[NV][4], db[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -462,89 +569,87 @@ __global__ void __launch_bounds__(NORM_TPB) norm_backward_kernel(const NormBwd a
         if (a.w != nullptr && c < s.H) load_raw<true, WHOLE>(a.w, c, s.H, q);
         unpack<true>(q, w);
     };
-    NormBwdRow<NV, X32, Y32, WHOLE> next;
-    next.load(a, (int64_t)blockIdx.x * slots + slot, i);
-    for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < s.rows; r0 += step) {
-        const int64_t r = r0 + slot;
-        const NormBwdRow<NV, X32, Y32, WHOLE> row = next;
-        if (AHEAD && r0 + step < s.rows) next.load(a, r + step, i);
+    NormBwdRow<NV, X32, Y32, WHOLE> row;
+    row.load(a, walker * at.slots + at.slot, i);
+    for (int64_t r0 = walker * at.slots; r0 < s.rows; r0 += step) {
+        const int64_t r = r0 + at.slot;
         // with t = h - mean: n = t rstd, so sum(g n) = rstd sum(g t). Past H dy is zero, so t does not
         // matter there
-        const f32x2 mean = pair(-row.mean, -row.mean), rstd = pair(row.rstd, row.rstd);
-        f32x2 sg2 = 0, sgt2 = 0;
+        const float row_rstd = row.rstd;
+        const f32x2 mean = pair(-row.mean, -row.mean), rstd = pair(row_rstd, row_rstd);
+        f32x2 t[NV][4], g[NV][4], sg2 = 0, sgt2 = 0;
+        Raw<X32> dh[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            f32x2 t[4], dy[4], w[4];
-            unpack<X32>(row.h[k], t);
-            unpack<Y32>(row.dy[k], dy);
+            f32x2 w[4];
+            unpack<X32>(row.h[k], t[k]);
+            unpack<Y32>(row.dy[k], g[k]);
+            dh[k] = row.dh[k];
             weights(8 * (i + k * s.tpr), w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                t[j] = add2(t[j], mean);
-                const f32x2 g = mul2(dy[j], w[j]);
-                sg2 = add2(sg2, g);
-                sgt2 = fma2(g, t[j], sgt2);
-                dw[k][j] = fma2(mul2(dy[j], rstd), t[j], dw[k][j]);
-                db[k][j] = add2(db[k][j], dy[j]);
+                t[k][j] = add2(t[k][j], mean);
+                dw[k][j] = fma2(mul2(g[k][j], rstd), t[k][j], dw[k][j]);
+                db[k][j] = add2(db[k][j], g[k][j]);
+                g[k][j] = mul2(g[k][j], w[j]);
+                sg2 = add2(sg2, g[k][j]);
+                sgt2 = fma2(g[k][j], t[k][j], sgt2);
             }
         }
-        if (a.dx != nullptr) {
-            float sg = both(sg2).x + both(sg2).y, sgt = both(sgt2).x + both(sgt2).y;
-            team_sum(sgt, sg);
-            // dx = dh - rstd mean(g) + g rstd - t rstd^2 mean(g n)
-            const float c0 = s.layer ? -row.rstd * (sg / s.H) : 0.0f;
-            const float c1 = -row.rstd * row.rstd * (row.rstd * (sgt / s.H));
-            const f32x2 a0 = pair(c0, c0), a1 = pair(c1, c1);
+        if (r0 + step < s.rows) row.load(a, r + step, i);
+        if (a.dx == nullptr) continue;
+        float sg = both(sg2).x + both(sg2).y, sgt = both(sgt2).x + both(sgt2).y;
+        team_sum(sgt, sg);
+        // dx = dh - rstd mean(g) + g rstd - t rstd^2 mean(g n)
+        const float c0 = s.layer ? -row_rstd * (sg / s.H) : 0.0f;
+        const float c1 = -row_rstd * row_rstd * (row_rstd * (sgt / s.H));
+        const f32x2 a0 = pair(c0, c0), a1 = pair(c1, c1);
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = 8 * (i + k * s.tpr);
-                if (r >= s.rows || c >= s.H) continue;
-                f32x2 t[4], dy[4], w[4], v[4];
-                unpack<X32>(row.h[k], t);
-                unpack<Y32>(row.dy[k], dy);
-                unpack<X32>(row.dh[k], v);
-                weights(c, w);
-                float o[8];
+        for (int k = 0; k < NV; ++k) {
+            const int c = 8 * (i + k * s.tpr);
+            if (r >= s.rows || c >= s.H) continue;
+            f32x2 v[4];
+            unpack<X32>(dh[k], v);
+            float o[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[j] = fma2(mul2(dy[j], w[j]), rstd, add2(v[j], a0));
-                    v[j] = fma2(add2(t[j], mean), a1, v[j]);
-                    o[2 * j] = both(v[j]).x;
-                    o[2 * j + 1] = both(v[j]).y;
-                }
-                store8<X32, WHOLE>(row_of<X32>(a.dx, r, s.ld_x), c, s.H, o);
+            for (int j = 0; j < 4; ++j) {
+                v[j] = fma2(t[k][j], a1, fma2(g[k][j], rstd, add2(v[j], a0)));
+                o[2 * j] = both(v[j]).x;
+                o[2 * j + 1] = both(v[j]).y;
             }
+            store8<X32, WHOLE>(row_of<X32>(a.dx, r, s.ld_x), c, s.H, o);
         }
-        if (!AHEAD && r0 + step < s.rows) next.load(a, r + step, i);
     }
     for (int part = 0; part < 2; ++part) {
         float *out = part == 0 ? a.dw_part : a.db_part;
         if (out == nullptr) continue;
+        const int width = NV * 8 * s.tpr, c0 = (int)rank * width;  // the block's columns
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (i + k * s.tpr);
+            const int at_smem = at.slot * width + 8 * (i + k * s.tpr) - c0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float2 v = both(part == 0 ? dw[k][j >> 1] : db[k][j >> 1]);
-                if (c + j < s.H) norm_smem[slot * s.H + c + j] = (j & 1) ? v.y : v.x;
+                norm_smem[at_smem + j] = (j & 1) ? v.y : v.x;
             }
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < s.H; c += blockDim.x) {
+        for (int c = threadIdx.x; c < width && c0 + c < s.H; c += blockDim.x) {
             float t = 0.0f;
-            for (int k = 0; k < slots; ++k) t += norm_smem[k * s.H + c];
-            out[(int64_t)blockIdx.x * s.H + c] = t;
+            for (int k = 0; k < at.slots; ++k) t += norm_smem[k * width + c];
+            out[walker * s.H + c0 + c] = t;
         }
     }
+    team_sum.together();  // nobody sends to a block that has left
 }
 
 // longer rows: dx by a block a row, read twice
 template <bool X32, bool Y32>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBwd a) {
-    __shared__ float2 sh[64];
+    __shared__ NormShared sh;
     const NormShape &s = a.s;
-    TeamSum row_sum{sh, 1024, 0};
+    TeamSum<false> row_sum(&sh, s, 0);
     let_next_start();
     wait_for_previous();
     const int64_t r = blockIdx.x;
@@ -629,47 +734,42 @@ __global__ void __launch_bounds__(32 * NORM_SLICES)
 }
 
 // ---------------------------------------------------------------- host side
-NormShape norm_shape(const mok_norm_config &c) {
-    return NormShape{c.rows, c.ld_x, c.ld_y, c.H, 1024, c.kind == MOK_NORM_LAYER, c.eps};
-}
-int pow2_up(int n) {
-    int p = 1;
-    while (p < n) p *= 2;
-    return p;
+NormShape norm_shape(const mok_norm_config &c, int *status) {
+    return NormShape{c.rows, c.ld_x, c.ld_y, c.H, 1024, 1, c.kind == MOK_NORM_LAYER, c.eps, status};
 }
 
-// How rows are held. Two vectors a thread where both types are bf16, one otherwise, is what the
-// registers hold twice: a row, and the next on its way. Longer rows have twice as many vectors a
-// thread and load a row when the last is done; yet longer ones are read again.
+// How rows are held: two vectors a thread where both types are bf16, one otherwise, which is what the
+// registers hold with the next row's beside them; up to 512 threads a block, up to 8 blocks.
 struct NormPlan {
-    int nv, tpr, tpb;  // vectors a thread, threads of a team and of a block; nv 0: read again
-    bool ahead;
-    int64_t groups;    // of rows that a block takes at a time
-    int64_t parts;     // of the backward's column sums
+    int tpr, tpb, cluster;  // threads of a team and of a block, blocks of a row; tpr 0: read again
+    int64_t groups;         // of rows that a block or cluster takes at a time
+    int64_t parts;          // of the backward's column sums
 };
-NormPlan norm_plan(const mok_norm_config &c, bool backward) {
-    const int vecs = (c.H + 7) / 8, most = backward ? NORM_TPB : 1024;
-    const bool small = c.x_dtype == MOK_DTYPE_BF16 && c.y_dtype == MOK_DTYPE_BF16;
+NormPlan norm_plan(const mok_norm_config &c) {
+    const int vecs = (c.H + 7) / 8;
+    const int nv = c.x_dtype == MOK_DTYPE_BF16 && c.y_dtype == MOK_DTYPE_BF16 ? 2 : 1;
     NormPlan p = {};
-    p.nv = small ? 2 : 1;
-    p.ahead = vecs <= p.nv * most;
-    if (!p.ahead && (backward || !small)) p.nv *= 2;
-    if (vecs > p.nv * most) {
-        p.nv = 0;
+    p.cluster = (vecs + nv * NORM_TPB - 1) / (nv * NORM_TPB);
+    if (p.cluster > MOST_BLOCKS) {
         p.groups = c.rows;
         p.parts = c.rows < 32 ? c.rows : 32;
         return p;
     }
-    p.tpr = pow2_up((vecs + p.nv - 1) / p.nv);
-    // few rows: smaller blocks, on more SMs
-    p.tpb = p.tpr > NORM_TPB ? p.tpr : NORM_TPB;
-    while (p.tpb > 128 && p.tpb > p.tpr && c.rows * p.tpr < NORM_PARTS * p.tpb) p.tpb /= 2;
-    p.groups = (c.rows + p.tpb / p.tpr - 1) / (p.tpb / p.tpr);
-    p.parts = p.groups < NORM_PARTS ? p.groups : NORM_PARTS;
+    const int threads = (vecs + p.cluster * nv - 1) / (p.cluster * nv);
+    p.tpr = 1;
+    while (p.tpr < threads && p.tpr < 32) p.tpr *= 2;
+    if (threads > 32) p.tpr = (int)round_up(threads, 32);
+    // as many teams as a block holds; with few rows fewer, on more SMs
+    int teams = NORM_TPB / p.tpr;
+    while (teams > 1 && p.tpr * teams > 128 && c.rows < NORM_PARTS * teams) teams /= 2;
+    p.tpb = teams * p.tpr;
+    p.groups = (c.rows + teams - 1) / teams;
+    const int64_t most = NORM_PARTS / p.cluster;
+    p.parts = p.groups < most ? p.groups : most;
     return p;
 }
 size_t norm_part_bytes(const mok_norm_config &c) {
-    return (size_t)round_up(norm_plan(c, true).parts * c.H * 4, 256);
+    return (size_t)round_up(norm_plan(c).parts * c.H * 4, 256);
 }
 
 // f by the types of x and y, and whether rows are whole vectors
@@ -685,25 +785,22 @@ size_t norm_part_bytes(const mok_norm_config &c) {
 template <bool X32, bool Y32, bool WHOLE>
 cudaError_t launch_norm(NormFwd a, const NormPlan &p, cudaStream_t s) {
     constexpr int NV = X32 || Y32 ? 1 : 2;
-    a.s.tpr = p.tpr;
-    if (p.nv == 0)
+    if (p.tpr == 0)
         return launch_edge(norm_long_kernel<X32, Y32>, (unsigned)a.s.rows, 1024, 0, 1, s, a);
-    const int64_t most = (int64_t)device_sm_count() * (1024 / p.tpb);
-    const unsigned grid = (unsigned)(p.groups < most ? p.groups : most);
-    if constexpr (NV == 1)
-        if (!p.ahead)
-            return launch_edge(norm_kernel<2 * NV, X32, Y32, WHOLE, false, 1024>, grid, p.tpb, 0, 1, s, a);
-    if (p.tpb > NORM_TPB)
-        return launch_edge(norm_kernel<NV, X32, Y32, WHOLE, true, 1024>, grid, p.tpb, 0, 1, s, a);
-    return launch_edge(norm_kernel<NV, X32, Y32, WHOLE, true, NORM_TPB>, grid, p.tpb, 0, 1, s, a);
+    a.s.tpr = p.tpr;
+    a.s.cluster = p.cluster;
+    const int64_t all = (int64_t)device_sm_count() * (1024 / p.tpb) / p.cluster, most = all > 1 ? all : 1;
+    const unsigned grid = (unsigned)((p.groups < most ? p.groups : most) * p.cluster);
+    return p.cluster > 1
+               ? launch_edge(norm_kernel<NV, X32, Y32, WHOLE, true>, grid, p.tpb, 0, p.cluster, s, a)
+               : launch_edge(norm_kernel<NV, X32, Y32, WHOLE, false>, grid, p.tpb, 0, 1, s, a);
 }
 
 template <bool X32, bool Y32, bool WHOLE>
 cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, cudaStream_t s) {
     constexpr int NV = X32 || Y32 ? 1 : 2;
-    a.s.tpr = p.tpr;
     const bool sums = a.dw_part != nullptr || a.db_part != nullptr;
-    if (p.nv == 0) {
+    if (p.tpr == 0) {
         const dim3 cols((unsigned)((a.s.H + 8 * COLUMNS_TPB - 1) / (8 * COLUMNS_TPB)),
                         (unsigned)p.parts);
         cudaError_t e = cudaSuccess;
@@ -711,18 +808,14 @@ cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, cudaStream_t s) {
         if (e != cudaSuccess || a.dx == nullptr) return e;
         return launch_edge(norm_backward_long_kernel<X32, Y32>, (unsigned)a.s.rows, 1024, 0, 1, s, a);
     }
-    // the teams' sums of a block: at most 8 nv floats a thread
-    const int smem = sums ? p.tpb / p.tpr * a.s.H * 4 : 0;
-    const unsigned grid = (unsigned)p.parts;
-    if (p.ahead)
-        return launch_edge(norm_backward_kernel<NV, X32, Y32, WHOLE, true>, grid, p.tpb, smem, 1, s, a);
-    const auto wide = norm_backward_kernel<2 * NV, X32, Y32, WHOLE, false>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            wide, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * 2 * NV * NORM_TPB * 4);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_edge(wide, grid, p.tpb, smem, 1, s, a);
+    a.s.tpr = p.tpr;
+    a.s.cluster = p.cluster;
+    const int smem = sums ? p.tpb * NV * 8 * 4 : 0;  // the teams' sums of a block
+    const unsigned grid = (unsigned)(p.parts * p.cluster);
+    return p.cluster > 1 ? launch_edge(norm_backward_kernel<NV, X32, Y32, WHOLE, true>, grid, p.tpb,
+                                       smem, p.cluster, s, a)
+                         : launch_edge(norm_backward_kernel<NV, X32, Y32, WHOLE, false>, grid, p.tpb,
+                                       smem, 1, s, a);
 }
 
 }  // namespace
@@ -768,9 +861,9 @@ mok_status mok_norm_forward(const mok_norm_config *c, const void *x, const void 
     const void *ps[] = {x, residual, weight, bias, h, y, mean, rstd};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    const NormFwd a{norm_shape(*c), x, residual, weight, bias, h, y, mean, rstd};
+    const NormFwd a{norm_shape(*c, status), x, residual, weight, bias, h, y, mean, rstd};
     MOK_OP_LAUNCH(OP_NORM, 1,
-                  MOK_NORM_TYPES(launch_norm, a, norm_plan(*c, false), stream));
+                  MOK_NORM_TYPES(launch_norm, a, norm_plan(*c), stream));
     return MOK_OK;
 }
 
@@ -793,11 +886,11 @@ mok_status mok_norm_backward(const mok_norm_config *c, const void *h, const floa
     const void *ps[] = {h, mean, rstd, weight, dy, dh, dx, dw, db};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    const NormPlan plan = norm_plan(*c, true);
+    const NormPlan plan = norm_plan(*c);
     float *wp = dw ? (float *)ws : nullptr;
     float *bp = db ? (float *)((char *)ws + norm_part_bytes(*c)) : nullptr;
     if (c->rows > 0) {
-        const NormBwd a{norm_shape(*c), h, dy, dh, mean, rstd, weight, dx, wp, bp};
+        const NormBwd a{norm_shape(*c, status), h, dy, dh, mean, rstd, weight, dx, wp, bp};
         MOK_OP_LAUNCH(OP_NORM_BWD, 1,
                       MOK_NORM_TYPES(launch_norm_backward, a, plan, stream));
     }

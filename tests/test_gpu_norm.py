@@ -104,7 +104,8 @@ CASES = [
     dict(R=700, H=1000, y="fp32"), dict(R=9, H=4100, kind="rms", x="fp32", y="bf16"),
     dict(R=6000, H=512), dict(R=5, H=8193), dict(R=4, H=16384, x="fp32", y="fp32"),
     dict(R=3, H=30001, kind="rms"), dict(R=3, H=32768, x="fp32", y="fp32"),
-    dict(R=40, H=32776, extra=8), dict(R=2, H=100003, x="fp32", y="fp32"),
+    dict(R=40, H=32776, extra=8), dict(R=700, H=9000), dict(R=500, H=20000, x="fp32"),
+    dict(R=11, H=65536), dict(R=11, H=65544, extra=8), dict(R=2, H=100003, x="fp32", y="fp32"),
     dict(R=2, H=1 << 20, kind="rms", res=False),
 ]
 
@@ -185,7 +186,7 @@ def test_backward(kw):
                                    (True, False, True), (False, True, True)], ids=str)
 def test_backward_parts_have_the_same_bits(parts):
     torch = _t()
-    for H in (520, 40000):
+    for H in (520, 40000, 70000):  # a block's rows, a cluster's, rows that are read again
         c = Case(R=300 if H < 1000 else 40, H=H)
         *ins, dx, dw, db = check_backward(c)
         out = c.backward(*ins, parts)
@@ -256,7 +257,8 @@ def test_a_row_that_is_not_finite_spoils_itself_alone():
         assert device_ok()
 
 
-@pytest.mark.parametrize("kw", [dict(R=40, H=520, x="fp32", y="fp32"), dict(R=20, H=40000)], ids=str)
+@pytest.mark.parametrize("kw", [dict(R=40, H=520, x="fp32", y="fp32"), dict(R=20, H=40000),
+                                dict(R=20, H=70000)], ids=str)
 def test_in_place(kw):
     torch = _t()
     c = Case(**dict(kw, extra=0))
