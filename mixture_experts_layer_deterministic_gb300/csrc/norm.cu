@@ -6,9 +6,12 @@
 // All of it is HBM traffic. A row belongs to a team, a power of two of threads up to a warp or some
 // warps of a block, that hold NV vectors of 8 elements each; long rows are cut over the blocks of a
 // cluster, which exchange their sums through each other's shared memory. Blocks walk over the rows, and
-// a team's next row is on its way while it works on the last, so that the loads never pause. Rows too
+// a thread's pieces of the next rows are on their way to shared memory of its own (cp.async, which also
+// fills in the zeros past a row's end), so that the loads never pause and hold no registers. Rows too
 // long for a cluster are read again instead. The mean is taken in two steps (of h, then of h less the first), so
 // that rows far from zero keep their digits; the variance is that of h less the mean.
+#include <atomic>
+
 #include "ops_internal.h"
 #include "tc.cuh"
 
@@ -25,9 +28,9 @@ struct Raw {
     uint4 v[F32 ? 2 : 1];
 };
 // 8 elements from column c on, zeros past H (F32: two vectors)
-template <bool F32, bool WHOLE = false>
+template <bool F32>
 MOK_DEV void load8(const void *row, int c, int H, float (&v)[8]) {
-    if (WHOLE || c + 8 <= H) {
+    if (c + 8 <= H) {
         if (F32) {
             const uint4 a = ld_v4(static_cast<const float *>(row) + c);
             const uint4 b = ld_v4(static_cast<const float *>(row) + c + 4);
@@ -56,9 +59,9 @@ MOK_DEV uint32_t pack(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-template <bool F32, bool WHOLE = false>
+template <bool F32>
 MOK_DEV void store8(void *row, int c, int H, const float (&v)[8]) {
-    if (WHOLE || c + 8 <= H) {
+    if (c + 8 <= H) {
         if (F32) {
             float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(row) + c);
             p[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -77,6 +80,11 @@ MOK_DEV void store8(void *row, int c, int H, const float (&v)[8]) {
                 static_cast<uint16_t *>(row)[c + j] = f32_to_bf16(v[j]);
         }
     }
+}
+// `left` of 8 elements at p
+template <bool F32>
+MOK_DEV void store_left(void *p, int left, const float (&v)[8]) {
+    store8<F32>(p, 0, left, v);
 }
 // as it will be read back
 template <bool F32>
@@ -131,10 +139,10 @@ MOK_DEV void *row_of(void *p, int64_t r, int64_t ld) {
     return static_cast<char *>(p) + r * ld * (F32 ? 4 : 2);
 }
 
-// 8 elements from column c on, zeros past H; where rows are WHOLE vectors there is nothing past H
-template <bool F32, bool WHOLE>
+// 8 elements from column c on, zeros past H
+template <bool F32>
 MOK_DEV void load_raw(const void *row, int c, int H, Raw<F32> &q) {
-    if (WHOLE || c + 8 <= H) {
+    if (c + 8 <= H) {
         if (F32) {
             q.v[0] = ld_v4(static_cast<const float *>(row) + c);
             q.v[F32 ? 1 : 0] = ld_v4(static_cast<const float *>(row) + c + 4);
@@ -171,6 +179,49 @@ MOK_DEV void unpack(const Raw<F32> &q, float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         v[j] = F32 ? __uint_as_float(w[j]) : (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+}
+
+// A thread's pieces of the rows ahead: `stages` rows of UNITS 16-byte units, each in a place of its own.
+// Nobody else reads them, so there is no barrier; a place is filled again when its row is done with.
+struct Ahead {
+    uint32_t base, stage_bytes, unit_bytes;
+    MOK_DEV Ahead(void *smem, int units) {
+        unit_bytes = blockDim.x * 16;
+        stage_bytes = unit_bytes * units;
+        base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+    }
+    MOK_DEV uint32_t at(int stage, int unit) const { return base + stage * stage_bytes + unit * unit_bytes; }
+    // `left` elements (up to 8) from p on into unit `u` (and the next), zeros for the rest; nothing is
+    // read where there are none, p has to be an address all the same
+    template <bool F32>
+    MOK_DEV void fetch(int stage, int u, const void *p, int left) const {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+            const int bytes = F32 ? min(max(4 * left - 16 * i, 0), 16) : 2 * left;
+            const char *q = static_cast<const char *>(p) + (bytes > 0 ? 16 * i : 0);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, u + i)), "l"(q),
+                         "r"(bytes)
+                         : "memory");
+        }
+    }
+    template <bool F32>
+    MOK_DEV void take(int stage, int u, Raw<F32> &q) const {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(q.v[i].x), "=r"(q.v[i].y), "=r"(q.v[i].z), "=r"(q.v[i].w)
+                         : "r"(at(stage, u + i))
+                         : "memory");
+    }
+    MOK_DEV static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    template <int N>
+    MOK_DEV static void wait() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    }
+};
+template <bool F32>
+constexpr int units_of() {
+    return F32 ? 2 : 1;
 }
 
 // Where a thread's vectors lie: number k is column 8 (first + k tpr).
@@ -215,23 +266,35 @@ struct TeamSum {
             together();  // all blocks are there to be sent to
         }
     }
-    MOK_DEV void operator()(float &a, float &b) {
-        const int w = tpr < 32 ? tpr : 32;
-        for (int o = 1; o < w; o <<= 1) {
+    MOK_DEV void operator()(float &a) {
+        float none = 0.0f;
+        add<false>(a, none);
+    }
+    MOK_DEV void operator()(float &a, float &b) { add<true>(a, b); }
+    template <bool TWO>
+    MOK_DEV void add(float &a, float &b) {
+        const auto warp_sum = [&](int o) {
             a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            if (TWO) b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        };
+        if (tpr < 32) {
+            for (int o = 1; o < tpr; o <<= 1) warp_sum(o);
+            return;
         }
-        if (tpr <= 32) return;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) warp_sum(o);
+        if (tpr == 32) return;
         const int warp = threadIdx.x >> 5, n = tpr / 32, team = warp / n;
         const uint32_t turn = calls & 1;
         float2 *s = sh->warps[turn];
         if ((threadIdx.x & 31) == 0) s[warp] = make_float2(a, b);
         asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(tpr) : "memory");
         a = b = 0.0f;
+#pragma unroll 4
         for (int k = 0; k < n; ++k) {
             const float2 v = s[team * n + k];
             a += v.x;
-            b += v.y;
+            if (TWO) b += v.y;
         }
         if constexpr (CLUSTER) {
             uint64_t *bar = &sh->arrived[turn];
@@ -303,6 +366,14 @@ struct NormFwd {
     float *mean, *rstd;
 };
 
+// Vectors a thread, and rows ahead: what 128 registers and 192 KB of 512 threads hold. More vectors a
+// thread cost less per element: a row's own work is some 100 instructions a warp.
+template <bool X32>
+constexpr int fwd_vecs() {
+    return X32 ? 2 : 4;
+}
+constexpr int FWD_STAGES = 3;
+
 // columns past H of a vector are zeros: they add to no sum but that of (0 - mean)^2
 MOK_DEV float square_from(const float (&v)[8], float mean, int n) {
     float q = 0.0f;
@@ -312,109 +383,164 @@ MOK_DEV float square_from(const float (&v)[8], float mean, int n) {
     return q;
 }
 
-template <bool Y32, bool WHOLE = false>
+template <bool Y32>
 MOK_DEV void store_y(const NormFwd &a, int64_t r, int c, float mean, float rest, float rstd,
                      float (&v)[8]) {
     float p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (v[j] - mean - rest) * rstd;
     if (a.w != nullptr) {
-        load8<true, WHOLE>(a.w, c, a.s.H, p);
+        load8<true>(a.w, c, a.s.H, p);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= p[j];
     }
     if (a.b != nullptr) {
-        load8<true, WHOLE>(a.b, c, a.s.H, p);
+        load8<true>(a.b, c, a.s.H, p);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += p[j];
     }
-    store8<Y32, WHOLE>(row_of<Y32>(a.y, r, a.s.ld_y), c, a.s.H, v);
+    store8<Y32>(row_of<Y32>(a.y, r, a.s.ld_y), c, a.s.H, v);
 }
 
-// the vectors of one row that a thread holds
-template <int NV, bool X32, bool WHOLE>
-struct NormRow {
-    Raw<X32> x[NV], res[NV];
-    // i: the first of the thread's vectors
-    MOK_DEV void load(const NormFwd &a, int64_t r, int i) {
-        const void *px = row_of<X32>(a.x, r, a.s.ld_x), *pr = row_of<X32>(a.res, r, a.s.ld_x);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (i + k * a.s.tpr);
-            x[k].v[0] = x[k].v[X32] = make_uint4(0, 0, 0, 0);
-            res[k].v[0] = res[k].v[X32] = make_uint4(0, 0, 0, 0);
-            if (r < a.s.rows && c < a.s.H) {
-                load_raw<X32, WHOLE>(px, c, a.s.H, x[k]);
-                if (a.res != nullptr) load_raw<X32, WHOLE>(pr, c, a.s.H, res[k]);
-            }
-        }
-    }
-};
-
-template <int NV, bool X32, bool Y32, bool WHOLE, bool CLUSTER>
-__global__ void __launch_bounds__(NORM_TPB, 2) norm_kernel(const NormFwd a) {
+template <bool X32, bool Y32, bool CLUSTER>
+__global__ void __launch_bounds__(NORM_TPB) norm_kernel(const NormFwd a) {
+    extern __shared__ __align__(16) uint8_t norm_smem[];
     __shared__ NormShared sh;
+    constexpr int U = units_of<X32>(), NV = fwd_vecs<X32>(), XS = X32 ? 4 : 2, YS = Y32 ? 4 : 2;
     const NormShape &s = a.s;
     const uint32_t rank = block_of_cluster<CLUSTER>();
     TeamSum<CLUSTER> team_sum(&sh, s, rank);
+    const Ahead ahead(norm_smem, 2 * NV * U);
     let_next_start();
     wait_for_previous();
     const Place at(s, NV, rank);
-    const int i = at.first;
     const int64_t walkers = CLUSTER ? gridDim.x / s.cluster : gridDim.x;
     const int64_t walker = CLUSTER ? blockIdx.x / s.cluster : blockIdx.x, step = walkers * at.slots;
-    NormRow<NV, X32, WHOLE> row;
-    row.load(a, walker * at.slots + at.slot, i);
-    for (int64_t r0 = walker * at.slots; r0 < s.rows; r0 += step) {
-        const int64_t r = r0 + at.slot;
-        float v[NV][8];
-        float sum = 0.0f, rest = 0.0f, sq = 0.0f;
+    const int64_t first = walker * at.slots + at.slot;
+    // the thread's vectors, and what of them is in the row
+    int col[NV], left[NV];
+    float w[NV][8], b[NV][8];  // weight and bias stay: from memory they would be waited for in every row
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            unpack<X32>(row.x[k], v[k]);
-            if (a.res != nullptr) {
-                float q[8];
-                unpack<X32>(row.res[k], q);
+    for (int k = 0; k < NV; ++k) {
+        const int c = 8 * (at.first + k * s.tpr);
+        left[k] = min(max(s.H - c, 0), 8);
+        col[k] = left[k] > 0 ? c : 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[k][j] = rounded<X32>(v[k][j] + q[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum += v[k][j];
-        }
-        if (r0 + step < s.rows) row.load(a, r + step, i);
-        float mean = 0.0f;
-        if (s.layer) {
-            team_sum(sum, rest);
-            mean = sum / s.H;
-        }
-        rest = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (i + k * s.tpr), n = c >= s.H ? 0 : WHOLE ? 8 : s.H - c;
-            sq += square_from(v[k], mean, n);
-            if (s.layer)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n) rest += v[k][j] - mean;
-        }
-        team_sum(sq, rest);
-        rest /= s.H;  // what the mean's rounding left
-        const float var = fmaxf(sq / s.H - rest * rest, 0.0f);
-        const float rstd = 1.0f / sqrtf(var + s.eps);
-        if (r < s.rows) {
-            if (i == 0) {
-                if (a.mean != nullptr) a.mean[r] = mean + rest;
-                if (a.rstd != nullptr) a.rstd[r] = rstd;
-            }
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = 8 * (i + k * s.tpr);
-                if (c >= s.H) continue;
-                if (a.h != nullptr) store8<X32, WHOLE>(row_of<X32>(a.h, r, s.ld_x), c, s.H, v[k]);
-                store_y<Y32, WHOLE>(a, r, c, mean, rest, rstd, v[k]);
-            }
+        for (int j = 0; j < 8; ++j) {
+            w[k][j] = a.w != nullptr && c + j < s.H ? a.w[c + j] : 1.0f;
+            b[k][j] = a.b != nullptr && c + j < s.H ? a.b[c + j] : 0.0f;
         }
     }
+    const char *px = static_cast<const char *>(row_of<X32>(a.x, first, s.ld_x));
+    const char *pr = static_cast<const char *>(row_of<X32>(a.res, first, s.ld_x));
+    const int64_t dx = step * s.ld_x * XS;
+    const auto fetch = [&](int stage, int64_t r) {
+        const bool in = r < s.rows;
+        const char *qx = in ? px : static_cast<const char *>(a.x), *qr = in ? pr : static_cast<const char *>(a.res);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            ahead.fetch<X32>(stage, k * U, qx + col[k] * XS, in ? left[k] : 0);
+            if (a.res != nullptr) ahead.fetch<X32>(stage, (NV + k) * U, qr + col[k] * XS, in ? left[k] : 0);
+        }
+        ahead.commit();
+        px += dx;
+        pr += dx;
+    };
+#pragma unroll
+    for (int k = 0; k < FWD_STAGES; ++k) fetch(k, first + k * step);
+    char *ph = static_cast<char *>(row_of<X32>(a.h, first, s.ld_x));
+    char *py = static_cast<char *>(row_of<Y32>(a.y, first, s.ld_y));
+    const int64_t dy = step * s.ld_y * YS;
+    const float inv_n = 1.0f / s.H;
+    int stage = 0;
+    for (int64_t r = first, r0 = walker * at.slots; r0 < s.rows; r0 += step, r += step, ph += dx, py += dy) {
+        const bool in = r < s.rows;
+        ahead.wait<FWD_STAGES - 1>();
+        f32x2 v[NV][4], sum2 = 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            Raw<X32> q;
+            ahead.take<X32>(stage, k * U, q);
+            unpack<X32>(q, v[k]);
+            if (a.res != nullptr) {
+                Raw<X32> e;
+                f32x2 f[4];
+                ahead.take<X32>(stage, (NV + k) * U, e);
+                unpack<X32>(e, f);
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[k][j] = add2(v[k][j], f[j]);
+                    if (!X32) {  // as it is stored, and read by the backward pass
+                        const uint32_t p = pack(both(v[k][j]).x, both(v[k][j]).y);
+                        v[k][j] = pair(bf16_lo(p), bf16_hi(p));
+                    }
+                    o[2 * j] = both(v[k][j]).x;
+                    o[2 * j + 1] = both(v[k][j]).y;
+                }
+                if (a.h != nullptr && in) store_left<X32>(ph + col[k] * XS, left[k], o);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum2 = add2(sum2, v[k][j]);
+        }
+        float mean = 0.0f, rest = 0.0f;
+        if (s.layer) {
+            mean = both(sum2).x + both(sum2).y;
+            team_sum(mean);
+            mean *= inv_n;
+            const f32x2 minus = pair(-mean, -mean);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[k][j] = add2(v[k][j], minus);
+                    if (2 * j + 1 >= left[k]) {  // past the row
+                        const float2 d = both(v[k][j]);
+                        v[k][j] = pair(2 * j < left[k] ? d.x : 0.0f, 0.0f);
+                    }
+                }
+        }
+        f32x2 sq2 = 0, rest2 = 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sq2 = fma2(v[k][j], v[k][j], sq2);
+                rest2 = add2(rest2, v[k][j]);
+            }
+        float sq = both(sq2).x + both(sq2).y;
+        if (s.layer) {
+            rest = both(rest2).x + both(rest2).y;
+            team_sum(sq, rest);
+            rest *= inv_n;  // what the mean's rounding left
+        } else {
+            team_sum(sq);
+        }
+        fetch(stage, r + FWD_STAGES * step);
+        stage = stage + 1 == FWD_STAGES ? 0 : stage + 1;
+        const float var = fmaxf(sq * inv_n - rest * rest, 0.0f);
+        const float rstd = 1.0f / sqrtf(var + s.eps);
+        if (!in) continue;
+        if (at.first == 0) {
+            if (a.mean != nullptr) a.mean[r] = mean + rest;
+            if (a.rstd != nullptr) a.rstd[r] = rstd;
+        }
+        const f32x2 scale = pair(rstd, rstd), shift = pair(-rest * rstd, -rest * rstd);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (left[k] == 0) continue;
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f32x2 n = fma2(v[k][j], scale, shift);
+                const f32x2 y = fma2(n, pair(w[k][2 * j], w[k][2 * j + 1]), pair(b[k][2 * j], b[k][2 * j + 1]));
+                o[2 * j] = both(y).x;
+                o[2 * j + 1] = both(y).y;
+            }
+            store_left<Y32>(py + col[k] * YS, left[k], o);
+        }
+    }
+    ahead.wait<0>();
     team_sum.together();  // nobody sends to a block that has left
 }
 
@@ -515,111 +641,143 @@ MOK_DEV void store_dx(const NormBwd &a, int64_t r, int c, float rstd, float mg, 
     store8<X32>(row_of<X32>(a.dx, r, a.s.ld_x), c, a.s.H, v);
 }
 
-// the vectors of one row that a thread holds
-template <int NV, bool X32, bool Y32, bool WHOLE>
-struct NormBwdRow {
-    Raw<X32> h[NV], dh[NV];
-    Raw<Y32> dy[NV];
-    float mean, rstd;
-    MOK_DEV void load(const NormBwd &a, int64_t r, int i) {
-        const NormShape &s = a.s;
-        const bool in = r < s.rows;
-        const void *ph = row_of<X32>(a.h, r, s.ld_x), *pd = row_of<X32>(a.dh, r, s.ld_x);
-        const void *py = row_of<Y32>(a.dy, r, s.ld_y);
-        mean = in && s.layer ? a.mean[r] : 0.0f;
-        rstd = in ? a.rstd[r] : 0.0f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (i + k * s.tpr);
-            h[k].v[0] = h[k].v[X32] = dh[k].v[0] = dh[k].v[X32] = make_uint4(0, 0, 0, 0);
-            dy[k].v[0] = dy[k].v[Y32] = make_uint4(0, 0, 0, 0);
-            if (in && c < s.H) {
-                load_raw<X32, WHOLE>(ph, c, s.H, h[k]);
-                load_raw<Y32, WHOLE>(py, c, s.H, dy[k]);
-                if (a.dh != nullptr) load_raw<X32, WHOLE>(pd, c, s.H, dh[k]);
-            }
-        }
-    }
-};
+constexpr int BWD_VECS = 2;  // of a thread: their sums and products take 80 registers
+// rows ahead: up to three of what 192 KB hold
+template <bool X32, bool Y32>
+constexpr int bwd_units() {
+    return BWD_VECS * (2 * units_of<X32>() + units_of<Y32>());
+}
+template <bool X32, bool Y32>
+constexpr int bwd_stages() {
+    return bwd_units<X32, Y32>() <= 8 ? 3 : 2;
+}
 
 // The teams of block (or cluster) b take the b-th, (b + blocks)-th, .. rows, keep their columns' sums in
 // registers and add them in order at the end.
-template <int NV, bool X32, bool Y32, bool WHOLE, bool CLUSTER>
+template <bool X32, bool Y32, bool CLUSTER>
 __global__ void __launch_bounds__(NORM_TPB) norm_backward_kernel(const NormBwd a) {
-    extern __shared__ float norm_smem[];
+    extern __shared__ __align__(16) uint8_t norm_smem[];
     __shared__ NormShared sh;
+    constexpr int UX = units_of<X32>(), UY = units_of<Y32>(), NV = BWD_VECS;
+    constexpr int STAGES = bwd_stages<X32, Y32>(), XS = X32 ? 4 : 2, YS = Y32 ? 4 : 2;
     const NormShape &s = a.s;
     const uint32_t rank = block_of_cluster<CLUSTER>();
     TeamSum<CLUSTER> team_sum(&sh, s, rank);
+    const Ahead ahead(norm_smem, bwd_units<X32, Y32>());
     let_next_start();
     wait_for_previous();
     const Place at(s, NV, rank);
-    const int i = at.first;
     const int64_t walkers = CLUSTER ? gridDim.x / s.cluster : gridDim.x;
     const int64_t walker = CLUSTER ? blockIdx.x / s.cluster : blockIdx.x, step = walkers * at.slots;
+    const int64_t first = walker * at.slots + at.slot;
     f32x2 dw[NV][4], db[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) dw[k][j] = db[k][j] = 0;
-    // the weights of vector k, ones without them and past the row
-    const auto weights = [&](int c, f32x2 (&w)[4]) {
-        Raw<true> q;
-        q.v[0] = q.v[1] = make_uint4(0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u);
-        if (a.w != nullptr && c < s.H) load_raw<true, WHOLE>(a.w, c, s.H, q);
-        unpack<true>(q, w);
-    };
-    NormBwdRow<NV, X32, Y32, WHOLE> row;
-    row.load(a, walker * at.slots + at.slot, i);
-    for (int64_t r0 = walker * at.slots; r0 < s.rows; r0 += step) {
-        const int64_t r = r0 + at.slot;
-        // with t = h - mean: n = t rstd, so sum(g n) = rstd sum(g t). Past H dy is zero, so t does not
-        // matter there
-        const float row_rstd = row.rstd;
-        const f32x2 mean = pair(-row.mean, -row.mean), rstd = pair(row_rstd, row_rstd);
-        f32x2 t[NV][4], g[NV][4], sg2 = 0, sgt2 = 0;
-        Raw<X32> dh[NV];
+    // the thread's vectors, and what of them is in the row
+    int col[NV], left[NV];
+    f32x2 w[NV][4];  // the weights stay: from memory they would be waited for in every row
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = 8 * (at.first + k * s.tpr);
+        left[k] = min(max(s.H - c, 0), 8);
+        col[k] = left[k] > 0 ? c : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[k][j] = pair(a.w != nullptr && c + 2 * j < s.H ? a.w[c + 2 * j] : 1.0f,
+                           a.w != nullptr && c + 2 * j + 1 < s.H ? a.w[c + 2 * j + 1] : 1.0f);
+    }
+    // h, dy, dh of a row
+    const char *ph = static_cast<const char *>(row_of<X32>(a.h, first, s.ld_x));
+    const char *pd = static_cast<const char *>(row_of<X32>(a.dh, first, s.ld_x));
+    const char *py = static_cast<const char *>(row_of<Y32>(a.dy, first, s.ld_y));
+    const int64_t dx = step * s.ld_x * XS, dy = step * s.ld_y * YS;
+    const auto fetch = [&](int stage, int64_t r) {
+        const bool in = r < s.rows;
+        const char *qh = in ? ph : static_cast<const char *>(a.h);
+        const char *qd = in ? pd : static_cast<const char *>(a.dh);
+        const char *qy = in ? py : static_cast<const char *>(a.dy);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            f32x2 w[4];
-            unpack<X32>(row.h[k], t[k]);
-            unpack<Y32>(row.dy[k], g[k]);
-            dh[k] = row.dh[k];
-            weights(8 * (i + k * s.tpr), w);
+            const int n = in ? left[k] : 0;
+            ahead.fetch<X32>(stage, k * UX, qh + col[k] * XS, n);
+            ahead.fetch<Y32>(stage, NV * UX + k * UY, qy + col[k] * YS, n);
+            if (a.dh != nullptr)
+                ahead.fetch<X32>(stage, NV * (UX + UY) + k * UX, qd + col[k] * XS, n);
+        }
+        ahead.commit();
+        ph += dx;
+        pd += dx;
+        py += dy;
+    };
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k) fetch(k, first + k * step);
+    float next_mean = s.layer && first < s.rows ? a.mean[first] : 0.0f;
+    float next_rstd = first < s.rows ? a.rstd[first] : 0.0f;
+    char *out_row = static_cast<char *>(row_of<X32>(a.dx, first, s.ld_x));
+    const float inv_n = 1.0f / s.H;
+    int stage = 0;
+    for (int64_t r = first, r0 = walker * at.slots; r0 < s.rows; r0 += step, r += step, out_row += dx) {
+        // with t = h - mean: n = t rstd, so sum(g n) = rstd sum(g t). Past H dy is zero, so t does not
+        // matter there
+        const float row_rstd = next_rstd;
+        const f32x2 mean = pair(-next_mean, -next_mean), rstd = pair(row_rstd, row_rstd);
+        next_mean = s.layer && r + step < s.rows ? a.mean[r + step] : 0.0f;
+        next_rstd = r + step < s.rows ? a.rstd[r + step] : 0.0f;
+        f32x2 t[NV][4], g[NV][4], sg2 = 0, sgt2 = 0;
+        ahead.wait<STAGES - 1>();
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            Raw<X32> q;
+            Raw<Y32> y;
+            ahead.take<X32>(stage, k * UX, q);
+            ahead.take<Y32>(stage, NV * UX + k * UY, y);
+            unpack<X32>(q, t[k]);
+            unpack<Y32>(y, g[k]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 t[k][j] = add2(t[k][j], mean);
                 dw[k][j] = fma2(mul2(g[k][j], rstd), t[k][j], dw[k][j]);
                 db[k][j] = add2(db[k][j], g[k][j]);
-                g[k][j] = mul2(g[k][j], w[j]);
+                g[k][j] = mul2(g[k][j], w[k][j]);
                 sg2 = add2(sg2, g[k][j]);
                 sgt2 = fma2(g[k][j], t[k][j], sgt2);
             }
         }
-        if (r0 + step < s.rows) row.load(a, r + step, i);
-        if (a.dx == nullptr) continue;
-        float sg = both(sg2).x + both(sg2).y, sgt = both(sgt2).x + both(sgt2).y;
-        team_sum(sgt, sg);
-        // dx = dh - rstd mean(g) + g rstd - t rstd^2 mean(g n)
-        const float c0 = s.layer ? -row_rstd * (sg / s.H) : 0.0f;
-        const float c1 = -row_rstd * row_rstd * (row_rstd * (sgt / s.H));
-        const f32x2 a0 = pair(c0, c0), a1 = pair(c1, c1);
+        if (a.dx != nullptr) {
+            float sg = both(sg2).x + both(sg2).y, sgt = both(sgt2).x + both(sgt2).y;
+            team_sum(sgt, sg);
+            // dx = dh - rstd mean(g) + g rstd - t rstd^2 mean(g n)
+            const float c0 = s.layer ? -row_rstd * (sg * inv_n) : 0.0f;
+            const float c1 = -row_rstd * row_rstd * (row_rstd * (sgt * inv_n));
+            const f32x2 a0 = pair(c0, c0), a1 = pair(c1, c1);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = 8 * (i + k * s.tpr);
-            if (r >= s.rows || c >= s.H) continue;
-            f32x2 v[4];
-            unpack<X32>(dh[k], v);
-            float o[8];
+            for (int k = 0; k < NV; ++k) {
+                if (r >= s.rows || left[k] == 0) continue;
+                f32x2 v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = fma2(t[k][j], a1, fma2(g[k][j], rstd, add2(v[j], a0)));
-                o[2 * j] = both(v[j]).x;
-                o[2 * j + 1] = both(v[j]).y;
+                for (int j = 0; j < 4; ++j) v[j] = 0;
+                if (a.dh != nullptr) {
+                    Raw<X32> q;
+                    ahead.take<X32>(stage, NV * (UX + UY) + k * UX, q);
+                    unpack<X32>(q, v);
+                }
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = fma2(t[k][j], a1, fma2(g[k][j], rstd, add2(v[j], a0)));
+                    o[2 * j] = both(v[j]).x;
+                    o[2 * j + 1] = both(v[j]).y;
+                }
+                store_left<X32>(out_row + col[k] * XS, left[k], o);
             }
-            store8<X32, WHOLE>(row_of<X32>(a.dx, r, s.ld_x), c, s.H, o);
         }
+        fetch(stage, r + STAGES * step);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
+    ahead.wait<0>();
+    float *sums = reinterpret_cast<float *>(norm_smem);
     for (int part = 0; part < 2; ++part) {
         float *out = part == 0 ? a.dw_part : a.db_part;
         if (out == nullptr) continue;
@@ -627,17 +785,17 @@ __global__ void __launch_bounds__(NORM_TPB) norm_backward_kernel(const NormBwd a
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int at_smem = at.slot * width + 8 * (i + k * s.tpr) - c0;
+            const int at_smem = at.slot * width + 8 * (at.first + k * s.tpr) - c0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float2 v = both(part == 0 ? dw[k][j >> 1] : db[k][j >> 1]);
-                norm_smem[at_smem + j] = (j & 1) ? v.y : v.x;
+                sums[at_smem + j] = (j & 1) ? v.y : v.x;
             }
         }
         __syncthreads();
         for (int c = threadIdx.x; c < width && c0 + c < s.H; c += blockDim.x) {
             float t = 0.0f;
-            for (int k = 0; k < at.slots; ++k) t += norm_smem[k * width + c];
+            for (int k = 0; k < at.slots; ++k) t += sums[k * width + c];
             out[walker * s.H + c0 + c] = t;
         }
     }
@@ -738,16 +896,16 @@ NormShape norm_shape(const mok_norm_config &c, int *status) {
     return NormShape{c.rows, c.ld_x, c.ld_y, c.H, 1024, 1, c.kind == MOK_NORM_LAYER, c.eps, status};
 }
 
-// How rows are held: two vectors a thread where both types are bf16, one otherwise, which is what the
-// registers hold with the next row's beside them; up to 512 threads a block, up to 8 blocks.
+// How rows are held: up to 512 threads a block, up to 8 blocks.
 struct NormPlan {
     int tpr, tpb, cluster;  // threads of a team and of a block, blocks of a row; tpr 0: read again
     int64_t groups;         // of rows that a block or cluster takes at a time
     int64_t parts;          // of the backward's column sums
 };
-NormPlan norm_plan(const mok_norm_config &c) {
+NormPlan norm_plan(const mok_norm_config &c, bool backward) {
     const int vecs = (c.H + 7) / 8;
-    const int nv = c.x_dtype == MOK_DTYPE_BF16 && c.y_dtype == MOK_DTYPE_BF16 ? 2 : 1;
+    const int nv = backward ? BWD_VECS
+                            : c.x_dtype == MOK_DTYPE_F32 ? fwd_vecs<true>() : fwd_vecs<false>();
     NormPlan p = {};
     p.cluster = (vecs + nv * NORM_TPB - 1) / (nv * NORM_TPB);
     if (p.cluster > MOST_BLOCKS) {
@@ -769,36 +927,65 @@ NormPlan norm_plan(const mok_norm_config &c) {
     return p;
 }
 size_t norm_part_bytes(const mok_norm_config &c) {
-    return (size_t)round_up(norm_plan(c).parts * c.H * 4, 256);
+    return (size_t)round_up(norm_plan(c, true).parts * c.H * 4, 256);
 }
 
-// f by the types of x and y, and whether rows are whole vectors
-#define MOK_NORM_WHOLE(f, X, Y, ...) \
-    (c->H % 8 == 0 ? f<X, Y, true>(__VA_ARGS__) : f<X, Y, false>(__VA_ARGS__))
-#define MOK_NORM_TYPES(f, ...)                                                           \
-    (c->x_dtype == MOK_DTYPE_F32                                                         \
-         ? (c->y_dtype == MOK_DTYPE_F32 ? MOK_NORM_WHOLE(f, true, true, __VA_ARGS__)     \
-                                        : MOK_NORM_WHOLE(f, true, false, __VA_ARGS__))   \
-         : (c->y_dtype == MOK_DTYPE_F32 ? MOK_NORM_WHOLE(f, false, true, __VA_ARGS__)    \
-                                        : MOK_NORM_WHOLE(f, false, false, __VA_ARGS__)))
+// f by the types of x and y
+#define MOK_NORM_TYPES(f, ...)                                                              \
+    (c->x_dtype == MOK_DTYPE_F32                                                            \
+         ? (c->y_dtype == MOK_DTYPE_F32 ? f<true, true>(__VA_ARGS__) : f<true, false>(__VA_ARGS__)) \
+         : (c->y_dtype == MOK_DTYPE_F32 ? f<false, true>(__VA_ARGS__)                       \
+                                        : f<false, false>(__VA_ARGS__)))
 
-template <bool X32, bool Y32, bool WHOLE>
+// a launch with `smem` bytes of shared memory, whose opt-in is set once per device
+template <class... KA, class... A>
+cudaError_t launch_norm_kernel(void (*kernel)(KA...), std::atomic<uint64_t> &attr_set, unsigned grid,
+                               int tpb, int smem, int most_smem, int cluster, cudaStream_t s,
+                               const A &...args) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= MAX_DEV) return cudaErrorInvalidDevice;
+    const uint64_t bit = 1ull << dev;
+    if ((attr_set.load(std::memory_order_acquire) & bit) == 0) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+        if (e != cudaSuccess) return e;
+        attr_set.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return launch_edge(kernel, grid, tpb, smem, cluster, s, args...);
+}
+
+template <bool X32, bool Y32, bool CLUSTER>
+cudaError_t launch_norm_whole(const NormFwd &a, const NormPlan &p, unsigned grid, cudaStream_t s) {
+    static std::atomic<uint64_t> attr_set{0};
+    constexpr int per = FWD_STAGES * 2 * fwd_vecs<X32>() * units_of<X32>() * 16;  // a thread
+    return launch_norm_kernel(norm_kernel<X32, Y32, CLUSTER>, attr_set, grid, p.tpb, per * p.tpb,
+                              per * NORM_TPB, p.cluster, s, a);
+}
+template <bool X32, bool Y32>
 cudaError_t launch_norm(NormFwd a, const NormPlan &p, cudaStream_t s) {
-    constexpr int NV = X32 || Y32 ? 1 : 2;
     if (p.tpr == 0)
         return launch_edge(norm_long_kernel<X32, Y32>, (unsigned)a.s.rows, 1024, 0, 1, s, a);
     a.s.tpr = p.tpr;
     a.s.cluster = p.cluster;
-    const int64_t all = (int64_t)device_sm_count() * (1024 / p.tpb) / p.cluster, most = all > 1 ? all : 1;
+    const int64_t all = (int64_t)device_sm_count() * (NORM_TPB / p.tpb) / p.cluster;
+    const int64_t most = all > 1 ? all : 1;
     const unsigned grid = (unsigned)((p.groups < most ? p.groups : most) * p.cluster);
-    return p.cluster > 1
-               ? launch_edge(norm_kernel<NV, X32, Y32, WHOLE, true>, grid, p.tpb, 0, p.cluster, s, a)
-               : launch_edge(norm_kernel<NV, X32, Y32, WHOLE, false>, grid, p.tpb, 0, 1, s, a);
+    return p.cluster > 1 ? launch_norm_whole<X32, Y32, true>(a, p, grid, s)
+                         : launch_norm_whole<X32, Y32, false>(a, p, grid, s);
 }
 
-template <bool X32, bool Y32, bool WHOLE>
+template <bool X32, bool Y32, bool CLUSTER>
+cudaError_t launch_norm_backward_whole(const NormBwd &a, const NormPlan &p, unsigned grid,
+                                       cudaStream_t s) {
+    static std::atomic<uint64_t> attr_set{0};
+    constexpr int per = bwd_stages<X32, Y32>() * bwd_units<X32, Y32>() * 16;  // a thread
+    static_assert(per >= BWD_VECS * 8 * 4, "the teams' sums of a block go where its rows were");
+    return launch_norm_kernel(norm_backward_kernel<X32, Y32, CLUSTER>, attr_set, grid, p.tpb,
+                              per * p.tpb, per * NORM_TPB, p.cluster, s, a);
+}
+template <bool X32, bool Y32>
 cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, cudaStream_t s) {
-    constexpr int NV = X32 || Y32 ? 1 : 2;
     const bool sums = a.dw_part != nullptr || a.db_part != nullptr;
     if (p.tpr == 0) {
         const dim3 cols((unsigned)((a.s.H + 8 * COLUMNS_TPB - 1) / (8 * COLUMNS_TPB)),
@@ -810,12 +997,9 @@ cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, cudaStream_t s) {
     }
     a.s.tpr = p.tpr;
     a.s.cluster = p.cluster;
-    const int smem = sums ? p.tpb * NV * 8 * 4 : 0;  // the teams' sums of a block
     const unsigned grid = (unsigned)(p.parts * p.cluster);
-    return p.cluster > 1 ? launch_edge(norm_backward_kernel<NV, X32, Y32, WHOLE, true>, grid, p.tpb,
-                                       smem, p.cluster, s, a)
-                         : launch_edge(norm_backward_kernel<NV, X32, Y32, WHOLE, false>, grid, p.tpb,
-                                       smem, 1, s, a);
+    return p.cluster > 1 ? launch_norm_backward_whole<X32, Y32, true>(a, p, grid, s)
+                         : launch_norm_backward_whole<X32, Y32, false>(a, p, grid, s);
 }
 
 }  // namespace
@@ -863,7 +1047,7 @@ mok_status mok_norm_forward(const mok_norm_config *c, const void *x, const void 
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
     const NormFwd a{norm_shape(*c, status), x, residual, weight, bias, h, y, mean, rstd};
     MOK_OP_LAUNCH(OP_NORM, 1,
-                  MOK_NORM_TYPES(launch_norm, a, norm_plan(*c), stream));
+                  MOK_NORM_TYPES(launch_norm, a, norm_plan(*c, false), stream));
     return MOK_OK;
 }
 
@@ -886,7 +1070,7 @@ mok_status mok_norm_backward(const mok_norm_config *c, const void *h, const floa
     const void *ps[] = {h, mean, rstd, weight, dy, dh, dx, dw, db};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    const NormPlan plan = norm_plan(*c);
+    const NormPlan plan = norm_plan(*c, true);
     float *wp = dw ? (float *)ws : nullptr;
     float *bp = db ? (float *)((char *)ws + norm_part_bytes(*c)) : nullptr;
     if (c->rows > 0) {
