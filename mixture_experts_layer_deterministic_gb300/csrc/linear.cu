@@ -1362,6 +1362,8 @@ GradPlan plan_dense_grads(int64_t rows, int N, int Kin, int halves, bool cut) {
                            : grad_clocks(N, kb, w_blocks, Kin, pairs, fixed, most, c));
     };
     GradPlan p = {}, q = {};
+    p.x = p.w = Cut{1, 0, 0};
+    if (rows < 1) return p;  // nothing to run
     const int64_t tx = clocks(true, all, &p.x), tw = clocks(false, all, &p.w);
     p.alone = p.x.height;
     int64_t least = tx + tw + 12000;  // a launch, its fill and its drain

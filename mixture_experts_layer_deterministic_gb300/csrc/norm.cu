@@ -366,13 +366,17 @@ struct NormFwd {
     float *mean, *rstd;
 };
 
-// Vectors a thread, and rows ahead: what 128 registers and 192 KB of 512 threads hold. More vectors a
-// thread cost less per element: a row's own work is some 100 instructions a warp.
-template <bool X32>
-constexpr int fwd_vecs() {
-    return X32 ? 2 : 4;
+// Vectors a thread. A row's own work is some 100 instructions a warp, so long rows take as many vectors
+// as registers and the rows ahead allow: four of bf16 with two sums a row (layer), two with one (RMS, fp32).
+// Short rows take one, which leaves room for two blocks a SM. 16384 x 4096 bf16, layer and RMS: 139 and 90
+// us with one, 117 and 86 with two (6.2 TB/s), 89 and 99 with four; 20000 x 1111: 52, 58, 62; 1000000 x
+// 16: 24, 34, 43.
+int fwd_vecs(const mok_norm_config &c) {
+    if (c.H <= 2048) return 1;
+    return c.x_dtype == MOK_DTYPE_F32 || c.kind == MOK_NORM_RMS ? 2 : 4;
 }
-constexpr int FWD_STAGES = 3;
+constexpr int blocks_of_sm(int nv) { return nv == 1 ? 2 : 1; }
+constexpr int FWD_STAGES = 2;  // three do not help: 92 us for the layer norm above, 89 with two
 
 // columns past H of a vector are zeros: they add to no sum but that of (0 - mean)^2
 MOK_DEV float square_from(const float (&v)[8], float mean, int n) {
@@ -402,11 +406,11 @@ MOK_DEV void store_y(const NormFwd &a, int64_t r, int c, float mean, float rest,
     store8<Y32>(row_of<Y32>(a.y, r, a.s.ld_y), c, a.s.H, v);
 }
 
-template <bool X32, bool Y32, bool CLUSTER>
-__global__ void __launch_bounds__(NORM_TPB) norm_kernel(const NormFwd a) {
+template <int NV, bool X32, bool Y32, bool CLUSTER>
+__global__ void __launch_bounds__(NORM_TPB, NV == 1 ? 2 : 0) norm_kernel(const NormFwd a) {
     extern __shared__ __align__(16) uint8_t norm_smem[];
     __shared__ NormShared sh;
-    constexpr int U = units_of<X32>(), NV = fwd_vecs<X32>(), XS = X32 ? 4 : 2, YS = Y32 ? 4 : 2;
+    constexpr int U = units_of<X32>(), XS = X32 ? 4 : 2, YS = Y32 ? 4 : 2;
     const NormShape &s = a.s;
     const uint32_t rank = block_of_cluster<CLUSTER>();
     TeamSum<CLUSTER> team_sum(&sh, s, rank);
@@ -641,29 +645,31 @@ MOK_DEV void store_dx(const NormBwd &a, int64_t r, int c, float rstd, float mg, 
     store8<X32>(row_of<X32>(a.dx, r, a.s.ld_x), c, a.s.H, v);
 }
 
-constexpr int BWD_VECS = 2;  // of a thread: their sums and products take 80 registers
-// rows ahead: up to three of what 192 KB hold
-template <bool X32, bool Y32>
+// vectors a thread: two, whose sums and products take 80 registers; one for rows of a few (1000000 x 16:
+// 44 us with two, 36 with one; 200000 x 100: 43 and 56)
+int bwd_vecs(const mok_norm_config &c) { return c.H <= 64 ? 1 : 2; }
+// rows ahead: up to three of what 192 KB a SM hold
+template <int NV, bool X32, bool Y32>
 constexpr int bwd_units() {
-    return BWD_VECS * (2 * units_of<X32>() + units_of<Y32>());
+    return NV * (2 * units_of<X32>() + units_of<Y32>());
 }
-template <bool X32, bool Y32>
+template <int NV, bool X32, bool Y32>
 constexpr int bwd_stages() {
-    return bwd_units<X32, Y32>() <= 8 ? 3 : 2;
+    return bwd_units<NV, X32, Y32>() * blocks_of_sm(NV) <= 8 ? 3 : 2;
 }
 
 // The teams of block (or cluster) b take the b-th, (b + blocks)-th, .. rows, keep their columns' sums in
 // registers and add them in order at the end.
-template <bool X32, bool Y32, bool CLUSTER>
-__global__ void __launch_bounds__(NORM_TPB) norm_backward_kernel(const NormBwd a) {
+template <int NV, bool X32, bool Y32, bool CLUSTER>
+__global__ void __launch_bounds__(NORM_TPB, NV == 1 ? 2 : 0) norm_backward_kernel(const NormBwd a) {
     extern __shared__ __align__(16) uint8_t norm_smem[];
     __shared__ NormShared sh;
-    constexpr int UX = units_of<X32>(), UY = units_of<Y32>(), NV = BWD_VECS;
-    constexpr int STAGES = bwd_stages<X32, Y32>(), XS = X32 ? 4 : 2, YS = Y32 ? 4 : 2;
+    constexpr int UX = units_of<X32>(), UY = units_of<Y32>();
+    constexpr int STAGES = bwd_stages<NV, X32, Y32>(), XS = X32 ? 4 : 2, YS = Y32 ? 4 : 2;
     const NormShape &s = a.s;
     const uint32_t rank = block_of_cluster<CLUSTER>();
     TeamSum<CLUSTER> team_sum(&sh, s, rank);
-    const Ahead ahead(norm_smem, bwd_units<X32, Y32>());
+    const Ahead ahead(norm_smem, bwd_units<NV, X32, Y32>());
     let_next_start();
     wait_for_previous();
     const Place at(s, NV, rank);
@@ -898,15 +904,15 @@ NormShape norm_shape(const mok_norm_config &c, int *status) {
 
 // How rows are held: up to 512 threads a block, up to 8 blocks.
 struct NormPlan {
-    int tpr, tpb, cluster;  // threads of a team and of a block, blocks of a row; tpr 0: read again
-    int64_t groups;         // of rows that a block or cluster takes at a time
-    int64_t parts;          // of the backward's column sums
+    int nv, tpr, tpb, cluster;  // threads of a team and of a block, blocks of a row; tpr 0: read again
+    int64_t groups;             // of rows that a block or cluster takes at a time
+    int64_t parts;              // of the backward's column sums
 };
 NormPlan norm_plan(const mok_norm_config &c, bool backward) {
     const int vecs = (c.H + 7) / 8;
-    const int nv = backward ? BWD_VECS
-                            : c.x_dtype == MOK_DTYPE_F32 ? fwd_vecs<true>() : fwd_vecs<false>();
+    const int nv = backward ? bwd_vecs(c) : fwd_vecs(c);
     NormPlan p = {};
+    p.nv = nv;
     p.cluster = (vecs + nv * NORM_TPB - 1) / (nv * NORM_TPB);
     if (p.cluster > MOST_BLOCKS) {
         p.groups = c.rows;
@@ -919,10 +925,11 @@ NormPlan norm_plan(const mok_norm_config &c, bool backward) {
     if (threads > 32) p.tpr = (int)round_up(threads, 32);
     // as many teams as a block holds; with few rows fewer, on more SMs
     int teams = NORM_TPB / p.tpr;
-    while (teams > 1 && p.tpr * teams > 128 && c.rows < NORM_PARTS * teams) teams /= 2;
+    const int64_t blocks = NORM_PARTS * blocks_of_sm(nv);
+    while (teams > 1 && p.tpr * teams > 128 && c.rows < blocks * teams) teams /= 2;
     p.tpb = teams * p.tpr;
     p.groups = (c.rows + teams - 1) / teams;
-    const int64_t most = NORM_PARTS / p.cluster;
+    const int64_t most = blocks / p.cluster;
     p.parts = p.groups < most ? p.groups : most;
     return p;
 }
@@ -955,12 +962,17 @@ cudaError_t launch_norm_kernel(void (*kernel)(KA...), std::atomic<uint64_t> &att
     return launch_edge(kernel, grid, tpb, smem, cluster, s, args...);
 }
 
-template <bool X32, bool Y32, bool CLUSTER>
-cudaError_t launch_norm_whole(const NormFwd &a, const NormPlan &p, unsigned grid, cudaStream_t s) {
-    static std::atomic<uint64_t> attr_set{0};
-    constexpr int per = FWD_STAGES * 2 * fwd_vecs<X32>() * units_of<X32>() * 16;  // a thread
-    return launch_norm_kernel(norm_kernel<X32, Y32, CLUSTER>, attr_set, grid, p.tpb, per * p.tpb,
-                              per * NORM_TPB, p.cluster, s, a);
+template <int NV, bool X32, bool Y32>
+cudaError_t launch_norm_whole(NormFwd a, const NormPlan &p, cudaStream_t s) {
+    static std::atomic<uint64_t> attr_set[2];
+    constexpr int per = FWD_STAGES * 2 * NV * units_of<X32>() * 16;  // a thread
+    static_assert(per * NORM_TPB * blocks_of_sm(NV) <= 196608, "shared memory of a SM");
+    const int64_t all = (int64_t)device_sm_count() * blocks_of_sm(NV) * (NORM_TPB / p.tpb) / p.cluster;
+    const int64_t most = all > 1 ? all : 1;
+    const unsigned grid = (unsigned)((p.groups < most ? p.groups : most) * p.cluster);
+    const bool one = p.cluster == 1;
+    return launch_norm_kernel(one ? norm_kernel<NV, X32, Y32, false> : norm_kernel<NV, X32, Y32, true>,
+                              attr_set[one], grid, p.tpb, per * p.tpb, per * NORM_TPB, p.cluster, s, a);
 }
 template <bool X32, bool Y32>
 cudaError_t launch_norm(NormFwd a, const NormPlan &p, cudaStream_t s) {
@@ -968,21 +980,22 @@ cudaError_t launch_norm(NormFwd a, const NormPlan &p, cudaStream_t s) {
         return launch_edge(norm_long_kernel<X32, Y32>, (unsigned)a.s.rows, 1024, 0, 1, s, a);
     a.s.tpr = p.tpr;
     a.s.cluster = p.cluster;
-    const int64_t all = (int64_t)device_sm_count() * (NORM_TPB / p.tpb) / p.cluster;
-    const int64_t most = all > 1 ? all : 1;
-    const unsigned grid = (unsigned)((p.groups < most ? p.groups : most) * p.cluster);
-    return p.cluster > 1 ? launch_norm_whole<X32, Y32, true>(a, p, grid, s)
-                         : launch_norm_whole<X32, Y32, false>(a, p, grid, s);
+    if (p.nv == 1) return launch_norm_whole<1, X32, Y32>(a, p, s);
+    if constexpr (!X32)
+        if (p.nv == 4) return launch_norm_whole<4, X32, Y32>(a, p, s);
+    return launch_norm_whole<2, X32, Y32>(a, p, s);
 }
 
-template <bool X32, bool Y32, bool CLUSTER>
-cudaError_t launch_norm_backward_whole(const NormBwd &a, const NormPlan &p, unsigned grid,
-                                       cudaStream_t s) {
-    static std::atomic<uint64_t> attr_set{0};
-    constexpr int per = bwd_stages<X32, Y32>() * bwd_units<X32, Y32>() * 16;  // a thread
-    static_assert(per >= BWD_VECS * 8 * 4, "the teams' sums of a block go where its rows were");
-    return launch_norm_kernel(norm_backward_kernel<X32, Y32, CLUSTER>, attr_set, grid, p.tpb,
-                              per * p.tpb, per * NORM_TPB, p.cluster, s, a);
+template <int NV, bool X32, bool Y32>
+cudaError_t launch_norm_backward_whole(const NormBwd &a, const NormPlan &p, cudaStream_t s) {
+    static std::atomic<uint64_t> attr_set[2];
+    constexpr int per = bwd_stages<NV, X32, Y32>() * bwd_units<NV, X32, Y32>() * 16;  // a thread
+    static_assert(per >= NV * 8 * 4, "the teams' sums of a block go where its rows were");
+    static_assert(per * NORM_TPB * blocks_of_sm(NV) <= 196608, "shared memory of a SM");
+    const bool one = p.cluster == 1;
+    return launch_norm_kernel(
+        one ? norm_backward_kernel<NV, X32, Y32, false> : norm_backward_kernel<NV, X32, Y32, true>,
+        attr_set[one], (unsigned)(p.parts * p.cluster), p.tpb, per * p.tpb, per * NORM_TPB, p.cluster, s, a);
 }
 template <bool X32, bool Y32>
 cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, cudaStream_t s) {
@@ -997,9 +1010,8 @@ cudaError_t launch_norm_backward(NormBwd a, const NormPlan &p, cudaStream_t s) {
     }
     a.s.tpr = p.tpr;
     a.s.cluster = p.cluster;
-    const unsigned grid = (unsigned)(p.parts * p.cluster);
-    return p.cluster > 1 ? launch_norm_backward_whole<X32, Y32, true>(a, p, grid, s)
-                         : launch_norm_backward_whole<X32, Y32, false>(a, p, grid, s);
+    return p.nv == 1 ? launch_norm_backward_whole<1, X32, Y32>(a, p, s)
+                     : launch_norm_backward_whole<2, X32, Y32>(a, p, s);
 }
 
 }  // namespace
