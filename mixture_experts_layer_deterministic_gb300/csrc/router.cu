@@ -5,9 +5,12 @@
 //
 // One warp per token, whose logits stay in registers. Each group of experts has a power of two of
 // lanes (32 where there is one group), which hold its experts in turn, four at a time where rows
-// allow 16-byte loads. A choice takes K rounds: the warp's largest key by one integer reduction over
-// order-preserving images, the lowest id that holds it where several do; the lane that held it goes on
-// to its second, and looks for its next two when both are gone.
+// allow 16-byte loads. The K-th largest of the lanes' largest keys (order-preserving images; K integer
+// reductions) is a bound below which no expert is chosen; the few above it go side by side through
+// shared memory, one a lane, and count how many are before them. Where ties leave more than a warp
+// holds, K rounds take the warp's largest one after another.
+// What bounds it is the instructions of a warp a token, some 600 for 512 experts: 16384 x 512, top 10,
+// @E512@ us, floor 5.2; a thread a token would compare 10 values with each of 512.
 //
 // The choice has to be that of exact scores. fp32 scores are off by a few units in their last place
 // (bounds at score_error), so a choice is settled unless two neighbours in the order of the chosen,
@@ -381,11 +384,56 @@ struct Offer {
     }
 };
 
+// The `want` largest keys in order, lane k getting the k-th and its expert (more lanes may get the next
+// ones), by counting. False, and nothing done, where more than 32 are not below the bound.
+template <int PER, int VEC>
+MOK_DEV bool side_by_side(const uint32_t (&key)[PER], const Held<VEC> &h, int want, int lane,
+                          uint2 (&side)[64], uint32_t &sel, int &id) {
+    if (want > 32) return false;
+    uint32_t most = 0u;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) most = max(most, key[j]);
+    uint32_t bound = 0u;  // lanes of equal keys go at once: then it is lower than it might be
+    for (int k = 0; k < want; ++k) {
+        bound = __reduce_max_sync(0xFFFFFFFFu, most);
+        if (most == bound) most = 0u;
+    }
+    bound = max(bound, 1u);
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) n += key[j] >= bound ? 1 : 0;
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += u;
+    }
+    const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    if (all > 32) return false;
+    int at = upto - n;
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        if (key[j] >= bound) side[at++] = make_uint2(~(uint32_t)h.id(j), key[j]);
+    __syncwarp();
+    // largest key first, lowest expert among equals: one 64-bit order
+    const uint64_t *as64 = reinterpret_cast<const uint64_t *>(side);
+    const uint64_t mine = lane < all ? as64[lane] : 0ull;
+    int rank = 0;
+    for (int k = 0; k < all; ++k) rank += as64[k] > mine ? 1 : 0;
+    if (lane < all) side[32 + rank] = make_uint2((uint32_t)mine, (uint32_t)(mine >> 32));
+    __syncwarp();
+    const uint2 got = side[32 + lane];
+    sel = lane < all ? got.y : 0u;
+    id = lane < all ? (int)~got.x : 0;
+    return true;
+}
+
 // PER experts a lane. Scores are needed for the choice (SCORED: with a bias, or groups by the sum of
 // two), for the sums or for weights out of all of a softmax.
 template <int PER, int VEC, bool BF16, bool SCORED>
 __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(const RouterFwd a) {
     extern __shared__ uint32_t router_smem[];
+    __shared__ alignas(8) uint2 side[ROUTER_WARPS][64];
     const RouterShape &c = a.c;
     int32_t *hist = reinterpret_cast<int32_t *>(router_smem);            // [E]
     float *sums = reinterpret_cast<float *>(router_smem + c.E);          // [warps][E]
@@ -492,27 +540,34 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
         }
         uint32_t key[PER];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) key[j] = kept && j < h.n ? order_of(v[j]) : 0u;
-        Offer<PER, VEC> left;
-        left.taken = 0;
-        left.look(key, true);
+        for (int j = 0; j < PER; ++j) key[j] = j / VEC * VEC < (kept ? h.n : 0) ? order_of(v[j]) : 0u;
         uint32_t sel = 0u;  // lane k: the k-th key and expert
         int id = 0, e = 0;
-        for (int k = 0; k < c.K; ++k) {
-            const uint32_t top_key = left.next(key, h, true, e);
-            if (lane == k) {
-                sel = top_key;
-                id = e;
+        Offer<PER, VEC> left;
+        const auto rounds = [&] {
+            left.taken = 0;
+            left.look(key, true);
+            for (int k = 0; k < c.K; ++k) {
+                const uint32_t top_key = left.next(key, h, true, e);
+                if (lane == k) {
+                    sel = top_key;
+                    id = e;
+                }
             }
-        }
+        };
+        // with a bias one more, for the distance between the last chosen and the first that is not
+        const bool quick = side_by_side<PER, VEC>(key, h, biased ? c.K + 1 : c.K, lane, side[warp], sel, id);
+        if (!quick) rounds();
         bool exact = false;
         if (biased) {
             // neighbours in the order, the first that was not chosen among them, that the scores' errors
             // and the rounding of their sums with the bias could exchange
             const float tol = 2.0f * err + 1.1920928955078125e-7f * size;
             uint32_t after = __shfl_down_sync(0xFFFFFFFFu, sel, 1);
-            const uint32_t rest = __reduce_max_sync(0xFFFFFFFFu, left.k0);
-            if (lane == c.K - 1) after = rest;
+            if (!quick) {
+                const uint32_t rest = __reduce_max_sync(0xFFFFFFFFu, left.k0);
+                if (lane == c.K - 1) after = rest;
+            }
             const auto near = [&](uint32_t x, uint32_t y) {
                 return y > ORDER_MASKED && !(of_order(x) - of_order(y) > tol);
             };
@@ -521,6 +576,7 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
             };
             if (__any_sync(0xFFFFFFFFu, lane < c.K && near(sel, after))) {
                 // go on as long as the next is too close to the last to tell them apart
+                if (quick) rounds();
                 int many = c.K;
                 for (; many < 32; ++many) {
                     const uint32_t last = __shfl_sync(0xFFFFFFFFu, sel, many - 1);
