@@ -466,6 +466,13 @@ class AdamW:
             B.check(B.mok_adamw_step_at(cfg, tensors, self.clock, grad_scale, stream), "adamw")
 
 
+def _check_current(device):
+    """Kernels go to the current device, so it has to be the arrays'."""
+    if device.type == "cuda" and torch.cuda.current_device() != device.index:
+        raise ValueError("arrays on %s, the current device is cuda:%d" %
+                         (device, torch.cuda.current_device()))
+
+
 class _Workspace:
     """A pass's workspace, from the memory of the stream that first runs the pass, whose earlier work
     is then done with it; other streams are recorded, so it is not given away under their work."""
@@ -506,6 +513,7 @@ class Router:
         self.ws = _Workspace(self.here)
 
     def _check(self, logits, idx, w_name, w):
+        _check_current(self.here)
         n = self.T * self.K
         _check_vector("idx", idx, torch.int32, self.here, n if n else idx.numel())
         _check_vector(w_name, w, torch.float32, self.here, n if n else w.numel())
@@ -533,6 +541,7 @@ class Router:
 
     def update_bias(self, counts, rate, bias, new_bias=None, stream=None):
         """bias (or new_bias) one step towards equal loads."""
+        _check_current(self.here)
         new_bias = bias if new_bias is None else new_bias
         _check_vector("counts", counts, torch.int32, self.here, self.E)
         _check_vector("bias", bias, torch.float32, self.here, self.E)
@@ -560,6 +569,7 @@ class Norm:
 
     def _check(self, x=(), y=(), stats=(), weights=()):
         """(name, array) pairs of each kind."""
+        _check_current(self.here)
         c = self.cfg
         for name, t in x:
             _check_matrix(name, t, self.x_dtype, self.here, self.rows, self.H, c.ld_x)
@@ -615,6 +625,7 @@ class VocabLoss:
         return torch.zeros(V, ld, dtype=dtype, device=self.here)[:, :H]
 
     def _check(self, x, w, targets, values):
+        _check_current(self.here)
         _check_matrix("x", x, torch.bfloat16, self.here, *self.of_x)
         _check_matrix("w", w, torch.bfloat16, self.here, *self.of_w)
         for name, t, dtype in (("targets", targets, torch.int32),) + values:

@@ -409,6 +409,7 @@ struct Dx {
     Tiles tiles;
     int n_mb;     // ceil(Kin / 256)
     int halves;   // planes of dz: 2 for fp32 gradients of a dz that bf16 does not hold
+    int run;      // K elements of a segment (F32)
     int Kin, N;
     int64_t ld;   // row stride of dx
     void *dx;
@@ -429,11 +430,11 @@ struct Dx {
         if constexpr (CUT) kp.cut(q, u.part);
         return q;
     }
-    MOK_DEV int segments(const Unit &u) const { return F32 ? k_range(u).segments(halves) : 1; }
+    MOK_DEV int segments(const Unit &u) const { return F32 ? k_range(u).segments(halves, run) : 1; }
     MOK_DEV int long_steps(const Unit &) const { return 0; }
     MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
         LinGeom q = k_range(u);
-        if constexpr (F32) q.segment(seg, halves);
+        if constexpr (F32) q.segment(seg, halves, run);
         q.n_mma = (u.nr + 15) & ~15;
         q.a0 = u.mb * 256 + (int)rank * 128;
         q.a1 = 0;
@@ -551,7 +552,7 @@ struct Dw {
     const int32_t *starts, *valid;  // grouped: first row and row count of each group
     int64_t rows;                   // dense
     int G, n_mb, n_nb;              // ceil(Kin / 256), ceil(N / 256)
-    int halves;                     // planes of dz (F32; see Dx)
+    int halves, run;                // planes of dz, K elements of a segment (F32; see Dx)
     int Kin, N;
     int64_t ld;                     // row stride of dW
     void *dw;
@@ -581,12 +582,12 @@ struct Dw {
         if constexpr (CUT) kp.cut(q, u.part);
         return q;
     }
-    MOK_DEV int segments(const Unit &u) const { return F32 ? k_range(u).segments(halves) : 1; }
+    MOK_DEV int segments(const Unit &u) const { return F32 ? k_range(u).segments(halves, run) : 1; }
     MOK_DEV int long_steps(const Unit &u) const { return F32 ? 0 : (u.nr + 15) / 16; }
     MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
         const int mb = u.mb, nb = u.nb;
         LinGeom q = k_range(u);
-        if constexpr (F32) q.segment(seg, halves);
+        if constexpr (F32) q.segment(seg, halves, run);
         // MN-major B comes in boxes of 64 columns per CTA: N of the MMA is 128 or 256, columns
         // past the matrix being zeros
         q.n_mma = N - nb * 256 <= 128 ? 128 : 256;
@@ -1337,8 +1338,8 @@ cudaError_t dense_grads(const DenseGrads &a, const GradPlan &plan, const KParts 
     const int n_kb = (a.Kin + 255) / 256, n_nb = (a.N + 255) / 256;
     const bool both = a.dx && a.dw && plan.split > 0;
     const Tiles tiles = dense_tiles(a.rows, both ? plan.height : plan.alone);
-    const Dx<F, CUT> px{tiles, n_kb, a.halves, a.Kin, a.N, a.ld_x, a.dx, status, xk};
-    const Dw<F, CUT> pw{nullptr, nullptr, a.rows, 1, n_kb, n_nb, a.halves, a.Kin, a.N, a.ld_w, a.dw,
+    const Dx<F, CUT> px{tiles, n_kb, a.halves, a.run, a.Kin, a.N, a.ld_dx, a.dx, status, xk};
+    const Dw<F, CUT> pw{nullptr, nullptr, a.rows, 1, n_kb, n_nb, a.halves, a.run, a.Kin, a.N, a.ld_w, a.dw,
                         status, DbArgs{nullptr, nullptr, 0, nullptr}, wk};
     *launches = both ? 1 : (a.dx != nullptr) + (a.dw != nullptr);
     if (both) return launch_both(wa, wb, pw, xa, xb, px, plan.split, plan.pairs, s);
@@ -1419,7 +1420,7 @@ cudaError_t launch_dense_grads(const DenseGrads &a, int *status, int *launches, 
     if (e != cudaSuccess) return e;
     JoinArgs j = {};
     int n = 0;
-    if (a.dx && plan.x.parts > 1) j.o[n++] = join_out(xk, a.rows, a.Kin, a.dx, a.ld_x);
+    if (a.dx && plan.x.parts > 1) j.o[n++] = join_out(xk, a.rows, a.Kin, a.dx, a.ld_dx);
     if (a.dw && plan.w.parts > 1) j.o[n++] = join_out(wk, a.N, a.Kin, a.dw, a.ld_w);
     *launches += n > 0;
     return n > 0 ? launch_join(a.f32, j, s) : cudaSuccess;
@@ -1633,8 +1634,8 @@ mok_status mok_linear_backward(const mok_linear_config *c, const void *x, const 
     if (!db_in_dw) dwb.db = nullptr;
 #define MOK_BWD(F, CUT)                                                                         \
     do {                                                                                        \
-        const Dx<F, CUT> px{tiles, n_kb, halves, Kin, N, c->ld_in, dx, status, xk};                       \
-        const Dw<F, CUT> pw{starts, valid, c->rows, G, n_kb, n_nb, halves, Kin, N, c->ld_w, dw, status, dwb, \
+        const Dx<F, CUT> px{tiles, n_kb, halves, SEG_K, Kin, N, c->ld_in, dx, status, xk};              \
+        const Dw<F, CUT> pw{starts, valid, c->rows, G, n_kb, n_nb, halves, SEG_K, Kin, N, c->ld_w, dw, status, dwb, \
                         wkp};                                                                   \
         if (split > 0) {                                                                        \
             MOK_OP_LAUNCH(OP_LINEAR_DX, 1,                                                      \

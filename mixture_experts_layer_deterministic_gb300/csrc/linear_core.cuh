@@ -113,16 +113,16 @@ struct LinGeom {
     int k_first;         // K element to begin at
     int half;            // of dz, where it comes as two bf16 values
 
-    // cut to segment `seg` of a sum that is kept in registers: SEG_K of its K, by one of the
+    // cut to segment `seg` of a sum that is kept in registers: `run` of its K, by one of the
     // halves of dz
-    MOK_DEV void segment(int seg, int halves) {
-        const int first = seg / halves * (SEG_K / 16);
+    MOK_DEV void segment(int seg, int halves, int run) {
+        const int first = seg / halves * (run / 16);
         half = seg % halves;
         k_first += first * 16;
-        k_steps = k_steps - first < SEG_K / 16 ? k_steps - first : SEG_K / 16;
+        k_steps = k_steps - first < run / 16 ? k_steps - first : run / 16;
     }
-    MOK_DEV int segments(int halves) const {
-        return k_steps > SEG_K / 16 ? (k_steps + SEG_K / 16 - 1) / (SEG_K / 16) * halves : halves;
+    MOK_DEV int segments(int halves, int run) const {
+        return k_steps > run / 16 ? (k_steps + run / 16 - 1) / (run / 16) * halves : halves;
     }
 };
 

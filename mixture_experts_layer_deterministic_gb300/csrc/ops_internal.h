@@ -40,7 +40,8 @@ struct DenseGrads {
     const uint16_t *x, *w, *dz;  // [rows][Kin], [N][Kin], [halves][rows][N]
     int64_t rows;
     int N, Kin, halves;
-    int64_t ld_x, ld_w, ld_dz;   // of x and dx, of w and dw, of dz
+    int run;                     // K elements that fp32 gradients sum at a time, a multiple of 64
+    int64_t ld_x, ld_dx, ld_w, ld_dz;  // of x, of dx, of w and dw, of dz
     void *dx, *dw;               // one of them may be nullptr
     bool f32;                    // their type
     // where N is a piece of the layer's: dx goes to dx_sum in fp32 (rows round_up(Kin, 4) apart;

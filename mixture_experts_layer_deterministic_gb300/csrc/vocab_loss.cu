@@ -115,9 +115,9 @@ struct VocabFwd {
         const int64_t row = (int64_t)u.mb * 256 + rank * 128 + q * 32 + lane;
         const int n = cols(u);
         MaxSum a{LOWEST, 0.0f};
-        int target = -1;
+        int target = -1;  // in the tile, where it is not below it
         if (last && row < rows) target = targets[row];
-        target -= u.nb * 256;
+        target = target >= u.nb * 256 ? target - u.nb * 256 : -1;
         if constexpr (SEGS) {
             sum_segments(c, hw, n, seg == 0, last, carry, [&](int n0, const float (&v)[16]) {
                 take(a, n0, n, v, target, row);
@@ -283,16 +283,57 @@ __global__ void vocab_rows_kernel(const float *lse, const float *d_loss, const i
     out[r] = RowGrad{l, in ? d * fmaf(2.0f * z, l, 1.0f) : 0.0f, d, in ? t : -1};
 }
 
+// x for the product of dW, zeros in the rows that take no part: their dl is zero, but nothing says that x is
+// finite there, and zero times infinity would reach all of dW. 8192 x 4096 20 us, beside 10 ms of products.
+__global__ void __launch_bounds__(256)
+    vocab_live_kernel(const uint16_t *x, int64_t ld, const int32_t *targets, int64_t rows, int H, int V,
+                      uint16_t *out, int64_t ld_out) {
+    let_next_start();
+    wait_for_previous();
+    const int64_t per = ld_out / 8, n = rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per;
+        const int c = (int)(i - r * per) * 8, t = targets[r];
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (t >= 0 && t < V) {
+            const uint16_t *p = x + r * ld + c;
+            if (c + 8 <= H) {
+                v = ld_v4(p);
+            } else {
+                uint32_t e[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < H) e[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+                v = make_uint4(e[0], e[1], e[2], e[3]);
+            }
+        }
+        *reinterpret_cast<uint4 *>(out + r * ld_out + c) = v;
+    }
+}
+
+// EXACT: the exponent's own rounding, half a unit of some 17, is put right to first order
+template <bool EXACT>
 MOK_DEV float dl_of(const RowGrad &g, float l, int v) {
-    const float p = g.p * exp2_hw((l - g.lse) * LOG2E_F);
+    const float x = l - g.lse, t = x * LOG2E_F;
+    float e = exp2_hw(t);
+    if (EXACT) {
+        constexpr float LOG2E_REST = 1.925963033500749e-8f;  // log2 e - LOG2E_F
+        const float rest = fmaf(x, LOG2E_F, -t) + x * LOG2E_REST;
+        if (rest == rest) e = fmaf(e * LN2_F, rest, e);  // not where x is infinite
+    }
+    const float p = g.p * e;
     return g.target < 0 ? 0.0f : v == g.target ? p - g.d : p;
 }
 
 // bf16 planes that dl comes in for fp32 gradients: each takes what the ones before it leave. Two
 // would do as for the linear layer's dz (rms 2.7e-6 of it), but dl has no rounding of its own that
-// this would hide behind: gradients of 1001 rows, 1000 x 5003, are 2.7e-6 of their norm off with two
-// and 1.2e-6 with three, plain fp32 products 1.3e-6.
+// this would hide behind. Gradients of 1001 rows, 1000 x 5003, are 2.7e-6 of their norm off with two
+// and 1.2e-6 with three; plain fp32 products 1.3e-6 (dx) and 5.4e-7 (dW).
 constexpr int PLANES = 3;
+// and what the tensor cores sum of them at a time: their error grows with a run's length (see Fwd in
+// linear.cu). Runs of 512, with the exponent's rounding put right in dl, 7.0e-7 and 6.9e-7 (3% slower
+// than runs of 1024)
+constexpr int GRAD_RUN = 512;
 
 // The gradient of the logits for vocabulary entries [v0, v0 + N), in N_PLANES planes of bf16. SEGS: of
 // logits whose segments of H were added in fp32 (for planes where H is long). Row tiles come first:
@@ -355,7 +396,7 @@ struct VocabDl {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     if (n0 + j >= u.nr) continue;
-                    float g = dl_of(rows[r0 + n0 + j], v[j], v0 + f);
+                    float g = dl_of<true>(rows[r0 + n0 + j], v[j], v0 + f);
 #pragma unroll
                     for (int k = 0; k < N_PLANES; ++k) {
                         const uint16_t b = f32_to_bf16(g);
@@ -383,7 +424,7 @@ struct VocabDl {
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            v[b][h][i] = dl_of(g[b][i & 1], w[h][b][i],
+                            v[b][h][i] = dl_of<(N_PLANES > 1)>(g[b][i & 1], w[h][b][i],
                                                v0 + f0 + 16 * h + 8 * (i >> 1) + (lane >> 2));
                     patch_write8(pt.patch(), pt.half, b, v[b], lane);
                 }
@@ -437,6 +478,8 @@ struct VocabWs {
     float *hit;
     RowGrad *rows;
     uint16_t *dl;
+    uint16_t *x;      // of the rows that take part
+    int64_t ld_x;
     float *dx_sum;
     GradPlan plan;    // of the gradient products, where the vocabulary is one piece
     void *grads;      // their parts
@@ -475,6 +518,8 @@ size_t carve_vocab(const mok_vocab_loss_config &c, int pass, void *ws, VocabWs *
         w.ld_dl = w.pieces > 1 ? piece : round_up(c.V, 8);
         w.rows = (RowGrad *)take((size_t)c.rows * sizeof(RowGrad));
         w.dl = (uint16_t *)take((size_t)planes * c.rows * w.ld_dl * 2);
+        w.ld_x = round_up(c.H, 8);
+        w.x = (uint16_t *)take((size_t)c.rows * w.ld_x * 2);
         if (w.pieces > 1 && c.grad_dtype == MOK_DTYPE_BF16)
             w.dx_sum = (float *)take((size_t)c.rows * round_up(c.H, 4) * 4);
         if (w.pieces == 1) {
@@ -621,6 +666,13 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
     MOK_OP_LAUNCH(OP_VOCAB_DL, 1,
                   launch_edge(vocab_rows_kernel, (unsigned)((c->rows + 255) / 256), 256, 0, 1, stream,
                               lse, d_loss, targets, c->rows, c->V, c->z_loss, wk.rows, status));
+    if (dw) {
+        const int64_t blocks = (c->rows * (wk.ld_x / 8) + 255) / 256, most = (int64_t)device_sm_count() * 16;
+        MOK_OP_LAUNCH(OP_VOCAB_DL, 1,
+                      launch_edge(vocab_live_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, 1,
+                                  stream, (const uint16_t *)x, c->ld_x, targets, c->rows, c->H, c->V,
+                                  wk.x, wk.ld_x));
+    }
     for (int k = 0; k < wk.pieces; ++k) {
         const int v0 = k * wk.piece, n = c->V - v0 < wk.piece ? c->V - v0 : wk.piece;
         const int n_mb = (n + 255) / 256;
@@ -638,8 +690,8 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
         else if (segs == 1) MOK_DL(PLANES, false);
         else MOK_DL(PLANES, true);
 #undef MOK_DL
-        const DenseGrads g{(const uint16_t *)x, (const uint16_t *)w + v0 * c->ld_w, wk.dl, c->rows, n,
-                           c->H, f32 ? PLANES : 1, c->ld_x, c->ld_w, wk.ld_dl, dx,
+        const DenseGrads g{wk.x, (const uint16_t *)w + v0 * c->ld_w, wk.dl, c->rows, n, c->H,
+                           f32 ? PLANES : 1, GRAD_RUN, wk.ld_x, c->ld_x, c->ld_w, wk.ld_dl, dx,
                            dw ? (char *)dw + v0 * c->ld_w * es : nullptr, f32,
                            dx ? wk.dx_sum : nullptr, dx && k > 0,
                            wk.pieces == 1 ? wk.plan

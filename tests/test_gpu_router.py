@@ -104,17 +104,16 @@ class Case:
     def weights64(self, idx):
         """Weights of the chosen ids, as shares of logarithms where they are renormalised."""
         torch = _t()
-        l = self.l
-        if self.score == "sigmoid":
-            ls = -torch.logaddexp(torch.zeros_like(l), -l)
-        else:
-            lse = torch.logsumexp(l, 1, keepdim=True)
-            ls = torch.where(torch.isneginf(lse), -INF, l - lse)
+
+        def shares(v):  # less the largest first: a sum's logarithm is lost beside 1e38
+            top = v.amax(1, keepdim=True)
+            v = v - torch.where(top == -INF, 0.0, top)
+            return torch.where(top == -INF, -INF, v - torch.logsumexp(v, 1, keepdim=True))
+
+        ls = -torch.logaddexp(torch.zeros_like(self.l), -self.l) if self.score == "sigmoid" \
+            else shares(self.l)
         ls = ls.gather(1, idx)
-        if self.renorm:
-            total = torch.logsumexp(ls, 1, keepdim=True)
-            ls = torch.where(torch.isneginf(total), -INF, ls - total)
-        return torch.exp(ls)
+        return torch.exp(shares(ls) if self.renorm else ls)
 
 
 def check_forward(c):

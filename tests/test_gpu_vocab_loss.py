@@ -223,10 +223,14 @@ def test_a_row_that_is_not_finite_spoils_its_own_loss_alone():
     c.x[9, 5] = 0.0
     dx2, _ = c.backward(lse[:40], dw=False)
     assert torch.equal(dx[keep], dx2[keep])
-    # such a row without a target: no gradient of its own either
-    c.x[9, 5], c.t[9] = float("nan"), -1
-    dx, _ = c.backward(lse2[:40], dw=False)
-    assert torch.equal(dx[keep], dx2[keep]) and bool((dx[9, :96] == 0).all())
+    # such a row without a target: no gradient of its own, and nothing of it in any other
+    c.t[9] = -1
+    _, dw2 = c.backward(lse[:40])
+    for bad in (float("nan"), float("inf")):
+        c.x[9, 5] = bad
+        dx, dw = c.backward(lse2[:40])
+        assert torch.equal(dx[keep], dx2[keep]) and bool((dx[9, :96] == 0).all())
+        assert torch.equal(dw, dw2)
     assert device_ok()
 
 

@@ -141,3 +141,12 @@ def test_nothing_to_do(calls):
     v.forward(torch.zeros(0, 16, dtype=BF), v.weights(), torch.zeros(1, dtype=I32), None,
               torch.zeros(0))
     assert len(calls) == 3
+
+
+def test_arrays_of_another_device_than_the_current(monkeypatch):
+    from mixture_experts_layer_deterministic_gb300 import buffers
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    buffers._check_current(torch.device("cuda", 0))
+    buffers._check_current(torch.device("cpu"))
+    with pytest.raises(ValueError):
+        buffers._check_current(torch.device("cuda", 1))
