@@ -139,30 +139,6 @@ MOK_DEV void *row_of(void *p, int64_t r, int64_t ld) {
     return static_cast<char *>(p) + r * ld * (F32 ? 4 : 2);
 }
 
-// 8 elements from column c on, zeros past H
-template <bool F32>
-MOK_DEV void load_raw(const void *row, int c, int H, Raw<F32> &q) {
-    if (c + 8 <= H) {
-        if (F32) {
-            q.v[0] = ld_v4(static_cast<const float *>(row) + c);
-            q.v[F32 ? 1 : 0] = ld_v4(static_cast<const float *>(row) + c + 4);
-        } else {
-            q.v[0] = ld_v4(static_cast<const uint16_t *>(row) + c);
-        }
-    } else {
-        uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (c + j >= H) continue;
-            if (F32)
-                e[j] = static_cast<const uint32_t *>(row)[c + j];
-            else
-                e[j >> 1] |= (uint32_t)static_cast<const uint16_t *>(row)[c + j] << (16 * (j & 1));
-        }
-        q.v[0] = make_uint4(e[0], e[1], e[2], e[3]);
-        if (F32) q.v[F32 ? 1 : 0] = make_uint4(e[4], e[5], e[6], e[7]);
-    }
-}
 template <bool F32>
 MOK_DEV void unpack(const Raw<F32> &q, f32x2 (&v)[4]) {
     const uint4 b = q.v[F32 ? 1 : 0];
@@ -172,15 +148,6 @@ MOK_DEV void unpack(const Raw<F32> &q, f32x2 (&v)[4]) {
         v[j] = F32 ? pair(__uint_as_float(w[F32 ? 2 * j : j]), __uint_as_float(w[F32 ? 2 * j + 1 : j]))
                    : pair(bf16_lo(w[j]), bf16_hi(w[j]));
 }
-template <bool F32>
-MOK_DEV void unpack(const Raw<F32> &q, float (&v)[8]) {
-    const uint4 b = q.v[F32 ? 1 : 0];
-    const uint32_t w[8] = {q.v[0].x, q.v[0].y, q.v[0].z, q.v[0].w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = F32 ? __uint_as_float(w[j]) : (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-}
-
 // A thread's pieces of the rows ahead: `stages` rows of UNITS 16-byte units, each in a place of its own.
 // Nobody else reads them, so there is no barrier; a place is filled again when its row is done with.
 struct Ahead {
