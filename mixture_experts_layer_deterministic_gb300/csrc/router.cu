@@ -9,6 +9,7 @@
 // reductions) is a bound below which no expert is chosen; the few above it go side by side through
 // shared memory, one a lane, and count how many are before them. Where ties leave more than a warp
 // holds, K rounds take the warp's largest one after another.
+// Few experts have a thread a token instead (below).
 // What bounds it is the instructions of a warp a token, some 600 for 512 experts: 16384 x 512, top 10,
 // 14.9 us (rounds alone: 23.4), floor 5.2; a thread a token would compare 10 values with each of 512.
 //
@@ -634,6 +635,152 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
     }
 }
 
+// ---- few experts: a thread a token ----
+//
+// Up to FEW_E experts and FEW_K choices by the logits themselves (no bias, one group), and gradients of
+// as many. A warp a token would leave most lanes idle: a row fits a thread's registers, K rounds compare
+// it, and nothing crosses lanes but a block's loads at its end. The rule looks at E and K alone, so that a
+// token's weights do not depend on how many others there are.
+// A warp against a thread a token, us: 131072 x 8, top 2 of a softmax 41 / 5.6, its gradient with the sums'
+// 67 / 5.8, 2.4 million x 2 of a sigmoid 693 / 48; 64 tokens of 8 top 2 2.3 / 2.4, of 16 top 4 2.3 / 3.1. With
+// 32 experts, top 8 and 4096 tokens it is 4.6 / 10.3: a thread's rounds are its own to wait for. What bounds
+// it: scattered rows of 8 to 64 bytes, and with loads the atomics on a block's few counts.
+constexpr int FEW_E = 16, FEW_K = 4, FEW_WARPS = 4;
+bool few(const RouterShape &c) { return c.G == 1 && c.E <= FEW_E && c.K <= FEW_K; }
+RouterShape few_shape(RouterShape c) {
+    c.lanes = 1;
+    return c;
+}
+
+template <int PER>
+MOK_DEV float few_softmax(float (&v)[PER], float &top) {
+    top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) top = fmaxf(top, v[j]);
+    const float shift = finite_top(top);
+    float den = 0.0f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        v[j] = exp2_hw((v[j] - shift) * LOG2E_R);
+        den += v[j];
+    }
+    const float inv = den > 0.0f ? 1.0f / den : den == 0.0f ? 0.0f : den;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) v[j] *= inv;
+    return inv;
+}
+
+// chosen_weight of a token's K logits (-inf past them): l becomes the weights
+MOK_DEV void few_weights(const RouterShape &c, float (&l)[FEW_K], float top, float inv) {
+    if (!c.renorm) {
+#pragma unroll
+        for (int k = 0; k < FEW_K; ++k)
+            l[k] = !(l[k] > -INFINITY) ? 0.0f : c.softmax ? expf(l[k] - finite_top(top)) * inv : sigmoid32(l[k]);
+        return;
+    }
+    float most = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int k = 0; k < FEW_K; ++k) most = fmaxf(most, l[k]);
+    const float t = fminf(most, 0.0f);
+#pragma unroll
+    for (int k = 0; k < FEW_K; ++k) {
+        if (k >= c.K) continue;
+        const bool in = l[k] > -INFINITY;
+        l[k] = !in          ? 0.0f
+               : c.softmax  ? expf(l[k] - most)
+               : l[k] >= 0.0f ? sigmoid32(l[k])
+                            : expf(l[k] - t) / (1.0f + expf(l[k]));
+        total += l[k];
+    }
+#pragma unroll
+    for (int k = 0; k < FEW_K; ++k)
+        l[k] = total > 0.0f ? __fdividef(l[k], total) : total == 0.0f ? 0.0f : total;
+}
+
+template <int PER, int VEC, bool BF16>
+__global__ void __launch_bounds__(32 * FEW_WARPS) router_few_kernel(const RouterFwd a) {
+    extern __shared__ uint32_t router_smem[];
+    const RouterShape &c = a.c;
+    int32_t *hist = reinterpret_cast<int32_t *>(router_smem);    // [E]
+    float *sums = reinterpret_cast<float *>(router_smem + c.E);  // [warps][E]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    let_next_start();
+    wait_for_previous();
+    if (a.count_part != nullptr) {
+        if (threadIdx.x < c.E) hist[threadIdx.x] = 0;
+        __syncthreads();
+    }
+    const Held<VEC> h(c, 0);
+    const bool row_scores = a.sum_part != nullptr || (c.softmax && !c.renorm);
+    float acc[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) acc[j] = 0.0f;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < c.T; t += step) {
+        float v[PER];
+        load_logits<PER, VEC, BF16>(static_cast<const char *>(a.logits) + t * c.ld * (BF16 ? 2 : 4), h, v);
+        uint32_t key[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) key[j] = j < c.E ? order_of(v[j]) : 0u;
+        float top = -INFINITY, inv = 0.0f;
+        if (row_scores) {
+            if (c.softmax) {
+                inv = few_softmax(v, top);
+            } else {
+#pragma unroll
+                for (int j = 0; j < PER; ++j) v[j] = sigmoid_hw(v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j) acc[j] += v[j];
+        }
+        int id[FEW_K];
+        float l[FEW_K];
+#pragma unroll
+        for (int k = 0; k < FEW_K; ++k) {
+            l[k] = -INFINITY;
+            if (k >= c.K) continue;
+            uint32_t most = 0u;
+            id[k] = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (key[j] > most) id[k] = j;
+                most = max(most, key[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (j == id[k]) key[j] = 0u;
+            l[k] = of_order(most);
+            if (a.count_part != nullptr) atomicAdd(&hist[id[k]], 1);
+        }
+        few_weights(c, l, top, inv);
+#pragma unroll
+        for (int k = 0; k < FEW_K; ++k) {
+            if (k >= c.K) continue;
+            a.idx[t * c.K + k] = id[k];
+            a.w[t * c.K + k] = c.scale * l[k];
+        }
+    }
+    if (a.sum_part == nullptr && a.count_part == nullptr) return;
+    if (a.sum_part != nullptr) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const float s = warp_sum(acc[j]);
+            if (lane == 0 && j < c.E) sums[warp * c.E + j] = s;
+        }
+    }
+    __syncthreads();
+    const int e = threadIdx.x;
+    if (e >= c.E) return;
+    const int64_t at = (int64_t)blockIdx.x * c.E + e;
+    if (a.count_part != nullptr) a.count_part[at] = hist[e];
+    if (a.sum_part != nullptr) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < FEW_WARPS; ++k) s += sums[k * c.E + e];
+        a.sum_part[at] = s;
+    }
+}
+
 // The blocks' counts (y = 0) and sums (y = 1), added in order: 32 experts a block, each warp a slice
 // of the parts.
 constexpr int LOAD_SLICES = 32;
@@ -812,6 +959,102 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, DENSE && PER == 16   ? 4
     }
 }
 
+// The gradient with a thread a token: the row as if nothing were chosen, then the chosen entries.
+template <int PER, int VEC, bool BF16, bool DENSE>
+__global__ void __launch_bounds__(32 * FEW_WARPS) router_few_backward_kernel(const RouterBwd a) {
+    const RouterShape &c = a.c;
+    let_next_start();
+    wait_for_previous();
+    const Held<VEC> h(c, 0);
+    float ds[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) ds[j] = DENSE && a.dsum != nullptr && j < c.E ? a.dsum[j] : 0.0f;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < c.T; t += step) {
+        const int64_t at = t * c.ld * (BF16 ? 2 : 4);
+        const void *row = static_cast<const char *>(a.logits) + at;
+        void *out = static_cast<char *>(a.dlogits) + at;
+        float s[PER];
+        if (DENSE) load_logits<PER, VEC, BF16>(row, h, s);
+        int id[FEW_K];
+        float dw[FEW_K], l[FEW_K], wt[FEW_K];
+#pragma unroll
+        for (int k = 0; k < FEW_K; ++k) {
+            id[k] = -1;
+            dw[k] = 0.0f;
+            if (k < c.K) {
+                id[k] = a.idx[t * c.K + k];
+                dw[k] = a.dw[t * c.K + k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < FEW_K; ++k) {
+            l[k] = -INFINITY;
+            if (k >= c.K) continue;
+            if (id[k] < 0 || id[k] >= c.E) {
+                raise_status(a.status, MOK_ERR_DEVICE_INVARIANT);
+                id[k] = -1;
+            } else {
+                l[k] = load_logit<BF16>(row, id[k]);
+            }
+        }
+        float top = -INFINITY, inv = 0.0f, mean = 0.0f;
+        if (DENSE && c.softmax) {
+            inv = few_softmax(s, top);
+            if (a.dsum != nullptr) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j) mean = fmaf(s[j], ds[j], mean);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < FEW_K; ++k) wt[k] = l[k];
+        few_weights(c, wt, top, inv);
+        float m = 0.0f;
+#pragma unroll
+        for (int k = 0; k < FEW_K; ++k)
+            if (l[k] > -INFINITY) m += dw[k] * wt[k];
+        const float all = c.softmax && !c.renorm ? c.scale * m + mean : mean;
+        float add[FEW_K];
+#pragma unroll
+        for (int k = 0; k < FEW_K; ++k) {
+            add[k] = 0.0f;
+            if (k < c.K && l[k] > -INFINITY) {
+                add[k] = c.scale * wt[k] * (c.renorm ? dw[k] - m : dw[k]);
+                if (!c.softmax) add[k] *= 1.0f / (1.0f + expf(l[k]));  // 1 - s
+            }
+            // the same id twice: the first adds up
+#pragma unroll
+            for (int i = 0; i < k; ++i)
+                if (id[i] >= 0 && id[i] == id[k]) {
+                    add[i] += add[k];
+                    id[k] = -1;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            if (!DENSE) {
+                s[j] = 0.0f;
+            } else if (c.softmax) {
+                s[j] *= ds[j] - all;
+            } else {
+                const float e = exp2_hw(-LOG2E_R * fabsf(s[j]));  // as in a warp's
+                s[j] = __fdividef(ds[j] * e, (1.0f + e) * (1.0f + e));
+            }
+        }
+        store_logits<PER, VEC, BF16>(out, h, s);
+#pragma unroll
+        for (int k = 0; k < FEW_K; ++k) {
+            if (id[k] < 0) continue;
+            if (DENSE && l[k] > -INFINITY) {
+                const float d = a.dsum != nullptr ? a.dsum[id[k]] : 0.0f;
+                add[k] += c.softmax ? expf(l[k] - finite_top(top)) * inv * (d - all)
+                                    : d * sigmoid32(l[k]) * (1.0f / (1.0f + expf(l[k])));
+            }
+            store_logit<BF16>(out, id[k], add[k]);
+        }
+    }
+}
+
 __global__ void router_bias_kernel(const int32_t *counts, int64_t routed, int E, float rate,
                                    const float *bias, float *out) {
     let_next_start();
@@ -873,8 +1116,40 @@ cudaError_t with_held(const RouterShape &s, F &&f) {
 #undef MOK_HELD
 }
 
+template <class F>
+cudaError_t with_few(const RouterShape &s, F &&f) {
+    using std::integral_constant;
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 4> four;
+    const integral_constant<int, 8> eight;
+    const integral_constant<int, FEW_E> all;
+    if (s.E <= 8) return loads_four(s) ? f(eight, four) : f(eight, one);
+    return loads_four(s) ? f(all, four) : f(all, one);
+}
+int64_t few_blocks(const RouterShape &s, int64_t most) {
+    const int64_t n = (s.T + 32 * FEW_WARPS - 1) / (32 * FEW_WARPS);
+    return n < most ? n : most;
+}
+
+// blocks of a forward pass, and so parts of its loads (never more than there is room for)
+int64_t parts_of(const RouterFwd &a) {
+    const int64_t n = blocks_of(a.c);
+    return few(a.c) && a.bias == nullptr ? few_blocks(a.c, n) : n;
+}
+
 cudaError_t launch_router(const RouterFwd &a, bool bf16, cudaStream_t s) {
-    const unsigned grid = (unsigned)blocks_of(a.c);
+    const unsigned grid = (unsigned)parts_of(a);
+    if (few(a.c) && a.bias == nullptr) {
+        RouterFwd b = a;
+        b.c = few_shape(a.c);
+        return with_few(a.c, [&](auto per, auto vec) {
+            const auto go = [&](auto *kernel) {
+                return launch_edge(kernel, grid, 32 * FEW_WARPS, (1 + FEW_WARPS) * a.c.E * 4, 1, s, b);
+            };
+            return bf16 ? go(router_few_kernel<per.value, vec.value, true>)
+                        : go(router_few_kernel<per.value, vec.value, false>);
+        });
+    }
     const int smem = a.sum_part != nullptr     ? (1 + ROUTER_WARPS) * a.c.E * 4
                      : a.count_part != nullptr ? a.c.E * 4
                                                : 0;
@@ -892,10 +1167,25 @@ cudaError_t launch_router(const RouterFwd &a, bool bf16, cudaStream_t s) {
 }
 
 cudaError_t launch_router_backward(const RouterBwd &a, bool bf16, cudaStream_t s) {
-    const int64_t blocks = (a.c.T + ROUTER_WARPS - 1) / ROUTER_WARPS;
+    const int64_t tokens = (a.c.T + ROUTER_WARPS - 1) / ROUTER_WARPS;
     const int64_t most = (int64_t)device_sm_count() * 8;
-    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    const unsigned grid = (unsigned)(tokens < most ? tokens : most);
     const bool dense = a.dsum != nullptr || (a.c.softmax && !a.c.renorm);
+    if (few(a.c)) {
+        RouterBwd b = a;
+        b.c = few_shape(a.c);
+        const unsigned blocks = (unsigned)few_blocks(a.c, 2 * most);
+        return with_few(a.c, [&](auto per, auto vec) {
+            const auto go = [&](auto *kernel) {
+                return launch_edge(kernel, blocks, 32 * FEW_WARPS, 0, 1, s, b);
+            };
+            if (dense)
+                return bf16 ? go(router_few_backward_kernel<per.value, vec.value, true, true>)
+                            : go(router_few_backward_kernel<per.value, vec.value, false, true>);
+            return bf16 ? go(router_few_backward_kernel<per.value, vec.value, true, false>)
+                        : go(router_few_backward_kernel<per.value, vec.value, false, false>);
+        });
+    }
     return with_held(a.c, [&](auto per, auto vec) {
         const auto go = [&](auto *kernel) {
             return launch_edge(kernel, grid, 32 * ROUTER_WARPS, 0, 1, s, a);
@@ -961,11 +1251,11 @@ mok_status mok_router_forward(const mok_router_config *c, const void *logits, co
     const void *ps[] = {logits, bias, topk_idx, topk_w, counts, score_sum};
     for (const void *p : ps)
         if (p && !op_aligned16(p)) return MOK_ERR_INVALID_ARG;
-    const int parts = (int)blocks_of(shape_of(*c, c->groups));
     int32_t *cp = counts != nullptr ? (int32_t *)ws : nullptr;
     float *sp = score_sum != nullptr ? (float *)((char *)ws + part_bytes(*c)) : nullptr;
+    const RouterFwd a{shape_of(*c, c->groups), logits, bias, topk_idx, topk_w, cp, sp};
+    const int parts = (int)parts_of(a);
     if (c->T > 0) {
-        const RouterFwd a{shape_of(*c, c->groups), logits, bias, topk_idx, topk_w, cp, sp};
         MOK_OP_LAUNCH(OP_ROUTER, 1, launch_router(a, c->dtype == MOK_DTYPE_BF16, stream));
     }
     if (load)

@@ -157,6 +157,20 @@ CASES = [
     dict(T=3000, E=128, K=4, bias=True),
     dict(T=2000, E=60, K=6, bias=True, dtype="bf16", renorm=False),
     dict(T=700, E=5, K=2, score="sigmoid", bias=True),
+    # few experts: rows that a thread holds, in all its sizes, and one past them
+    dict(T=1, E=2, K=1, score="sigmoid", renorm=False),
+    dict(T=700, E=8, K=2),
+    dict(T=700, E=8, K=4, dtype="bf16", renorm=False, scale=2.5),
+    dict(T=70, E=4, K=4, masked=0.5),
+    dict(T=129, E=7, K=3, extra=2, masked=0.5),
+    dict(T=300, E=16, K=4, extra=4, dtype="bf16", masked=0.3),
+    dict(T=300, E=13, K=3, score="sigmoid", dtype="bf16", std=30.0),
+    dict(T=1000, E=16, K=4, score="sigmoid", masked=0.8),
+    dict(T=1000, E=16, K=4, renorm=False, std=20.0),
+    dict(T=300, E=15, K=4, extra=1),
+    dict(T=300, E=16, K=5),
+    dict(T=300, E=17, K=4),
+    dict(T=250001, E=8, K=2),
 ]
 
 
@@ -222,19 +236,20 @@ def test_without_loads_and_repeated():
     assert torch.equal(idx, i3) and torch.equal(sums, s3) and device_ok()
 
 
-def test_nan_logits_give_ids_in_range_each_once():
+@pytest.mark.parametrize("E, K", [(16, 4), (64, 8)])
+def test_nan_logits_give_ids_in_range_each_once(E, K):
     torch = _t()
-    for kw in (dict(), dict(bias=True), dict(score="sigmoid", G=4, keep=2, top=2, bias=True)):
-        logits = torch.randn(40, 64, device="cuda")
+    for kw in (dict(), dict(bias=True), dict(score="sigmoid", G=2, keep=1, top=2, bias=True)):
+        logits = torch.randn(40, E, device="cuda")
         logits[::2, 5] = float("nan")
         logits[::3] = float("nan")
         logits[1::3, 9:12] = INF
         logits[4, :] = -float("nan")
-        c = Case(T=40, E=64, K=8, logits=logits, **kw)
-        idx = c.forward()[0][:320].view(40, 8)
-        assert bool(((idx >= 0) & (idx < 64)).all()) and device_ok()
+        c = Case(T=40, E=E, K=K, logits=logits, **kw)
+        idx = c.forward()[0][:40 * K].view(40, K)
+        assert bool(((idx >= 0) & (idx < E)).all()) and device_ok()
         for row in idx.tolist():
-            assert len(set(row)) == 8
+            assert len(set(row)) == K
 
 
 def test_no_tokens():
@@ -331,16 +346,17 @@ def test_gradient_against_differences(kw):
     assert abs(float((got * step).sum() - slope)) <= 2.0 ** -13 * float((mag * step.abs()).sum())
 
 
-def test_bad_and_repeated_ids():
+@pytest.mark.parametrize("E", [16, 20])
+def test_bad_and_repeated_ids(E):
     torch = _t()
-    c = Case(T=6, E=20, K=3, score="softmax", renorm=False)
+    c = Case(T=6, E=E, K=3, score="softmax", renorm=False)
     dw = torch.randn(6, 3, device="cuda", generator=c.gen)
-    idx = torch.tensor([[0, 1, 2], [3, 3, 3], [5, 19, 5], [-1, 4, 20], [7, 8, 9], [2 ** 30, 1, 0]],
+    idx = torch.tensor([[0, 1, 2], [3, 3, 3], [5, 15, 5], [-1, 4, E], [7, 8, 9], [2 ** 30, 1, 0]],
                        dtype=torch.int32, device="cuda")
     got = backward(c, idx, dw, None)
     assert B.mok_read_device_status()[1] == B.MOK_ERR_DEVICE_INVARIANT
     B.mok_clear_device_status()
-    ok = (idx >= 0) & (idx < 20)
+    ok = (idx >= 0) & (idx < E)
     ref, mag = gradient64(c, torch.where(ok, idx, 0).long(), torch.where(ok, dw, 0.0).double(), None)
     assert bool(((got.double() - ref).abs() <= 2.0 ** -14 * mag + 1e-36).all())
 
