@@ -352,8 +352,8 @@ mok_status mok_check_norm_config(const mok_norm_config *cfg);
 size_t mok_norm_workspace_size(const mok_norm_config *cfg);
 
 /* x [rows][H]; residual NULL or [rows][H]; weight, bias NULL (one, zero) or fp32 [H]; h NULL or
- * [rows][H] out (with a residual; may be x or residual); y [rows][H] out (may be x where the types
- * and strides are the same and h is not x); mean, rstd NULL or fp32 [rows] out, for the backward
+ * [rows][H] out (with a residual; may be x or residual); y [rows][H] out (may be x or residual where
+ * the types and strides are the same and h is another); mean, rstd NULL or fp32 [rows] out, for the backward
  * (mean of MOK_NORM_LAYER only). */
 mok_status mok_norm_forward(const mok_norm_config *cfg, const void *x, const void *residual,
                             const float *weight, const float *bias, void *h, void *y, float *mean,
@@ -416,7 +416,8 @@ mok_status mok_vocab_loss_forward(const mok_vocab_loss_config *cfg, const void *
  *   dl_v = d_loss ((1 + 2 z_loss lse) exp(l_v - lse) - [v == target])
  *   dx = dl W            dW = dl^T x
  * dl enters the products rounded to bf16 for bf16 gradients (as the linear layer's dz does), as three
- * bf16 values that add up to it for fp32 ones. dx NULL or [rows][H] out, dw NULL or [V][H] out; one of them at least. */
+ * bf16 values that add up to it for fp32 ones. dx NULL or [rows][H] out, dw NULL or [V][H] out; one of
+ * them at least, and neither is x or W. */
 mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *cfg, const void *x, const void *w,
                                    const int32_t *targets, const float *lse, const float *d_loss,
                                    void *dx, void *dw, void *ws, size_t ws_bytes,

@@ -1019,7 +1019,7 @@ mok_status mok_norm_forward(const mok_norm_config *c, const void *x, const void 
     if ((st = current_device_status_word(&status)) != MOK_OK) return st;
     if (c->rows == 0) return MOK_OK;
     if (!x || !y || (h && !residual) || (mean && c->kind == MOK_NORM_RMS)) return MOK_ERR_INVALID_ARG;
-    if (y == h || (y == x && (c->x_dtype != c->y_dtype || c->ld_x != c->ld_y)))
+    if (y == h || ((y == x || y == residual) && (c->x_dtype != c->y_dtype || c->ld_x != c->ld_y)))
         return MOK_ERR_INVALID_ARG;
     const void *ps[] = {x, residual, weight, bias, h, y, mean, rstd};
     for (const void *p : ps)

@@ -646,6 +646,7 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
     mok_status st = check_vocab(c, MOK_VOCAB_LOSS_BACKWARD, ws, ws_bytes, &status, &wk);
     if (st != MOK_OK) return st;
     if (!dx && !dw) return MOK_ERR_INVALID_ARG;
+    if ((dx && (dx == x || dx == w)) || (dw && (dw == x || dw == w))) return MOK_ERR_INVALID_ARG;
     if (c->rows > 0 && (!x || !w || !targets || !lse || !d_loss)) return MOK_ERR_INVALID_ARG;
     const void *ps[] = {x, w, targets, lse, d_loss, dx, dw};
     for (const void *p : ps)

@@ -328,6 +328,7 @@ def test_refusals():
     wide = B.make_norm(8, 64, ld_y=72)
     big = torch.zeros(8, 72, device="cuda", dtype=torch.bfloat16)
     assert f(cfg=wide, y=big) == B.MOK_OK and f(cfg=wide, y=c.x, x=c.x, h=None) == bad
+    assert f(cfg=wide, y=c.res, h=None) == bad and f(y=c.res, h=None) == B.MOK_OK
     assert f(cfg=B.make_norm(8, 64, eps=0.0)) == bad
     n = B.mok_norm_workspace_size(c.cfg)
     ws = torch.zeros(n + 256, dtype=torch.uint8, device="cuda")

@@ -286,6 +286,7 @@ def test_refusals():
         B.mok_vocab_loss_backward(c.cfg, x, w, t, s, d, dx, dw, ws, n)  # noqa: E731
     assert g() == B.MOK_OK and g(dx=None) == B.MOK_OK and g(dw=None) == B.MOK_OK
     assert g(dx=None, dw=None) == bad
+    assert g(dx=c.x) == bad and g(dw=c.w) == bad and g(dx=c.w) == bad and g(dw=c.x) == bad
     for k in ("x", "w", "t", "s", "d"):
         assert g(**{k: None}) == bad
     for k in ("x", "w", "t", "s", "d", "dx", "dw"):
