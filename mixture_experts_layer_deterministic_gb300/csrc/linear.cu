@@ -1412,7 +1412,8 @@ cudaError_t launch_dense_grads(const DenseGrads &a, int *status, int *launches, 
     KParts xk = k_parts(plan.x, parts, a.rows, a.Kin);
     const KParts wk = k_parts(
         plan.w, parts + round_up((int64_t)part_bytes(plan.x, a.rows, a.Kin), 256) / 4, a.N, a.Kin);
-    if (a.dx_sum != nullptr || a.add) xk = KParts{1, 0, a.dx_sum, round_up(a.Kin, 4), 0, a.add};
+    if (plan.x.parts == 1 && (a.dx_sum != nullptr || a.add))
+        xk = KParts{1, 0, a.dx_sum, round_up(a.Kin, 4), 0, a.add};
     const bool cut = xk.out != nullptr || xk.add || wk.out != nullptr;
     e = (a.f32 ? (cut ? dense_grads<true, true> : dense_grads<true, false>)
                : (cut ? dense_grads<false, true> : dense_grads<false, false>))(
@@ -1420,7 +1421,14 @@ cudaError_t launch_dense_grads(const DenseGrads &a, int *status, int *launches, 
     if (e != cudaSuccess) return e;
     JoinArgs j = {};
     int n = 0;
-    if (a.dx && plan.x.parts > 1) j.o[n++] = join_out(xk, a.rows, a.Kin, a.dx, a.ld_dx);
+    if (a.dx && plan.x.parts > 1 && a.dx_sum != nullptr) {  // fp32, whatever dW is
+        j.o[0] = join_out(xk, a.rows, a.Kin, a.dx_sum, round_up(a.Kin, 4));
+        ++*launches;
+        if ((e = launch_join(true, j, s)) != cudaSuccess) return e;
+        j = JoinArgs{};
+    } else if (a.dx && plan.x.parts > 1) {
+        j.o[n++] = join_out(xk, a.rows, a.Kin, a.dx, a.ld_dx);
+    }
     if (a.dw && plan.w.parts > 1) j.o[n++] = join_out(wk, a.N, a.Kin, a.dw, a.ld_w);
     *launches += n > 0;
     return n > 0 ? launch_join(a.f32, j, s) : cudaSuccess;

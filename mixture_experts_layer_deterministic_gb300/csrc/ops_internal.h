@@ -44,8 +44,8 @@ struct DenseGrads {
     int64_t ld_x, ld_dx, ld_w, ld_dz;  // of x, of dx, of w and dw, of dz
     void *dx, *dw;               // one of them may be nullptr
     bool f32;                    // their type
-    // where N is a piece of the layer's: dx goes to dx_sum in fp32 (rows round_up(Kin, 4) apart;
-    // nullptr where dx is fp32 itself), and adds to it from the second piece on
+    // where not nullptr, dx goes to dx_sum in fp32 (rows round_up(Kin, 4) apart), if dx is not nullptr;
+    // where N is a piece of the layer's, dx adds to it (or to an fp32 dx) from the second piece on
     float *dx_sum;
     bool add;
     GradPlan plan;

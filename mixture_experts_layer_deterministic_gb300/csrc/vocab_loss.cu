@@ -285,9 +285,10 @@ __global__ void vocab_rows_kernel(const float *lse, const float *d_loss, const i
 
 // x for the product of dW, zeros in the rows that take no part: their dl is zero, but nothing says that x is
 // finite there, and zero times infinity would reach all of dW. 8192 x 4096 20 us, beside 10 ms of products.
+// `copies` of them, one below the other.
 __global__ void __launch_bounds__(256)
-    vocab_live_kernel(const uint16_t *x, int64_t ld, const int32_t *targets, int64_t rows, int H, int V,
-                      uint16_t *out, int64_t ld_out) {
+    vocab_live_kernel(const uint16_t *x, int64_t ld, const int32_t *targets, int64_t rows, int copies,
+                      int H, int V, uint16_t *out, int64_t ld_out) {
     let_next_start();
     wait_for_previous();
     const int64_t per = ld_out / 8, n = rows * per;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(256)
                 v = make_uint4(e[0], e[1], e[2], e[3]);
             }
         }
-        *reinterpret_cast<uint4 *>(out + r * ld_out + c) = v;
+        for (int k = 0; k < copies; ++k) *reinterpret_cast<uint4 *>(out + (k * rows + r) * ld_out + c) = v;
     }
 }
 
@@ -334,6 +335,14 @@ constexpr int PLANES = 3;
 // linear.cu). Runs of 512, with the exponent's rounding put right in dl, 7.0e-7 and 6.9e-7 (3% slower
 // than runs of 1024)
 constexpr int GRAD_RUN = 512;
+
+// Rows up to which bf16 gradients take two planes too, as rows of their own: dl is then twice as many rows,
+// with x twice for dW, and dx the sum of its two halves. A row's gradient is for the most part its target's
+// entry, so rounding that one entry to bf16 scales all of it, by up to 2^-8: with three rows 2.3e-3 of dx's
+// norm where rounding dx itself is 1.6e-3. Over many rows this averages out.
+// One plane against two, us: 3 rows, 45 x 11962 15 / 18; 4, 4096 x 131072 601 / 605; 64, 4096 x 32000 170 /
+// 165; 128 164 / 185; 256 186 / 244.
+constexpr int TWICE_ROWS = 256;
 
 // The gradient of the logits for vocabulary entries [v0, v0 + N), in N_PLANES planes of bf16. SEGS: of
 // logits whose segments of H were added in fp32 (for planes where H is long). Row tiles come first:
@@ -448,16 +457,21 @@ struct VocabDl {
     }
 };
 
-// dx of several pieces, from fp32 sums
+// dx of several pieces, or of dl's two planes (`copies` 2), from fp32 sums
 __global__ void __launch_bounds__(256)
-    vocab_round_kernel(const float *sum, int64_t ld_sum, int64_t rows, int H, uint16_t *dx, int64_t ld) {
+    vocab_round_kernel(const float *sum, int64_t ld_sum, int64_t rows, int copies, int H, uint16_t *dx,
+                       int64_t ld) {
     let_next_start();
     wait_for_previous();
     const int64_t n = rows * (ld_sum / 4);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / (ld_sum / 4);
         const int c = (int)(i - r * (ld_sum / 4)) * 4;
-        const float4 v = *reinterpret_cast<const float4 *>(sum + r * ld_sum + c);
+        float4 v = *reinterpret_cast<const float4 *>(sum + r * ld_sum + c);
+        if (copies == 2) {
+            const float4 u = *reinterpret_cast<const float4 *>(sum + (rows + r) * ld_sum + c);
+            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+        }
         uint16_t *p = dx + r * ld + c;
         if (c + 4 <= H) {
             *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
@@ -483,6 +497,7 @@ struct VocabWs {
     float *dx_sum;
     GradPlan plan;    // of the gradient products, where the vocabulary is one piece
     void *grads;      // their parts
+    int planes, copies;  // of dl; of the rows, as the gradient products take them
     int clusters;     // of a few rows' forward
     int piece, pieces;
     int64_t ld_dl;
@@ -503,7 +518,10 @@ size_t carve_vocab(const mok_vocab_loss_config &c, int pass, void *ws, VocabWs *
         w.part = (float2 *)take((size_t)c.rows * (c.rows <= FEW_ROWS ? 8 * w.clusters : 4 * n_vt) * 8);
         w.hit = (float *)take((size_t)c.rows * 4);
     } else {
-        const int64_t planes = c.grad_dtype == MOK_DTYPE_F32 ? PLANES : 1;
+        const bool f32 = c.grad_dtype == MOK_DTYPE_F32;
+        const int64_t copies = !f32 && c.rows <= TWICE_ROWS ? 2 : 1, planes = f32 ? PLANES : copies;
+        w.planes = (int)planes;
+        w.copies = (int)copies;
         const int64_t all = round_up(c.V, 256), row = 2 * planes * (c.rows > 0 ? c.rows : 1);
         int64_t piece = c.piece;
         if (piece == 0) {
@@ -519,12 +537,12 @@ size_t carve_vocab(const mok_vocab_loss_config &c, int pass, void *ws, VocabWs *
         w.rows = (RowGrad *)take((size_t)c.rows * sizeof(RowGrad));
         w.dl = (uint16_t *)take((size_t)planes * c.rows * w.ld_dl * 2);
         w.ld_x = round_up(c.H, 8);
-        w.x = (uint16_t *)take((size_t)c.rows * w.ld_x * 2);
-        if (w.pieces > 1 && c.grad_dtype == MOK_DTYPE_BF16)
-            w.dx_sum = (float *)take((size_t)c.rows * round_up(c.H, 4) * 4);
+        w.x = (uint16_t *)take((size_t)copies * c.rows * w.ld_x * 2);
+        if (!f32 && (w.pieces > 1 || copies > 1))
+            w.dx_sum = (float *)take((size_t)copies * c.rows * round_up(c.H, 4) * 4);
         if (w.pieces == 1) {
-            w.plan = plan_dense_grads(c.rows, c.V, c.H, (int)planes, true);
-            w.grads = take(dense_grads_bytes(w.plan, c.rows, c.V, c.H));
+            w.plan = plan_dense_grads(copies * c.rows, c.V, c.H, f32 ? PLANES : 1, true);
+            w.grads = take(dense_grads_bytes(w.plan, copies * c.rows, c.V, c.H));
         }
     }
     if (o != nullptr) *o = w;
@@ -671,13 +689,13 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
         const int64_t blocks = (c->rows * (wk.ld_x / 8) + 255) / 256, most = (int64_t)device_sm_count() * 16;
         MOK_OP_LAUNCH(OP_VOCAB_DL, 1,
                       launch_edge(vocab_live_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, 1,
-                                  stream, (const uint16_t *)x, c->ld_x, targets, c->rows, c->H, c->V,
-                                  wk.x, wk.ld_x));
+                                  stream, (const uint16_t *)x, c->ld_x, targets, c->rows, wk.copies,
+                                  c->H, c->V, wk.x, wk.ld_x));
     }
     for (int k = 0; k < wk.pieces; ++k) {
         const int v0 = k * wk.piece, n = c->V - v0 < wk.piece ? c->V - v0 : wk.piece;
         const int n_mb = (n + 255) / 256;
-        const Tiles tiles = dense_tiles(c->rows, dl_height(c->rows, n_mb, c->H, f32));
+        const Tiles tiles = dense_tiles(c->rows, dl_height(c->rows, n_mb, c->H, wk.planes > 1));
         const int band = 4096 / tiles.height;
         const int64_t units = tiles.cap * n_mb, plane = c->rows * wk.ld_dl;
         const int segs = f32 ? (c->H + SEG_K - 1) / SEG_K : 1;
@@ -687,16 +705,18 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
                                      plane, status};                                             \
         MOK_OP_LAUNCH(OP_VOCAB_DL, 1, launch_linear(ma, mb, p, units, stream));                  \
     } while (0)
-        if (!f32) MOK_DL(1, false);
+        if (wk.planes == 1) MOK_DL(1, false);
+        else if (wk.planes == 2) MOK_DL(2, false);
         else if (segs == 1) MOK_DL(PLANES, false);
         else MOK_DL(PLANES, true);
 #undef MOK_DL
-        const DenseGrads g{wk.x, (const uint16_t *)w + v0 * c->ld_w, wk.dl, c->rows, n, c->H,
+        const int64_t rows = wk.copies * c->rows;
+        const DenseGrads g{wk.x, (const uint16_t *)w + v0 * c->ld_w, wk.dl, rows, n, c->H,
                            f32 ? PLANES : 1, GRAD_RUN, wk.ld_x, c->ld_x, c->ld_w, wk.ld_dl, dx,
                            dw ? (char *)dw + v0 * c->ld_w * es : nullptr, f32,
                            dx ? wk.dx_sum : nullptr, dx && k > 0,
                            wk.pieces == 1 ? wk.plan
-                                          : plan_dense_grads(c->rows, n, c->H, f32 ? PLANES : 1, false),
+                                          : plan_dense_grads(rows, n, c->H, f32 ? PLANES : 1, false),
                            wk.grads};
         int launches = 0;
         MOK_OP_LAUNCH(OP_VOCAB_GRADS, launches, launch_dense_grads(g, status, &launches, stream));
@@ -707,7 +727,7 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
         MOK_OP_LAUNCH(OP_VOCAB_GRADS, 1,
                       launch_edge(vocab_round_kernel, (unsigned)(blocks < most ? blocks : most), 256,
                                   0, 1, stream, (const float *)wk.dx_sum, round_up(c->H, 4), c->rows,
-                                  c->H, (uint16_t *)dx, c->ld_x));
+                                  wk.copies, c->H, (uint16_t *)dx, c->ld_x));
     }
     return MOK_OK;
 }
