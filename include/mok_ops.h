@@ -416,7 +416,7 @@ mok_status mok_vocab_loss_forward(const mok_vocab_loss_config *cfg, const void *
  *   dl_v = d_loss ((1 + 2 z_loss lse) exp(l_v - lse) - [v == target])
  *   dx = dl W            dW = dl^T x
  * dl enters the products rounded to bf16 for bf16 gradients (as the linear layer's dz does) of more than
- * 256 rows, as two bf16 values that add up to it up to 256, as three for fp32 gradients. dx NULL or
+ * 512 rows, as two bf16 values that add up to it up to 512, as three for fp32 gradients. dx NULL or
  * [rows][H] out, dw NULL or [V][H] out; one of them at least, and neither is x or W. */
 mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *cfg, const void *x, const void *w,
                                    const int32_t *targets, const float *lse, const float *d_loss,

@@ -7,7 +7,7 @@ logit. lse moves by at most the largest el; 2^x is within 2^-22 and its argument
 probability's factor of at most 1), and a sum of V terms over 16-column runs and joins adds
 2^-17: 2^-16 in all; rounding lse and the loss 2^-22 of their size. dl is off by what its logit and lse
 are off, relative to the probability; it enters the products rounded to bf16 (2^-8), as two values (2^-16)
-up to 256 rows, or as three (2^-17) for fp32 gradients; outputs are rounded to their type."""
+up to 512 rows, or as three (2^-17) for fp32 gradients; outputs are rounded to their type."""
 import math
 
 import pytest
@@ -123,7 +123,7 @@ def check_backward(c, **parts):
     dl.scatter_add_(1, c.t.long().clamp(min=0)[:, None], -d)
     arg = (l - a).abs()
     edl = p.abs() * (el + 2.0 ** -23 * arg + 2.0 ** -20) + 2.0 ** -23 * dl.abs() + 2.0 ** -126
-    step = 2.0 ** -17 if c.gd != torch.bfloat16 else 2.0 ** -16 if c.R <= 256 else 2.0 ** -8
+    step = 2.0 ** -17 if c.gd != torch.bfloat16 else 2.0 ** -16 if c.R <= 512 else 2.0 ** -8
     edl = edl + step * (dl.abs() + edl)
     u = 2.0 ** -8 if c.gd == torch.bfloat16 else 2.0 ** -23
     pieces = 1 + (c.cfg.piece > 0) * c.V // max(c.cfg.piece, 1)
@@ -154,7 +154,8 @@ CASES = [
     dict(R=5, H=72, V=1000, piece=256),
     dict(R=130, H=1030, V=20000),
     dict(R=256, H=200, V=3000, z=1e-3),
-    dict(R=257, H=200, V=3000, z=1e-3),
+    dict(R=512, H=200, V=3000, z=1e-3),
+    dict(R=513, H=200, V=3000, z=1e-3),
 ]
 
 
