@@ -591,18 +591,20 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
                 }
                 after = __shfl_down_sync(0xFFFFFFFFu, sel, 1);
                 const int other = __shfl_down_sync(0xFFFFFFFFu, id, 1);
-                const bool close = lane < many - 1 && near(sel, after) && !alike(id, other);
-                if (many == 32) {  // no lane left: is any of the rest close, and no tie?
+                const bool close = __any_sync(0xFFFFFFFFu, lane < many - 1 && near(sel, after) && !alike(id, other));
+                // No lane left: is any of the rest close? Ties of the last may stay behind only where the
+                // order of the run stands: they may all be better than others in it.
+                if (many == 32) {
                     const uint32_t last = __shfl_sync(0xFFFFFFFFu, sel, 31);
                     const int of_last = __shfl_sync(0xFFFFFFFFu, id, 31);
                     for (int j = 0; j < h.n; ++j) {
                         const int i = h.id(j);
                         const uint32_t u = kept && ((left.taken >> j) & 1u) == 0 ? key_of(key, j) : 0u;
-                        exact = exact || (near(last, u) && !alike(of_last, i));
+                        exact = exact || (near(last, u) && (close || !alike(of_last, i)));
                     }
                     exact = __any_sync(0xFFFFFFFFu, exact);
                 }
-                if (!exact && __any_sync(0xFFFFFFFFu, close))
+                if (!exact && close)
                     id = choose_among<VEC, BF16>(c, row, a.bias, finite_top(top), id, many, lane);
             }
         }

@@ -1,0 +1,45 @@
+"""The router, the norm and the vocabulary loss at corners that the other files do not reach. References
+and tolerances: those of test_gpu_router.py, test_gpu_norm.py and test_gpu_vocab_loss.py unless said."""
+import math
+
+import pytest
+
+from mixture_experts_layer_deterministic_gb300 import binding as B
+import test_gpu_norm
+import test_gpu_router
+import test_gpu_vocab_loss
+
+pytestmark = pytest.mark.gpu
+
+
+def _t():
+    import torch
+    return torch
+
+
+def device_ok():
+    st, dev = B.mok_read_device_status()
+    B.mok_clear_device_status()
+    return (st, dev) == (B.MOK_OK, B.MOK_OK)
+
+
+# ------------------------------------------------------------------------------- router
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kw", [dict(E=64), dict(E=200), dict(E=128, G=2, keep=1)], ids=str)
+def test_ties_that_are_better_than_a_run_of_close_scores(score, kw):
+    """More than 32 close scores, the last of them in order ties that are better than the first."""
+    torch = _t()
+    E = kw["E"]
+    for low, high, b in ((20.0, 21.0, 0.0), (1.0, 1.0 + 2.0 ** -23, 0.25)):
+        if low == 20.0 and score == "softmax":
+            continue  # far apart there
+        for first in (31, 5, 32):
+            logits = torch.full((3, E), low, device="cuda")
+            logits[:, first:] = high
+            logits[1, -1] = low
+            logits[2, :2] = high
+            bias = torch.full((E,), b, device="cuda")
+            for K in (1, 8, 31, 32):
+                test_gpu_router.check_forward(test_gpu_router.Case(
+                    T=3, K=K, score=score, top=2, bias=bias, logits=logits, **kw))
