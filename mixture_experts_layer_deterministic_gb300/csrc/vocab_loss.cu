@@ -256,10 +256,9 @@ __global__ void __launch_bounds__(32 * FINISH_WARPS)
     if (lane != 0) return;
     const float l = a.m + log2f(a.s) * LN2_F;
     lse[r] = l;
-    if (loss == nullptr) return;
     const int t = targets[r];
     if (t >= V) raise_status(status, MOK_ERR_DEVICE_INVARIANT);
-    loss[r] = t >= 0 && t < V ? (l - hit[r]) + z * l * l : 0.0f;
+    if (loss != nullptr) loss[r] = t >= 0 && t < V ? (l - hit[r]) + z * l * l : 0.0f;
 }
 
 // ---------------------------------------------------------------- backward

@@ -43,3 +43,20 @@ def test_ties_that_are_better_than_a_run_of_close_scores(score, kw):
             for K in (1, 8, 31, 32):
                 test_gpu_router.check_forward(test_gpu_router.Case(
                     T=3, K=K, score=score, top=2, bias=bias, logits=logits, **kw))
+
+
+# --------------------------------------------------------------------- vocabulary loss
+
+def test_targets_past_the_vocabulary_without_a_loss():
+    torch = _t()
+    for R in (40, 300):
+        c = test_gpu_vocab_loss.Case(R=R, H=100, V=500, ignore=0.0)
+        loss, lse = c.forward()
+        assert device_ok()
+        c.t[5] = 500
+        out = torch.full_like(lse, 7.0)
+        ws, n = c.ws(B.MOK_VOCAB_LOSS_FORWARD)
+        B.check(B.mok_vocab_loss_forward(c.cfg, c.x, c.w, c.t, None, out, ws, n))
+        assert torch.equal(out, lse)
+        assert B.mok_read_device_status()[1] == B.MOK_ERR_DEVICE_INVARIANT
+        B.mok_clear_device_status()
