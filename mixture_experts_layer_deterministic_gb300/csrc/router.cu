@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(32 * ROUTER_WARPS, per_sm(PER)) router_kernel(
                 b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
                 b1 = fmaxf(b1, o1);
             }
-            const float score = SCORED && c.top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+            // (two biases near the lowest value are still above a group of masked experts)
+            const float score = SCORED && c.top == 2 && b2 > -INFINITY ? fmaxf(b1 + b2, -3.402823466e38f) : b1;
             int rank = 0;
             for (int g = 0; g < c.G; ++g) {
                 const float other = __shfl_sync(0xFFFFFFFFu, score, g * c.lanes);

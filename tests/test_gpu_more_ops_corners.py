@@ -45,6 +45,21 @@ def test_ties_that_are_better_than_a_run_of_close_scores(score, kw):
                     T=3, K=K, score=score, top=2, bias=bias, logits=logits, **kw))
 
 
+@pytest.mark.parametrize("kw", [dict(E=16, G=4, keep=2, K=5), dict(E=64, G=8, keep=3, K=20)], ids=str)
+def test_groups_whose_sum_of_two_passes_32_bits(kw):
+    """Biases near the lowest value: two of them are no fp32 number, and still before a masked group."""
+    torch = _t()
+    E, per = kw["E"], kw["E"] // kw["G"]
+    gen = torch.Generator("cuda").manual_seed(3)
+    logits = torch.randn(4, E, device="cuda", generator=gen)
+    logits[0, :per], logits[1, per:2 * per], logits[2, :2 * per] = -math.inf, -math.inf, -math.inf
+    bias = torch.full((E,), -3.0e38, device="cuda")
+    bias[-per:] = 0.0
+    for score in ("softmax", "sigmoid"):
+        test_gpu_router.check_forward(test_gpu_router.Case(T=4, score=score, top=2, bias=bias,
+                                                           logits=logits, **kw))
+
+
 # --------------------------------------------------------------------- vocabulary loss
 
 def test_targets_past_the_vocabulary_without_a_loss():
