@@ -723,7 +723,8 @@ __global__ void __launch_bounds__(NORM_TPB, NV == 1 ? 2 : 0) norm_backward_kerne
             team_sum(sgt, sg);
             // dx = dh - rstd mean(g) + g rstd - t rstd^2 mean(g n)
             const float c0 = s.layer ? -row_rstd * (sg * inv_n) : 0.0f;
-            const float c1 = -row_rstd * row_rstd * (row_rstd * (sgt * inv_n));
+            // (from the inside: rstd^2 alone passes fp32 for a row of zeros and an eps below 3e-39)
+            const float c1 = -row_rstd * (row_rstd * (row_rstd * (sgt * inv_n)));
             const f32x2 a0 = pair(c0, c0), a1 = pair(c1, c1);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {

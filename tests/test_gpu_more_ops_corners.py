@@ -60,6 +60,26 @@ def test_groups_whose_sum_of_two_passes_32_bits(kw):
                                                            logits=logits, **kw))
 
 
+# --------------------------------------------------------------------------------- norm
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("H", [64, 4096])
+def test_gradient_of_rows_of_one_value_with_a_small_eps(kind, H):
+    """rstd is 1e20 and its square no fp32 number; n is 0, so dx = rstd (g - mean(g))."""
+    torch = _t()
+    c = test_gpu_norm.Case(R=3, H=H, kind=kind, x="fp32", y="fp32", res=False, eps=1e-40)
+    c.x[:, :H] = 0.0
+    _, y, mean, rstd = c.forward()
+    dy = c.rand(c.ld_y, c.yd)
+    dx, dw, db = c.backward(c.x, mean, rstd, dy, None)
+    g = c.live(dy) * c.w.double()
+    want = g - (g.mean(1, keepdim=True) if kind == "layer" else 0.0)
+    want = want * rstd[:3].double()[:, None]
+    size = rstd[:3].double()[:, None] * (g.abs() + g.abs().mean(1, keepdim=True))
+    assert bool(((c.live(dx) - want).abs() <= 2.0 ** -16 * size).all())
+    assert bool((dw[:H] == 0).all()) and device_ok()
+
+
 # --------------------------------------------------------------------- vocabulary loss
 
 def test_targets_past_the_vocabulary_without_a_loss():
