@@ -344,8 +344,15 @@ constexpr int GRAD_RUN = 512;
 // 165; 256 185 / 228; 512 255 / 421.
 constexpr int TWICE_ROWS = 512;
 
+// Elements of H that the logits of bf16 gradients are summed over at a time. A tensor-core sum loses up to
+// 2^-23 of what it has so far with every 16 terms, so a run of n terms of one sign n / 32 of that: 2^-16 of
+// a logit with runs of 4096, while one of 2^18 may lose 2^-10: 0.3 of a logit of 300, 30% of its dl. Gradients
+// of 4096 rows, 8192 x 32768, 3803 us with runs of 4096, 3787 with one, 3980 with runs of 1024 (the sums leave
+// TMEM more often); 600 rows, 8192 x 32000, 760, 737 and 793; 16 rows 327, 324 and 328.
+constexpr int BF16_RUN = 4096;
+
 // The gradient of the logits for vocabulary entries [v0, v0 + N), in N_PLANES planes of bf16. SEGS: of
-// logits whose segments of H were added in fp32 (for planes where H is long). Row tiles come first:
+// logits whose segments of H were added in fp32. Row tiles come first:
 // a band of 4096 rows of x stays in L2 while W passes by once (the other way round W passes by for
 // every tile, 4096 rows, 4096 x 65536: 1450 against 1200 us under the profiler).
 template <int N_PLANES, bool SEGS>
@@ -355,7 +362,7 @@ struct VocabDl {
     Tiles tiles;
     int band;        // tiles that take a block of W one after another
     int n_mb;        // ceil(N / 256)
-    int segs;
+    int segs, run;   // of H, and their elements
     int H, v0, N;
     const RowGrad *rows;
     uint16_t *dl;
@@ -375,13 +382,13 @@ struct VocabDl {
     MOK_DEV LinGeom geom(const Unit &u, int seg, uint32_t rank) const {
         LinGeom q;
         q.n_mma = (u.nr + 15) & ~15;
-        q.a0 = seg * SEG_K;
+        q.a0 = seg * run;
         q.a1 = v0 + u.mb * 256 + (int)rank * 128;
         q.a2 = 0;
         q.b0 = q.a0;
         q.b1 = u.r0 + (int)rank * (q.n_mma / 2);
         q.nbox = (q.n_mma / 2 + 31) / 32;
-        const int k = segs > 1 && H - q.a0 > SEG_K ? SEG_K : H - q.a0;
+        const int k = H - q.a0 > run ? run : H - q.a0;
         q.k_steps = (k + 15) / 16;
         q.k_first = q.half = 0;
         return q;
@@ -405,7 +412,7 @@ struct VocabDl {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     if (n0 + j >= u.nr) continue;
-                    float g = dl_of<true>(rows[r0 + n0 + j], v[j], v0 + f);
+                    float g = dl_of<(N_PLANES > 1)>(rows[r0 + n0 + j], v[j], v0 + f);
 #pragma unroll
                     for (int k = 0; k < N_PLANES; ++k) {
                         const uint16_t b = f32_to_bf16(g);
@@ -698,17 +705,22 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
         const Tiles tiles = dense_tiles(c->rows, dl_height(c->rows, n_mb, c->H, wk.planes > 1));
         const int band = 4096 / tiles.height;
         const int64_t units = tiles.cap * n_mb, plane = c->rows * wk.ld_dl;
-        const int segs = f32 ? (c->H + SEG_K - 1) / SEG_K : 1;
+        const int run = f32 ? SEG_K : BF16_RUN, segs = (c->H + run - 1) / run;
 #define MOK_DL(...)                                                                              \
     do {                                                                                         \
-        const VocabDl<__VA_ARGS__> p{tiles, band, n_mb, segs, c->H, v0, n, wk.rows, wk.dl, wk.ld_dl, \
+        const VocabDl<__VA_ARGS__> p{tiles, band, n_mb, segs, run, c->H, v0, n, wk.rows, wk.dl, wk.ld_dl, \
                                      plane, status};                                             \
         MOK_OP_LAUNCH(OP_VOCAB_DL, 1, launch_linear(ma, mb, p, units, stream));                  \
     } while (0)
-        if (wk.planes == 1) MOK_DL(1, false);
-        else if (wk.planes == 2) MOK_DL(2, false);
-        else if (segs == 1) MOK_DL(PLANES, false);
-        else MOK_DL(PLANES, true);
+        if (segs == 1) {
+            if (wk.planes == 1) MOK_DL(1, false);
+            else if (wk.planes == 2) MOK_DL(2, false);
+            else MOK_DL(PLANES, false);
+        } else {
+            if (wk.planes == 1) MOK_DL(1, true);
+            else if (wk.planes == 2) MOK_DL(2, true);
+            else MOK_DL(PLANES, true);
+        }
 #undef MOK_DL
         const int64_t rows = wk.copies * c->rows;
         const DenseGrads g{wk.x, (const uint16_t *)w + v0 * c->ld_w, wk.dl, rows, n, c->H,

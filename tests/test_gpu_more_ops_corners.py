@@ -95,3 +95,31 @@ def test_targets_past_the_vocabulary_without_a_loss():
         assert torch.equal(out, lse)
         assert B.mok_read_device_status()[1] == B.MOK_ERR_DEVICE_INVARIANT
         B.mok_clear_device_status()
+
+
+@pytest.mark.parametrize("R", [40, 520])
+@pytest.mark.parametrize("H", [4104, 1 << 18])
+def test_logits_of_long_rows(R, H):
+    """Logits of some 300 out of H terms of one sign. A tensor-core sum loses at most 2^-23 of what it has
+    with every 16 terms, so up to 4096 terms, which are what is summed at a time, 4096 / 32 of that: 2^-16;
+    adding the H / 4096 parts loses 2^-24 each of what they have so far. dl is off by its logit's error (and as
+    test_gpu_vocab_loss.py says)."""
+    torch = _t()
+    V = 60
+    c = test_gpu_vocab_loss.Case(R=R, H=H, V=V, ignore=0.1)
+    c.x[:R, :H] = 0.5 + torch.rand(R, H, device="cuda", generator=c.gen)
+    c.w[:V, :H] = (0.5 + torch.rand(V, H, device="cuda", generator=c.gen)) * (300.0 / H)
+    x, w = c.x[:R, :H].double(), c.w[:V, :H].double()
+    l = x @ w.T
+    lse = torch.logsumexp(l, 1)
+    d = torch.where(c.t >= 0, c.d.double(), 0.0)[:, None]
+    dl = torch.exp(l - lse.float().double()[:, None]) * d
+    err = dl.abs() * (l.abs() * (2.0 ** -16 + H / 4096 / 2 * 2.0 ** -24) + 2.0 ** -16)
+    dl.scatter_add_(1, c.t.long().clamp(min=0)[:, None], -d)
+    err = err + (2.0 ** -8 if R > 512 else 2.0 ** -16) * dl.abs()
+    dx, dw = c.backward(lse.float())
+    assert device_ok()
+    for got, want, tol in ((dx[:R, :H], dl @ w, err @ w.abs()), (dw[:V, :H], dl.T @ x, err.T @ x.abs())):
+        tol = tol + 2.0 ** -18 * (dl.abs() @ w.abs() if want.shape[0] == R else dl.T.abs() @ x.abs())
+        tol = tol + 2.0 ** -8 * (want.abs() + tol)
+        assert bool(((got.double() - want).abs() <= tol).all())
