@@ -403,7 +403,9 @@ typedef enum mok_vocab_loss_pass {
 mok_status mok_check_vocab_loss_config(const mok_vocab_loss_config *cfg);
 
 /* Bytes of workspace of a pass (256-byte aligned, contents on entry do not matter); 0 for an
- * invalid configuration. */
+ * invalid configuration. The forward's grows with rows V / 8 (a maximum and a sum for each row and 64
+ * entries: 134 MB for 8192 rows and 131072 entries), up to 64 rows with rows alone (4864 bytes each); the backward's with
+ * rows times piece (2 bytes of each value of dl) and rows times H. */
 size_t mok_vocab_loss_workspace_size(const mok_vocab_loss_config *cfg, int pass);
 
 /* targets int32 [rows]; loss NULL or fp32 [rows] out, lse fp32 [rows] out (of every row, whatever its
@@ -415,8 +417,12 @@ mok_status mok_vocab_loss_forward(const mok_vocab_loss_config *cfg, const void *
 /* With d_loss fp32 [rows] and lse from the forward:
  *   dl_v = d_loss ((1 + 2 z_loss lse) exp(l_v - lse) - [v == target])
  *   dx = dl W            dW = dl^T x
- * dl enters the products rounded to bf16 for bf16 gradients (as the linear layer's dz does) of more than
- * 512 rows, as two bf16 values that add up to it up to 512, as three for fp32 gradients. dx NULL or
+ * dl enters the products as three bf16 values that add up to it for fp32 gradients, as two for bf16
+ * gradients of up to 512 rows, and rounded to one (as the linear layer's dz does) for bf16 gradients of more
+ * rows, whether they take part or not. Each entry is then off by up to 2^-8 of itself, and since a row's gradient
+ * is for the most part its target's entry, that may scale a row of dx, or of dW, by as much, whatever the other
+ * rows are (2.3e-3 of the norm, with the outputs' own rounding, where that alone is 1.7e-3); fp32
+ * gradients have 7e-7. Logits are summed over 1024 elements of H at a time, for bf16 gradients 4096. dx NULL or
  * [rows][H] out, dw NULL or [V][H] out; one of them at least, and neither is x or W. */
 mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *cfg, const void *x, const void *w,
                                    const int32_t *targets, const float *lse, const float *d_loss,

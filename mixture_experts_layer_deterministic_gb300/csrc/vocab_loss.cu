@@ -337,9 +337,10 @@ constexpr int GRAD_RUN = 512;
 
 // Rows up to which bf16 gradients take two planes too, as rows of their own: dl is then twice as many rows,
 // with x twice for dW, and dx the sum of its two halves. A row's gradient is for the most part its target's
-// entry, so rounding that one entry to bf16 scales all of it, by up to 2^-8: with three rows 2.3e-3 of dx's
-// norm where rounding dx itself is 1.6e-3, with 300 still up to 2.5e-3. Over many rows this averages out (4096
-// of them: 2.3e-3 whatever their factors) and two planes would be half of all work again.
+// entry, so rounding that one entry to bf16 scales all of it, by up to 2^-8, whatever the other rows are: with
+// one plane any number of rows is 2.3e-3 of the norm off where rounding the outputs alone is 1.7e-3, and few rows may be
+// 2.5e-3. The bound is one of cost: two planes are half again the products of many rows, and little beside W's bytes and
+// the launches of few.
 // One plane against two, us: 3 rows, 45 x 11962 15 / 18; 4, 4096 x 131072 601 / 605; 64, 4096 x 32000 170 /
 // 165; 256 185 / 228; 512 255 / 421.
 constexpr int TWICE_ROWS = 512;
