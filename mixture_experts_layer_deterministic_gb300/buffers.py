@@ -515,8 +515,8 @@ class Router:
     def _check(self, logits, idx, w_name, w):
         _check_current(self.here)
         n = self.T * self.K
-        _check_vector("idx", idx, torch.int32, self.here, n if n else idx.numel())
-        _check_vector(w_name, w, torch.float32, self.here, n if n else w.numel())
+        for name, t, dtype in (("idx", idx, torch.int32), (w_name, w, torch.float32)):
+            _check_vector(name, t, dtype, self.here, n if n or t is None else t.numel())
         _check_matrix("logits", logits, self.dtype, self.here, self.T, self.E, self.ld)
 
     def forward(self, logits, idx, topk_w, bias=None, counts=None, score_sum=None, stream=None):

@@ -150,3 +150,11 @@ def test_arrays_of_another_device_than_the_current(monkeypatch):
     buffers._check_current(torch.device("cpu"))
     with pytest.raises(ValueError):
         buffers._check_current(torch.device("cuda", 1))
+
+
+def test_no_tokens_without_arrays(calls):
+    """The entry points take null arrays where there is nothing in them."""
+    r = Router(0, 8, 2, device="cpu")
+    r.forward(torch.zeros(0, 8), None, None, counts=torch.zeros(8, dtype=I32))
+    r.backward(None, None, None, None)
+    assert len(calls) == 2 and calls[0][1][3] is None and calls[1][1][5] is None
