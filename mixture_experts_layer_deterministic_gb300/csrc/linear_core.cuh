@@ -18,14 +18,6 @@
 namespace mok {
 namespace {
 
-// two fp32 values to bf16 in one conversion, lo in the low half (two single conversions run on
-// the slow pipe and held the epilogue: dW of 64 x 1024 x 4096 164 against 139 us)
-MOK_DEV uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 constexpr int BOX = 64 * 128;      // one 64 x 64 bf16 box (8 KB)
 constexpr int LSTAGES = 6;
 constexpr int LSTAGE_BYTES = 4 * BOX;
@@ -702,7 +694,7 @@ cudaError_t launch_both(const CUtensorMap &pa, const CUtensorMap &pb, const P &p
 }
 
 // Plans that a result's rounding depends on count the GB300's pairs of SMs, not the device's.
-constexpr int64_t PLAN_PAIRS = 76;
+constexpr int64_t PLAN_PAIRS = GB300_SMS / 2;
 
 // clocks of a 64-element K block on tiles of h rows: the larger of the MMAs' (2 a row) and the
 // loads' (64 bytes a clock and SM: 256 for the weights, 64 for each box of 32 rows)

@@ -19,8 +19,6 @@ namespace mok {
 namespace {
 
 constexpr int NORM_TPB = 512;
-// blocks whose column sums are added in order: not of the device, the sums' bits depend on it
-constexpr int64_t NORM_PARTS = 152;
 
 // 8 elements as they lie in memory
 template <bool F32>
@@ -54,11 +52,6 @@ MOK_DEV void load8(const void *row, int c, int H, float (&v)[8]) {
                               : bf16_to_f32(static_cast<const uint16_t *>(row)[c + j]);
     }
 }
-MOK_DEV uint32_t pack(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 template <bool F32>
 MOK_DEV void store8(void *row, int c, int H, const float (&v)[8]) {
     if (c + 8 <= H) {
@@ -68,7 +61,7 @@ MOK_DEV void store8(void *row, int c, int H, const float (&v)[8]) {
             p[1] = make_float4(v[4], v[5], v[6], v[7]);
         } else {
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + c) = make_uint4(
-                pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
+                pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
         }
     } else {
 #pragma unroll
@@ -443,7 +436,7 @@ __global__ void __launch_bounds__(NORM_TPB, NV == 1 ? 2 : 0) norm_kernel(const N
                 for (int j = 0; j < 4; ++j) {
                     v[k][j] = add2(v[k][j], f[j]);
                     if (!X32) {  // as it is stored, and read by the backward pass
-                        const uint32_t p = pack(both(v[k][j]).x, both(v[k][j]).y);
+                        const uint32_t p = pack2(both(v[k][j]).x, both(v[k][j]).y);
                         v[k][j] = pair(bf16_lo(p), bf16_hi(p));
                     }
                     o[2 * j] = both(v[k][j]).x;
@@ -575,7 +568,7 @@ struct NormBwd {
     const void *h, *dy, *dh;
     const float *mean, *rstd, *w;
     void *dx;
-    float *dw_part, *db_part;  // [NORM_PARTS][H], or nullptr
+    float *dw_part, *db_part;  // [NormPlan::parts][H], or nullptr
 };
 
 // n and g of 8 columns, and what they add to the row's sums
@@ -893,7 +886,7 @@ NormPlan norm_plan(const mok_norm_config &c, bool backward) {
     if (threads > 32) p.tpr = (int)round_up(threads, 32);
     // as many teams as a block holds; with few rows fewer, on more SMs
     int teams = NORM_TPB / p.tpr;
-    const int64_t blocks = NORM_PARTS * blocks_of_sm(nv);
+    const int64_t blocks = GB300_SMS * blocks_of_sm(nv);
     while (teams > 1 && p.tpr * teams > 128 && c.rows < blocks * teams) teams /= 2;
     p.tpb = teams * p.tpr;
     p.groups = (c.rows + teams - 1) / teams;

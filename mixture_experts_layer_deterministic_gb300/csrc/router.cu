@@ -32,7 +32,6 @@ constexpr int ROUTER_WARPS = 8;
 // added in order, so their number is not the device's (with an earlier choice 16384 x 512: 23.4 us in one
 // wave, 26.6 in 1.3; 100000 x 60: 50 us at 4 blocks a SM, 75 at 3)
 constexpr int per_sm(int held) { return held <= 4 ? 6 : held <= 8 ? 4 : held <= 16 ? 3 : held <= 32 ? 2 : 1; }
-constexpr int64_t SMS = 152;
 constexpr int MAX_E = 1024, MAX_GROUPS = 32;
 
 // order-preserving image of a float; -0 as +0. Everything, NaN of either sign too, maps above 0
@@ -113,11 +112,6 @@ MOK_DEV void load_logits(const void *row, const Held<VEC> &h, float (&v)[PER]) {
 // and reciprocal
 MOK_DEV float sigmoid32(float l) { return 1.0f / (1.0f + expf(-l)); }
 constexpr float LOG2E_R = 1.4426950408889634f;
-MOK_DEV float exp2_hw(float x) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
-    return e;
-}
 MOK_DEV float sigmoid_hw(float l) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_hw(-LOG2E_R * l)));
@@ -1097,7 +1091,7 @@ int held_of(const RouterShape &s) {
     return 64;  // only with many groups: 17 of 60 experts have one lane each
 }
 int64_t blocks_of(const RouterShape &s) {
-    const int64_t n = (s.T + ROUTER_WARPS - 1) / ROUTER_WARPS, most = SMS * per_sm(held_of(s));
+    const int64_t n = (s.T + ROUTER_WARPS - 1) / ROUTER_WARPS, most = GB300_SMS * per_sm(held_of(s));
     return n < most ? n : most;
 }
 

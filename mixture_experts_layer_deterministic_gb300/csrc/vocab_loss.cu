@@ -24,12 +24,6 @@ namespace {
 constexpr float LOG2E_F = 1.4426950408889634f, LN2_F = 0.6931471805599453f;
 constexpr float LOWEST = -3.0e38f;  // below any logit; differences with it stay finite or -inf
 
-MOK_DEV float exp2_hw(float x) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
-    return e;
-}
-
 // Running maximum and sum of exponentials, in powers of two.
 struct MaxSum {
     float m, s;
