@@ -345,6 +345,16 @@ constexpr int TWICE_ROWS = 512;
 // of 4096 rows, 8192 x 32768, 3803 us with runs of 4096, 3787 with one, 3980 with runs of 1024 (the sums leave
 // TMEM more often); 600 rows, 8192 x 32000, 760, 737 and 793; 16 rows 327, 324 and 328.
 constexpr int BF16_RUN = 4096;
+// ... and of fp32 gradients: 512, as many as GRAD_RUN, or all of H up to SEG_K where dl has many entries. A logit's
+// error reaches the probabilities alone, which are the less of a row's dl the more entries share them, and sums in
+// segments leave TMEM through fp32 stores of their own: 1001 rows, 1000 x 5003, 108 us and 7.2e-7 in one run, 124 us
+// and 6.8e-7 in two. 2000 rows, 1000 x 64: 53 us, 1.4e-6 and 60 us, 8.4e-7; 6251 rows, 1044 x 90, with runs of 1024
+// 99 us, 1.5e-6, of 512 99 us, 9.3e-7; 4096 rows, 4096 x 4096 651 and 657 us.
+constexpr int F32_RUN = 512, F32_FEW = 512;
+int dl_run(const mok_vocab_loss_config &c) {
+    if (c.grad_dtype != MOK_DTYPE_F32) return BF16_RUN;
+    return c.H <= SEG_K && c.V > F32_FEW ? SEG_K : F32_RUN;
+}
 
 // The gradient of the logits for vocabulary entries [v0, v0 + N), in N_PLANES planes of bf16. SEGS: of
 // logits whose segments of H were added in fp32. Row tiles come first:
@@ -700,7 +710,7 @@ mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *c, const void *x
         const Tiles tiles = dense_tiles(c->rows, dl_height(c->rows, n_mb, c->H, wk.planes > 1));
         const int band = 4096 / tiles.height;
         const int64_t units = tiles.cap * n_mb, plane = c->rows * wk.ld_dl;
-        const int run = f32 ? SEG_K : BF16_RUN, segs = (c->H + run - 1) / run;
+        const int run = dl_run(*c), segs = (c->H + run - 1) / run;
 #define MOK_DL(...)                                                                              \
     do {                                                                                         \
         const VocabDl<__VA_ARGS__> p{tiles, band, n_mb, segs, run, c->H, v0, n, wk.rows, wk.dl, wk.ld_dl, \
