@@ -423,8 +423,8 @@ mok_status mok_vocab_loss_forward(const mok_vocab_loss_config *cfg, const void *
  * is for the most part its target's entry, that may scale a row of dx, or of dW, by as much, whatever the other
  * rows are (2.3e-3 of the norm, with the outputs' own rounding, where that alone is 1.7e-3); fp32
  * gradients have 4e-7 to 1.2e-6. Logits are summed over up to 1024 elements of H at a time, for bf16
- * gradients 4096. dx NULL or
- * [rows][H] out, dw NULL or [V][H] out; one of them at least, and neither is x or W. */
+ * gradients 4096.
+ * dx NULL or [rows][H] out, dw NULL or [V][H] out; one of them at least, and neither is x or W. */
 mok_status mok_vocab_loss_backward(const mok_vocab_loss_config *cfg, const void *x, const void *w,
                                    const int32_t *targets, const float *lse, const float *d_loss,
                                    void *dx, void *dw, void *ws, size_t ws_bytes,
